@@ -403,6 +403,129 @@ MUON_API muon_status muon_plan_partition(const muon_plan_t* plan, int world, int
                                          double flops_per_s, double bytes_per_s, int* owner,
                                          double* rank_load);
 
+/*
+ * Operators of a training step that stand between its matrix products and
+ * feed the optimizer: layer norm (alone, or behind dropout and the residual
+ * add), dropout, and the expert router with its balance loss, each with its
+ * gradient.  All are asynchronous on `stream`, allocate nothing, keep nothing
+ * between calls and validate their arguments before any launch.  Activations
+ * and logits are MUON_BF16 or MUON_F32; rows are `ld` elements apart (any
+ * ld >= 0 for inputs; every output is dense).  Sums, means and softmax
+ * statistics are held in fp32.  Results do not depend on scheduling: no
+ * floating-point atomics.  Outputs must not overlap inputs or one another
+ * unless said otherwise.  MUON_FAULT=launch applies (MUON_ERR_CUDA after
+ * validation); pointers that are not aligned to their element type give
+ * MUON_ERR_ALIGNMENT.
+ *
+ * Random bits of dropout: Philox4x32-10 (J. Salmon, M. Moraes, R. Dror, D.
+ * Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC 2011) with key =
+ * seed and counter = offset + i / 8 for element i in row-major order; the
+ * eight 16-bit halves of a block's four words, low half first, serve elements
+ * 8 (i / 8) .. + 7.  With t = floor(65536 p + 1/2), element i is kept when its
+ * half is >= t and is then multiplied by 65536 / (65536 - t), the exact
+ * inverse of the probability used; a dropped element is an exact 0 whatever
+ * it held.  The flags depend on (seed, offset, i) alone, so the gradient
+ * recomputes them and no mask is stored.  A call uses ceil(n / 8) counters: the
+ * next call with the same seed takes an offset at least that much higher.  A
+ * captured graph replays the seed and offset it was captured with.
+ */
+
+/*
+ * Layer norm of each row, optionally behind dropout and a residual add:
+ *   s = residual + dropout(x);  y = (s - mean) * rstd * weight + bias,
+ *   mean = mean(s), rstd = 1 / sqrt(mean((s - mean)^2) + eps)
+ * over `cols`.  Statistics and y use s in fp32; `sum` receives s rounded.
+ *   rows >= 0, cols in [1, 2^30]
+ *   wdtype       type of weight and bias
+ *   residual     null: s = dropout(x)
+ *   weight, bias [cols], each may be null (1, 0)
+ *   p            dropout probability in [0, 1]; 0: no random bits are drawn
+ *   sum          [rows, cols] of dtype, or null (not needed)
+ *   y            [rows, cols] of dtype
+ *   mean, rstd   [rows] fp32, each may be null
+ */
+MUON_API muon_status muon_layer_norm(int64_t rows, int64_t cols, int dtype, int wdtype,
+                                     const void* x, int64_t ldx, const void* residual,
+                                     int64_t ldr, const void* weight, const void* bias, float eps,
+                                     float p, uint64_t seed, uint64_t offset, void* sum, void* y,
+                                     float* mean, float* rstd, void* stream);
+
+/*
+ * Gradient of muon_layer_norm.  With g = dy * weight and h = (sum - mean) *
+ * rstd:
+ *   d = rstd * (g - mean(g) - h * mean(g * h)) + dsum
+ *   dresidual = d;  dx = dropout(d), with the forward pass's p, seed, offset
+ *   dweight = sum over rows of dy * h;  dbias = sum over rows of dy
+ *   sum          the forward pass's sum (its x when it had neither residual
+ *                nor dropout), mean and rstd its statistics
+ *   dsum         gradient that reaches s past the norm, or null (0)
+ *   dx, dresidual, dweight, dbias   each may be null (not needed)
+ *   workspace    device, 256-byte aligned, >= muon_layer_norm_workspace_bytes
+ *                (any content); unused, and may be null, when neither dweight
+ *                nor dbias is asked for
+ */
+MUON_API muon_status muon_layer_norm_backward(
+    int64_t rows, int64_t cols, int dtype, int wdtype, const void* dy, int64_t lddy,
+    const void* sum, int64_t ldsum, const float* mean, const float* rstd, const void* weight,
+    const void* dsum, int64_t ldds, float p, uint64_t seed, uint64_t offset, void* dx,
+    void* dresidual, void* dweight, void* dbias, void* workspace, size_t ws_bytes, void* stream);
+MUON_API muon_status muon_layer_norm_workspace_bytes(int64_t rows, int64_t cols, size_t* out);
+
+/*
+ * y = residual + dropout(x) over n >= 0 dense elements (residual null: 0).
+ * The gradient of x is the same call on dy without a residual.  y may be x or
+ * residual itself.
+ */
+MUON_API muon_status muon_dropout(int64_t n, int dtype, const void* x, const void* residual,
+                                  float p, uint64_t seed, uint64_t offset, void* y, void* stream);
+
+/*
+ * Expert router: choice of k experts per token, their combine weights, the
+ * per-expert counts and the balance loss.
+ *   A token is routed when its mask is nonzero (or there is no mask) and some
+ *   logit is above -inf.  p = softmax of its logits; its picks are the k
+ *   largest logits, ties to the lowest index; an expert at -inf is never
+ *   picked.  A missing pick (fewer than k experts above -inf, or a token that
+ *   is not routed) has index -1 and weight 0.  weight = softmax over the picks
+ *   (normalize != 0) or p at the pick.
+ *   n = routed tokens, P_e = sum of p_e / n, c_e = picks of e:
+ *   loss = experts * sum over e of c_e / (k n) * P_e   (1 when balanced; 0
+ *   when n = 0)
+ * What the logits of a masked token hold has no effect.  A NaN ranks above
+ * every number; a routed token with a NaN or +inf has NaN weights, and so have
+ * mean_prob and the loss.
+ *   tokens >= 0 with tokens * k < 2^31, experts in [1, 1024], k in [1,
+ *   min(experts, 32)]
+ *   token_mask  [tokens] bytes, or null
+ *   weights     [tokens, k] fp32;  index [tokens, k]
+ *   counts      [experts + 1]: c_e, then n
+ *   mean_prob   [experts] fp32: P_e;  loss one fp32
+ *   workspace   device, 256-byte aligned, >= muon_route_workspace_bytes (any
+ *               content)
+ */
+MUON_API muon_status muon_route(int64_t tokens, int experts, int k, int dtype, const void* logits,
+                                int64_t ld, const uint8_t* token_mask, int normalize,
+                                float* weights, int32_t* index, int32_t* counts, float* mean_prob,
+                                float* loss, void* workspace, size_t ws_bytes, void* stream);
+MUON_API muon_status muon_route_workspace_bytes(int64_t tokens, int experts, size_t* out);
+
+/*
+ * Gradient of muon_route's weights and loss with respect to the logits (the
+ * counts are constants of the loss).
+ *   index, counts   the forward pass's
+ *   dweights        [tokens, k] fp32, or null (0)
+ *   dloss           one fp32 on the device, or null (0)
+ *   dlogits         [tokens, experts] of dtype; a token that is not routed gets
+ *                   zeros
+ * Other arguments are those of muon_route.  An index outside [0, experts) is
+ * a missing pick.
+ */
+MUON_API muon_status muon_route_backward(int64_t tokens, int experts, int k, int dtype,
+                                         const void* logits, int64_t ld, const uint8_t* token_mask,
+                                         int normalize, const int32_t* index,
+                                         const int32_t* counts, const float* dweights,
+                                         const float* dloss, void* dlogits, void* stream);
+
 MUON_API void muon_plan_destroy(muon_plan_t* plan);
 MUON_API const char* muon_status_string(muon_status s);
 

@@ -71,7 +71,9 @@ EXPORTS = ["muon_options_default", "muon_plan", "muon_plan_workspace_bytes",
            "muon_plan_launches", "muon_plan_destroy", "muon_status_string", "muon_step_static",
            "muon_step_amp", "muon_adamw_step", "muon_plan_partition", "muon_static_error",
            "muon_step_timed", "muon_step_host", "muon_plan_host_unit_bytes",
-           "muon_host_alloc", "muon_host_free"]
+           "muon_host_alloc", "muon_host_free", "muon_layer_norm", "muon_layer_norm_backward",
+           "muon_layer_norm_workspace_bytes", "muon_dropout", "muon_route", "muon_route_backward",
+           "muon_route_workspace_bytes"]
 
 STATIC_WORKSPACE_BYTES = 32 << 20   # MUON_STATIC_WORKSPACE_BYTES in include/muon.h
 
@@ -124,6 +126,16 @@ def load(path: str = LIB_PATH):
     L.muon_plan_partition.argtypes = [vp, ctypes.c_int, ctypes.c_int, ctypes.c_double,
                                       ctypes.c_double, ctypes.POINTER(ctypes.c_int),
                                       ctypes.POINTER(ctypes.c_double)]
+    i32, i64, u64, f32 = ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
+    L.muon_layer_norm.argtypes = [i64, i64, i32, i32, vp, i64, vp, i64, vp, vp, f32, f32, u64, u64,
+                                  vp, vp, vp, vp, vp]
+    L.muon_layer_norm_backward.argtypes = [i64, i64, i32, i32, vp, i64, vp, i64, vp, vp, vp, vp,
+                                           i64, f32, u64, u64, vp, vp, vp, vp, vp, sz, vp]
+    L.muon_layer_norm_workspace_bytes.argtypes = [i64, i64, ctypes.POINTER(sz)]
+    L.muon_dropout.argtypes = [i64, i32, vp, vp, f32, u64, u64, vp, vp]
+    L.muon_route.argtypes = [i64, i32, i32, i32, vp, i64, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.muon_route_workspace_bytes.argtypes = [i64, i32, ctypes.POINTER(sz)]
+    L.muon_route_backward.argtypes = [i64, i32, i32, i32, vp, i64, vp, i32, vp, vp, vp, vp, vp, vp]
     L.muon_plan_destroy.argtypes = [vp]
     L.muon_plan_destroy.restype = None
     L.muon_status_string.argtypes = [ctypes.c_int]
@@ -133,7 +145,9 @@ def load(path: str = LIB_PATH):
                "muon_step_ortho", "muon_workspace_error", "muon_plan_launches",
                "muon_step_static", "muon_step_amp", "muon_adamw_step", "muon_plan_partition",
                "muon_static_error", "muon_step_timed", "muon_step_host",
-               "muon_plan_host_unit_bytes", "muon_host_alloc", "muon_host_free"):
+               "muon_plan_host_unit_bytes", "muon_host_alloc", "muon_host_free", "muon_layer_norm",
+               "muon_layer_norm_backward", "muon_layer_norm_workspace_bytes", "muon_dropout",
+               "muon_route", "muon_route_backward", "muon_route_workspace_bytes"):
         getattr(L, fn).restype = ctypes.c_int
     _lib = L
     return L
