@@ -54,6 +54,36 @@ __device__ __forceinline__ uint32_t half_of(const uint4& w, int j) {
   return (j & 1) ? x >> 16 : x & 0xffffu;
 }
 
+// dropout of eight consecutive elements, the first of index i (which may be
+// below zero where a row's first chunk begins ahead of the row: such elements
+// are not used).  When i is not a multiple of eight the elements straddle two
+// blocks, whose sixteen halves are shifted into place.
+__device__ __forceinline__ void drop8(float2 (&v)[4], int64_t i, const Drop& d) {
+  const uint64_t c = d.offset + (uint64_t)(i >> 3);
+  uint4 w = philox(c, d.k0, d.k1);
+  const int shift = (int)(i & 7);
+  if (shift) {
+    const uint4 n = philox(c + 1, d.k0, d.k1);
+    uint32_t a[8] = {w.x, w.y, w.z, w.w, n.x, n.y, n.z, n.w};
+    if (shift & 4) {
+      #pragma unroll
+      for (int j = 0; j < 6; ++j) a[j] = a[j + 2];
+    }
+    if (shift & 2) {
+      #pragma unroll
+      for (int j = 0; j < 5; ++j) a[j] = a[j + 1];
+    }
+    const uint32_t bits = (shift & 1) * 16;
+    w = make_uint4(__funnelshift_r(a[0], a[1], bits), __funnelshift_r(a[1], a[2], bits),
+                   __funnelshift_r(a[2], a[3], bits), __funnelshift_r(a[3], a[4], bits));
+  }
+  #pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[j].x = half_of(w, 2 * j) >= d.threshold ? v[j].x * d.scale : 0.f;
+    v[j].y = half_of(w, 2 * j + 1) >= d.threshold ? v[j].y * d.scale : 0.f;
+  }
+}
+
 // dropout of one element by its index (a whole generator block for it alone)
 __device__ __forceinline__ float drop_one(float x, uint64_t i, const Drop& d) {
   const uint4 w = philox(d.offset + (i >> 3), d.k0, d.k1);
