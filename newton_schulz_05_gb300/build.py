@@ -20,7 +20,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmuon.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["plan.cpp", "step.cu", "dense.cu", "skinny.cu", "tc_gemm.cu", "noalloc.cu", "adamw.cu",
-           "host.cu", "norm.cu", "dropout.cu", "route.cu"]
+           "host.cu", "norm.cu", "norm_grad.cu", "dropout.cu", "route.cu"]
 
 
 def _nvcc() -> str:
