@@ -1,6 +1,14 @@
 // Dropout from a counter-based generator, alone or added to a residual.
+//
+// Bound by HBM: x (and the residual) read once, y written once; the flags come
+// from the generator, one block for the eight elements of a chunk (random.cuh).
+// A chunk starts at an aligned address, so a tensor that does not has its first
+// chunk begin ahead of it; operands whose addresses are aligned differently
+// are read element by element.  A thread loads all of its chunks before it
+// draws for the first, so the loads cover the generator's latency.
 #include <cmath>
 
+#include "chunk.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "random.cuh"
@@ -9,15 +17,70 @@ namespace muon {
 
 namespace {
 
-template <typename T>
-__global__ void __launch_bounds__(256) dropout_kernel(int64_t n, const T* x, const T* residual,
-                                                      Drop d, T* y) {
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    float v = drop_one(to_f(x[i]), (uint64_t)i, d);
-    if (residual) v += to_f(residual[i]);
-    y[i] = from_f<T>(v);
+constexpr int kDropThreads = 256;
+
+template <typename T, int U, bool RES>
+__global__ void __launch_bounds__(kDropThreads) dropout_kernel(int64_t n, const T* x,
+                                                               const T* residual, Drop d, T* y,
+                                                               int phase, bool vec) {
+  constexpr int P = kPieces<T>;
+  uint4 ux[U][P], ur[U][P];
+  const int64_t first =
+      ((int64_t)blockIdx.x * (U * kDropThreads) + threadIdx.x) * 8 - phase;
+  #pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t i = first + u * (kDropThreads * 8);
+    if (vec && i >= 0 && i + 8 <= n) {
+      #pragma unroll
+      for (int q = 0; q < P; ++q) {
+        ux[u][q] = __ldcs(reinterpret_cast<const uint4*>(x + i) + q);
+        if (RES) ur[u][q] = __ldcs(reinterpret_cast<const uint4*>(residual + i) + q);
+      }
+    }
   }
+  #pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t i = first + u * (kDropThreads * 8);
+    if (vec && i >= 0 && i + 8 <= n) {
+      Chunk c, r;
+      widen(c, ux[u]);
+      drop8(c.v, i, d);
+      if (RES) {
+        widen(r, ur[u]);
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) c.v[j] = add2(c.v[j], r.v[j]);
+      }
+      store8(y + i, c);
+    } else if (i < n) {
+      Chunk c;
+      #pragma unroll
+      for (int j = 0; j < 8; ++j) elem(c, j) = i + j >= 0 && i + j < n ? to_f(x[i + j]) : 0.f;
+      drop8(c.v, i, d);
+      #pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i + j >= 0 && i + j < n)
+          y[i + j] = from_f<T>(RES ? elem(c, j) + to_f(residual[i + j]) : elem(c, j));
+    }
+  }
+}
+
+template <typename T>
+cudaError_t dropout(int64_t n, const void* x, const void* residual, const Drop& d, void* y,
+                    cudaStream_t s) {
+  const T* px = static_cast<const T*>(x);
+  const T* pr = static_cast<const T*>(residual);
+  auto phase_of = [](const void* p) { return (int)(reinterpret_cast<uintptr_t>(p) / sizeof(T) & 7); };
+  const bool vec = phase_of(x) == phase_of(y) && (!residual || phase_of(x) == phase_of(residual));
+  const int phase = vec ? phase_of(x) : 0;
+  constexpr int U = 2;
+  const int64_t blocks = ((n + phase + 7) / 8 + U * kDropThreads - 1) / (U * kDropThreads);
+  if (residual)
+    dropout_kernel<T, U, true><<<(unsigned)blocks, kDropThreads, 0, s>>>(
+        n, px, pr, d, static_cast<T*>(y), phase, vec);
+  else
+    dropout_kernel<T, U, false><<<(unsigned)blocks, kDropThreads, 0, s>>>(
+        n, px, pr, d, static_cast<T*>(y), phase, vec);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -30,6 +93,7 @@ extern "C" muon_status muon_dropout(int64_t n, int dtype, const void* x, const v
                                     float p, uint64_t seed, uint64_t offset, void* y,
                                     void* stream) {
   if (n < 0 || (n > 0 && (!x || !y)) || !(p >= 0.f && p <= 1.f)) return MUON_ERR_INVALID_ARG;
+  if (n > (int64_t)1 << 42) return MUON_ERR_UNSUPPORTED_SHAPE;
   if (dtype != MUON_BF16 && dtype != MUON_F32) return MUON_ERR_DTYPE;
   const size_t es = dtype == MUON_BF16 ? 2 : 4;
   if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(residual) |
@@ -40,15 +104,7 @@ extern "C" muon_status muon_dropout(int64_t n, int dtype, const void* x, const v
   NvtxRange range("muon_dropout");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const Drop d = make_drop(p, seed, offset);
-  const int64_t want = (n + 255) / 256;
-  const int grid = (int)(want < 152 * 8 ? want : 152 * 8);
-  if (dtype == MUON_BF16)
-    dropout_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(
-        n, static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(residual), d,
-        static_cast<__nv_bfloat16*>(y));
-  else
-    dropout_kernel<float><<<grid, 256, 0, s>>>(n, static_cast<const float*>(x),
-                                               static_cast<const float*>(residual), d,
-                                               static_cast<float*>(y));
-  return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  const cudaError_t e = dtype == MUON_BF16 ? dropout<__nv_bfloat16>(n, x, residual, d, y, s)
+                                           : dropout<float>(n, x, residual, d, y, s);
+  return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }

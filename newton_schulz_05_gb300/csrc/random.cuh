@@ -15,12 +15,15 @@
 
 #include <cuda_runtime.h>
 
+#include "chunk.cuh"
+
 namespace muon {
 
 struct Drop {
   uint32_t k0, k1;     // key: low and high word of the seed
   uint64_t offset;     // counter of element 0
-  uint32_t threshold;  // an element is kept when its 16 bits are >= this
+  uint32_t threshold;  // an element is kept when its 16 bits are >= this ...
+  uint32_t high;       // ... which a word shows for its high half by being >= this
   float scale;         // 65536 / (65536 - threshold)
 };
 
@@ -30,6 +33,7 @@ inline Drop make_drop(float p, uint64_t seed, uint64_t offset) {
   d.k1 = (uint32_t)(seed >> 32);
   d.offset = offset;
   d.threshold = (uint32_t)std::floor((double)p * 65536.0 + 0.5);
+  d.high = d.threshold < 65536u ? d.threshold << 16 : 0u;
   d.scale = d.threshold < 65536u ? (float)(65536.0 / (65536.0 - d.threshold)) : 0.f;
   return d;
 }
@@ -59,6 +63,11 @@ __device__ __forceinline__ uint32_t half_of(const uint4& w, int j) {
 // are not used).  When i is not a multiple of eight the elements straddle two
 // blocks, whose sixteen halves are shifted into place.
 __device__ __forceinline__ void drop8(float2 (&v)[4], int64_t i, const Drop& d) {
+  if (d.threshold > 65535u) {      // p = 1
+    #pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = both(0.f);
+    return;
+  }
   const uint64_t c = d.offset + (uint64_t)(i >> 3);
   uint4 w = philox(c, d.k0, d.k1);
   const int shift = (int)(i & 7);
@@ -77,10 +86,12 @@ __device__ __forceinline__ void drop8(float2 (&v)[4], int64_t i, const Drop& d) 
     w = make_uint4(__funnelshift_r(a[0], a[1], bits), __funnelshift_r(a[1], a[2], bits),
                    __funnelshift_r(a[2], a[3], bits), __funnelshift_r(a[3], a[4], bits));
   }
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
   #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    v[j].x = half_of(w, 2 * j) >= d.threshold ? v[j].x * d.scale : 0.f;
-    v[j].y = half_of(w, 2 * j + 1) >= d.threshold ? v[j].y * d.scale : 0.f;
+    const float2 k = mul2(v[j], both(d.scale));
+    v[j].x = (u[j] << 16) >= d.high ? k.x : 0.f;
+    v[j].y = u[j] >= d.high ? k.y : 0.f;
   }
 }
 

@@ -1,7 +1,24 @@
 // Expert router: top-k choice, combine weights, per-expert counts and the
 // balance loss of a token batch, and the gradient of weights and loss.
+//
+// A token's logits live in the registers of G lanes, eight consecutive experts
+// a lane (two or four times eight for more than 256 experts), so one warp takes
+// 32 / G tokens at once and every reduction over experts is log2 G shuffles.  An
+// expert stays with its lane for all of a warp's tokens: probabilities add up
+// in registers, and the gradient's per-expert factors are loaded once.
+//
+// The choice.  Logits map to unsigned keys of the same order.  Each lane sorts
+// its eight once; a pick is then the largest head of the G lists, whose owner
+// drops it.  bf16 keys leave sixteen bits for the complement of the index, so
+// one unsigned maximum settles value and tie; fp32 keys carry the index beside
+// them, and the lowest lane with the largest head wins, its list being sorted
+// stably.
+//
+// Both passes read the logits once from HBM; the forward pass is bound by the
+// instructions of the choice, the gradient by HBM.
 #include <cmath>
 
+#include "chunk.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -11,165 +28,38 @@ namespace {
 
 constexpr int kRouteThreads = 256;
 constexpr int kRouteWarps = kRouteThreads / 32;
-constexpr int kRouteParts = 304;      // blocks of the forward pass, partial sums of each
+constexpr int kRouteParts = 152 * 4;  // blocks of a pass, partial sums of the forward one
 constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxK = 32;
-constexpr int kLane = kRouteMaxExperts / 32;
+constexpr uint32_t kAll = 0xffffffffu;
 
-struct RouteArgs {
+struct RouteFwd {
   int64_t tokens, ld;
   int experts, k, normalize;
+  int vec;              // rows of whole, aligned chunks
   const void* logits;
   const uint8_t* mask;
   float* weights;
   int32_t* index;
-  float* part_p;       // [parts][experts]
-  int32_t* part_c;     // [parts][experts + 1]
+  float* part_p;        // [parts][experts]
+  int32_t* part_c;      // [parts][experts + 1]
+  unsigned* ticket;     // zeroed here for the join
 };
 
-// A key whose unsigned order is the order of the logits: NaN above +inf,
-// -0 equal to +0.  0 is below the key of every value.
-__device__ __forceinline__ uint32_t order_key(float v) {
-  if (v != v) return 0xffffffffu;
-  const uint32_t u = __float_as_uint(v + 0.f);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-constexpr uint32_t kKeyNegInf = 0x007fffffu;   // order_key(-inf)
-
-__device__ __forceinline__ float warp_sum(float v) {
-  #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// One warp a token; expert e belongs to lane e % 32.
-template <typename T>
-__global__ void __launch_bounds__(kRouteThreads) route_kernel(const __grid_constant__ RouteArgs a) {
-  __shared__ float sp[kRouteMaxExperts];
-  __shared__ int sc[kRouteMaxExperts + 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int e = threadIdx.x; e <= a.experts; e += kRouteThreads) {
-    sc[e] = 0;
-    if (e < a.experts) sp[e] = 0.f;
-  }
-  __syncthreads();
-  float acc[kLane];
-  #pragma unroll
-  for (int j = 0; j < kLane; ++j) acc[j] = 0.f;
-  const T* logits = static_cast<const T*>(a.logits);
-  for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < a.tokens;
-       t += (int64_t)gridDim.x * kRouteWarps) {
-    const bool masked = a.mask && !a.mask[t];
-    float v[kLane];
-    uint32_t key[kLane];
-    #pragma unroll
-    for (int j = 0; j < kLane; ++j) {
-      const int e = j * 32 + lane;
-      v[j] = e < a.experts ? to_f(logits[t * a.ld + e]) : -INFINITY;
-      key[j] = e < a.experts ? order_key(v[j]) : 0u;
-    }
-    float top = 0.f, norm = 0.f, p_norm = 0.f;
-    bool routed = !masked;
-    float mine = 0.f;        // lane j holds pick j
-    int mine_e = -1;
-    for (int pick = 0; pick < a.k; ++pick) {
-      uint32_t best = 0;
-      int best_j = 0;
-      #pragma unroll
-      for (int j = 0; j < kLane; ++j)
-        if (key[j] > best) { best = key[j]; best_j = j; }
-      const uint32_t win = __reduce_max_sync(0xffffffffu, best);
-      const uint32_t e = __reduce_min_sync(
-          0xffffffffu, best == win ? (uint32_t)(best_j * 32 + lane) : 0xffffffffu);
-      if (pick == 0) {
-        routed = routed && win > kKeyNegInf;
-        top = win > kKeyNegInf
-            ? __uint_as_float(win == 0xffffffffu ? 0x7fc00000u
-                              : win & 0x80000000u ? win & 0x7fffffffu : ~win)
-            : 0.f;
-        float s = 0.f;
-        #pragma unroll
-        for (int j = 0; j < kLane; ++j) {
-          v[j] = routed ? expf(v[j] - top) : 0.f;
-          s += v[j];
-        }
-        p_norm = warp_sum(s);
-        #pragma unroll
-        for (int j = 0; j < kLane; ++j)
-          if (routed && j * 32 + lane < a.experts) acc[j] += v[j] / p_norm;
-      }
-      const bool ok = routed && win > kKeyNegInf;
-      float x = 0.f;
-      #pragma unroll
-      for (int j = 0; j < kLane; ++j)
-        if (j * 32 + lane == (int)e) {
-          key[j] = 0;
-          x = v[j];
-        }
-      x = __shfl_sync(0xffffffffu, x, (int)(e & 31));
-      if (ok) norm += x;
-      if (lane == pick) {
-        mine = ok ? x : 0.f;
-        mine_e = ok ? (int)e : -1;
-      }
-    }
-    if (lane < a.k) {
-      const float z = a.normalize ? norm : p_norm;
-      a.weights[t * a.k + lane] = mine_e >= 0 ? mine / z : 0.f;
-      a.index[t * a.k + lane] = mine_e;
-      if (mine_e >= 0) atomicAdd(&sc[mine_e], 1);
-    }
-    if (lane == 0 && routed) atomicAdd(&sc[a.experts], 1);
-  }
-  // the block's sums, warp after warp
-  for (int w = 0; w < kRouteWarps; ++w) {
-    if (w == warp) {
-      #pragma unroll
-      for (int j = 0; j < kLane; ++j)
-        if (j * 32 + lane < a.experts) sp[j * 32 + lane] += acc[j];
-    }
-    __syncthreads();
-  }
-  for (int e = threadIdx.x; e <= a.experts; e += kRouteThreads) {
-    if (e < a.experts) a.part_p[(int64_t)blockIdx.x * a.experts + e] = sp[e];
-    a.part_c[(int64_t)blockIdx.x * (a.experts + 1) + e] = sc[e];
-  }
-}
-
-// counts, mean probabilities and the loss from the blocks' partial sums
-__global__ void __launch_bounds__(kRouteThreads) route_join_kernel(
-    int experts, int k, int parts, const float* part_p, const int32_t* part_c, int32_t* counts,
-    float* mean_prob, float* loss) {
-  __shared__ float red[kRouteWarps];
-  __shared__ int routed;
-  int c = 0;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < parts; ++i) c += part_c[(int64_t)i * (experts + 1) + experts];
-    routed = c;
-    counts[experts] = c;
-  }
-  __syncthreads();
-  const float n = (float)(routed > 0 ? routed : 1);
-  float l = 0.f;
-  for (int e = threadIdx.x; e < experts; e += kRouteThreads) {
-    int ce = 0;
-    float p = 0.f;
-    for (int i = 0; i < parts; ++i) {
-      ce += part_c[(int64_t)i * (experts + 1) + e];
-      p += part_p[(int64_t)i * experts + e];
-    }
-    p /= n;
-    counts[e] = ce;
-    mean_prob[e] = p;
-    l = fmaf((float)ce / ((float)k * n), p, l);
-  }
-  l = block_sum<kRouteThreads>(l, red);
-  if (threadIdx.x == 0) *loss = (float)experts * l;
-}
+struct RouteJoin {
+  int experts, k, parts;
+  const float* part_p;
+  const int32_t* part_c;
+  int32_t* counts;
+  float *mean_prob, *loss;
+  float* part_loss;     // one a block
+  unsigned* ticket;
+};
 
 struct RouteBwd {
   int64_t tokens, ld;
   int experts, k, normalize;
+  int vec;
   const void* logits;
   const uint8_t* mask;
   const int32_t *index, *counts;
@@ -177,93 +67,447 @@ struct RouteBwd {
   void* dlogits;
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(
-    const __grid_constant__ RouteBwd a) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const T* logits = static_cast<const T*>(a.logits);
-  const float n = (float)(a.counts[a.experts] > 0 ? a.counts[a.experts] : 1);
-  const float c = a.dloss ? *a.dloss * (float)a.experts / ((float)a.k * n * n) : 0.f;
-  for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < a.tokens;
-       t += (int64_t)gridDim.x * kRouteWarps) {
-    const bool masked = a.mask && !a.mask[t];
-    float v[kLane], g[kLane];
-    float top = -INFINITY;
-    bool nan = false;
-    #pragma unroll
-    for (int j = 0; j < kLane; ++j) {
-      const int e = j * 32 + lane;
-      v[j] = e < a.experts ? to_f(logits[t * a.ld + e]) : -INFINITY;
-      g[j] = e < a.experts ? c * (float)a.counts[e] : 0.f;
-      top = fmaxf(top, v[j]);
-      nan = nan || v[j] != v[j];
+// A key whose unsigned order is the order of the logits; 0 is below every
+// key.  Adding 0 turns -0 into +0 and every NaN into the canonical positive
+// one, which ranks above +inf.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t u = __float_as_uint(v + 0.f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+constexpr uint32_t kKeyNegInf = 0x007fffffu;   // order_key(-inf)
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+// Sum or maximum over the G lanes of a token
+template <int G> __device__ __forceinline__ float group_sum(float v) {
+  #pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+template <int G> __device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  if constexpr (G == 32) return __reduce_max_sync(kAll, v);
+  #pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+
+// The candidates of one lane: next() gives the largest over the group that has
+// not been given yet, as a key and an expert.
+template <typename T, int G, int N> struct Choice;
+
+// bf16: key and index in one word.  N == 8: a sorted list.
+template <int G, int N> struct Choice<__nv_bfloat16, G, N> {
+  uint32_t k[N];
+  __device__ __forceinline__ void set(int j, float v, int e, bool in) {
+    k[j] = in ? (order_key(v) & 0xffff0000u) | (uint32_t)(0xffff - e) : 0u;
+  }
+  __device__ __forceinline__ void order() {
+    if constexpr (N == 8) {
+      auto ce = [&](int a, int b) {
+        const uint32_t hi = max(k[a], k[b]);
+        k[b] = min(k[a], k[b]);
+        k[a] = hi;
+      };
+      // nineteen exchanges (Batcher's odd-even merge of two sorted fours)
+      ce(0, 1); ce(2, 3); ce(4, 5); ce(6, 7);
+      ce(0, 2); ce(1, 3); ce(4, 6); ce(5, 7);
+      ce(1, 2); ce(5, 6);
+      ce(0, 4); ce(1, 5); ce(2, 6); ce(3, 7);
+      ce(2, 4); ce(3, 5);
+      ce(1, 2); ce(3, 4); ce(5, 6);
     }
-    #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    nan = __any_sync(0xffffffffu, nan);
-    const bool routed = !masked && (nan || top > -INFINITY);
-    float s = 0.f;
-    #pragma unroll
-    for (int j = 0; j < kLane; ++j) {
-      v[j] = routed ? expf(v[j] - top) : 0.f;
-      s += v[j];
+  }
+  __device__ __forceinline__ void next(int, uint32_t& key, int& e) {
+    uint32_t head = k[0];
+    if constexpr (N != 8) {
+      #pragma unroll
+      for (int j = 1; j < N; ++j) head = max(head, k[j]);
     }
-    s = warp_sum(s);
-    // picks: lane j holds pick j
-    int e = -1;
-    float dw = 0.f;
-    if (lane < a.k) {
-      e = a.index[t * a.k + lane];
-      if (e < 0 || e >= a.experts) e = -1;
-      if (e >= 0 && a.dweights) dw = a.dweights[t * a.k + lane];
-    }
-    float w = 0.f, add = dw;
-    if (a.normalize) {
-      if (e >= 0) w = expf(to_f(logits[t * a.ld + e]) - top);
-      if (nan && e >= 0) w = NAN;
-      const float z = warp_sum(w);
-      w = z != 0.f ? w / z : 0.f;
-      add = w * (dw - warp_sum(w * dw));
+    const uint32_t win = group_max<G>(head);
+    if constexpr (N == 8) {
+      if (head == win) {
+        #pragma unroll
+        for (int j = 0; j < 7; ++j) k[j] = k[j + 1];
+        k[7] = 0;
+      }
     } else {
-      for (int i = 0; i < a.k; ++i) {
-        const int ei = __shfl_sync(0xffffffffu, e, i);
-        const float di = __shfl_sync(0xffffffffu, dw, i);
+      #pragma unroll
+      for (int j = 0; j < N; ++j) k[j] = k[j] == win ? 0u : k[j];
+    }
+    // the value's low sixteen bits are zeros, in the key's own sense
+    key = win & 0x80000000u ? win & 0xffff0000u : win | 0xffffu;
+    e = 0xffff - (int)(win & 0xffffu);
+  }
+};
+
+// fp32: key and index side by side
+template <int G, int N> struct Choice<float, G, N> {
+  uint32_t k[N];
+  int id[N];
+  __device__ __forceinline__ void set(int j, float v, int e, bool in) {
+    k[j] = in ? order_key(v) : 0u;
+    id[j] = e;
+  }
+  __device__ __forceinline__ void order() {
+    if constexpr (N == 8) {
+      // odd-even transposition: neighbours are exchanged only when out of
+      // order, so equal keys keep their order
+      #pragma unroll
+      for (int r = 0; r < 8; ++r)
         #pragma unroll
-        for (int j = 0; j < kLane; ++j)
-          if (j * 32 + lane == ei) g[j] += di;
+        for (int j = r & 1; j + 1 < 8; j += 2) {
+          const bool s = k[j + 1] > k[j];
+          const uint32_t a = s ? k[j + 1] : k[j], b = s ? k[j] : k[j + 1];
+          const int x = s ? id[j + 1] : id[j], y = s ? id[j] : id[j + 1];
+          k[j] = a; k[j + 1] = b;
+          id[j] = x; id[j + 1] = y;
+        }
+    }
+  }
+  __device__ __forceinline__ void next(int group_lanes, uint32_t& key, int& e) {
+    if constexpr (N == 8) {
+      key = group_max<G>(k[0]);
+      const uint32_t who = __ballot_sync(kAll, k[0] == key) & (uint32_t)group_lanes;
+      const int lane = __ffs(who) - 1;
+      e = __shfl_sync(kAll, id[0], lane);
+      if ((int)(threadIdx.x & 31) == lane) {
+        #pragma unroll
+        for (int j = 0; j < 7; ++j) { k[j] = k[j + 1]; id[j] = id[j + 1]; }
+        k[7] = 0;
+      }
+    } else {      // a lane's experts are not consecutive: the lowest index decides
+      uint32_t head = 0;
+      int first = 0x7fffffff;
+      #pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (k[j] > head) { head = k[j]; first = id[j]; }
+      key = group_max<G>(head);
+      e = (int)__reduce_min_sync(kAll, head == key ? (uint32_t)first : 0x7fffffffu);
+      #pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (id[j] == e) k[j] = 0;
+    }
+  }
+};
+
+// eight logits from column e0 of a row; -inf where there is no expert
+template <typename T>
+__device__ __forceinline__ void logits8(float (&v)[8], const T* row, int e0, int experts, bool vec,
+                                        bool live) {
+  if (live && vec && e0 < experts) {
+    uint4 u[kPieces<T>];
+    #pragma unroll
+    for (int q = 0; q < kPieces<T>; ++q) u[q] = reinterpret_cast<const uint4*>(row + e0)[q];
+    Chunk c;
+    widen(c, u);
+    #pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = elem(c, j);
+  } else {
+    #pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = live && e0 + j < experts ? to_f(row[e0 + j]) : -INFINITY;
+  }
+}
+
+// Lane l of a token's G lanes has experts (c G + l) 8 .. + 7 for c = 0 .. NCH - 1.
+template <typename T, int G, int NCH>
+__global__ void __launch_bounds__(kRouteThreads) route_kernel(const __grid_constant__ RouteFwd a) {
+  constexpr int TPW = 32 / G, N = NCH * 8;
+  constexpr int kStage = TPW * (G * N < kRouteMaxK ? G * N : kRouteMaxK);
+  __shared__ float sp[G * N];
+  __shared__ int sc[G * N + 1];
+  __shared__ float sw[kRouteWarps][kStage];
+  __shared__ int se[kRouteWarps][kStage];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int gl = lane % G, grp = lane / G;
+  const int group_lanes = (int)((G == 32 ? kAll : ((1u << (G & 31)) - 1u) << (grp * G)));
+  for (int e = threadIdx.x; e <= G * N; e += kRouteThreads) {
+    sc[e] = 0;
+    if (e < G * N) sp[e] = 0.f;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+  __syncthreads();
+  float acc[N];
+  #pragma unroll
+  for (int j = 0; j < N; ++j) acc[j] = 0.f;
+  int routed_count = 0;
+  const T* logits = static_cast<const T*>(a.logits);
+  const int64_t stride = (int64_t)gridDim.x * kRouteWarps * TPW;
+  for (int64_t t0 = ((int64_t)blockIdx.x * kRouteWarps + warp) * TPW; t0 < a.tokens; t0 += stride) {
+    const int64_t t = t0 + grp;
+    const bool live = t < a.tokens && !(a.mask && !a.mask[t]);
+    float v[N];
+    Choice<T, G, N> choice;
+    #pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const int e0 = (c * G + gl) * 8;
+      float u[8];
+      logits8<T>(u, logits + t * a.ld, e0, a.experts, a.vec, live);
+      #pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[c * 8 + j] = u[j];
+        choice.set(c * 8 + j, u[j], e0 + j, e0 + j < a.experts);
       }
     }
-    float dot = 0.f;
-    #pragma unroll
-    for (int j = 0; j < kLane; ++j) {
-      v[j] = routed ? v[j] / s : 0.f;
-      dot = fmaf(v[j], g[j], dot);
-    }
-    dot = warp_sum(dot);
-    #pragma unroll
-    for (int j = 0; j < kLane; ++j) v[j] *= g[j] - dot;
-    if (a.normalize) {
-      for (int i = 0; i < a.k; ++i) {
-        const int ei = __shfl_sync(0xffffffffu, e, i);
-        const float di = __shfl_sync(0xffffffffu, add, i);
+    choice.order();
+    float top = 0.f, picked = 0.f, total = 0.f;
+    bool routed = false;
+    float* w = sw[warp] + grp * a.k;
+    int* x = se[warp] + grp * a.k;
+    for (int p = 0; p < a.k; ++p) {
+      uint32_t key;
+      int e;
+      choice.next(group_lanes, key, e);
+      if (p == 0) {
+        routed = live && key > kKeyNegInf;
+        top = key_value(key);
+        float s = 0.f;
         #pragma unroll
-        for (int j = 0; j < kLane; ++j)
-          if (j * 32 + lane == ei) v[j] += di;
+        for (int j = 0; j < N; ++j) {
+          v[j] = __expf(v[j] - top);
+          s += v[j];
+        }
+        total = group_sum<G>(s);
+        if (routed) {
+          const float inv = 1.f / total;
+          #pragma unroll
+          for (int j = 0; j < N; ++j) acc[j] = fmaf(v[j], inv, acc[j]);
+          if (gl == 0) ++routed_count;
+        }
+      }
+      const bool ok = routed && key > kKeyNegInf;
+      const float y = ok ? __expf(key_value(key) - top) : 0.f;
+      picked += y;
+      if (gl == 0) {
+        w[p] = y;
+        x[p] = ok ? e : -1;
+        if (ok) atomicAdd(&sc[e], 1);
       }
     }
+    const float z = a.normalize ? picked : total;
+    __syncwarp();
+    if (t < a.tokens)
+      for (int p = gl; p < a.k; p += G) {
+        const int e = x[p];
+        a.weights[t * a.k + p] = e >= 0 ? w[p] / z : 0.f;
+        a.index[t * a.k + p] = e;
+      }
+    __syncwarp();
+  }
+  if (routed_count) atomicAdd(&sc[G * N], routed_count);
+  // the block's sums: lanes of a warp, then warps in order
+  #pragma unroll
+  for (int o = G; o < 32; o <<= 1)
     #pragma unroll
-    for (int j = 0; j < kLane; ++j) {
-      const int o = j * 32 + lane;
-      if (o < a.experts)
-        static_cast<T*>(a.dlogits)[t * a.experts + o] = from_f<T>(routed ? v[j] : 0.f);
+    for (int j = 0; j < N; ++j) acc[j] += __shfl_xor_sync(kAll, acc[j], o);
+  for (int i = 0; i < kRouteWarps; ++i) {
+    if (i == warp && grp == 0) {
+      #pragma unroll
+      for (int j = 0; j < N; ++j) sp[((j / 8) * G + gl) * 8 + j % 8] += acc[j];
+    }
+    __syncthreads();
+  }
+  for (int e = threadIdx.x; e <= a.experts; e += kRouteThreads) {
+    if (e < a.experts) a.part_p[(int64_t)blockIdx.x * a.experts + e] = sp[e];
+    a.part_c[(int64_t)blockIdx.x * (a.experts + 1) + e] = sc[e < a.experts ? e : G * N];
+  }
+}
+
+// Counts, mean probabilities and the loss from the blocks' partial sums: 32
+// experts a block, eight threads an expert; the block that finishes last adds
+// up the blocks' shares of the loss in order.
+__global__ void __launch_bounds__(256) route_join_kernel(const __grid_constant__ RouteJoin a) {
+  __shared__ float red_p[8][32];
+  __shared__ int red_c[8][32], red_n[8];
+  __shared__ unsigned arrived;
+  pdl_wait();
+  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+  const int e = blockIdx.x * 32 + lane;
+  float p = 0.f;
+  int c = 0, n = 0;
+  if (e < a.experts) {
+    #pragma unroll 4
+    for (int i = row; i < a.parts; i += 8) {
+      p += a.part_p[(int64_t)i * a.experts + e];
+      c += a.part_c[(int64_t)i * (a.experts + 1) + e];
+    }
+  }
+  for (int i = threadIdx.x; i < a.parts; i += 256) n += a.part_c[(int64_t)i * (a.experts + 1) + a.experts];
+  n = __reduce_add_sync(kAll, n);
+  red_p[row][lane] = p;
+  red_c[row][lane] = c;
+  if (lane == 0) red_n[row] = n;
+  __syncthreads();
+  if (row == 0) {
+    n = 0;
+    p = 0.f;
+    c = 0;
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      n += red_n[i];
+      p += red_p[i][lane];
+      c += red_c[i][lane];
+    }
+    const float fn = (float)(n > 0 ? n : 1);
+    p /= fn;
+    if (e < a.experts) {
+      a.counts[e] = c;
+      a.mean_prob[e] = p;
+    }
+    if (blockIdx.x == 0 && lane == 0) a.counts[a.experts] = n;
+    const float l = group_sum<32>((float)c / ((float)a.k * fn) * p);
+    if (lane == 0) {
+      if (gridDim.x == 1) {
+        *a.loss = (float)a.experts * l;
+      } else {
+        a.part_loss[blockIdx.x] = l;
+        __threadfence();
+        arrived = atomicAdd(a.ticket, 1u);
+      }
+    }
+    __syncwarp();
+    if (gridDim.x > 1 && arrived == gridDim.x - 1) {
+      __threadfence();
+      const float s = group_sum<32>(lane < (int)gridDim.x ? __ldcg(a.part_loss + lane) : 0.f);
+      if (lane == 0) *a.loss = (float)a.experts * s;
     }
   }
 }
 
-int route_blocks(int64_t tokens) {
-  const int64_t b = (tokens + kRouteWarps - 1) / kRouteWarps;
-  return (int)(b < kRouteParts ? b : kRouteParts);
+template <typename T, int G, int NCH>
+__global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(
+    const __grid_constant__ RouteBwd a) {
+  constexpr int TPW = 32 / G, N = NCH * 8, E = G * N;
+  __shared__ alignas(16) float add[kRouteWarps][TPW * E];   // what the picks add, by expert
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int gl = lane % G, grp = lane / G;
+  for (int i = lane; i < TPW * E; i += 32) add[warp][i] = 0.f;
+  __syncwarp();
+  const T* logits = static_cast<const T*>(a.logits);
+  const int routed_tokens = a.counts[a.experts];
+  const float n = (float)(routed_tokens > 0 ? routed_tokens : 1);
+  const float f = a.dloss ? *a.dloss * (float)a.experts / ((float)a.k * n) / n : 0.f;
+  float b[N];            // the loss's gradient by probability
+  #pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int e = ((j / 8) * G + gl) * 8 + j % 8;
+    b[j] = e < a.experts ? f * (float)a.counts[e] : 0.f;
+  }
+  float* mine = add[warp] + grp * E;
+  const int64_t stride = (int64_t)gridDim.x * kRouteWarps * TPW;
+  for (int64_t t0 = ((int64_t)blockIdx.x * kRouteWarps + warp) * TPW; t0 < a.tokens; t0 += stride) {
+    const int64_t t = t0 + grp;
+    const bool live = t < a.tokens && !(a.mask && !a.mask[t]);
+    float v[N];
+    uint32_t best = 0;
+    #pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const int e0 = (c * G + gl) * 8;
+      float u[8];
+      logits8<T>(u, logits + t * a.ld, e0, a.experts, a.vec, live);
+      #pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[c * 8 + j] = u[j];
+        best = max(best, order_key(u[j]));
+      }
+    }
+    best = group_max<G>(best);
+    const bool routed = live && best > kKeyNegInf;
+    const float top = key_value(best);
+    float s = 0.f;
+    #pragma unroll
+    for (int j = 0; j < N; ++j) {
+      v[j] = __expf(v[j] - top);
+      s += v[j];
+    }
+    const float inv = 1.f / group_sum<G>(s);
+    // the picks, a lane each: what they add goes to their experts' places
+    float z = 0.f, wd = 0.f;
+    if (a.normalize) {
+      for (int p = gl; p < a.k; p += G) {
+        const int e = routed ? a.index[t * a.k + p] : -1;
+        if (e >= 0 && e < a.experts) {
+          const float w = __expf(to_f(logits[t * a.ld + e]) - top);
+          z += w;
+          if (a.dweights) wd = fmaf(w, a.dweights[t * a.k + p], wd);
+        }
+      }
+      z = group_sum<G>(z);
+      wd = group_sum<G>(wd) / z;
+    }
+    if (routed && a.dweights)
+      for (int p = gl; p < a.k; p += G) {
+        const int e = a.index[t * a.k + p];
+        if (e >= 0 && e < a.experts) {
+          float d = a.dweights[t * a.k + p];
+          if (a.normalize) d = __expf(to_f(logits[t * a.ld + e]) - top) / z * (d - wd);
+          mine[e] = d;
+        }
+      }
+    __syncwarp();
+    float extra[N];
+    float dot = 0.f;
+    #pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const float4* q = reinterpret_cast<const float4*>(mine + (c * G + gl) * 8);
+      const float4 q0 = q[0], q1 = q[1];
+      extra[c * 8 + 0] = q0.x; extra[c * 8 + 1] = q0.y; extra[c * 8 + 2] = q0.z;
+      extra[c * 8 + 3] = q0.w; extra[c * 8 + 4] = q1.x; extra[c * 8 + 5] = q1.y;
+      extra[c * 8 + 6] = q1.z; extra[c * 8 + 7] = q1.w;
+    }
+    #pragma unroll
+    for (int j = 0; j < N; ++j) {
+      v[j] *= inv;
+      dot = fmaf(v[j], a.normalize ? b[j] : b[j] + extra[j], dot);
+    }
+    dot = group_sum<G>(dot);
+    #pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const float y = a.normalize ? fmaf(v[j], b[j] - dot, extra[j]) : v[j] * (b[j] + extra[j] - dot);
+      v[j] = routed ? y : 0.f;
+    }
+    __syncwarp();
+    if (routed && a.dweights)
+      for (int p = gl; p < a.k; p += G) {
+        const int e = a.index[t * a.k + p];
+        if (e >= 0 && e < a.experts) mine[e] = 0.f;
+      }
+    if (t < a.tokens) {
+      #pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        const int e0 = (c * G + gl) * 8;
+        T* out = static_cast<T*>(a.dlogits) + t * a.experts + e0;
+        if (a.vec && e0 < a.experts) {
+          Chunk o;
+          #pragma unroll
+          for (int j = 0; j < 8; ++j) elem(o, j) = v[c * 8 + j];
+          store8(out, o);
+        } else {
+          #pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (e0 + j < a.experts) out[j] = from_f<T>(v[c * 8 + j]);
+        }
+      }
+    }
+    __syncwarp();
+  }
 }
+
+// lanes a token
+int lanes_of(int experts) {
+  int g = 1;
+  while (g < 32 && g * 8 < experts) g *= 2;
+  return g;
+}
+
+// blocks of a pass: one for every token group, up to four an SM
+int route_blocks(int64_t tokens, int experts) {
+  const int per = kRouteWarps * 32 / lanes_of(experts);
+  const int64_t b = (tokens + per - 1) / per;
+  return (int)(b < 1 ? 1 : b < kRouteParts ? b : kRouteParts);
+}
+
+int join_blocks(int experts) { return (experts + 31) / 32; }
 
 bool misaligned(const void* p, size_t es) { return reinterpret_cast<uintptr_t>(p) % es != 0; }
 
@@ -276,9 +520,54 @@ muon_status check_route(int64_t tokens, int experts, int k, int dtype, int64_t l
   return MUON_OK;
 }
 
-size_t counts_offset(int64_t tokens, int experts) {
-  return ((size_t)route_blocks(tokens) * experts * sizeof(float) + 255) / 256 * 256;
+// every row of p in whole, 16-byte aligned chunks
+bool whole_rows(const void* p, int64_t tokens, int64_t ld, int experts, size_t es) {
+  return experts % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 &&
+         (tokens <= 1 || (size_t)ld * es % 16 == 0);
 }
+
+// workspace: ticket and shares of the loss, counts, probabilities
+constexpr size_t kJoinBytes = 256;
+size_t probs_offset(int64_t tokens, int experts) {
+  return kJoinBytes +
+         ((size_t)route_blocks(tokens, experts) * (experts + 1) * sizeof(int32_t) + 255) / 256 * 256;
+}
+
+template <typename F>
+cudaError_t by_experts(int dtype, int experts, F f) {
+  auto pick = [&](auto t) -> cudaError_t {
+    using T = decltype(t);
+    if (experts <= 8) return f.template operator()<T, 1, 1>();
+    if (experts <= 16) return f.template operator()<T, 2, 1>();
+    if (experts <= 32) return f.template operator()<T, 4, 1>();
+    if (experts <= 64) return f.template operator()<T, 8, 1>();
+    if (experts <= 128) return f.template operator()<T, 16, 1>();
+    if (experts <= 256) return f.template operator()<T, 32, 1>();
+    if (experts <= 512) return f.template operator()<T, 32, 2>();
+    return f.template operator()<T, 32, 4>();
+  };
+  return dtype == MUON_BF16 ? pick(__nv_bfloat16()) : pick(float());
+}
+
+struct LaunchFwd {
+  const RouteFwd& a;
+  int blocks;
+  cudaStream_t s;
+  template <typename T, int G, int NCH> cudaError_t operator()() const {
+    route_kernel<T, G, NCH><<<blocks, kRouteThreads, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+};
+
+struct LaunchBwd {
+  const RouteBwd& a;
+  int blocks;
+  cudaStream_t s;
+  template <typename T, int G, int NCH> cudaError_t operator()() const {
+    route_bwd_kernel<T, G, NCH><<<blocks, kRouteThreads, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+};
 
 }  // namespace
 
@@ -289,8 +578,8 @@ using namespace muon;
 extern "C" muon_status muon_route_workspace_bytes(int64_t tokens, int experts, size_t* out) {
   if (!out || tokens < 0) return MUON_ERR_INVALID_ARG;
   if (experts < 1 || experts > kRouteMaxExperts) return MUON_ERR_UNSUPPORTED_SHAPE;
-  *out = counts_offset(tokens, experts) +
-         (size_t)route_blocks(tokens) * (experts + 1) * sizeof(int32_t) + 256;
+  *out = probs_offset(tokens, experts) +
+         (size_t)route_blocks(tokens, experts) * experts * sizeof(float);
   return MUON_OK;
 }
 
@@ -314,18 +603,20 @@ extern "C" muon_status muon_route(int64_t tokens, int experts, int k, int dtype,
   if (fault_switch() == kFaultLaunch) return MUON_ERR_CUDA;
   NvtxRange range("muon_route");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int blocks = route_blocks(tokens);
-  RouteArgs a = {tokens, ld, experts, k, normalize, logits, token_mask, weights, index,
-                 static_cast<float*>(workspace),
-                 reinterpret_cast<int32_t*>(static_cast<char*>(workspace) +
-                                            counts_offset(tokens, experts))};
-  if (blocks > 0) {
-    if (dtype == MUON_BF16) route_kernel<__nv_bfloat16><<<blocks, kRouteThreads, 0, s>>>(a);
-    else route_kernel<float><<<blocks, kRouteThreads, 0, s>>>(a);
+  const int blocks = route_blocks(tokens, experts);
+  char* ws = static_cast<char*>(workspace);
+  const size_t es = dtype == MUON_BF16 ? 2 : 4;
+  const RouteFwd a = {tokens, ld, experts, k, normalize,
+                      whole_rows(logits, tokens, ld, experts, es), logits, token_mask, weights,
+                      index, reinterpret_cast<float*>(ws + probs_offset(tokens, experts)),
+                      reinterpret_cast<int32_t*>(ws + kJoinBytes), reinterpret_cast<unsigned*>(ws)};
+  cudaError_t e = by_experts(dtype, experts, LaunchFwd{a, blocks, s});
+  if (e == cudaSuccess) {
+    const RouteJoin j = {experts, k, blocks, a.part_p, a.part_c, counts, mean_prob, loss,
+                         reinterpret_cast<float*>(ws) + 1, a.ticket};
+    e = launch_k(route_join_kernel, dim3(join_blocks(experts)), dim3(256), 0, s, true, j);
   }
-  route_join_kernel<<<1, kRouteThreads, 0, s>>>(experts, k, blocks, a.part_p, a.part_c, counts,
-                                                mean_prob, loss);
-  return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
 
 extern "C" muon_status muon_route_backward(int64_t tokens, int experts, int k, int dtype,
@@ -345,11 +636,11 @@ extern "C" muon_status muon_route_backward(int64_t tokens, int experts, int k, i
   if (tokens == 0) return MUON_OK;
   NvtxRange range("muon_route_backward");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const RouteBwd a = {tokens, ld, experts, k, normalize, logits, token_mask, index, counts,
-                      dweights, dloss, dlogits};
-  const int64_t want = (tokens + kRouteWarps - 1) / kRouteWarps;
-  const int blocks = (int)(want < 152 * 4 ? want : 152 * 4);
-  if (dtype == MUON_BF16) route_bwd_kernel<__nv_bfloat16><<<blocks, kRouteThreads, 0, s>>>(a);
-  else route_bwd_kernel<float><<<blocks, kRouteThreads, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  const RouteBwd a = {tokens, ld, experts, k, normalize,
+                      whole_rows(logits, tokens, ld, experts, es) &&
+                          reinterpret_cast<uintptr_t>(dlogits) % 16 == 0,
+                      logits, token_mask, index, counts, dweights, dloss, dlogits};
+  const cudaError_t e =
+      by_experts(dtype, experts, LaunchBwd{a, route_blocks(tokens, experts), s});
+  return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }

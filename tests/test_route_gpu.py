@@ -172,6 +172,15 @@ def test_nan_and_inf_of_a_routed_token(layers):
         assert np.isfinite(np.delete(g, [3, 4], 0)).all() and np.isnan(g[3]).any() and np.isnan(g[4]).any()
 
 
+def test_nan_of_either_sign_ranks_first(layers):
+    for dtype in (BF, F32):
+        l = draw(6, 100, dtype, 14)
+        l[1, 70], l[2, 3] = float("nan"), -l.new_tensor(float("nan"))
+        l[2, 50] = float("inf")
+        idx = layers.route_forward(l, 2).index.cpu().numpy()
+        assert idx[1, 0] == 70 and list(idx[2]) == [3, 50]
+
+
 def test_indices_out_of_range_are_missing_picks(layers):
     l = draw(30, 16, F32, 8)
     o = layers.route_forward(l, 3)
