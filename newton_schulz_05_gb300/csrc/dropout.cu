@@ -20,47 +20,49 @@ namespace {
 constexpr int kDropThreads = 256;
 
 template <typename T, int U, bool RES>
-__global__ void __launch_bounds__(kDropThreads) dropout_kernel(int64_t n, const T* x,
-                                                               const T* residual, Drop d, T* y,
-                                                               int phase, bool vec) {
-  constexpr int P = kPieces<T>;
-  uint4 ux[U][P], ur[U][P];
-  const int64_t first =
-      ((int64_t)blockIdx.x * (U * kDropThreads) + threadIdx.x) * 8 - phase;
-  #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t i = first + u * (kDropThreads * 8);
-    if (vec && i >= 0 && i + 8 <= n) {
+__global__ void __launch_bounds__(kDropThreads, 4)
+dropout_kernel(int64_t n, const T* x, const T* residual, const __grid_constant__ Drop d, T* y,
+               int phase, bool vec) {
+  constexpr int P = kPieces<T>, kSpan = U * kDropThreads * 8;   // elements a block
+  const int64_t block = (int64_t)blockIdx.x * kSpan - phase;
+  const int64_t first = block + threadIdx.x * 8;
+  if (vec && block >= 0 && block + kSpan <= n) {
+    const uint4* px = reinterpret_cast<const uint4*>(x + first);
+    const uint4* pr = reinterpret_cast<const uint4*>(residual + (RES ? first : 0));
+    uint4 ux[U][P], ur[U][P];
+    #pragma unroll
+    for (int u = 0; u < U; ++u) {
       #pragma unroll
       for (int q = 0; q < P; ++q) {
-        ux[u][q] = __ldcs(reinterpret_cast<const uint4*>(x + i) + q);
-        if (RES) ur[u][q] = __ldcs(reinterpret_cast<const uint4*>(residual + i) + q);
+        ux[u][q] = px[u * kDropThreads * P + q];
+        if (RES) ur[u][q] = pr[u * kDropThreads * P + q];
       }
     }
-  }
-  #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t i = first + u * (kDropThreads * 8);
-    if (vec && i >= 0 && i + 8 <= n) {
+    #pragma unroll
+    for (int u = 0; u < U; ++u) {
       Chunk c, r;
       widen(c, ux[u]);
-      drop8(c.v, i, d);
+      drop8(c.v, first + u * (kDropThreads * 8), d);
       if (RES) {
         widen(r, ur[u]);
         #pragma unroll
         for (int j = 0; j < 4; ++j) c.v[j] = add2(c.v[j], r.v[j]);
       }
-      store8(y + i, c);
-    } else if (i < n) {
-      Chunk c;
-      #pragma unroll
-      for (int j = 0; j < 8; ++j) elem(c, j) = i + j >= 0 && i + j < n ? to_f(x[i + j]) : 0.f;
-      drop8(c.v, i, d);
-      #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (i + j >= 0 && i + j < n)
-          y[i + j] = from_f<T>(RES ? elem(c, j) + to_f(residual[i + j]) : elem(c, j));
+      store8(y + first + u * (kDropThreads * 8), c);
     }
+    return;
+  }
+  for (int u = 0; u < U; ++u) {       // the tensor's ends, or differently aligned operands
+    const int64_t i = first + u * (kDropThreads * 8);
+    if (i >= n) break;
+    Chunk c;
+    #pragma unroll
+    for (int j = 0; j < 8; ++j) elem(c, j) = i + j >= 0 && i + j < n ? to_f(x[i + j]) : 0.f;
+    drop8(c.v, i, d);
+    #pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + j >= 0 && i + j < n)
+        y[i + j] = from_f<T>(RES ? elem(c, j) + to_f(residual[i + j]) : elem(c, j));
   }
 }
 
@@ -72,7 +74,7 @@ cudaError_t dropout(int64_t n, const void* x, const void* residual, const Drop& 
   auto phase_of = [](const void* p) { return (int)(reinterpret_cast<uintptr_t>(p) / sizeof(T) & 7); };
   const bool vec = phase_of(x) == phase_of(y) && (!residual || phase_of(x) == phase_of(residual));
   const int phase = vec ? phase_of(x) : 0;
-  constexpr int U = 2;
+  constexpr int U = 8 / (int)sizeof(T);      // 64 bytes of an operand a thread
   const int64_t blocks = ((n + phase + 7) / 8 + U * kDropThreads - 1) / (U * kDropThreads);
   if (residual)
     dropout_kernel<T, U, true><<<(unsigned)blocks, kDropThreads, 0, s>>>(

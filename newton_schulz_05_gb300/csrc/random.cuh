@@ -20,7 +20,7 @@
 namespace muon {
 
 struct Drop {
-  uint32_t k0, k1;     // key: low and high word of the seed
+  uint32_t key[20];    // the rounds' keys, two a round (kernel parameters: constant operands)
   uint64_t offset;     // counter of element 0
   uint32_t threshold;  // an element is kept when its 16 bits are >= this ...
   uint32_t high;       // ... which a word shows for its high half by being >= this
@@ -29,8 +29,10 @@ struct Drop {
 
 inline Drop make_drop(float p, uint64_t seed, uint64_t offset) {
   Drop d;
-  d.k0 = (uint32_t)seed;
-  d.k1 = (uint32_t)(seed >> 32);
+  for (int r = 0; r < 10; ++r) {
+    d.key[2 * r] = (uint32_t)seed + r * 0x9E3779B9u;
+    d.key[2 * r + 1] = (uint32_t)(seed >> 32) + r * 0xBB67AE85u;
+  }
   d.offset = offset;
   d.threshold = (uint32_t)std::floor((double)p * 65536.0 + 0.5);
   d.high = d.threshold < 65536u ? d.threshold << 16 : 0u;
@@ -38,13 +40,13 @@ inline Drop make_drop(float p, uint64_t seed, uint64_t offset) {
   return d;
 }
 
-__device__ __forceinline__ uint4 philox(uint64_t counter, uint32_t k0, uint32_t k1) {
+__device__ __forceinline__ uint4 philox(uint64_t counter, const Drop& d) {
   uint32_t c0 = (uint32_t)counter, c1 = (uint32_t)(counter >> 32), c2 = 0, c3 = 0;
   #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
-    c0 = (uint32_t)(b >> 32) ^ c1 ^ (k0 + r * 0x9E3779B9u);
-    c2 = (uint32_t)(a >> 32) ^ c3 ^ (k1 + r * 0xBB67AE85u);
+    c0 = (uint32_t)(b >> 32) ^ c1 ^ d.key[2 * r];
+    c2 = (uint32_t)(a >> 32) ^ c3 ^ d.key[2 * r + 1];
     c1 = (uint32_t)b;
     c3 = (uint32_t)a;
   }
@@ -69,10 +71,10 @@ __device__ __forceinline__ void drop8(float2 (&v)[4], int64_t i, const Drop& d) 
     return;
   }
   const uint64_t c = d.offset + (uint64_t)(i >> 3);
-  uint4 w = philox(c, d.k0, d.k1);
+  uint4 w = philox(c, d);
   const int shift = (int)(i & 7);
   if (shift) {
-    const uint4 n = philox(c + 1, d.k0, d.k1);
+    const uint4 n = philox(c + 1, d);
     uint32_t a[8] = {w.x, w.y, w.z, w.w, n.x, n.y, n.z, n.w};
     if (shift & 4) {
       #pragma unroll
@@ -97,7 +99,7 @@ __device__ __forceinline__ void drop8(float2 (&v)[4], int64_t i, const Drop& d) 
 
 // dropout of one element by its index (a whole generator block for it alone)
 __device__ __forceinline__ float drop_one(float x, uint64_t i, const Drop& d) {
-  const uint4 w = philox(d.offset + (i >> 3), d.k0, d.k1);
+  const uint4 w = philox(d.offset + (i >> 3), d);
   return half_of(w, (int)(i & 7)) >= d.threshold ? x * d.scale : 0.f;
 }
 

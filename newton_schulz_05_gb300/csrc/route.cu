@@ -26,9 +26,10 @@ namespace muon {
 
 namespace {
 
-constexpr int kRouteThreads = 256;
+constexpr int kRouteThreads = 512;
 constexpr int kRouteWarps = kRouteThreads / 32;
-constexpr int kRouteParts = 152 * 4;  // blocks of a pass, partial sums of the forward one
+constexpr int kRouteParts = 152 * 2;  // blocks of a pass, partial sums of the forward one
+constexpr int kJoinExperts = 8;       // experts of a block of the join
 constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxK = 32;
 constexpr uint32_t kAll = 0xffffffffu;
@@ -44,6 +45,8 @@ struct RouteFwd {
   float* part_p;        // [parts][experts]
   int32_t* part_c;      // [parts][experts + 1]
   unsigned* ticket;     // zeroed here for the join
+  int32_t* counts;      // written here when one block does it all
+  float *mean_prob, *loss;
 };
 
 struct RouteJoin {
@@ -79,6 +82,14 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
+// exp(v - top): the difference is rounded once, so the relative error is that
+// of the difference, a few units more for 2^x; below 2^-126 the result is 0
+__device__ __forceinline__ float exp_below(float v, float top) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((v - top) * 1.4426950408889634f));
+  return y;
+}
+
 // Sum or maximum over the G lanes of a token
 template <int G> __device__ __forceinline__ float group_sum(float v) {
   #pragma unroll
@@ -93,7 +104,8 @@ template <int G> __device__ __forceinline__ uint32_t group_max(uint32_t v) {
 }
 
 // The candidates of one lane: next() gives the largest over the group that has
-// not been given yet, as a key and an expert.
+// not been given yet, as a word that value() and expert() read (for fp32 the
+// expert comes beside it).
 template <typename T, int G, int N> struct Choice;
 
 // bf16: key and index in one word.  N == 8: a sorted list.
@@ -118,7 +130,7 @@ template <int G, int N> struct Choice<__nv_bfloat16, G, N> {
       ce(1, 2); ce(3, 4); ce(5, 6);
     }
   }
-  __device__ __forceinline__ void next(int, uint32_t& key, int& e) {
+  __device__ __forceinline__ uint32_t next(int, int&) {
     uint32_t head = k[0];
     if constexpr (N != 8) {
       #pragma unroll
@@ -135,9 +147,14 @@ template <int G, int N> struct Choice<__nv_bfloat16, G, N> {
       #pragma unroll
       for (int j = 0; j < N; ++j) k[j] = k[j] == win ? 0u : k[j];
     }
-    // the value's low sixteen bits are zeros, in the key's own sense
-    key = win & 0x80000000u ? win & 0xffff0000u : win | 0xffffu;
-    e = 0xffff - (int)(win & 0xffffu);
+    return win;
+  }
+  // the value's low sixteen bits are zeros, in the key's own sense
+  static __device__ __forceinline__ uint32_t key(uint32_t win) {
+    return win & 0x80000000u ? win & 0xffff0000u : win | 0xffffu;
+  }
+  static __device__ __forceinline__ int expert(uint32_t win, int) {
+    return 0xffff - (int)(win & 0xffffu);
   }
 };
 
@@ -165,10 +182,11 @@ template <int G, int N> struct Choice<float, G, N> {
         }
     }
   }
-  __device__ __forceinline__ void next(int group_lanes, uint32_t& key, int& e) {
+  __device__ __forceinline__ uint32_t next(int group_lanes, int& e) {
+    uint32_t win;
     if constexpr (N == 8) {
-      key = group_max<G>(k[0]);
-      const uint32_t who = __ballot_sync(kAll, k[0] == key) & (uint32_t)group_lanes;
+      win = group_max<G>(k[0]);
+      const uint32_t who = __ballot_sync(kAll, k[0] == win) & (uint32_t)group_lanes;
       const int lane = __ffs(who) - 1;
       e = __shfl_sync(kAll, id[0], lane);
       if ((int)(threadIdx.x & 31) == lane) {
@@ -182,67 +200,94 @@ template <int G, int N> struct Choice<float, G, N> {
       #pragma unroll
       for (int j = 0; j < N; ++j)
         if (k[j] > head) { head = k[j]; first = id[j]; }
-      key = group_max<G>(head);
-      e = (int)__reduce_min_sync(kAll, head == key ? (uint32_t)first : 0x7fffffffu);
+      win = group_max<G>(head);
+      e = (int)__reduce_min_sync(kAll, head == win ? (uint32_t)first : 0x7fffffffu);
       #pragma unroll
       for (int j = 0; j < N; ++j)
         if (id[j] == e) k[j] = 0;
     }
+    return win;
+  }
+  static __device__ __forceinline__ uint32_t key(uint32_t win) { return win; }
+  static __device__ __forceinline__ int expert(uint32_t, int e) { return e; }
+};
+
+// One token's logits as a lane holds them: its chunks as loaded (rows of whole,
+// aligned chunks), so that the next token's can be in flight while this one is
+// worked on, and the mask's verdict.
+template <typename T, int G, int NCH> struct Logits {
+  uint4 u[NCH][kPieces<T>];
+  bool live;
+  template <typename A>
+  __device__ __forceinline__ void load(const A& a, int64_t t, int gl) {
+    live = t < a.tokens && !(a.mask && !a.mask[t]);
+    if (!a.vec || t >= a.tokens) return;
+    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    #pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const int e0 = (c * G + gl) * 8;
+      if (e0 < a.experts) {
+        #pragma unroll
+        for (int q = 0; q < kPieces<T>; ++q) u[c][q] = __ldg(reinterpret_cast<const uint4*>(row + e0) + q);
+      }
+    }
+  }
+  // chunk c in fp32; -inf where there is no expert, and for a masked token
+  template <typename A>
+  __device__ __forceinline__ void get(float (&v)[8], const A& a, int64_t t, int c, int gl) const {
+    const int e0 = (c * G + gl) * 8;
+    if (a.vec) {
+      Chunk w;
+      widen(w, u[c]);
+      #pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = live && e0 < a.experts ? elem(w, j) : -INFINITY;
+    } else {
+      const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+      #pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = live && e0 + j < a.experts ? to_f(row[e0 + j]) : -INFINITY;
+    }
   }
 };
 
-// eight logits from column e0 of a row; -inf where there is no expert
-template <typename T>
-__device__ __forceinline__ void logits8(float (&v)[8], const T* row, int e0, int experts, bool vec,
-                                        bool live) {
-  if (live && vec && e0 < experts) {
-    uint4 u[kPieces<T>];
-    #pragma unroll
-    for (int q = 0; q < kPieces<T>; ++q) u[q] = reinterpret_cast<const uint4*>(row + e0)[q];
-    Chunk c;
-    widen(c, u);
-    #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = elem(c, j);
-  } else {
-    #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = live && e0 + j < experts ? to_f(row[e0 + j]) : -INFINITY;
-  }
-}
-
 // Lane l of a token's G lanes has experts (c G + l) 8 .. + 7 for c = 0 .. NCH - 1.
 template <typename T, int G, int NCH>
-__global__ void __launch_bounds__(kRouteThreads) route_kernel(const __grid_constant__ RouteFwd a) {
-  constexpr int TPW = 32 / G, N = NCH * 8;
-  constexpr int kStage = TPW * (G * N < kRouteMaxK ? G * N : kRouteMaxK);
-  __shared__ float sp[G * N];
-  __shared__ int sc[G * N + 1];
-  __shared__ float sw[kRouteWarps][kStage];
+__global__ void __launch_bounds__(kRouteThreads, NCH == 1 ? 2 : 1)
+route_kernel(const __grid_constant__ RouteFwd a) {
+  constexpr int TPW = 32 / G, N = NCH * 8, E = G * N;
+  constexpr int kStage = TPW * (E < kRouteMaxK ? E : kRouteMaxK);
+  // warps whose sums are added side by side
+  constexpr int kRows = E <= 256 ? kRouteWarps : 2;
+  __shared__ float sp[kRows][E];
+  __shared__ int sc[E + 1];
+  __shared__ uint32_t sw[kRouteWarps][kStage];     // picks: the winning words, then weights
   __shared__ int se[kRouteWarps][kStage];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gl = lane % G, grp = lane / G;
   const int group_lanes = (int)((G == 32 ? kAll : ((1u << (G & 31)) - 1u) << (grp * G)));
-  for (int e = threadIdx.x; e <= G * N; e += kRouteThreads) {
-    sc[e] = 0;
-    if (e < G * N) sp[e] = 0.f;
-  }
+  for (int e = threadIdx.x; e <= E; e += kRouteThreads) sc[e] = 0;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
   __syncthreads();
   float acc[N];
   #pragma unroll
   for (int j = 0; j < N; ++j) acc[j] = 0.f;
   int routed_count = 0;
-  const T* logits = static_cast<const T*>(a.logits);
   const int64_t stride = (int64_t)gridDim.x * kRouteWarps * TPW;
-  for (int64_t t0 = ((int64_t)blockIdx.x * kRouteWarps + warp) * TPW; t0 < a.tokens; t0 += stride) {
+  const int64_t begin = ((int64_t)blockIdx.x * kRouteWarps + warp) * TPW;
+  Logits<T, G, NCH> now, next;
+  next.load(a, begin + grp, gl);
+  uint32_t* const w = sw[warp] + grp * a.k;
+  int* const x = se[warp] + grp * a.k;
+  for (int64_t t0 = begin; t0 < a.tokens; t0 += stride) {
     const int64_t t = t0 + grp;
-    const bool live = t < a.tokens && !(a.mask && !a.mask[t]);
+    now = next;
+    next.load(a, t + stride, gl);
     float v[N];
     Choice<T, G, N> choice;
     #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       const int e0 = (c * G + gl) * 8;
       float u[8];
-      logits8<T>(u, logits + t * a.ld, e0, a.experts, a.vec, live);
+      now.get(u, a, t, c, gl);
       #pragma unroll
       for (int j = 0; j < 8; ++j) {
         v[c * 8 + j] = u[j];
@@ -250,161 +295,230 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const __grid_const
       }
     }
     choice.order();
-    float top = 0.f, picked = 0.f, total = 0.f;
-    bool routed = false;
-    float* w = sw[warp] + grp * a.k;
-    int* x = se[warp] + grp * a.k;
+    uint32_t first = 0;
     for (int p = 0; p < a.k; ++p) {
-      uint32_t key;
-      int e;
-      choice.next(group_lanes, key, e);
-      if (p == 0) {
-        routed = live && key > kKeyNegInf;
-        top = key_value(key);
-        float s = 0.f;
-        #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          v[j] = __expf(v[j] - top);
-          s += v[j];
-        }
-        total = group_sum<G>(s);
-        if (routed) {
-          const float inv = 1.f / total;
-          #pragma unroll
-          for (int j = 0; j < N; ++j) acc[j] = fmaf(v[j], inv, acc[j]);
-          if (gl == 0) ++routed_count;
-        }
-      }
-      const bool ok = routed && key > kKeyNegInf;
-      const float y = ok ? __expf(key_value(key) - top) : 0.f;
-      picked += y;
+      int e = 0;
+      const uint32_t win = choice.next(group_lanes, e);
+      if (p == 0) first = win;
       if (gl == 0) {
-        w[p] = y;
-        x[p] = ok ? e : -1;
-        if (ok) atomicAdd(&sc[e], 1);
+        w[p] = win;
+        if (sizeof(T) == 4) x[p] = e;
       }
     }
-    const float z = a.normalize ? picked : total;
+    first = choice.key(first);
+    const bool routed = now.live && first > kKeyNegInf;
+    const float top = key_value(first);
+    float s = 0.f;
+    #pragma unroll
+    for (int j = 0; j < N; ++j) {
+      v[j] = exp_below(v[j], top);
+      s += v[j];
+    }
+    const float total = group_sum<G>(s);
+    if (routed) {
+      const float inv = __frcp_rn(total);
+      #pragma unroll
+      for (int j = 0; j < N; ++j) acc[j] = fmaf(v[j], inv, acc[j]);
+      if (gl == 0) ++routed_count;
+    }
+    // the picks, a lane each
     __syncwarp();
+    float picked = 0.f;
+    for (int p = gl; p < a.k; p += G) {
+      const uint32_t key = choice.key(w[p]);
+      const bool ok = routed && key > kKeyNegInf;
+      const int e = ok ? choice.expert(w[p], x[p]) : -1;
+      const float y = ok ? exp_below(key_value(key), top) : 0.f;
+      picked += y;
+      w[p] = __float_as_uint(y);
+      x[p] = e;
+      if (ok) atomicAdd(&sc[e], 1);
+    }
+    const float z = __frcp_rn(a.normalize ? group_sum<G>(picked) : total);
     if (t < a.tokens)
       for (int p = gl; p < a.k; p += G) {
         const int e = x[p];
-        a.weights[t * a.k + p] = e >= 0 ? w[p] / z : 0.f;
+        a.weights[t * a.k + p] = e >= 0 ? __uint_as_float(w[p]) * z : 0.f;
         a.index[t * a.k + p] = e;
       }
     __syncwarp();
   }
-  if (routed_count) atomicAdd(&sc[G * N], routed_count);
+  // the join may be set up while the sums are put together
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (routed_count) atomicAdd(&sc[E], routed_count);
   // the block's sums: lanes of a warp, then warps in order
   #pragma unroll
   for (int o = G; o < 32; o <<= 1)
     #pragma unroll
     for (int j = 0; j < N; ++j) acc[j] += __shfl_xor_sync(kAll, acc[j], o);
-  for (int i = 0; i < kRouteWarps; ++i) {
-    if (i == warp && grp == 0) {
+  for (int i = 0; i < kRouteWarps; i += kRows) {
+    if (grp == 0 && warp >= i && warp < i + kRows) {
       #pragma unroll
-      for (int j = 0; j < N; ++j) sp[((j / 8) * G + gl) * 8 + j % 8] += acc[j];
+      for (int j = 0; j < N; ++j) {
+        float& to = sp[warp - i][((j / 8) * G + gl) * 8 + j % 8];
+        to = i ? to + acc[j] : acc[j];
+      }
     }
     __syncthreads();
   }
-  for (int e = threadIdx.x; e <= a.experts; e += kRouteThreads) {
-    if (e < a.experts) a.part_p[(int64_t)blockIdx.x * a.experts + e] = sp[e];
-    a.part_c[(int64_t)blockIdx.x * (a.experts + 1) + e] = sc[e < a.experts ? e : G * N];
+  if (gridDim.x > 1) {
+    for (int e = threadIdx.x; e <= a.experts; e += kRouteThreads) {
+      if (e < a.experts) {
+        float p = 0.f;
+        #pragma unroll
+        for (int i = 0; i < kRows; ++i) p += sp[i][e];
+        a.part_p[(int64_t)blockIdx.x * a.experts + e] = p;
+      }
+      a.part_c[(int64_t)blockIdx.x * (a.experts + 1) + e] = sc[e < a.experts ? e : E];
+    }
+    return;
+  }
+  // one block: the results themselves
+  const int n = sc[E];
+  const float fn = (float)(n > 0 ? n : 1);
+  float l = 0.f;
+  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) {
+    float p = 0.f;
+    #pragma unroll
+    for (int i = 0; i < kRows; ++i) p += sp[i][e];
+    p /= fn;
+    a.counts[e] = sc[e];
+    a.mean_prob[e] = p;
+    l = fmaf((float)sc[e] / ((float)a.k * fn), p, l);
+  }
+  __shared__ float red[kRouteWarps];
+  l = block_sum<kRouteThreads>(l, red);
+  if (threadIdx.x == 0) {
+    a.counts[a.experts] = n;
+    *a.loss = (float)a.experts * l;
   }
 }
 
-// Counts, mean probabilities and the loss from the blocks' partial sums: 32
-// experts a block, eight threads an expert; the block that finishes last adds
-// up the blocks' shares of the loss in order.
+// Counts, mean probabilities and the loss from the blocks' partial sums: eight
+// experts a block, 32 threads an expert; the block that finishes last adds up
+// the blocks' shares of the loss in order.
 __global__ void __launch_bounds__(256) route_join_kernel(const __grid_constant__ RouteJoin a) {
-  __shared__ float red_p[8][32];
-  __shared__ int red_c[8][32], red_n[8];
+  __shared__ float red_p[8][kJoinExperts];
+  __shared__ int red_c[8][kJoinExperts], red_n[8];
   __shared__ unsigned arrived;
   pdl_wait();
-  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-  const int e = blockIdx.x * 32 + lane;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = lane % kJoinExperts, row = threadIdx.x / kJoinExperts;
+  const int e = blockIdx.x * kJoinExperts + col;
   float p = 0.f;
   int c = 0, n = 0;
   if (e < a.experts) {
-    #pragma unroll 4
-    for (int i = row; i < a.parts; i += 8) {
+    #pragma unroll 5
+    for (int i = row; i < a.parts; i += 256 / kJoinExperts) {
       p += a.part_p[(int64_t)i * a.experts + e];
       c += a.part_c[(int64_t)i * (a.experts + 1) + e];
     }
   }
   for (int i = threadIdx.x; i < a.parts; i += 256) n += a.part_c[(int64_t)i * (a.experts + 1) + a.experts];
   n = __reduce_add_sync(kAll, n);
-  red_p[row][lane] = p;
-  red_c[row][lane] = c;
-  if (lane == 0) red_n[row] = n;
+  #pragma unroll
+  for (int o = kJoinExperts; o < 32; o <<= 1) {
+    p += __shfl_xor_sync(kAll, p, o);
+    c += __shfl_xor_sync(kAll, c, o);
+  }
+  if (lane < kJoinExperts) {
+    red_p[warp][lane] = p;
+    red_c[warp][lane] = c;
+  }
+  if (lane == 0) red_n[warp] = n;
   __syncthreads();
-  if (row == 0) {
-    n = 0;
-    p = 0.f;
-    c = 0;
-    #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      n += red_n[i];
-      p += red_p[i][lane];
-      c += red_c[i][lane];
-    }
-    const float fn = (float)(n > 0 ? n : 1);
-    p /= fn;
-    if (e < a.experts) {
-      a.counts[e] = c;
-      a.mean_prob[e] = p;
-    }
-    if (blockIdx.x == 0 && lane == 0) a.counts[a.experts] = n;
-    const float l = group_sum<32>((float)c / ((float)a.k * fn) * p);
-    if (lane == 0) {
-      if (gridDim.x == 1) {
-        *a.loss = (float)a.experts * l;
-      } else {
-        a.part_loss[blockIdx.x] = l;
-        __threadfence();
-        arrived = atomicAdd(a.ticket, 1u);
-      }
-    }
-    __syncwarp();
-    if (gridDim.x > 1 && arrived == gridDim.x - 1) {
-      __threadfence();
-      const float s = group_sum<32>(lane < (int)gridDim.x ? __ldcg(a.part_loss + lane) : 0.f);
-      if (lane == 0) *a.loss = (float)a.experts * s;
-    }
+  if (warp != 0) return;
+  n = 0;
+  p = 0.f;
+  c = 0;
+  #pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    n += red_n[i];
+    p += red_p[i][col];
+    c += red_c[i][col];
+  }
+  const float fn = (float)(n > 0 ? n : 1);
+  p /= fn;
+  const bool mine = lane < kJoinExperts && e < a.experts;
+  if (mine) {
+    a.counts[e] = c;
+    a.mean_prob[e] = p;
+  }
+  if (blockIdx.x == 0 && lane == 0) a.counts[a.experts] = n;
+  const float l = group_sum<32>(mine ? (float)c / ((float)a.k * fn) * p : 0.f);
+  if (lane == 0) {
+    a.part_loss[blockIdx.x] = l;
+    __threadfence();
+    arrived = atomicAdd(a.ticket, 1u);
+  }
+  __syncwarp();
+  if (arrived == gridDim.x - 1) {
+    __threadfence();
+    float s = 0.f;
+    for (int i = lane; i < (int)gridDim.x; i += 32) s += __ldcg(a.part_loss + i);
+    s = group_sum<32>(s);
+    if (lane == 0) *a.loss = (float)a.experts * s;
   }
 }
 
+// The gradient of a logit is p (b - dot + x): b the loss's gradient by the
+// probability, x what the combine weights add at a picked expert, dot the sum
+// over experts of p times the rest.  Unnormalised weights are probabilities, so
+// x = dw and dot counts it.  Normalised ones are w = p / sum of the picks' p, so
+// x = (dw - sum of w dw) / (sum of the picks' p), whose mean under p is zero.
 template <typename T, int G, int NCH>
-__global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(
-    const __grid_constant__ RouteBwd a) {
+__global__ void __launch_bounds__(kRouteThreads, NCH == 1 ? 2 : 1)
+route_bwd_kernel(const __grid_constant__ RouteBwd a) {
   constexpr int TPW = 32 / G, N = NCH * 8, E = G * N;
-  __shared__ alignas(16) float add[kRouteWarps][TPW * E];   // what the picks add, by expert
+  constexpr int KS = ((E < kRouteMaxK ? E : kRouteMaxK) + G - 1) / G;   // picks a lane
+  extern __shared__ float smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gl = lane % G, grp = lane / G;
-  for (int i = lane; i < TPW * E; i += 32) add[warp][i] = 0.f;
+  float* const px = smem + (warp * TPW + grp) * (2 * E);   // exponentials of the token's row
+  float* const xx = px + E;                                // x by expert, zeros between tokens
+  for (int i = gl; i < E; i += G) xx[i] = 0.f;
   __syncwarp();
-  const T* logits = static_cast<const T*>(a.logits);
   const int routed_tokens = a.counts[a.experts];
   const float n = (float)(routed_tokens > 0 ? routed_tokens : 1);
   const float f = a.dloss ? *a.dloss * (float)a.experts / ((float)a.k * n) / n : 0.f;
-  float b[N];            // the loss's gradient by probability
+  float b[N];
   #pragma unroll
   for (int j = 0; j < N; ++j) {
     const int e = ((j / 8) * G + gl) * 8 + j % 8;
     b[j] = e < a.experts ? f * (float)a.counts[e] : 0.f;
   }
-  float* mine = add[warp] + grp * E;
   const int64_t stride = (int64_t)gridDim.x * kRouteWarps * TPW;
-  for (int64_t t0 = ((int64_t)blockIdx.x * kRouteWarps + warp) * TPW; t0 < a.tokens; t0 += stride) {
+  const int64_t begin = ((int64_t)blockIdx.x * kRouteWarps + warp) * TPW;
+  Logits<T, G, NCH> now, next;
+  int e_now[KS], e_next[KS];
+  float d_now[KS], d_next[KS];
+  auto load_picks = [&](int64_t t) {
+    #pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int p = gl + s * G;
+      e_next[s] = -1;
+      d_next[s] = 0.f;
+      if (a.dweights && p < a.k && t < a.tokens) {
+        e_next[s] = a.index[t * a.k + p];
+        d_next[s] = a.dweights[t * a.k + p];
+      }
+    }
+  };
+  next.load(a, begin + grp, gl);
+  load_picks(begin + grp);
+  for (int64_t t0 = begin; t0 < a.tokens; t0 += stride) {
     const int64_t t = t0 + grp;
-    const bool live = t < a.tokens && !(a.mask && !a.mask[t]);
+    now = next;
+    #pragma unroll
+    for (int s = 0; s < KS; ++s) { e_now[s] = e_next[s]; d_now[s] = d_next[s]; }
+    next.load(a, t + stride, gl);
+    load_picks(t + stride);
     float v[N];
     uint32_t best = 0;
     #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-      const int e0 = (c * G + gl) * 8;
       float u[8];
-      logits8<T>(u, logits + t * a.ld, e0, a.experts, a.vec, live);
+      now.get(u, a, t, c, gl);
       #pragma unroll
       for (int j = 0; j < 8; ++j) {
         v[c * 8 + j] = u[j];
@@ -412,76 +526,73 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(
       }
     }
     best = group_max<G>(best);
-    const bool routed = live && best > kKeyNegInf;
+    const bool routed = now.live && best > kKeyNegInf;
     const float top = key_value(best);
     float s = 0.f;
     #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      v[j] = __expf(v[j] - top);
-      s += v[j];
-    }
-    const float inv = 1.f / group_sum<G>(s);
-    // the picks, a lane each: what they add goes to their experts' places
-    float z = 0.f, wd = 0.f;
-    if (a.normalize) {
-      for (int p = gl; p < a.k; p += G) {
-        const int e = routed ? a.index[t * a.k + p] : -1;
-        if (e >= 0 && e < a.experts) {
-          const float w = __expf(to_f(logits[t * a.ld + e]) - top);
-          z += w;
-          if (a.dweights) wd = fmaf(w, a.dweights[t * a.k + p], wd);
-        }
+    for (int c = 0; c < NCH; ++c) {
+      #pragma unroll
+      for (int j = c * 8; j < c * 8 + 8; ++j) {
+        v[j] = exp_below(v[j], top);
+        s += v[j];
       }
-      z = group_sum<G>(z);
-      wd = group_sum<G>(wd) / z;
+      float4* q = reinterpret_cast<float4*>(px + (c * G + gl) * 8);
+      q[0] = make_float4(v[c * 8], v[c * 8 + 1], v[c * 8 + 2], v[c * 8 + 3]);
+      q[1] = make_float4(v[c * 8 + 4], v[c * 8 + 5], v[c * 8 + 6], v[c * 8 + 7]);
     }
-    if (routed && a.dweights)
-      for (int p = gl; p < a.k; p += G) {
-        const int e = a.index[t * a.k + p];
-        if (e >= 0 && e < a.experts) {
-          float d = a.dweights[t * a.k + p];
-          if (a.normalize) d = __expf(to_f(logits[t * a.ld + e]) - top) / z * (d - wd);
-          mine[e] = d;
-        }
-      }
+    const float total = group_sum<G>(s);
     __syncwarp();
-    float extra[N];
+    if (a.dweights) {
+      float z = 0.f, wd = 0.f;
+      #pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        if (!routed || e_now[s] < 0 || e_now[s] >= a.experts) e_now[s] = -1;
+        const float y = e_now[s] >= 0 ? px[e_now[s]] : 0.f;
+        z += y;
+        wd = fmaf(y, d_now[s], wd);
+      }
+      if (a.normalize) {
+        z = __frcp_rn(group_sum<G>(z));
+        wd = group_sum<G>(wd) * z;
+        z *= total;
+        #pragma unroll
+        for (int s = 0; s < KS; ++s) d_now[s] = (d_now[s] - wd) * z;
+      }
+      #pragma unroll
+      for (int s = 0; s < KS; ++s)
+        if (e_now[s] >= 0) xx[e_now[s]] = d_now[s];
+      __syncwarp();
+    }
+    const float inv = __frcp_rn(total);
+    float x[N];
     float dot = 0.f;
     #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-      const float4* q = reinterpret_cast<const float4*>(mine + (c * G + gl) * 8);
+      const float4* q = reinterpret_cast<const float4*>(xx + (c * G + gl) * 8);
       const float4 q0 = q[0], q1 = q[1];
-      extra[c * 8 + 0] = q0.x; extra[c * 8 + 1] = q0.y; extra[c * 8 + 2] = q0.z;
-      extra[c * 8 + 3] = q0.w; extra[c * 8 + 4] = q1.x; extra[c * 8 + 5] = q1.y;
-      extra[c * 8 + 6] = q1.z; extra[c * 8 + 7] = q1.w;
+      x[c * 8 + 0] = q0.x; x[c * 8 + 1] = q0.y; x[c * 8 + 2] = q0.z; x[c * 8 + 3] = q0.w;
+      x[c * 8 + 4] = q1.x; x[c * 8 + 5] = q1.y; x[c * 8 + 6] = q1.z; x[c * 8 + 7] = q1.w;
     }
     #pragma unroll
     for (int j = 0; j < N; ++j) {
       v[j] *= inv;
-      dot = fmaf(v[j], a.normalize ? b[j] : b[j] + extra[j], dot);
+      const float bx = b[j] + x[j];
+      dot = fmaf(v[j], a.normalize ? b[j] : bx, dot);
+      x[j] = bx;
     }
     dot = group_sum<G>(dot);
     #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const float y = a.normalize ? fmaf(v[j], b[j] - dot, extra[j]) : v[j] * (b[j] + extra[j] - dot);
-      v[j] = routed ? y : 0.f;
-    }
-    __syncwarp();
-    if (routed && a.dweights)
-      for (int p = gl; p < a.k; p += G) {
-        const int e = a.index[t * a.k + p];
-        if (e >= 0 && e < a.experts) mine[e] = 0.f;
-      }
+    for (int j = 0; j < N; ++j) v[j] = routed ? v[j] * (x[j] - dot) : 0.f;
     if (t < a.tokens) {
       #pragma unroll
       for (int c = 0; c < NCH; ++c) {
         const int e0 = (c * G + gl) * 8;
         T* out = static_cast<T*>(a.dlogits) + t * a.experts + e0;
-        if (a.vec && e0 < a.experts) {
+        if (a.vec) {
           Chunk o;
           #pragma unroll
           for (int j = 0; j < 8; ++j) elem(o, j) = v[c * 8 + j];
-          store8(out, o);
+          if (e0 < a.experts) store8(out, o);
         } else {
           #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -490,6 +601,12 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(
       }
     }
     __syncwarp();
+    if (a.dweights) {
+      #pragma unroll
+      for (int s = 0; s < KS; ++s)
+        if (e_now[s] >= 0) xx[e_now[s]] = 0.f;
+      __syncwarp();
+    }
   }
 }
 
@@ -500,14 +617,14 @@ int lanes_of(int experts) {
   return g;
 }
 
-// blocks of a pass: one for every token group, up to four an SM
+// blocks of a pass: a warp for every token group, up to two blocks an SM
 int route_blocks(int64_t tokens, int experts) {
   const int per = kRouteWarps * 32 / lanes_of(experts);
   const int64_t b = (tokens + per - 1) / per;
   return (int)(b < 1 ? 1 : b < kRouteParts ? b : kRouteParts);
 }
 
-int join_blocks(int experts) { return (experts + 31) / 32; }
+int join_blocks(int experts) { return (experts + kJoinExperts - 1) / kJoinExperts; }
 
 bool misaligned(const void* p, size_t es) { return reinterpret_cast<uintptr_t>(p) % es != 0; }
 
@@ -527,7 +644,7 @@ bool whole_rows(const void* p, int64_t tokens, int64_t ld, int experts, size_t e
 }
 
 // workspace: ticket and shares of the loss, counts, probabilities
-constexpr size_t kJoinBytes = 256;
+constexpr size_t kJoinBytes = 1024;
 size_t probs_offset(int64_t tokens, int experts) {
   return kJoinBytes +
          ((size_t)route_blocks(tokens, experts) * (experts + 1) * sizeof(int32_t) + 255) / 256 * 256;
@@ -564,7 +681,13 @@ struct LaunchBwd {
   int blocks;
   cudaStream_t s;
   template <typename T, int G, int NCH> cudaError_t operator()() const {
-    route_bwd_kernel<T, G, NCH><<<blocks, kRouteThreads, 0, s>>>(a);
+    const size_t smem = (size_t)kRouteWarps * (32 / G) * 2 * G * NCH * 8 * sizeof(float);
+    if (smem > 48u << 10) {
+      const cudaError_t e = cudaFuncSetAttribute(route_bwd_kernel<T, G, NCH>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+    }
+    route_bwd_kernel<T, G, NCH><<<blocks, kRouteThreads, smem, s>>>(a);
     return cudaGetLastError();
   }
 };
@@ -609,9 +732,10 @@ extern "C" muon_status muon_route(int64_t tokens, int experts, int k, int dtype,
   const RouteFwd a = {tokens, ld, experts, k, normalize,
                       whole_rows(logits, tokens, ld, experts, es), logits, token_mask, weights,
                       index, reinterpret_cast<float*>(ws + probs_offset(tokens, experts)),
-                      reinterpret_cast<int32_t*>(ws + kJoinBytes), reinterpret_cast<unsigned*>(ws)};
+                      reinterpret_cast<int32_t*>(ws + kJoinBytes), reinterpret_cast<unsigned*>(ws),
+                      counts, mean_prob, loss};
   cudaError_t e = by_experts(dtype, experts, LaunchFwd{a, blocks, s});
-  if (e == cudaSuccess) {
+  if (e == cudaSuccess && blocks > 1) {
     const RouteJoin j = {experts, k, blocks, a.part_p, a.part_c, counts, mean_prob, loss,
                          reinterpret_cast<float*>(ws) + 1, a.ticket};
     e = launch_k(route_join_kernel, dim3(join_blocks(experts)), dim3(256), 0, s, true, j);
