@@ -82,6 +82,12 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // exp(v - top): the difference is rounded once, so the relative error is that
 // of the difference, a few units more for 2^x; below 2^-126 the result is 0
 __device__ __forceinline__ float exp_below(float v, float top) {
@@ -111,8 +117,19 @@ template <typename T, int G, int N> struct Choice;
 // bf16: key and index in one word.  N == 8: a sorted list.
 template <int G, int N> struct Choice<__nv_bfloat16, G, N> {
   uint32_t k[N];
-  __device__ __forceinline__ void set(int j, float v, int e, bool in) {
-    k[j] = in ? (order_key(v) & 0xffff0000u) | (uint32_t)(0xffff - e) : 0u;
+  // chunk c, which begins at expert e0, as loaded: keys of two at once
+  __device__ __forceinline__ void set(int c, const uint4 (&u)[1], int e0) {
+    const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+    #pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // adding 0 turns -0 into +0 and a NaN into the canonical positive one
+      uint32_t x;
+      asm("{.reg .b32 z;\n mov.b32 z, 0;\n add.rn.bf16x2 %0, %1, z;}" : "=r"(x) : "r"(w[j]));
+      // a set sign flips all sixteen bits, a clear one the sign alone
+      x ^= ((x >> 15) & 0x00010001u) * 0x7fffu | 0x80008000u;
+      k[c * 8 + 2 * j] = x * 65536u + (uint32_t)(0xffff - (e0 + 2 * j));
+      k[c * 8 + 2 * j + 1] = (x & 0xffff0000u) | (uint32_t)(0xffff - (e0 + 2 * j + 1));
+    }
   }
   __device__ __forceinline__ void order() {
     if constexpr (N == 8) {
@@ -130,7 +147,8 @@ template <int G, int N> struct Choice<__nv_bfloat16, G, N> {
       ce(1, 2); ce(3, 4); ce(5, 6);
     }
   }
-  __device__ __forceinline__ uint32_t next(int, int&) {
+  // `left` (known at compile time): picks that may still follow
+  __device__ __forceinline__ uint32_t next(int, int&, int left) {
     uint32_t head = k[0];
     if constexpr (N != 8) {
       #pragma unroll
@@ -140,8 +158,9 @@ template <int G, int N> struct Choice<__nv_bfloat16, G, N> {
     if constexpr (N == 8) {
       if (head == win) {
         #pragma unroll
-        for (int j = 0; j < 7; ++j) k[j] = k[j + 1];
-        k[7] = 0;
+        for (int j = 0; j < 7; ++j)
+          if (j < left) k[j] = k[j + 1];
+        if (left > 7) k[7] = 0;
       }
     } else {
       #pragma unroll
@@ -162,9 +181,13 @@ template <int G, int N> struct Choice<__nv_bfloat16, G, N> {
 template <int G, int N> struct Choice<float, G, N> {
   uint32_t k[N];
   int id[N];
-  __device__ __forceinline__ void set(int j, float v, int e, bool in) {
-    k[j] = in ? order_key(v) : 0u;
-    id[j] = e;
+  __device__ __forceinline__ void set(int c, const uint4 (&u)[2], int e0) {
+    const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+    #pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      k[c * 8 + j] = order_key(__uint_as_float(w[j]));
+      id[c * 8 + j] = e0 + j;
+    }
   }
   __device__ __forceinline__ void order() {
     if constexpr (N == 8) {
@@ -182,7 +205,7 @@ template <int G, int N> struct Choice<float, G, N> {
         }
     }
   }
-  __device__ __forceinline__ uint32_t next(int group_lanes, int& e) {
+  __device__ __forceinline__ uint32_t next(int group_lanes, int& e, int left) {
     uint32_t win;
     if constexpr (N == 8) {
       win = group_max<G>(k[0]);
@@ -191,8 +214,9 @@ template <int G, int N> struct Choice<float, G, N> {
       e = __shfl_sync(kAll, id[0], lane);
       if ((int)(threadIdx.x & 31) == lane) {
         #pragma unroll
-        for (int j = 0; j < 7; ++j) { k[j] = k[j + 1]; id[j] = id[j + 1]; }
-        k[7] = 0;
+        for (int j = 0; j < 7; ++j)
+          if (j < left) { k[j] = k[j + 1]; id[j] = id[j + 1]; }
+        if (left > 7) k[7] = 0;
       }
     } else {      // a lane's experts are not consecutive: the lowest index decides
       uint32_t head = 0;
@@ -212,12 +236,21 @@ template <int G, int N> struct Choice<float, G, N> {
   static __device__ __forceinline__ int expert(uint32_t, int e) { return e; }
 };
 
-// One token's logits as a lane holds them: its chunks as loaded (rows of whole,
-// aligned chunks), so that the next token's can be in flight while this one is
-// worked on, and the mask's verdict.
+// One token's logits as a lane holds them: its chunks as loaded, -inf where
+// there is no expert.  Rows of whole, aligned chunks are loaded ahead, so that
+// the next token's are in flight while this one is worked on; others when they
+// are needed.  A token past the end or masked keeps what was there: its results
+// are thrown away.
 template <typename T, int G, int NCH> struct Logits {
   uint4 u[NCH][kPieces<T>];
   bool live;
+  __device__ __forceinline__ void clear() {
+    const uint32_t w = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+    #pragma unroll
+    for (int c = 0; c < NCH; ++c)
+      #pragma unroll
+      for (int q = 0; q < kPieces<T>; ++q) u[c][q] = make_uint4(w, w, w, w);
+  }
   template <typename A>
   __device__ __forceinline__ void load(const A& a, int64_t t, int gl) {
     live = t < a.tokens && !(a.mask && !a.mask[t]);
@@ -232,19 +265,17 @@ template <typename T, int G, int NCH> struct Logits {
       }
     }
   }
-  // chunk c in fp32; -inf where there is no expert, and for a masked token
   template <typename A>
-  __device__ __forceinline__ void get(float (&v)[8], const A& a, int64_t t, int c, int gl) const {
-    const int e0 = (c * G + gl) * 8;
-    if (a.vec) {
+  __device__ __forceinline__ void arrive(const A& a, int64_t t, int gl) {
+    if (a.vec || t >= a.tokens) return;
+    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    #pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const int e0 = (c * G + gl) * 8;
       Chunk w;
-      widen(w, u[c]);
       #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = live && e0 < a.experts ? elem(w, j) : -INFINITY;
-    } else {
-      const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-      #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = live && e0 + j < a.experts ? to_f(row[e0 + j]) : -INFINITY;
+      for (int j = 0; j < 8; ++j) elem(w, j) = e0 + j < a.experts ? to_f(row[e0 + j]) : -INFINITY;
+      store8(reinterpret_cast<T*>(&u[c][0]), w);
     }
   }
 };
@@ -274,36 +305,43 @@ route_kernel(const __grid_constant__ RouteFwd a) {
   const int64_t stride = (int64_t)gridDim.x * kRouteWarps * TPW;
   const int64_t begin = ((int64_t)blockIdx.x * kRouteWarps + warp) * TPW;
   Logits<T, G, NCH> now, next;
+  next.clear();
   next.load(a, begin + grp, gl);
   uint32_t* const w = sw[warp] + grp * a.k;
   int* const x = se[warp] + grp * a.k;
   for (int64_t t0 = begin; t0 < a.tokens; t0 += stride) {
     const int64_t t = t0 + grp;
     now = next;
+    now.arrive(a, t, gl);
     next.load(a, t + stride, gl);
-    float v[N];
     Choice<T, G, N> choice;
     #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const int e0 = (c * G + gl) * 8;
-      float u[8];
-      now.get(u, a, t, c, gl);
-      #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[c * 8 + j] = u[j];
-        choice.set(c * 8 + j, u[j], e0 + j, e0 + j < a.experts);
-      }
-    }
+    for (int c = 0; c < NCH; ++c) choice.set(c, now.u[c], (c * G + gl) * 8);
     choice.order();
     uint32_t first = 0;
-    for (int p = 0; p < a.k; ++p) {
+    auto pick = [&](int p, int left) {
       int e = 0;
-      const uint32_t win = choice.next(group_lanes, e);
+      const uint32_t win = choice.next(group_lanes, e, left);
       if (p == 0) first = win;
       if (gl == 0) {
         w[p] = win;
         if (sizeof(T) == 4) x[p] = e;
       }
+    };
+    if (a.k <= 8) {
+      #pragma unroll
+      for (int p = 0; p < 8; ++p)
+        if (p < a.k) pick(p, 7 - p);
+    } else {
+      for (int p = 0; p < a.k; ++p) pick(p, 8);
+    }
+    float v[N];
+    #pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      Chunk u;
+      widen(u, now.u[c]);
+      #pragma unroll
+      for (int j = 0; j < 8; ++j) v[c * 8 + j] = elem(u, j);
     }
     first = choice.key(first);
     const bool routed = now.live && first > kKeyNegInf;
@@ -504,6 +542,7 @@ route_bwd_kernel(const __grid_constant__ RouteBwd a) {
       }
     }
   };
+  next.clear();
   next.load(a, begin + grp, gl);
   load_picks(begin + grp);
   for (int64_t t0 = begin; t0 < a.tokens; t0 += stride) {
@@ -511,23 +550,23 @@ route_bwd_kernel(const __grid_constant__ RouteBwd a) {
     now = next;
     #pragma unroll
     for (int s = 0; s < KS; ++s) { e_now[s] = e_next[s]; d_now[s] = d_next[s]; }
+    now.arrive(a, t, gl);
     next.load(a, t + stride, gl);
     load_picks(t + stride);
     float v[N];
-    uint32_t best = 0;
+    float best = -INFINITY;
     #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-      float u[8];
-      now.get(u, a, t, c, gl);
+      Chunk u;
+      widen(u, now.u[c]);
       #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v[c * 8 + j] = u[j];
-        best = max(best, order_key(u[j]));
+        v[c * 8 + j] = elem(u, j);
+        best = max_nan(best, v[c * 8 + j]);
       }
     }
-    best = group_max<G>(best);
-    const bool routed = now.live && best > kKeyNegInf;
-    const float top = key_value(best);
+    const float top = key_value(group_max<G>(order_key(best)));
+    const bool routed = now.live && top != -INFINITY;
     float s = 0.f;
     #pragma unroll
     for (int c = 0; c < NCH; ++c) {
@@ -546,7 +585,10 @@ route_bwd_kernel(const __grid_constant__ RouteBwd a) {
       float z = 0.f, wd = 0.f;
       #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        if (!routed || e_now[s] < 0 || e_now[s] >= a.experts) e_now[s] = -1;
+        if (!routed || e_now[s] < 0 || e_now[s] >= a.experts) {
+          e_now[s] = -1;
+          d_now[s] = 0.f;      // whatever a missing pick's gradient holds
+        }
         const float y = e_now[s] >= 0 ? px[e_now[s]] : 0.f;
         z += y;
         wd = fmaf(y, d_now[s], wd);

@@ -194,6 +194,22 @@ def test_indices_out_of_range_are_missing_picks(layers):
         assert torch.equal(a, b)
 
 
+def test_gradients_of_missing_picks_have_no_effect(layers):
+    l = draw(40, 12, F32, 15)
+    l[3:9, 2:] = float("-inf")                    # two experts left for four picks
+    mask = torch.ones(40, dtype=torch.bool, device="cuda")
+    mask[20:25] = False
+    dw = torch.randn(40, 4, device="cuda")
+    for normalize in (True, False):
+        o = layers.route_forward(l, 4, token_mask=mask, normalize=normalize)
+        bad = torch.where(o.index < 0, float("nan"), dw)
+        a = layers.route_backward(l, o.index, o.counts, dweights=bad, dloss=o.loss, token_mask=mask,
+                                  normalize=normalize)
+        b = layers.route_backward(l, o.index, o.counts, dweights=dw, dloss=o.loss, token_mask=mask,
+                                  normalize=normalize)
+        assert int((o.index < 0).sum()) == 6 * 2 + 5 * 4 and torch.equal(a, b)
+
+
 def test_same_bits_every_time_and_on_another_stream(layers):
     l = draw(30011, 48, BF, 9)
     dw = torch.randn(30011, 5, device="cuda")
