@@ -6,7 +6,8 @@ They produce what MuonWithAdamW.step consumes: the 1-D gradients of norm scales
 and biases (the AdamW path), and the router gradient and per-expert token sets
 of [E, M, N] expert stacks (the Muon path).  Every computation runs in libmuon's
 kernels (muon_layer_norm, muon_dropout, muon_route and their gradients in
-include/muon.h, which states the formulas); this module marshals tensors.
+include/muon.h, which states the formulas); this module and its compiled half
+(csrc/binding.cpp) check and marshal tensors.
 
 Two levels:
   * layer_norm, dropout_add_layer_norm, dropout, route: differentiable
@@ -23,18 +24,17 @@ offsets that never overlap.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 from typing import NamedTuple, Optional
 
 import torch
 
-from . import MUON_BF16, MUON_F32, _check, load
+from . import _PKG, _check, load
 
 __all__ = ["layer_norm", "dropout_add_layer_norm", "dropout", "route", "RandomCounter",
            "layer_norm_forward", "layer_norm_backward", "dropout_forward", "dropout_backward",
            "route_forward", "route_backward", "NormOut", "NormGrad", "RouteOut"]
-
-_DT = {torch.bfloat16: MUON_BF16, torch.float32: MUON_F32}
-
 
 class NormOut(NamedTuple):
     y: torch.Tensor
@@ -71,74 +71,33 @@ class RandomCounter:
         return at
 
 
-def _dtype(t: torch.Tensor, what: str) -> int:
-    dt = _DT.get(t.dtype)
-    if dt is None:
-        raise TypeError("%s must be bf16 or fp32, got %s" % (what, t.dtype))
-    return dt
+_bound = None
 
 
-def _rows(t: torch.Tensor, what: str):
-    """(rows, cols, row stride) of a tensor of rows; ValueError when it is
-    not one."""
-    if not t.is_cuda:
-        raise ValueError("%s is not on a CUDA device" % what)
-    shape = t.shape
-    if not shape:
-        raise ValueError("%s needs at least one dimension" % what)
-    cols = shape[-1]
-    if len(shape) == 2 and (cols <= 1 or t.stride(1) == 1):
-        return shape[0], cols, t.stride(0)
-    if t.is_contiguous():
-        return (t.numel() // cols if cols else 0), cols, cols
-    stride, rows, ld = t.stride(), 1, None
-    for d in range(len(shape) - 2, -1, -1):       # leading dims, innermost first
-        if shape[d] == 1:
-            continue
-        if ld is None:
-            ld = stride[d]
-        elif stride[d] != ld * rows:
-            raise ValueError("the leading dimensions of %s are not rows at one stride" % what)
-        rows *= shape[d]
-    if cols > 1 and stride[-1] != 1:
-        raise ValueError("the last dimension of %s is not dense" % what)
-    return rows, cols, cols if ld is None else ld
+def _b():
+    """The compiled half (built by newton_schulz_05_gb300.build.build()), which
+    checks tensors, allocates outputs and calls libmuon."""
+    global _bound
+    if _bound is None:
+        lib = load()
+        path = os.path.join(_PKG, "_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError("_binding.so not built at %s: run newton_schulz_05_gb300.build.build()"
+                               % path)
+        spec = importlib.util.spec_from_file_location(__package__ + "._binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                     for name in ("muon_layer_norm", "muon_layer_norm_backward",
+                                  "muon_layer_norm_workspace_bytes", "muon_dropout", "muon_route",
+                                  "muon_route_workspace_bytes", "muon_route_backward")})
+        _bound = module
+    return _bound
 
 
 def _as_rows(t: torch.Tensor) -> torch.Tensor:
     """t, or a dense copy when its strides are not those of rows."""
-    try:
-        _rows(t, "")
-        return t
-    except ValueError:
-        return t.contiguous()
-
-
-def _vector(t, cols: int, like: torch.Tensor, what: str) -> Optional[int]:
-    if t is None:
-        return None
-    if t.dim() != 1 or t.shape[0] != cols or not t.is_contiguous():
-        raise ValueError("%s must be a dense vector of %d elements" % (what, cols))
-    if t.device != like.device:
-        raise ValueError("%s is not on the device of the rows" % what)
-    return t.data_ptr()
-
-
-def _same(t: torch.Tensor, like: torch.Tensor, what: str):
-    """Row stride of `t`, which must match `like` in shape, type and device."""
-    if t.shape != like.shape or t.device != like.device:
-        raise ValueError("%s must have shape %s on %s" % (what, tuple(like.shape), like.device))
-    if t.dtype != like.dtype:
-        raise TypeError("%s must be %s, got %s" % (what, like.dtype, t.dtype))
-    return _rows(t, what)[2]
-
-
-def _flat(t: torch.Tensor, numel: int, dtype, like: torch.Tensor, what: str) -> int:
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
-    if t.numel() != numel or not t.is_contiguous() or t.device != like.device:
-        raise ValueError("%s must be dense with %d elements on %s" % (what, numel, like.device))
-    return t.data_ptr()
+    return t if _b().is_rows(t) else t.contiguous()
 
 
 def _on(stream, fn, args, kw):
@@ -152,21 +111,6 @@ def _on(stream, fn, args, kw):
     return out
 
 
-def _here(t: torch.Tensor) -> int:
-    """The current stream's handle on the device of t, which must be the
-    current device."""
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError("tensors are on cuda:%d, the current device is cuda:%d"
-                         % (t.get_device(), torch.cuda.current_device()))
-    return torch.cuda.current_stream().cuda_stream
-
-
-def _scratch(fn, rows: int, cols: int, like: torch.Tensor) -> torch.Tensor:
-    need = ctypes.c_size_t()
-    _check(fn(rows, cols, ctypes.byref(need)), "workspace_bytes")
-    return torch.empty(need.value, dtype=torch.uint8, device=like.device)
-
-
 def layer_norm_forward(x, weight=None, bias=None, *, eps: float = 1e-5, residual=None,
                        p: float = 0.0, seed: int = 0, offset: int = 0, stream=None) -> NormOut:
     """muon_layer_norm: y = norm(residual + dropout(x)) * weight + bias over
@@ -174,29 +118,11 @@ def layer_norm_forward(x, weight=None, bias=None, *, eps: float = 1e-5, residual
     if stream is not None:
         return _on(stream, layer_norm_forward, (x, weight, bias),
                    dict(eps=eps, residual=residual, p=p, seed=seed, offset=offset))
-    dt = _dtype(x, "x")
-    rows, cols, ld = _rows(x, "x")
-    wdt = MUON_F32
-    if weight is not None or bias is not None:
-        wdt = _dtype(weight if weight is not None else bias, "weight and bias")
-        if weight is not None and bias is not None and weight.dtype != bias.dtype:
-            raise TypeError("weight and bias must be of one type")
-    wp, bp = _vector(weight, cols, x, "weight"), _vector(bias, cols, x, "bias")
-    handle = _here(x)
-    rp, ldr, total, tp = None, 0, x, None
-    if residual is not None:
-        ldr = _same(residual, x, "residual")
-        rp = residual.data_ptr()
-    if rp is not None or p != 0.0:
-        total = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        tp = total.data_ptr()
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    rstd = torch.empty_like(mean)
-    _check(load().muon_layer_norm(rows, cols, dt, wdt, x.data_ptr(), ld, rp, ldr, wp, bp, eps, p,
-                                  seed, offset, tp, y.data_ptr(), mean.data_ptr(),
-                                  rstd.data_ptr(), handle), "muon_layer_norm")
-    return NormOut(y, total, mean, rstd)
+    r = (_bound or _b()).layer_norm_forward(x, weight, bias, eps, residual, p, seed, offset)
+    if type(r) is int:
+        _check(r, "muon_layer_norm")
+    y, total, mean, rstd = r
+    return NormOut(y, x if total is None else total, mean, rstd)
 
 
 def layer_norm_backward(dy, sum, mean, rstd, weight=None, *, dsum=None, p: float = 0.0,
@@ -210,37 +136,12 @@ def layer_norm_backward(dy, sum, mean, rstd, weight=None, *, dsum=None, p: float
         return _on(stream, layer_norm_backward, (dy, sum, mean, rstd, weight),
                    dict(dsum=dsum, p=p, seed=seed, offset=offset, need_weight=need_weight,
                         need_bias=need_bias))
-    L = load()
-    dt = _dtype(dy, "dy")
-    rows, cols, ld = _rows(dy, "dy")
-    lds = _same(sum, dy, "sum")
-    mp = _flat(mean, rows, torch.float32, dy, "mean")
-    vp = _flat(rstd, rows, torch.float32, dy, "rstd")
-    wdtype = torch.float32 if weight is None else weight.dtype
-    wdt = MUON_F32 if weight is None else _dtype(weight, "weight")
-    wp = _vector(weight, cols, dy, "weight")
-    handle = _here(dy)
-    dp, ldd = None, 0
-    if dsum is not None:
-        ldd = _same(dsum, dy, "dsum")
-        dp = dsum.data_ptr()
-    dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
-    dres, drp = dx, None
-    if p != 0.0:
-        dres = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
-        drp = dres.data_ptr()
-    dw = db = wsp = None
-    nbytes = 0
-    if need_weight or need_bias:
-        dw = torch.empty(cols, dtype=wdtype, device=dy.device) if need_weight else None
-        db = torch.empty(cols, dtype=wdtype, device=dy.device) if need_bias else None
-        ws = _scratch(L.muon_layer_norm_workspace_bytes, rows, cols, dy)
-        wsp, nbytes = ws.data_ptr(), ws.numel()
-    _check(L.muon_layer_norm_backward(
-        rows, cols, dt, wdt, dy.data_ptr(), ld, sum.data_ptr(), lds, mp, vp, wp, dp, ldd, p, seed,
-        offset, dx.data_ptr(), drp, None if dw is None else dw.data_ptr(),
-        None if db is None else db.data_ptr(), wsp, nbytes, handle), "muon_layer_norm_backward")
-    return NormGrad(dx, dres, dw, db)
+    r = (_bound or _b()).layer_norm_backward(dy, sum, mean, rstd, weight, dsum, p, seed, offset,
+                                             need_weight, need_bias)
+    if type(r) is int:
+        _check(r, "muon_layer_norm_backward")
+    dx, dres, dw, db = r
+    return NormGrad(dx, dx if dres is None else dres, dw, db)
 
 
 def dropout_forward(x, p: float, *, seed: int, offset: int = 0, residual=None, out=None,
@@ -250,38 +151,16 @@ def dropout_forward(x, p: float, *, seed: int, offset: int = 0, residual=None, o
     if stream is not None:
         return _on(stream, dropout_forward, (x, p),
                    dict(seed=seed, offset=offset, residual=residual, out=out))
-    dt = _dtype(x, "x")
-    n = x.numel()
-    xp = _flat(x, n, x.dtype, x, "x")
-    if not x.is_cuda:
-        raise ValueError("x is not on a CUDA device")
-    handle = _here(x)
-    rp = None
-    if residual is not None:
-        if residual.shape != x.shape:
-            raise ValueError("residual must have shape %s" % (tuple(x.shape),))
-        rp = _flat(residual, n, x.dtype, x, "residual")
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape:
-        raise ValueError("out must have shape %s" % (tuple(x.shape),))
-    op = _flat(out, n, x.dtype, x, "out")
-    _check(load().muon_dropout(n, dt, xp, rp, p, seed, offset, op, handle), "muon_dropout")
-    return out
+    r = (_bound or _b()).dropout(x, p, seed, offset, residual, out)
+    if type(r) is int:
+        _check(r, "muon_dropout")
+    return r
 
 
 def dropout_backward(dy, p: float, *, seed: int, offset: int = 0, out=None,
                      stream=None) -> torch.Tensor:
     """Gradient of dropout_forward's x (the residual's is dy itself)."""
     return dropout_forward(dy, p, seed=seed, offset=offset, out=out, stream=stream)
-
-
-def _mask_ptr(token_mask, tokens: int, like: torch.Tensor) -> Optional[int]:
-    if token_mask is None:
-        return None
-    if token_mask.dtype not in (torch.bool, torch.uint8):
-        raise TypeError("token_mask must be bool or uint8, got %s" % token_mask.dtype)
-    return _flat(token_mask, tokens, token_mask.dtype, like, "token_mask")
 
 
 def route_forward(logits, k: int, *, token_mask=None, normalize: bool = True,
@@ -292,24 +171,10 @@ def route_forward(logits, k: int, *, token_mask=None, normalize: bool = True,
     if stream is not None:
         return _on(stream, route_forward, (logits, k),
                    dict(token_mask=token_mask, normalize=normalize))
-    L = load()
-    dt = _dtype(logits, "logits")
-    tokens, experts, ld = _rows(logits, "logits")
-    handle = _here(logits)
-    dev = logits.device
-    mp = _mask_ptr(token_mask, tokens, logits)
-    ws = _scratch(L.muon_route_workspace_bytes, tokens, experts, logits)
-    shape = logits.shape[:-1] + (max(k, 0),)
-    weights = torch.empty(shape, dtype=torch.float32, device=dev)
-    index = torch.empty(shape, dtype=torch.int32, device=dev)
-    counts = torch.empty(experts + 1, dtype=torch.int32, device=dev)
-    mean_prob = torch.empty(experts, dtype=torch.float32, device=dev)
-    loss = torch.empty((), dtype=torch.float32, device=dev)
-    _check(L.muon_route(tokens, experts, k, dt, logits.data_ptr(), ld, mp, 1 if normalize else 0,
-                        weights.data_ptr(), index.data_ptr(), counts.data_ptr(),
-                        mean_prob.data_ptr(), loss.data_ptr(), ws.data_ptr(), ws.numel(), handle),
-           "muon_route")
-    return RouteOut(weights, index, counts, mean_prob, loss)
+    r = (_bound or _b()).route_forward(logits, k, token_mask, normalize)
+    if type(r) is int:
+        _check(r, "muon_route")
+    return RouteOut._make(r)
 
 
 def route_backward(logits, index, counts, *, dweights=None, dloss=None, token_mask=None,
@@ -321,22 +186,10 @@ def route_backward(logits, index, counts, *, dweights=None, dloss=None, token_ma
         return _on(stream, route_backward, (logits, index, counts),
                    dict(dweights=dweights, dloss=dloss, token_mask=token_mask,
                         normalize=normalize))
-    dt = _dtype(logits, "logits")
-    tokens, experts, ld = _rows(logits, "logits")
-    handle = _here(logits)
-    if not index.dim() or index.shape[:-1] != logits.shape[:-1]:
-        raise ValueError("index must have one row of picks a token")
-    k = index.shape[-1]
-    ip = _flat(index, tokens * k, torch.int32, logits, "index")
-    cp = _flat(counts, experts + 1, torch.int32, logits, "counts")
-    wp = None if dweights is None else _flat(dweights, tokens * k, torch.float32, logits, "dweights")
-    lp = None if dloss is None else _flat(dloss, 1, torch.float32, logits, "dloss")
-    mp = _mask_ptr(token_mask, tokens, logits)
-    dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    _check(load().muon_route_backward(tokens, experts, k, dt, logits.data_ptr(), ld, mp,
-                                      1 if normalize else 0, ip, cp, wp, lp, dlogits.data_ptr(),
-                                      handle), "muon_route_backward")
-    return dlogits
+    r = (_bound or _b()).route_backward(logits, index, counts, dweights, dloss, token_mask, normalize)
+    if type(r) is int:
+        _check(r, "muon_route_backward")
+    return r
 
 
 class _LayerNorm(torch.autograd.Function):
