@@ -472,7 +472,7 @@ MUON_API muon_status muon_layer_norm_backward(
 MUON_API muon_status muon_layer_norm_workspace_bytes(int64_t rows, int64_t cols, size_t* out);
 
 /*
- * y = residual + dropout(x) over 0 <= n <= 2^42 dense elements (residual null: 0).
+ * y = residual + dropout(x) over 0 <= n <= 2^40 dense elements (residual null: 0).
  * The gradient of x is the same call on dy without a residual.  y may be x or
  * residual itself.
  */

@@ -1,16 +1,17 @@
 // Dropout from a counter-based generator, alone or added to a residual.
 //
 // Bound by HBM: x (and the residual) read once, y written once; the flags come
-// from the generator, one block for the eight elements of a chunk (random.cuh).
-// A chunk starts at an aligned address, so a tensor that does not has its first
-// chunk begin ahead of it; operands whose addresses are aligned differently
-// are read element by element.  A thread loads all of its chunks before it
-// draws for the first, so the loads cover the generator's latency.
+// from the generator, a block for eight elements (random.cuh).  A thread moves
+// 16-byte pieces that are aligned in memory, so a tensor that does not start at
+// an aligned address has its first piece begin ahead of it; operands whose
+// addresses are aligned differently are read element by element.  A thread
+// loads all of its pieces before it draws for the first, so the loads cover the
+// generator's latency.
 #include <cmath>
 
-#include "chunk.cuh"
 #include "common.cuh"
 #include "internal.h"
+#include "pieces.cuh"
 #include "random.cuh"
 
 namespace muon {
@@ -18,51 +19,49 @@ namespace muon {
 namespace {
 
 constexpr int kDropThreads = 256;
+constexpr int kDropPieces = 4;      // a thread: 64 bytes of an operand in flight
 
-template <typename T, int U, bool RES>
+template <typename T, bool RES>
 __global__ void __launch_bounds__(kDropThreads, 4)
 dropout_kernel(int64_t n, const T* x, const T* residual, const __grid_constant__ Drop d, T* y,
                int phase, bool vec) {
-  constexpr int P = kPieces<T>, kSpan = U * kDropThreads * 8;   // elements a block
+  constexpr int E = kEl<T>, U = kDropPieces, kSpan = U * kDropThreads * E;   // elements a block
   const int64_t block = (int64_t)blockIdx.x * kSpan - phase;
-  const int64_t first = block + threadIdx.x * 8;
+  const int64_t first = block + threadIdx.x * E;
   if (vec && block >= 0 && block + kSpan <= n) {
     const uint4* px = reinterpret_cast<const uint4*>(x + first);
     const uint4* pr = reinterpret_cast<const uint4*>(residual + (RES ? first : 0));
-    uint4 ux[U][P], ur[U][P];
+    uint4 ux[U], ur[U];
     #pragma unroll
     for (int u = 0; u < U; ++u) {
-      #pragma unroll
-      for (int q = 0; q < P; ++q) {
-        ux[u][q] = px[u * kDropThreads * P + q];
-        if (RES) ur[u][q] = pr[u * kDropThreads * P + q];
-      }
+      ux[u] = px[u * kDropThreads];
+      if (RES) ur[u] = pr[u * kDropThreads];
     }
     #pragma unroll
     for (int u = 0; u < U; ++u) {
-      Chunk c, r;
-      widen(c, ux[u]);
-      drop8(c.v, first + u * (kDropThreads * 8), d);
+      Piece<E> v, r;
+      widen(v, ux[u]);
+      drop<E>(v.v, first + u * (kDropThreads * E), d);
       if (RES) {
         widen(r, ur[u]);
         #pragma unroll
-        for (int j = 0; j < 4; ++j) c.v[j] = add2(c.v[j], r.v[j]);
+        for (int j = 0; j < E / 2; ++j) v.v[j] = add2(v.v[j], r.v[j]);
       }
-      store8(y + first + u * (kDropThreads * 8), c);
+      reinterpret_cast<uint4*>(y + first)[u * kDropThreads] = narrow(v);
     }
     return;
   }
   for (int u = 0; u < U; ++u) {       // the tensor's ends, or differently aligned operands
-    const int64_t i = first + u * (kDropThreads * 8);
+    const int64_t i = first + u * (kDropThreads * E);
     if (i >= n) break;
-    Chunk c;
+    Piece<E> v;
     #pragma unroll
-    for (int j = 0; j < 8; ++j) elem(c, j) = i + j >= 0 && i + j < n ? to_f(x[i + j]) : 0.f;
-    drop8(c.v, i, d);
+    for (int j = 0; j < E; ++j) elem(v, j) = i + j >= 0 && i + j < n ? to_f(x[i + j]) : 0.f;
+    drop<E>(v.v, i, d);
     #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < E; ++j)
       if (i + j >= 0 && i + j < n)
-        y[i + j] = from_f<T>(RES ? elem(c, j) + to_f(residual[i + j]) : elem(c, j));
+        y[i + j] = from_f<T>(RES ? elem(v, j) + to_f(residual[i + j]) : elem(v, j));
   }
 }
 
@@ -71,17 +70,18 @@ cudaError_t dropout(int64_t n, const void* x, const void* residual, const Drop& 
                     cudaStream_t s) {
   const T* px = static_cast<const T*>(x);
   const T* pr = static_cast<const T*>(residual);
-  auto phase_of = [](const void* p) { return (int)(reinterpret_cast<uintptr_t>(p) / sizeof(T) & 7); };
+  constexpr int E = kEl<T>;
+  auto phase_of = [](const void* p) {
+    return (int)(reinterpret_cast<uintptr_t>(p) / sizeof(T) & (E - 1));
+  };
   const bool vec = phase_of(x) == phase_of(y) && (!residual || phase_of(x) == phase_of(residual));
   const int phase = vec ? phase_of(x) : 0;
-  constexpr int U = 8 / (int)sizeof(T);      // 64 bytes of an operand a thread
-  const int64_t blocks = ((n + phase + 7) / 8 + U * kDropThreads - 1) / (U * kDropThreads);
+  const int64_t span = (int64_t)kDropPieces * kDropThreads * E;
+  const unsigned blocks = (unsigned)((n + phase + span - 1) / span);
   if (residual)
-    dropout_kernel<T, U, true><<<(unsigned)blocks, kDropThreads, 0, s>>>(
-        n, px, pr, d, static_cast<T*>(y), phase, vec);
+    dropout_kernel<T, true><<<blocks, kDropThreads, 0, s>>>(n, px, pr, d, static_cast<T*>(y), phase, vec);
   else
-    dropout_kernel<T, U, false><<<(unsigned)blocks, kDropThreads, 0, s>>>(
-        n, px, pr, d, static_cast<T*>(y), phase, vec);
+    dropout_kernel<T, false><<<blocks, kDropThreads, 0, s>>>(n, px, pr, d, static_cast<T*>(y), phase, vec);
   return cudaGetLastError();
 }
 
@@ -95,7 +95,7 @@ extern "C" muon_status muon_dropout(int64_t n, int dtype, const void* x, const v
                                     float p, uint64_t seed, uint64_t offset, void* y,
                                     void* stream) {
   if (n < 0 || (n > 0 && (!x || !y)) || !(p >= 0.f && p <= 1.f)) return MUON_ERR_INVALID_ARG;
-  if (n > (int64_t)1 << 42) return MUON_ERR_UNSUPPORTED_SHAPE;
+  if (n > (int64_t)1 << 40) return MUON_ERR_UNSUPPORTED_SHAPE;
   if (dtype != MUON_BF16 && dtype != MUON_F32) return MUON_ERR_DTYPE;
   const size_t es = dtype == MUON_BF16 ? 2 : 4;
   if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(residual) |

@@ -11,23 +11,30 @@ struct NormFwd {
   void *sum, *y;
   float *mean, *rstd;
   float eps;
-  int wbf16;        // weight and bias are bf16
+  int wbf16;        // weight and bias are bf16 ...
+  int wvec;         // ... and 16-byte aligned
   int drop;
   int vec;          // every operand's rows share one phase
-  int depth;        // of the ring
   Drop d;
 };
 
-// TPR threads a row (0: the block), C chunks a thread.  FUSED: residual and
-// dropout may be present.
+// blocks of NT threads an SM: 24 warps, 80 registers a thread
+__host__ __device__ constexpr int fwd_blocks(int nt) { return nt <= 768 ? 768 / nt : 1; }
+
+// TPR threads a row (0: the block), C eights of elements a thread.  FUSED:
+// residual and dropout may be present.
 template <typename T, int TPR, int C, int NT, bool FUSED, bool REG>
-__global__ void __launch_bounds__(NT, fwd_blocks(TPR, C, NT))
+__global__ void __launch_bounds__(NT, fwd_blocks(NT))
 norm_fwd_kernel(const __grid_constant__ NormFwd a) {
   extern __shared__ uint4 ring[];
   __shared__ alignas(16) float slots[2][32];
-  constexpr int OPS = FUSED ? 2 : 1, PER = C * kPieces<T>;
-  const Place<TPR> at;
-  const int nt = blockDim.x, warps = nt >> 5, cols = (int)a.cols;
+  constexpr int E = kEl<T>, OPS = FUSED ? 2 : 1, PER = C * 8 / E;   // pieces a thread and operand
+  constexpr int D = ring_depth(NT, C, sizeof(T), OPS, fwd_blocks(NT), 0);
+  const int nt = REG || TPR ? NT : blockDim.x;
+  const int width = TPR ? TPR : nt, groups = TPR ? NT / (TPR ? TPR : 1) : 1;
+  const int t = TPR ? (int)threadIdx.x % (TPR ? TPR : 1) : (int)threadIdx.x;
+  const int g = TPR ? (int)threadIdx.x / (TPR ? TPR : 1) : 0;
+  const int cols = (int)a.cols;
   const T* x = static_cast<const T*>(a.x);
   const T* res = static_cast<const T*>(a.residual);
   if constexpr (TPR == 0) {
@@ -35,12 +42,11 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
     __syncthreads();
   }
   const bool vec = REG || a.vec;
-  const Visits go = visits(at, a.rows);
-  const int phase =
-      REG || !vec ? 0
-                  : (int)((reinterpret_cast<uintptr_t>(x) / sizeof(T) + (uint64_t)go.first * a.ldx) & 7);
-  const int col = at.t * 8 - phase;             // chunk i begins at column col + i * span
-  const int span = at.width * 8;
+  const Visits go = visits(groups, g, a.rows);
+  const int phase = REG || !vec ? 0
+      : (int)((reinterpret_cast<uintptr_t>(x) / sizeof(T) + (uint64_t)go.first * a.ldx) & (E - 1));
+  const int col = t * E - phase;                // piece k begins at column col + k * span
+  const int span = width * E;
   // this thread's place in the next row to copy in, and in the current row
   const T *fx = x + go.first * a.ldx + col, *fr = res + go.first * a.ldr + col;
   const T *cx = fx, *cr = fr;
@@ -52,11 +58,10 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
   auto start = [&] {
     if (vec && ahead < go.mine) {
       #pragma unroll
-      for (int i = 0; i < C; ++i) {
-        const int c0 = col + i * span;
-        fetch<T, REG>(fill + i * kPieces<T> * nt, nt, fx + i * span, x, c0, cols);
-        if (FUSED && res)
-          fetch<T, REG>(fill + (PER + i * kPieces<T>) * nt, nt, fr + i * span, res, c0, cols);
+      for (int k = 0; k < PER; ++k) {
+        const int c0 = col + k * span;
+        fetch<T, REG>(fill + k * nt, fx + k * span, x, c0, cols);
+        if (FUSED && res) fetch<T, REG>(fill + (PER + k) * nt, fr + k * span, res, c0, cols);
       }
     }
     copy_commit();
@@ -64,73 +69,75 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
     fx += go.step * a.ldx;
     if constexpr (FUSED) fr += go.step * a.ldr;
     fill += stage_len;
-    if (fill == ring0 + a.depth * stage_len) fill = ring0;
+    if (fill == ring0 + D * stage_len) fill = ring0;
   };
-  for (int s = 0; s + 1 < a.depth; ++s) start();
-  Chunk w[C], b[C];
   #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    columns(w[i], a.weight, a.wbf16, col + i * span, cols, 1.f);
-    columns(b[i], a.bias, a.wbf16, col + i * span, cols, 0.f);
+  for (int s = 0; s + 1 < D; ++s) start();
+  Piece<E> w[PER], b[PER];
+  #pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    columns<T, REG>(w[k], a.weight, a.wbf16, col + k * span, cols, 1.f, a.wvec);
+    columns<T, REG>(b[k], a.bias, a.wbf16, col + k * span, cols, 0.f, a.wvec);
   }
   const float inv = 1.f / (float)cols;
   const uint4* from = ring0;
   int64_t row = go.first;
   for (int visit = 0; visit < go.all; ++visit) {
     start();                              // into the slot read in the last visit
-    copy_wait(a.depth - 1);
+    copy_wait<D - 1>();
     const bool live = TPR == 0 || visit < go.mine;
-    Chunk v[C];
+    Piece<E> v[PER];
     float2 s2 = both(0.f);
     #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int c0 = col + i * span;
+    for (int k = 0; k < PER; ++k) {
+      const int c0 = col + k * span;
       if (live) {
-        take<T, REG>(v[i], from + i * kPieces<T> * nt, nt, cx + i * span, x, c0, cols, vec);
+        take<T, REG>(v[k], from + k * nt, cx + k * span, x, c0, cols, vec);
         if constexpr (FUSED) {
-          if (a.drop) drop8(v[i].v, out + i * span, a.d);
+          if (a.drop) drop<E>(v[k].v, out + k * span, a.d);
           if (res) {
-            Chunk r;
-            take<T, REG>(r, from + (PER + i * kPieces<T>) * nt, nt, cr + i * span, res, c0, cols, vec);
+            Piece<E> r;
+            take<T, REG>(r, from + (PER + k) * nt, cr + k * span, res, c0, cols, vec);
             #pragma unroll
-            for (int j = 0; j < 4; ++j) v[i].v[j] = add2(v[i].v[j], r.v[j]);
+            for (int j = 0; j < E / 2; ++j) v[k].v[j] = add2(v[k].v[j], r.v[j]);
           }
-          if (a.sum) put<T, REG>(static_cast<T*>(a.sum) + out + i * span, c0, cols, v[i], vec);
+          if (a.sum) put<T, REG>(static_cast<T*>(a.sum) + out + k * span, c0, cols, v[k], vec);
         }
       } else {
-        clear(v[i]);
+        clear(v[k]);
       }
       #pragma unroll
-      for (int j = 0; j < 4; ++j) s2 = add2(s2, v[i].v[j]);
+      for (int j = 0; j < E / 2; ++j) s2 = add2(s2, v[k].v[j]);
     }
-    const float mean = row_sum<TPR>(s2.x + s2.y, slots[0], warps) * inv;
+    const float mean = row_sum<TPR>(s2.x + s2.y, slots[0], nt >> 5) * inv;
     const float2 m2 = both(-mean);
     float2 q2 = both(0.f);
     #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int c0 = col + i * span;
+    for (int k = 0; k < PER; ++k) {
+      const int c0 = col + k * span;
       #pragma unroll
-      for (int j = 0; j < 4; ++j) v[i].v[j] = add2(v[i].v[j], m2);
-      if (whole<REG>(c0, cols)) {
+      for (int j = 0; j < E / 2; ++j) v[k].v[j] = add2(v[k].v[j], m2);
+      if (whole<T, REG>(c0, cols)) {
         #pragma unroll
-        for (int j = 0; j < 4; ++j) q2 = fma2(v[i].v[j], v[i].v[j], q2);
+        for (int j = 0; j < E / 2; ++j) q2 = fma2(v[k].v[j], v[k].v[j], q2);
       } else if (!REG) {
         #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (inside(c0 + j, cols)) q2.x = fmaf(elem(v[i], j), elem(v[i], j), q2.x);
+        for (int j = 0; j < E; ++j)
+          if (inside(c0 + j, cols)) q2.x = fmaf(elem(v[k], j), elem(v[k], j), q2.x);
       }
     }
-    const float rstd = rsqrtf(row_sum<TPR>(q2.x + q2.y, slots[1], warps) * inv + a.eps);
+    const float rstd = rsqrtf(row_sum<TPR>(q2.x + q2.y, slots[1], nt >> 5) * inv + a.eps);
     if (live) {
       const float2 r2 = both(rstd);
       #pragma unroll
-      for (int i = 0; i < C; ++i) {
-        const int c0 = col + i * span;
+      for (int k = 0; k < PER; ++k) {
+        const int c0 = col + k * span;
         #pragma unroll
-        for (int j = 0; j < 4; ++j) v[i].v[j] = fma2(mul2(v[i].v[j], r2), w[i].v[j], b[i].v[j]);
-        put<T, REG>(static_cast<T*>(a.y) + out + i * span, c0, cols, v[i], vec);
+        for (int j = 0; j < E / 2; ++j)
+          v[k].v[j] = fma2(mul2(v[k].v[j], r2), w[k].v[j], b[k].v[j]);
+        put<T, REG>(static_cast<T*>(a.y) + out + k * span, c0, cols, v[k], vec);
       }
-      if (at.t == 0) {
+      if (t == 0) {
         if (a.mean) a.mean[row] = mean;
         if (a.rstd) a.rstd[row] = rstd;
       }
@@ -142,7 +149,7 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
       cr += go.step * a.ldr;
     }
     from += stage_len;
-    if (from == ring0 + a.depth * stage_len) from = ring0;
+    if (from == ring0 + D * stage_len) from = ring0;
   }
 }
 
@@ -186,27 +193,41 @@ __global__ void __launch_bounds__(kNormThreads) norm_long_fwd_kernel(const __gri
 
 // --------------------------------------------------------------------- host
 
+// One kernel of the forward pass: `nt` threads a block, at most NT.
+template <typename T, int TPR, int C, int NT, bool FUSED, bool REG>
+cudaError_t launch_fwd(const NormFwd& a, int nt, cudaStream_t s) {
+  constexpr int D = ring_depth(NT, C, sizeof(T), FUSED ? 2 : 1, fwd_blocks(NT), 0);
+  const size_t smem = (size_t)D * nt * C * 8 * sizeof(T) * (FUSED ? 2 : 1);
+  return launch_rows(norm_fwd_kernel<T, TPR, C, NT, FUSED, REG>, a,
+                     blocks_for(a.rows, TPR ? NT / (TPR ? TPR : 1) : 1, fwd_blocks(nt)), nt, smem, s);
+}
+
+// Rows of up to 64 columns take 8 lanes, of up to 512 a warp, longer ones a
+// block of sixteen elements a thread.  Regular rows run on the next block size
+// that is compiled in; ragged ones on exactly the warps that their pieces
+// need, eight elements a thread where that leaves fewer idle.
 template <typename T, bool FUSED, bool REG>
-cudaError_t forward(NormFwd a, int64_t chunks, cudaStream_t s) {
-  const Shape sh = norm_shape(chunks, false);
-  size_t smem;
-  ring_of(sh, sizeof(T), FUSED ? 2 : 1, &a.depth, &smem);
-  const int64_t grid = norm_grid(sh, a.rows);
-  if (sh.tpr == 8)
-    return launch_rows(norm_fwd_kernel<T, 8, 1, 256, FUSED, REG>, a, grid, sh.nt, smem, s);
-  if (sh.tpr == 32 && sh.c == 1)
-    return launch_rows(norm_fwd_kernel<T, 32, 1, 256, FUSED, REG>, a, grid, sh.nt, smem, s);
-  if (sh.tpr == 32)
-    return launch_rows(norm_fwd_kernel<T, 32, 2, 256, FUSED, REG>, a, grid, sh.nt, smem, s);
-  if (sh.c == 1)
-    return launch_rows(norm_fwd_kernel<T, 0, 1, 128, FUSED, REG>, a, grid, sh.nt, smem, s);
-  if (sh.nt <= 128)
-    return launch_rows(norm_fwd_kernel<T, 0, 2, 128, FUSED, REG>, a, grid, sh.nt, smem, s);
-  if (sh.nt <= 256)
-    return launch_rows(norm_fwd_kernel<T, 0, 2, 256, FUSED, REG>, a, grid, sh.nt, smem, s);
-  if (sh.nt <= 512)
-    return launch_rows(norm_fwd_kernel<T, 0, 2, 512, FUSED, REG>, a, grid, sh.nt, smem, s);
-  return launch_rows(norm_fwd_kernel<T, 0, 2, 1024, FUSED, REG>, a, grid, sh.nt, smem, s);
+cudaError_t forward(const NormFwd& a, int64_t chunks, cudaStream_t s) {
+  if (chunks <= 8) return launch_fwd<T, 8, 1, 256, FUSED, REG>(a, 256, s);
+  if (chunks <= 32) return launch_fwd<T, 32, 1, 256, FUSED, REG>(a, 256, s);
+  if (chunks <= 64) return launch_fwd<T, 32, 2, 256, FUSED, REG>(a, 256, s);
+  const int one = (int)(chunks + 31) / 32 * 32, two = (int)((chunks + 1) / 2 + 31) / 32 * 32;
+  if constexpr (REG) {
+    if (chunks <= 128) return launch_fwd<T, 0, 1, 128, FUSED, REG>(a, 128, s);
+    if (two <= 128) return launch_fwd<T, 0, 2, 128, FUSED, REG>(a, 128, s);
+    if (two <= 192) return launch_fwd<T, 0, 2, 192, FUSED, REG>(a, 192, s);
+    if (two <= 256) return launch_fwd<T, 0, 2, 256, FUSED, REG>(a, 256, s);
+    if (two <= 384) return launch_fwd<T, 0, 2, 384, FUSED, REG>(a, 384, s);
+    if (two <= 512) return launch_fwd<T, 0, 2, 512, FUSED, REG>(a, 512, s);
+    if (two <= 704) return launch_fwd<T, 0, 2, 704, FUSED, REG>(a, 704, s);
+    return launch_fwd<T, 0, 2, 1024, FUSED, REG>(a, 1024, s);
+  } else {
+    if (one <= 256 && one < 2 * two) return launch_fwd<T, 0, 1, 256, FUSED, REG>(a, one, s);
+    if (two <= 128) return launch_fwd<T, 0, 2, 128, FUSED, REG>(a, two, s);
+    if (two <= 256) return launch_fwd<T, 0, 2, 256, FUSED, REG>(a, two, s);
+    if (two <= 512) return launch_fwd<T, 0, 2, 512, FUSED, REG>(a, two, s);
+    return launch_fwd<T, 0, 2, 1024, FUSED, REG>(a, two, s);
+  }
 }
 
 template <typename T>
@@ -247,7 +268,8 @@ extern "C" muon_status muon_layer_norm(int64_t rows, int64_t cols, int dtype, in
   ph.add(y, cols);
   const bool fused = residual || sum || p > 0.f;
   const NormFwd a = {rows, cols, ldx, ldr, x, residual, weight, bias, sum, y, mean, rstd, eps,
-                     wdtype == MUON_BF16, p > 0.f, ph.same, 1, make_drop(p, seed, offset)};
+                     wdtype == MUON_BF16, !misaligned(weight, 16) && !misaligned(bias, 16), p > 0.f,
+                     ph.same, make_drop(p, seed, offset)};
   cudaError_t e;
   if (ph.chunks() > kMaxChunks) {
     const int grid = (int)(rows < kSMs * 8 ? rows : kSMs * 8);

@@ -11,38 +11,59 @@ struct NormBwd {
   const float *mean, *rstd;
   void *dx, *dresidual;
   float* part;      // [parts][2][cols], or null
-  int wbf16;
+  int wbf16;        // the weight is bf16 ...
+  int wvec;         // ... and 16-byte aligned
   int drop;
-  int vec;
-  int depth;
+  int vec;          // every operand's rows share one phase
+  int width;        // threads a row
   Drop d;
 };
 
-// KEEP: the row's values stay in registers between the reduction and the
-// output; otherwise (blocks of 1024 threads, 64 registers each) they are read
-// from the ring twice, and the weight from memory.
-template <typename T, int TPR, int C, int NT, bool FUSED, bool KEEP, bool REG>
-__global__ void __launch_bounds__(NT, bwd_blocks(NT))
+// waits for the threads of row group g alone
+__device__ __forceinline__ void group_sync(int g, int width) {
+  asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(width) : "memory");
+}
+
+constexpr int kBwdThreads = 512;     // one block an SM, 128 registers a thread
+
+// shared memory for the weight of C eights of columns a thread, where the ring
+// leaves room for it
+__host__ __device__ constexpr int weight_bytes(int c, int es, int ops) {
+  const int w = kBwdThreads * c * 8 * 4;
+  return kBwdThreads * c * 8 * es * ops + w <= 220 << 10 ? w : 0;
+}
+
+// One block an SM, cut into row groups of TPR lanes or (TPR 0) of W threads
+// (W 0: a.width), so that an SM leaves one partial column sum; C eights of
+// elements a thread.  KEEP: the row's values and the weight stay in registers
+// between the reduction and the output; otherwise (long rows) the values are
+// read from the ring twice, and the weight from shared memory.
+template <typename T, int TPR, int C, int W, bool FUSED, bool KEEP, bool REG>
+__global__ void __launch_bounds__(kBwdThreads, 1)
 norm_bwd_kernel(const __grid_constant__ NormBwd a) {
   extern __shared__ uint4 ring[];
-  __shared__ alignas(16) float slots[2][2][32];
-  constexpr int OPS = FUSED ? 3 : 2, PER = C * kPieces<T>;
-  const Place<TPR> at;
-  const int nt = blockDim.x, warps = nt >> 5, cols = (int)a.cols;
+  __shared__ alignas(16) float slots[2][2][40];
+  constexpr int E = kEl<T>, OPS = FUSED ? 3 : 2, PER = C * 8 / E;
+  constexpr int WB = KEEP ? 0 : weight_bytes(C, sizeof(T), OPS);
+  constexpr int D = ring_depth(kBwdThreads, C, sizeof(T), OPS, 1, WB);
+  const int nt = TPR || W ? kBwdThreads : blockDim.x;
+  const int width = TPR ? TPR : W ? W : a.width;
+  const int groups = nt / width, g = (int)threadIdx.x / width, t = (int)threadIdx.x - g * width;
+  const int warps = ((width >> 5) + 3) & ~3;      // of a row group, in whole float4s
+  const int cols = (int)a.cols;
   const T* dy = static_cast<const T*>(a.dy);
   const T* sum = static_cast<const T*>(a.sum);
   const T* ds = static_cast<const T*>(a.dsum);
   if constexpr (TPR == 0) {
-    for (int i = threadIdx.x; i < 128; i += nt) (&slots[0][0][0])[i] = 0.f;
+    for (int i = threadIdx.x; i < 160; i += nt) (&slots[0][0][0])[i] = 0.f;
     __syncthreads();
   }
   const bool vec = REG || a.vec;
-  const Visits go = visits(at, a.rows);
-  const int phase =
-      REG || !vec ? 0
-                  : (int)((reinterpret_cast<uintptr_t>(dy) / sizeof(T) + (uint64_t)go.first * a.lddy) & 7);
-  const int col = at.t * 8 - phase;             // chunk i begins at column col + i * span
-  const int span = at.width * 8;
+  const Visits go = visits(groups, g, a.rows);
+  const int phase = REG || !vec ? 0
+      : (int)((reinterpret_cast<uintptr_t>(dy) / sizeof(T) + (uint64_t)go.first * a.lddy) & (E - 1));
+  const int col = t * E - phase;                // piece k begins at column col + k * span
+  const int span = width * E;
   // this thread's place in the next row to copy in, and in the current row
   const T *fy = dy + go.first * a.lddy + col, *fs = sum + go.first * a.lds + col,
           *fd = ds + go.first * a.ldds + col;
@@ -55,12 +76,11 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
   auto start = [&] {
     if (vec && ahead < go.mine) {
       #pragma unroll
-      for (int i = 0; i < C; ++i) {
-        const int c0 = col + i * span;
-        fetch<T, REG>(fill + i * kPieces<T> * nt, nt, fy + i * span, dy, c0, cols);
-        fetch<T, REG>(fill + (PER + i * kPieces<T>) * nt, nt, fs + i * span, sum, c0, cols);
-        if (FUSED && ds)
-          fetch<T, REG>(fill + (2 * PER + i * kPieces<T>) * nt, nt, fd + i * span, ds, c0, cols);
+      for (int k = 0; k < PER; ++k) {
+        const int c0 = col + k * span;
+        fetch<T, REG>(fill + k * nt, fy + k * span, dy, c0, cols);
+        fetch<T, REG>(fill + (PER + k) * nt, fs + k * span, sum, c0, cols);
+        if (FUSED && ds) fetch<T, REG>(fill + (2 * PER + k) * nt, fd + k * span, ds, c0, cols);
       }
     }
     copy_commit();
@@ -69,119 +89,153 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
     fs += go.step * a.lds;
     if constexpr (FUSED) fd += go.step * a.ldds;
     fill += stage_len;
-    if (fill == ring0 + a.depth * stage_len) fill = ring0;
+    if (fill == ring0 + D * stage_len) fill = ring0;
   };
-  for (int s = 0; s + 1 < a.depth; ++s) start();
-  Chunk w[KEEP ? C : 1], accw[C], accb[C];
   #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    if constexpr (KEEP) columns(w[i], a.weight, a.wbf16, col + i * span, cols, 1.f);
-    clear(accw[i]);
-    clear(accb[i]);
+  for (int s = 0; s + 1 < D; ++s) start();
+  Piece<E> w[KEEP ? PER : 1], accw[PER], accb[PER];
+  // the weight's place in shared memory, two pairs at a time
+  float4* const ws = reinterpret_cast<float4*>(ring + D * stage_len) + threadIdx.x;
+  #pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    Piece<E>& wk = w[KEEP ? k : 0];
+    if (KEEP || WB) columns<T, REG>(wk, a.weight, a.wbf16, col + k * span, cols, 1.f, a.wvec);
+    if (!KEEP && WB) {
+      #pragma unroll
+      for (int j = 0; j < E / 4; ++j)
+        ws[(k * (E / 4) + j) * nt] = make_float4(wk.v[2 * j].x, wk.v[2 * j].y, wk.v[2 * j + 1].x,
+                                                 wk.v[2 * j + 1].y);
+    }
+    clear(accw[k]);
+    clear(accb[k]);
   }
+  auto weight = [&](int k) {      // into w[0], where it is not kept
+    if constexpr (WB) {
+      #pragma unroll
+      for (int j = 0; j < E / 4; ++j) {
+        const float4 q = ws[(k * (E / 4) + j) * nt];
+        w[0].v[2 * j] = make_float2(q.x, q.y);
+        w[0].v[2 * j + 1] = make_float2(q.z, q.w);
+      }
+    } else {
+      columns<T, REG>(w[0], a.weight, a.wbf16, col + k * span, cols, 1.f, a.wvec);
+    }
+  };
   const float inv = 1.f / (float)cols;
   const float *pm = a.mean + go.first, *pr = a.rstd + go.first;
   float mean_next = 0.f, rstd_next = 0.f;
   if (go.mine > 0) { mean_next = *pm; rstd_next = *pr; }
   const uint4* from = ring0;
   int turn = 0;
-  for (int visit = 0; visit < go.all; ++visit) {
+  // groups of whole warps meet only among themselves, so each makes its own
+  // visits; lanes that share a warp make the block's
+  const int visits_made = TPR == 0 ? go.mine : go.all;
+  for (int visit = 0; visit < visits_made; ++visit) {
     start();                              // into the slot read in the last visit
     const bool live = TPR == 0 || visit < go.mine;
     const float2 mean = both(-mean_next), rstd = both(rstd_next);
     pm += go.step;
     pr += go.step;
     if (visit + 1 < go.mine) { mean_next = *pm; rstd_next = *pr; }
-    copy_wait(a.depth - 1);
-    // dy and h = (sum - mean) * rstd of chunk i
-    auto value = [&](int i, Chunk& y, Chunk& h) {
-      const int c0 = col + i * span;
-      take<T, REG>(y, from + i * kPieces<T> * nt, nt, cy + i * span, dy, c0, cols, vec);
-      take<T, REG>(h, from + (PER + i * kPieces<T>) * nt, nt, cs + i * span, sum, c0, cols, vec);
+    copy_wait<D - 1>();
+    // dy and h = (sum - mean) * rstd of piece k
+    auto value = [&](int k, Piece<E>& y, Piece<E>& h) {
+      const int c0 = col + k * span;
+      take<T, REG>(y, from + k * nt, cy + k * span, dy, c0, cols, vec);
+      take<T, REG>(h, from + (PER + k) * nt, cs + k * span, sum, c0, cols, vec);
       #pragma unroll
-      for (int j = 0; j < 4; ++j) h.v[j] = mul2(add2(h.v[j], mean), rstd);
-      if (!REG && !whole<REG>(c0, cols)) {     // dy is 0 there, but h may be infinite
+      for (int j = 0; j < E / 2; ++j) h.v[j] = mul2(add2(h.v[j], mean), rstd);
+      if (!REG && !whole<T, REG>(c0, cols)) {     // dy is 0 there, but h may be infinite
         #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < E; ++j)
           if (!inside(c0 + j, cols)) elem(h, j) = 0.f;
       }
     };
-    Chunk g[KEEP ? C : 1], h[KEEP ? C : 1];
+    Piece<E> gk[KEEP ? PER : 1], hk[KEEP ? PER : 1];
     float2 sg2 = both(0.f), sh2 = both(0.f);
     #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      Chunk& gi = g[KEEP ? i : 0];
-      Chunk& hi = h[KEEP ? i : 0];
-      Chunk& wi = w[KEEP ? i : 0];
-      if (live && (!REG || col + i * span < cols)) {
-        value(i, gi, hi);
+    for (int k = 0; k < PER; ++k) {
+      Piece<E>& gi = gk[KEEP ? k : 0];
+      Piece<E>& hi = hk[KEEP ? k : 0];
+      if (live && (!REG || col + k * span < cols)) {
+        value(k, gi, hi);
       } else {
         clear(gi);
         clear(hi);
       }
-      if constexpr (!KEEP) columns(wi, a.weight, a.wbf16, col + i * span, cols, 1.f);
+      if constexpr (!KEEP) weight(k);
+      const Piece<E>& wi = w[KEEP ? k : 0];
       #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        accw[i].v[j] = fma2(gi.v[j], hi.v[j], accw[i].v[j]);
-        accb[i].v[j] = add2(gi.v[j], accb[i].v[j]);
+      for (int j = 0; j < E / 2; ++j) {
+        accw[k].v[j] = fma2(gi.v[j], hi.v[j], accw[k].v[j]);
+        accb[k].v[j] = add2(gi.v[j], accb[k].v[j]);
         gi.v[j] = mul2(gi.v[j], wi.v[j]);
         sg2 = add2(sg2, gi.v[j]);
         sh2 = fma2(gi.v[j], hi.v[j], sh2);
       }
     }
-    // the two sums share a barrier; a slot pair is rewritten two rows later,
-    // after the barrier of the row between
     float sg = sg2.x + sg2.y, sh = sh2.x + sh2.y;
-    float* s2 = slots[turn][0];
-    turn ^= 1;
-    #pragma unroll
-    for (int o = (TPR == 0 ? 32 : TPR) / 2; o > 0; o >>= 1) {
-      sg += __shfl_xor_sync(0xffffffffu, sg, o);
-      sh += __shfl_xor_sync(0xffffffffu, sh, o);
-    }
-    if constexpr (TPR == 0) {
-      if ((threadIdx.x & 31) == 0) {
-        s2[threadIdx.x >> 5] = sg;
-        s2[32 + (threadIdx.x >> 5)] = sh;
+    if constexpr (TPR == 8) {
+      #pragma unroll
+      for (int o = 4; o > 0; o >>= 1) {
+        sg += __shfl_xor_sync(0xffffffffu, sg, o);
+        sh += __shfl_xor_sync(0xffffffffu, sh, o);
       }
-      __syncthreads();
-      sg = sh = 0.f;
-      for (int i = 0; i < warps; i += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(s2 + i);
-        const float4 e = *reinterpret_cast<const float4*>(s2 + 32 + i);
-        sg += (f.x + f.y) + (f.z + f.w);
-        sh += (e.x + e.y) + (e.z + e.w);
+    } else {
+      // half a warp adds up one sum, half the other
+      const bool low = (threadIdx.x & 16) == 0;
+      float v = (low ? sg : sh) + __shfl_xor_sync(0xffffffffu, low ? sh : sg, 16);
+      #pragma unroll
+      for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if constexpr (TPR == 32) {
+        sg = __shfl_sync(0xffffffffu, v, 0);
+        sh = __shfl_sync(0xffffffffu, v, 16);
+      } else {
+        // a slot pair is rewritten two rows later, after the barrier of the
+        // row between
+        float* s2 = slots[turn][0] + g * warps;
+        turn ^= 1;
+        if ((threadIdx.x & 15) == 0) s2[(low ? 0 : 40) + (t >> 5)] = v;
+        group_sync(g, width);
+        sg = sh = 0.f;
+        #pragma unroll 4
+        for (int i = 0; i < warps; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(s2 + i);
+          const float4 e = *reinterpret_cast<const float4*>(s2 + 40 + i);
+          sg += (f.x + f.y) + (f.z + f.w);
+          sh += (e.x + e.y) + (e.z + e.w);
+        }
       }
     }
     const float2 mg = both(-sg * inv), mh = both(-sh * inv);
     if (live) {
       #pragma unroll
-      for (int i = 0; i < C; ++i) {
-        const int c0 = col + i * span;
-        Chunk d;
-        Chunk& gi = g[KEEP ? i : 0];
-        Chunk& hi = h[KEEP ? i : 0];
+      for (int k = 0; k < PER; ++k) {
+        const int c0 = col + k * span;
+        Piece<E> d;
+        Piece<E>& gi = gk[KEEP ? k : 0];
+        Piece<E>& hi = hk[KEEP ? k : 0];
         if constexpr (!KEEP) {
-          value(i, gi, hi);
-          columns(w[0], a.weight, a.wbf16, c0, cols, 1.f);
+          value(k, gi, hi);
+          weight(k);
           #pragma unroll
-          for (int j = 0; j < 4; ++j) gi.v[j] = mul2(gi.v[j], w[0].v[j]);
+          for (int j = 0; j < E / 2; ++j) gi.v[j] = mul2(gi.v[j], w[0].v[j]);
         }
         #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < E / 2; ++j)
           d.v[j] = mul2(rstd, fma2(hi.v[j], mh, add2(gi.v[j], mg)));
         if constexpr (FUSED) {
           if (ds) {
-            Chunk e;
-            take<T, REG>(e, from + (2 * PER + i * kPieces<T>) * nt, nt, cd + i * span, ds, c0, cols, vec);
+            Piece<E> e;
+            take<T, REG>(e, from + (2 * PER + k) * nt, cd + k * span, ds, c0, cols, vec);
             #pragma unroll
-            for (int j = 0; j < 4; ++j) d.v[j] = add2(d.v[j], e.v[j]);
+            for (int j = 0; j < E / 2; ++j) d.v[j] = add2(d.v[j], e.v[j]);
           }
           if (a.dresidual)
-            put<T, REG>(static_cast<T*>(a.dresidual) + out + i * span, c0, cols, d, vec);
-          if (a.drop) drop8(d.v, out + i * span, a.d);
+            put<T, REG>(static_cast<T*>(a.dresidual) + out + k * span, c0, cols, d, vec);
+          if (a.drop) drop<E>(d.v, out + k * span, a.d);
         }
-        if (a.dx) put<T, REG>(static_cast<T*>(a.dx) + out + i * span, c0, cols, d, vec);
+        if (a.dx) put<T, REG>(static_cast<T*>(a.dx) + out + k * span, c0, cols, d, vec);
       }
     }
     out += go.step * a.cols;
@@ -191,76 +245,88 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
       cd += go.step * a.ldds;
     }
     from += stage_len;
-    if (from == ring0 + a.depth * stage_len) from = ring0;
+    if (from == ring0 + D * stage_len) from = ring0;
   }
+  // the join may be set up while the column sums are put together
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!a.part) return;
-  // this block's column sums
   float* pw = a.part + (int64_t)blockIdx.x * 2 * a.cols;
   float* pb = pw + a.cols;
-  if constexpr (TPR == 0) {
+  if (TPR == 0 && groups == 1) {
     #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int c0 = col + i * span;
+    for (int k = 0; k < PER; ++k) {
+      const int c0 = col + k * span;
       #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < E; ++j)
         if (inside(c0 + j, cols)) {
-          pw[c0 + j] = elem(accw[i], j);
-          pb[c0 + j] = elem(accb[i], j);
+          pw[c0 + j] = elem(accw[k], j);
+          pb[c0 + j] = elem(accb[k], j);
         }
     }
-  } else {
-    // row groups in order, through the ring's memory (every copy has landed
-    // and been read)
-    copy_wait(0);
-    __syncthreads();
-    float* buf = reinterpret_cast<float*>(ring);
-    for (int c = threadIdx.x; c < 2 * cols; c += nt) buf[c] = 0.f;
-    __syncthreads();
-    for (int r = 0; r < at.rows; ++r) {
-      if (r == at.g) {
-        #pragma unroll
-        for (int i = 0; i < C; ++i) {
-          const int c0 = col + i * span;
-          #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (inside(c0 + j, cols)) {
-              buf[c0 + j] += elem(accw[i], j);
-              buf[cols + c0 + j] += elem(accb[i], j);
-            }
-        }
-      }
-      __syncthreads();
-    }
-    for (int c = threadIdx.x; c < 2 * cols; c += nt) pw[c] = buf[c];
+    return;
   }
+  // row groups in order, through the ring's memory (every copy has landed and
+  // been read)
+  copy_wait<0>();
+  __syncthreads();
+  float* buf = reinterpret_cast<float*>(ring);
+  // regular rows have their columns at the same lanes in every group, so the
+  // groups of a warp are added by shuffles first
+  constexpr int kTogether = REG && TPR == 8 ? 4 : 1;
+  if constexpr (kTogether == 4) {
+    #pragma unroll
+    for (int o = 8; o < 32; o <<= 1)
+      #pragma unroll
+      for (int k = 0; k < PER; ++k)
+        #pragma unroll
+        for (int j = 0; j < E; ++j) {
+          elem(accw[k], j) += __shfl_xor_sync(0xffffffffu, elem(accw[k], j), o);
+          elem(accb[k], j) += __shfl_xor_sync(0xffffffffu, elem(accb[k], j), o);
+        }
+  }
+  for (int r = 0; r < groups; r += kTogether) {
+    if (r == g) {
+      #pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const int c0 = col + k * span;
+        #pragma unroll
+        for (int j = 0; j < E; ++j)
+          if (inside(c0 + j, cols)) {
+            float &w0 = buf[c0 + j], &b0 = buf[cols + c0 + j];
+            w0 = r ? w0 + elem(accw[k], j) : elem(accw[k], j);
+            b0 = r ? b0 + elem(accb[k], j) : elem(accb[k], j);
+          }
+      }
+    }
+    __syncthreads();
+  }
+  for (int c = threadIdx.x; c < 2 * cols; c += nt) pw[c] = buf[c];
 }
 
-// dweight and dbias from the blocks' column sums: 32 columns a block, eight
-// threads a column, then the eight in order
+// dweight (blockIdx.y 0) and dbias (1) from the blocks' column sums: 32 columns a
+// block, eight threads a column, then the eight in order
 template <typename WT>
 __global__ void __launch_bounds__(256) norm_join_kernel(int64_t cols, int parts, const float* part,
                                                         WT* dweight, WT* dbias) {
-  __shared__ float red[2][8][32];
-  pdl_wait();
+  __shared__ float red[8][32];
+  WT* out = blockIdx.y == 0 ? dweight : dbias;
+  if (!out) return;
   const int64_t c = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
   const int k = threadIdx.x >> 5;
-  float w = 0.f, b = 0.f;
+  const float* p = part + blockIdx.y * cols + c;
+  float s = 0.f;
+  pdl_wait();
   if (c < cols) {
-    #pragma unroll 4
-    for (int i = k; i < parts; i += 8) {
-      w += part[(int64_t)i * 2 * cols + c];
-      b += part[((int64_t)i * 2 + 1) * cols + c];
-    }
+    #pragma unroll 10
+    for (int i = k; i < parts; i += 8) s += p[(int64_t)i * 2 * cols];
   }
-  red[0][k][threadIdx.x & 31] = w;
-  red[1][k][threadIdx.x & 31] = b;
+  red[k][threadIdx.x & 31] = s;
   __syncthreads();
-  if (k < 2 && c < cols) {
-    float s = 0.f;
+  if (k == 0 && c < cols) {
+    s = 0.f;
     #pragma unroll
-    for (int i = 0; i < 8; ++i) s += red[k][i][threadIdx.x & 31];
-    WT* out = k == 0 ? dweight : dbias;
-    if (out) out[c] = from_f<WT>(s);
+    for (int i = 0; i < 8; ++i) s += red[i][threadIdx.x];
+    out[c] = from_f<WT>(s);
   }
 }
 
@@ -315,28 +381,47 @@ __global__ void __launch_bounds__(kNormThreads) norm_cols_kernel(const __grid_co
 
 // --------------------------------------------------------------------- host
 
-template <typename T, bool FUSED, bool REG>
-cudaError_t backward(NormBwd a, int64_t chunks, int* parts, cudaStream_t s) {
-  const Shape sh = norm_shape(chunks, true);
-  size_t smem;
-  ring_of(sh, sizeof(T), FUSED ? 3 : 2, &a.depth, &smem);
-  const int64_t grid = norm_grid(sh, a.rows);
+// partial column sums of a gradient, whatever the phases of its operands
+int64_t norm_parts(int64_t rows, int64_t cols) {
+  const int64_t most = (cols + 14) / 8 > kMaxChunks ? kLongParts : kSMs;
+  return rows < most ? rows : most;
+}
+
+template <typename T, int TPR, int C, int W, bool FUSED, bool KEEP, bool REG>
+cudaError_t launch_bwd(NormBwd a, int width, int nt, int* parts, cudaStream_t s) {
+  constexpr int OPS = FUSED ? 3 : 2, WB = KEEP ? 0 : weight_bytes(C, sizeof(T), OPS);
+  constexpr int D = ring_depth(kBwdThreads, C, sizeof(T), OPS, 1, WB);
+  a.width = width;
+  const int64_t grid = blocks_for(a.rows, nt / width, 1);
   *parts = (int)grid;
-  if (sh.tpr == 8)
-    return launch_rows(norm_bwd_kernel<T, 8, 1, 256, FUSED, true, REG>, a, grid, sh.nt, smem, s);
-  if (sh.tpr == 32 && sh.c == 1)
-    return launch_rows(norm_bwd_kernel<T, 32, 1, 256, FUSED, true, REG>, a, grid, sh.nt, smem, s);
-  if (sh.tpr == 32)
-    return launch_rows(norm_bwd_kernel<T, 32, 2, 256, FUSED, true, REG>, a, grid, sh.nt, smem, s);
-  if (sh.c == 1)
-    return launch_rows(norm_bwd_kernel<T, 0, 1, 128, FUSED, true, REG>, a, grid, sh.nt, smem, s);
-  if (sh.nt <= 128)
-    return launch_rows(norm_bwd_kernel<T, 0, 2, 128, FUSED, true, REG>, a, grid, sh.nt, smem, s);
-  if (sh.nt <= 256)
-    return launch_rows(norm_bwd_kernel<T, 0, 2, 256, FUSED, true, REG>, a, grid, sh.nt, smem, s);
-  if (sh.nt <= 512)
-    return launch_rows(norm_bwd_kernel<T, 0, 2, 512, FUSED, true, REG>, a, grid, sh.nt, smem, s);
-  return launch_rows(norm_bwd_kernel<T, 0, 2, 1024, FUSED, false, REG>, a, grid, sh.nt, smem, s);
+  return launch_rows(norm_bwd_kernel<T, TPR, C, W, FUSED, KEEP, REG>, a, grid, nt,
+                     (size_t)nt * C * 8 * sizeof(T) * OPS * D + (WB ? (size_t)nt * C * 32 : 0), s);
+}
+
+// Rows of up to 64 columns take 8 lanes, of up to 512 a warp, of up to 8192
+// whole warps of sixteen elements a thread, longer ones the block.  Regular rows
+// run on the next power of two of threads, ragged ones on exactly the warps that
+// their pieces need.
+template <typename T, bool FUSED, bool REG>
+cudaError_t backward(const NormBwd& a, int64_t chunks, int* parts, cudaStream_t s) {
+  constexpr int N = kBwdThreads;
+  if (chunks <= 8) return launch_bwd<T, 8, 1, 0, FUSED, true, REG>(a, 8, N, parts, s);
+  if (chunks <= 32) return launch_bwd<T, 32, 1, 0, FUSED, true, REG>(a, 32, N, parts, s);
+  if (chunks <= 64) return launch_bwd<T, 32, 2, 0, FUSED, true, REG>(a, 32, N, parts, s);
+  if constexpr (REG) {
+    if (chunks <= 128) return launch_bwd<T, 0, 2, 64, FUSED, true, REG>(a, 64, N, parts, s);
+    if (chunks <= 256) return launch_bwd<T, 0, 2, 128, FUSED, true, REG>(a, 128, N, parts, s);
+    if (chunks <= 512) return launch_bwd<T, 0, 2, 256, FUSED, true, REG>(a, 256, N, parts, s);
+    if (chunks <= 1024) return launch_bwd<T, 0, 2, 512, FUSED, true, REG>(a, 512, N, parts, s);
+    if (chunks <= 1536) return launch_bwd<T, 0, 3, 512, FUSED, false, REG>(a, 512, N, parts, s);
+    return launch_bwd<T, 0, 4, 512, FUSED, false, REG>(a, 512, N, parts, s);
+  } else {
+    const int c = chunks <= 1024 ? 2 : chunks <= 1536 ? 3 : 4;
+    const int width = (int)((chunks + c - 1) / c + 31) / 32 * 32;
+    if (c == 2) return launch_bwd<T, 0, 2, 0, FUSED, true, REG>(a, width, N / width * width, parts, s);
+    if (c == 3) return launch_bwd<T, 0, 3, 0, FUSED, false, REG>(a, width, width, parts, s);
+    return launch_bwd<T, 0, 4, 0, FUSED, false, REG>(a, width, width, parts, s);
+  }
 }
 
 template <typename T>
@@ -351,7 +436,7 @@ cudaError_t backward(const NormBwd& a, const Phases& ph, bool fused, int* parts,
 template <typename WT>
 cudaError_t join(int64_t cols, int parts, const float* part, void* dweight, void* dbias,
                  cudaStream_t s) {
-  return launch_k(norm_join_kernel<WT>, dim3((unsigned)((cols + 31) / 32)), dim3(256), 0, s, true,
+  return launch_k(norm_join_kernel<WT>, dim3((unsigned)((cols + 31) / 32), 2), dim3(256), 0, s, true,
                   cols, parts, part, static_cast<WT*>(dweight), static_cast<WT*>(dbias));
 }
 
@@ -409,7 +494,8 @@ extern "C" muon_status muon_layer_norm_backward(
   const bool fused = dsum || dresidual || p > 0.f;
   const NormBwd a = {rows, cols, lddy, ldsum, ldds, dy, sum, dsum, weight, mean, rstd, dx,
                      dresidual, cols_wanted ? static_cast<float*>(workspace) : nullptr,
-                     wdtype == MUON_BF16, p > 0.f, ph.same, 1, make_drop(p, seed, offset)};
+                     wdtype == MUON_BF16, !misaligned(weight, 16), p > 0.f, ph.same, 0,
+                     make_drop(p, seed, offset)};
   cudaError_t e;
   int parts = (int)(rows < kLongParts ? rows : kLongParts);
   if (ph.chunks() > kMaxChunks) {

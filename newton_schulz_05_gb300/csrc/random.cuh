@@ -15,7 +15,7 @@
 
 #include <cuda_runtime.h>
 
-#include "chunk.cuh"
+#include "pieces.cuh"
 
 namespace muon {
 
@@ -60,16 +60,11 @@ __device__ __forceinline__ uint32_t half_of(const uint4& w, int j) {
   return (j & 1) ? x >> 16 : x & 0xffffu;
 }
 
-// dropout of eight consecutive elements, the first of index i (which may be
-// below zero where a row's first chunk begins ahead of the row: such elements
-// are not used).  When i is not a multiple of eight the elements straddle two
-// blocks, whose sixteen halves are shifted into place.
-__device__ __forceinline__ void drop8(float2 (&v)[4], int64_t i, const Drop& d) {
-  if (d.threshold > 65535u) {      // p = 1
-    #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = both(0.f);
-    return;
-  }
+// The sixteen-bit halves of eight consecutive elements, the first of index i
+// (which may be below zero where a row's first piece begins ahead of the row:
+// such elements are not used).  When i is not a multiple of eight the elements
+// straddle two blocks, whose sixteen halves are shifted into place.
+__device__ __forceinline__ uint4 drop_bits(int64_t i, const Drop& d) {
   const uint64_t c = d.offset + (uint64_t)(i >> 3);
   uint4 w = philox(c, d);
   const int shift = (int)(i & 7);
@@ -88,9 +83,28 @@ __device__ __forceinline__ void drop8(float2 (&v)[4], int64_t i, const Drop& d) 
     w = make_uint4(__funnelshift_r(a[0], a[1], bits), __funnelshift_r(a[1], a[2], bits),
                    __funnelshift_r(a[2], a[3], bits), __funnelshift_r(a[3], a[4], bits));
   }
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  return w;
+}
+
+// dropout of E (4 or 8) consecutive elements, the first of index i
+template <int E>
+__device__ __forceinline__ void drop(float2 (&v)[E / 2], int64_t i, const Drop& d) {
+  if (d.threshold > 65535u) {      // p = 1
+    #pragma unroll
+    for (int j = 0; j < E / 2; ++j) v[j] = both(0.f);
+    return;
+  }
+  uint32_t u[4];
+  if (E == 4 && (i & 3) == 0) {    // half a block
+    const uint4 w = philox(d.offset + (uint64_t)(i >> 3), d);
+    u[0] = i & 4 ? w.z : w.x;
+    u[1] = i & 4 ? w.w : w.y;
+  } else {
+    const uint4 w = drop_bits(i, d);
+    u[0] = w.x; u[1] = w.y; u[2] = w.z; u[3] = w.w;
+  }
   #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < E / 2; ++j) {
     const float2 k = mul2(v[j], both(d.scale));
     v[j].x = (u[j] << 16) >= d.high ? k.x : 0.f;
     v[j].y = u[j] >= d.high ? k.y : 0.f;

@@ -18,9 +18,9 @@
 // instructions of the choice, the gradient by HBM.
 #include <cmath>
 
-#include "chunk.cuh"
 #include "common.cuh"
 #include "internal.h"
+#include "pieces.cuh"
 
 namespace muon {
 
@@ -69,6 +69,32 @@ struct RouteBwd {
   const float *dweights, *dloss;
   void* dlogits;
 };
+
+// 16-byte pieces of eight logits, as loaded, and the eight in fp32
+template <typename T> constexpr int kPieces = 8 / kEl<T>;
+__device__ __forceinline__ void widen8(float (&v)[8], const uint4 (&u)[1]) {
+  Piece<8> p;
+  widen(p, u[0]);
+  #pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = elem(p, j);
+}
+__device__ __forceinline__ void widen8(float (&v)[8], const uint4 (&u)[2]) {
+  const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+  #pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+}
+__device__ __forceinline__ void narrow8(uint4 (&u)[1], const float (&v)[8]) {
+  Piece<8> p;
+  #pragma unroll
+  for (int j = 0; j < 8; ++j) elem(p, j) = v[j];
+  u[0] = narrow(p);
+}
+__device__ __forceinline__ void narrow8(uint4 (&u)[2], const float (&v)[8]) {
+  #pragma unroll
+  for (int q = 0; q < 2; ++q)
+    u[q] = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                      __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+}
 
 // A key whose unsigned order is the order of the logits; 0 is below every
 // key.  Adding 0 turns -0 into +0 and every NaN into the canonical positive
@@ -272,10 +298,10 @@ template <typename T, int G, int NCH> struct Logits {
     #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       const int e0 = (c * G + gl) * 8;
-      Chunk w;
+      float w[8];
       #pragma unroll
-      for (int j = 0; j < 8; ++j) elem(w, j) = e0 + j < a.experts ? to_f(row[e0 + j]) : -INFINITY;
-      store8(reinterpret_cast<T*>(&u[c][0]), w);
+      for (int j = 0; j < 8; ++j) w[j] = e0 + j < a.experts ? to_f(row[e0 + j]) : -INFINITY;
+      narrow8(u[c], w);
     }
   }
 };
@@ -338,10 +364,10 @@ route_kernel(const __grid_constant__ RouteFwd a) {
     float v[N];
     #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-      Chunk u;
-      widen(u, now.u[c]);
+      float u[8];
+      widen8(u, now.u[c]);
       #pragma unroll
-      for (int j = 0; j < 8; ++j) v[c * 8 + j] = elem(u, j);
+      for (int j = 0; j < 8; ++j) v[c * 8 + j] = u[j];
     }
     first = choice.key(first);
     const bool routed = now.live && first > kKeyNegInf;
@@ -557,11 +583,11 @@ route_bwd_kernel(const __grid_constant__ RouteBwd a) {
     float best = -INFINITY;
     #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-      Chunk u;
-      widen(u, now.u[c]);
+      float u[8];
+      widen8(u, now.u[c]);
       #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v[c * 8 + j] = elem(u, j);
+        v[c * 8 + j] = u[j];
         best = max_nan(best, v[c * 8 + j]);
       }
     }
@@ -631,10 +657,15 @@ route_bwd_kernel(const __grid_constant__ RouteBwd a) {
         const int e0 = (c * G + gl) * 8;
         T* out = static_cast<T*>(a.dlogits) + t * a.experts + e0;
         if (a.vec) {
-          Chunk o;
+          float o[8];
+          uint4 u[kPieces<T>];
           #pragma unroll
-          for (int j = 0; j < 8; ++j) elem(o, j) = v[c * 8 + j];
-          if (e0 < a.experts) store8(out, o);
+          for (int j = 0; j < 8; ++j) o[j] = v[c * 8 + j];
+          narrow8(u, o);
+          if (e0 < a.experts) {
+            #pragma unroll
+            for (int q = 0; q < kPieces<T>; ++q) reinterpret_cast<uint4*>(out)[q] = u[q];
+          }
         } else {
           #pragma unroll
           for (int j = 0; j < 8; ++j)
