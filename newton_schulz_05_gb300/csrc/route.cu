@@ -38,6 +38,7 @@ struct RouteFwd {
   int64_t tokens, ld;
   int experts, k, normalize;
   int vec;              // rows of whole, aligned chunks
+  int wide;             // weights and index are 16-byte aligned
   const void* logits;
   const uint8_t* mask;
   float* weights;
@@ -135,6 +136,74 @@ template <int G> __device__ __forceinline__ uint32_t group_max(uint32_t v) {
   return v;
 }
 
+__device__ __forceinline__ float2 exp_below2(float2 v, float top) {
+  const float2 x = mul2(add2(v, both(-top)), both(1.4426950408889634f));
+  float2 y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(x.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(x.y));
+  return y;
+}
+
+// Words that order logits and carry the expert, larger for the larger logit and
+// for the lower index: key and complement of the index, sixteen bits each for
+// bf16, 32 for fp32.
+template <typename T> struct WordOf;
+template <> struct WordOf<__nv_bfloat16> { using type = uint32_t; };
+template <> struct WordOf<float> { using type = unsigned long long; };
+template <typename T> using Word = typename WordOf<T>::type;
+
+// of the chunk that begins at expert e0, as loaded: two bf16 at a time
+__device__ __forceinline__ void keys8(uint32_t (&k)[8], const uint4 (&u)[1], int e0) {
+  const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+  #pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    // adding 0 turns -0 into +0 and a NaN into the canonical positive one
+    uint32_t x;
+    asm("{.reg .b32 z;\n mov.b32 z, 0;\n add.rn.bf16x2 %0, %1, z;}" : "=r"(x) : "r"(w[j]));
+    // a set sign flips all sixteen bits, a clear one the sign alone
+    x ^= ((x >> 15) & 0x00010001u) * 0x7fffu | 0x80008000u;
+    k[2 * j] = x * 65536u + (uint32_t)(0xffff - (e0 + 2 * j));
+    k[2 * j + 1] = (x & 0xffff0000u) | (uint32_t)(0xffff - (e0 + 2 * j + 1));
+  }
+}
+__device__ __forceinline__ void keys8(unsigned long long (&k)[8], const uint4 (&u)[2], int e0) {
+  const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+  #pragma unroll
+  for (int j = 0; j < 8; ++j)
+    k[j] = (unsigned long long)order_key(__uint_as_float(w[j])) << 32 | (uint32_t)~(e0 + j);
+}
+// the logit's own key (a bf16 value's low sixteen bits are zeros, in the key's
+// own sense) and the expert
+__device__ __forceinline__ uint32_t key_of(uint32_t w) {
+  return w & 0x80000000u ? w & 0xffff0000u : w | 0xffffu;
+}
+__device__ __forceinline__ uint32_t key_of(unsigned long long w) { return (uint32_t)(w >> 32); }
+__device__ __forceinline__ int expert_of(uint32_t w) { return 0xffff - (int)(w & 0xffffu); }
+__device__ __forceinline__ int expert_of(unsigned long long w) { return (int)~(uint32_t)w; }
+
+// a, b = the larger, the smaller
+__device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b) {
+  const uint32_t hi = max(a, b);
+  b = min(a, b);
+  a = hi;
+}
+__device__ __forceinline__ void exchange(unsigned long long& a, unsigned long long& b) {
+  const bool s = b > a;
+  const unsigned long long hi = s ? b : a;
+  b = s ? a : b;
+  a = hi;
+}
+// descending order in nineteen exchanges (two sorted fours and Batcher's
+// odd-even merge)
+template <typename W> __device__ __forceinline__ void sort8(W (&k)[8]) {
+  exchange(k[0], k[1]); exchange(k[2], k[3]); exchange(k[4], k[5]); exchange(k[6], k[7]);
+  exchange(k[0], k[2]); exchange(k[1], k[3]); exchange(k[4], k[6]); exchange(k[5], k[7]);
+  exchange(k[1], k[2]); exchange(k[5], k[6]);
+  exchange(k[0], k[4]); exchange(k[1], k[5]); exchange(k[2], k[6]); exchange(k[3], k[7]);
+  exchange(k[2], k[4]); exchange(k[3], k[5]);
+  exchange(k[1], k[2]); exchange(k[3], k[4]); exchange(k[5], k[6]);
+}
+
 // The candidates of one lane: next() gives the largest over the group that has
 // not been given yet, as a word that value() and expert() read (for fp32 the
 // expert comes beside it).
@@ -143,35 +212,15 @@ template <typename T, int G, int N> struct Choice;
 // bf16: key and index in one word.  N == 8: a sorted list.
 template <int G, int N> struct Choice<__nv_bfloat16, G, N> {
   uint32_t k[N];
-  // chunk c, which begins at expert e0, as loaded: keys of two at once
+  // chunk c, which begins at expert e0, as loaded
   __device__ __forceinline__ void set(int c, const uint4 (&u)[1], int e0) {
-    const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+    uint32_t w[8];
+    keys8(w, u, e0);
     #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      // adding 0 turns -0 into +0 and a NaN into the canonical positive one
-      uint32_t x;
-      asm("{.reg .b32 z;\n mov.b32 z, 0;\n add.rn.bf16x2 %0, %1, z;}" : "=r"(x) : "r"(w[j]));
-      // a set sign flips all sixteen bits, a clear one the sign alone
-      x ^= ((x >> 15) & 0x00010001u) * 0x7fffu | 0x80008000u;
-      k[c * 8 + 2 * j] = x * 65536u + (uint32_t)(0xffff - (e0 + 2 * j));
-      k[c * 8 + 2 * j + 1] = (x & 0xffff0000u) | (uint32_t)(0xffff - (e0 + 2 * j + 1));
-    }
+    for (int j = 0; j < 8; ++j) k[c * 8 + j] = w[j];
   }
   __device__ __forceinline__ void order() {
-    if constexpr (N == 8) {
-      auto ce = [&](int a, int b) {
-        const uint32_t hi = max(k[a], k[b]);
-        k[b] = min(k[a], k[b]);
-        k[a] = hi;
-      };
-      // nineteen exchanges (Batcher's odd-even merge of two sorted fours)
-      ce(0, 1); ce(2, 3); ce(4, 5); ce(6, 7);
-      ce(0, 2); ce(1, 3); ce(4, 6); ce(5, 7);
-      ce(1, 2); ce(5, 6);
-      ce(0, 4); ce(1, 5); ce(2, 6); ce(3, 7);
-      ce(2, 4); ce(3, 5);
-      ce(1, 2); ce(3, 4); ce(5, 6);
-    }
+    if constexpr (N == 8) sort8(k);
   }
   // `left` (known at compile time): picks that may still follow
   __device__ __forceinline__ uint32_t next(int, int&, int left) {
@@ -194,13 +243,8 @@ template <int G, int N> struct Choice<__nv_bfloat16, G, N> {
     }
     return win;
   }
-  // the value's low sixteen bits are zeros, in the key's own sense
-  static __device__ __forceinline__ uint32_t key(uint32_t win) {
-    return win & 0x80000000u ? win & 0xffff0000u : win | 0xffffu;
-  }
-  static __device__ __forceinline__ int expert(uint32_t win, int) {
-    return 0xffff - (int)(win & 0xffffu);
-  }
+  static __device__ __forceinline__ uint32_t key(uint32_t win) { return key_of(win); }
+  static __device__ __forceinline__ int expert(uint32_t win, int) { return expert_of(win); }
 };
 
 // fp32: key and index side by side
@@ -306,6 +350,39 @@ template <typename T, int G, int NCH> struct Logits {
   }
 };
 
+// The end of a forward block: its probabilities (`sums` rows of `stride` floats
+// to add up in order), counts sc and n routed tokens become its partial sums, or
+// the results where it is the only block.  The whole block calls it, after a
+// barrier.
+__device__ __forceinline__ void finish(const RouteFwd& a, const float* sums, int rows, int stride,
+                                       const int* sc, int n) {
+  __shared__ float red[kRouteWarps];
+  const float fn = (float)(n > 0 ? n : 1);
+  float l = 0.f;
+  for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
+    float p = 0.f;
+    for (int i = 0; i < rows; ++i) p += sums[i * stride + e];
+    if (gridDim.x > 1) {
+      a.part_p[(int64_t)blockIdx.x * a.experts + e] = p;
+      a.part_c[(int64_t)blockIdx.x * (a.experts + 1) + e] = sc[e];
+    } else {
+      p /= fn;
+      a.counts[e] = sc[e];
+      a.mean_prob[e] = p;
+      l = fmaf((float)sc[e] / ((float)a.k * fn), p, l);
+    }
+  }
+  if (gridDim.x > 1) {
+    if (threadIdx.x == 0) a.part_c[(int64_t)blockIdx.x * (a.experts + 1) + a.experts] = n;
+    return;
+  }
+  l = block_sum<kRouteThreads>(l, red);
+  if (threadIdx.x == 0) {
+    a.counts[a.experts] = n;
+    *a.loss = (float)a.experts * l;
+  }
+}
+
 // Lane l of a token's G lanes has experts (c G + l) 8 .. + 7 for c = 0 .. NCH - 1.
 template <typename T, int G, int NCH>
 __global__ void __launch_bounds__(kRouteThreads, NCH == 1 ? 2 : 1)
@@ -372,13 +449,15 @@ route_kernel(const __grid_constant__ RouteFwd a) {
     first = choice.key(first);
     const bool routed = now.live && first > kKeyNegInf;
     const float top = key_value(first);
-    float s = 0.f;
+    float2 s2 = both(0.f);
     #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      v[j] = exp_below(v[j], top);
-      s += v[j];
+    for (int j = 0; j < N; j += 2) {
+      const float2 e = exp_below2(make_float2(v[j], v[j + 1]), top);
+      v[j] = e.x;
+      v[j + 1] = e.y;
+      s2 = add2(s2, e);
     }
-    const float total = group_sum<G>(s);
+    const float total = group_sum<G>(s2.x + s2.y);
     if (routed) {
       const float inv = __frcp_rn(total);
       #pragma unroll
@@ -425,37 +504,216 @@ route_kernel(const __grid_constant__ RouteFwd a) {
     }
     __syncthreads();
   }
-  if (gridDim.x > 1) {
-    for (int e = threadIdx.x; e <= a.experts; e += kRouteThreads) {
-      if (e < a.experts) {
-        float p = 0.f;
-        #pragma unroll
-        for (int i = 0; i < kRows; ++i) p += sp[i][e];
-        a.part_p[(int64_t)blockIdx.x * a.experts + e] = p;
-      }
-      a.part_c[(int64_t)blockIdx.x * (a.experts + 1) + e] = sc[e < a.experts ? e : E];
-    }
-    return;
-  }
-  // one block: the results themselves
-  const int n = sc[E];
-  const float fn = (float)(n > 0 ? n : 1);
-  float l = 0.f;
-  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) {
-    float p = 0.f;
+  finish(a, &sp[0][0], kRows, E, sc, sc[E]);
+}
+
+// Many tokens: a lane a token.  A warp copies 32 rows, 128 bytes of each at a
+// time, into shared memory (rows 144 bytes apart, which spreads a column over
+// the banks); each lane reads its own row in eights, sorts each eight, merges it
+// into its K largest so far, and keeps a running maximum and sum of
+// exponentials.  No lane waits for another, so a token costs a third of the
+// instructions of the lanes-a-token form.  Then the lanes take columns and add up
+// the 32 tokens' probabilities; rows longer than a slice are read again for
+// that, from L2.
+constexpr int kSlice = 128, kSliceRow = kSlice + 16, kSliceBytes = 32 * kSliceRow;
+
+// shared memory of a warp: slices, column sums, each token's maximum and
+// reciprocal sum
+__host__ __device__ constexpr int rows_warp_bytes(int slices, int experts_padded) {
+  return (slices > 1 ? 2 : 1) * kSliceBytes + experts_padded * 4 + 32 * 8;
+}
+
+template <typename W, int K> struct Best {
+  W k[K];      // descending
+  __device__ __forceinline__ void clear() {
     #pragma unroll
-    for (int i = 0; i < kRows; ++i) p += sp[i][e];
-    p /= fn;
-    a.counts[e] = sc[e];
-    a.mean_prob[e] = p;
-    l = fmaf((float)sc[e] / ((float)a.k * fn), p, l);
+    for (int j = 0; j < K; ++j) k[j] = 0;
   }
-  __shared__ float red[kRouteWarps];
-  l = block_sum<kRouteThreads>(l, red);
-  if (threadIdx.x == 0) {
-    a.counts[a.experts] = n;
-    *a.loss = (float)a.experts * l;
+  // merge eight sorted words: the larger of each opposite pair are the K
+  // largest of both, in bitonic order
+  __device__ __forceinline__ void merge(const W (&c)[8]) {
+    #pragma unroll
+    for (int j = 0; j < K; ++j) k[j] = k[j] > c[K - 1 - j] ? k[j] : c[K - 1 - j];
+    #pragma unroll
+    for (int o = K / 2; o > 0; o >>= 1)
+      #pragma unroll
+      for (int j = 0; j < K; ++j)
+        if (!(j & o)) exchange(k[j], k[j + o]);
   }
+};
+
+template <typename T, int K>
+__global__ void __launch_bounds__(kRouteThreads, sizeof(T) == 2 ? 2 : 1)
+route_rows_kernel(const __grid_constant__ RouteFwd a) {
+  constexpr int P = kPieces<T>, SE = kSlice / (int)sizeof(T);    // experts of a slice
+  extern __shared__ __align__(16) char smem[];
+  __shared__ int sc[kRouteMaxExperts + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int slices = (a.experts + SE - 1) / SE, padded = slices * SE;
+  char* const mine = smem + warp * rows_warp_bytes(slices, padded);
+  const int buffers = slices > 1 ? 2 : 1;
+  float* const col = reinterpret_cast<float*>(mine + buffers * kSliceBytes);
+  float2* const stat = reinterpret_cast<float2*>(col + padded);
+  for (int e = threadIdx.x; e <= a.experts; e += blockDim.x) sc[e] = 0;
+  for (int e = lane; e < padded; e += 32) col[e] = 0.f;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+  __syncthreads();
+  const T* logits = static_cast<const T*>(a.logits);
+  const int64_t tiles = (a.tokens + 31) / 32, stride = (int64_t)gridDim.x * warps;
+  const int passes = slices > 1 ? 2 : 1;        // times a tile is read
+  // the slice to copy next: tile, pass and slice
+  int64_t ft = (int64_t)blockIdx.x * warps + warp;
+  int fp = 0, fs = 0, fb = 0;
+  auto start = [&] {
+    if (ft < tiles) {
+      char* to = mine + fb * kSliceBytes + (lane >> 3) * kSliceRow + (lane & 7) * 16;
+      const int e0 = fs * SE + (lane & 7) * kEl<T>;
+      const int64_t row = ft * 32 + (lane >> 3);
+      const T* from = logits + row * a.ld + e0;
+      #pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint4* slot = reinterpret_cast<uint4*>(to + i * 4 * kSliceRow);
+        if (e0 >= a.experts) {
+          const uint32_t w = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;    // -inf
+          *slot = make_uint4(w, w, w, w);
+        } else if (row + 4 * i < a.tokens) {
+          const uint32_t s = (uint32_t)__cvta_generic_to_shared(slot);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(s), "l"(from + 4 * i * a.ld)
+                       : "memory");
+        }
+      }
+      if (++fs == slices) {
+        fs = 0;
+        if (++fp == passes) { fp = 0; ft += stride; }
+      }
+      if (++fb == buffers) fb = 0;
+    }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+  };
+  int buffer = 0;
+  if (buffers == 2) start();
+  // the next slice in sequence, its successor under way
+  auto arrive = [&]() -> const char* {
+    __syncwarp();            // the buffer filled next has been read by all lanes
+    start();
+    if (buffers == 2) asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+    __syncwarp();
+    const char* b = mine + buffer * kSliceBytes;
+    if (++buffer == buffers) buffer = 0;
+    return b;
+  };
+  int routed_count = 0;
+  for (int64_t tile = (int64_t)blockIdx.x * warps + warp; tile < tiles; tile += stride) {
+    const int64_t t = tile * 32 + lane;
+    const bool live = t < a.tokens && !(a.mask && !a.mask[t]);
+    Best<Word<T>, K> best;
+    best.clear();
+    float top = -INFINITY, total = 0.f;
+    const char* slice = nullptr;
+    for (int s = 0; s < slices; ++s) {
+      slice = arrive();
+      const uint4* row = reinterpret_cast<const uint4*>(slice + lane * kSliceRow);
+      #pragma unroll 2
+      for (int c = 0; c < SE / 8; ++c) {
+        uint4 u[P];
+        #pragma unroll
+        for (int q = 0; q < P; ++q) u[q] = row[c * P + q];
+        Word<T> w[8];
+        keys8(w, u, s * SE + c * 8);
+        sort8(w);
+        best.merge(w);
+        const float higher = max_nan(top, key_value(key_of(w[0])));
+        const float at = higher == -INFINITY ? 0.f : higher;
+        float v[8];
+        widen8(v, u);
+        float2 e = make_float2(total * exp_below(top, at), 0.f);
+        #pragma unroll
+        for (int j = 0; j < 8; j += 2) e = add2(e, exp_below2(make_float2(v[j], v[j + 1]), at));
+        total = e.x + e.y;
+        top = higher;
+      }
+    }
+    const bool routed = live && top != -INFINITY;
+    const float inv = __frcp_rn(total);
+    // the picks
+    float y[K];
+    int x[K];
+    float picked = 0.f;
+    #pragma unroll
+    for (int p = 0; p < K; ++p) {
+      const uint32_t key = key_of(best.k[p]);
+      const bool ok = routed && p < a.k && key > kKeyNegInf;
+      x[p] = ok ? expert_of(best.k[p]) : -1;
+      y[p] = ok ? exp_below(key_value(key), top) : 0.f;
+      picked += y[p];
+      if (ok) atomicAdd(&sc[x[p]], 1);
+    }
+    const float z = a.normalize ? __frcp_rn(picked) : inv;
+    if (t < a.tokens) {
+      float* w = a.weights + t * a.k;
+      int32_t* ix = a.index + t * a.k;
+      #pragma unroll
+      for (int p = 0; p < K; ++p) y[p] = x[p] >= 0 ? y[p] * z : 0.f;
+      if (K >= 4 && a.k % 4 == 0 && a.wide) {
+        #pragma unroll
+        for (int p = 0; p + 3 < K; p += 4)
+          if (p < a.k) {
+            *reinterpret_cast<float4*>(w + p) = make_float4(y[p], y[p + 1], y[p + 2], y[p + 3]);
+            *reinterpret_cast<int4*>(ix + p) = make_int4(x[p], x[p + 1], x[p + 2], x[p + 3]);
+          }
+      } else if (a.k % 2 == 0 && a.wide) {
+        #pragma unroll
+        for (int p = 0; p + 1 < K; p += 2)
+          if (p < a.k) {
+            *reinterpret_cast<float2*>(w + p) = make_float2(y[p], y[p + 1]);
+            *reinterpret_cast<int2*>(ix + p) = make_int2(x[p], x[p + 1]);
+          }
+      } else {
+        #pragma unroll
+        for (int p = 0; p < K; ++p)
+          if (p < a.k) { w[p] = y[p]; ix[p] = x[p]; }
+      }
+    }
+    // column sums of the tile's probabilities
+    const uint32_t which = __ballot_sync(kAll, routed);
+    routed_count += __popc(which);
+    stat[lane] = make_float2(top, inv);
+    __syncwarp();
+    for (int s = 0; s < slices; ++s) {
+      if (slices > 1) slice = arrive();
+      float sum[4 / sizeof(T)] = {};
+      auto add = [&](int i) {
+        const float2 st = stat[i];
+        const uint32_t u = *reinterpret_cast<const uint32_t*>(slice + i * kSliceRow + lane * 4);
+        if constexpr (sizeof(T) == 2) {
+          const float2 e = exp_below2(
+              make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)), st.x);
+          sum[0] = fmaf(e.x, st.y, sum[0]);
+          sum[1] = fmaf(e.y, st.y, sum[1]);
+        } else {
+          sum[0] = fmaf(exp_below(__uint_as_float(u), st.x), st.y, sum[0]);
+        }
+      };
+      if (which == kAll) {
+        #pragma unroll 8
+        for (int i = 0; i < 32; ++i) add(i);
+      } else {
+        for (uint32_t m = which; m; m &= m - 1) add(__ffs(m) - 1);
+      }
+      #pragma unroll
+      for (int j = 0; j < 4 / (int)sizeof(T); ++j) col[s * SE + lane * (4 / (int)sizeof(T)) + j] += sum[j];
+    }
+    __syncwarp();
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ int routed_tokens;
+  if (threadIdx.x == 0) routed_tokens = 0;
+  __syncthreads();
+  if (lane == 0) atomicAdd(&routed_tokens, routed_count);
+  __syncthreads();
+  finish(a, reinterpret_cast<const float*>(smem + buffers * kSliceBytes), warps,
+         rows_warp_bytes(slices, padded) / 4, sc, routed_tokens);
 }
 
 // Counts, mean probabilities and the loss from the blocks' partial sums: eight
@@ -530,154 +788,194 @@ __global__ void __launch_bounds__(256) route_join_kernel(const __grid_constant__
 // over experts of p times the rest.  Unnormalised weights are probabilities, so
 // x = dw and dot counts it.  Normalised ones are w = p / sum of the picks' p, so
 // x = (dw - sum of w dw) / (sum of the picks' p), whose mean under p is zero.
-template <typename T, int G, int NCH>
-__global__ void __launch_bounds__(kRouteThreads, NCH == 1 ? 2 : 1)
+//
+// A token takes G lanes, piece k of lane l its experts (k G + l) E .. + E - 1
+// (E = 8 bf16, 4 fp32: a 16-byte piece), NP pieces a lane.  The next token's
+// logits and picks are in flight while this one is worked on.
+constexpr int kBwdThreads = 256, kBwdWarps = kBwdThreads / 32;
+// blocks an SM, by the logits a lane holds: 64, 85 or 128 registers
+__host__ __device__ constexpr int bwd_blocks(int n) { return n <= 8 ? 4 : n <= 16 ? 3 : 2; }
+
+template <typename T, int G, int NP>
+__global__ void __launch_bounds__(kBwdThreads, bwd_blocks(NP * kEl<T>))
 route_bwd_kernel(const __grid_constant__ RouteBwd a) {
-  constexpr int TPW = 32 / G, N = NCH * 8, E = G * N;
-  constexpr int KS = ((E < kRouteMaxK ? E : kRouteMaxK) + G - 1) / G;   // picks a lane
-  extern __shared__ float smem[];
+  constexpr int E = kEl<T>, TPW = 32 / G, N = NP * E, KS = 2;
+  extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gl = lane % G, grp = lane / G;
-  float* const px = smem + (warp * TPW + grp) * (2 * E);   // exponentials of the token's row
-  float* const xx = px + E;                                // x by expert, zeros between tokens
-  for (int i = gl; i < E; i += G) xx[i] = 0.f;
+  // x by expert, zeros between tokens
+  float* const xx = reinterpret_cast<float*>(smem) + (warp * TPW + grp) * (G * N);
+  for (int i = gl; i < G * N; i += G) xx[i] = 0.f;
   __syncwarp();
+  const T* logits = static_cast<const T*>(a.logits);
   const int routed_tokens = a.counts[a.experts];
   const float n = (float)(routed_tokens > 0 ? routed_tokens : 1);
   const float f = a.dloss ? *a.dloss * (float)a.experts / ((float)a.k * n) / n : 0.f;
-  float b[N];
+  float2 b[N / 2];
   #pragma unroll
   for (int j = 0; j < N; ++j) {
-    const int e = ((j / 8) * G + gl) * 8 + j % 8;
-    b[j] = e < a.experts ? f * (float)a.counts[e] : 0.f;
+    const int e = ((j / E) * G + gl) * E + j % E;
+    const float v = e < a.experts ? f * (float)a.counts[e] : 0.f;
+    if (j & 1) b[j / 2].y = v;
+    else b[j / 2].x = v;
   }
-  const int64_t stride = (int64_t)gridDim.x * kRouteWarps * TPW;
-  const int64_t begin = ((int64_t)blockIdx.x * kRouteWarps + warp) * TPW;
-  Logits<T, G, NCH> now, next;
-  int e_now[KS], e_next[KS];
-  float d_now[KS], d_next[KS];
-  auto load_picks = [&](int64_t t) {
+  const int64_t stride = (int64_t)gridDim.x * kBwdWarps * TPW;
+  const int64_t begin = ((int64_t)blockIdx.x * kBwdWarps + warp) * TPW;
+  const uint32_t minus = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;    // -inf
+  uint4 next[NP];
+  bool live_next;
+  int e_next[KS];
+  float d_next[KS];
+  #pragma unroll
+  for (int k = 0; k < NP; ++k) next[k] = make_uint4(minus, minus, minus, minus);
+  auto load = [&](int64_t t) {
+    const bool in = t < a.tokens;
+    live_next = in && !(a.mask && !a.mask[t]);
+    const T* row = logits + t * a.ld + gl * E;
+    #pragma unroll
+    for (int k = 0; k < NP; ++k)
+      if (a.vec && in && (k * G + gl) * E < a.experts)
+        next[k] = __ldg(reinterpret_cast<const uint4*>(row + k * G * E));
     #pragma unroll
     for (int s = 0; s < KS; ++s) {
       const int p = gl + s * G;
       e_next[s] = -1;
       d_next[s] = 0.f;
-      if (a.dweights && p < a.k && t < a.tokens) {
+      if (a.dweights && p < a.k && in) {
         e_next[s] = a.index[t * a.k + p];
         d_next[s] = a.dweights[t * a.k + p];
       }
     }
   };
-  next.clear();
-  next.load(a, begin + grp, gl);
-  load_picks(begin + grp);
+  load(begin + grp);
   for (int64_t t0 = begin; t0 < a.tokens; t0 += stride) {
     const int64_t t = t0 + grp;
-    now = next;
+    const T* row = logits + t * a.ld;
+    const bool live = live_next;
+    uint4 u[NP];
+    int e[KS];
+    float d[KS], l[KS];
     #pragma unroll
-    for (int s = 0; s < KS; ++s) { e_now[s] = e_next[s]; d_now[s] = d_next[s]; }
-    now.arrive(a, t, gl);
-    next.load(a, t + stride, gl);
-    load_picks(t + stride);
-    float v[N];
+    for (int s = 0; s < KS; ++s) {
+      e[s] = e_next[s];
+      d[s] = d_next[s];
+      if (!live || e[s] < 0 || e[s] >= a.experts) {
+        e[s] = -1;
+        d[s] = 0.f;              // whatever a missing pick's gradient holds
+      }
+      l[s] = e[s] >= 0 ? to_f(row[e[s]]) : -INFINITY;
+    }
+    #pragma unroll
+    for (int k = 0; k < NP; ++k) u[k] = next[k];
+    if (!a.vec && t < a.tokens) {
+      #pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const int e0 = (k * G + gl) * E;
+        Piece<E> w;
+        #pragma unroll
+        for (int j = 0; j < E; ++j) elem(w, j) = e0 + j < a.experts ? to_f(row[e0 + j]) : -INFINITY;
+        u[k] = narrow(w);
+      }
+    }
+    load(t + stride);
+    float2 v[N / 2];
     float best = -INFINITY;
     #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      float u[8];
-      widen8(u, now.u[c]);
+    for (int k = 0; k < NP; ++k) {
+      Piece<E> w;
+      widen(w, u[k]);
       #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[c * 8 + j] = u[j];
-        best = max_nan(best, v[c * 8 + j]);
+      for (int j = 0; j < E / 2; ++j) {
+        v[k * (E / 2) + j] = w.v[j];
+        best = max_nan(best, max_nan(w.v[j].x, w.v[j].y));
       }
     }
     const float top = key_value(group_max<G>(order_key(best)));
-    const bool routed = now.live && top != -INFINITY;
-    float s = 0.f;
+    const bool routed = live && top != -INFINITY;
+    float2 s2 = both(0.f);
     #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      #pragma unroll
-      for (int j = c * 8; j < c * 8 + 8; ++j) {
-        v[j] = exp_below(v[j], top);
-        s += v[j];
-      }
-      float4* q = reinterpret_cast<float4*>(px + (c * G + gl) * 8);
-      q[0] = make_float4(v[c * 8], v[c * 8 + 1], v[c * 8 + 2], v[c * 8 + 3]);
-      q[1] = make_float4(v[c * 8 + 4], v[c * 8 + 5], v[c * 8 + 6], v[c * 8 + 7]);
+    for (int j = 0; j < N / 2; ++j) {
+      v[j] = exp_below2(v[j], top);
+      s2 = add2(s2, v[j]);
     }
-    const float total = group_sum<G>(s);
-    __syncwarp();
+    const float total = group_sum<G>(s2.x + s2.y);
     if (a.dweights) {
-      float z = 0.f, wd = 0.f;
-      #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        if (!routed || e_now[s] < 0 || e_now[s] >= a.experts) {
-          e_now[s] = -1;
-          d_now[s] = 0.f;      // whatever a missing pick's gradient holds
-        }
-        const float y = e_now[s] >= 0 ? px[e_now[s]] : 0.f;
-        z += y;
-        wd = fmaf(y, d_now[s], wd);
-      }
       if (a.normalize) {
+        float z = 0.f, wd = 0.f;
+        #pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const float y = exp_below(l[s], top);
+          z += e[s] >= 0 ? y : 0.f;
+          wd += e[s] >= 0 ? y * d[s] : 0.f;
+        }
         z = __frcp_rn(group_sum<G>(z));
         wd = group_sum<G>(wd) * z;
         z *= total;
         #pragma unroll
-        for (int s = 0; s < KS; ++s) d_now[s] = (d_now[s] - wd) * z;
+        for (int s = 0; s < KS; ++s) d[s] = (d[s] - wd) * z;
       }
       #pragma unroll
       for (int s = 0; s < KS; ++s)
-        if (e_now[s] >= 0) xx[e_now[s]] = d_now[s];
+        if (e[s] >= 0) xx[e[s]] = d[s];
       __syncwarp();
     }
-    const float inv = __frcp_rn(total);
-    float x[N];
-    float dot = 0.f;
-    #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const float4* q = reinterpret_cast<const float4*>(xx + (c * G + gl) * 8);
-      const float4 q0 = q[0], q1 = q[1];
-      x[c * 8 + 0] = q0.x; x[c * 8 + 1] = q0.y; x[c * 8 + 2] = q0.z; x[c * 8 + 3] = q0.w;
-      x[c * 8 + 4] = q1.x; x[c * 8 + 5] = q1.y; x[c * 8 + 6] = q1.z; x[c * 8 + 7] = q1.w;
-    }
-    #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      v[j] *= inv;
-      const float bx = b[j] + x[j];
-      dot = fmaf(v[j], a.normalize ? b[j] : bx, dot);
-      x[j] = bx;
-    }
-    dot = group_sum<G>(dot);
-    #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = routed ? v[j] * (x[j] - dot) : 0.f;
-    if (t < a.tokens) {
+    const float2 inv = both(__frcp_rn(total));
+    // x of piece k
+    auto added = [&](int k, float2 (&x)[E / 2]) {
       #pragma unroll
-      for (int c = 0; c < NCH; ++c) {
-        const int e0 = (c * G + gl) * 8;
-        T* out = static_cast<T*>(a.dlogits) + t * a.experts + e0;
+      for (int q = 0; q < E / 4; ++q) {
+        const float4 w = *reinterpret_cast<const float4*>(xx + (k * G + gl) * E + q * 4);
+        x[2 * q] = make_float2(w.x, w.y);
+        x[2 * q + 1] = make_float2(w.z, w.w);
+      }
+    };
+    float2 dot2 = both(0.f);
+    #pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      float2 x[E / 2];
+      if (!a.normalize) added(k, x);
+      #pragma unroll
+      for (int j = 0; j < E / 2; ++j) {
+        float2& p = v[k * (E / 2) + j];
+        const float2 bj = b[k * (E / 2) + j];
+        p = mul2(p, inv);
+        dot2 = fma2(p, a.normalize ? bj : add2(x[j], bj), dot2);
+      }
+    }
+    const float2 minus_dot = both(-group_sum<G>(dot2.x + dot2.y));
+    #pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      float2 x[E / 2];
+      added(k, x);
+      #pragma unroll
+      for (int j = 0; j < E / 2; ++j) {
+        float2& p = v[k * (E / 2) + j];
+        p = mul2(p, add2(add2(x[j], b[k * (E / 2) + j]), minus_dot));
+      }
+    }
+    if (t < a.tokens) {
+      T* out = static_cast<T*>(a.dlogits) + t * a.experts;
+      #pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const int e0 = (k * G + gl) * E;
+        Piece<E> w;
+        #pragma unroll
+        for (int j = 0; j < E / 2; ++j) w.v[j] = v[k * (E / 2) + j];
+        if (!routed) clear(w);
         if (a.vec) {
-          float o[8];
-          uint4 u[kPieces<T>];
-          #pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = v[c * 8 + j];
-          narrow8(u, o);
-          if (e0 < a.experts) {
-            #pragma unroll
-            for (int q = 0; q < kPieces<T>; ++q) reinterpret_cast<uint4*>(out)[q] = u[q];
-          }
+          if (e0 < a.experts) *reinterpret_cast<uint4*>(out + e0) = narrow(w);
         } else {
           #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (e0 + j < a.experts) out[j] = from_f<T>(v[c * 8 + j]);
+          for (int j = 0; j < E; ++j)
+            if (e0 + j < a.experts) out[e0 + j] = from_f<T>(elem(w, j));
         }
       }
     }
-    __syncwarp();
     if (a.dweights) {
+      __syncwarp();
       #pragma unroll
       for (int s = 0; s < KS; ++s)
-        if (e_now[s] >= 0) xx[e_now[s]] = 0.f;
+        if (e[s] >= 0) xx[e[s]] = 0.f;
       __syncwarp();
     }
   }
@@ -690,7 +988,15 @@ int lanes_of(int experts) {
   return g;
 }
 
-// blocks of a pass: a warp for every token group, up to two blocks an SM
+// Tokens from which the lane-a-token form is taken.  Its 32 tokens are one warp's
+// serial work, so it pays once every SM has many warps: 64 experts, k = 6, bf16
+// took 9.0 against 6.7 us at 4096 tokens, 11.3 against 11.8 at 32768 and 21.9
+// against 25.0 at 131072; 256 experts, k = 8, fp32 28 against 20 at 16384 and 38
+// against 33 at 32768; 160 experts at 65537 42 against 60.
+constexpr int64_t kRowsTokens = 49152;
+
+// blocks of a pass: a warp for every token group, up to two blocks an SM (the
+// lane-a-token form has fewer groups)
 int route_blocks(int64_t tokens, int experts) {
   const int per = kRouteWarps * 32 / lanes_of(experts);
   const int64_t b = (tokens + per - 1) / per;
@@ -718,9 +1024,12 @@ bool whole_rows(const void* p, int64_t tokens, int64_t ld, int experts, size_t e
 
 // workspace: ticket and shares of the loss, counts, probabilities
 constexpr size_t kJoinBytes = 1024;
+int64_t most_blocks(int64_t tokens, int experts) {     // of either form
+  return tokens >= kRowsTokens ? kRouteParts : route_blocks(tokens, experts);
+}
 size_t probs_offset(int64_t tokens, int experts) {
   return kJoinBytes +
-         ((size_t)route_blocks(tokens, experts) * (experts + 1) * sizeof(int32_t) + 255) / 256 * 256;
+         ((size_t)most_blocks(tokens, experts) * (experts + 1) * sizeof(int32_t) + 255) / 256 * 256;
 }
 
 template <typename F>
@@ -749,21 +1058,80 @@ struct LaunchFwd {
   }
 };
 
-struct LaunchBwd {
-  const RouteBwd& a;
-  int blocks;
-  cudaStream_t s;
-  template <typename T, int G, int NCH> cudaError_t operator()() const {
-    const size_t smem = (size_t)kRouteWarps * (32 / G) * 2 * G * NCH * 8 * sizeof(float);
-    if (smem > 48u << 10) {
-      const cudaError_t e = cudaFuncSetAttribute(route_bwd_kernel<T, G, NCH>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (e != cudaSuccess) return e;
-    }
-    route_bwd_kernel<T, G, NCH><<<blocks, kRouteThreads, smem, s>>>(a);
-    return cudaGetLastError();
+template <typename T, int K>
+cudaError_t launch_rows_k(const RouteFwd& a, int blocks, int warps, cudaStream_t s) {
+  constexpr int SE = kSlice / (int)sizeof(T);
+  const int slices = (a.experts + SE - 1) / SE;
+  const size_t smem = (size_t)warps * rows_warp_bytes(slices, slices * SE);
+  const cudaError_t e = cudaFuncSetAttribute(route_rows_kernel<T, K>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  route_rows_kernel<T, K><<<blocks, 32 * warps, smem, s>>>(a);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_rows(const RouteFwd& a, int blocks, int warps, cudaStream_t s) {
+  return a.k <= 2 ? launch_rows_k<T, 2>(a, blocks, warps, s)
+       : a.k <= 4 ? launch_rows_k<T, 4>(a, blocks, warps, s) : launch_rows_k<T, 8>(a, blocks, warps, s);
+}
+
+// Blocks and warps a block of the lane-a-token form: the tiles of 32 tokens are
+// spread evenly, over two blocks an SM where their shared memory allows (a
+// slice a row), else one.
+void rows_grid(int64_t tokens, int experts, size_t es, int* blocks, int* warps) {
+  const int64_t tiles = (tokens + 31) / 32;
+  const int most = (size_t)experts * es <= kSlice ? kRouteParts : kRouteParts / 2;
+  const int64_t w = (tiles + most - 1) / most;
+  *warps = (int)(w < kRouteWarps ? w : kRouteWarps);
+  const int64_t b = (tiles + *warps - 1) / *warps;
+  *blocks = (int)(b < most ? b : most);
+}
+
+// the lane-a-token form: rows of whole, aligned 16-byte pieces, up to eight
+// picks, and column sums that fit beside the slices in shared memory
+bool rows_form(int64_t tokens, int experts, int k, const void* p, int64_t ld, size_t es) {
+  return tokens >= kRowsTokens && k <= 8 && experts <= 512 && experts % (16 / es) == 0 &&
+         reinterpret_cast<uintptr_t>(p) % 16 == 0 && (size_t)ld * es % 16 == 0;
+}
+
+template <typename T, int G, int NP>
+cudaError_t launch_bwd(const RouteBwd& a, cudaStream_t s) {
+  const size_t smem = (size_t)kBwdWarps * 32 * NP * kEl<T> * sizeof(float);
+  if (smem > 48u << 10) {
+    const cudaError_t e = cudaFuncSetAttribute(route_bwd_kernel<T, G, NP>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
   }
-};
+  const int per = kBwdWarps * 32 / G;
+  const int64_t want = (a.tokens + per - 1) / per;
+  const int64_t most = 152 * bwd_blocks(NP * kEl<T>);
+  route_bwd_kernel<T, G, NP><<<(unsigned)(want < most ? want : most), kBwdThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+// Lanes a token: the fewest that leave a lane at most two picks and twenty fp32
+// or 24 bf16 logits (more only where 32 lanes leave more), so that a warp has
+// many tokens and few lanes idle.
+template <typename T, int G> cudaError_t bwd_pieces(const RouteBwd& a, cudaStream_t s) {
+  constexpr int kMost = sizeof(T) == 2 ? 3 : 5;
+  const int pieces = (a.experts + kEl<T> - 1) / kEl<T>, np = (pieces + G - 1) / G;
+  if constexpr (G < 32) {
+    if (np > kMost || 2 * G < a.k) return bwd_pieces<T, 2 * G>(a, s);
+  }
+  switch (np) {
+    case 1: return launch_bwd<T, G, 1>(a, s);
+    case 2: return launch_bwd<T, G, 2>(a, s);
+    case 3: return launch_bwd<T, G, 3>(a, s);
+  }
+  if constexpr (sizeof(T) == 4) {
+    if (np == 4) return launch_bwd<T, G, 4>(a, s);
+    if (np == 5) return launch_bwd<T, G, 5>(a, s);
+    if constexpr (G == 32) return np <= 6 ? launch_bwd<T, G, 6>(a, s) : launch_bwd<T, G, 8>(a, s);
+  } else if constexpr (G == 32) {
+    return launch_bwd<T, G, 4>(a, s);
+  }
+  return cudaErrorInvalidValue;
+}
 
 }  // namespace
 
@@ -775,7 +1143,7 @@ extern "C" muon_status muon_route_workspace_bytes(int64_t tokens, int experts, s
   if (!out || tokens < 0) return MUON_ERR_INVALID_ARG;
   if (experts < 1 || experts > kRouteMaxExperts) return MUON_ERR_UNSUPPORTED_SHAPE;
   *out = probs_offset(tokens, experts) +
-         (size_t)route_blocks(tokens, experts) * experts * sizeof(float);
+         (size_t)most_blocks(tokens, experts) * experts * sizeof(float);
   return MUON_OK;
 }
 
@@ -799,15 +1167,24 @@ extern "C" muon_status muon_route(int64_t tokens, int experts, int k, int dtype,
   if (fault_switch() == kFaultLaunch) return MUON_ERR_CUDA;
   NvtxRange range("muon_route");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int blocks = route_blocks(tokens, experts);
+  int blocks = route_blocks(tokens, experts);
   char* ws = static_cast<char*>(workspace);
   const size_t es = dtype == MUON_BF16 ? 2 : 4;
   const RouteFwd a = {tokens, ld, experts, k, normalize,
-                      whole_rows(logits, tokens, ld, experts, es), logits, token_mask, weights,
+                      whole_rows(logits, tokens, ld, experts, es),
+                      !misaligned(weights, 16) && !misaligned(index, 16), logits, token_mask, weights,
                       index, reinterpret_cast<float*>(ws + probs_offset(tokens, experts)),
                       reinterpret_cast<int32_t*>(ws + kJoinBytes), reinterpret_cast<unsigned*>(ws),
                       counts, mean_prob, loss};
-  cudaError_t e = by_experts(dtype, experts, LaunchFwd{a, blocks, s});
+  cudaError_t e;
+  if (rows_form(tokens, experts, k, logits, ld, es)) {
+    int warps;
+    rows_grid(tokens, experts, es, &blocks, &warps);
+    e = dtype == MUON_BF16 ? launch_rows<__nv_bfloat16>(a, blocks, warps, s)
+                           : launch_rows<float>(a, blocks, warps, s);
+  } else {
+    e = by_experts(dtype, experts, LaunchFwd{a, blocks, s});
+  }
   if (e == cudaSuccess && blocks > 1) {
     const RouteJoin j = {experts, k, blocks, a.part_p, a.part_c, counts, mean_prob, loss,
                          reinterpret_cast<float*>(ws) + 1, a.ticket};
@@ -834,10 +1211,10 @@ extern "C" muon_status muon_route_backward(int64_t tokens, int experts, int k, i
   NvtxRange range("muon_route_backward");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const RouteBwd a = {tokens, ld, experts, k, normalize,
-                      whole_rows(logits, tokens, ld, experts, es) &&
-                          reinterpret_cast<uintptr_t>(dlogits) % 16 == 0,
+                      experts % (int)(16 / es) == 0 && !misaligned(logits, 16) &&
+                          !misaligned(dlogits, 16) && (tokens <= 1 || (size_t)ld * es % 16 == 0),
                       logits, token_mask, index, counts, dweights, dloss, dlogits};
   const cudaError_t e =
-      by_experts(dtype, experts, LaunchBwd{a, route_blocks(tokens, experts), s});
+      dtype == MUON_BF16 ? bwd_pieces<__nv_bfloat16, 1>(a, s) : bwd_pieces<float, 1>(a, s);
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
