@@ -135,6 +135,19 @@ template <int G> __device__ __forceinline__ uint32_t group_max(uint32_t v) {
   for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
   return v;
 }
+template <int G> __device__ __forceinline__ unsigned long long group_max(unsigned long long v) {
+  if constexpr (G == 32) {
+    const uint32_t hi = __reduce_max_sync(kAll, (uint32_t)(v >> 32));
+    const uint32_t lo = __reduce_max_sync(kAll, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+    return (unsigned long long)hi << 32 | lo;
+  }
+  #pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) {
+    const unsigned long long x = __shfl_xor_sync(kAll, v, o);
+    v = x > v ? x : v;
+  }
+  return v;
+}
 
 __device__ __forceinline__ float2 exp_below2(float2 v, float top) {
   const float2 x = mul2(add2(v, both(-top)), both(1.4426950408889634f));
@@ -152,8 +165,8 @@ template <> struct WordOf<__nv_bfloat16> { using type = uint32_t; };
 template <> struct WordOf<float> { using type = unsigned long long; };
 template <typename T> using Word = typename WordOf<T>::type;
 
-// of the chunk that begins at expert e0, as loaded: two bf16 at a time
-__device__ __forceinline__ void keys8(uint32_t (&k)[8], const uint4 (&u)[1], int e0) {
+// of eight logits as loaded, experts e0, e0 + step, ...: two bf16 at a time
+__device__ __forceinline__ void keys8(uint32_t (&k)[8], const uint4 (&u)[1], int e0, int step) {
   const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
   #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -162,15 +175,16 @@ __device__ __forceinline__ void keys8(uint32_t (&k)[8], const uint4 (&u)[1], int
     asm("{.reg .b32 z;\n mov.b32 z, 0;\n add.rn.bf16x2 %0, %1, z;}" : "=r"(x) : "r"(w[j]));
     // a set sign flips all sixteen bits, a clear one the sign alone
     x ^= ((x >> 15) & 0x00010001u) * 0x7fffu | 0x80008000u;
-    k[2 * j] = x * 65536u + (uint32_t)(0xffff - (e0 + 2 * j));
-    k[2 * j + 1] = (x & 0xffff0000u) | (uint32_t)(0xffff - (e0 + 2 * j + 1));
+    k[2 * j] = x * 65536u + (uint32_t)(0xffff - (e0 + 2 * j * step));
+    k[2 * j + 1] = (x & 0xffff0000u) | (uint32_t)(0xffff - (e0 + (2 * j + 1) * step));
   }
 }
-__device__ __forceinline__ void keys8(unsigned long long (&k)[8], const uint4 (&u)[2], int e0) {
+__device__ __forceinline__ void keys8(unsigned long long (&k)[8], const uint4 (&u)[2], int e0,
+                                      int step) {
   const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
   #pragma unroll
   for (int j = 0; j < 8; ++j)
-    k[j] = (unsigned long long)order_key(__uint_as_float(w[j])) << 32 | (uint32_t)~(e0 + j);
+    k[j] = (unsigned long long)order_key(__uint_as_float(w[j])) << 32 | (uint32_t)~(e0 + j * step);
 }
 // the logit's own key (a bf16 value's low sixteen bits are zeros, in the key's
 // own sense) and the expert
@@ -204,18 +218,14 @@ template <typename W> __device__ __forceinline__ void sort8(W (&k)[8]) {
   exchange(k[1], k[2]); exchange(k[3], k[4]); exchange(k[5], k[6]);
 }
 
-// The candidates of one lane: next() gives the largest over the group that has
-// not been given yet, as a word that value() and expert() read (for fp32 the
-// expert comes beside it).
-template <typename T, int G, int N> struct Choice;
-
-// bf16: key and index in one word.  N == 8: a sorted list.
-template <int G, int N> struct Choice<__nv_bfloat16, G, N> {
-  uint32_t k[N];
-  // chunk c, which begins at expert e0, as loaded
-  __device__ __forceinline__ void set(int c, const uint4 (&u)[1], int e0) {
-    uint32_t w[8];
-    keys8(w, u, e0);
+// The candidates of one lane, a sorted list where there are eight: next() gives
+// the largest word over the group that has not been given yet.
+template <typename T, int G, int N> struct Choice {
+  Word<T> k[N];
+  // eight logits as loaded, experts e0, e0 + step, ...
+  __device__ __forceinline__ void set(int c, const uint4 (&u)[kPieces<T>], int e0, int step) {
+    Word<T> w[8];
+    keys8(w, u, e0, step);
     #pragma unroll
     for (int j = 0; j < 8; ++j) k[c * 8 + j] = w[j];
   }
@@ -223,13 +233,13 @@ template <int G, int N> struct Choice<__nv_bfloat16, G, N> {
     if constexpr (N == 8) sort8(k);
   }
   // `left` (known at compile time): picks that may still follow
-  __device__ __forceinline__ uint32_t next(int, int&, int left) {
-    uint32_t head = k[0];
+  __device__ __forceinline__ Word<T> next(int left) {
+    Word<T> head = k[0];
     if constexpr (N != 8) {
       #pragma unroll
-      for (int j = 1; j < N; ++j) head = max(head, k[j]);
+      for (int j = 1; j < N; ++j) head = head > k[j] ? head : k[j];
     }
-    const uint32_t win = group_max<G>(head);
+    const Word<T> win = group_max<G>(head);
     if constexpr (N == 8) {
       if (head == win) {
         #pragma unroll
@@ -239,114 +249,76 @@ template <int G, int N> struct Choice<__nv_bfloat16, G, N> {
       }
     } else {
       #pragma unroll
-      for (int j = 0; j < N; ++j) k[j] = k[j] == win ? 0u : k[j];
+      for (int j = 0; j < N; ++j) k[j] = k[j] == win ? 0 : k[j];
     }
     return win;
   }
-  static __device__ __forceinline__ uint32_t key(uint32_t win) { return key_of(win); }
-  static __device__ __forceinline__ int expert(uint32_t win, int) { return expert_of(win); }
 };
 
-// fp32: key and index side by side
-template <int G, int N> struct Choice<float, G, N> {
-  uint32_t k[N];
-  int id[N];
-  __device__ __forceinline__ void set(int c, const uint4 (&u)[2], int e0) {
-    const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
-    #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      k[c * 8 + j] = order_key(__uint_as_float(w[j]));
-      id[c * 8 + j] = e0 + j;
-    }
-  }
-  __device__ __forceinline__ void order() {
-    if constexpr (N == 8) {
-      // odd-even transposition: neighbours are exchanged only when out of
-      // order, so equal keys keep their order
-      #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        #pragma unroll
-        for (int j = r & 1; j + 1 < 8; j += 2) {
-          const bool s = k[j + 1] > k[j];
-          const uint32_t a = s ? k[j + 1] : k[j], b = s ? k[j] : k[j + 1];
-          const int x = s ? id[j + 1] : id[j], y = s ? id[j] : id[j + 1];
-          k[j] = a; k[j + 1] = b;
-          id[j] = x; id[j + 1] = y;
-        }
-    }
-  }
-  __device__ __forceinline__ uint32_t next(int group_lanes, int& e, int left) {
-    uint32_t win;
-    if constexpr (N == 8) {
-      win = group_max<G>(k[0]);
-      const uint32_t who = __ballot_sync(kAll, k[0] == win) & (uint32_t)group_lanes;
-      const int lane = __ffs(who) - 1;
-      e = __shfl_sync(kAll, id[0], lane);
-      if ((int)(threadIdx.x & 31) == lane) {
-        #pragma unroll
-        for (int j = 0; j < 7; ++j)
-          if (j < left) { k[j] = k[j + 1]; id[j] = id[j + 1]; }
-        if (left > 7) k[7] = 0;
-      }
-    } else {      // a lane's experts are not consecutive: the lowest index decides
-      uint32_t head = 0;
-      int first = 0x7fffffff;
-      #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (k[j] > head) { head = k[j]; first = id[j]; }
-      win = group_max<G>(head);
-      e = (int)__reduce_min_sync(kAll, head == win ? (uint32_t)first : 0x7fffffffu);
-      #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (id[j] == e) k[j] = 0;
-    }
-    return win;
-  }
-  static __device__ __forceinline__ uint32_t key(uint32_t win) { return win; }
-  static __device__ __forceinline__ int expert(uint32_t, int e) { return e; }
-};
-
-// One token's logits as a lane holds them: its chunks as loaded, -inf where
-// there is no expert.  Rows of whole, aligned chunks are loaded ahead, so that
-// the next token's are in flight while this one is worked on; others when they
-// are needed.  A token past the end or masked keeps what was there: its results
-// are thrown away.
-template <typename T, int G, int NCH> struct Logits {
-  uint4 u[NCH][kPieces<T>];
+// A lane's logits of one token in flight, so that the next token's load while
+// this one is worked on.  VEC: rows of whole, aligned 16-byte pieces, a lane's
+// chunk of eight being eight consecutive experts; else single logits, the eight
+// G experts apart, so that the lanes of a load are neighbours in memory all the
+// same.  -inf where there is no expert; a token past the end or masked keeps
+// what was there: its results are thrown away.
+template <typename T, int G, int NCH, bool VEC> struct Logits {
+  static constexpr int P = kPieces<T>, STEP = VEC ? 1 : G;
+  uint4 u[VEC ? NCH : 1][P];
+  uint32_t w[VEC ? 1 : NCH * 8];
   bool live;
+  static __device__ __forceinline__ int first(int c, int gl) { return VEC ? (c * G + gl) * 8 : c * 8 * G + gl; }
   __device__ __forceinline__ void clear() {
-    const uint32_t w = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+    const uint32_t m = sizeof(T) == 2 ? (VEC ? 0xff80ff80u : 0xff80u) : 0xff800000u;
+    if constexpr (VEC) {
+      #pragma unroll
+      for (int c = 0; c < NCH; ++c)
+        #pragma unroll
+        for (int q = 0; q < P; ++q) u[c][q] = make_uint4(m, m, m, m);
+    } else {
+      #pragma unroll
+      for (int j = 0; j < NCH * 8; ++j) w[j] = m;
+    }
+  }
+  __device__ __forceinline__ void load(const RouteFwd& a, int64_t t, int gl) {
+    live = t < a.tokens && !(a.mask && !a.mask[t]);
+    if (t >= a.tokens) return;
+    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    #pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const int e0 = first(c, gl);
+      if constexpr (VEC) {
+        if (e0 < a.experts) {
+          #pragma unroll
+          for (int q = 0; q < P; ++q) u[c][q] = __ldg(reinterpret_cast<const uint4*>(row + e0) + q);
+        }
+      } else {
+        #pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (e0 + j * G < a.experts) w[c * 8 + j] = raw(row + e0 + j * G);
+      }
+    }
+  }
+  static __device__ __forceinline__ uint32_t raw(const __nv_bfloat16* p) {
+    return __ldg(reinterpret_cast<const unsigned short*>(p));
+  }
+  static __device__ __forceinline__ uint32_t raw(const float* p) {
+    return __ldg(reinterpret_cast<const unsigned*>(p));
+  }
+  __device__ __forceinline__ void get(uint4 (&to)[NCH][P]) const {
     #pragma unroll
     for (int c = 0; c < NCH; ++c)
       #pragma unroll
-      for (int q = 0; q < kPieces<T>; ++q) u[c][q] = make_uint4(w, w, w, w);
-  }
-  template <typename A>
-  __device__ __forceinline__ void load(const A& a, int64_t t, int gl) {
-    live = t < a.tokens && !(a.mask && !a.mask[t]);
-    if (!a.vec || t >= a.tokens) return;
-    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-    #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const int e0 = (c * G + gl) * 8;
-      if (e0 < a.experts) {
-        #pragma unroll
-        for (int q = 0; q < kPieces<T>; ++q) u[c][q] = __ldg(reinterpret_cast<const uint4*>(row + e0) + q);
+      for (int q = 0; q < P; ++q) {
+        if constexpr (VEC) {
+          to[c][q] = u[c][q];
+        } else if constexpr (sizeof(T) == 2) {
+          const uint32_t* x = w + c * 8;
+          to[c][q] = make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
+        } else {
+          const uint32_t* x = w + c * 8 + q * 4;
+          to[c][q] = make_uint4(x[0], x[1], x[2], x[3]);
+        }
       }
-    }
-  }
-  template <typename A>
-  __device__ __forceinline__ void arrive(const A& a, int64_t t, int gl) {
-    if (a.vec || t >= a.tokens) return;
-    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-    #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const int e0 = (c * G + gl) * 8;
-      float w[8];
-      #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = e0 + j < a.experts ? to_f(row[e0 + j]) : -INFINITY;
-      narrow8(u[c], w);
-    }
   }
 };
 
@@ -383,21 +355,20 @@ __device__ __forceinline__ void finish(const RouteFwd& a, const float* sums, int
   }
 }
 
-// Lane l of a token's G lanes has experts (c G + l) 8 .. + 7 for c = 0 .. NCH - 1.
-template <typename T, int G, int NCH>
+// A token takes G lanes, NCH eights of experts a lane.
+template <typename T, int G, int NCH, bool VEC>
 __global__ void __launch_bounds__(kRouteThreads, NCH == 1 ? 2 : 1)
 route_kernel(const __grid_constant__ RouteFwd a) {
+  using Row = Logits<T, G, NCH, VEC>;
   constexpr int TPW = 32 / G, N = NCH * 8, E = G * N;
   constexpr int kStage = TPW * (E < kRouteMaxK ? E : kRouteMaxK);
   // warps whose sums are added side by side
   constexpr int kRows = E <= 256 ? kRouteWarps : 2;
   __shared__ float sp[kRows][E];
   __shared__ int sc[E + 1];
-  __shared__ uint32_t sw[kRouteWarps][kStage];     // picks: the winning words, then weights
-  __shared__ int se[kRouteWarps][kStage];
+  __shared__ uint2 picks[kRouteWarps][kStage];     // the winning words, then weight and expert
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gl = lane % G, grp = lane / G;
-  const int group_lanes = (int)((G == 32 ? kAll : ((1u << (G & 31)) - 1u) << (grp * G)));
   for (int e = threadIdx.x; e <= E; e += kRouteThreads) sc[e] = 0;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
   __syncthreads();
@@ -407,29 +378,25 @@ route_kernel(const __grid_constant__ RouteFwd a) {
   int routed_count = 0;
   const int64_t stride = (int64_t)gridDim.x * kRouteWarps * TPW;
   const int64_t begin = ((int64_t)blockIdx.x * kRouteWarps + warp) * TPW;
-  Logits<T, G, NCH> now, next;
+  Row next;
   next.clear();
   next.load(a, begin + grp, gl);
-  uint32_t* const w = sw[warp] + grp * a.k;
-  int* const x = se[warp] + grp * a.k;
+  uint2* const mine = picks[warp] + grp * a.k;
   for (int64_t t0 = begin; t0 < a.tokens; t0 += stride) {
     const int64_t t = t0 + grp;
-    now = next;
-    now.arrive(a, t, gl);
+    const bool live = next.live;
+    uint4 now[NCH][kPieces<T>];
+    next.get(now);
     next.load(a, t + stride, gl);
     Choice<T, G, N> choice;
     #pragma unroll
-    for (int c = 0; c < NCH; ++c) choice.set(c, now.u[c], (c * G + gl) * 8);
+    for (int c = 0; c < NCH; ++c) choice.set(c, now[c], Row::first(c, gl), Row::STEP);
     choice.order();
-    uint32_t first = 0;
+    Word<T> most = 0;
     auto pick = [&](int p, int left) {
-      int e = 0;
-      const uint32_t win = choice.next(group_lanes, e, left);
-      if (p == 0) first = win;
-      if (gl == 0) {
-        w[p] = win;
-        if (sizeof(T) == 4) x[p] = e;
-      }
+      const Word<T> win = choice.next(left);
+      if (p == 0) most = win;
+      if (gl == 0) *reinterpret_cast<Word<T>*>(mine + p) = win;
     };
     if (a.k <= 8) {
       #pragma unroll
@@ -438,24 +405,22 @@ route_kernel(const __grid_constant__ RouteFwd a) {
     } else {
       for (int p = 0; p < a.k; ++p) pick(p, 8);
     }
+    const uint32_t first = key_of(most);
+    const bool routed = live && first > kKeyNegInf;
+    const float top = key_value(first);
     float v[N];
+    float2 s2 = both(0.f);
     #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       float u[8];
-      widen8(u, now.u[c]);
+      widen8(u, now[c]);
       #pragma unroll
-      for (int j = 0; j < 8; ++j) v[c * 8 + j] = u[j];
-    }
-    first = choice.key(first);
-    const bool routed = now.live && first > kKeyNegInf;
-    const float top = key_value(first);
-    float2 s2 = both(0.f);
-    #pragma unroll
-    for (int j = 0; j < N; j += 2) {
-      const float2 e = exp_below2(make_float2(v[j], v[j + 1]), top);
-      v[j] = e.x;
-      v[j + 1] = e.y;
-      s2 = add2(s2, e);
+      for (int j = 0; j < 8; j += 2) {
+        const float2 e = exp_below2(make_float2(u[j], u[j + 1]), top);
+        v[c * 8 + j] = e.x;
+        v[c * 8 + j + 1] = e.y;
+        s2 = add2(s2, e);
+      }
     }
     const float total = group_sum<G>(s2.x + s2.y);
     if (routed) {
@@ -468,21 +433,21 @@ route_kernel(const __grid_constant__ RouteFwd a) {
     __syncwarp();
     float picked = 0.f;
     for (int p = gl; p < a.k; p += G) {
-      const uint32_t key = choice.key(w[p]);
+      const Word<T> win = *reinterpret_cast<const Word<T>*>(mine + p);
+      const uint32_t key = key_of(win);
       const bool ok = routed && key > kKeyNegInf;
-      const int e = ok ? choice.expert(w[p], x[p]) : -1;
+      const int e = ok ? expert_of(win) : -1;
       const float y = ok ? exp_below(key_value(key), top) : 0.f;
       picked += y;
-      w[p] = __float_as_uint(y);
-      x[p] = e;
+      mine[p] = make_uint2(__float_as_uint(y), (uint32_t)e);
       if (ok) atomicAdd(&sc[e], 1);
     }
     const float z = __frcp_rn(a.normalize ? group_sum<G>(picked) : total);
     if (t < a.tokens)
       for (int p = gl; p < a.k; p += G) {
-        const int e = x[p];
-        a.weights[t * a.k + p] = e >= 0 ? __uint_as_float(w[p]) * z : 0.f;
-        a.index[t * a.k + p] = e;
+        const uint2 x = mine[p];
+        a.weights[t * a.k + p] = (int)x.y >= 0 ? __uint_as_float(x.x) * z : 0.f;
+        a.index[t * a.k + p] = (int)x.y;
       }
     __syncwarp();
   }
@@ -498,7 +463,7 @@ route_kernel(const __grid_constant__ RouteFwd a) {
     if (grp == 0 && warp >= i && warp < i + kRows) {
       #pragma unroll
       for (int j = 0; j < N; ++j) {
-        float& to = sp[warp - i][((j / 8) * G + gl) * 8 + j % 8];
+        float& to = sp[warp - i][Row::first(j / 8, gl) + (j % 8) * Row::STEP];
         to = i ? to + acc[j] : acc[j];
       }
     }
@@ -620,7 +585,7 @@ route_rows_kernel(const __grid_constant__ RouteFwd a) {
         #pragma unroll
         for (int q = 0; q < P; ++q) u[q] = row[c * P + q];
         Word<T> w[8];
-        keys8(w, u, s * SE + c * 8);
+        keys8(w, u, s * SE + c * 8, 1);
         sort8(w);
         best.merge(w);
         const float higher = max_nan(top, key_value(key_of(w[0])));
@@ -790,13 +755,15 @@ __global__ void __launch_bounds__(256) route_join_kernel(const __grid_constant__
 // x = (dw - sum of w dw) / (sum of the picks' p), whose mean under p is zero.
 //
 // A token takes G lanes, piece k of lane l its experts (k G + l) E .. + E - 1
-// (E = 8 bf16, 4 fp32: a 16-byte piece), NP pieces a lane.  The next token's
+// (E = 8 bf16, 4 fp32: a 16-byte piece), NP pieces a lane; rows that are not
+// whole, aligned pieces take single logits G experts apart instead, so that the
+// lanes of an access are neighbours in memory all the same.  The next token's
 // logits and picks are in flight while this one is worked on.
 constexpr int kBwdThreads = 256, kBwdWarps = kBwdThreads / 32;
 // blocks an SM, by the logits a lane holds: 64, 85 or 128 registers
 __host__ __device__ constexpr int bwd_blocks(int n) { return n <= 8 ? 4 : n <= 16 ? 3 : 2; }
 
-template <typename T, int G, int NP>
+template <typename T, int G, int NP, bool VEC>
 __global__ void __launch_bounds__(kBwdThreads, bwd_blocks(NP * kEl<T>))
 route_bwd_kernel(const __grid_constant__ RouteBwd a) {
   constexpr int E = kEl<T>, TPW = 32 / G, N = NP * E, KS = 2;
@@ -807,6 +774,8 @@ route_bwd_kernel(const __grid_constant__ RouteBwd a) {
   float* const xx = reinterpret_cast<float*>(smem) + (warp * TPW + grp) * (G * N);
   for (int i = gl; i < G * N; i += G) xx[i] = 0.f;
   __syncwarp();
+  // expert j of piece k
+  auto expert = [&](int k, int j) { return VEC ? (k * G + gl) * E + j : k * G * E + j * G + gl; };
   const T* logits = static_cast<const T*>(a.logits);
   const int routed_tokens = a.counts[a.experts];
   const float n = (float)(routed_tokens > 0 ? routed_tokens : 1);
@@ -814,7 +783,7 @@ route_bwd_kernel(const __grid_constant__ RouteBwd a) {
   float2 b[N / 2];
   #pragma unroll
   for (int j = 0; j < N; ++j) {
-    const int e = ((j / E) * G + gl) * E + j % E;
+    const int e = expert(j / E, j % E);
     const float v = e < a.experts ? f * (float)a.counts[e] : 0.f;
     if (j & 1) b[j / 2].y = v;
     else b[j / 2].x = v;
@@ -822,20 +791,34 @@ route_bwd_kernel(const __grid_constant__ RouteBwd a) {
   const int64_t stride = (int64_t)gridDim.x * kBwdWarps * TPW;
   const int64_t begin = ((int64_t)blockIdx.x * kBwdWarps + warp) * TPW;
   const uint32_t minus = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;    // -inf
-  uint4 next[NP];
+  uint4 next[VEC ? NP : 1];
+  uint32_t single[VEC ? 1 : N];
   bool live_next;
   int e_next[KS];
   float d_next[KS];
-  #pragma unroll
-  for (int k = 0; k < NP; ++k) next[k] = make_uint4(minus, minus, minus, minus);
+  if constexpr (VEC) {
+    #pragma unroll
+    for (int k = 0; k < NP; ++k) next[k] = make_uint4(minus, minus, minus, minus);
+  } else {
+    #pragma unroll
+    for (int j = 0; j < N; ++j) single[j] = sizeof(T) == 2 ? 0xff80u : 0xff800000u;
+  }
   auto load = [&](int64_t t) {
     const bool in = t < a.tokens;
     live_next = in && !(a.mask && !a.mask[t]);
-    const T* row = logits + t * a.ld + gl * E;
+    const T* row = logits + t * a.ld;
     #pragma unroll
-    for (int k = 0; k < NP; ++k)
-      if (a.vec && in && (k * G + gl) * E < a.experts)
-        next[k] = __ldg(reinterpret_cast<const uint4*>(row + k * G * E));
+    for (int k = 0; k < NP; ++k) {
+      if constexpr (VEC) {
+        if (in && expert(k, 0) < a.experts)
+          next[k] = __ldg(reinterpret_cast<const uint4*>(row + expert(k, 0)));
+      } else {
+        #pragma unroll
+        for (int j = 0; j < E; ++j)
+          if (in && expert(k, j) < a.experts)
+            single[k * E + j] = Logits<T, G, 1, false>::raw(row + expert(k, j));
+      }
+    }
     #pragma unroll
     for (int s = 0; s < KS; ++s) {
       const int p = gl + s * G;
@@ -866,15 +849,14 @@ route_bwd_kernel(const __grid_constant__ RouteBwd a) {
       l[s] = e[s] >= 0 ? to_f(row[e[s]]) : -INFINITY;
     }
     #pragma unroll
-    for (int k = 0; k < NP; ++k) u[k] = next[k];
-    if (!a.vec && t < a.tokens) {
-      #pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        const int e0 = (k * G + gl) * E;
-        Piece<E> w;
-        #pragma unroll
-        for (int j = 0; j < E; ++j) elem(w, j) = e0 + j < a.experts ? to_f(row[e0 + j]) : -INFINITY;
-        u[k] = narrow(w);
+    for (int k = 0; k < NP; ++k) {
+      if constexpr (VEC) {
+        u[k] = next[k];
+      } else if constexpr (sizeof(T) == 2) {
+        const uint32_t* x = single + k * E;
+        u[k] = make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
+      } else {
+        u[k] = make_uint4(single[k * E], single[k * E + 1], single[k * E + 2], single[k * E + 3]);
       }
     }
     load(t + stride);
@@ -922,11 +904,17 @@ route_bwd_kernel(const __grid_constant__ RouteBwd a) {
     const float2 inv = both(__frcp_rn(total));
     // x of piece k
     auto added = [&](int k, float2 (&x)[E / 2]) {
-      #pragma unroll
-      for (int q = 0; q < E / 4; ++q) {
-        const float4 w = *reinterpret_cast<const float4*>(xx + (k * G + gl) * E + q * 4);
-        x[2 * q] = make_float2(w.x, w.y);
-        x[2 * q + 1] = make_float2(w.z, w.w);
+      if constexpr (VEC) {
+        #pragma unroll
+        for (int q = 0; q < E / 4; ++q) {
+          const float4 w = *reinterpret_cast<const float4*>(xx + expert(k, q * 4));
+          x[2 * q] = make_float2(w.x, w.y);
+          x[2 * q + 1] = make_float2(w.z, w.w);
+        }
+      } else {
+        #pragma unroll
+        for (int j = 0; j < E / 2; ++j)
+          x[j] = make_float2(xx[expert(k, 2 * j)], xx[expert(k, 2 * j + 1)]);
       }
     };
     float2 dot2 = both(0.f);
@@ -957,17 +945,16 @@ route_bwd_kernel(const __grid_constant__ RouteBwd a) {
       T* out = static_cast<T*>(a.dlogits) + t * a.experts;
       #pragma unroll
       for (int k = 0; k < NP; ++k) {
-        const int e0 = (k * G + gl) * E;
         Piece<E> w;
         #pragma unroll
         for (int j = 0; j < E / 2; ++j) w.v[j] = v[k * (E / 2) + j];
         if (!routed) clear(w);
-        if (a.vec) {
-          if (e0 < a.experts) *reinterpret_cast<uint4*>(out + e0) = narrow(w);
+        if constexpr (VEC) {
+          if (expert(k, 0) < a.experts) *reinterpret_cast<uint4*>(out + expert(k, 0)) = narrow(w);
         } else {
           #pragma unroll
           for (int j = 0; j < E; ++j)
-            if (e0 + j < a.experts) out[e0 + j] = from_f<T>(elem(w, j));
+            if (expert(k, j) < a.experts) out[expert(k, j)] = from_f<T>(elem(w, j));
         }
       }
     }
@@ -1053,7 +1040,8 @@ struct LaunchFwd {
   int blocks;
   cudaStream_t s;
   template <typename T, int G, int NCH> cudaError_t operator()() const {
-    route_kernel<T, G, NCH><<<blocks, kRouteThreads, 0, s>>>(a);
+    if (a.vec) route_kernel<T, G, NCH, true><<<blocks, kRouteThreads, 0, s>>>(a);
+    else route_kernel<T, G, NCH, false><<<blocks, kRouteThreads, 0, s>>>(a);
     return cudaGetLastError();
   }
 };
@@ -1094,19 +1082,23 @@ bool rows_form(int64_t tokens, int experts, int k, const void* p, int64_t ld, si
          reinterpret_cast<uintptr_t>(p) % 16 == 0 && (size_t)ld * es % 16 == 0;
 }
 
-template <typename T, int G, int NP>
+template <typename T, int G, int NP, bool VEC>
 cudaError_t launch_bwd(const RouteBwd& a, cudaStream_t s) {
   const size_t smem = (size_t)kBwdWarps * 32 * NP * kEl<T> * sizeof(float);
   if (smem > 48u << 10) {
-    const cudaError_t e = cudaFuncSetAttribute(route_bwd_kernel<T, G, NP>,
+    const cudaError_t e = cudaFuncSetAttribute(route_bwd_kernel<T, G, NP, VEC>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
   const int per = kBwdWarps * 32 / G;
   const int64_t want = (a.tokens + per - 1) / per;
   const int64_t most = 152 * bwd_blocks(NP * kEl<T>);
-  route_bwd_kernel<T, G, NP><<<(unsigned)(want < most ? want : most), kBwdThreads, smem, s>>>(a);
+  route_bwd_kernel<T, G, NP, VEC>
+      <<<(unsigned)(want < most ? want : most), kBwdThreads, smem, s>>>(a);
   return cudaGetLastError();
+}
+template <typename T, int G, int NP> cudaError_t launch_bwd(const RouteBwd& a, cudaStream_t s) {
+  return a.vec ? launch_bwd<T, G, NP, true>(a, s) : launch_bwd<T, G, NP, false>(a, s);
 }
 
 // Lanes a token: the fewest that leave a lane at most two picks and twenty fp32
