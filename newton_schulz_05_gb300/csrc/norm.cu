@@ -222,7 +222,7 @@ cudaError_t forward(const NormFwd& a, int64_t chunks, cudaStream_t s) {
     if (two <= 704) return launch_fwd<T, 0, 2, 704, FUSED, REG>(a, 704, s);
     return launch_fwd<T, 0, 2, 1024, FUSED, REG>(a, 1024, s);
   } else {
-    if (one <= 256 && one < 2 * two) return launch_fwd<T, 0, 1, 256, FUSED, REG>(a, one, s);
+    if (one <= 256) return launch_fwd<T, 0, 1, 256, FUSED, REG>(a, one, s);
     if (two <= 128) return launch_fwd<T, 0, 2, 128, FUSED, REG>(a, two, s);
     if (two <= 256) return launch_fwd<T, 0, 2, 256, FUSED, REG>(a, two, s);
     if (two <= 512) return launch_fwd<T, 0, 2, 512, FUSED, REG>(a, two, s);

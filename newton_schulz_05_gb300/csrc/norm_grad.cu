@@ -265,42 +265,37 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
     }
     return;
   }
-  // row groups in order, through the ring's memory (every copy has landed and
-  // been read)
+  // through the ring's memory (every copy has landed and been read): each group
+  // leaves its sums as an image of its row, `phase` elements late, and columns
+  // are added over the groups in order
   copy_wait<0>();
   __syncthreads();
-  float* buf = reinterpret_cast<float*>(ring);
-  // regular rows have their columns at the same lanes in every group, so the
-  // groups of a warp are added by shuffles first
-  constexpr int kTogether = REG && TPR == 8 ? 4 : 1;
-  if constexpr (kTogether == 4) {
+  constexpr int kImage = PER * E;        // floats a thread and sum
+  float* const image = reinterpret_cast<float*>(ring) + (size_t)g * 2 * width * kImage;
+  #pragma unroll
+  for (int k = 0; k < PER; ++k)
     #pragma unroll
-    for (int o = 8; o < 32; o <<= 1)
-      #pragma unroll
-      for (int k = 0; k < PER; ++k)
-        #pragma unroll
-        for (int j = 0; j < E; ++j) {
-          elem(accw[k], j) += __shfl_xor_sync(0xffffffffu, elem(accw[k], j), o);
-          elem(accb[k], j) += __shfl_xor_sync(0xffffffffu, elem(accb[k], j), o);
-        }
-  }
-  for (int r = 0; r < groups; r += kTogether) {
-    if (r == g) {
-      #pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        const int c0 = col + k * span;
-        #pragma unroll
-        for (int j = 0; j < E; ++j)
-          if (inside(c0 + j, cols)) {
-            float &w0 = buf[c0 + j], &b0 = buf[cols + c0 + j];
-            w0 = r ? w0 + elem(accw[k], j) : elem(accw[k], j);
-            b0 = r ? b0 + elem(accb[k], j) : elem(accb[k], j);
-          }
-      }
+    for (int q = 0; q < E / 4; ++q) {
+      float4* to = reinterpret_cast<float4*>(image + (t + k * width) * E) + q;
+      to[0] = make_float4(accw[k].v[2 * q].x, accw[k].v[2 * q].y, accw[k].v[2 * q + 1].x,
+                          accw[k].v[2 * q + 1].y);
+      to[width * kImage / 4] = make_float4(accb[k].v[2 * q].x, accb[k].v[2 * q].y,
+                                           accb[k].v[2 * q + 1].x, accb[k].v[2 * q + 1].y);
     }
-    __syncthreads();
+  __syncthreads();
+  const uint64_t base = reinterpret_cast<uintptr_t>(dy) / sizeof(T);
+  for (int c = threadIdx.x; c < cols; c += nt) {
+    float sw = 0.f, sb = 0.f;
+    for (int r = 0; r < groups; ++r) {
+      const int late = REG || !vec ? 0
+          : (int)((base + ((uint64_t)blockIdx.x * groups + r) * a.lddy) & (E - 1));
+      const float* from = reinterpret_cast<const float*>(ring) + (size_t)r * 2 * width * kImage + c + late;
+      sw += from[0];
+      sb += from[width * kImage];
+    }
+    pw[c] = sw;
+    pb[c] = sb;
   }
-  for (int c = threadIdx.x; c < 2 * cols; c += nt) pw[c] = buf[c];
 }
 
 // dweight (blockIdx.y 0) and dbias (1) from the blocks' column sums: 32 columns a
