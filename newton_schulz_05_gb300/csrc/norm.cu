@@ -22,7 +22,7 @@ struct NormFwd {
 __host__ __device__ constexpr int fwd_blocks(int nt) { return nt <= 768 ? 768 / nt : 1; }
 
 // TPR threads a row (0: the block), C eights of elements a thread.  FUSED:
-// residual and dropout may be present.
+// residual and dropout may be present.  
 template <typename T, int TPR, int C, int NT, bool FUSED, bool REG>
 __global__ void __launch_bounds__(NT, fwd_blocks(NT))
 norm_fwd_kernel(const __grid_constant__ NormFwd a) {
@@ -45,12 +45,17 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
   const Visits go = visits(groups, g, a.rows);
   const int phase = REG || !vec ? 0
       : (int)((reinterpret_cast<uintptr_t>(x) / sizeof(T) + (uint64_t)go.first * a.ldx) & (E - 1));
-  const int col = t * E - phase;                // piece k begins at column col + k * span
-  const int span = width * E;
-  // this thread's place in the next row to copy in, and in the current row
-  const T *fx = x + go.first * a.ldx + col, *fr = res + go.first * a.ldr + col;
+  int c0[PER];               // first column of each of the thread's pieces
+  uint32_t in[PER];          // which of its elements are inside the row
+  #pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    c0[k] = (t + k * width) * E - phase;
+    in[k] = inside<E, REG>(c0[k], cols);
+  }
+  // the next row to copy in, and the current row
+  const T *fx = x + go.first * a.ldx, *fr = res + go.first * a.ldr;
   const T *cx = fx, *cr = fr;
-  int64_t out = go.first * a.cols + col;
+  int64_t out = go.first * a.cols;
   const int stage_len = OPS * PER * nt;
   uint4* const ring0 = ring + threadIdx.x;
   uint4* fill = ring0;
@@ -59,9 +64,8 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
     if (vec && ahead < go.mine) {
       #pragma unroll
       for (int k = 0; k < PER; ++k) {
-        const int c0 = col + k * span;
-        fetch<T, REG>(fill + k * nt, fx + k * span, x, c0, cols);
-        if (FUSED && res) fetch<T, REG>(fill + (PER + k) * nt, fr + k * span, res, c0, cols);
+        fetch<T, REG>(fill + k * nt, fx + c0[k], x, in[k]);
+        if (FUSED && res) fetch<T, REG>(fill + (PER + k) * nt, fr + c0[k], res, in[k]);
       }
     }
     copy_commit();
@@ -76,8 +80,8 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
   Piece<E> w[PER], b[PER];
   #pragma unroll
   for (int k = 0; k < PER; ++k) {
-    columns<T, REG>(w[k], a.weight, a.wbf16, col + k * span, cols, 1.f, a.wvec);
-    columns<T, REG>(b[k], a.bias, a.wbf16, col + k * span, cols, 0.f, a.wvec);
+    columns<T, REG>(w[k], a.weight, a.wbf16, c0[k], in[k], 1.f, a.wvec);
+    columns<T, REG>(b[k], a.bias, a.wbf16, c0[k], in[k], 0.f, a.wvec);
   }
   const float inv = 1.f / (float)cols;
   const uint4* from = ring0;
@@ -90,18 +94,17 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
     float2 s2 = both(0.f);
     #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      const int c0 = col + k * span;
       if (live) {
-        take<T, REG>(v[k], from + k * nt, cx + k * span, x, c0, cols, vec);
+        take<T, REG>(v[k], from + k * nt, cx + c0[k], x, in[k], vec);
         if constexpr (FUSED) {
-          if (a.drop) drop<E>(v[k].v, out + k * span, a.d);
+          if (a.drop) drop<E>(v[k].v, out + c0[k], a.d);
           if (res) {
             Piece<E> r;
-            take<T, REG>(r, from + (PER + k) * nt, cr + k * span, res, c0, cols, vec);
+            take<T, REG>(r, from + (PER + k) * nt, cr + c0[k], res, in[k], vec);
             #pragma unroll
             for (int j = 0; j < E / 2; ++j) v[k].v[j] = add2(v[k].v[j], r.v[j]);
           }
-          if (a.sum) put<T, REG>(static_cast<T*>(a.sum) + out + k * span, c0, cols, v[k], vec);
+          if (a.sum) put<T, REG>(static_cast<T*>(a.sum) + out + c0[k], v[k], in[k], vec);
         }
       } else {
         clear(v[k]);
@@ -114,16 +117,15 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
     float2 q2 = both(0.f);
     #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      const int c0 = col + k * span;
       #pragma unroll
       for (int j = 0; j < E / 2; ++j) v[k].v[j] = add2(v[k].v[j], m2);
-      if (whole<T, REG>(c0, cols)) {
+      if (in[k] == kFull<E>) {
         #pragma unroll
         for (int j = 0; j < E / 2; ++j) q2 = fma2(v[k].v[j], v[k].v[j], q2);
       } else if (!REG) {
         #pragma unroll
         for (int j = 0; j < E; ++j)
-          if (inside(c0 + j, cols)) q2.x = fmaf(elem(v[k], j), elem(v[k], j), q2.x);
+          if (in[k] >> j & 1) q2.x = fmaf(elem(v[k], j), elem(v[k], j), q2.x);
       }
     }
     const float rstd = rsqrtf(row_sum<TPR>(q2.x + q2.y, slots[1], nt >> 5) * inv + a.eps);
@@ -131,11 +133,10 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
       const float2 r2 = both(rstd);
       #pragma unroll
       for (int k = 0; k < PER; ++k) {
-        const int c0 = col + k * span;
         #pragma unroll
         for (int j = 0; j < E / 2; ++j)
           v[k].v[j] = fma2(mul2(v[k].v[j], r2), w[k].v[j], b[k].v[j]);
-        put<T, REG>(static_cast<T*>(a.y) + out + k * span, c0, cols, v[k], vec);
+        put<T, REG>(static_cast<T*>(a.y) + out + c0[k], v[k], in[k], vec);
       }
       if (t == 0) {
         if (a.mean) a.mean[row] = mean;

@@ -55,72 +55,82 @@ template <int N> __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
+// Which of a thread's E elements are inside the row: bit j for column c0 + j.
 // REG (regular): every piece of every row lies wholly inside the row or wholly
-// past its end, so one comparison says which.  Otherwise a piece may begin
-// ahead of the row, end past it, or (operands of different phases) be read
-// element by element.
-template <typename T, bool REG>
-__device__ __forceinline__ bool whole(int c0, int cols) {
-  return REG ? c0 < cols : c0 >= 0 && c0 + kEl<T> <= cols;
+// past its end.  Otherwise a piece may begin ahead of the row, end past it, or
+// (operands of different phases) be read element by element.
+template <int E> constexpr uint32_t kFull = (1u << E) - 1;
+template <int E, bool REG> __device__ __forceinline__ uint32_t inside(int c0, int cols) {
+  if (REG) return c0 < cols ? kFull<E> : 0u;
+  if (c0 >= cols || c0 + E <= 0) return 0u;
+  const uint32_t tail = cols - c0 < E ? (1u << (cols - c0)) - 1 : kFull<E>;
+  return c0 < 0 ? tail & (kFull<E> << -c0) : tail;
 }
-__device__ __forceinline__ bool inside(int c, int cols) { return c >= 0 && c < cols; }
 
-// Start the copy of the piece at p, column c0 of its row.  Bytes past the row
-// are not read; bytes ahead of it are, when they lie inside the tensor (from
-// `base`), and masked later.
+// Start the copy of the piece at p.  Bytes past the row are not read; bytes
+// ahead of it are, when they lie inside the tensor (from `base`), and masked
+// later.
 template <typename T, bool REG>
-__device__ __forceinline__ void fetch(uint4* slot, const T* p, const T* base, int c0, int cols) {
-  if (whole<T, REG>(c0, cols)) {
-    copy16(slot, p);
-  } else if (!REG && p >= base && c0 < cols) {
-    const int left = cols - c0;
-    copy16(slot, p, (left < kEl<T> ? left : kEl<T>) * (int)sizeof(T));
-  }
+__device__ __forceinline__ void fetch(uint4* slot, const T* p, const T* base, uint32_t in) {
+  if (in == kFull<kEl<T>>) copy16(slot, p);
+  else if (!REG && in && p >= base) copy16(slot, p, (32 - __clz(in)) * (int)sizeof(T));
 }
 
 // The piece in fp32, zeros outside the row: from its ring slot, or from memory
 // where fetch() made no copy.
 template <typename T, bool REG>
 __device__ __forceinline__ void take(Piece<kEl<T>>& v, const uint4* slot, const T* p, const T* base,
-                                     int c0, int cols, bool vec) {
-  if (REG) {
-    if (c0 < cols) widen(v, *slot);
-    else clear(v);
-  } else if (vec && whole<T, REG>(c0, cols)) {
+                                     uint32_t in, bool vec) {
+  if (REG ? in != 0 : vec && in == kFull<kEl<T>>) {
     widen(v, *slot);
-  } else if (vec && p >= base && c0 < cols) {
+  } else if (REG) {
+    clear(v);
+  } else if (vec && in && p >= base) {
     widen(v, *slot);
     #pragma unroll
     for (int j = 0; j < kEl<T>; ++j)
-      if (!inside(c0 + j, cols)) elem(v, j) = 0.f;
+      if (!(in >> j & 1)) elem(v, j) = 0.f;
   } else {
     #pragma unroll
-    for (int j = 0; j < kEl<T>; ++j) elem(v, j) = inside(c0 + j, cols) ? to_f(p[j]) : 0.f;
+    for (int j = 0; j < kEl<T>; ++j) elem(v, j) = in >> j & 1 ? to_f(p[j]) : 0.f;
   }
 }
 
 template <typename T, bool REG>
-__device__ __forceinline__ void put(T* p, int c0, int cols, Piece<kEl<T>>& v, bool vec) {
-  if ((REG || vec) && whole<T, REG>(c0, cols)) {
+__device__ __forceinline__ void put(T* p, Piece<kEl<T>>& v, uint32_t in, bool vec) {
+  if ((REG || vec) && in == kFull<kEl<T>>) {
     *reinterpret_cast<uint4*>(p) = narrow(v);
-  } else if (!REG) {
+  } else if (!REG && in) {
+    if constexpr (sizeof(T) == 2) {
+      if (vec) {       // a piece's words are aligned
+        const uint4 u = narrow(v);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t two = in >> 2 * j & 3;
+          if (two == 3) reinterpret_cast<uint32_t*>(p)[j] = w[j];
+          else if (two) reinterpret_cast<uint16_t*>(p)[2 * j + (two >> 1)] = (uint16_t)(two == 2 ? w[j] >> 16 : w[j]);
+        }
+        return;
+      }
+    }
     #pragma unroll
     for (int j = 0; j < kEl<T>; ++j)
-      if (inside(c0 + j, cols)) p[j] = from_f<T>(elem(v, j));
+      if (in >> j & 1) p[j] = from_f<T>(elem(v, j));
   }
 }
 
 // weight (or bias) of the piece's columns; `none` where there is no vector.
 // `vec`: the vector is 16-byte aligned.
 template <typename T, bool REG>
-__device__ __forceinline__ void columns(Piece<kEl<T>>& v, const void* w, int bf16, int c0, int cols,
-                                        float none, bool vec) {
+__device__ __forceinline__ void columns(Piece<kEl<T>>& v, const void* w, int bf16, int c0,
+                                        uint32_t in, float none, bool vec) {
   constexpr int E = kEl<T>;
   #pragma unroll
   for (int j = 0; j < E / 2; ++j) v.v[j] = both(none);
   if (!w) return;
   if (REG && vec) {
-    if (c0 >= cols) return;
+    if (!in) return;
     if (bf16) {
       const uint2* q = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(w) + c0);
       #pragma unroll
@@ -142,7 +152,7 @@ __device__ __forceinline__ void columns(Piece<kEl<T>>& v, const void* w, int bf1
   }
   #pragma unroll
   for (int j = 0; j < E; ++j)
-    if (inside(c0 + j, cols))
+    if (in >> j & 1)
       elem(v, j) = bf16 ? to_f(static_cast<const __nv_bfloat16*>(w)[c0 + j])
                         : static_cast<const float*>(w)[c0 + j];
 }

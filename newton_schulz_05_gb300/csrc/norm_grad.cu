@@ -62,13 +62,17 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
   const Visits go = visits(groups, g, a.rows);
   const int phase = REG || !vec ? 0
       : (int)((reinterpret_cast<uintptr_t>(dy) / sizeof(T) + (uint64_t)go.first * a.lddy) & (E - 1));
-  const int col = t * E - phase;                // piece k begins at column col + k * span
-  const int span = width * E;
-  // this thread's place in the next row to copy in, and in the current row
-  const T *fy = dy + go.first * a.lddy + col, *fs = sum + go.first * a.lds + col,
-          *fd = ds + go.first * a.ldds + col;
+  int c0[PER];               // first column of each of the thread's pieces
+  uint32_t in[PER];          // which of its elements are inside the row
+  #pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    c0[k] = (t + k * width) * E - phase;
+    in[k] = inside<E, REG>(c0[k], cols);
+  }
+  // the next row to copy in, and the current row
+  const T *fy = dy + go.first * a.lddy, *fs = sum + go.first * a.lds, *fd = ds + go.first * a.ldds;
   const T *cy = fy, *cs = fs, *cd = fd;
-  int64_t out = go.first * a.cols + col;
+  int64_t out = go.first * a.cols;
   const int stage_len = OPS * PER * nt;
   uint4* const ring0 = ring + threadIdx.x;
   uint4* fill = ring0;
@@ -77,10 +81,9 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
     if (vec && ahead < go.mine) {
       #pragma unroll
       for (int k = 0; k < PER; ++k) {
-        const int c0 = col + k * span;
-        fetch<T, REG>(fill + k * nt, fy + k * span, dy, c0, cols);
-        fetch<T, REG>(fill + (PER + k) * nt, fs + k * span, sum, c0, cols);
-        if (FUSED && ds) fetch<T, REG>(fill + (2 * PER + k) * nt, fd + k * span, ds, c0, cols);
+        fetch<T, REG>(fill + k * nt, fy + c0[k], dy, in[k]);
+        fetch<T, REG>(fill + (PER + k) * nt, fs + c0[k], sum, in[k]);
+        if (FUSED && ds) fetch<T, REG>(fill + (2 * PER + k) * nt, fd + c0[k], ds, in[k]);
       }
     }
     copy_commit();
@@ -99,7 +102,7 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
   #pragma unroll
   for (int k = 0; k < PER; ++k) {
     Piece<E>& wk = w[KEEP ? k : 0];
-    if (KEEP || WB) columns<T, REG>(wk, a.weight, a.wbf16, col + k * span, cols, 1.f, a.wvec);
+    if (KEEP || WB) columns<T, REG>(wk, a.weight, a.wbf16, c0[k], in[k], 1.f, a.wvec);
     if (!KEEP && WB) {
       #pragma unroll
       for (int j = 0; j < E / 4; ++j)
@@ -118,7 +121,7 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
         w[0].v[2 * j + 1] = make_float2(q.z, q.w);
       }
     } else {
-      columns<T, REG>(w[0], a.weight, a.wbf16, col + k * span, cols, 1.f, a.wvec);
+      columns<T, REG>(w[0], a.weight, a.wbf16, c0[k], in[k], 1.f, a.wvec);
     }
   };
   const float inv = 1.f / (float)cols;
@@ -138,18 +141,13 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
     pr += go.step;
     if (visit + 1 < go.mine) { mean_next = *pm; rstd_next = *pr; }
     copy_wait<D - 1>();
-    // dy and h = (sum - mean) * rstd of piece k
+    // dy and h = (sum - mean) * rstd of piece k; outside the row dy is 0 and h is
+    // finite whenever the row's own values are, so products with dy vanish there
     auto value = [&](int k, Piece<E>& y, Piece<E>& h) {
-      const int c0 = col + k * span;
-      take<T, REG>(y, from + k * nt, cy + k * span, dy, c0, cols, vec);
-      take<T, REG>(h, from + (PER + k) * nt, cs + k * span, sum, c0, cols, vec);
+      take<T, REG>(y, from + k * nt, cy + c0[k], dy, in[k], vec);
+      take<T, REG>(h, from + (PER + k) * nt, cs + c0[k], sum, in[k], vec);
       #pragma unroll
       for (int j = 0; j < E / 2; ++j) h.v[j] = mul2(add2(h.v[j], mean), rstd);
-      if (!REG && !whole<T, REG>(c0, cols)) {     // dy is 0 there, but h may be infinite
-        #pragma unroll
-        for (int j = 0; j < E; ++j)
-          if (!inside(c0 + j, cols)) elem(h, j) = 0.f;
-      }
     };
     Piece<E> gk[KEEP ? PER : 1], hk[KEEP ? PER : 1];
     float2 sg2 = both(0.f), sh2 = both(0.f);
@@ -157,7 +155,7 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
     for (int k = 0; k < PER; ++k) {
       Piece<E>& gi = gk[KEEP ? k : 0];
       Piece<E>& hi = hk[KEEP ? k : 0];
-      if (live && (!REG || col + k * span < cols)) {
+      if (live && (!REG || in[k])) {
         value(k, gi, hi);
       } else {
         clear(gi);
@@ -211,7 +209,6 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
     if (live) {
       #pragma unroll
       for (int k = 0; k < PER; ++k) {
-        const int c0 = col + k * span;
         Piece<E> d;
         Piece<E>& gi = gk[KEEP ? k : 0];
         Piece<E>& hi = hk[KEEP ? k : 0];
@@ -227,15 +224,15 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
         if constexpr (FUSED) {
           if (ds) {
             Piece<E> e;
-            take<T, REG>(e, from + (2 * PER + k) * nt, cd + k * span, ds, c0, cols, vec);
+            take<T, REG>(e, from + (2 * PER + k) * nt, cd + c0[k], ds, in[k], vec);
             #pragma unroll
             for (int j = 0; j < E / 2; ++j) d.v[j] = add2(d.v[j], e.v[j]);
           }
           if (a.dresidual)
-            put<T, REG>(static_cast<T*>(a.dresidual) + out + k * span, c0, cols, d, vec);
-          if (a.drop) drop<E>(d.v, out + k * span, a.d);
+            put<T, REG>(static_cast<T*>(a.dresidual) + out + c0[k], d, in[k], vec);
+          if (a.drop) drop<E>(d.v, out + c0[k], a.d);
         }
-        if (a.dx) put<T, REG>(static_cast<T*>(a.dx) + out + k * span, c0, cols, d, vec);
+        if (a.dx) put<T, REG>(static_cast<T*>(a.dx) + out + c0[k], d, in[k], vec);
       }
     }
     out += go.step * a.cols;
@@ -255,12 +252,11 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
   if (TPR == 0 && groups == 1) {
     #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      const int c0 = col + k * span;
       #pragma unroll
       for (int j = 0; j < E; ++j)
-        if (inside(c0 + j, cols)) {
-          pw[c0 + j] = elem(accw[k], j);
-          pb[c0 + j] = elem(accb[k], j);
+        if (in[k] >> j & 1) {
+          pw[c0[k] + j] = elem(accw[k], j);
+          pb[c0[k] + j] = elem(accb[k], j);
         }
     }
     return;
@@ -276,7 +272,8 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
   for (int k = 0; k < PER; ++k)
     #pragma unroll
     for (int q = 0; q < E / 4; ++q) {
-      float4* to = reinterpret_cast<float4*>(image + (t + k * width) * E) + q;
+      if (!in[k]) continue;
+      float4* to = reinterpret_cast<float4*>(image + c0[k] + phase) + q;
       to[0] = make_float4(accw[k].v[2 * q].x, accw[k].v[2 * q].y, accw[k].v[2 * q + 1].x,
                           accw[k].v[2 * q + 1].y);
       to[width * kImage / 4] = make_float4(accb[k].v[2 * q].x, accb[k].v[2 * q].y,
