@@ -25,6 +25,7 @@ template <typename T, bool RES>
 __global__ void __launch_bounds__(kDropThreads, 4)
 dropout_kernel(int64_t n, const T* x, const T* residual, const __grid_constant__ Drop d, T* y,
                int phase, bool vec) {
+  pdl_wait();
   constexpr int E = kEl<T>, U = kDropPieces, kSpan = U * kDropThreads * E;   // elements a block
   const int64_t block = (int64_t)blockIdx.x * kSpan - phase;
   const int64_t first = block + threadIdx.x * E;
@@ -78,11 +79,8 @@ cudaError_t dropout(int64_t n, const void* x, const void* residual, const Drop& 
   const int phase = vec ? phase_of(x) : 0;
   const int64_t span = (int64_t)kDropPieces * kDropThreads * E;
   const unsigned blocks = (unsigned)((n + phase + span - 1) / span);
-  if (residual)
-    dropout_kernel<T, true><<<blocks, kDropThreads, 0, s>>>(n, px, pr, d, static_cast<T*>(y), phase, vec);
-  else
-    dropout_kernel<T, false><<<blocks, kDropThreads, 0, s>>>(n, px, pr, d, static_cast<T*>(y), phase, vec);
-  return cudaGetLastError();
+  return launch_k(residual ? dropout_kernel<T, true> : dropout_kernel<T, false>, dim3(blocks),
+                  dim3(kDropThreads), 0, s, true, n, px, pr, d, static_cast<T*>(y), phase, vec);
 }
 
 }  // namespace

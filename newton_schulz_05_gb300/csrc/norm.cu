@@ -22,7 +22,7 @@ struct NormFwd {
 __host__ __device__ constexpr int fwd_blocks(int nt) { return nt <= 768 ? 768 / nt : 1; }
 
 // TPR threads a row (0: the block), C eights of elements a thread.  FUSED:
-// residual and dropout may be present.  
+// residual and dropout may be present.
 template <typename T, int TPR, int C, int NT, bool FUSED, bool REG>
 __global__ void __launch_bounds__(NT, fwd_blocks(NT))
 norm_fwd_kernel(const __grid_constant__ NormFwd a) {
@@ -41,6 +41,7 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
     for (int i = threadIdx.x; i < 64; i += nt) (&slots[0][0])[i] = 0.f;
     __syncthreads();
   }
+  pdl_wait();
   const bool vec = REG || a.vec;
   const Visits go = visits(groups, g, a.rows);
   const int phase = REG || !vec ? 0
@@ -112,7 +113,7 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
       #pragma unroll
       for (int j = 0; j < E / 2; ++j) s2 = add2(s2, v[k].v[j]);
     }
-    const float mean = row_sum<TPR>(s2.x + s2.y, slots[0], nt >> 5) * inv;
+    const float mean = row_sum<TPR, sizeof(T) == 2>(s2.x + s2.y, slots[0], nt >> 5) * inv;
     const float2 m2 = both(-mean);
     float2 q2 = both(0.f);
     #pragma unroll
@@ -128,7 +129,7 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
           if (in[k] >> j & 1) q2.x = fmaf(elem(v[k], j), elem(v[k], j), q2.x);
       }
     }
-    const float rstd = rsqrtf(row_sum<TPR>(q2.x + q2.y, slots[1], nt >> 5) * inv + a.eps);
+    const float rstd = rsqrtf(row_sum<TPR, sizeof(T) == 2>(q2.x + q2.y, slots[1], nt >> 5) * inv + a.eps);
     if (live) {
       const float2 r2 = both(rstd);
       #pragma unroll

@@ -58,6 +58,7 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
     for (int i = threadIdx.x; i < 160; i += nt) (&slots[0][0][0])[i] = 0.f;
     __syncthreads();
   }
+  pdl_wait();
   const bool vec = REG || a.vec;
   const Visits go = visits(groups, g, a.rows);
   const int phase = REG || !vec ? 0

@@ -370,6 +370,7 @@ route_kernel(const __grid_constant__ RouteFwd a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gl = lane % G, grp = lane / G;
   for (int e = threadIdx.x; e <= E; e += kRouteThreads) sc[e] = 0;
+  pdl_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
   __syncthreads();
   float acc[N];
@@ -521,6 +522,7 @@ route_rows_kernel(const __grid_constant__ RouteFwd a) {
   float2* const stat = reinterpret_cast<float2*>(col + padded);
   for (int e = threadIdx.x; e <= a.experts; e += blockDim.x) sc[e] = 0;
   for (int e = lane; e < padded; e += 32) col[e] = 0.f;
+  pdl_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
   __syncthreads();
   const T* logits = static_cast<const T*>(a.logits);
@@ -774,6 +776,7 @@ route_bwd_kernel(const __grid_constant__ RouteBwd a) {
   float* const xx = reinterpret_cast<float*>(smem) + (warp * TPW + grp) * (G * N);
   for (int i = gl; i < G * N; i += G) xx[i] = 0.f;
   __syncwarp();
+  pdl_wait();
   // expert j of piece k
   auto expert = [&](int k, int j) { return VEC ? (k * G + gl) * E + j : k * G * E + j * G + gl; };
   const T* logits = static_cast<const T*>(a.logits);
@@ -1040,9 +1043,8 @@ struct LaunchFwd {
   int blocks;
   cudaStream_t s;
   template <typename T, int G, int NCH> cudaError_t operator()() const {
-    if (a.vec) route_kernel<T, G, NCH, true><<<blocks, kRouteThreads, 0, s>>>(a);
-    else route_kernel<T, G, NCH, false><<<blocks, kRouteThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_k(a.vec ? route_kernel<T, G, NCH, true> : route_kernel<T, G, NCH, false>, dim3(blocks),
+                    dim3(kRouteThreads), 0, s, true, a);
   }
 };
 
@@ -1054,8 +1056,7 @@ cudaError_t launch_rows_k(const RouteFwd& a, int blocks, int warps, cudaStream_t
   const cudaError_t e = cudaFuncSetAttribute(route_rows_kernel<T, K>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  route_rows_kernel<T, K><<<blocks, 32 * warps, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_k(route_rows_kernel<T, K>, dim3(blocks), dim3(32 * warps), smem, s, true, a);
 }
 template <typename T>
 cudaError_t launch_rows(const RouteFwd& a, int blocks, int warps, cudaStream_t s) {
@@ -1093,9 +1094,8 @@ cudaError_t launch_bwd(const RouteBwd& a, cudaStream_t s) {
   const int per = kBwdWarps * 32 / G;
   const int64_t want = (a.tokens + per - 1) / per;
   const int64_t most = 152 * bwd_blocks(NP * kEl<T>);
-  route_bwd_kernel<T, G, NP, VEC>
-      <<<(unsigned)(want < most ? want : most), kBwdThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_k(route_bwd_kernel<T, G, NP, VEC>, dim3((unsigned)(want < most ? want : most)),
+                  dim3(kBwdThreads), smem, s, true, a);
 }
 template <typename T, int G, int NP> cudaError_t launch_bwd(const RouteBwd& a, cudaStream_t s) {
   return a.vec ? launch_bwd<T, G, NP, true>(a, s) : launch_bwd<T, G, NP, false>(a, s);
