@@ -10,7 +10,7 @@ include/muon.h, which states the formulas); this module and its compiled half
 (csrc/binding.cpp) check and marshal tensors.
 
 Two levels:
-  * layer_norm, dropout_add_layer_norm, dropout, route: differentiable
+  * layer_norm, dropout_add_layer_norm, dropout, route: differentiable once
     (torch.autograd), inputs of any strides;
   * *_forward / *_backward: one library call each, outputs as named tuples.
 
@@ -29,6 +29,7 @@ import os
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _PKG, _check, load
 
@@ -206,6 +207,7 @@ class _LayerNorm(torch.autograd.Function):
         return o.y, o.sum
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dsum):
         total, mean, rstd, weight = ctx.saved_tensors
         if dy is None and dsum is None:
@@ -243,6 +245,7 @@ class _Dropout(torch.autograd.Function):
         return dropout_forward(x, p, seed=seed, offset=offset, residual=residual)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         dx = dropout_backward(dy.contiguous(), **ctx.drop) if ctx.needs_input_grad[0] else None
         return dx, dy if ctx.needs_input_grad[1] else None, None, None, None
@@ -266,6 +269,7 @@ class _Route(torch.autograd.Function):
         return o.weights, o.index, o.counts, o.mean_prob, o.loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dweights, _index, _counts, _mean_prob, dloss):
         if dweights is None and dloss is None:
             return None, None, None, None

@@ -242,6 +242,56 @@ def test_many_tokens(layers):
         assert abs(float(o.loss) - loss) <= 800 * ref.U * loss
 
 
+@pytest.mark.parametrize("experts,k", [(8, 1), (16, 2), (24, 3), (40, 4), (64, 6), (72, 5), (160, 8),
+                                       (256, 8), (512, 7)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_large_batches(layers, experts, k, dtype, normalize):
+    # batches of many tokens, with ties, padded tokens, rows that leave nothing
+    # or fewer than k experts, and numbers at the type's ends, against torch in
+    # 64 bits; the same tokens in small batches give the same picks
+    tokens = 49152 + 77
+    g = torch.Generator().manual_seed(16)
+    l = (torch.randint(-12, 13, (tokens, experts), generator=g) / 4).to(dtype).cuda()
+    l[::3] = draw(len(range(0, tokens, 3)), experts, dtype, 17)
+    mask = (torch.rand(tokens, generator=g) > 0.1).cuda()
+    mask[1000:1040] = mask[2000:2030] = mask[3000:3003] = True
+    l[~mask] = float("nan")
+    l[1000:1040] = float("-inf")
+    l[2000:2030, min(2, experts - 1):] = float("-inf")
+    l[3000] = torch.finfo(dtype).min
+    l[3001, ::2] = torch.finfo(dtype).min
+    l[3002, 0] = torch.finfo(dtype).max
+    l[2000:2030, :2] = 1.0
+    o = layers.route_forward(l, k, token_mask=mask, normalize=normalize)
+    l64 = l.double()
+    routed = mask & (l64 > float("-inf")).any(1)
+    safe = torch.where(routed[:, None], l64, 0.0)
+    p = torch.softmax(safe, 1) * routed[:, None]
+    top, idx = torch.sort(safe, dim=1, descending=True, stable=True)
+    top, idx = top[:, :k], idx[:, :k]
+    ok = routed[:, None] & (top > float("-inf"))
+    assert torch.equal(o.index.long(), torch.where(ok, idx, -1))
+    w = torch.softmax(torch.where(ok, top, -1e300), 1) if normalize else p.gather(1, idx)
+    w = torch.where(ok, w, 0.0)
+    at = torch.where(ok, (top[:, :1] - top).clamp(max=1e6), 0.0)
+    assert bool(((o.weights.double() - w).abs() <= (at + 150) * ref.U * w + 1e-37).all())
+    n = int(routed.sum())
+    assert torch.equal(o.counts.long(), torch.cat((torch.bincount(idx[ok], minlength=experts),
+                                                   routed.sum()[None])))
+    mp = p.sum(0) / n
+    assert bool(((o.mean_prob.double() - mp).abs() <= 720 * ref.U * mp + 1e-37).all())
+    part = layers.route_forward(l[900:3100], k, token_mask=mask[900:3100], normalize=normalize)
+    assert torch.equal(part.index, o.index[900:3100])
+    dw = torch.randn(tokens, k, device="cuda")
+    a = layers.route_backward(l, o.index, o.counts, dweights=dw, dloss=o.loss, token_mask=mask,
+                              normalize=normalize)
+    b = layers.route_backward(l[900:3100], o.index[900:3100].contiguous(), o.counts,
+                              dweights=dw[900:3100].contiguous(), dloss=o.loss,
+                              token_mask=mask[900:3100], normalize=normalize)
+    assert torch.equal(a[900:3100], b)
+
+
 def test_more_than_32_bits_of_logits(layers):
     tokens, experts, k = (1 << 22) + 37, 520, 3
     l = torch.zeros((tokens, experts), device="cuda", dtype=BF)
