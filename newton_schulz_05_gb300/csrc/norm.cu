@@ -14,7 +14,6 @@ struct NormFwd {
   int wbf16;        // weight and bias are bf16 ...
   int wvec;         // ... and 16-byte aligned
   int drop;
-  int vec;          // every operand's rows share one phase
   Drop d;
 };
 
@@ -30,8 +29,8 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
   __shared__ alignas(16) float slots[2][32];
   constexpr int E = kEl<T>, OPS = FUSED ? 2 : 1, PER = C * 8 / E;   // pieces a thread and operand
   constexpr int D = ring_depth(NT, C, sizeof(T), OPS, fwd_blocks(NT), 0);
-  const int nt = REG || TPR ? NT : blockDim.x;
-  const int width = TPR ? TPR : nt, groups = TPR ? NT / (TPR ? TPR : 1) : 1;
+  constexpr int nt = NT;
+  constexpr int width = TPR ? TPR : nt, groups = TPR ? NT / (TPR ? TPR : 1) : 1;
   const int t = TPR ? (int)threadIdx.x % (TPR ? TPR : 1) : (int)threadIdx.x;
   const int g = TPR ? (int)threadIdx.x / (TPR ? TPR : 1) : 0;
   const int cols = (int)a.cols;
@@ -42,9 +41,8 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
     __syncthreads();
   }
   pdl_wait();
-  const bool vec = REG || a.vec;
   const Visits go = visits(groups, g, a.rows);
-  const int phase = REG || !vec ? 0
+  const int phase = REG ? 0
       : (int)((reinterpret_cast<uintptr_t>(x) / sizeof(T) + (uint64_t)go.first * a.ldx) & (E - 1));
   int c0[PER];               // first column of each of the thread's pieces
   uint32_t in[PER];          // which of its elements are inside the row
@@ -62,7 +60,7 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
   uint4* fill = ring0;
   int ahead = 0;
   auto start = [&] {
-    if (vec && ahead < go.mine) {
+    if (ahead < go.mine) {
       #pragma unroll
       for (int k = 0; k < PER; ++k) {
         fetch<T, REG>(fill + k * nt, fx + c0[k], x, in[k]);
@@ -96,16 +94,16 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
     #pragma unroll
     for (int k = 0; k < PER; ++k) {
       if (live) {
-        take<T, REG>(v[k], from + k * nt, cx + c0[k], x, in[k], vec);
+        take<T, REG>(v[k], from + k * nt, cx + c0[k], x, in[k]);
         if constexpr (FUSED) {
           if (a.drop) drop<E>(v[k].v, out + c0[k], a.d);
           if (res) {
             Piece<E> r;
-            take<T, REG>(r, from + (PER + k) * nt, cr + c0[k], res, in[k], vec);
+            take<T, REG>(r, from + (PER + k) * nt, cr + c0[k], res, in[k]);
             #pragma unroll
             for (int j = 0; j < E / 2; ++j) v[k].v[j] = add2(v[k].v[j], r.v[j]);
           }
-          if (a.sum) put<T, REG>(static_cast<T*>(a.sum) + out + c0[k], v[k], in[k], vec);
+          if (a.sum) put<T, REG>(static_cast<T*>(a.sum) + out + c0[k], v[k], in[k]);
         }
       } else {
         clear(v[k]);
@@ -137,7 +135,7 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
         #pragma unroll
         for (int j = 0; j < E / 2; ++j)
           v[k].v[j] = fma2(mul2(v[k].v[j], r2), w[k].v[j], b[k].v[j]);
-        put<T, REG>(static_cast<T*>(a.y) + out + c0[k], v[k], in[k], vec);
+        put<T, REG>(static_cast<T*>(a.y) + out + c0[k], v[k], in[k]);
       }
       if (t == 0) {
         if (a.mean) a.mean[row] = mean;
@@ -155,7 +153,7 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
   }
 }
 
-// ------------------------------------------------- rows longer than a block
+// ------- rows longer than a block, and operands whose phases differ
 
 template <typename T, typename WT>
 __global__ void __launch_bounds__(kNormThreads) norm_long_fwd_kernel(const __grid_constant__ NormFwd a) {
@@ -195,41 +193,32 @@ __global__ void __launch_bounds__(kNormThreads) norm_long_fwd_kernel(const __gri
 
 // --------------------------------------------------------------------- host
 
-// One kernel of the forward pass: `nt` threads a block, at most NT.
 template <typename T, int TPR, int C, int NT, bool FUSED, bool REG>
-cudaError_t launch_fwd(const NormFwd& a, int nt, cudaStream_t s) {
+cudaError_t launch_fwd(const NormFwd& a, cudaStream_t s) {
   constexpr int D = ring_depth(NT, C, sizeof(T), FUSED ? 2 : 1, fwd_blocks(NT), 0);
-  const size_t smem = (size_t)D * nt * C * 8 * sizeof(T) * (FUSED ? 2 : 1);
   return launch_rows(norm_fwd_kernel<T, TPR, C, NT, FUSED, REG>, a,
-                     blocks_for(a.rows, TPR ? NT / (TPR ? TPR : 1) : 1, fwd_blocks(nt)), nt, smem, s);
+                     blocks_for(a.rows, TPR ? NT / (TPR ? TPR : 1) : 1, fwd_blocks(NT)), NT,
+                     (size_t)D * NT * C * 8 * sizeof(T) * (FUSED ? 2 : 1), s);
 }
 
 // Rows of up to 64 columns take 8 lanes, of up to 512 a warp, longer ones a
-// block of sixteen elements a thread.  Regular rows run on the next block size
-// that is compiled in; ragged ones on exactly the warps that their pieces
-// need, eight elements a thread where that leaves fewer idle.
+// block of the next size compiled in: eight elements a thread up to 1536 columns,
+// sixteen beyond.
 template <typename T, bool FUSED, bool REG>
 cudaError_t forward(const NormFwd& a, int64_t chunks, cudaStream_t s) {
-  if (chunks <= 8) return launch_fwd<T, 8, 1, 256, FUSED, REG>(a, 256, s);
-  if (chunks <= 32) return launch_fwd<T, 32, 1, 256, FUSED, REG>(a, 256, s);
-  if (chunks <= 64) return launch_fwd<T, 32, 2, 256, FUSED, REG>(a, 256, s);
-  const int one = (int)(chunks + 31) / 32 * 32, two = (int)((chunks + 1) / 2 + 31) / 32 * 32;
-  if constexpr (REG) {
-    if (chunks <= 128) return launch_fwd<T, 0, 1, 128, FUSED, REG>(a, 128, s);
-    if (two <= 128) return launch_fwd<T, 0, 2, 128, FUSED, REG>(a, 128, s);
-    if (two <= 192) return launch_fwd<T, 0, 2, 192, FUSED, REG>(a, 192, s);
-    if (two <= 256) return launch_fwd<T, 0, 2, 256, FUSED, REG>(a, 256, s);
-    if (two <= 384) return launch_fwd<T, 0, 2, 384, FUSED, REG>(a, 384, s);
-    if (two <= 512) return launch_fwd<T, 0, 2, 512, FUSED, REG>(a, 512, s);
-    if (two <= 704) return launch_fwd<T, 0, 2, 704, FUSED, REG>(a, 704, s);
-    return launch_fwd<T, 0, 2, 1024, FUSED, REG>(a, 1024, s);
-  } else {
-    if (one <= 256) return launch_fwd<T, 0, 1, 256, FUSED, REG>(a, one, s);
-    if (two <= 128) return launch_fwd<T, 0, 2, 128, FUSED, REG>(a, two, s);
-    if (two <= 256) return launch_fwd<T, 0, 2, 256, FUSED, REG>(a, two, s);
-    if (two <= 512) return launch_fwd<T, 0, 2, 512, FUSED, REG>(a, two, s);
-    return launch_fwd<T, 0, 2, 1024, FUSED, REG>(a, two, s);
-  }
+  if (chunks <= 8) return launch_fwd<T, 8, 1, 256, FUSED, REG>(a, s);
+  if (chunks <= 32) return launch_fwd<T, 32, 1, 256, FUSED, REG>(a, s);
+  if (chunks <= 64) return launch_fwd<T, 32, 2, 256, FUSED, REG>(a, s);
+  if (chunks <= 128) return launch_fwd<T, 0, 1, 128, FUSED, REG>(a, s);
+  if (chunks <= 160) return launch_fwd<T, 0, 1, 160, FUSED, REG>(a, s);
+  if (chunks <= 192) return launch_fwd<T, 0, 1, 192, FUSED, REG>(a, s);
+  if (chunks <= 256) return launch_fwd<T, 0, 2, 128, FUSED, REG>(a, s);
+  if (chunks <= 384) return launch_fwd<T, 0, 2, 192, FUSED, REG>(a, s);
+  if (chunks <= 512) return launch_fwd<T, 0, 2, 256, FUSED, REG>(a, s);
+  if (chunks <= 768) return launch_fwd<T, 0, 2, 384, FUSED, REG>(a, s);
+  if (chunks <= 1024) return launch_fwd<T, 0, 2, 512, FUSED, REG>(a, s);
+  if (chunks <= 1408) return launch_fwd<T, 0, 2, 704, FUSED, REG>(a, s);
+  return launch_fwd<T, 0, 2, 1024, FUSED, REG>(a, s);
 }
 
 template <typename T>
@@ -271,9 +260,9 @@ extern "C" muon_status muon_layer_norm(int64_t rows, int64_t cols, int dtype, in
   const bool fused = residual || sum || p > 0.f;
   const NormFwd a = {rows, cols, ldx, ldr, x, residual, weight, bias, sum, y, mean, rstd, eps,
                      wdtype == MUON_BF16, !misaligned(weight, 16) && !misaligned(bias, 16), p > 0.f,
-                     ph.same, make_drop(p, seed, offset)};
+                     make_drop(p, seed, offset)};
   cudaError_t e;
-  if (ph.chunks() > kMaxChunks) {
+  if (!ph.same || ph.chunks() > kMaxChunks) {
     const int grid = (int)(rows < kSMs * 8 ? rows : kSMs * 8);
     e = by_types(dtype, wdtype, [&](auto t, auto wt) {
       norm_long_fwd_kernel<decltype(t), decltype(wt)><<<grid, kNormThreads, 0, s>>>(a);

@@ -16,7 +16,8 @@
 // threads take neighbouring pieces, and a thread takes the same pieces of every
 // row it visits (row steps are multiples of eight, which keeps the phase), so
 // weights stay in registers and the column sums of the gradient accumulate
-// there.  Operands whose phases differ are read element by element.
+// there.  Operands whose phases differ take the kernels for rows longer than a block
+// holds, which move single elements.
 //
 // Rows stream through a ring of asynchronous copies into shared memory.  Each
 // thread copies, waits for and reads only its own pieces, so the ring needs no
@@ -57,8 +58,7 @@ template <int N> __device__ __forceinline__ void copy_wait() {
 
 // Which of a thread's E elements are inside the row: bit j for column c0 + j.
 // REG (regular): every piece of every row lies wholly inside the row or wholly
-// past its end.  Otherwise a piece may begin ahead of the row, end past it, or
-// (operands of different phases) be read element by element.
+// past its end.  Otherwise a piece may begin ahead of the row or end past it.
 template <int E> constexpr uint32_t kFull = (1u << E) - 1;
 template <int E, bool REG> __device__ __forceinline__ uint32_t inside(int c0, int cols) {
   if (REG) return c0 < cols ? kFull<E> : 0u;
@@ -80,12 +80,12 @@ __device__ __forceinline__ void fetch(uint4* slot, const T* p, const T* base, ui
 // where fetch() made no copy.
 template <typename T, bool REG>
 __device__ __forceinline__ void take(Piece<kEl<T>>& v, const uint4* slot, const T* p, const T* base,
-                                     uint32_t in, bool vec) {
-  if (REG ? in != 0 : vec && in == kFull<kEl<T>>) {
+                                     uint32_t in) {
+  if (in == kFull<kEl<T>>) {
     widen(v, *slot);
-  } else if (REG) {
+  } else if (REG || !in) {
     clear(v);
-  } else if (vec && in && p >= base) {
+  } else if (p >= base) {
     widen(v, *slot);
     #pragma unroll
     for (int j = 0; j < kEl<T>; ++j)
@@ -97,26 +97,24 @@ __device__ __forceinline__ void take(Piece<kEl<T>>& v, const uint4* slot, const 
 }
 
 template <typename T, bool REG>
-__device__ __forceinline__ void put(T* p, Piece<kEl<T>>& v, uint32_t in, bool vec) {
-  if ((REG || vec) && in == kFull<kEl<T>>) {
+__device__ __forceinline__ void put(T* p, Piece<kEl<T>>& v, uint32_t in) {
+  if (in == kFull<kEl<T>>) {
     *reinterpret_cast<uint4*>(p) = narrow(v);
   } else if (!REG && in) {
     if constexpr (sizeof(T) == 2) {
-      if (vec) {       // a piece's words are aligned
-        const uint4 u = narrow(v);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t two = in >> 2 * j & 3;
-          if (two == 3) reinterpret_cast<uint32_t*>(p)[j] = w[j];
-          else if (two) reinterpret_cast<uint16_t*>(p)[2 * j + (two >> 1)] = (uint16_t)(two == 2 ? w[j] >> 16 : w[j]);
-        }
-        return;
+      const uint4 u = narrow(v);         // the piece's words are aligned
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      #pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t two = in >> 2 * j & 3;
+        if (two == 3) reinterpret_cast<uint32_t*>(p)[j] = w[j];
+        else if (two) reinterpret_cast<uint16_t*>(p)[2 * j + (two >> 1)] = (uint16_t)(two == 2 ? w[j] >> 16 : w[j]);
       }
+    } else {
+      #pragma unroll
+      for (int j = 0; j < kEl<T>; ++j)
+        if (in >> j & 1) p[j] = from_f<T>(elem(v, j));
     }
-    #pragma unroll
-    for (int j = 0; j < kEl<T>; ++j)
-      if (in >> j & 1) p[j] = from_f<T>(elem(v, j));
   }
 }
 
@@ -250,7 +248,7 @@ struct Phases {
   // eights of elements that the pieces of the longest row span
   int64_t chunks() const {
     const int64_t e = (int64_t)(16 / es);
-    const int64_t most = !same ? 0 : ld ? e - 1 : phase;
+    const int64_t most = ld ? e - 1 : phase;
     return ((cols + most + e - 1) / e * e + 7) / 8;
   }
 };

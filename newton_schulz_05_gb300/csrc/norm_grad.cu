@@ -14,8 +14,6 @@ struct NormBwd {
   int wbf16;        // the weight is bf16 ...
   int wvec;         // ... and 16-byte aligned
   int drop;
-  int vec;          // every operand's rows share one phase
-  int width;        // threads a row
   Drop d;
 };
 
@@ -33,8 +31,7 @@ __host__ __device__ constexpr int weight_bytes(int c, int es, int ops) {
   return kBwdThreads * c * 8 * es * ops + w <= 220 << 10 ? w : 0;
 }
 
-// One block an SM, cut into row groups of TPR lanes or (TPR 0) of W threads
-// (W 0: a.width), so that an SM leaves one partial column sum; C eights of
+// One block an SM, cut into row groups of TPR lanes or (TPR 0) of W threads, so that an SM leaves one partial column sum; C eights of
 // elements a thread.  KEEP: the row's values and the weight stay in registers
 // between the reduction and the output; otherwise (long rows) the values are
 // read from the ring twice, and the weight from shared memory.
@@ -46,10 +43,9 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
   constexpr int E = kEl<T>, OPS = FUSED ? 3 : 2, PER = C * 8 / E;
   constexpr int WB = KEEP ? 0 : weight_bytes(C, sizeof(T), OPS);
   constexpr int D = ring_depth(kBwdThreads, C, sizeof(T), OPS, 1, WB);
-  const int nt = TPR || W ? kBwdThreads : blockDim.x;
-  const int width = TPR ? TPR : W ? W : a.width;
-  const int groups = nt / width, g = (int)threadIdx.x / width, t = (int)threadIdx.x - g * width;
-  const int warps = ((width >> 5) + 3) & ~3;      // of a row group, in whole float4s
+  constexpr int width = TPR ? TPR : W, groups = kBwdThreads / width, nt = groups * width;
+  const int g = (int)threadIdx.x / width, t = (int)threadIdx.x - g * width;
+  constexpr int warps = ((width >> 5) + 3) & ~3;  // of a row group, in whole float4s
   const int cols = (int)a.cols;
   const T* dy = static_cast<const T*>(a.dy);
   const T* sum = static_cast<const T*>(a.sum);
@@ -59,9 +55,8 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
     __syncthreads();
   }
   pdl_wait();
-  const bool vec = REG || a.vec;
   const Visits go = visits(groups, g, a.rows);
-  const int phase = REG || !vec ? 0
+  const int phase = REG ? 0
       : (int)((reinterpret_cast<uintptr_t>(dy) / sizeof(T) + (uint64_t)go.first * a.lddy) & (E - 1));
   int c0[PER];               // first column of each of the thread's pieces
   uint32_t in[PER];          // which of its elements are inside the row
@@ -79,7 +74,7 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
   uint4* fill = ring0;
   int ahead = 0;
   auto start = [&] {
-    if (vec && ahead < go.mine) {
+    if (ahead < go.mine) {
       #pragma unroll
       for (int k = 0; k < PER; ++k) {
         fetch<T, REG>(fill + k * nt, fy + c0[k], dy, in[k]);
@@ -145,8 +140,8 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
     // dy and h = (sum - mean) * rstd of piece k; outside the row dy is 0 and h is
     // finite whenever the row's own values are, so products with dy vanish there
     auto value = [&](int k, Piece<E>& y, Piece<E>& h) {
-      take<T, REG>(y, from + k * nt, cy + c0[k], dy, in[k], vec);
-      take<T, REG>(h, from + (PER + k) * nt, cs + c0[k], sum, in[k], vec);
+      take<T, REG>(y, from + k * nt, cy + c0[k], dy, in[k]);
+      take<T, REG>(h, from + (PER + k) * nt, cs + c0[k], sum, in[k]);
       #pragma unroll
       for (int j = 0; j < E / 2; ++j) h.v[j] = mul2(add2(h.v[j], mean), rstd);
     };
@@ -197,7 +192,7 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
         if ((threadIdx.x & 15) == 0) s2[(low ? 0 : 40) + (t >> 5)] = v;
         group_sync(g, width);
         sg = sh = 0.f;
-        #pragma unroll 4
+        #pragma unroll
         for (int i = 0; i < warps; i += 4) {
           const float4 f = *reinterpret_cast<const float4*>(s2 + i);
           const float4 e = *reinterpret_cast<const float4*>(s2 + 40 + i);
@@ -225,15 +220,15 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
         if constexpr (FUSED) {
           if (ds) {
             Piece<E> e;
-            take<T, REG>(e, from + (2 * PER + k) * nt, cd + c0[k], ds, in[k], vec);
+            take<T, REG>(e, from + (2 * PER + k) * nt, cd + c0[k], ds, in[k]);
             #pragma unroll
             for (int j = 0; j < E / 2; ++j) d.v[j] = add2(d.v[j], e.v[j]);
           }
           if (a.dresidual)
-            put<T, REG>(static_cast<T*>(a.dresidual) + out + c0[k], d, in[k], vec);
+            put<T, REG>(static_cast<T*>(a.dresidual) + out + c0[k], d, in[k]);
           if (a.drop) drop<E>(d.v, out + c0[k], a.d);
         }
-        if (a.dx) put<T, REG>(static_cast<T*>(a.dx) + out + c0[k], d, in[k], vec);
+        if (a.dx) put<T, REG>(static_cast<T*>(a.dx) + out + c0[k], d, in[k]);
       }
     }
     out += go.step * a.cols;
@@ -285,7 +280,7 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
   for (int c = threadIdx.x; c < cols; c += nt) {
     float sw = 0.f, sb = 0.f;
     for (int r = 0; r < groups; ++r) {
-      const int late = REG || !vec ? 0
+      const int late = REG ? 0
           : (int)((base + ((uint64_t)blockIdx.x * groups + r) * a.lddy) & (E - 1));
       const float* from = reinterpret_cast<const float*>(ring) + (size_t)r * 2 * width * kImage + c + late;
       sw += from[0];
@@ -323,7 +318,7 @@ __global__ void __launch_bounds__(256) norm_join_kernel(int64_t cols, int parts,
   }
 }
 
-// ------------------------------------------------- rows longer than a block
+// ------- rows longer than a block, and operands whose phases differ
 
 template <typename T, typename WT>
 __global__ void __launch_bounds__(kNormThreads) norm_long_bwd_kernel(const __grid_constant__ NormBwd a) {
@@ -376,45 +371,35 @@ __global__ void __launch_bounds__(kNormThreads) norm_cols_kernel(const __grid_co
 
 // partial column sums of a gradient, whatever the phases of its operands
 int64_t norm_parts(int64_t rows, int64_t cols) {
-  const int64_t most = (cols + 14) / 8 > kMaxChunks ? kLongParts : kSMs;
-  return rows < most ? rows : most;
+  return rows < kLongParts ? rows : kLongParts;
 }
 
 template <typename T, int TPR, int C, int W, bool FUSED, bool KEEP, bool REG>
-cudaError_t launch_bwd(NormBwd a, int width, int nt, int* parts, cudaStream_t s) {
+cudaError_t launch_bwd(const NormBwd& a, int* parts, cudaStream_t s) {
   constexpr int OPS = FUSED ? 3 : 2, WB = KEEP ? 0 : weight_bytes(C, sizeof(T), OPS);
   constexpr int D = ring_depth(kBwdThreads, C, sizeof(T), OPS, 1, WB);
-  a.width = width;
-  const int64_t grid = blocks_for(a.rows, nt / width, 1);
+  constexpr int width = TPR ? TPR : W, groups = kBwdThreads / width, nt = groups * width;
+  const int64_t grid = blocks_for(a.rows, groups, 1);
   *parts = (int)grid;
   return launch_rows(norm_bwd_kernel<T, TPR, C, W, FUSED, KEEP, REG>, a, grid, nt,
                      (size_t)nt * C * 8 * sizeof(T) * OPS * D + (WB ? (size_t)nt * C * 32 : 0), s);
 }
 
-// Rows of up to 64 columns take 8 lanes, of up to 512 a warp, of up to 8192
-// whole warps of sixteen elements a thread, longer ones the block.  Regular rows
-// run on the next power of two of threads, ragged ones on exactly the warps that
-// their pieces need.
+// Rows of up to 64 columns take 8 lanes, of up to 512 a warp, of up to 8192 the
+// next number of threads that is compiled in, sixteen elements each, longer ones
+// the whole block.
 template <typename T, bool FUSED, bool REG>
 cudaError_t backward(const NormBwd& a, int64_t chunks, int* parts, cudaStream_t s) {
-  constexpr int N = kBwdThreads;
-  if (chunks <= 8) return launch_bwd<T, 8, 1, 0, FUSED, true, REG>(a, 8, N, parts, s);
-  if (chunks <= 32) return launch_bwd<T, 32, 1, 0, FUSED, true, REG>(a, 32, N, parts, s);
-  if (chunks <= 64) return launch_bwd<T, 32, 2, 0, FUSED, true, REG>(a, 32, N, parts, s);
-  if constexpr (REG) {
-    if (chunks <= 128) return launch_bwd<T, 0, 2, 64, FUSED, true, REG>(a, 64, N, parts, s);
-    if (chunks <= 256) return launch_bwd<T, 0, 2, 128, FUSED, true, REG>(a, 128, N, parts, s);
-    if (chunks <= 512) return launch_bwd<T, 0, 2, 256, FUSED, true, REG>(a, 256, N, parts, s);
-    if (chunks <= 1024) return launch_bwd<T, 0, 2, 512, FUSED, true, REG>(a, 512, N, parts, s);
-    if (chunks <= 1536) return launch_bwd<T, 0, 3, 512, FUSED, false, REG>(a, 512, N, parts, s);
-    return launch_bwd<T, 0, 4, 512, FUSED, false, REG>(a, 512, N, parts, s);
-  } else {
-    const int c = chunks <= 1024 ? 2 : chunks <= 1536 ? 3 : 4;
-    const int width = (int)((chunks + c - 1) / c + 31) / 32 * 32;
-    if (c == 2) return launch_bwd<T, 0, 2, 0, FUSED, true, REG>(a, width, N / width * width, parts, s);
-    if (c == 3) return launch_bwd<T, 0, 3, 0, FUSED, false, REG>(a, width, width, parts, s);
-    return launch_bwd<T, 0, 4, 0, FUSED, false, REG>(a, width, width, parts, s);
-  }
+  if (chunks <= 8) return launch_bwd<T, 8, 1, 0, FUSED, true, REG>(a, parts, s);
+  if (chunks <= 32) return launch_bwd<T, 32, 1, 0, FUSED, true, REG>(a, parts, s);
+  if (chunks <= 64) return launch_bwd<T, 32, 2, 0, FUSED, true, REG>(a, parts, s);
+  if (chunks <= 128) return launch_bwd<T, 0, 2, 64, FUSED, true, REG>(a, parts, s);
+  if (chunks <= 192) return launch_bwd<T, 0, 2, 96, FUSED, true, REG>(a, parts, s);
+  if (chunks <= 256) return launch_bwd<T, 0, 2, 128, FUSED, true, REG>(a, parts, s);
+  if (chunks <= 512) return launch_bwd<T, 0, 2, 256, FUSED, true, REG>(a, parts, s);
+  if (chunks <= 1024) return launch_bwd<T, 0, 2, 512, FUSED, true, REG>(a, parts, s);
+  if (chunks <= 1536) return launch_bwd<T, 0, 3, 512, FUSED, false, REG>(a, parts, s);
+  return launch_bwd<T, 0, 4, 512, FUSED, false, REG>(a, parts, s);
 }
 
 template <typename T>
@@ -487,11 +472,11 @@ extern "C" muon_status muon_layer_norm_backward(
   const bool fused = dsum || dresidual || p > 0.f;
   const NormBwd a = {rows, cols, lddy, ldsum, ldds, dy, sum, dsum, weight, mean, rstd, dx,
                      dresidual, cols_wanted ? static_cast<float*>(workspace) : nullptr,
-                     wdtype == MUON_BF16, !misaligned(weight, 16), p > 0.f, ph.same, 0,
+                     wdtype == MUON_BF16, !misaligned(weight, 16), p > 0.f,
                      make_drop(p, seed, offset)};
   cudaError_t e;
   int parts = (int)(rows < kLongParts ? rows : kLongParts);
-  if (ph.chunks() > kMaxChunks) {
+  if (!ph.same || ph.chunks() > kMaxChunks) {
     const int64_t tiles = (cols + kNormThreads - 1) / kNormThreads;
     e = by_types(dtype, wdtype, [&](auto t, auto wt) {
       using T = decltype(t);
