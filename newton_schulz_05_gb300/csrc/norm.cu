@@ -201,17 +201,27 @@ cudaError_t launch_fwd(const NormFwd& a, cudaStream_t s) {
                      (size_t)D * NT * C * 8 * sizeof(T) * (FUSED ? 2 : 1), s);
 }
 
-// Rows of up to 64 columns take 8 lanes, of up to 512 a warp, longer ones a
-// block of the next size compiled in: eight elements a thread up to 1536 columns,
-// sixteen beyond.
+// Rows of up to 64 columns take 8 lanes, of up to 512 a warp ([100000, 400] bf16
+// 26.8 against 35.1 us with two, but behind dropout [65536, 512] 60.3 against
+// 47.1), longer ones a block of the next size compiled in: eight elements a thread
+// up to 1536 columns (ragged fp32 4096: [9000, 3001] 39.8 against 58.5 us), sixteen
+// beyond.
 template <typename T, bool FUSED, bool REG>
 cudaError_t forward(const NormFwd& a, int64_t chunks, cudaStream_t s) {
   if (chunks <= 8) return launch_fwd<T, 8, 1, 256, FUSED, REG>(a, s);
   if (chunks <= 32) return launch_fwd<T, 32, 1, 256, FUSED, REG>(a, s);
-  if (chunks <= 64) return launch_fwd<T, 32, 2, 256, FUSED, REG>(a, s);
+  if (chunks <= 64) {     // the random bits want registers: two warps a row where they are drawn
+    if constexpr (FUSED) return launch_fwd<T, 0, 1, 64, FUSED, REG>(a, s);
+    else return launch_fwd<T, 32, 2, 256, FUSED, REG>(a, s);
+  }
   if (chunks <= 128) return launch_fwd<T, 0, 1, 128, FUSED, REG>(a, s);
   if (chunks <= 160) return launch_fwd<T, 0, 1, 160, FUSED, REG>(a, s);
   if (chunks <= 192) return launch_fwd<T, 0, 1, 192, FUSED, REG>(a, s);
+  if constexpr (!REG && sizeof(T) == 4) {      // sixteen elements would spill
+    if (chunks <= 256) return launch_fwd<T, 0, 1, 256, FUSED, REG>(a, s);
+    if (chunks <= 384) return launch_fwd<T, 0, 1, 384, FUSED, REG>(a, s);
+    if (chunks <= 512) return launch_fwd<T, 0, 1, 512, FUSED, REG>(a, s);
+  }
   if (chunks <= 256) return launch_fwd<T, 0, 2, 128, FUSED, REG>(a, s);
   if (chunks <= 384) return launch_fwd<T, 0, 2, 192, FUSED, REG>(a, s);
   if (chunks <= 512) return launch_fwd<T, 0, 2, 256, FUSED, REG>(a, s);
