@@ -43,7 +43,7 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
   pdl_wait();
   const Visits go = visits(groups, g, a.rows);
   const int phase = REG ? 0
-      : (int)((reinterpret_cast<uintptr_t>(x) / sizeof(T) + (uint64_t)go.first * a.ldx) & (E - 1));
+      : (int)(((uint64_t)go.first * a.ldx) & (E - 1));
   int c0[PER];               // first column of each of the thread's pieces
   uint32_t in[PER];          // which of its elements are inside the row
   #pragma unroll
@@ -51,9 +51,9 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
     c0[k] = (t + k * width) * E - phase;
     in[k] = inside<E, REG>(c0[k], cols);
   }
-  // the next row to copy in, and the current row
+  const uint4 front = front_mask<T, REG>(c0[0]);
+  // the next row to copy in, and the current row's elements in the outputs
   const T *fx = x + go.first * a.ldx, *fr = res + go.first * a.ldr;
-  const T *cx = fx, *cr = fr;
   int64_t out = go.first * a.cols;
   const int stage_len = OPS * PER * nt;
   uint4* const ring0 = ring + threadIdx.x;
@@ -63,8 +63,8 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
     if (ahead < go.mine) {
       #pragma unroll
       for (int k = 0; k < PER; ++k) {
-        fetch<T, REG>(fill + k * nt, fx + c0[k], x, in[k]);
-        if (FUSED && res) fetch<T, REG>(fill + (PER + k) * nt, fr + c0[k], res, in[k]);
+        fetch<T, REG>(fill + k * nt, fx + c0[k], in[k]);
+        if (FUSED && res) fetch<T, REG>(fill + (PER + k) * nt, fr + c0[k], in[k]);
       }
     }
     copy_commit();
@@ -94,12 +94,12 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
     #pragma unroll
     for (int k = 0; k < PER; ++k) {
       if (live) {
-        take<T, REG>(v[k], from + k * nt, cx + c0[k], x, in[k]);
+        take<T, REG>(v[k], from + k * nt, in[k], k == 0, front);
         if constexpr (FUSED) {
           if (a.drop) drop<E>(v[k].v, out + c0[k], a.d);
           if (res) {
             Piece<E> r;
-            take<T, REG>(r, from + (PER + k) * nt, cr + c0[k], res, in[k]);
+            take<T, REG>(r, from + (PER + k) * nt, in[k], k == 0, front);
             #pragma unroll
             for (int j = 0; j < E / 2; ++j) v[k].v[j] = add2(v[k].v[j], r.v[j]);
           }
@@ -144,10 +144,6 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
     }
     row += go.step;
     out += go.step * a.cols;
-    if constexpr (!REG) {
-      cx += go.step * a.ldx;
-      cr += go.step * a.ldr;
-    }
     from += stage_len;
     if (from == ring0 + D * stage_len) from = ring0;
   }

@@ -16,8 +16,8 @@
 // threads take neighbouring pieces, and a thread takes the same pieces of every
 // row it visits (row steps are multiples of eight, which keeps the phase), so
 // weights stay in registers and the column sums of the gradient accumulate
-// there.  Operands whose phases differ take the kernels for rows longer than a block
-// holds, which move single elements.
+// there.  Operands whose phases differ, or whose first row is not aligned, take the
+// kernels for rows longer than a block holds, which move single elements.
 //
 // Rows stream through a ring of asynchronous copies into shared memory.  Each
 // thread copies, waits for and reads only its own pieces, so the ring needs no
@@ -67,33 +67,44 @@ template <int E, bool REG> __device__ __forceinline__ uint32_t inside(int c0, in
   return c0 < 0 ? tail & (kFull<E> << -c0) : tail;
 }
 
-// Start the copy of the piece at p.  Bytes past the row are not read; bytes
-// ahead of it are, when they lie inside the tensor (from `base`), and masked
-// later.
+// Start the copy of the piece at p.  Bytes past the row are not read and arrive
+// as zeros; bytes ahead of it are read (they lie inside the tensor, whose first
+// row begins at an aligned address) and masked when the piece is taken.
 template <typename T, bool REG>
-__device__ __forceinline__ void fetch(uint4* slot, const T* p, const T* base, uint32_t in) {
-  if (in == kFull<kEl<T>>) copy16(slot, p);
-  else if (!REG && in && p >= base) copy16(slot, p, (32 - __clz(in)) * (int)sizeof(T));
+__device__ __forceinline__ void fetch(uint4* slot, const T* p, uint32_t in) {
+  if (!REG) copy16(slot, p, (32 - __clz(in)) * (int)sizeof(T));
+  else if (in) copy16(slot, p);
 }
 
-// The piece in fp32, zeros outside the row: from its ring slot, or from memory
-// where fetch() made no copy.
-template <typename T, bool REG>
-__device__ __forceinline__ void take(Piece<kEl<T>>& v, const uint4* slot, const T* p, const T* base,
-                                     uint32_t in) {
-  if (in == kFull<kEl<T>>) {
-    widen(v, *slot);
-  } else if (REG || !in) {
-    clear(v);
-  } else if (p >= base) {
-    widen(v, *slot);
+// A thread's first piece ANDed with this has nothing from ahead of the row
+template <typename T, bool REG> __device__ __forceinline__ uint4 front_mask(int c0) {
+  uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
+  if (!REG && c0 < 0) {
     #pragma unroll
-    for (int j = 0; j < kEl<T>; ++j)
-      if (!(in >> j & 1)) elem(v, j) = 0.f;
-  } else {
-    #pragma unroll
-    for (int j = 0; j < kEl<T>; ++j) elem(v, j) = in >> j & 1 ? to_f(p[j]) : 0.f;
+    for (int j = 0; j < 4; ++j) {
+      const int ahead = -c0 * (int)sizeof(T) - 4 * j;      // bytes of word j
+      w[j] = ahead >= 4 ? 0u : ahead > 0 ? ~0u << 8 * ahead : ~0u;
+    }
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The piece in fp32, zeros outside the row
+template <typename T, bool REG>
+__device__ __forceinline__ void take(Piece<kEl<T>>& v, const uint4* slot, uint32_t in, bool first,
+                                     const uint4& front) {
+  if (REG && !in) {
+    clear(v);
+    return;
+  }
+  uint4 u = *slot;
+  if (!REG && first) {
+    u.x &= front.x;
+    u.y &= front.y;
+    u.z &= front.z;
+    u.w &= front.w;
+  }
+  widen(v, u);
 }
 
 template <typename T, bool REG>
@@ -229,26 +240,26 @@ inline int64_t blocks_for(int64_t rows, int groups, int per_sm) {
 bool misaligned(const void* p, size_t es) { return reinterpret_cast<uintptr_t>(p) % es != 0; }
 
 // Collects the phases of the operands' rows (in elements of a 16-byte piece):
-// `same` while they all agree.
+// `same` while they all agree and every first row is aligned.
 struct Phases {
   int64_t rows, cols;
   size_t es;
   bool same = true, any = false;
-  int phase = 0, ld = 0;
+  int ld = 0;
   void add(const void* p, int64_t stride) {
     if (!p) return;
     const int last = (int)(16 / es) - 1;
     const int f = (int)(reinterpret_cast<uintptr_t>(p) / es & last);
     const int l = rows > 1 ? (int)(stride & last) : 0;
-    if (any && (f != phase || l != ld)) same = false;
-    if (!any) { any = true; phase = f; ld = l; }
+    if (f || (any && l != ld)) same = false;
+    if (!any) { any = true; ld = l; }
   }
   // every piece wholly inside or past its row
-  bool regular() const { return same && phase == 0 && ld == 0 && cols % (int64_t)(16 / es) == 0; }
+  bool regular() const { return same && ld == 0 && cols % (int64_t)(16 / es) == 0; }
   // eights of elements that the pieces of the longest row span
   int64_t chunks() const {
     const int64_t e = (int64_t)(16 / es);
-    const int64_t most = ld ? e - 1 : phase;
+    const int64_t most = ld ? e - 1 : 0;
     return ((cols + most + e - 1) / e * e + 7) / 8;
   }
 };

@@ -57,7 +57,7 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
   pdl_wait();
   const Visits go = visits(groups, g, a.rows);
   const int phase = REG ? 0
-      : (int)((reinterpret_cast<uintptr_t>(dy) / sizeof(T) + (uint64_t)go.first * a.lddy) & (E - 1));
+      : (int)(((uint64_t)go.first * a.lddy) & (E - 1));
   int c0[PER];               // first column of each of the thread's pieces
   uint32_t in[PER];          // which of its elements are inside the row
   #pragma unroll
@@ -65,9 +65,9 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
     c0[k] = (t + k * width) * E - phase;
     in[k] = inside<E, REG>(c0[k], cols);
   }
-  // the next row to copy in, and the current row
+  const uint4 front = front_mask<T, REG>(c0[0]);
+  // the next row to copy in, and the current row's elements in the outputs
   const T *fy = dy + go.first * a.lddy, *fs = sum + go.first * a.lds, *fd = ds + go.first * a.ldds;
-  const T *cy = fy, *cs = fs, *cd = fd;
   int64_t out = go.first * a.cols;
   const int stage_len = OPS * PER * nt;
   uint4* const ring0 = ring + threadIdx.x;
@@ -77,9 +77,9 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
     if (ahead < go.mine) {
       #pragma unroll
       for (int k = 0; k < PER; ++k) {
-        fetch<T, REG>(fill + k * nt, fy + c0[k], dy, in[k]);
-        fetch<T, REG>(fill + (PER + k) * nt, fs + c0[k], sum, in[k]);
-        if (FUSED && ds) fetch<T, REG>(fill + (2 * PER + k) * nt, fd + c0[k], ds, in[k]);
+        fetch<T, REG>(fill + k * nt, fy + c0[k], in[k]);
+        fetch<T, REG>(fill + (PER + k) * nt, fs + c0[k], in[k]);
+        if (FUSED && ds) fetch<T, REG>(fill + (2 * PER + k) * nt, fd + c0[k], in[k]);
       }
     }
     copy_commit();
@@ -137,11 +137,11 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
     pr += go.step;
     if (visit + 1 < go.mine) { mean_next = *pm; rstd_next = *pr; }
     copy_wait<D - 1>();
-    // dy and h = (sum - mean) * rstd of piece k; outside the row dy is 0 and h is
-    // finite whenever the row's own values are, so products with dy vanish there
+    // dy and h = (sum - mean) * rstd of piece k; outside the row dy and sum are 0, and
+    // h is finite whenever the row's own values are, so products with dy vanish there
     auto value = [&](int k, Piece<E>& y, Piece<E>& h) {
-      take<T, REG>(y, from + k * nt, cy + c0[k], dy, in[k]);
-      take<T, REG>(h, from + (PER + k) * nt, cs + c0[k], sum, in[k]);
+      take<T, REG>(y, from + k * nt, in[k], k == 0, front);
+      take<T, REG>(h, from + (PER + k) * nt, in[k], k == 0, front);
       #pragma unroll
       for (int j = 0; j < E / 2; ++j) h.v[j] = mul2(add2(h.v[j], mean), rstd);
     };
@@ -220,7 +220,7 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
         if constexpr (FUSED) {
           if (ds) {
             Piece<E> e;
-            take<T, REG>(e, from + (2 * PER + k) * nt, cd + c0[k], ds, in[k]);
+            take<T, REG>(e, from + (2 * PER + k) * nt, in[k], false, front);
             #pragma unroll
             for (int j = 0; j < E / 2; ++j) d.v[j] = add2(d.v[j], e.v[j]);
           }
@@ -232,11 +232,6 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
       }
     }
     out += go.step * a.cols;
-    if constexpr (!REG) {
-      cy += go.step * a.lddy;
-      cs += go.step * a.lds;
-      cd += go.step * a.ldds;
-    }
     from += stage_len;
     if (from == ring0 + D * stage_len) from = ring0;
   }
@@ -276,12 +271,11 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
                                            accb[k].v[2 * q + 1].x, accb[k].v[2 * q + 1].y);
     }
   __syncthreads();
-  const uint64_t base = reinterpret_cast<uintptr_t>(dy) / sizeof(T);
   for (int c = threadIdx.x; c < cols; c += nt) {
     float sw = 0.f, sb = 0.f;
     for (int r = 0; r < groups; ++r) {
-      const int late = REG ? 0
-          : (int)((base + ((uint64_t)blockIdx.x * groups + r) * a.lddy) & (E - 1));
+      const int late =
+          REG ? 0 : (int)((((uint64_t)blockIdx.x * groups + r) * a.lddy) & (E - 1));
       const float* from = reinterpret_cast<const float*>(ring) + (size_t)r * 2 * width * kImage + c + late;
       sw += from[0];
       sb += from[width * kImage];
