@@ -52,6 +52,15 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
     in[k] = inside<E, REG>(c0[k], cols);
   }
   const uint4 front = front_mask<T, REG>(c0[0]);
+  // 1 for the elements inside the row, 0 for the others
+  float2 one[REG ? 1 : PER][E / 2];
+  if constexpr (!REG) {
+    #pragma unroll
+    for (int k = 0; k < PER; ++k)
+      #pragma unroll
+      for (int j = 0; j < E / 2; ++j)
+        one[k][j] = make_float2(in[k] >> 2 * j & 1 ? 1.f : 0.f, in[k] >> (2 * j + 1) & 1 ? 1.f : 0.f);
+  }
   // the next row to copy in, and the current row's elements in the outputs
   const T *fx = x + go.first * a.ldx, *fr = res + go.first * a.ldr;
   int64_t out = go.first * a.cols;
@@ -116,15 +125,13 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
     float2 q2 = both(0.f);
     #pragma unroll
     for (int k = 0; k < PER; ++k) {
+      // outside the row the zeros stay
       #pragma unroll
-      for (int j = 0; j < E / 2; ++j) v[k].v[j] = add2(v[k].v[j], m2);
-      if (in[k] == kFull<E>) {
+      for (int j = 0; j < E / 2; ++j)
+        v[k].v[j] = REG ? add2(v[k].v[j], m2) : fma2(one[REG ? 0 : k][j], m2, v[k].v[j]);
+      if (!REG || in[k]) {
         #pragma unroll
         for (int j = 0; j < E / 2; ++j) q2 = fma2(v[k].v[j], v[k].v[j], q2);
-      } else if (!REG) {
-        #pragma unroll
-        for (int j = 0; j < E; ++j)
-          if (in[k] >> j & 1) q2.x = fmaf(elem(v[k], j), elem(v[k], j), q2.x);
       }
     }
     const float rstd = rsqrtf(row_sum<TPR, sizeof(T) == 2>(q2.x + q2.y, slots[1], nt >> 5) * inv + a.eps);
