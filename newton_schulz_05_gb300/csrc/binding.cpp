@@ -128,6 +128,27 @@ at::Tensor empty(at::IntArrayRef size, at::ScalarType type, const at::Tensor& li
   return at::Tensor(at::detail::empty_cuda(size, type, like.device(), std::nullopt));
 }
 
+// Small outputs of a call share one allocation, each at its own 256-byte
+// boundary: an allocation and its release cost as much host time as the checks
+// of a call.
+struct Carved {
+  at::Tensor bytes;
+  int64_t used = 0;
+  static int64_t room(int64_t numel, int64_t size) { return (numel * size + 255) / 256 * 256; }
+  Carved(int64_t total, const at::Tensor& like) : bytes(empty({total}, at::kByte, like)) {}
+  at::Tensor take(at::IntArrayRef size, at::ScalarType type) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+        c10::Storage(bytes.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+        c10::scalarTypeToTypeMeta(type));
+    c10::TensorImpl* impl = t.unsafeGetTensorImpl();
+    const int64_t es = (int64_t)c10::elementSize(type);
+    impl->set_storage_offset(used / es);
+    impl->set_sizes_contiguous(size);
+    used += room(t.numel(), es);
+    return t;
+  }
+};
+
 PyObject* wrap(at::Tensor t) { return THPVariable_Wrap(std::move(t)); }
 PyObject* none() { Py_RETURN_NONE; }
 
@@ -207,7 +228,8 @@ PyObject* layer_norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (res || p != 0.0) total = empty(x.sizes(), type, x);
     at::Tensor y = empty(x.sizes(), type, x);
     const at::IntArrayRef lead = x.sizes().slice(0, x.dim() - 1);
-    at::Tensor mean = empty(lead, at::kFloat, x), rstd = empty(lead, at::kFloat, x);
+    Carved stats(2 * Carved::room(r.rows, 4), x);
+    at::Tensor mean = stats.take(lead, at::kFloat), rstd = stats.take(lead, at::kFloat);
     const muon_status st = p_layer_norm(
         r.rows, r.cols, dt, wdt, x.const_data_ptr(), r.ld, res ? res->const_data_ptr() : nullptr, ldr,
         pw, pb, (float)eps, (float)p, seed, offset,
@@ -246,8 +268,10 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (need_w || need_b) {
       const muon_status st = p_layer_norm_workspace_bytes(r.rows, r.cols, &bytes);
       if (st != MUON_OK) return PyLong_FromLong(st);
-      if (need_w) dw = empty({r.cols}, wtype, dy);
-      if (need_b) db = empty({r.cols}, wtype, dy);
+      const int64_t room = Carved::room(r.cols, (int64_t)c10::elementSize(wtype));
+      Carved sums(room * (need_w + need_b), dy);
+      if (need_w) dw = sums.take({r.cols}, wtype);
+      if (need_b) db = sums.take({r.cols}, wtype);
       ws = empty({(int64_t)bytes}, at::kByte, dy);
     }
     auto ptr = [](at::Tensor& t) { return t.defined() ? t.mutable_data_ptr() : nullptr; };
@@ -327,8 +351,9 @@ PyObject* route_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     c10::SmallVector<int64_t, 6> shape(l.sizes().begin(), l.sizes().end());
     shape.back() = k;
     at::Tensor weights = empty(shape, at::kFloat, l), index = empty(shape, at::kInt, l);
-    at::Tensor counts = empty({experts + 1}, at::kInt, l);
-    at::Tensor mean_prob = empty({experts}, at::kFloat, l), loss = empty({}, at::kFloat, l);
+    Carved batch(Carved::room(experts + 1, 4) + Carved::room(experts, 4) + 256, l);
+    at::Tensor counts = batch.take({experts + 1}, at::kInt);
+    at::Tensor mean_prob = batch.take({experts}, at::kFloat), loss = batch.take({}, at::kFloat);
     st = p_route(r.rows, experts, k, dt, l.const_data_ptr(), r.ld, pm, normalize,
                  static_cast<float*>(weights.mutable_data_ptr()),
                  static_cast<int32_t*>(index.mutable_data_ptr()),
