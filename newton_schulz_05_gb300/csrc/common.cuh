@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 #include <utility>
 
@@ -29,6 +30,21 @@ inline cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, siz
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Lets Kernel be launched with up to `bytes` of dynamic shared memory (beyond the
+// 48 KB of every kernel); the driver is told once per device.
+template <auto Kernel>
+inline cudaError_t allow_shared(size_t bytes) {
+  static std::atomic<uint64_t> told{0};      // a bit per device
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = device < 64 ? (uint64_t)1 << device : 0;
+  if (told.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) told.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 __device__ __forceinline__ float to_f(float x) { return x; }

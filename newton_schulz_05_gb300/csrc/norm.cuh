@@ -273,14 +273,14 @@ muon_status check_common(int64_t rows, int64_t cols, int dtype, int wdtype, floa
   return MUON_OK;
 }
 
-template <typename K, typename A>
-cudaError_t launch_rows(K kernel, const A& a, int64_t grid, int nt, size_t smem, cudaStream_t s) {
+// smem: the same for every launch of the kernel
+template <auto Kernel, typename A>
+cudaError_t launch_rows(const A& a, int64_t grid, int nt, size_t smem, cudaStream_t s) {
   if (smem > 40u << 10) {     // 48 KB with the static part, without the attribute
-    const cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_shared<Kernel>(smem);
     if (e != cudaSuccess) return e;
   }
-  return launch_k(kernel, dim3((unsigned)grid), dim3(nt), smem, s, true, a);
+  return launch_k(Kernel, dim3((unsigned)grid), dim3(nt), smem, s, true, a);
 }
 
 template <typename F>

@@ -7,15 +7,18 @@
 // expert stays with its lane for all of a warp's tokens: probabilities add up
 // in registers, and the gradient's per-expert factors are loaded once.
 //
-// The choice.  Logits map to unsigned keys of the same order.  Each lane sorts
-// its eight once; a pick is then the largest head of the G lists, whose owner
-// drops it.  bf16 keys leave sixteen bits for the complement of the index, so
-// one unsigned maximum settles value and tie; fp32 keys carry the index beside
-// them, and the lowest lane with the largest head wins, its list being sorted
-// stably.
+// The choice.  Logits map to unsigned keys of the same order, and a key and the
+// complement of its index share a word (sixteen bits each for bf16, 32 for
+// fp32), so one unsigned maximum settles value and tie.  Each lane sorts its
+// eight words once; a pick is then the largest head of the G lists, whose owner
+// drops it.  From 48 Ki tokens on a lane takes a whole token instead
+// (route_rows_kernel).
 //
-// Both passes read the logits once from HBM; the forward pass is bound by the
-// instructions of the choice, the gradient by HBM.
+// Both passes read the logits once from HBM.  The forward pass is bound by the
+// instructions of the choice: [131072, 64] bf16, k = 6, takes 21.2 us where its
+// 23 MB would take 3.4, the integer pipe 53% busy; a join of the blocks' partial
+// sums costs 3 us of that and of every call of more than one block.  The
+// gradient comes nearer HBM: [65537, 160] fp32, k = 8, 18.3 us, 4.8 TB/s.
 #include <cmath>
 
 #include "common.cuh"
@@ -83,18 +86,6 @@ __device__ __forceinline__ void widen8(float (&v)[8], const uint4 (&u)[2]) {
   const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
   #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
-}
-__device__ __forceinline__ void narrow8(uint4 (&u)[1], const float (&v)[8]) {
-  Piece<8> p;
-  #pragma unroll
-  for (int j = 0; j < 8; ++j) elem(p, j) = v[j];
-  u[0] = narrow(p);
-}
-__device__ __forceinline__ void narrow8(uint4 (&u)[2], const float (&v)[8]) {
-  #pragma unroll
-  for (int q = 0; q < 2; ++q)
-    u[q] = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
-                      __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
 }
 
 // A key whose unsigned order is the order of the logits; 0 is below every
@@ -477,10 +468,10 @@ route_kernel(const __grid_constant__ RouteFwd a) {
 // time, into shared memory (rows 144 bytes apart, which spreads a column over
 // the banks); each lane reads its own row in eights, sorts each eight, merges it
 // into its K largest so far, and keeps a running maximum and sum of
-// exponentials.  No lane waits for another, so a token costs a third of the
-// instructions of the lanes-a-token form.  Then the lanes take columns and add up
-// the 32 tokens' probabilities; rows longer than a slice are read again for
-// that, from L2.
+// exponentials.  No lane waits for another, and a token takes 79 instructions of
+// a warp where the lanes-a-token form takes about 110 (64 experts, k = 6).  Then
+// the lanes take columns and add up the 32 tokens' probabilities; rows longer
+// than a slice are read again for that, from L2.
 constexpr int kSlice = 128, kSliceRow = kSlice + 16, kSliceBytes = 32 * kSliceRow;
 
 // shared memory of a warp: slices, column sums, each token's maximum and
@@ -1053,8 +1044,8 @@ cudaError_t launch_rows_k(const RouteFwd& a, int blocks, int warps, cudaStream_t
   constexpr int SE = kSlice / (int)sizeof(T);
   const int slices = (a.experts + SE - 1) / SE;
   const size_t smem = (size_t)warps * rows_warp_bytes(slices, slices * SE);
-  const cudaError_t e = cudaFuncSetAttribute(route_rows_kernel<T, K>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = allow_shared<route_rows_kernel<T, K>>(
+      kRouteWarps * rows_warp_bytes(2, 512));       // of the most warps and experts
   if (e != cudaSuccess) return e;
   return launch_k(route_rows_kernel<T, K>, dim3(blocks), dim3(32 * warps), smem, s, true, a);
 }
@@ -1087,8 +1078,7 @@ template <typename T, int G, int NP, bool VEC>
 cudaError_t launch_bwd(const RouteBwd& a, cudaStream_t s) {
   const size_t smem = (size_t)kBwdWarps * 32 * NP * kEl<T> * sizeof(float);
   if (smem > 48u << 10) {
-    const cudaError_t e = cudaFuncSetAttribute(route_bwd_kernel<T, G, NP, VEC>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_shared<route_bwd_kernel<T, G, NP, VEC>>(smem);
     if (e != cudaSuccess) return e;
   }
   const int per = kBwdWarps * 32 / G;
