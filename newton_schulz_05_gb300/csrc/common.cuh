@@ -33,17 +33,17 @@ inline cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, siz
 }
 
 // Lets Kernel be launched with up to `bytes` of dynamic shared memory (beyond the
-// 48 KB of every kernel); the driver is told once per device.
+// 48 KB of every kernel); set once per device.
 template <auto Kernel>
 inline cudaError_t allow_shared(size_t bytes) {
-  static std::atomic<uint64_t> told{0};      // a bit per device
+  static std::atomic<uint64_t> done{0};      // a bit per device
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
   const uint64_t bit = device < 64 ? (uint64_t)1 << device : 0;
-  if (told.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
   e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) told.fetch_or(bit, std::memory_order_relaxed);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }
 

@@ -7,6 +7,8 @@
 // which the random bits take 12.
 #include "norm.cuh"
 
+#include <type_traits>
+
 namespace muon {
 
 namespace {
@@ -163,34 +165,64 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
 
 // ------- rows longer than a block, and operands whose phases differ
 
-template <typename T, typename WT>
+// Eight neighbours a thread, so that a generator block serves them all.  KEPT: the row's sums stay in shared memory (fp32) between the three
+// passes; otherwise each pass reads and computes them again.
+template <typename T, typename WT, bool KEPT, bool VEC>
 __global__ void __launch_bounds__(kNormThreads) norm_long_fwd_kernel(const __grid_constant__ NormFwd a) {
+  extern __shared__ uint4 ring[];
   __shared__ float red[kNormThreads / 32 + 1];
+  Piece<8>* const kept = reinterpret_cast<Piece<8>*>(ring);
   const T* x = static_cast<const T*>(a.x);
   const T* r = static_cast<const T*>(a.residual);
   const WT* w = static_cast<const WT*>(a.weight);
   const WT* b = static_cast<const WT*>(a.bias);
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    auto value = [&](int64_t c) {
-      float v = to_f(x[row * a.ldx + c]);
-      if (a.drop) v = drop_one(v, (uint64_t)(row * a.cols + c), a.d);
-      return r ? v + to_f(r[row * a.ldr + c]) : v;
+    // the sums of eight columns from c; zeros past the row
+    auto value = [&](Piece<8>& v, int64_t c) {
+      load8<VEC>(v, x + row * a.ldx + c, a.cols - c);
+      if (a.drop) drop<8>(v.v, row * a.cols + c, a.d);
+      if (r) {
+        Piece<8> e;
+        load8<VEC>(e, r + row * a.ldr + c, a.cols - c);
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) v.v[j] = add2(v.v[j], e.v[j]);
+      }
+    };
+    auto again = [&](Piece<8>& v, int64_t c) {
+      if (KEPT) v = kept[c >> 3];
+      else value(v, c);
     };
     float s = 0.f;
-    for (int64_t c = threadIdx.x; c < a.cols; c += kNormThreads) s += value(c);
+    for (int64_t c = threadIdx.x * 8; c < a.cols; c += kNormThreads * 8) {
+      Piece<8> v;
+      value(v, c);
+      if (KEPT) kept[c >> 3] = v;       // read by this thread alone
+      #pragma unroll
+      for (int j = 0; j < 8; ++j) s += elem(v, j);
+    }
     const float mean = block_all_sum<kNormThreads>(s, red) / (float)a.cols;
     float q = 0.f;
-    for (int64_t c = threadIdx.x; c < a.cols; c += kNormThreads) {
-      const float e = value(c) - mean;
-      q = fmaf(e, e, q);
+    for (int64_t c = threadIdx.x * 8; c < a.cols; c += kNormThreads * 8) {
+      Piece<8> v;
+      again(v, c);
+      #pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float e = c + j < a.cols ? elem(v, j) - mean : 0.f;
+        q = fmaf(e, e, q);
+      }
     }
-    const float rstd = 1.f / sqrtf(block_all_sum<kNormThreads>(q, red) / (float)a.cols + a.eps);
-    for (int64_t c = threadIdx.x; c < a.cols; c += kNormThreads) {
-      const float v = value(c);
-      const float h = (v - mean) * rstd;
-      static_cast<T*>(a.y)[row * a.cols + c] =
-          from_f<T>(fmaf(h, w ? to_f(w[c]) : 1.f, b ? to_f(b[c]) : 0.f));
-      if (a.sum) static_cast<T*>(a.sum)[row * a.cols + c] = from_f<T>(v);
+    const float rstd = rsqrtf(block_all_sum<kNormThreads>(q, red) / (float)a.cols + a.eps);
+    for (int64_t c = threadIdx.x * 8; c < a.cols; c += kNormThreads * 8) {
+      Piece<8> v;
+      again(v, c);
+      if (a.sum) store8<VEC>(static_cast<T*>(a.sum) + row * a.cols + c, v, a.cols - c);
+      Piece<8> wc, bc;
+      weight8<VEC>(wc, w, c, a.cols, 1.f, a.wvec);
+      weight8<VEC>(bc, b, c, a.cols, 0.f, a.wvec);
+      const float2 m2 = both(-mean), r2 = both(rstd);
+      #pragma unroll
+      for (int j = 0; j < 4; ++j) v.v[j] = fma2(mul2(add2(v.v[j], m2), r2), wc.v[j], bc.v[j]);
+      store8<VEC>(static_cast<T*>(a.y) + row * a.cols + c, v, a.cols - c);
     }
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[row] = mean;
@@ -281,10 +313,24 @@ extern "C" muon_status muon_layer_norm(int64_t rows, int64_t cols, int dtype, in
                      make_drop(p, seed, offset)};
   cudaError_t e;
   if (!ph.same || ph.chunks() > kMaxChunks) {
-    const int grid = (int)(rows < kSMs * 8 ? rows : kSMs * 8);
+    constexpr size_t kMost = 200u << 10;      // of a row kept in shared memory
+    const size_t row = ((size_t)cols + 7) / 8 * sizeof(Piece<8>);
+    const int per_sm = row > kMost || row < 24u << 10 ? 4 : (int)((220u << 10) / row);
+    const int64_t grid = blocks_for(rows, 1, per_sm);
     e = by_types(dtype, wdtype, [&](auto t, auto wt) {
-      norm_long_fwd_kernel<decltype(t), decltype(wt)><<<grid, kNormThreads, 0, s>>>(a);
-      return cudaGetLastError();
+      using T = decltype(t);
+      using WT = decltype(wt);
+      auto run = [&](auto vec) {
+        constexpr bool VEC = decltype(vec)::value;
+        if (row > kMost)
+          return launch_k(norm_long_fwd_kernel<T, WT, false, VEC>, dim3((unsigned)grid),
+                          dim3(kNormThreads), 0, s, false, a);
+        const cudaError_t set = allow_shared<norm_long_fwd_kernel<T, WT, true, VEC>>(kMost);
+        if (set != cudaSuccess) return set;
+        return launch_k(norm_long_fwd_kernel<T, WT, true, VEC>, dim3((unsigned)grid),
+                        dim3(kNormThreads), row, s, false, a);
+      };
+      return ph.eights() ? run(std::true_type()) : run(std::false_type());
     });
   } else {
     e = dtype == MUON_BF16 ? forward<__nv_bfloat16>(a, ph, fused, s) : forward<float>(a, ph, fused, s);

@@ -335,7 +335,9 @@ __global__ void __launch_bounds__(256) norm_join_kernel(int64_t cols, int parts,
 
 // ------- rows longer than a block, and operands whose phases differ
 
-template <typename T, typename WT>
+// Eight neighbours a thread, so that a generator block serves them all; the
+// second pass finds the row in L2.
+template <typename T, typename WT, bool VEC>
 __global__ void __launch_bounds__(kNormThreads) norm_long_bwd_kernel(const __grid_constant__ NormBwd a) {
   __shared__ float red[kNormThreads / 32 + 1];
   const T* dy = static_cast<const T*>(a.dy);
@@ -344,22 +346,46 @@ __global__ void __launch_bounds__(kNormThreads) norm_long_bwd_kernel(const __gri
   const WT* w = static_cast<const WT*>(a.weight);
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const float mean = a.mean[row], rstd = a.rstd[row];
-    float sg = 0.f, sh = 0.f;
-    for (int64_t c = threadIdx.x; c < a.cols; c += kNormThreads) {
-      const float g = to_f(dy[row * a.lddy + c]) * (w ? to_f(w[c]) : 1.f);
-      sg += g;
-      sh = fmaf(g, (to_f(sum[row * a.lds + c]) - mean) * rstd, sh);
+    // g = dy weight and h = (sum - mean) rstd of eight columns from c; g is 0 past
+    // the row
+    auto value = [&](int64_t c, Piece<8>& g, Piece<8>& h) {
+      Piece<8> wc;
+      load8<VEC>(g, dy + row * a.lddy + c, a.cols - c);
+      load8<VEC>(h, sum + row * a.lds + c, a.cols - c);
+      weight8<VEC>(wc, w, c, a.cols, 1.f, a.wvec);
+      #pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        g.v[j] = mul2(g.v[j], wc.v[j]);
+        h.v[j] = mul2(add2(h.v[j], both(-mean)), both(rstd));
+      }
+    };
+    float2 sg2 = both(0.f), sh2 = both(0.f);
+    for (int64_t c = threadIdx.x * 8; c < a.cols; c += kNormThreads * 8) {
+      Piece<8> g, h;
+      value(c, g, h);
+      #pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sg2 = add2(sg2, g.v[j]);
+        sh2 = fma2(g.v[j], h.v[j], sh2);
+      }
     }
-    sg = block_all_sum<kNormThreads>(sg, red) / (float)a.cols;
-    sh = block_all_sum<kNormThreads>(sh, red) / (float)a.cols;
-    for (int64_t c = threadIdx.x; c < a.cols; c += kNormThreads) {
-      const float g = to_f(dy[row * a.lddy + c]) * (w ? to_f(w[c]) : 1.f);
-      const float h = (to_f(sum[row * a.lds + c]) - mean) * rstd;
-      float d = rstd * (g - sg - h * sh);
-      if (ds) d += to_f(ds[row * a.ldds + c]);
-      if (a.dresidual) static_cast<T*>(a.dresidual)[row * a.cols + c] = from_f<T>(d);
-      if (a.drop) d = drop_one(d, (uint64_t)(row * a.cols + c), a.d);
-      if (a.dx) static_cast<T*>(a.dx)[row * a.cols + c] = from_f<T>(d);
+    const float sg = block_all_sum<kNormThreads>(sg2.x + sg2.y, red) / (float)a.cols;
+    const float sh = block_all_sum<kNormThreads>(sh2.x + sh2.y, red) / (float)a.cols;
+    for (int64_t c = threadIdx.x * 8; c < a.cols; c += kNormThreads * 8) {
+      Piece<8> g, h;
+      value(c, g, h);
+      #pragma unroll
+      for (int j = 0; j < 4; ++j)
+        g.v[j] = mul2(both(rstd), fma2(h.v[j], both(-sh), add2(g.v[j], both(-sg))));
+      if (ds) {
+        Piece<8> e;
+        load8<VEC>(e, ds + row * a.ldds + c, a.cols - c);
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) g.v[j] = add2(g.v[j], e.v[j]);
+      }
+      if (a.dresidual) store8<VEC>(static_cast<T*>(a.dresidual) + row * a.cols + c, g, a.cols - c);
+      if (a.drop) drop<8>(g.v, row * a.cols + c, a.d);
+      if (a.dx) store8<VEC>(static_cast<T*>(a.dx) + row * a.cols + c, g, a.cols - c);
     }
   }
 }
@@ -508,9 +534,10 @@ extern "C" muon_status muon_layer_norm_backward(
     const int64_t tiles = (cols + kNormThreads - 1) / kNormThreads;
     e = by_types(dtype, wdtype, [&](auto t, auto wt) {
       using T = decltype(t);
+      using WT = decltype(wt);
       if (dx || dresidual)
-        norm_long_bwd_kernel<T, decltype(wt)>
-            <<<(int)(rows < kSMs * 8 ? rows : kSMs * 8), kNormThreads, 0, s>>>(a);
+        launch_k(ph.eights() ? norm_long_bwd_kernel<T, WT, true> : norm_long_bwd_kernel<T, WT, false>,
+                 dim3((unsigned)blocks_for(rows, 1, 4)), dim3(kNormThreads), 0, s, false, a);
       if (cols_wanted)
         norm_cols_kernel<T><<<dim3(parts, (unsigned)(tiles < 65535 ? tiles : 65535)), kNormThreads,
                               0, s>>>(a);

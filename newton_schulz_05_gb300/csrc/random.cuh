@@ -53,13 +53,6 @@ __device__ __forceinline__ uint4 philox(uint64_t counter, const Drop& d) {
   return make_uint4(c0, c1, c2, c3);
 }
 
-// value j (0..7) of a block's eight 16-bit halves, j known at compile time
-// after unrolling
-__device__ __forceinline__ uint32_t half_of(const uint4& w, int j) {
-  const uint32_t x = j < 2 ? w.x : j < 4 ? w.y : j < 6 ? w.z : w.w;
-  return (j & 1) ? x >> 16 : x & 0xffffu;
-}
-
 // The sixteen-bit halves of eight consecutive elements, the first of index i
 // (which may be below zero where a row's first piece begins ahead of the row:
 // such elements are not used).  When i is not a multiple of eight the elements
@@ -109,12 +102,6 @@ __device__ __forceinline__ void drop(float2 (&v)[E / 2], int64_t i, const Drop& 
     v[j].x = (u[j] << 16) >= d.high ? k.x : 0.f;
     v[j].y = u[j] >= d.high ? k.y : 0.f;
   }
-}
-
-// dropout of one element by its index (a whole generator block for it alone)
-__device__ __forceinline__ float drop_one(float x, uint64_t i, const Drop& d) {
-  const uint4 w = philox(d.offset + (i >> 3), d);
-  return half_of(w, (int)(i & 7)) >= d.threshold ? x * d.scale : 0.f;
 }
 
 }  // namespace muon
