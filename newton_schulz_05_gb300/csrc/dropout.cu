@@ -22,7 +22,8 @@ namespace {
 constexpr int kDropThreads = 256;
 constexpr int kDropPieces = 4;      // a thread: 64 bytes of an operand in flight
 
-template <typename T, bool RES>
+// DRAW: something may be dropped
+template <typename T, bool RES, bool DRAW>
 __global__ void __launch_bounds__(kDropThreads, 4)
 dropout_kernel(int64_t n, const T* x, const T* residual, const __grid_constant__ Drop d, T* y,
                int phase, bool vec) {
@@ -43,7 +44,7 @@ dropout_kernel(int64_t n, const T* x, const T* residual, const __grid_constant__
     for (int u = 0; u < U; ++u) {
       Piece<E> v, r;
       widen(v, ux[u]);
-      drop<E>(v.v, first + u * (kDropThreads * E), d);
+      if (DRAW) drop<E, false>(v.v, first + u * (kDropThreads * E), d);
       if (RES) {
         widen(r, ur[u]);
         #pragma unroll
@@ -59,7 +60,7 @@ dropout_kernel(int64_t n, const T* x, const T* residual, const __grid_constant__
     Piece<E> v;
     #pragma unroll
     for (int j = 0; j < E; ++j) elem(v, j) = i + j >= 0 && i + j < n ? to_f(x[i + j]) : 0.f;
-    drop<E>(v.v, i, d);
+    if (DRAW) drop<E, false>(v.v, i, d);
     #pragma unroll
     for (int j = 0; j < E; ++j)
       if (i + j >= 0 && i + j < n)
@@ -68,7 +69,7 @@ dropout_kernel(int64_t n, const T* x, const T* residual, const __grid_constant__
 }
 
 template <typename T>
-cudaError_t dropout(int64_t n, const void* x, const void* residual, const Drop& d, void* y,
+cudaError_t dropout(int64_t n, const void* x, const void* residual, const Drop& d, bool draw, void* y,
                     cudaStream_t s) {
   const T* px = static_cast<const T*>(x);
   const T* pr = static_cast<const T*>(residual);
@@ -80,8 +81,10 @@ cudaError_t dropout(int64_t n, const void* x, const void* residual, const Drop& 
   const int phase = vec ? phase_of(x) : 0;
   const int64_t span = (int64_t)kDropPieces * kDropThreads * E;
   const unsigned blocks = (unsigned)((n + phase + span - 1) / span);
-  return launch_k(residual ? dropout_kernel<T, true> : dropout_kernel<T, false>, dim3(blocks),
-                  dim3(kDropThreads), 0, s, true, n, px, pr, d, static_cast<T*>(y), phase, vec);
+  auto kernel = draw ? (residual ? dropout_kernel<T, true, true> : dropout_kernel<T, false, true>)
+                     : (residual ? dropout_kernel<T, true, false> : dropout_kernel<T, false, false>);
+  return launch_k(kernel, dim3(blocks), dim3(kDropThreads), 0, s, true, n, px, pr, d,
+                  static_cast<T*>(y), phase, vec);
 }
 
 }  // namespace
@@ -105,7 +108,8 @@ extern "C" muon_status muon_dropout(int64_t n, int dtype, const void* x, const v
   NvtxRange range("muon_dropout");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const Drop d = make_drop(p, seed, offset);
-  const cudaError_t e = dtype == MUON_BF16 ? dropout<__nv_bfloat16>(n, x, residual, d, y, s)
-                                           : dropout<float>(n, x, residual, d, y, s);
+  const bool draw = drop_threshold(p) > 0;
+  const cudaError_t e = dtype == MUON_BF16 ? dropout<__nv_bfloat16>(n, x, residual, d, draw, y, s)
+                                           : dropout<float>(n, x, residual, d, draw, y, s);
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }

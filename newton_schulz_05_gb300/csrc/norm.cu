@@ -1,7 +1,7 @@
 // Layer norm, alone or behind dropout and the residual add: the forward pass.
 //
 // Measured: [16384, 4096] bf16 45 us, 5.9 TB/s of x and y (41 us, 6.6 TB/s, of the
-// kernel alone); behind dropout and the residual add [8192, 10240] 127 us, 5.3 TB/s;
+// kernel alone); behind dropout and the residual add [8192, 10240] 117 us, 5.75 TB/s;
 // [4096, 10240] fp32 54 us, 6.2 TB/s; [9000, 3001] fp32 36 us, 5.9 TB/s; one row
 // 2.5 us.  16-bit rows behind dropout are bound by instructions, 33 an element of
 // which the random bits take 12.
@@ -112,7 +112,10 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
       if (live) {
         take<T, REG>(v[k], from + k * nt, in[k], k == 0, front);
         if constexpr (FUSED) {
-          if (a.drop) drop<E>(v[k].v, out + c0[k], a.d);
+          // without a branch the generator blocks of a thread's pieces overlap, where
+          // there are registers for it: [8192, 10240] bf16 116.7 against 126.7 us, but
+          // [4096, 16384] 118.6 against 96.8 and fp32 [4096, 10240] 116.6 against 108.6
+          if (a.drop) drop<E, REG && sizeof(T) == 2 && NT <= 704>(v[k].v, out + c0[k], a.d);
           if (res) {
             Piece<E> r;
             take<T, REG>(r, from + (PER + k) * nt, in[k], k == 0, front);
@@ -180,7 +183,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_long_fwd_kernel(const __gri
     // the sums of eight columns from c; zeros past the row
     auto value = [&](Piece<8>& v, int64_t c) {
       load8<VEC>(v, x + row * a.ldx + c, a.cols - c);
-      if (a.drop) drop<8>(v.v, row * a.cols + c, a.d);
+      if (a.drop) drop<8, false>(v.v, row * a.cols + c, a.d);
       if (r) {
         Piece<8> e;
         load8<VEC>(e, r + row * a.ldr + c, a.cols - c);
@@ -309,7 +312,7 @@ extern "C" muon_status muon_layer_norm(int64_t rows, int64_t cols, int dtype, in
   ph.add(y, cols);
   const bool fused = residual || sum || p > 0.f;
   const NormFwd a = {rows, cols, ldx, ldr, x, residual, weight, bias, sum, y, mean, rstd, eps,
-                     wdtype == MUON_BF16, !misaligned(weight, 16) && !misaligned(bias, 16), p > 0.f,
+                     wdtype == MUON_BF16, !misaligned(weight, 16) && !misaligned(bias, 16), drop_threshold(p) > 0,
                      make_drop(p, seed, offset)};
   cudaError_t e;
   if (!ph.same || ph.chunks() > kMaxChunks) {

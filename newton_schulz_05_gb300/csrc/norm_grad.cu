@@ -239,7 +239,7 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
           }
           if (a.dresidual)
             put<T, REG>(static_cast<T*>(a.dresidual) + out + c0[k], d, in[k]);
-          if (a.drop) drop<E>(d.v, out + c0[k], a.d);
+          if (a.drop) drop<E, false>(d.v, out + c0[k], a.d);
         }
         if (a.dx) put<T, REG>(static_cast<T*>(a.dx) + out + c0[k], d, in[k]);
       }
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_long_bwd_kernel(const __gri
         for (int j = 0; j < 4; ++j) g.v[j] = add2(g.v[j], e.v[j]);
       }
       if (a.dresidual) store8<VEC>(static_cast<T*>(a.dresidual) + row * a.cols + c, g, a.cols - c);
-      if (a.drop) drop<8>(g.v, row * a.cols + c, a.d);
+      if (a.drop) drop<8, false>(g.v, row * a.cols + c, a.d);
       if (a.dx) store8<VEC>(static_cast<T*>(a.dx) + row * a.cols + c, g, a.cols - c);
     }
   }
@@ -525,7 +525,7 @@ extern "C" muon_status muon_layer_norm_backward(
   const bool fused = dsum || dresidual || p > 0.f;
   const NormBwd a = {rows, cols, lddy, ldsum, ldds, dy, sum, dsum, weight, mean, rstd, dx,
                      dresidual, cols_wanted ? static_cast<float*>(workspace) : nullptr, dweight, dbias,
-                     wdtype == MUON_BF16, !misaligned(weight, 16), p > 0.f,
+                     wdtype == MUON_BF16, !misaligned(weight, 16), drop_threshold(p) > 0,
                      make_drop(p, seed, offset)};
   cudaError_t e;
   int parts = (int)(rows < kLongParts ? rows : kLongParts);

@@ -22,21 +22,27 @@ namespace muon {
 struct Drop {
   uint32_t key[20];    // the rounds' keys, two a round (kernel parameters: constant operands)
   uint64_t offset;     // counter of element 0
-  uint32_t threshold;  // an element is kept when its 16 bits are >= this ...
-  uint32_t high;       // ... which a word shows for its high half by being >= this
-  float scale;         // 65536 / (65536 - threshold)
+  uint32_t limit;      // an element is kept when its 16 bits, moved to a word's high half,
+                       // are above this
+  float scale;         // of the kept elements
 };
 
+// floor(65536 p + 1/2): an element is kept when its 16 bits are >= this
+inline uint32_t drop_threshold(float p) { return (uint32_t)std::floor((double)p * 65536.0 + 0.5); }
+
+// of a threshold above 0 (at 0 nothing is dropped and nothing need be drawn): 16
+// bits h are >= threshold when h << 16 (whatever its low half) is above
+// (threshold << 16) - 1
 inline Drop make_drop(float p, uint64_t seed, uint64_t offset) {
+  const uint32_t threshold = drop_threshold(p);
   Drop d;
   for (int r = 0; r < 10; ++r) {
     d.key[2 * r] = (uint32_t)seed + r * 0x9E3779B9u;
     d.key[2 * r + 1] = (uint32_t)(seed >> 32) + r * 0xBB67AE85u;
   }
   d.offset = offset;
-  d.threshold = (uint32_t)std::floor((double)p * 65536.0 + 0.5);
-  d.high = d.threshold < 65536u ? d.threshold << 16 : 0u;
-  d.scale = d.threshold < 65536u ? (float)(65536.0 / (65536.0 - d.threshold)) : 0.f;
+  d.limit = (uint32_t)(((uint64_t)threshold << 16) - 1);
+  d.scale = threshold < 65536u ? (float)(65536.0 / (65536.0 - threshold)) : 0.f;
   return d;
 }
 
@@ -79,28 +85,29 @@ __device__ __forceinline__ uint4 drop_bits(int64_t i, const Drop& d) {
   return w;
 }
 
-// dropout of E (4 or 8) consecutive elements, the first of index i
-template <int E>
+// Dropout of E (4 or 8) consecutive elements, the first of index i.  ALIGNED: i is
+// known to be a multiple of E.
+template <int E, bool ALIGNED>
 __device__ __forceinline__ void drop(float2 (&v)[E / 2], int64_t i, const Drop& d) {
-  if (d.threshold > 65535u) {      // p = 1
+  if (!ALIGNED && d.limit == 0xffffffffu) {     // p = 1
     #pragma unroll
     for (int j = 0; j < E / 2; ++j) v[j] = both(0.f);
     return;
   }
   uint32_t u[4];
-  if (E == 4 && (i & 3) == 0) {    // half a block
+  if (E == 4 && (ALIGNED || (i & 3) == 0)) {    // half a block
     const uint4 w = philox(d.offset + (uint64_t)(i >> 3), d);
     u[0] = i & 4 ? w.z : w.x;
     u[1] = i & 4 ? w.w : w.y;
   } else {
-    const uint4 w = drop_bits(i, d);
+    const uint4 w = ALIGNED ? philox(d.offset + (uint64_t)(i >> 3), d) : drop_bits(i, d);
     u[0] = w.x; u[1] = w.y; u[2] = w.z; u[3] = w.w;
   }
   #pragma unroll
   for (int j = 0; j < E / 2; ++j) {
     const float2 k = mul2(v[j], both(d.scale));
-    v[j].x = (u[j] << 16) >= d.high ? k.x : 0.f;
-    v[j].y = u[j] >= d.high ? k.y : 0.f;
+    v[j].x = (u[j] << 16) > d.limit ? k.x : 0.f;
+    v[j].y = u[j] > d.limit ? k.y : 0.f;
   }
 }
 
