@@ -8,7 +8,7 @@
 // do not depend on scheduling and nothing is added atomically.
 //
 // Measured: [16384, 4096] bf16 71 us, 5.7 TB/s of dy, sum and dx (67 us here, 4 in
-// the join); with dropout and dsum [8192, 4096] 63 us, 5.3 TB/s; [8192, 4096] fp32
+// the join); with dropout and dsum [8192, 4096] 60 us, 5.6 TB/s; [8192, 4096] fp32
 // 67 us, 6.0 TB/s; [9000, 3001] fp32 68 us, 4.8 TB/s.  16-bit rows are bound by
 // instructions at sixteen warps an SM (the column sums take the registers of more):
 // 19 an element, 37 with the random bits.
@@ -251,58 +251,65 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
   // the join may be set up while the column sums are put together
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!a.part) return;
-  // a column's sums: the block's share of them, or the gradients themselves
-  auto leave = [&](int c, float sw, float sb) {
-    if (gridDim.x > 1) {
-      float* p = a.part + (int64_t)blockIdx.x * 2 * a.cols + c;
-      p[0] = sw;
-      p[a.cols] = sb;
-    } else if (a.wbf16) {
+  float* const pw = a.part + (int64_t)blockIdx.x * 2 * a.cols;
+  float* const pb = pw + a.cols;
+  if (TPR == 0 && groups == 1) {
+    #pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      #pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (in[k] >> j & 1) {
+          pw[c0[k] + j] = elem(accw[k], j);
+          pb[c0[k] + j] = elem(accb[k], j);
+        }
+    }
+  } else {
+    // through the ring's memory (every copy has landed and been read): each group
+    // leaves its sums as an image of its row, `phase` elements late, and columns
+    // are added over the groups in order
+    copy_wait<0>();
+    __syncthreads();
+    constexpr int kImage = PER * E;      // floats a thread and sum
+    float* const image = reinterpret_cast<float*>(ring) + (size_t)g * 2 * width * kImage;
+    #pragma unroll
+    for (int k = 0; k < PER; ++k)
+      #pragma unroll
+      for (int q = 0; q < E / 4; ++q) {
+        if (!in[k]) continue;
+        float4* to = reinterpret_cast<float4*>(image + c0[k] + phase) + q;
+        to[0] = make_float4(accw[k].v[2 * q].x, accw[k].v[2 * q].y, accw[k].v[2 * q + 1].x,
+                            accw[k].v[2 * q + 1].y);
+        to[width * kImage / 4] = make_float4(accb[k].v[2 * q].x, accb[k].v[2 * q].y,
+                                             accb[k].v[2 * q + 1].x, accb[k].v[2 * q + 1].y);
+      }
+    __syncthreads();
+    for (int c = threadIdx.x; c < cols; c += nt) {
+      float sw = 0.f, sb = 0.f;
+      for (int r = 0; r < groups; ++r) {
+        const int late =
+            REG ? 0 : (int)((((uint64_t)blockIdx.x * groups + r) * a.lddy) & (E - 1));
+        const float* from =
+            reinterpret_cast<const float*>(ring) + (size_t)r * 2 * width * kImage + c + late;
+        sw += from[0];
+        sb += from[width * kImage];
+      }
+      pw[c] = sw;
+      pb[c] = sb;
+    }
+  }
+  // a block alone joins its sums itself.  A loop of its own: written into the
+  // unrolled stores above the choice of types cost [2000, 7001] fp32 9 of 40 us
+  if (gridDim.x > 1) return;
+  __syncthreads();
+  for (int c = threadIdx.x; c < cols; c += nt) {
+    const float sw = pw[c], sb = pb[c];
+    if (a.wbf16) {
       if (a.dweight) static_cast<__nv_bfloat16*>(a.dweight)[c] = from_f<__nv_bfloat16>(sw);
       if (a.dbias) static_cast<__nv_bfloat16*>(a.dbias)[c] = from_f<__nv_bfloat16>(sb);
     } else {
       if (a.dweight) static_cast<float*>(a.dweight)[c] = sw;
       if (a.dbias) static_cast<float*>(a.dbias)[c] = sb;
     }
-  };
-  if (TPR == 0 && groups == 1) {
-    #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      #pragma unroll
-      for (int j = 0; j < E; ++j)
-        if (in[k] >> j & 1) leave(c0[k] + j, elem(accw[k], j), elem(accb[k], j));
-    }
-    return;
-  }
-  // through the ring's memory (every copy has landed and been read): each group
-  // leaves its sums as an image of its row, `phase` elements late, and columns
-  // are added over the groups in order
-  copy_wait<0>();
-  __syncthreads();
-  constexpr int kImage = PER * E;        // floats a thread and sum
-  float* const image = reinterpret_cast<float*>(ring) + (size_t)g * 2 * width * kImage;
-  #pragma unroll
-  for (int k = 0; k < PER; ++k)
-    #pragma unroll
-    for (int q = 0; q < E / 4; ++q) {
-      if (!in[k]) continue;
-      float4* to = reinterpret_cast<float4*>(image + c0[k] + phase) + q;
-      to[0] = make_float4(accw[k].v[2 * q].x, accw[k].v[2 * q].y, accw[k].v[2 * q + 1].x,
-                          accw[k].v[2 * q + 1].y);
-      to[width * kImage / 4] = make_float4(accb[k].v[2 * q].x, accb[k].v[2 * q].y,
-                                           accb[k].v[2 * q + 1].x, accb[k].v[2 * q + 1].y);
-    }
-  __syncthreads();
-  for (int c = threadIdx.x; c < cols; c += nt) {
-    float sw = 0.f, sb = 0.f;
-    for (int r = 0; r < groups; ++r) {
-      const int late =
-          REG ? 0 : (int)((((uint64_t)blockIdx.x * groups + r) * a.lddy) & (E - 1));
-      const float* from = reinterpret_cast<const float*>(ring) + (size_t)r * 2 * width * kImage + c + late;
-      sw += from[0];
-      sb += from[width * kImage];
-    }
-    leave(c, sw, sb);
   }
 }
 
