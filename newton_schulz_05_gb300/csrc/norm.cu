@@ -3,8 +3,7 @@
 // Measured: [16384, 4096] bf16 45 us, 5.9 TB/s of x and y (41 us, 6.6 TB/s, of the
 // kernel alone); behind dropout and the residual add [8192, 10240] 117 us, 5.75 TB/s;
 // [4096, 10240] fp32 54 us, 6.2 TB/s; [9000, 3001] fp32 36 us, 5.9 TB/s; one row
-// 2.5 us.  16-bit rows behind dropout are bound by instructions, 33 an element of
-// which the random bits take 12.
+// 2.5 us.  16-bit rows behind dropout are bound by instructions, 30 an element.
 #include "norm.cuh"
 
 #include <type_traits>
@@ -113,9 +112,11 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
         take<T, REG>(v[k], from + k * nt, in[k], k == 0, front);
         if constexpr (FUSED) {
           // without a branch the generator blocks of a thread's pieces overlap, where
-          // there are registers for it: [8192, 10240] bf16 116.7 against 126.7 us, but
-          // [4096, 16384] 118.6 against 96.8 and fp32 [4096, 10240] 116.6 against 108.6
-          if (a.drop) drop<E, REG && sizeof(T) == 2 && NT <= 704>(v[k].v, out + c0[k], a.d);
+          // there are registers for it: [8192, 10240] bf16 116.7 against 126.7 us,
+          // [8192, 4096] fp32 91.8 against 92.9, [65536, 256] fp32 48.1 against 49.8; but
+          // [4096, 16384] bf16 118.6 against 97.2, [4096, 10240] fp32 116.6 against 108.2
+          if (a.drop)
+            drop<E, REG && NT <= (sizeof(T) == 2 ? 704 : 512)>(v[k].v, out + c0[k], a.d);
           if (res) {
             Piece<E> r;
             take<T, REG>(r, from + (PER + k) * nt, in[k], k == 0, front);
