@@ -183,6 +183,28 @@ def test_dropped_infinities_are_zeros(layers, dtype):
     assert all(torch.equal(u, v) for u, v in zip(a, b))
 
 
+# a probability that rounds to nothing, the largest below one, and one, on both
+# sides of every choice of how the random bits are drawn: NaN and infinities in
+# dropped places leave no trace, forwards or backwards
+@pytest.mark.parametrize("p", [1e-6, 0.3, 65535 / 65536, 1.0])
+@pytest.mark.parametrize("dtype,cols", [(BF, 512), (BF, 4096), (BF, 5632), (BF, 16384), (BF, 1001),
+                                        (BF, 16400), (F32, 256), (F32, 4096), (F32, 10240),
+                                        (F32, 333)])
+def test_extreme_dropout(layers, dtype, cols, p):
+    rows = 7
+    x, r = draw((rows, cols), dtype, 1), draw((rows, cols), dtype, 5)
+    w, b = draw(cols, dtype, 2, 0.3, 1.0), draw(cols, dtype, 3, 0.2)
+    o = check_forward(layers, x, r, w, b, p)
+    check_backward(layers, draw((rows, cols), dtype, 4, 0.1), o.sum, o.mean, o.rstd, w, None, p)
+    f = ref.factors(rows * cols, p, 11, 5).reshape(rows, cols)
+    gone = torch.from_numpy(f == 0).cuda()
+    bad = x.clone()
+    bad[gone] = torch.tensor([float("nan"), float("inf"), -float("inf")], device="cuda",
+                             dtype=dtype).repeat(gone.sum() // 3 + 1)[:gone.sum()]
+    again = layers.layer_norm_forward(bad, w, b, eps=EPS, residual=r, p=p, seed=11, offset=5)
+    assert all(torch.equal(u, v) for u, v in zip(o, again))
+
+
 @pytest.mark.parametrize("shape", [(0, 16), (2, 0, 16)])
 def test_no_rows(layers, shape):
     x = torch.empty(shape, device="cuda", dtype=BF)
