@@ -89,7 +89,10 @@ __device__ __forceinline__ uint4 drop_bits(int64_t i, const Drop& d) {
 // known to be a multiple of E.
 template <int E, bool ALIGNED>
 __device__ __forceinline__ void drop(float2 (&v)[E / 2], int64_t i, const Drop& d) {
-  if (!ALIGNED && d.limit == 0xffffffffu) {     // p = 1
+  // p = 1.  The comparison below drops everything by itself; the branch keeps the
+  // pieces' blocks apart where registers are short: layer norm of [4096, 16384] bf16
+  // 97.2 us against 102.0 without it, of [4096, 10240] fp32 108.2 against 114.6
+  if (!ALIGNED && d.limit == 0xffffffffu) {
     #pragma unroll
     for (int j = 0; j < E / 2; ++j) v[j] = both(0.f);
     return;
