@@ -306,6 +306,8 @@ extern "C" muon_status muon_layer_norm(int64_t rows, int64_t cols, int dtype, in
   if (rows == 0) return MUON_OK;
   NvtxRange range("muon_layer_norm");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ldx = row_stride(rows, ldx);
+  ldr = row_stride(rows, ldr);
   Phases ph{rows, cols, es};
   ph.add(x, ldx);
   ph.add(residual, ldr);

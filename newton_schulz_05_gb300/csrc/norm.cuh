@@ -287,6 +287,11 @@ inline int64_t blocks_for(int64_t rows, int groups, int per_sm) {
 
 bool misaligned(const void* p, size_t es) { return reinterpret_cast<uintptr_t>(p) % es != 0; }
 
+// The stride the kernels are given.  That of a single row has no meaning and is 0:
+// a row group without a row of its own then takes the phase that the first row
+// has, for which the layout was chosen, in its column sums.
+inline int64_t row_stride(int64_t rows, int64_t ld) { return rows > 1 ? ld : 0; }
+
 // Collects the phases of the operands' rows (in elements of a 16-byte piece):
 // `same` while they all agree and every first row is aligned.
 struct Phases {

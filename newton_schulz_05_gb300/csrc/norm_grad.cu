@@ -525,6 +525,9 @@ extern "C" muon_status muon_layer_norm_backward(
       return MUON_ERR_CUDA;
     return MUON_OK;
   }
+  lddy = row_stride(rows, lddy);
+  ldsum = row_stride(rows, ldsum);
+  ldds = row_stride(rows, ldds);
   Phases ph{rows, cols, es};
   ph.add(dy, lddy);
   ph.add(sum, ldsum);

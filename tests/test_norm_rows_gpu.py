@@ -1,0 +1,67 @@
+"""Layer norm and its gradient at numbers of rows and widths where the row
+groups of a block differ: one and two rows just below the widths of each
+layout, against the 64-bit host reference with the bounds of layers_ref."""
+import ctypes
+
+import pytest
+import torch
+
+from helpers import muon
+from test_norm_gpu import BF, EPS, F32, check_backward, check_forward, draw, layers  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def loud(layers, cols, dtype):
+    """A large gradient of the same width whose values stay behind in the
+    multiprocessors' shared memory."""
+    x = torch.full((2000, cols), 3e4, device="cuda", dtype=dtype)
+    x[:, ::2] = -3e4
+    one = torch.ones(2000, device="cuda")
+    layers.layer_norm_backward(x, x, one, one, dsum=x)
+    layers.layer_norm_backward(x, x, one, one)
+
+
+# just below the widths at which a row takes more threads, elements a thread or
+# row groups a block
+WIDTHS = [63, 255, 511, 1023, 1533, 1535, 2045, 2047, 4093, 4094, 4095, 8191]
+
+
+@pytest.mark.parametrize("rows", [1, 2])
+@pytest.mark.parametrize("cols", WIDTHS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_one_and_two_rows_of_ragged_widths(layers, rows, cols, dtype):  # noqa: F811
+    x, r = draw((rows, cols), dtype, 1, 1.3, 0.4), draw((rows, cols), dtype, 5, 2.0)
+    dy, ds = draw((rows, cols), dtype, 4, 0.1), draw((rows, cols), dtype, 6, 0.1)
+    w, b = draw(cols, F32, 2, 0.3, 1.0), draw(cols, F32, 3, 0.2)
+    for p, res, dsum in ((0.0, None, None), (0.0, r, ds), (0.25, r, ds)):
+        o = check_forward(layers, x, res, w, b, p)
+        loud(layers, cols, dtype)
+        check_backward(layers, dy, o.sum, o.mean, o.rstd, w, dsum, p)
+
+
+@pytest.mark.parametrize("ld", [1, 3, 7, 4097])
+@pytest.mark.parametrize("dtype,cols", [(BF, 1529), (BF, 4089), (F32, 4094), (F32, 4096), (BF, 61)])
+def test_one_row_of_any_stride(layers, dtype, cols, ld):  # noqa: F811
+    # the stride of a single row has no meaning, whatever it is
+    lib = muon().load()
+    dt = 1 if dtype == F32 else 0
+    dy, s = draw((1, cols), dtype, 4, 0.1), draw((1, cols), dtype, 1)
+    w = draw(cols, F32, 2, 0.3, 1.0)
+    o = layers.layer_norm_forward(s, w)
+    want = layers.layer_norm_backward(dy, s, o.mean, o.rstd, w)
+    loud(layers, cols, dtype)
+    need = ctypes.c_size_t()
+    assert lib.muon_layer_norm_workspace_bytes(1, cols, ctypes.byref(need)) == 0
+    ws = torch.empty(need.value, dtype=torch.uint8, device="cuda")
+    dx, (dw, db), y = torch.empty_like(dy), torch.empty(2, cols, device="cuda"), torch.empty_like(s)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lib.muon_layer_norm_backward(
+        1, cols, dt, 1, dy.data_ptr(), ld, s.data_ptr(), ld, o.mean.data_ptr(), o.rstd.data_ptr(),
+        w.data_ptr(), None, 0, 0.0, 0, 0, dx.data_ptr(), None, dw.data_ptr(), db.data_ptr(),
+        ws.data_ptr(), need.value, stream) == 0
+    assert lib.muon_layer_norm(1, cols, dt, 1, s.data_ptr(), ld, None, 0, w.data_ptr(), None, EPS, 0.0,
+                               0, 0, None, y.data_ptr(), None, None, stream) == 0
+    torch.cuda.synchronize()
+    for got, exact in ((dx, want.dx), (dw, want.dweight), (db, want.dbias), (y, o.y)):
+        assert torch.equal(got, exact)
