@@ -7,7 +7,8 @@ import pytest
 import torch
 
 from helpers import muon
-from test_norm_gpu import BF, EPS, F32, check_backward, check_forward, draw, layers  # noqa: F401
+from test_norm_gpu import (BF, EPS, F32, check_backward, check_forward, draw, layers,  # noqa: F401
+                           placed)
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +66,19 @@ def test_one_row_of_any_stride(layers, dtype, cols, ld):  # noqa: F811
     torch.cuda.synchronize()
     for got, exact in ((dx, want.dx), (dw, want.dweight), (db, want.dbias), (y, o.y)):
         assert torch.equal(got, exact)
+
+
+# h = (sum - mean) rstd is 0 in a constant row, however large mean * rstd is
+@pytest.mark.parametrize("cols", [7, 56, 61, 333, 1000, 1023, 4093, 8190, 16401])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_gradient_of_large_constant_rows(layers, dtype, cols):  # noqa: F811
+    rows = 5
+    s = torch.full((rows, cols), 2.0 ** 120, device="cuda", dtype=dtype)
+    s[::2] = draw((3, cols), dtype, 1)
+    mean, rstd = (torch.full((rows,), v, device="cuda") for v in (2.0 ** 120, 512.0))
+    mean[::2], rstd[::2] = 0.1, 1.1
+    w = draw(cols, F32, 2, 0.3, 1.0)
+    check_backward(layers, draw((rows, cols), dtype, 4, 0.1), s, mean, rstd, w, None, 0.0)
+    check_backward(layers, draw((rows, cols), dtype, 4, 0.1), s, mean, rstd, w,
+                   draw((rows, cols), dtype, 6, 0.1), 0.25)
+    check_backward(layers, placed(draw((rows, cols), dtype, 4, 0.1), 3, 1), s, mean, rstd, w, None, 0.0)
