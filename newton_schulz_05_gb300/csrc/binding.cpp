@@ -12,6 +12,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -306,6 +307,10 @@ PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (given) {
       if (given->sizes() != x.sizes()) value_error("out must have the shape of x");
       check_flat(*given, x.numel(), type, x, "out");
+      if (c10::GradMode::is_enabled() && given->requires_grad())
+        throw Raise{PyExc_RuntimeError, "out requires grad, and the call is not differentiable"};
+      // what autograd has saved of it is no longer what it saw
+      given->unsafeGetTensorImpl()->bump_version();
       y = *given;
     } else {
       y = empty(x.sizes(), type, x);

@@ -148,7 +148,9 @@ def layer_norm_backward(dy, sum, mean, rstd, weight=None, *, dsum=None, p: float
 def dropout_forward(x, p: float, *, seed: int, offset: int = 0, residual=None, out=None,
                     stream=None) -> torch.Tensor:
     """muon_dropout: residual + dropout(x) over dense tensors; `out` may be x
-    or residual itself."""
+    or residual itself.  Writing to `out` counts as an in-place change of it: a
+    backward pass that saved it raises, and while gradients are recorded an
+    `out` that requires grad is refused."""
     if stream is not None:
         return _on(stream, dropout_forward, (x, p),
                    dict(seed=seed, offset=offset, residual=residual, out=out))
