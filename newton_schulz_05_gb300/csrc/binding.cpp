@@ -125,6 +125,29 @@ void check_flat(const at::Tensor& t, int64_t numel, at::ScalarType type, const a
                 " elements on the device of the rows");
 }
 
+// Whether two shapes of as many elements list them alike: the first is one
+// dimension, or both are the same but for dimensions of one.
+bool listed_alike(at::IntArrayRef a, at::IntArrayRef b) {
+  size_t i = 0, j = 0;
+  if (a.size() == 1) return true;
+  for (;;) {
+    while (i < a.size() && a[i] == 1) ++i;
+    while (j < b.size() && b[j] == 1) ++j;
+    if (i == a.size() || j == b.size()) return i == a.size() && j == b.size();
+    if (a[i++] != b[j++]) return false;
+  }
+}
+
+// t has one element for each row of `like`, in the order of its leading
+// dimensions.  Other shapes of as many elements are refused: a transposed one would
+// be read in the wrong order.
+void check_each_row(const at::Tensor& t, int64_t rows, at::ScalarType type, const at::Tensor& like,
+                    const char* what) {
+  check_flat(t, rows, type, like, what);
+  if (!listed_alike(t.sizes(), like.sizes().slice(0, like.dim() - 1)))
+    value_error(std::string(what) + " must have the shape of the rows' leading dimensions, or one dimension");
+}
+
 at::Tensor empty(at::IntArrayRef size, at::ScalarType type, const at::Tensor& like) {
   return at::Tensor(at::detail::empty_cuda(size, type, like.device(), std::nullopt));
 }
@@ -256,8 +279,8 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int dt = dtype_of(dy, "dy");
     const Rows r = rows_or_raise(dy, "dy");
     const int64_t lds = same_rows(sum, dy, "sum");
-    check_flat(mean, r.rows, at::kFloat, dy, "mean");
-    check_flat(rstd, r.rows, at::kFloat, dy, "rstd");
+    check_each_row(mean, r.rows, at::kFloat, dy, "mean");
+    check_each_row(rstd, r.rows, at::kFloat, dy, "rstd");
     const int wdt = w ? dtype_of(*w, "weight") : MUON_F32;
     const at::ScalarType wtype = w ? w->scalar_type() : at::kFloat, type = dy.scalar_type();
     const void* pw = vector_of(w, r.cols, dy, "weight");
@@ -331,7 +354,7 @@ const uint8_t* mask_of(const at::Tensor* m, int64_t tokens, const at::Tensor& li
   if (!m) return nullptr;
   if (m->scalar_type() != at::kBool && m->scalar_type() != at::kByte)
     type_error(std::string("token_mask must be bool or uint8, got ") + c10::toString(m->scalar_type()));
-  check_flat(*m, tokens, m->scalar_type(), like, "token_mask");
+  check_each_row(*m, tokens, m->scalar_type(), like, "token_mask");
   return static_cast<const uint8_t*>(m->const_data_ptr());
 }
 
@@ -389,8 +412,12 @@ PyObject* route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (r.cols > 0x7fffffff || k > 0x7fffffff) return PyLong_FromLong(MUON_ERR_UNSUPPORTED_SHAPE);
     check_flat(index, r.rows * k, at::kInt, l, "index");
     check_flat(counts, r.cols + 1, at::kInt, l, "counts");
-    if (dw) check_flat(*dw, r.rows * k, at::kFloat, l, "dweights");
-    if (dl) check_flat(*dl, 1, at::kFloat, l, "dloss");
+    if (dw) {
+      check_flat(*dw, r.rows * k, at::kFloat, l, "dweights");
+      const int64_t two[2] = {r.rows, k};
+      if (!listed_alike(dw->sizes(), index.sizes()) && !listed_alike(dw->sizes(), two))
+        value_error("dweights must have the shape of index, or its rows in two dimensions or one");
+    }
     const uint8_t* pm = mask_of(mask, r.rows, l);
     at::Tensor out = empty(l.sizes(), l.scalar_type(), l);
     const muon_status st = p_route_backward(

@@ -170,7 +170,8 @@ def route_forward(logits, k: int, *, token_mask=None, normalize: bool = True,
                   stream=None) -> RouteOut:
     """muon_route over logits [..., experts]: the k largest of each token,
     their combine weights, per-expert counts, mean probabilities and the
-    balance loss.  token_mask (bool or uint8, one a token): tokens that count."""
+    balance loss.  token_mask (bool or uint8, one a token, in the shape of the
+    logits' leading dimensions or as one dimension): tokens that count."""
     if stream is not None:
         return _on(stream, route_forward, (logits, k),
                    dict(token_mask=token_mask, normalize=normalize))

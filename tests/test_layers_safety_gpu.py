@@ -39,3 +39,32 @@ def test_out_that_requires_grad_is_refused_while_grads_are_recorded(layers):
             layers.dropout_forward(x, 0.5, seed=1, out=out)
         with torch.no_grad():
             assert layers.dropout_forward(x, 0.5, seed=1, out=out) is out
+
+
+def test_shapes_that_only_count_alike_are_refused(layers):
+    b, t, e = 3, 8, 16
+    l = torch.randn(b, t, e, device="cuda")
+    mask = torch.rand(b, t, device="cuda") > 0.3
+    o = layers.route_forward(l, 2, token_mask=mask)
+    flat = layers.route_forward(l, 2, token_mask=mask.view(-1))
+    assert torch.equal(o.index, flat.index)
+    with pytest.raises(ValueError):
+        layers.route_forward(l, 2, token_mask=mask.view(t, b))
+    with pytest.raises(ValueError):
+        layers.route(l, 2, token_mask=mask.t())
+    dw = torch.randn(b, t, 2, device="cuda")
+    args = (l, o.index, o.counts)
+    g = layers.route_backward(*args, dweights=dw, token_mask=mask)
+    assert torch.equal(g, layers.route_backward(*args, dweights=dw.view(-1, 2), token_mask=mask))
+    for bad in (dw.view(t, b, 2), dw.view(2, -1)):
+        with pytest.raises(ValueError):
+            layers.route_backward(*args, dweights=bad, token_mask=mask)
+    with pytest.raises(ValueError):
+        layers.route_backward(*args, dweights=dw, token_mask=mask.view(t, b))
+    n = layers.layer_norm_forward(l)
+    g = layers.layer_norm_backward(l, l, n.mean, n.rstd)
+    for mean, rstd in ((n.mean.view(-1), n.rstd.view(-1)), (n.mean[..., None], n.rstd[None])):
+        assert torch.equal(g.dx, layers.layer_norm_backward(l, l, mean, rstd).dx)
+    for mean, rstd in ((n.mean.view(t, b), n.rstd), (n.mean, n.rstd.view(t, b)), (n.mean.view(2, -1), n.rstd)):
+        with pytest.raises(ValueError):
+            layers.layer_norm_backward(l, l, mean, rstd)
