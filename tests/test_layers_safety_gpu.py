@@ -68,3 +68,16 @@ def test_shapes_that_only_count_alike_are_refused(layers):
     for mean, rstd in ((n.mean.view(t, b), n.rstd), (n.mean, n.rstd.view(t, b)), (n.mean.view(2, -1), n.rstd)):
         with pytest.raises(ValueError):
             layers.layer_norm_backward(l, l, mean, rstd)
+
+
+def test_every_result_has_memory_of_its_own(layers):
+    x = torch.randn(40, 24, device="cuda")
+    w = torch.ones(24, device="cuda")
+    o = layers.layer_norm_forward(x, w, w, residual=x, p=0.1)
+    g = layers.layer_norm_backward(x, o.sum, o.mean, o.rstd, w, p=0.1)
+    r = layers.route_forward(x, 2)
+    for out in (o, g, r):
+        storages = [t.untyped_storage() for t in out]
+        assert len({s.data_ptr() for s in storages}) == len(out)
+        for t, s in zip(out, storages):
+            assert s.nbytes() == t.numel() * t.element_size() and t.storage_offset() == 0
