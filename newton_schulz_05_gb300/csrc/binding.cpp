@@ -188,6 +188,15 @@ bool truth(PyObject* o) {
   return v != 0;
 }
 
+// Gives up the interpreter lock for its lifetime: allocation and launch may block (a
+// full queue, a device allocation), and other Python threads run meanwhile.
+struct Unlocked {
+  PyThreadState* const state = PyEval_SaveThread();
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // Runs f, which returns a new reference, and turns C++ errors into Python ones
 template <typename F>
 PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
@@ -239,17 +248,22 @@ PyObject* layer_norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* stream = stream_of(x);
     const int64_t ldr = res ? same_rows(*res, x, "residual") : 0;
     const at::ScalarType type = x.scalar_type();
-    at::Tensor total;
-    if (res || p != 0.0) total = empty(x.sizes(), type);
-    at::Tensor y = empty(x.sizes(), type);
-    const at::IntArrayRef lead = x.sizes().slice(0, x.dim() - 1);
-    at::Tensor mean = empty(lead, at::kFloat), rstd = empty(lead, at::kFloat);
-    const muon_status st = p_layer_norm(
-        r.rows, r.cols, dt, wdt, x.const_data_ptr(), r.ld, res ? res->const_data_ptr() : nullptr, ldr,
-        pw, pb, (float)eps, (float)p, seed, offset,
-        total.defined() ? total.mutable_data_ptr() : nullptr, y.mutable_data_ptr(),
-        static_cast<float*>(mean.mutable_data_ptr()), static_cast<float*>(rstd.mutable_data_ptr()),
-        stream);
+    at::Tensor total, y, mean, rstd;
+    muon_status st;
+    {
+      const Unlocked unlocked;
+      if (res || p != 0.0) total = empty(x.sizes(), type);
+      y = empty(x.sizes(), type);
+      const at::IntArrayRef lead = x.sizes().slice(0, x.dim() - 1);
+      mean = empty(lead, at::kFloat);
+      rstd = empty(lead, at::kFloat);
+      st = p_layer_norm(
+          r.rows, r.cols, dt, wdt, x.const_data_ptr(), r.ld, res ? res->const_data_ptr() : nullptr, ldr,
+          pw, pb, (float)eps, (float)p, seed, offset,
+          total.defined() ? total.mutable_data_ptr() : nullptr, y.mutable_data_ptr(),
+          static_cast<float*>(mean.mutable_data_ptr()), static_cast<float*>(rstd.mutable_data_ptr()),
+          stream);
+    }
     if (st != MUON_OK) return PyLong_FromLong(st);
     return tuple_of({wrap(std::move(y)), total.defined() ? wrap(std::move(total)) : none(),
                      wrap(std::move(mean)), wrap(std::move(rstd))});
@@ -276,22 +290,25 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* pw = vector_of(w, r.cols, dy, "weight");
     void* stream = stream_of(dy);
     const int64_t ldd = ds ? same_rows(*ds, dy, "dsum") : 0;
-    at::Tensor dx = empty(dy.sizes(), type), dres, dw, db, ws;
-    if (p != 0.0) dres = empty(dy.sizes(), type);
+    at::Tensor dx, dres, dw, db, ws;
     size_t bytes = 0;
-    if (need_w || need_b) {
-      const muon_status st = p_layer_norm_workspace_bytes(r.rows, r.cols, &bytes);
-      if (st != MUON_OK) return PyLong_FromLong(st);
+    muon_status st = MUON_OK;
+    if (need_w || need_b) st = p_layer_norm_workspace_bytes(r.rows, r.cols, &bytes);
+    if (st != MUON_OK) return PyLong_FromLong(st);
+    {
+      const Unlocked unlocked;
+      dx = empty(dy.sizes(), type);
+      if (p != 0.0) dres = empty(dy.sizes(), type);
       if (need_w) dw = empty({r.cols}, wtype);
       if (need_b) db = empty({r.cols}, wtype);
-      ws = empty({(int64_t)bytes}, at::kByte);
+      if (need_w || need_b) ws = empty({(int64_t)bytes}, at::kByte);
+      auto ptr = [](at::Tensor& t) { return t.defined() ? t.mutable_data_ptr() : nullptr; };
+      st = p_layer_norm_backward(
+          r.rows, r.cols, dt, wdt, dy.const_data_ptr(), r.ld, sum.const_data_ptr(), lds,
+          static_cast<const float*>(mean.const_data_ptr()),
+          static_cast<const float*>(rstd.const_data_ptr()), pw, ds ? ds->const_data_ptr() : nullptr, ldd,
+          (float)p, seed, offset, ptr(dx), ptr(dres), ptr(dw), ptr(db), ptr(ws), bytes, stream);
     }
-    auto ptr = [](at::Tensor& t) { return t.defined() ? t.mutable_data_ptr() : nullptr; };
-    const muon_status st = p_layer_norm_backward(
-        r.rows, r.cols, dt, wdt, dy.const_data_ptr(), r.ld, sum.const_data_ptr(), lds,
-        static_cast<const float*>(mean.const_data_ptr()),
-        static_cast<const float*>(rstd.const_data_ptr()), pw, ds ? ds->const_data_ptr() : nullptr, ldd,
-        (float)p, seed, offset, ptr(dx), ptr(dres), ptr(dw), ptr(db), ptr(ws), bytes, stream);
     if (st != MUON_OK) return PyLong_FromLong(st);
     auto out = [](at::Tensor& t) { return t.defined() ? wrap(std::move(t)) : none(); };
     return tuple_of({out(dx), out(dres), out(dw), out(db)});
@@ -323,12 +340,14 @@ PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
       // what autograd has saved of it is no longer what it saw
       given->unsafeGetTensorImpl()->bump_version();
       y = *given;
-    } else {
-      y = empty(x.sizes(), type);
     }
-    const muon_status st = p_dropout(x.numel(), dt, x.const_data_ptr(),
-                                     res ? res->const_data_ptr() : nullptr, (float)p, seed, offset,
-                                     y.mutable_data_ptr(), stream);
+    muon_status st;
+    {
+      const Unlocked unlocked;
+      if (!given) y = empty(x.sizes(), type);
+      st = p_dropout(x.numel(), dt, x.const_data_ptr(), res ? res->const_data_ptr() : nullptr, (float)p,
+                     seed, offset, y.mutable_data_ptr(), stream);
+    }
     if (st != MUON_OK) return PyLong_FromLong(st);
     if (given) {
       Py_INCREF(a[5]);
@@ -363,18 +382,24 @@ PyObject* route_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     muon_status st = k < 1 ? MUON_ERR_INVALID_ARG : k > experts ? MUON_ERR_UNSUPPORTED_SHAPE
                            : p_route_workspace_bytes(r.rows, experts, &bytes);
     if (st != MUON_OK) return PyLong_FromLong(st);
-    at::Tensor ws = empty({(int64_t)bytes}, at::kByte);
     c10::SmallVector<int64_t, 6> shape(l.sizes().begin(), l.sizes().end());
     shape.back() = k;
-    at::Tensor weights = empty(shape, at::kFloat), index = empty(shape, at::kInt);
-    at::Tensor counts = empty({experts + 1}, at::kInt), mean_prob = empty({experts}, at::kFloat);
-    at::Tensor loss = empty({}, at::kFloat);
-    st = p_route(r.rows, experts, k, dt, l.const_data_ptr(), r.ld, pm, normalize,
-                 static_cast<float*>(weights.mutable_data_ptr()),
-                 static_cast<int32_t*>(index.mutable_data_ptr()),
-                 static_cast<int32_t*>(counts.mutable_data_ptr()),
-                 static_cast<float*>(mean_prob.mutable_data_ptr()),
-                 static_cast<float*>(loss.mutable_data_ptr()), ws.mutable_data_ptr(), bytes, stream);
+    at::Tensor ws, weights, index, counts, mean_prob, loss;
+    {
+      const Unlocked unlocked;
+      ws = empty({(int64_t)bytes}, at::kByte);
+      weights = empty(shape, at::kFloat);
+      index = empty(shape, at::kInt);
+      counts = empty({experts + 1}, at::kInt);
+      mean_prob = empty({experts}, at::kFloat);
+      loss = empty({}, at::kFloat);
+      st = p_route(r.rows, experts, k, dt, l.const_data_ptr(), r.ld, pm, normalize,
+                   static_cast<float*>(weights.mutable_data_ptr()),
+                   static_cast<int32_t*>(index.mutable_data_ptr()),
+                   static_cast<int32_t*>(counts.mutable_data_ptr()),
+                   static_cast<float*>(mean_prob.mutable_data_ptr()),
+                   static_cast<float*>(loss.mutable_data_ptr()), ws.mutable_data_ptr(), bytes, stream);
+    }
     if (st != MUON_OK) return PyLong_FromLong(st);
     return tuple_of({wrap(std::move(weights)), wrap(std::move(index)), wrap(std::move(counts)),
                      wrap(std::move(mean_prob)), wrap(std::move(loss))});
@@ -406,13 +431,18 @@ PyObject* route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         value_error("dweights must have the shape of index, or its rows in two dimensions or one");
     }
     const uint8_t* pm = mask_of(mask, r.rows, l);
-    at::Tensor out = empty(l.sizes(), l.scalar_type());
-    const muon_status st = p_route_backward(
-        r.rows, (int)r.cols, (int)k, dt, l.const_data_ptr(), r.ld, pm, normalize,
-        static_cast<const int32_t*>(index.const_data_ptr()),
-        static_cast<const int32_t*>(counts.const_data_ptr()),
-        dw ? static_cast<const float*>(dw->const_data_ptr()) : nullptr,
-        dl ? static_cast<const float*>(dl->const_data_ptr()) : nullptr, out.mutable_data_ptr(), stream);
+    at::Tensor out;
+    muon_status st;
+    {
+      const Unlocked unlocked;
+      out = empty(l.sizes(), l.scalar_type());
+      st = p_route_backward(
+          r.rows, (int)r.cols, (int)k, dt, l.const_data_ptr(), r.ld, pm, normalize,
+          static_cast<const int32_t*>(index.const_data_ptr()),
+          static_cast<const int32_t*>(counts.const_data_ptr()),
+          dw ? static_cast<const float*>(dw->const_data_ptr()) : nullptr,
+          dl ? static_cast<const float*>(dl->const_data_ptr()) : nullptr, out.mutable_data_ptr(), stream);
+    }
     if (st != MUON_OK) return PyLong_FromLong(st);
     return wrap(std::move(out));
   });

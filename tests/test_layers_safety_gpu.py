@@ -1,5 +1,9 @@
 """What a call of the training operators may do to tensors, threads and memory
 around it."""
+import ctypes
+import threading
+import time
+
 import pytest
 import torch
 
@@ -81,3 +85,36 @@ def test_every_result_has_memory_of_its_own(layers):
         assert len({s.data_ptr() for s in storages}) == len(out)
         for t, s in zip(out, storages):
             assert s.nbytes() == t.numel() * t.element_size() and t.storage_offset() == 0
+
+
+def test_other_threads_run_while_a_call_is_in_the_library(layers):
+    # the library's entry point replaced by the C library's usleep, which takes the
+    # number of elements for microseconds and returns 0 (no error)
+    binding = layers._b()
+    lib = muon().load()
+    names = ("muon_layer_norm", "muon_layer_norm_backward", "muon_layer_norm_workspace_bytes",
+             "muon_dropout", "muon_route", "muon_route_workspace_bytes", "muon_route_backward")
+    real = {n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}
+    sleep = ctypes.cast(ctypes.CDLL(None).usleep, ctypes.c_void_p).value
+    x = torch.zeros(500000, device="cuda")
+    out = torch.empty_like(x)
+    ticks, stop = [], threading.Event()
+
+    def tick():
+        while not stop.is_set():
+            ticks.append(time.perf_counter())
+            time.sleep(0.005)
+
+    thread = threading.Thread(target=tick)
+    binding.bind(dict(real, muon_dropout=sleep))
+    try:
+        thread.start()
+        begin = time.perf_counter()
+        layers.dropout_forward(x, 0.5, seed=1, out=out)
+        end = time.perf_counter()
+    finally:
+        stop.set()
+        thread.join()
+        binding.bind(real)
+    assert end - begin >= 0.4                       # the call did wait ...
+    assert sum(begin + 0.05 < t < end - 0.05 for t in ticks) >= 10      # ... and the thread ran
