@@ -19,7 +19,8 @@ dense and whose leading dimensions are rows at one stride.  Calls run on the
 current stream, or on `stream`: then outputs belong to that stream, and the
 caller orders it after whatever produced the inputs.  Nothing is kept between
 calls.  Dropout takes an explicit `seed` and `offset`; RandomCounter hands out
-offsets that never overlap.
+offsets that never overlap.  A captured CUDA graph replays the seed and offset it
+was captured with: the same elements are dropped at every replay.
 """
 from __future__ import annotations
 
@@ -61,12 +62,22 @@ class RouteOut(NamedTuple):
 
 class RandomCounter:
     """Offsets of dropout calls that share a seed: take(n) returns the offset
-    of a call over n elements and moves past the counters it uses."""
+    of a call over n elements and moves past the counters it uses.
+
+    Under activation checkpointing the forward pass runs again during the
+    backward pass and must drop the same elements, so its offsets are taken
+    outside of the checkpointed function and passed in.  take() raises where it
+    is called during a backward pass: the offset would be another than the first
+    run's, and the gradients wrong without a sign of it."""
 
     def __init__(self, seed: int, offset: int = 0):
         self.seed, self.offset = seed, offset
 
     def take(self, numel: int) -> int:
+        if torch._C._current_graph_task_id() != -1:
+            raise RuntimeError("RandomCounter.take() in a backward pass: a recomputed forward pass "
+                               "would drop other elements than the first run; take the offset outside "
+                               "of the checkpointed function and pass it in")
         at = self.offset
         self.offset += (numel + 7) // 8
         return at
