@@ -32,7 +32,8 @@ from typing import NamedTuple, Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _PKG, _check, load
+from . import _check, load
+from .build import binding_path
 
 __all__ = ["layer_norm", "dropout_add_layer_norm", "dropout", "route", "RandomCounter",
            "layer_norm_forward", "layer_norm_backward", "dropout_forward", "dropout_backward",
@@ -92,9 +93,9 @@ def _b():
     global _bound
     if _bound is None:
         lib = load()
-        path = os.path.join(_PKG, "_binding.so")
+        path = binding_path()
         if not os.path.exists(path):
-            raise RuntimeError("_binding.so not built at %s: run newton_schulz_05_gb300.build.build()"
+            raise RuntimeError("the binding is not built at %s: run newton_schulz_05_gb300.build.build()"
                                % path)
         spec = importlib.util.spec_from_file_location(__package__ + "._binding", path)
         module = importlib.util.module_from_spec(spec)
