@@ -6,9 +6,10 @@ import ctypes
 import pytest
 import torch
 
+import layers_ref as ref
 from helpers import muon
 from test_norm_gpu import (BF, EPS, F32, check_backward, check_forward, draw, layers,  # noqa: F401
-                           placed)
+                           near, placed)
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +83,15 @@ def test_gradient_of_large_constant_rows(layers, dtype, cols):  # noqa: F811
     check_backward(layers, draw((rows, cols), dtype, 4, 0.1), s, mean, rstd, w,
                    draw((rows, cols), dtype, 6, 0.1), 0.25)
     check_backward(layers, placed(draw((rows, cols), dtype, 4, 0.1), 3, 1), s, mean, rstd, w, None, 0.0)
+
+
+# sums of these are exact in fp32, so the mean is the value itself and y the bias
+@pytest.mark.parametrize("cols", [3, 49, 63, 333, 1000, 1023, 3001, 4099, 10240, 16383])
+@pytest.mark.parametrize("value", [3.0, 1000.0, -640.0])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_constant_rows_give_the_bias(layers, dtype, value, cols):  # noqa: F811
+    x = torch.full((5, cols), value, device="cuda", dtype=dtype)
+    w, b = draw(cols, dtype, 2, 0.3, 1.0), draw(cols, dtype, 3)
+    o = layers.layer_norm_forward(x, w, b, eps=EPS)
+    assert bool((o.mean == value).all()) and torch.equal(o.y, b.expand(5, cols))
+    near(o.rstd, ref.f64(torch.full((5,), EPS).double()) ** -0.5, 1e-3, F32)
