@@ -1,6 +1,7 @@
 """Layer norm and its gradient at numbers of rows and widths where the row
 groups of a block differ: one and two rows just below the widths of each
-layout, against the 64-bit host reference with the bounds of layers_ref."""
+layout, and many rows a group, against the 64-bit host reference with the
+bounds of layers_ref."""
 import ctypes
 
 import pytest
@@ -67,6 +68,32 @@ def test_one_row_of_any_stride(layers, dtype, cols, ld):  # noqa: F811
     torch.cuda.synchronize()
     for got, exact in ((dx, want.dx), (dw, want.dweight), (db, want.dbias), (y, o.y)):
         assert torch.equal(got, exact)
+
+
+# several rows a row group: the ring wraps, the warps' slots are used again, and
+# a thread adds up columns over its rows
+@pytest.mark.parametrize("rows,cols", [(40000, 24), (20000, 61), (6000, 200), (6000, 397), (3000, 512),
+                                       (6000, 1023), (3000, 1024), (3000, 1500), (1500, 2999),
+                                       (1500, 4096), (1000, 6001), (700, 8192), (500, 11008),
+                                       (400, 16384), (350, 16001), (700, 17000)])
+@pytest.mark.parametrize("dtype,p", [(BF, 0.0), (F32, 0.0), (BF, 0.2), (F32, 0.2)])
+def test_many_rows_a_group(layers, rows, cols, dtype, p):  # noqa: F811
+    x, dy = draw((rows, cols), dtype, 1, 1.3, 0.4), draw((rows, cols), dtype, 4, 0.1)
+    w, b = draw(cols, dtype, 2, 0.3, 1.0), draw(cols, F32, 3, 0.2).to(dtype)
+    r, ds = (draw((rows, cols), dtype, i) if p else None for i in (5, 6))
+    o = check_forward(layers, x, r, w, b, p)
+    check_backward(layers, dy, o.sum, o.mean, o.rstd, w, ds, p)
+
+
+@pytest.mark.parametrize("pads,leads", [((8, 8), (0, 0)), ((7, 7), (0, 0)), ((7, 0), (0, 0)), ((0, 0), (1, 3))])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_many_rows_of_other_strides(layers, dtype, pads, leads):  # noqa: F811
+    rows, cols = 2500, 1409
+    x, r = (placed(draw((rows, cols), dtype, i), pads[0], leads[0]) for i in (1, 5))
+    dy = placed(draw((rows, cols), dtype, 4, 0.1), pads[1], leads[1])
+    w, b = draw(cols, F32, 2, 0.3, 1.0), draw(cols, F32, 3)
+    o = check_forward(layers, x, r, w, b, 0.0)
+    check_backward(layers, dy, placed(o.sum, pads[0], leads[0]), o.mean, o.rstd, w, None, 0.0)
 
 
 # h = (sum - mean) rstd is 0 in a constant row, however large mean * rstd is
