@@ -268,10 +268,11 @@ cudaError_t forward(const NormFwd& a, int64_t chunks, cudaStream_t s) {
     if (chunks <= 256) return launch_fwd<T, 0, 1, 256, FUSED, REG>(a, s);
     if (chunks <= 384) return launch_fwd<T, 0, 1, 384, FUSED, REG>(a, s);
     if (chunks <= 512) return launch_fwd<T, 0, 1, 512, FUSED, REG>(a, s);
+  } else {
+    if (chunks <= 256) return launch_fwd<T, 0, 2, 128, FUSED, REG>(a, s);
+    if (chunks <= 384) return launch_fwd<T, 0, 2, 192, FUSED, REG>(a, s);
+    if (chunks <= 512) return launch_fwd<T, 0, 2, 256, FUSED, REG>(a, s);
   }
-  if (chunks <= 256) return launch_fwd<T, 0, 2, 128, FUSED, REG>(a, s);
-  if (chunks <= 384) return launch_fwd<T, 0, 2, 192, FUSED, REG>(a, s);
-  if (chunks <= 512) return launch_fwd<T, 0, 2, 256, FUSED, REG>(a, s);
   if (chunks <= 768) return launch_fwd<T, 0, 2, 384, FUSED, REG>(a, s);
   if (chunks <= 1024) return launch_fwd<T, 0, 2, 512, FUSED, REG>(a, s);
   if (chunks <= 1408) return launch_fwd<T, 0, 2, 704, FUSED, REG>(a, s);

@@ -444,10 +444,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_cols_kernel(const __grid_co
 
 // --------------------------------------------------------------------- host
 
-// partial column sums of a gradient, whatever the phases of its operands
-int64_t norm_parts(int64_t rows, int64_t cols) {
-  return rows < kLongParts ? rows : kLongParts;
-}
+// partial column sums of a gradient, whatever its width and the phases of its operands
+int64_t norm_parts(int64_t rows) { return rows < kLongParts ? rows : kLongParts; }
 
 template <typename T, int TPR, int C, int W, bool FUSED, bool KEEP, bool REG>
 cudaError_t launch_bwd(const NormBwd& a, int* parts, cudaStream_t s) {
@@ -514,7 +512,7 @@ using namespace muon;
 extern "C" muon_status muon_layer_norm_workspace_bytes(int64_t rows, int64_t cols, size_t* out) {
   if (!out || rows < 0) return MUON_ERR_INVALID_ARG;
   if (cols < 1 || cols > (int64_t)1 << 30) return MUON_ERR_UNSUPPORTED_SHAPE;
-  *out = (size_t)norm_parts(rows, cols) * 2 * (size_t)cols * sizeof(float) + 256;
+  *out = (size_t)norm_parts(rows) * 2 * (size_t)cols * sizeof(float) + 256;
   return MUON_OK;
 }
 
@@ -565,20 +563,21 @@ extern "C" muon_status muon_layer_norm_backward(
                      wdtype == MUON_BF16, !misaligned(weight, 16), drop_threshold(p) > 0,
                      make_drop(p, seed, offset)};
   cudaError_t e;
-  int parts = (int)(rows < kLongParts ? rows : kLongParts);
+  int parts = (int)norm_parts(rows);
   bool joined = false;
   if (!ph.same || ph.chunks() > kMaxChunks) {
     const int64_t tiles = (cols + kNormThreads - 1) / kNormThreads;
     e = by_types(dtype, wdtype, [&](auto t, auto wt) {
       using T = decltype(t);
       using WT = decltype(wt);
+      cudaError_t e = cudaSuccess;
       if (dx || dresidual)
-        launch_k(ph.eights() ? norm_long_bwd_kernel<T, WT, true> : norm_long_bwd_kernel<T, WT, false>,
-                 dim3((unsigned)blocks_for(rows, 1, 4)), dim3(kNormThreads), 0, s, false, a);
-      if (cols_wanted)
-        norm_cols_kernel<T><<<dim3(parts, (unsigned)(tiles < 65535 ? tiles : 65535)), kNormThreads,
-                              0, s>>>(a);
-      return cudaGetLastError();
+        e = launch_k(ph.eights() ? norm_long_bwd_kernel<T, WT, true> : norm_long_bwd_kernel<T, WT, false>,
+                     dim3((unsigned)blocks_for(rows, 1, 4)), dim3(kNormThreads), 0, s, false, a);
+      if (cols_wanted && e == cudaSuccess)
+        e = launch_k(norm_cols_kernel<T>, dim3(parts, (unsigned)(tiles < 65535 ? tiles : 65535)),
+                     dim3(kNormThreads), 0, s, false, a);
+      return e;
     });
   } else {
     e = dtype == MUON_BF16 ? backward<__nv_bfloat16>(a, ph, fused, &parts, s)

@@ -314,30 +314,31 @@ template <typename T, int G, int NCH, bool VEC> struct Logits {
 };
 
 // The end of a forward block: its probabilities (`sums` rows of `stride` floats
-// to add up in order), counts sc and n routed tokens become its partial sums, or
-// the results where it is the only block.  The whole block calls it, after a
-// barrier.
+// to add up in order), counts sc and n routed tokens become its partial sums.  The
+// whole block calls it, after a barrier.
 __device__ __forceinline__ void finish(const RouteFwd& a, const float* sums, int rows, int stride,
                                        const int* sc, int n) {
-  __shared__ float red[kRouteWarps];
-  const float fn = (float)(n > 0 ? n : 1);
-  float l = 0.f;
   for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
     float p = 0.f;
     for (int i = 0; i < rows; ++i) p += sums[i * stride + e];
-    if (gridDim.x > 1) {
-      a.part_p[(int64_t)blockIdx.x * a.experts + e] = p;
-      a.part_c[(int64_t)blockIdx.x * (a.experts + 1) + e] = sc[e];
-    } else {
-      p /= fn;
-      a.counts[e] = sc[e];
-      a.mean_prob[e] = p;
-      l = fmaf((float)sc[e] / ((float)a.k * fn), p, l);
-    }
+    a.part_p[(int64_t)blockIdx.x * a.experts + e] = p;
+    a.part_c[(int64_t)blockIdx.x * (a.experts + 1) + e] = sc[e];
   }
-  if (gridDim.x > 1) {
-    if (threadIdx.x == 0) a.part_c[(int64_t)blockIdx.x * (a.experts + 1) + a.experts] = n;
-    return;
+  if (threadIdx.x == 0) a.part_c[(int64_t)blockIdx.x * (a.experts + 1) + a.experts] = n;
+}
+// The same where the block, of kRouteThreads, is the only one: they become the results.
+__device__ __forceinline__ void finish_alone(const RouteFwd& a, const float* sums, int rows, int stride,
+                                             const int* sc, int n) {
+  __shared__ float red[kRouteWarps];
+  const float fn = (float)(n > 0 ? n : 1);
+  float l = 0.f;
+  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) {
+    float p = 0.f;
+    for (int i = 0; i < rows; ++i) p += sums[i * stride + e];
+    p /= fn;
+    a.counts[e] = sc[e];
+    a.mean_prob[e] = p;
+    l = fmaf((float)sc[e] / ((float)a.k * fn), p, l);
   }
   l = block_sum<kRouteThreads>(l, red);
   if (threadIdx.x == 0) {
@@ -461,7 +462,8 @@ route_kernel(const __grid_constant__ RouteFwd a) {
     }
     __syncthreads();
   }
-  finish(a, &sp[0][0], kRows, E, sc, sc[E]);
+  if (gridDim.x > 1) finish(a, &sp[0][0], kRows, E, sc, sc[E]);
+  else finish_alone(a, &sp[0][0], kRows, E, sc, sc[E]);
 }
 
 // Many tokens: a lane a token.  A warp copies 32 rows, 128 bytes of each at a
@@ -975,6 +977,7 @@ int lanes_of(int experts) {
 // against 25.0 at 131072; 256 experts, k = 8, fp32 28 against 20 at 16384 and 38
 // against 33 at 32768; 160 experts at 65537 42 against 60.
 constexpr int64_t kRowsTokens = 49152;
+static_assert((kRowsTokens + 31) / 32 > kRouteWarps, "the lane-a-token form has several blocks");
 
 // blocks of a pass: a warp for every token group, up to two blocks an SM (the
 // lane-a-token form has fewer groups)
