@@ -260,7 +260,10 @@ norm_bwd_kernel(const __grid_constant__ NormBwd a) {
           if (a.dresidual)
             put<T, REG>(static_cast<T*>(a.dresidual) + out + c0[k], d, in[k]);
           // without a branch the generator blocks of a thread's pieces overlap: [8192,
-          // 4096] bf16 58.5 against 60.1 us, fp32 115.4 against 124.2
+          // 4096] bf16 58.5 against 60.0 us, fp32 114.8 against 123.8; the long forms
+          // [3276, 10240] 78.4 against 85.3, 128.5 against 129.9, [2048, 16384] 98.8
+          // against 101.1, 166.0 against 168.0; from 64 columns on none is slower by
+          // more than 1%
           if (a.drop) drop<E, REG>(d.v, out + c0[k], a.d);
         }
         if (a.dx) put<T, REG>(static_cast<T*>(a.dx) + out + c0[k], d, in[k]);
@@ -469,14 +472,18 @@ cudaError_t backward(const NormBwd& a, int64_t chunks, int* parts, cudaStream_t 
     if constexpr (FUSED) return launch_bwd<T, 0, 1, 64, FUSED, true, REG>(a, parts, s);
     else return launch_bwd<T, 32, 2, 0, FUSED, true, REG>(a, parts, s);
   }
-  // ragged fp32 rows of sixteen elements a thread spill: eight ([9000, 3001] 104
-  // against 164 us), unless there are few rows and more groups a block count for
-  // more ([517, 1023] 8.7 against 7.0 us)
-  if (!REG && sizeof(T) == 4 && a.rows > 16 * kSMs) {
-    if (chunks <= 128) return launch_bwd<T, 0, 1, 128, FUSED, true, REG>(a, parts, s);
-    if (chunks <= 160) return launch_bwd<T, 0, 1, 160, FUSED, true, REG>(a, parts, s);
-    if (chunks <= 256) return launch_bwd<T, 0, 1, 256, FUSED, true, REG>(a, parts, s);
-    if (chunks <= 512) return launch_bwd<T, 0, 1, 512, FUSED, true, REG>(a, parts, s);
+  // Ragged fp32 rows with dsum or dropout: sixteen elements a thread spill, so eight
+  // ([9000, 3001] p .1 107.6 against 126.9 us, dsum alone 81.2 against 96.8; [1000, 1023]
+  // 13.0 against 14.7, 11.2 against 12.4), unless there are few rows and more groups a
+  // block count for more ([517, 1023] 10.5 against 9.0, 8.8 against 7.6).  Without them
+  // sixteen fit ([9000, 3001] 57.5 against 68.1, [2000, 3001] 20.7 against 22.6).
+  if constexpr (!REG && sizeof(T) == 4 && FUSED) {
+    if (a.rows > 4 * kSMs) {
+      if (chunks <= 128) return launch_bwd<T, 0, 1, 128, FUSED, true, REG>(a, parts, s);
+      if (chunks <= 160) return launch_bwd<T, 0, 1, 160, FUSED, true, REG>(a, parts, s);
+      if (chunks <= 256) return launch_bwd<T, 0, 1, 256, FUSED, true, REG>(a, parts, s);
+      if (chunks <= 512) return launch_bwd<T, 0, 1, 512, FUSED, true, REG>(a, parts, s);
+    }
   }
   if (chunks <= 128) return launch_bwd<T, 0, 2, 64, FUSED, true, REG>(a, parts, s);
   if (chunks <= 192) return launch_bwd<T, 0, 2, 96, FUSED, true, REG>(a, parts, s);
