@@ -1,7 +1,7 @@
 // Layer norm, alone or behind dropout and the residual add: the forward pass.
 //
-// Measured: [16384, 4096] bf16 45 us, 5.9 TB/s of x and y (41 us, 6.6 TB/s, of the
-// kernel alone); behind dropout and the residual add [8192, 10240] 117 us, 5.75 TB/s;
+// Measured: [16384, 4096] bf16 44.6 us, 6.0 TB/s of x and y (41.8 us, 6.4 TB/s, of the
+// kernel alone); behind dropout and the residual add [8192, 10240] 118 us, 5.7 TB/s;
 // [4096, 10240] fp32 54 us, 6.2 TB/s; [9000, 3001] fp32 36 us, 5.9 TB/s; one row
 // 2.5 us.  16-bit rows behind dropout are bound by instructions, 30 an element.
 #include "norm.cuh"
@@ -112,9 +112,9 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
         take<T, REG>(v[k], from + k * nt, in[k], k == 0, front);
         if constexpr (FUSED) {
           // without a branch the generator blocks of a thread's pieces overlap, where
-          // there are registers for it: [8192, 10240] bf16 116.7 against 126.7 us,
-          // [8192, 4096] fp32 91.8 against 92.9, [65536, 256] fp32 48.1 against 49.8; but
-          // [4096, 16384] bf16 118.6 against 97.2, [4096, 10240] fp32 116.6 against 108.2
+          // there are registers for it: [8192, 10240] bf16 117.9 against 127.0 us,
+          // [8192, 4096] fp32 92.7 against 93.7, [65536, 256] fp32 49.2 against 50.8; but
+          // [4096, 16384] bf16 108.0 against 97.1, [4096, 10240] fp32 116.4 against 108.4
           if (a.drop)
             drop<E, REG && NT <= (sizeof(T) == 2 ? 704 : 512)>(v[k].v, out + c0[k], a.d);
           if (res) {
@@ -131,10 +131,14 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
       #pragma unroll
       for (int j = 0; j < E / 2; ++j) s2 = add2(s2, v[k].v[j]);
     }
-    // divided: times a rounded 1 / cols the mean of a constant row of 1000 was off by
-    // its last bit and y by 0.02.  [65536, 512] p .1 47.1 against 45.5 us, [16384, 4096]
-    // 44.3 against 45.0, others within 2%
-    const float mean = row_sum<TPR, sizeof(T) == 2>(s2.x + s2.y, slots[0], nt >> 5) / (float)cols;
+    // The mean: the sum times a rounded 1 / cols, and one step of iterative refinement
+    // by what that leaves of the sum (nothing to refine where the sum is infinite).
+    // Without it the mean of a constant row of 1000 was off by its last bit and y by
+    // 0.02; a division cost [32768, 1024] bf16 26.3 against 25.3 us
+    // (24.9 without either).
+    const float total = row_sum<TPR, sizeof(T) == 2>(s2.x + s2.y, slots[0], nt >> 5);
+    const float near = total * inv, left = fmaf(-near, (float)cols, total);
+    const float mean = fabsf(left) < INFINITY ? fmaf(left, inv, near) : near;
     const float2 m2 = both(-mean);
     float2 q2 = both(0.f);
     #pragma unroll
@@ -148,6 +152,7 @@ norm_fwd_kernel(const __grid_constant__ NormFwd a) {
         for (int j = 0; j < E / 2; ++j) q2 = fma2(v[k].v[j], v[k].v[j], q2);
       }
     }
+    // rsqrtf is within two units of its last place, the sum within a few of its own
     const float rstd = rsqrtf(row_sum<TPR, sizeof(T) == 2>(q2.x + q2.y, slots[1], nt >> 5) * inv + a.eps);
     if (live) {
       const float2 r2 = both(rstd);
@@ -249,10 +254,12 @@ cudaError_t launch_fwd(const NormFwd& a, cudaStream_t s) {
 }
 
 // Rows of up to 64 columns take 8 lanes, of up to 512 a warp ([100000, 400] bf16
-// 26.8 against 35.1 us with two, but behind dropout [65536, 512] 60.3 against
+// 28.0 against 35.1 us with two, but behind dropout [65536, 512] 60.3 against
 // 47.1), longer ones a block of the next size compiled in: eight elements a thread
-// up to 1536 columns (ragged fp32 4096: [9000, 3001] 39.8 against 58.5 us), sixteen
-// beyond.
+// up to 1536 columns, sixteen beyond.  Ragged fp32 keeps eight up to 4096: one row of
+// 3001 2.4 against 2.6 us, 500 rows 5.2 against 5.9, 9000 36.1 against 37.7, behind
+// dropout 2.9, 8.2 and 73.8 against 3.6, 8.9 and 76.9; near the end of its block
+// sixteen are faster ([9000, 4093] 53.0 against 58.1, behind dropout 97.3 against 110.8).
 template <typename T, bool FUSED, bool REG>
 cudaError_t forward(const NormFwd& a, int64_t chunks, cudaStream_t s) {
   if (chunks <= 8) return launch_fwd<T, 8, 1, 256, FUSED, REG>(a, s);
@@ -264,7 +271,7 @@ cudaError_t forward(const NormFwd& a, int64_t chunks, cudaStream_t s) {
   if (chunks <= 128) return launch_fwd<T, 0, 1, 128, FUSED, REG>(a, s);
   if (chunks <= 160) return launch_fwd<T, 0, 1, 160, FUSED, REG>(a, s);
   if (chunks <= 192) return launch_fwd<T, 0, 1, 192, FUSED, REG>(a, s);
-  if constexpr (!REG && sizeof(T) == 4) {      // sixteen elements would spill
+  if constexpr (!REG && sizeof(T) == 4) {
     if (chunks <= 256) return launch_fwd<T, 0, 1, 256, FUSED, REG>(a, s);
     if (chunks <= 384) return launch_fwd<T, 0, 1, 384, FUSED, REG>(a, s);
     if (chunks <= 512) return launch_fwd<T, 0, 1, 512, FUSED, REG>(a, s);

@@ -18,8 +18,8 @@
 // weights stay in registers and the column sums of the gradient accumulate
 // there.  Operands whose phases differ, or whose first row is not aligned, take the
 // kernels for rows longer than a block holds, which move single elements then:
-// 12 to 14% of the copy rate at 16381 columns, 24 to 42% for long rows of whole
-// eights.
+// 12 to 13% of the copy rate at 16381 bf16 columns, 22 to 42% for long rows of
+// whole eights.
 //
 // Rows stream through a ring of asynchronous copies into shared memory.  Each
 // thread copies, waits for and reads only its own pieces, so the ring needs no
@@ -172,9 +172,10 @@ __device__ __forceinline__ void columns(Piece<kEl<T>>& v, const void* w, int bf1
 // same value in each; slots: one float a warp, zeros past the last.
 // SHORT: the warps' sums are added by shuffles, in fewer instructions but more
 // latency than four at a time from shared memory.  It pays for 16-bit rows, which
-// have the more instructions a byte, of more than 16 warps: [4096, 11008] 33.9
-// against 37.8 us, [4096, 16384] 54.0 against 64.2; at 16 warps 55.0 against 53.2,
-// for fp32 [4096, 10240] 56.7 against 53.7.
+// have the more instructions a byte, of more than 16 warps: [4096, 11008] 36.1
+// against 39.0 us, [4096, 16384] 50.5 against 63.3, [8192, 10240] behind dropout 118
+// against 125; at 16 warps ([8192, 8192]) 54.2 against 53.0, for fp32 [4096, 10240]
+// 56.7 against 53.3.
 template <int TPR, bool SHORT>
 __device__ __forceinline__ float row_sum(float v, float* slots, int warps) {
   #pragma unroll

@@ -9,7 +9,7 @@
 //
 // Measured: [16384, 4096] bf16 71 us, 5.7 TB/s of dy, sum and dx (67 us here, 4 in
 // the join); with dropout and dsum [8192, 4096] 58 us, 5.7 TB/s; [8192, 4096] fp32
-// 67 us, 6.0 TB/s; [9000, 3001] fp32 68 us, 4.8 TB/s.  16-bit rows are bound by
+// 64 us, 6.3 TB/s; [9000, 3001] fp32 57 us, 5.6 TB/s.  16-bit rows are bound by
 // instructions at sixteen warps an SM (the column sums take the registers of more):
 // 18 an element, 35 with the random bits.
 #include "norm.cuh"

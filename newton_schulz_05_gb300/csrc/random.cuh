@@ -90,8 +90,8 @@ __device__ __forceinline__ uint4 drop_bits(int64_t i, const Drop& d) {
 template <int E, bool ALIGNED>
 __device__ __forceinline__ void drop(float2 (&v)[E / 2], int64_t i, const Drop& d) {
   // p = 1.  The comparison below drops everything by itself; the branch keeps the
-  // pieces' blocks apart where registers are short: layer norm of [4096, 16384] bf16
-  // 97.2 us against 102.0 without it, of [4096, 10240] fp32 108.2 against 114.6
+  // pieces' blocks apart where registers are short: layer norm of [4096, 10240] fp32
+  // 108.4 us against 114.9 without it (of [4096, 16384] bf16 97.1 against 95.0)
   if (!ALIGNED && d.limit == 0xffffffffu) {
     #pragma unroll
     for (int j = 0; j < E / 2; ++j) v[j] = both(0.f);

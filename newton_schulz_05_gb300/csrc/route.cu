@@ -14,11 +14,12 @@
 // drops it.  From 48 Ki tokens on a lane takes a whole token instead
 // (route_rows_kernel).
 //
-// Both passes read the logits once from HBM.  The forward pass is bound by the
-// instructions of the choice: [131072, 64] bf16, k = 6, takes 21.2 us where its
-// 23 MB would take 3.4, the integer pipe 53% busy; a join of the blocks' partial
-// sums costs 3 us of that and of every call of more than one block.  The
-// gradient comes nearer HBM: [65537, 160] fp32, k = 8, 18.3 us, 4.8 TB/s.
+// Both passes read the logits once from HBM.  The forward pass of [131072, 64] bf16,
+// k = 6, takes 21.3 us where its 23 MB would take 3.4.  No pipe is full (issue 63%,
+// integer pipe 53%, 38% of the warps active): a lane waits on its own chain of copy,
+// sort and merge; a join of the blocks' partial sums costs 3 us of that and of every
+// call of more than one block.  The gradient comes nearer HBM: [65537, 160] fp32,
+// k = 8, 18.3 us, 4.8 TB/s.
 #include <cmath>
 
 #include "common.cuh"
@@ -106,8 +107,10 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return y;
 }
 
-// exp(v - top): the difference is rounded once, so the relative error is that
-// of the difference, a few units more for 2^x; below 2^-126 the result is 0
+// exp(v - top) as 2^x, x = (v - top) log2 e.  The difference, the product and log2 e
+// are rounded to 24 bits, each of which moves the result by up to |v - top| 2^-24 of
+// itself (bf16 logits: the difference is mostly exact), and 2^x adds two units: 7 units
+// at 8 below the top, 15 at 20 below.  Below 2^-126 the result is 0.
 __device__ __forceinline__ float exp_below(float v, float top) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((v - top) * 1.4426950408889634f));

@@ -122,3 +122,12 @@ def test_constant_rows_give_the_bias(layers, dtype, value, cols):  # noqa: F811
     o = layers.layer_norm_forward(x, w, b, eps=EPS)
     assert bool((o.mean == value).all()) and torch.equal(o.y, b.expand(5, cols))
     near(o.rstd, ref.f64(torch.full((5,), EPS).double()) ** -0.5, 1e-3, F32)
+
+
+@pytest.mark.parametrize("cols", [7, 64, 333, 1024, 4093, 16400])
+def test_mean_of_rows_with_infinities(layers, cols):  # noqa: F811
+    x = draw((4, cols), F32, 1)
+    inf = float("inf")
+    x[0, 3], x[1, 5], x[2, 2], x[2, 4] = inf, -inf, inf, -inf
+    mean = layers.layer_norm_forward(x).mean.tolist()
+    assert mean[0] == inf and mean[1] == -inf and mean[2] != mean[2] and abs(mean[3]) < 2
