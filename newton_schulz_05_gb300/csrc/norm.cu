@@ -1,6 +1,6 @@
 // Layer norm, alone or behind dropout and the residual add: the forward pass.
 //
-// Measured: [16384, 4096] bf16 44.6 us, 6.0 TB/s of x and y (41.8 us, 6.4 TB/s, of the
+// Measured: [16384, 4096] bf16 44.9 us, 6.0 TB/s of x and y (42.6 us, 6.3 TB/s, of the
 // kernel alone); behind dropout and the residual add [8192, 10240] 118 us, 5.7 TB/s;
 // [4096, 10240] fp32 54 us, 6.2 TB/s; [9000, 3001] fp32 36 us, 5.9 TB/s; one row
 // 2.5 us.  16-bit rows behind dropout are bound by instructions, 30 an element.

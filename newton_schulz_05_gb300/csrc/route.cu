@@ -15,7 +15,7 @@
 // (route_rows_kernel).
 //
 // Both passes read the logits once from HBM.  The forward pass of [131072, 64] bf16,
-// k = 6, takes 21.3 us where its 23 MB would take 3.4.  No pipe is full (issue 63%,
+// k = 6, takes 21.3 us where its 23 MB would take 3.4.  No pipe is full (issue 62%,
 // integer pipe 53%, 38% of the warps active): a lane waits on its own chain of copy,
 // sort and merge; a join of the blocks' partial sums costs 3 us of that and of every
 // call of more than one block.  The gradient comes nearer HBM: [65537, 160] fp32,
