@@ -526,6 +526,194 @@ MUON_API muon_status muon_route_backward(int64_t tokens, int experts, int k, int
                                          const int32_t* counts, const float* dweights,
                                          const float* dloss, void* dlogits, void* stream);
 
+/*
+ * Operators over sequences, with the conventions above: a gated linear
+ * recurrence, the norms of query and key heads with the rotation of positions,
+ * log probabilities of given tokens, and a clipped policy loss on them, each
+ * with its gradient.  Flags (starts, token_mask) are bytes: nonzero is true.
+ * A call of no elements touches nothing but what is said to be written.
+ */
+
+/*
+ * Gated linear recurrence over `length` tokens of each of `batch` sequences,
+ * one recurrence a channel, with a = sigmoid(gate):
+ *   p = 0 at a token that starts over, else the state before it
+ *   h = a p + (1 - a) x   (mix != 0)   or   h = a p + x   (mix == 0)
+ * h is the state behind the token.  A masked token changes nothing: its h is
+ * the state before it, whatever its gate and x hold and whether it starts over.
+ * The state is held in fp32; h is that rounded.  Gate, x and states are finite;
+ * what a sequence's state is after a value that is not, up to the next start,
+ * is not defined (other sequences and channels are not affected).
+ *   0 <= batch, length < 2^31, dim in [1, 2^20], batch * dim < 2^33
+ *   gate, x      [batch * length, dim] of dtype, rows ldg and ldx apart
+ *   state        [batch, dim] fp32: the state before the first token; null: 0
+ *   starts       [batch, length] bytes, or null: no token starts over
+ *   token_mask   [batch, length] bytes: 0 for masked tokens; null: none
+ *   h            [batch, length, dim] of dtype
+ *   last         [batch, dim] fp32: the state behind the last token (`state` for
+ *                no tokens), or null; may be `state` itself
+ */
+MUON_API muon_status muon_gated_scan(int64_t batch, int64_t length, int64_t dim, int dtype,
+                                     const void* gate, int64_t ldg, const void* x, int64_t ldx,
+                                     const float* state, const uint8_t* starts,
+                                     const uint8_t* token_mask, int mix, void* h, float* last,
+                                     void* stream);
+
+/*
+ * Gradient of muon_gated_scan.  With l the gradient of the state behind a
+ * token (dh plus what reaches it through the next token, dlast for the last
+ * one) and p as in the forward pass, from the rounded h:
+ *   dx = (1 - a) l or l,   dgate = a (1 - a) l (p - x) or a (1 - a) l p
+ *   dstate = what reaches the state before the first token
+ * 0 for the gate and x of masked tokens.
+ *   dh           [batch * length, dim] of dtype, rows lddh apart
+ *   x            unused, and may be null, where mix == 0
+ *   h            the forward pass's, rows ldh apart
+ *   dlast        [batch, dim] fp32, or null (0)
+ *   dgate, dx    [batch, length, dim] of dtype, each may be null (not needed)
+ *   dstate       [batch, dim] fp32, or null; may be dlast itself
+ * Other arguments are those of muon_gated_scan.
+ */
+MUON_API muon_status muon_gated_scan_backward(
+    int64_t batch, int64_t length, int64_t dim, int dtype, const void* dh, int64_t lddh,
+    const void* gate, int64_t ldg, const void* x, int64_t ldx, const void* h, int64_t ldh,
+    const float* state, const float* dlast, const uint8_t* starts, const uint8_t* token_mask,
+    int mix, void* dgate, void* dx, float* dstate, void* stream);
+
+/*
+ * RMS norm of each query and key head, and the rotation of its first `rotary`
+ * elements by the angles of the token's position:
+ *   n = x / sqrt(mean(x^2) + eps) * weight   over the dim elements of a head
+ *   (y_i, y_j) = (n_i c - n_j s, n_j c + n_i s)   for pair m of rotary / 2, with
+ *   c, s = cos[position, m], sin[position, m]; i, j = m, m + rotary / 2, or
+ *   2 m, 2 m + 1 (neighbours != 0).  Elements from `rotary` on keep n.
+ * A token whose position is outside of the table is no token: its heads are 0,
+ * whatever they hold.
+ *   0 <= tokens < 2^31, 0 <= heads <= 65536, dim in [1, 1024], rotary even, in
+ *   [0, dim]
+ *   wdtype         type of the weights
+ *   q, k           [tokens, heads, dim] of dtype: tokens ldq and ldk apart,
+ *                  heads q_step and k_step
+ *   q_weight, k_weight   [dim], each may be null (1)
+ *   cos, sin       [table, rotary / 2] fp32; unused where rotary == 0
+ *   positions      [tokens], or null: token t has position t % period
+ *   q_out, k_out   [tokens, heads, dim] of dtype
+ */
+MUON_API muon_status muon_norm_rotate_heads(
+    int64_t tokens, int q_heads, int k_heads, int dim, int rotary, int dtype, int wdtype,
+    const void* q, int64_t ldq, int64_t q_step, const void* k, int64_t ldk, int64_t k_step,
+    const void* q_weight, const void* k_weight, float eps, const float* cos, const float* sin,
+    int64_t table, const int64_t* positions, int64_t period, int neighbours, void* q_out,
+    void* k_out, void* stream);
+
+/*
+ * Gradient of muon_norm_rotate_heads.  With g = dy rotated back, h = x * rstd:
+ *   dx = rstd * (g * weight - h * mean(g * weight * h))
+ *   dweight = sum over tokens and heads of g * h
+ *   dq, dk         gradients of q_out and k_out, laid out as q and k are, with
+ *                  strides of their own
+ *   q_grad, k_grad [tokens, heads, dim] of dtype, each may be null (not needed)
+ *   q_dweight, k_dweight [dim] of wdtype, each may be null
+ *   workspace      device, 256-byte aligned, >= the bytes of
+ *                  muon_norm_rotate_heads_workspace_bytes (any content); unused, and
+ *                  may be null, where no weight gradient is asked for
+ * Other arguments are those of muon_norm_rotate_heads.
+ */
+MUON_API muon_status muon_norm_rotate_heads_backward(
+    int64_t tokens, int q_heads, int k_heads, int dim, int rotary, int dtype, int wdtype,
+    const void* dq, int64_t lddq, int64_t dq_step, const void* dk, int64_t lddk, int64_t dk_step,
+    const void* q, int64_t ldq, int64_t q_step, const void* k, int64_t ldk, int64_t k_step,
+    const void* q_weight, const void* k_weight, float eps, const float* cos, const float* sin,
+    int64_t table, const int64_t* positions, int64_t period, int neighbours, void* q_grad,
+    void* k_grad, void* q_dweight, void* k_dweight, void* workspace, size_t ws_bytes,
+    void* stream);
+MUON_API muon_status muon_norm_rotate_heads_workspace_bytes(int64_t tokens, int q_heads,
+                                                            int k_heads, int dim, size_t* out);
+
+/*
+ * Log probability of a given token under softmax(scale * logits), and the
+ * logarithm of the softmax's sum:
+ *   lse = log(sum over v of exp(scale * logits_v))
+ *   log_probs = scale * logits_index - lse
+ * A token whose index is outside of [0, vocab) is ignored: both are 0 whatever
+ * its logits hold.  A logit of -inf has no share (scale > 0).  A row with a NaN, a
+ * +inf or nothing above -inf has NaN in log_probs.
+ *   0 <= tokens < 2^31, vocab in [1, 2^30], scale finite and > 0
+ *   logits       [tokens, vocab] of dtype, rows ld apart
+ *   index        [tokens]
+ *   log_probs, lse [tokens] fp32
+ */
+MUON_API muon_status muon_token_log_probs(int64_t tokens, int64_t vocab, int dtype,
+                                          const void* logits, int64_t ld, const int64_t* index,
+                                          float scale, float* log_probs, float* lse, void* stream);
+
+/*
+ * Gradient of muon_token_log_probs's log_probs:
+ *   dlogits_v = scale * dlog_probs * ((v == index) - exp(scale * logits_v - lse))
+ * A token that is ignored, or whose dlog_probs is 0, gets zeros, whatever its
+ * logits hold.
+ *   dlog_probs   [tokens] fp32
+ *   dlogits      [tokens, vocab] of dtype; may be logits itself, where its rows are
+ *                dense (ld == vocab)
+ * Other arguments are those of muon_token_log_probs, lse its result.
+ */
+MUON_API muon_status muon_token_log_probs_backward(int64_t tokens, int64_t vocab, int dtype,
+                                                   const float* dlog_probs, const void* logits,
+                                                   int64_t ld, const int64_t* index,
+                                                   const float* lse, float scale, void* dlogits,
+                                                   void* stream);
+
+/*
+ * Clipped policy loss with a KL term, over `length` tokens of each of `batch`
+ * sequences, with d = log_probs - old, A the advantage, r = exp(d) and
+ * e = ref - log_probs:
+ *   each = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_weight * k
+ *   k = exp(e) - e - 1   (0 without ref)
+ *   loss = sum of w each,  kl = sum of w k,
+ *   clipped = sum of w over the tokens whose minimum is the clipped side, which
+ *   is where d > log(1 + clip_high) and A >= 0, or d < log(1 - clip_low) and A < 0,
+ *   decided on the exact difference
+ *   w = 1 / tokens (all that count), or with by_sequence != 0
+ *   w = 1 / (sequences that have a token * tokens of the sequence)
+ * Masked tokens have no effect, whatever they hold.  No token at all: all 0.
+ *   0 <= batch, length < 2^31, batch * length < 2^40, 0 <= clip_low < 1,
+ *   0 <= clip_high, both and kl_weight finite
+ *   log_probs, old, ref  fp32 rows of `length`, ldl, ldo and ldr apart; ref may be
+ *                null
+ *   advantages   fp32 rows of `length`, lda apart, or one a sequence (lda < 0):
+ *                [batch]
+ *   token_mask   [batch, length] bytes, or null
+ *   loss, kl, clipped    one fp32 each; the last two may be null
+ *   weights      [batch] fp32: w of the sequence's tokens (0 where it has none)
+ *   workspace    device, 256-byte aligned, >= muon_policy_loss_workspace_bytes
+ *                (any content)
+ */
+MUON_API muon_status muon_policy_loss(int64_t batch, int64_t length, const float* log_probs,
+                                      int64_t ldl, const float* old, int64_t ldo,
+                                      const float* advantages, int64_t lda, const float* ref,
+                                      int64_t ldr, const uint8_t* token_mask, double clip_low,
+                                      double clip_high, float kl_weight, int by_sequence,
+                                      float* loss, float* kl, float* clipped, float* weights,
+                                      void* workspace, size_t ws_bytes, void* stream);
+MUON_API muon_status muon_policy_loss_workspace_bytes(int64_t batch, int64_t length, size_t* out);
+
+/*
+ * Gradient of muon_policy_loss's loss with respect to log_probs (old, ref and
+ * the advantages are constants):
+ *   dlog_probs = dloss * w * ((clipped ? 0 : -r A) + kl_weight * (1 - exp(e)))
+ * 0 at masked tokens.
+ *   weights      the forward pass's
+ *   dloss        one fp32 on the device, or null (1)
+ *   dlog_probs   [batch, length] fp32; may be log_probs, old or ref itself, where its
+ *                rows are dense
+ * Other arguments are those of muon_policy_loss.
+ */
+MUON_API muon_status muon_policy_loss_backward(
+    int64_t batch, int64_t length, const float* log_probs, int64_t ldl, const float* old,
+    int64_t ldo, const float* advantages, int64_t lda, const float* ref, int64_t ldr,
+    const uint8_t* token_mask, double clip_low, double clip_high, float kl_weight,
+    const float* weights, const float* dloss, float* dlog_probs, void* stream);
+
 MUON_API void muon_plan_destroy(muon_plan_t* plan);
 MUON_API const char* muon_status_string(muon_status s);
 

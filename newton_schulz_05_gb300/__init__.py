@@ -73,6 +73,10 @@ EXPORTS = ["muon_options_default", "muon_plan", "muon_plan_workspace_bytes",
            "muon_step_timed", "muon_step_host", "muon_plan_host_unit_bytes",
            "muon_host_alloc", "muon_host_free", "muon_layer_norm", "muon_layer_norm_backward",
            "muon_layer_norm_workspace_bytes", "muon_dropout", "muon_route", "muon_route_backward",
+           "muon_gated_scan", "muon_gated_scan_backward", "muon_norm_rotate_heads",
+           "muon_norm_rotate_heads_backward", "muon_norm_rotate_heads_workspace_bytes",
+           "muon_token_log_probs", "muon_token_log_probs_backward", "muon_policy_loss",
+           "muon_policy_loss_backward", "muon_policy_loss_workspace_bytes",
            "muon_route_workspace_bytes"]
 
 STATIC_WORKSPACE_BYTES = 32 << 20   # MUON_STATIC_WORKSPACE_BYTES in include/muon.h
@@ -136,6 +140,22 @@ def load(path: str = LIB_PATH):
     L.muon_route.argtypes = [i64, i32, i32, i32, vp, i64, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
     L.muon_route_workspace_bytes.argtypes = [i64, i32, ctypes.POINTER(sz)]
     L.muon_route_backward.argtypes = [i64, i32, i32, i32, vp, i64, vp, i32, vp, vp, vp, vp, vp, vp]
+    f64 = ctypes.c_double
+    L.muon_gated_scan.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, vp, vp, i32, vp, vp, vp]
+    L.muon_gated_scan_backward.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp,
+                                           vp, vp, vp, i32, vp, vp, vp, vp]
+    turn = [vp, vp, f32, vp, vp, i64, vp, i64, i32]     # weights, eps, table, positions, pairing
+    L.muon_norm_rotate_heads.argtypes = [i64] + [i32] * 6 + [vp, i64, i64] * 2 + turn + [vp, vp, vp]
+    L.muon_norm_rotate_heads_backward.argtypes = [i64] + [i32] * 6 + [vp, i64, i64] * 4 + turn + \
+        [vp] * 5 + [sz, vp]
+    L.muon_norm_rotate_heads_workspace_bytes.argtypes = [i64, i32, i32, i32, ctypes.POINTER(sz)]
+    L.muon_token_log_probs.argtypes = [i64, i64, i32, vp, i64, vp, f32, vp, vp, vp]
+    L.muon_token_log_probs_backward.argtypes = [i64, i64, i32, vp, vp, i64, vp, vp, f32, vp, vp]
+    L.muon_policy_loss.argtypes = [i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, f64, f64, f32, i32,
+                                   vp, vp, vp, vp, vp, sz, vp]
+    L.muon_policy_loss_backward.argtypes = [i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, f64, f64,
+                                            f32, vp, vp, vp, vp]
+    L.muon_policy_loss_workspace_bytes.argtypes = [i64, i64, ctypes.POINTER(sz)]
     L.muon_plan_destroy.argtypes = [vp]
     L.muon_plan_destroy.restype = None
     L.muon_status_string.argtypes = [ctypes.c_int]
@@ -147,7 +167,11 @@ def load(path: str = LIB_PATH):
                "muon_static_error", "muon_step_timed", "muon_step_host",
                "muon_plan_host_unit_bytes", "muon_host_alloc", "muon_host_free", "muon_layer_norm",
                "muon_layer_norm_backward", "muon_layer_norm_workspace_bytes", "muon_dropout",
-               "muon_route", "muon_route_backward", "muon_route_workspace_bytes"):
+               "muon_route", "muon_route_backward", "muon_route_workspace_bytes", "muon_gated_scan",
+               "muon_gated_scan_backward", "muon_norm_rotate_heads", "muon_norm_rotate_heads_backward",
+               "muon_norm_rotate_heads_workspace_bytes", "muon_token_log_probs",
+               "muon_token_log_probs_backward", "muon_policy_loss", "muon_policy_loss_backward",
+               "muon_policy_loss_workspace_bytes"):
         getattr(L, fn).restype = ctypes.c_int
     _lib = L
     return L

@@ -31,6 +31,16 @@ decltype(&muon_dropout) p_dropout;
 decltype(&muon_route) p_route;
 decltype(&muon_route_workspace_bytes) p_route_workspace_bytes;
 decltype(&muon_route_backward) p_route_backward;
+decltype(&muon_gated_scan) p_gated_scan;
+decltype(&muon_gated_scan_backward) p_gated_scan_backward;
+decltype(&muon_norm_rotate_heads) p_norm_rotate_heads;
+decltype(&muon_norm_rotate_heads_backward) p_norm_rotate_heads_backward;
+decltype(&muon_norm_rotate_heads_workspace_bytes) p_norm_rotate_heads_workspace_bytes;
+decltype(&muon_token_log_probs) p_token_log_probs;
+decltype(&muon_token_log_probs_backward) p_token_log_probs_backward;
+decltype(&muon_policy_loss) p_policy_loss;
+decltype(&muon_policy_loss_backward) p_policy_loss_backward;
+decltype(&muon_policy_loss_workspace_bytes) p_policy_loss_workspace_bytes;
 
 // a Python error to raise
 struct Raise {
@@ -448,6 +458,423 @@ PyObject* route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// ------------------------------------------------------- operators over sequences
+
+// the data of a tensor that may be absent
+template <typename T> const T* data(const at::Tensor* t) {
+  return t ? static_cast<const T*>(t->const_data_ptr()) : nullptr;
+}
+template <typename T> T* data(at::Tensor& t) {
+  return t.defined() ? static_cast<T*>(t.mutable_data_ptr()) : nullptr;
+}
+PyObject* wrapped(at::Tensor& t) { return t.defined() ? wrap(std::move(t)) : none(); }
+
+// bytes, one for each of `shape`, of a bool or uint8 tensor that lists its elements
+// like them
+const uint8_t* flags_of(const at::Tensor* t, at::IntArrayRef shape, int64_t numel,
+                        const at::Tensor& like, const char* what) {
+  if (!t) return nullptr;
+  if (t->scalar_type() != at::kBool && t->scalar_type() != at::kByte)
+    type_error(std::string(what) + " must be bool or uint8, got " + c10::toString(t->scalar_type()));
+  check_flat(*t, numel, t->scalar_type(), like, what);
+  if (!listed_alike(t->sizes(), shape))
+    value_error(std::string(what) + " must have the shape of the tokens, or one dimension");
+  return data<uint8_t>(t);
+}
+
+// Sequences of rows: [..., length, dim]
+struct Sequences { int64_t batch, length, dim; };
+Sequences sequences_of(const at::Tensor& t, const char* what) {
+  const int64_t nd = t.dim();
+  if (nd < 2) value_error(std::string(what) + " needs at least two dimensions, tokens and channels");
+  int64_t batch = 1;
+  for (int64_t d = 0; d < nd - 2; ++d) batch *= t.size(d);
+  return {batch, t.size(nd - 2), t.size(nd - 1)};
+}
+// the dense fp32 state of each sequence and channel
+const float* state_of(const at::Tensor* t, const Sequences& q, const at::Tensor& like, const char* what) {
+  if (!t) return nullptr;
+  check_flat(*t, q.batch * q.dim, at::kFloat, like, what);
+  c10::SmallVector<int64_t, 6> shape(like.sizes().begin(), like.sizes().end() - 2);
+  shape.push_back(q.dim);
+  const int64_t two[2] = {q.batch, q.dim};
+  if (t->sizes() != at::IntArrayRef(shape) && t->sizes() != at::IntArrayRef(two))
+    value_error(std::string(what) + " must have the shape of x without the tokens' dimension");
+  return data<float>(t);
+}
+at::Tensor empty_state(const at::Tensor& like, const Sequences& q) {
+  c10::SmallVector<int64_t, 6> shape(like.sizes().begin(), like.sizes().end() - 2);
+  shape.push_back(q.dim);
+  return empty(shape, at::kFloat);
+}
+
+// (gate, x, state, starts, token_mask, mix) -> (h, state)
+PyObject* gated_scan_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 6, [&]() -> PyObject* {
+    const at::Tensor &gate = tensor(a[0], "gate"), &x = tensor(a[1], "x");
+    const at::Tensor *state = maybe(a[2], "state"), *starts = maybe(a[3], "starts"),
+                     *mask = maybe(a[4], "token_mask");
+    const bool mix = truth(a[5]);
+    const int dt = dtype_of(x, "x");
+    const Rows r = rows_or_raise(x, "x");
+    const Sequences q = sequences_of(x, "x");
+    const int64_t ldg = same_rows(gate, x, "gate");
+    void* stream = stream_of(x);
+    const at::IntArrayRef tokens = x.sizes().slice(0, x.dim() - 1);
+    const uint8_t* ps = flags_of(starts, tokens, q.batch * q.length, x, "starts");
+    const uint8_t* pm = flags_of(mask, tokens, q.batch * q.length, x, "token_mask");
+    const float* p0 = state_of(state, q, x, "state");
+    at::Tensor h, last;
+    muon_status st;
+    {
+      const Unlocked unlocked;
+      h = empty(x.sizes(), x.scalar_type());
+      last = empty_state(x, q);
+      st = p_gated_scan(q.batch, q.length, q.dim, dt, gate.const_data_ptr(), ldg, x.const_data_ptr(), r.ld,
+                        p0, ps, pm, mix, h.mutable_data_ptr(), data<float>(last), stream);
+    }
+    if (st != MUON_OK) return PyLong_FromLong(st);
+    return tuple_of({wrap(std::move(h)), wrap(std::move(last))});
+  });
+}
+
+// (dh, gate, x, h, state, dstate, starts, token_mask, mix, need_gate, need_x,
+// need_state) -> (dgate or None, dx or None, dstate or None)
+PyObject* gated_scan_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 12, [&]() -> PyObject* {
+    const at::Tensor &dh = tensor(a[0], "dh"), &gate = tensor(a[1], "gate"), &h = tensor(a[3], "h");
+    const at::Tensor *x = maybe(a[2], "x"), *state = maybe(a[4], "state"), *dlast = maybe(a[5], "dstate"),
+                     *starts = maybe(a[6], "starts"), *mask = maybe(a[7], "token_mask");
+    const bool mix = truth(a[8]), need_g = truth(a[9]), need_x = truth(a[10]), need_s = truth(a[11]);
+    const int dt = dtype_of(dh, "dh");
+    const Rows r = rows_or_raise(dh, "dh");
+    const Sequences q = sequences_of(dh, "dh");
+    const int64_t ldg = same_rows(gate, dh, "gate"), ldh = same_rows(h, dh, "h");
+    const int64_t ldx = x ? same_rows(*x, dh, "x") : 0;
+    void* stream = stream_of(dh);
+    const at::IntArrayRef tokens = dh.sizes().slice(0, dh.dim() - 1);
+    const uint8_t* ps = flags_of(starts, tokens, q.batch * q.length, dh, "starts");
+    const uint8_t* pm = flags_of(mask, tokens, q.batch * q.length, dh, "token_mask");
+    const float *p0 = state_of(state, q, dh, "state"), *pl = state_of(dlast, q, dh, "dstate");
+    at::Tensor dg, dx, ds;
+    muon_status st;
+    {
+      const Unlocked unlocked;
+      if (need_g) dg = empty(dh.sizes(), dh.scalar_type());
+      if (need_x) dx = empty(dh.sizes(), dh.scalar_type());
+      if (need_s) ds = empty_state(dh, q);
+      st = p_gated_scan_backward(q.batch, q.length, q.dim, dt, dh.const_data_ptr(), r.ld,
+                                 gate.const_data_ptr(), ldg, data<void>(x), ldx, h.const_data_ptr(), ldh, p0,
+                                 pl, ps, pm, mix, data<void>(dg), data<void>(dx), data<float>(ds), stream);
+    }
+    if (st != MUON_OK) return PyLong_FromLong(st);
+    return tuple_of({wrapped(dg), wrapped(dx), wrapped(ds)});
+  });
+}
+
+// Heads of tokens: [..., heads, dim] with a dense last dimension, heads at one
+// stride, tokens at one stride
+struct HeadRows { int64_t tokens, heads, dim, ld, step; };
+const char* heads_of(const at::Tensor& t, HeadRows* r) {
+  if (!t.is_cuda()) return " is not on a CUDA device";
+  const int64_t nd = t.dim();
+  if (nd < 2) return " needs at least two dimensions, heads and their elements";
+  const auto size = t.sizes(), stride = t.strides();
+  *r = {1, size[nd - 2], size[nd - 1], -1, size[nd - 2] > 1 ? stride[nd - 2] : size[nd - 1]};
+  if (r->dim > 1 && stride[nd - 1] != 1) return " has a last dimension that is not dense";
+  const bool none = t.numel() == 0;
+  for (int64_t d = nd - 3; d >= 0; --d) {
+    if (size[d] != 1 && !none) {
+      if (r->ld < 0) r->ld = stride[d];
+      else if (stride[d] != r->ld * r->tokens) return " has leading dimensions that are not tokens at one stride";
+    }
+    r->tokens *= size[d];
+  }
+  if (r->ld < 0) r->ld = r->heads * r->dim;
+  return nullptr;
+}
+HeadRows heads_or_raise(const at::Tensor& t, const char* what) {
+  HeadRows r;
+  if (const char* why = heads_of(t, &r)) value_error(std::string(what) + why);
+  return r;
+}
+// laid out like `like` but for its strides
+HeadRows same_heads(const at::Tensor& t, const at::Tensor& like, const char* what) {
+  if (t.sizes() != like.sizes() || t.device() != like.device())
+    value_error(std::string(what) + " must have its heads' shape and device");
+  if (t.scalar_type() != like.scalar_type())
+    type_error(std::string(what) + " must be of its heads' type, got " + c10::toString(t.scalar_type()));
+  return heads_or_raise(t, what);
+}
+
+// What the two passes over heads share: (q, k or None, q_weight, k_weight, cos, sin, positions,
+// eps, neighbours) from a[0] on
+struct HeadCall {
+  const at::Tensor *q, *k, *qw, *kw, *cos, *sin, *pos;
+  HeadRows rq{}, rk{};
+  int dt, wdt, rotary = 0;
+  int64_t table = 0, period = 1;
+  float eps;
+  bool neighbours;
+  at::ScalarType wtype = at::kFloat;
+  const void *pqw, *pkw;
+  explicit HeadCall(PyObject* const* a)
+      : q(&tensor(a[0], "q")), k(maybe(a[1], "k")), qw(maybe(a[2], "q_weight")), kw(maybe(a[3], "k_weight")),
+        cos(maybe(a[4], "cos")), sin(maybe(a[5], "sin")), pos(maybe(a[6], "positions")),
+        eps((float)number(a[7])), neighbours(truth(a[8])) {
+    dt = dtype_of(*q, "q");
+    rq = heads_or_raise(*q, "q");
+    if (k) {
+      if (k->scalar_type() != q->scalar_type())
+        type_error(std::string("k must be of q's type, got ") + c10::toString(k->scalar_type()));
+      rk = heads_or_raise(*k, "k");
+      const int64_t nd = q->dim();
+      if (k->device() != q->device() || k->dim() != nd ||
+          k->sizes().slice(0, nd - 2) != q->sizes().slice(0, nd - 2) || rk.dim != rq.dim)
+        value_error("k must have q's tokens, head width and device");
+    }
+    wdt = MUON_F32;
+    if (qw || kw) {
+      wdt = dtype_of(qw ? *qw : *kw, "q_weight and k_weight");
+      wtype = (qw ? *qw : *kw).scalar_type();
+    }
+    if (qw && kw && qw->scalar_type() != kw->scalar_type())
+      type_error("q_weight and k_weight must be of one type");
+    pqw = vector_of(qw, rq.dim, *q, "q_weight");
+    pkw = vector_of(kw, rq.dim, *q, "k_weight");
+    if (!cos != !sin) value_error("cos and sin go together");
+    if (cos) {
+      if (cos->dim() != 2 || cos->sizes() != sin->sizes()) value_error("cos and sin must be of one shape [table, pairs]");
+      check_flat(*cos, cos->numel(), at::kFloat, *q, "cos");
+      check_flat(*sin, sin->numel(), at::kFloat, *q, "sin");
+      table = cos->size(0);
+      if (2 * cos->size(1) > rq.dim) value_error("cos and sin have more pairs than a head");
+      rotary = (int)(2 * cos->size(1));
+    }
+    const at::IntArrayRef tokens = q->sizes().slice(0, q->dim() - 2);
+    if (pos) {
+      check_flat(*pos, rq.tokens, at::kLong, *q, "positions");
+      if (!listed_alike(pos->sizes(), tokens))
+        value_error("positions must have the shape of the tokens, or one dimension");
+    } else if (!tokens.empty() && tokens.back() > 0) {
+      period = tokens.back();
+    }
+    if (rq.heads > 65536 || rk.heads > 65536) value_error("more than 65536 heads");
+    if (rq.dim > 1024) value_error("heads of more than 1024 elements");
+  }
+};
+
+// (q, k, q_weight, k_weight, cos, sin, positions, eps, neighbours) -> (q, k or None)
+PyObject* norm_rotate_heads_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> PyObject* {
+    const HeadCall c(a);
+    void* stream = stream_of(*c.q);
+    at::Tensor yq, yk;
+    muon_status st;
+    {
+      const Unlocked unlocked;
+      yq = empty(c.q->sizes(), c.q->scalar_type());
+      if (c.k) yk = empty(c.k->sizes(), c.q->scalar_type());
+      st = p_norm_rotate_heads(c.rq.tokens, (int)c.rq.heads, (int)c.rk.heads, (int)c.rq.dim, c.rotary, c.dt,
+                               c.wdt, c.q->const_data_ptr(), c.rq.ld, c.rq.step, data<void>(c.k), c.rk.ld,
+                               c.rk.step, c.pqw, c.pkw, c.eps, data<float>(c.cos), data<float>(c.sin),
+                               c.table, data<int64_t>(c.pos), c.period, c.neighbours, data<void>(yq),
+                               data<void>(yk), stream);
+    }
+    if (st != MUON_OK) return PyLong_FromLong(st);
+    return tuple_of({wrapped(yq), wrapped(yk)});
+  });
+}
+
+// (q, k, q_weight, k_weight, cos, sin, positions, eps, neighbours, dq, dk, need_q, need_k,
+// need_q_weight, need_k_weight) -> (dq, dk, dq_weight, dk_weight), each or None
+PyObject* norm_rotate_heads_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 15, [&]() -> PyObject* {
+    const HeadCall c(a);
+    const at::Tensor &dq = tensor(a[9], "dq"), *dk = maybe(a[10], "dk");
+    const bool nq = truth(a[11]), nk = truth(a[12]), nqw = truth(a[13]), nkw = truth(a[14]);
+    if (!c.k != !dk) value_error("k and dk go together");
+    const HeadRows rdq = same_heads(dq, *c.q, "dq"), rdk = c.k ? same_heads(*dk, *c.k, "dk") : HeadRows{};
+    void* stream = stream_of(*c.q);
+    size_t bytes = 0;
+    muon_status st = MUON_OK;
+    if (nqw || nkw)
+      st = p_norm_rotate_heads_workspace_bytes(c.rq.tokens, (int)c.rq.heads, (int)c.rk.heads, (int)c.rq.dim,
+                                               &bytes);
+    if (st != MUON_OK) return PyLong_FromLong(st);
+    at::Tensor gq, gk, gqw, gkw, ws;
+    {
+      const Unlocked unlocked;
+      if (nq) gq = empty(c.q->sizes(), c.q->scalar_type());
+      if (nk && c.k) gk = empty(c.k->sizes(), c.q->scalar_type());
+      if (nqw) gqw = empty({c.rq.dim}, c.wtype);
+      if (nkw) gkw = empty({c.rq.dim}, c.wtype);
+      if (nqw || nkw) ws = empty({(int64_t)bytes}, at::kByte);
+      st = p_norm_rotate_heads_backward(
+          c.rq.tokens, (int)c.rq.heads, (int)c.rk.heads, (int)c.rq.dim, c.rotary, c.dt, c.wdt,
+          dq.const_data_ptr(), rdq.ld, rdq.step, data<void>(dk), rdk.ld, rdk.step, c.q->const_data_ptr(),
+          c.rq.ld, c.rq.step, data<void>(c.k), c.rk.ld, c.rk.step, c.pqw, c.pkw, c.eps, data<float>(c.cos),
+          data<float>(c.sin), c.table, data<int64_t>(c.pos), c.period, c.neighbours, data<void>(gq),
+          data<void>(gk), data<void>(gqw), data<void>(gkw), data<void>(ws), bytes, stream);
+    }
+    if (st != MUON_OK) return PyLong_FromLong(st);
+    return tuple_of({wrapped(gq), wrapped(gk), wrapped(gqw), wrapped(gkw)});
+  });
+}
+
+// the tokens whose log probabilities are asked for
+const int64_t* tokens_of(const at::Tensor& t, int64_t rows, const at::Tensor& logits) {
+  check_each_row(t, rows, at::kLong, logits, "tokens");
+  return data<int64_t>(&t);
+}
+
+// (logits, tokens, scale) -> (log_probs, lse)
+PyObject* token_log_probs_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 3, [&]() -> PyObject* {
+    const at::Tensor &l = tensor(a[0], "logits"), &tokens = tensor(a[1], "tokens");
+    const float scale = (float)number(a[2]);
+    const int dt = dtype_of(l, "logits");
+    const Rows r = rows_or_raise(l, "logits");
+    void* stream = stream_of(l);
+    const int64_t* index = tokens_of(tokens, r.rows, l);
+    at::Tensor lp, lse;
+    muon_status st;
+    {
+      const Unlocked unlocked;
+      const at::IntArrayRef lead = l.sizes().slice(0, l.dim() - 1);
+      lp = empty(lead, at::kFloat);
+      lse = empty(lead, at::kFloat);
+      st = p_token_log_probs(r.rows, r.cols, dt, l.const_data_ptr(), r.ld, index, scale, data<float>(lp),
+                             data<float>(lse), stream);
+    }
+    if (st != MUON_OK) return PyLong_FromLong(st);
+    return tuple_of({wrap(std::move(lp)), wrap(std::move(lse))});
+  });
+}
+
+// (dlog_probs, logits, tokens, lse, scale, out) -> dlogits
+PyObject* token_log_probs_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 6, [&]() -> PyObject* {
+    const at::Tensor &d = tensor(a[0], "dlog_probs"), &l = tensor(a[1], "logits"),
+                     &tokens = tensor(a[2], "tokens"), &lse = tensor(a[3], "lse");
+    const float scale = (float)number(a[4]);
+    const at::Tensor* given = maybe(a[5], "out");
+    const int dt = dtype_of(l, "logits");
+    const Rows r = rows_or_raise(l, "logits");
+    void* stream = stream_of(l);
+    const int64_t* index = tokens_of(tokens, r.rows, l);
+    check_each_row(d, r.rows, at::kFloat, l, "dlog_probs");
+    check_each_row(lse, r.rows, at::kFloat, l, "lse");
+    at::Tensor out;
+    if (given) {
+      if (given->sizes() != l.sizes()) value_error("out must have the shape of logits");
+      check_flat(*given, l.numel(), l.scalar_type(), l, "out");
+      if (c10::GradMode::is_enabled() && given->requires_grad())
+        throw Raise{PyExc_RuntimeError, "out requires grad, and the call is not differentiable"};
+      given->unsafeGetTensorImpl()->bump_version();
+      out = *given;
+    }
+    muon_status st;
+    {
+      const Unlocked unlocked;
+      if (!given) out = empty(l.sizes(), l.scalar_type());
+      st = p_token_log_probs_backward(r.rows, r.cols, dt, data<float>(&d), l.const_data_ptr(), r.ld, index,
+                                      data<float>(&lse), scale, out.mutable_data_ptr(), stream);
+    }
+    if (st != MUON_OK) return PyLong_FromLong(st);
+    if (given) {
+      Py_INCREF(a[5]);
+      return a[5];
+    }
+    return wrap(std::move(out));
+  });
+}
+
+// What the two passes of the policy loss share: (log_probs, old, advantages, ref, token_mask,
+// clip_low, clip_high, kl) from a[0] on
+struct PolicyCall {
+  const at::Tensor *lp, *old, *adv, *ref, *mask;
+  double low, high;
+  float kl;
+  int64_t batch, length, ldl, ldo, lda, ldr;
+  const uint8_t* pm;
+  explicit PolicyCall(PyObject* const* a)
+      : lp(&tensor(a[0], "log_probs")), old(&tensor(a[1], "old_log_probs")), adv(&tensor(a[2], "advantages")),
+        ref(maybe(a[3], "ref_log_probs")), mask(maybe(a[4], "token_mask")), low(number(a[5])),
+        high(number(a[6])), kl((float)number(a[7])) {
+    if (lp->scalar_type() != at::kFloat)
+      type_error(std::string("log_probs must be fp32, got ") + c10::toString(lp->scalar_type()));
+    const Rows r = rows_or_raise(*lp, "log_probs");
+    length = r.cols;
+    batch = 1;
+    for (int64_t d = 0; d + 1 < lp->dim(); ++d) batch *= lp->size(d);
+    ldl = r.ld;
+    ldo = same_rows(*old, *lp, "old_log_probs");
+    ldr = ref ? same_rows(*ref, *lp, "ref_log_probs") : 0;
+    const at::IntArrayRef lead = lp->sizes().slice(0, lp->dim() - 1);
+    if (adv->sizes() == lp->sizes()) {
+      lda = same_rows(*adv, *lp, "advantages");
+    } else {
+      check_flat(*adv, batch, at::kFloat, *lp, "advantages");
+      const int64_t one[1] = {batch};
+      if (adv->sizes() != lead && adv->sizes() != at::IntArrayRef(one))
+        value_error("advantages must be one a token or one a sequence");
+      lda = -1;
+    }
+    pm = flags_of(mask, lp->sizes(), batch * length, *lp, "token_mask");
+  }
+};
+
+// (log_probs, old, advantages, ref, token_mask, clip_low, clip_high, kl, by_sequence)
+// -> (loss, kl, clipped, weights)
+PyObject* policy_loss_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> PyObject* {
+    const PolicyCall c(a);
+    const bool by_sequence = truth(a[8]);
+    void* stream = stream_of(*c.lp);
+    size_t bytes = 0;
+    muon_status st = p_policy_loss_workspace_bytes(c.batch, c.length, &bytes);
+    if (st != MUON_OK) return PyLong_FromLong(st);
+    at::Tensor loss, kl, clipped, weights, ws;
+    {
+      const Unlocked unlocked;
+      loss = empty({}, at::kFloat);
+      kl = empty({}, at::kFloat);
+      clipped = empty({}, at::kFloat);
+      weights = empty(c.lp->sizes().slice(0, c.lp->dim() - 1), at::kFloat);
+      ws = empty({(int64_t)bytes}, at::kByte);
+      st = p_policy_loss(c.batch, c.length, data<float>(c.lp), c.ldl, data<float>(c.old), c.ldo,
+                         data<float>(c.adv), c.lda, data<float>(c.ref), c.ldr, c.pm, c.low, c.high, c.kl,
+                         by_sequence, data<float>(loss), data<float>(kl), data<float>(clipped),
+                         data<float>(weights), data<void>(ws), bytes, stream);
+    }
+    if (st != MUON_OK) return PyLong_FromLong(st);
+    return tuple_of({wrapped(loss), wrapped(kl), wrapped(clipped), wrapped(weights)});
+  });
+}
+
+// (log_probs, old, advantages, ref, token_mask, clip_low, clip_high, kl, weights, dloss) -> dlog_probs
+PyObject* policy_loss_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 10, [&]() -> PyObject* {
+    const PolicyCall c(a);
+    const at::Tensor &weights = tensor(a[8], "weights"), *dloss = maybe(a[9], "dloss");
+    check_each_row(weights, c.batch, at::kFloat, *c.lp, "weights");
+    if (dloss) check_flat(*dloss, 1, at::kFloat, *c.lp, "dloss");
+    void* stream = stream_of(*c.lp);
+    at::Tensor out;
+    muon_status st;
+    {
+      const Unlocked unlocked;
+      out = empty(c.lp->sizes(), at::kFloat);
+      st = p_policy_loss_backward(c.batch, c.length, data<float>(c.lp), c.ldl, data<float>(c.old), c.ldo,
+                                  data<float>(c.adv), c.lda, data<float>(c.ref), c.ldr, c.pm, c.low, c.high,
+                                  c.kl, data<float>(&weights), data<float>(dloss), data<float>(out), stream);
+    }
+    if (st != MUON_OK) return PyLong_FromLong(st);
+    return wrap(std::move(out));
+  });
+}
+
 // whether a tensor can be passed as rows without a copy
 PyObject* is_rows(PyObject*, PyObject* o) {
   if (!THPVariable_Check(o)) {
@@ -458,21 +885,47 @@ PyObject* is_rows(PyObject*, PyObject* o) {
   return PyBool_FromLong(rows_of(THPVariable_Unpack(o), &r) == nullptr);
 }
 
-// bind({name: address}): the library's entry points
+// whether a tensor can be passed as heads of tokens without a copy
+PyObject* is_heads(PyObject*, PyObject* o) {
+  if (!THPVariable_Check(o)) {
+    PyErr_SetString(PyExc_TypeError, "expected a tensor");
+    return nullptr;
+  }
+  HeadRows r;
+  return PyBool_FromLong(heads_of(THPVariable_Unpack(o), &r) == nullptr);
+}
+
+// bind({name: address}): the library's entry points.  A name that is left out keeps what
+// it was bound to; each must be bound to something.
 PyObject* bind(PyObject*, PyObject* names) {
+  bool all = true;
   auto get = [&](const char* name, auto& to) {
     PyObject* v = PyDict_Check(names) ? PyDict_GetItemString(names, name) : nullptr;
-    void* p = v ? PyLong_AsVoidPtr(v) : nullptr;
-    to = reinterpret_cast<std::decay_t<decltype(to)>>(p);
-    return p != nullptr;
+    if (void* p = v ? PyLong_AsVoidPtr(v) : nullptr) to = reinterpret_cast<std::decay_t<decltype(to)>>(p);
+    if (!to) all = false;
   };
-  if (!get("muon_layer_norm", p_layer_norm) ||
-      !get("muon_layer_norm_backward", p_layer_norm_backward) ||
-      !get("muon_layer_norm_workspace_bytes", p_layer_norm_workspace_bytes) ||
-      !get("muon_dropout", p_dropout) || !get("muon_route", p_route) ||
-      !get("muon_route_workspace_bytes", p_route_workspace_bytes) ||
-      !get("muon_route_backward", p_route_backward)) {
-    if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "an entry point of libmuon is missing");
+#define BIND(f) get("muon_" #f, p_##f)
+  BIND(layer_norm);
+  BIND(layer_norm_backward);
+  BIND(layer_norm_workspace_bytes);
+  BIND(dropout);
+  BIND(route);
+  BIND(route_workspace_bytes);
+  BIND(route_backward);
+  BIND(gated_scan);
+  BIND(gated_scan_backward);
+  BIND(norm_rotate_heads);
+  BIND(norm_rotate_heads_backward);
+  BIND(norm_rotate_heads_workspace_bytes);
+  BIND(token_log_probs);
+  BIND(token_log_probs_backward);
+  BIND(policy_loss);
+  BIND(policy_loss_backward);
+  BIND(policy_loss_workspace_bytes);
+#undef BIND
+  if (PyErr_Occurred()) return nullptr;
+  if (!all) {
+    PyErr_SetString(PyExc_ValueError, "an entry point of libmuon is missing");
     return nullptr;
   }
   Py_RETURN_NONE;
@@ -481,7 +934,10 @@ PyObject* bind(PyObject*, PyObject* names) {
 #define FAST(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
     FAST(layer_norm_forward), FAST(layer_norm_backward), FAST(dropout), FAST(route_forward),
-    FAST(route_backward), {"is_rows", is_rows, METH_O, nullptr}, {"bind", bind, METH_O, nullptr},
+    FAST(route_backward), FAST(gated_scan_forward), FAST(gated_scan_backward),
+    FAST(norm_rotate_heads_forward), FAST(norm_rotate_heads_backward), FAST(token_log_probs_forward),
+    FAST(token_log_probs_backward), FAST(policy_loss_forward), FAST(policy_loss_backward),
+    {"is_rows", is_rows, METH_O, nullptr}, {"is_heads", is_heads, METH_O, nullptr}, {"bind", bind, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,

@@ -1,16 +1,19 @@
 """Training operators around the optimizer step: layer norm (alone, or behind
-dropout and the residual add), dropout from a counter-based generator, and the
-expert router with its balance loss, each with its gradient.
+dropout and the residual add), dropout from a counter-based generator, the
+expert router with its balance loss; and over sequences a gated linear
+recurrence, the norms of query and key heads with the rotation of positions, log
+probabilities of given tokens and the clipped policy loss on them.  Each comes
+with its gradient.
 
 They produce what MuonWithAdamW.step consumes: the 1-D gradients of norm scales
-and biases (the AdamW path), and the router gradient and per-expert token sets
-of [E, M, N] expert stacks (the Muon path).  Every computation runs in libmuon's
-kernels (muon_layer_norm, muon_dropout, muon_route and their gradients in
-include/muon.h, which states the formulas); this module and its compiled half
+and biases (the AdamW path), and what the gradients of the matrices between them
+are made from (the Muon path).  Every computation runs in libmuon's kernels
+(include/muon.h states the formulas); this module and its compiled half
 (csrc/binding.cpp) check and marshal tensors.
 
 Two levels:
-  * layer_norm, dropout_add_layer_norm, dropout, route: differentiable once
+  * layer_norm, dropout_add_layer_norm, dropout, route, gated_scan,
+    norm_rotate_heads, token_log_probs, policy_loss: differentiable once
     (torch.autograd), inputs of any strides;
   * *_forward / *_backward: one library call each, outputs as named tuples.
 
@@ -37,7 +40,12 @@ from .build import binding_path
 
 __all__ = ["layer_norm", "dropout_add_layer_norm", "dropout", "route", "RandomCounter",
            "layer_norm_forward", "layer_norm_backward", "dropout_forward", "dropout_backward",
-           "route_forward", "route_backward", "NormOut", "NormGrad", "RouteOut"]
+           "route_forward", "route_backward", "NormOut", "NormGrad", "RouteOut",
+           "gated_scan", "norm_rotate_heads", "rotation_table", "token_log_probs", "policy_loss",
+           "gated_scan_forward", "gated_scan_backward", "norm_rotate_heads_forward",
+           "norm_rotate_heads_backward", "token_log_probs_forward", "token_log_probs_backward",
+           "policy_loss_forward", "policy_loss_backward", "ScanOut", "ScanGrad", "HeadsOut",
+           "HeadsGrad", "LogProbsOut", "PolicyOut"]
 
 class NormOut(NamedTuple):
     y: torch.Tensor
@@ -59,6 +67,41 @@ class RouteOut(NamedTuple):
     counts: torch.Tensor     # [experts + 1] int32: picks of each expert, then routed tokens
     mean_prob: torch.Tensor  # [experts] fp32
     loss: torch.Tensor       # fp32 scalar
+
+
+class ScanOut(NamedTuple):
+    h: torch.Tensor          # the state behind each token, in x's type
+    state: torch.Tensor      # [..., dim] fp32: the state behind the last token
+
+
+class ScanGrad(NamedTuple):
+    dgate: Optional[torch.Tensor]
+    dx: Optional[torch.Tensor]
+    dstate: Optional[torch.Tensor]     # of the state before the first token
+
+
+class HeadsOut(NamedTuple):
+    q: torch.Tensor
+    k: Optional[torch.Tensor]
+
+
+class HeadsGrad(NamedTuple):
+    dq: Optional[torch.Tensor]
+    dk: Optional[torch.Tensor]
+    dq_weight: Optional[torch.Tensor]
+    dk_weight: Optional[torch.Tensor]
+
+
+class LogProbsOut(NamedTuple):
+    log_probs: torch.Tensor  # fp32, one a token, 0 for an ignored one
+    lse: torch.Tensor        # fp32: logarithm of the softmax's sum
+
+
+class PolicyOut(NamedTuple):
+    loss: torch.Tensor       # fp32 scalars: the loss,
+    kl: torch.Tensor         # its KL term before kl's factor,
+    clipped: torch.Tensor    # the share of clipped tokens
+    weights: torch.Tensor    # [...] fp32: weight of each token of a sequence
 
 
 class RandomCounter:
@@ -84,6 +127,13 @@ class RandomCounter:
         return at
 
 
+_ENTRY_POINTS = (
+    "muon_layer_norm", "muon_layer_norm_backward", "muon_layer_norm_workspace_bytes", "muon_dropout",
+    "muon_route", "muon_route_workspace_bytes", "muon_route_backward", "muon_gated_scan",
+    "muon_gated_scan_backward", "muon_norm_rotate_heads", "muon_norm_rotate_heads_backward",
+    "muon_norm_rotate_heads_workspace_bytes", "muon_token_log_probs", "muon_token_log_probs_backward",
+    "muon_policy_loss", "muon_policy_loss_backward", "muon_policy_loss_workspace_bytes")
+
 _bound = None
 
 
@@ -101,9 +151,7 @@ def _b():
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         module.bind({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
-                     for name in ("muon_layer_norm", "muon_layer_norm_backward",
-                                  "muon_layer_norm_workspace_bytes", "muon_dropout", "muon_route",
-                                  "muon_route_workspace_bytes", "muon_route_backward")})
+                     for name in _ENTRY_POINTS})
         _bound = module
     return _bound
 
@@ -300,3 +348,282 @@ def route(logits, k: int, *, token_mask=None, normalize: bool = True) -> RouteOu
     weights and from the balance loss."""
     mask = None if token_mask is None else token_mask.contiguous()
     return RouteOut(*_Route.apply(_as_rows(logits), k, mask, normalize))
+
+
+# ---------------------------------------------------------------- over sequences
+
+def gated_scan_forward(gate, x, *, state=None, starts=None, token_mask=None, mix: bool = True,
+                       stream=None) -> ScanOut:
+    """muon_gated_scan over x [..., tokens, dim]: h = a p + (1 - a) x (or a p + x
+    without `mix`) with a = sigmoid(gate) and p the state before the token, 0
+    where the token starts over.  state: [..., dim] fp32, the state before the
+    first token.  starts, token_mask: bool or uint8, one a token; masked tokens
+    pass the state on."""
+    if stream is not None:
+        return _on(stream, gated_scan_forward, (gate, x),
+                   dict(state=state, starts=starts, token_mask=token_mask, mix=mix))
+    r = (_bound or _b()).gated_scan_forward(gate, x, state, starts, token_mask, mix)
+    if type(r) is int:
+        _check(r, "muon_gated_scan")
+    return ScanOut._make(r)
+
+
+def gated_scan_backward(dh, gate, x, h, *, state=None, dstate=None, starts=None, token_mask=None,
+                        mix: bool = True, need_gate: bool = True, need_x: bool = True,
+                        need_state: bool = True, stream=None) -> ScanGrad:
+    """muon_gated_scan_backward: gradients of gate, x and the state before the
+    first token from those of h and (dstate) of the last state; h and the
+    flags are the forward pass's.  x is not read without `mix` and may be None."""
+    if stream is not None:
+        return _on(stream, gated_scan_backward, (dh, gate, x, h),
+                   dict(state=state, dstate=dstate, starts=starts, token_mask=token_mask, mix=mix,
+                        need_gate=need_gate, need_x=need_x, need_state=need_state))
+    r = (_bound or _b()).gated_scan_backward(dh, gate, x, h, state, dstate, starts, token_mask, mix,
+                                             need_gate, need_x, need_state)
+    if type(r) is int:
+        _check(r, "muon_gated_scan_backward")
+    return ScanGrad._make(r)
+
+
+class _GatedScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, gate, x, state, starts, token_mask, mix):
+        o = gated_scan_forward(gate, x, state=state, starts=starts, token_mask=token_mask, mix=mix)
+        ctx.save_for_backward(gate, x if mix else None, o.h, state, starts, token_mask)
+        ctx.mix = mix
+        ctx.set_materialize_grads(False)
+        return o.h, o.state
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dh, dstate):
+        if dh is None and dstate is None:
+            return (None,) * 6
+        gate, x, h, state, starts, token_mask = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        g = gated_scan_backward(torch.zeros_like(h) if dh is None else _as_rows(dh), gate, x, h,
+                                state=state, dstate=None if dstate is None else dstate.contiguous(),
+                                starts=starts, token_mask=token_mask, mix=ctx.mix, need_gate=need[0],
+                                need_x=need[1], need_state=need[2])
+        return g.dgate, g.dx, g.dstate, None, None, None
+
+
+def gated_scan(gate, x, *, state=None, starts=None, token_mask=None, mix: bool = True) -> ScanOut:
+    """Differentiable gated linear recurrence: gradients flow to gate, x and
+    state, from h and from the last state."""
+    dense = [None if t is None else t.contiguous() for t in (state, starts, token_mask)]
+    return ScanOut(*_GatedScan.apply(_as_rows(gate), _as_rows(x), *dense, mix))
+
+
+def rotation_table(length: int, rotary: int, *, base: float = 10000.0, device="cuda"):
+    """(cos, sin) of the angles position * base ** (-2 m / rotary), [length, rotary / 2]
+    fp32, from 64-bit angles: a program makes it once and hands it to
+    norm_rotate_heads."""
+    if rotary < 0 or rotary % 2:
+        raise ValueError("rotary must be even and not negative, got %d" % rotary)
+    pairs = torch.arange(rotary // 2, dtype=torch.float64, device=device)
+    angle = torch.arange(length, dtype=torch.float64, device=device)[:, None] * \
+        base ** (-2.0 * pairs / max(rotary, 1))
+    return angle.cos().float(), angle.sin().float()
+
+
+def norm_rotate_heads_forward(q, k=None, q_weight=None, k_weight=None, *, cos=None, sin=None,
+                              positions=None, eps: float = 1e-6, neighbours: bool = False,
+                              stream=None) -> HeadsOut:
+    """muon_norm_rotate_heads: RMS norm of each head of q and k [..., heads, dim]
+    over its elements, times the weights [dim], and the rotation of the first
+    2 * cos.shape[1] elements by the angles of the tokens' positions (rows of
+    cos and sin [table, pairs]; int64, one a token; without them a token's index
+    in the last dimension of the tokens).  Pairs are elements m and m + pairs, or
+    2 m and 2 m + 1 (neighbours).  A token whose position is outside of the table is
+    none: its heads are 0."""
+    if stream is not None:
+        return _on(stream, norm_rotate_heads_forward, (q, k, q_weight, k_weight),
+                   dict(cos=cos, sin=sin, positions=positions, eps=eps, neighbours=neighbours))
+    r = (_bound or _b()).norm_rotate_heads_forward(q, k, q_weight, k_weight, cos, sin, positions, eps,
+                                                   neighbours)
+    if type(r) is int:
+        _check(r, "muon_norm_rotate_heads")
+    return HeadsOut._make(r)
+
+
+def norm_rotate_heads_backward(dq, dk, q, k=None, q_weight=None, k_weight=None, *, cos=None, sin=None,
+                               positions=None, eps: float = 1e-6, neighbours: bool = False,
+                               need_q: bool = True, need_k: bool = True, need_q_weight: bool = True,
+                               need_k_weight: bool = True, stream=None) -> HeadsGrad:
+    """muon_norm_rotate_heads_backward: gradients of q, k and (where needed) of
+    the weights, in the weights' type (fp32 without weights), from those of the
+    forward pass's outputs; everything else as in the forward pass."""
+    if stream is not None:
+        return _on(stream, norm_rotate_heads_backward, (dq, dk, q, k, q_weight, k_weight),
+                   dict(cos=cos, sin=sin, positions=positions, eps=eps, neighbours=neighbours,
+                        need_q=need_q, need_k=need_k, need_q_weight=need_q_weight,
+                        need_k_weight=need_k_weight))
+    r = (_bound or _b()).norm_rotate_heads_backward(q, k, q_weight, k_weight, cos, sin, positions, eps,
+                                                    neighbours, dq, dk, need_q, need_k, need_q_weight,
+                                                    need_k_weight)
+    if type(r) is int:
+        _check(r, "muon_norm_rotate_heads_backward")
+    return HeadsGrad._make(r)
+
+
+def _as_heads(t: torch.Tensor) -> torch.Tensor:
+    """t, or a dense copy when its strides are not those of heads of tokens."""
+    return t if _b().is_heads(t) else t.contiguous()
+
+
+class _NormRotateHeads(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, eps, neighbours):
+        o = norm_rotate_heads_forward(q, k, q_weight, k_weight, cos=cos, sin=sin, positions=positions,
+                                      eps=eps, neighbours=neighbours)
+        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
+        ctx.how = dict(eps=eps, neighbours=neighbours)
+        ctx.set_materialize_grads(False)
+        return o.q, o.k
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk):
+        if dq is None and dk is None:
+            return (None,) * 9
+        q, k, q_weight, k_weight, cos, sin, positions = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dq = torch.zeros_like(q) if dq is None else _as_heads(dq)
+        if k is not None:
+            dk = torch.zeros_like(k) if dk is None else _as_heads(dk)
+        g = norm_rotate_heads_backward(dq, dk, q, k, q_weight, k_weight, cos=cos, sin=sin,
+                                       positions=positions, need_q=need[0], need_k=need[1],
+                                       need_q_weight=need[2], need_k_weight=need[3], **ctx.how)
+        return g.dq, g.dk, g.dq_weight, g.dk_weight, None, None, None, None, None
+
+
+def norm_rotate_heads(q, k=None, q_weight=None, k_weight=None, *, cos=None, sin=None, positions=None,
+                      eps: float = 1e-6, neighbours: bool = False) -> HeadsOut:
+    """Differentiable norms of query and key heads with the rotation of
+    positions."""
+    if positions is not None:
+        positions = positions.contiguous()
+    return HeadsOut(*_NormRotateHeads.apply(_as_heads(q), None if k is None else _as_heads(k), q_weight,
+                                            k_weight, cos, sin, positions, eps, neighbours))
+
+
+def token_log_probs_forward(logits, tokens, *, scale: float = 1.0, stream=None) -> LogProbsOut:
+    """muon_token_log_probs: log softmax(scale * logits) [..., vocab] at the
+    given tokens (int64, one a row), and the logarithm of the softmax's sum.  A
+    token outside of the vocabulary (-100, say) is ignored: 0."""
+    if stream is not None:
+        return _on(stream, token_log_probs_forward, (logits, tokens), dict(scale=scale))
+    r = (_bound or _b()).token_log_probs_forward(logits, tokens, scale)
+    if type(r) is int:
+        _check(r, "muon_token_log_probs")
+    return LogProbsOut._make(r)
+
+
+def token_log_probs_backward(dlog_probs, logits, tokens, lse, *, scale: float = 1.0, out=None,
+                             stream=None) -> torch.Tensor:
+    """muon_token_log_probs_backward: gradient of the logits.  `out` may be
+    the logits themselves, which it then replaces; writing to it counts as an
+    in-place change, and while gradients are recorded an `out` that requires
+    grad is refused."""
+    if stream is not None:
+        return _on(stream, token_log_probs_backward, (dlog_probs, logits, tokens, lse),
+                   dict(scale=scale, out=out))
+    r = (_bound or _b()).token_log_probs_backward(dlog_probs, logits, tokens, lse, scale, out)
+    if type(r) is int:
+        _check(r, "muon_token_log_probs_backward")
+    return r
+
+
+class _TokenLogProbs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, tokens, scale):
+        o = token_log_probs_forward(logits, tokens, scale=scale)
+        ctx.save_for_backward(logits, tokens, o.lse)
+        ctx.scale = scale
+        ctx.mark_non_differentiable(o.lse)
+        ctx.set_materialize_grads(False)
+        return o.log_probs, o.lse
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dlog_probs, _lse):
+        if dlog_probs is None:
+            return None, None, None
+        logits, tokens, lse = ctx.saved_tensors
+        return token_log_probs_backward(dlog_probs.contiguous(), logits, tokens, lse,
+                                        scale=ctx.scale), None, None
+
+
+def token_log_probs(logits, tokens, *, scale: float = 1.0) -> torch.Tensor:
+    """Differentiable log probabilities of given tokens, fp32, one a row.  Minus
+    their mean is the cross entropy."""
+    return _TokenLogProbs.apply(_as_rows(logits), tokens.contiguous(), scale)[0]
+
+
+def policy_loss_forward(log_probs, old_log_probs, advantages, *, ref_log_probs=None, token_mask=None,
+                        clip_low: float = 0.2, clip_high: float = 0.2, kl: float = 0.0,
+                        by_sequence: bool = False, stream=None) -> PolicyOut:
+    """muon_policy_loss over fp32 [..., tokens]: the clipped surrogate of the
+    ratios exp(log_probs - old_log_probs) times the advantages (one a token, or
+    one a sequence) plus kl times the KL estimate against ref_log_probs, as
+    a mean over all tokens that count, or over sequences of the means over
+    theirs.  token_mask (bool or uint8, one a token): tokens that count."""
+    if stream is not None:
+        return _on(stream, policy_loss_forward, (log_probs, old_log_probs, advantages),
+                   dict(ref_log_probs=ref_log_probs, token_mask=token_mask, clip_low=clip_low,
+                        clip_high=clip_high, kl=kl, by_sequence=by_sequence))
+    r = (_bound or _b()).policy_loss_forward(log_probs, old_log_probs, advantages, ref_log_probs,
+                                             token_mask, clip_low, clip_high, kl, by_sequence)
+    if type(r) is int:
+        _check(r, "muon_policy_loss")
+    return PolicyOut._make(r)
+
+
+def policy_loss_backward(log_probs, old_log_probs, advantages, weights, *, dloss=None,
+                         ref_log_probs=None, token_mask=None, clip_low: float = 0.2,
+                         clip_high: float = 0.2, kl: float = 0.0, stream=None) -> torch.Tensor:
+    """muon_policy_loss_backward: gradient of log_probs; weights are the
+    forward pass's, dloss an fp32 scalar on the device (None: 1)."""
+    if stream is not None:
+        return _on(stream, policy_loss_backward, (log_probs, old_log_probs, advantages, weights),
+                   dict(dloss=dloss, ref_log_probs=ref_log_probs, token_mask=token_mask,
+                        clip_low=clip_low, clip_high=clip_high, kl=kl))
+    r = (_bound or _b()).policy_loss_backward(log_probs, old_log_probs, advantages, ref_log_probs,
+                                              token_mask, clip_low, clip_high, kl, weights, dloss)
+    if type(r) is int:
+        _check(r, "muon_policy_loss_backward")
+    return r
+
+
+class _PolicyLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, log_probs, old, advantages, ref, token_mask, clip_low, clip_high, kl, by_sequence):
+        ctx.how = dict(clip_low=clip_low, clip_high=clip_high, kl=kl)
+        o = policy_loss_forward(log_probs, old, advantages, ref_log_probs=ref, token_mask=token_mask,
+                                by_sequence=by_sequence, **ctx.how)
+        ctx.save_for_backward(log_probs, old, advantages, ref, token_mask, o.weights)
+        ctx.mark_non_differentiable(o.kl, o.clipped, o.weights)
+        ctx.set_materialize_grads(False)
+        return o.loss, o.kl, o.clipped, o.weights
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss, _kl, _clipped, _weights):
+        if dloss is None:
+            return (None,) * 9
+        log_probs, old, advantages, ref, token_mask, weights = ctx.saved_tensors
+        return (policy_loss_backward(log_probs, old, advantages, weights, dloss=dloss.contiguous(),
+                                     ref_log_probs=ref, token_mask=token_mask, **ctx.how),) + (None,) * 8
+
+
+def policy_loss(log_probs, old_log_probs, advantages, *, ref_log_probs=None, token_mask=None,
+                clip_low: float = 0.2, clip_high: float = 0.2, kl: float = 0.0,
+                by_sequence: bool = False) -> PolicyOut:
+    """Differentiable clipped policy loss: gradients flow from the loss to
+    log_probs; old and reference log probabilities and advantages are constants."""
+    rows = [_as_rows(t) for t in (log_probs, old_log_probs)]
+    advantages = _as_rows(advantages) if advantages.shape == log_probs.shape else advantages.contiguous()
+    ref = None if ref_log_probs is None else _as_rows(ref_log_probs)
+    mask = None if token_mask is None else token_mask.contiguous()
+    return PolicyOut(*_PolicyLoss.apply(*rows, advantages, ref, mask, clip_low, clip_high, kl, by_sequence))
