@@ -16,6 +16,22 @@ struct Scan {
   float* last;
 };
 
+// a = sigmoid(g), 1 - a, and the input's part of the step
+struct Step { Quad keep, lose, in; };
+__device__ __forceinline__ Step step_of(const Quad& g, const Quad& x, float mix) {
+  Step s;
+  #pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float2 t = mul2(g.v[j], both(-1.4426950408889634f));
+    t = add2(make_float2(exp2_fast(t.x), exp2_fast(t.y)), both(1.f));
+    s.keep.v[j] = make_float2(reciprocal_fast(t.x), reciprocal_fast(t.y));
+    // 1 - a of the rounded a: a constant input then comes out unchanged
+    s.lose.v[j] = fma2(s.keep.v[j], both(-1.f), both(1.f));
+    s.in.v[j] = mul2(fma2(s.keep.v[j], both(-mix), both(1.f)), x.v[j]);
+  }
+  return s;
+}
+
 // W warps a block, S tokens a segment, CL blocks a cluster, D chunks in flight (0: a
 // chunk is read when it is needed)
 template <typename T, int W, int S, int CL, int D, bool VEC, bool FLAGS>
@@ -29,21 +45,33 @@ scan_kernel(const __grid_constant__ Scan a) {
   const int64_t unit = blockIdx.x / CL, b = unit / a.strips;
   const Channels<VEC> ch((int)(unit % a.strips), a.dim);
   const int64_t row0 = b * a.length;
-  const T* gate = static_cast<const T*>(a.gate) + row0 * a.ldg + ch.first;
-  const T* x = static_cast<const T*>(a.x) + row0 * a.ldx + ch.first;
-  T* h = static_cast<T*>(a.h) + row0 * a.dim + ch.first;
-  Quad carry = a.state ? ch.state(a.state + b * a.dim + ch.first) : quad(0.f);
-  const int seg = threadIdx.x >> 4;
+  const int seg = threadIdx.x >> 4, length = (int)a.length;
+  const int64_t stride = (int64_t)kSpan * CL;
+  // the chunk to read next and the one to write, at the lane's first channel
+  const T* gate = static_cast<const T*>(a.gate) + (row0 + rank * kSpan) * a.ldg + ch.first;
+  const T* x = static_cast<const T*>(a.x) + (row0 + rank * kSpan) * a.ldx + ch.first;
+  T* h = static_cast<T*>(a.h) + (row0 + rank * kSpan + seg * S) * a.dim + ch.first;
+  int left_in = length - rank * kSpan - seg * S, left = left_in;    // tokens from the segment's first on
+  gate += seg * S * a.ldg;
+  x += seg * S * a.ldx;
+  if (threadIdx.x < 16)
+    sh.carry[0][threadIdx.x] = four(a.state ? ch.state(a.state + b * a.dim + ch.first) : quad(0.f));
   Raw4<T>* const slots = reinterpret_cast<Raw4<T>*>(ring) + threadIdx.x;
   Flags ahead[D > 0 ? D : 1];
-  const int64_t first = (int64_t)rank * kSpan + seg * S, stride = (int64_t)kSpan * CL;
-  auto start = [&](int64_t t0, int stage) {
+  auto ask_next = [&] { return ask<S>(a.starts, a.mask, row0, length - left_in, length); };
+  auto advance = [&] {
+    gate += stride * a.ldg;
+    x += stride * a.ldx;
+    left_in -= (int)stride;
+  };
+  auto start = [&](int stage) {
+    const int n = ch.any() ? left_in : 0;
     #pragma unroll
     for (int i = 0; i < S; ++i) {
       Raw4<T>* const to = slots + (stage * 2 * S + i) * NT;
-      if (t0 + i < a.length && ch.any()) {
-        ch.copy(to, gate + (t0 + i) * a.ldg);
-        ch.copy(to + S * NT, x + (t0 + i) * a.ldx);
+      if (i < n) {
+        ch.copy(to, gate + i * a.ldg);
+        ch.copy(to + S * NT, x + i * a.ldx);
       } else {
         infinite(to[0]);
         zero(to[S * NT]);
@@ -53,31 +81,33 @@ scan_kernel(const __grid_constant__ Scan a) {
   };
   #pragma unroll
   for (int d = 0; d < D; ++d) {
-    start(first + d * stride, d);
-    if (FLAGS) ahead[d] = ask<S>(a.starts, a.mask, row0, first + d * stride, a.length);
+    start(d);
+    if (FLAGS) ahead[d] = ask_next();
+    advance();
   }
   if (CL > 1) cluster_barrier();      // every block has begun before one writes to another
-  int round = 0, stage = 0;
-  int64_t t0 = first;
-  for (int64_t done = 0; done < a.length; done += stride, t0 += stride, ++round) {
-    if (FLAGS && D == 0) ahead[0] = ask<S>(a.starts, a.mask, row0, t0, a.length);
+  int stage = 0;
+  const int rounds = (int)((a.length + stride - 1) / stride);
+  for (int round = 0; round < rounds; ++round) {
     Raw4<T> rg[S], rx[S];
     if constexpr (D > 0) {
       copies_wait<D - 1>();
     } else {
+      if (FLAGS) ahead[0] = ask_next();
+      const int n = ch.any() ? left_in : 0;
       #pragma unroll
       for (int i = 0; i < S; ++i) {
         infinite(rg[i]);
         zero(rx[i]);
-        if (t0 + i < a.length && ch.any()) {
-          ch.load(rg[i], gate + (t0 + i) * a.ldg);
-          ch.load(rx[i], x + (t0 + i) * a.ldx);
+        if (i < n) {
+          ch.load(rg[i], gate + i * a.ldg);
+          ch.load(rx[i], x + i * a.ldx);
         }
       }
+      advance();
     }
     Quad P[S], H[S];
-    Run run = {quad(1.f), quad(0.f), false};       // m: the factor, until the end
-    Quad lost = quad(0.f);                          // 1 minus it
+    Segment run = {quad(1.f), quad(0.f), quad(0.f), false};
     const Flags now = FLAGS ? bits(ahead[0]) : Flags{0, 0};
     #pragma unroll
     for (int i = 0; i < S; ++i) {
@@ -93,44 +123,89 @@ scan_kernel(const __grid_constant__ Scan a) {
         infinite(gi);
         zero(vi);
       }
-      const Quad g = widen(gi), xi = widen(vi);
-      Quad k, u, in;
-      #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float2 t = mul2(g.v[j], both(-1.4426950408889634f));
-        t = add2(make_float2(exp2_fast(t.x), exp2_fast(t.y)), both(1.f));
-        k.v[j] = make_float2(reciprocal_fast(t.x), reciprocal_fast(t.y));
-        u.v[j] = fma2(k.v[j], both(-1.f), both(1.f));
-        in.v[j] = mul2(fma2(u.v[j], both(a.mix), both(1.f - a.mix)), xi.v[j]);
-      }
+      const Step st = step_of(widen(gi), widen(vi), a.mix);
       if (FLAGS && (now.starts >> i & 1)) {
-        run.m = run.H = quad(0.f);
+        run.P = run.H = quad(0.f);
         run.cut = true;
       }
-      run.m = mul(run.m, k);
-      run.H = fma(k, run.H, in);
-      lost = fma(k, lost, u);
-      P[i] = run.m;
-      H[i] = run.H;
+      P[i] = run.P = mul(run.P, st.keep);
+      H[i] = run.H = fma(st.keep, run.H, st.in);
+      run.Q = fma(st.keep, run.Q, st.lose);
     }
-    run.m = shares(run.m, lost);
     if constexpr (D > 0) {
-      start(t0 + D * stride, stage);
+      start(stage);
       stage = stage + 1 == D ? 0 : stage + 1;
       if (FLAGS) {
         #pragma unroll
         for (int d = 0; d + 1 < D; ++d) ahead[d] = ahead[d + 1];
-        ahead[D - 1] = ask<S>(a.starts, a.mask, row0, t0 + D * stride, a.length);
+        ahead[D - 1] = ask_next();
       }
+      advance();
     }
-    Quad front = join_runs<W, CL, FLAGS, false>(sh, run, carry, round);
+    Quad front = join_segments<W, CL, FLAGS, false>(sh, run, round);
+    const int n = ch.any() ? left : 0;
     #pragma unroll
     for (int i = 0; i < S; ++i) {
       if (FLAGS && (now.starts >> i & 1)) front = quad(0.f);
-      if (t0 + i < a.length && ch.any()) ch.store(h + (t0 + i) * a.dim, fma(P[i], front, H[i]));
+      if (i < n) ch.store(h + i * a.dim, fma(P[i], front, H[i]));
+    }
+    h += stride * a.dim;
+    left -= (int)stride;
+  }
+  if (a.last && rank == 0) {
+    __syncthreads();
+    if (threadIdx.x < 16) ch.put_state(a.last + b * a.dim + ch.first, quad(sh.carry[rounds & 1][threadIdx.x]));
+  }
+}
+
+constexpr int kShortThreads = 128, kShortAhead = 4;
+// Short sequences: 16 lanes walk a strip's tokens, four of them in flight
+template <typename T, bool VEC, bool FLAGS>
+__global__ void __launch_bounds__(kShortThreads) scan_short_kernel(const __grid_constant__ Scan a, int64_t units) {
+  pdl_wait();
+  const int64_t unit = (int64_t)blockIdx.x * (kShortThreads / 16) + (threadIdx.x >> 4);
+  if (unit >= units) return;
+  const int64_t b = unit / a.strips, row0 = b * a.length;
+  const Channels<VEC> ch((int)(unit % a.strips), a.dim);
+  if (!ch.any()) return;
+  const int length = (int)a.length;
+  const T* gate = static_cast<const T*>(a.gate) + row0 * a.ldg + ch.first;
+  const T* x = static_cast<const T*>(a.x) + row0 * a.ldx + ch.first;
+  T* h = static_cast<T*>(a.h) + row0 * a.dim + ch.first;
+  Quad p = a.state ? ch.state(a.state + b * a.dim + ch.first) : quad(0.f);
+  for (int t0 = 0; t0 < length; t0 += kShortAhead) {
+    Raw4<T> rg[kShortAhead], rx[kShortAhead];
+    bool live[kShortAhead], begins[kShortAhead];
+    #pragma unroll
+    for (int i = 0; i < kShortAhead; ++i) {
+      const int t = t0 + i;
+      if (t >= length) continue;
+      ch.load(rg[i], gate + t * a.ldg);
+      ch.load(rx[i], x + t * a.ldx);
+      if (FLAGS) {
+        live[i] = !a.mask || a.mask[row0 + t];
+        begins[i] = a.starts && a.starts[row0 + t];
+      }
+    }
+    #pragma unroll
+    for (int i = 0; i < kShortAhead; ++i) {
+      const int t = t0 + i;
+      if (t >= length) continue;
+      const Step st = step_of(widen(rg[i]), widen(rx[i]), a.mix);
+      Quad q = p;
+      if (FLAGS && begins[i]) q = quad(0.f);
+      q = fma(st.keep, q, st.in);
+      if (!FLAGS || live[i]) p = q;
+      ch.store(h + t * a.dim, p);
     }
   }
-  if (a.last && rank == 0 && seg == 0) ch.put_state(a.last + b * a.dim + ch.first, carry);
+  if (a.last) ch.put_state(a.last + b * a.dim + ch.first, p);
+}
+
+template <typename T, bool VEC> cudaError_t scan_short(const Scan& a, int64_t strips, cudaStream_t s) {
+  constexpr int per = kShortThreads / 16;
+  return launch_k(a.starts || a.mask ? scan_short_kernel<T, VEC, true> : scan_short_kernel<T, VEC, false>,
+                  dim3((unsigned)((strips + per - 1) / per)), dim3(kShortThreads), 0, s, true, a, strips);
 }
 
 template <typename T, int W, int S, int CL, int D, bool VEC>
@@ -147,11 +222,12 @@ cudaError_t scan_with(const Scan& a, int64_t strips, cudaStream_t s) {
 
 template <typename T, bool VEC> cudaError_t scan_by_size(const Scan& a, int64_t strips, cudaStream_t s) {
   constexpr int S = sizeof(T) == 2 ? 8 : 4, D = VEC ? 3 : 0;
+  if (a.length <= 4 || (a.length <= 32 && strips >= 2048)) return scan_short<T, VEC>(a, strips, s);
   if (a.length <= 2 * S) return scan_with<T, 1, S, 1, 0, VEC>(a, strips, s);
   if (a.length <= 8 * S) return scan_with<T, 4, S, 1, 0, VEC>(a, strips, s);
   if (strips >= 304 || a.length <= 16 * S) return scan_with<T, 8, S, 1, D, VEC>(a, strips, s);
-  if (strips >= 76 || a.length <= 64 * S) return scan_with<T, 8, S, 4, D, VEC>(a, strips, s);
-  return scan_with<T, 8, S, 8, D, VEC>(a, strips, s);
+  if (strips >= 76 || a.length <= 64 * S) return scan_with<T, 8, S, 4, VEC ? 2 : 0, VEC>(a, strips, s);
+  return scan_with<T, 8, S, 8, VEC ? 2 : 0, VEC>(a, strips, s);
 }
 
 }  // namespace

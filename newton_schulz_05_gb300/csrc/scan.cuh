@@ -176,62 +176,59 @@ template <bool VEC> struct Channels {
   }
 };
 
-// A run of tokens as a map of the state p in front of it: H + P p.  Where P is 1/2 or
-// more, m is -(1 - P), with its sign bit set, and the map is p + (H + m p); else m is P.
-// 1 - P decides how much of the state a long run forgets, and P has no bits for it: with
-// P alone, 3000 tokens of the gate 8 took a constant state off by 1.6e-5 of itself.
+// A run of tokens as a map of the state p in front of it, H + (k + m) p: where its
+// factor P is 1/2 or more, k is 1 and m is -(1 - P), else k is 0 and m is P.  1 - P
+// decides how much of the state a long run forgets, and P has no bits for it: with P
+// alone, 3000 tokens of the gate 8 took a constant state off by 1.6e-5 of itself.
 // cut: some token of the run starts over, and H is the state whatever p was.
 struct Run {
-  Quad m, H;
+  Quad m, k, H;
   bool cut;
 };
-__device__ __forceinline__ bool keeps(float m) { return __float_as_int(m) < 0; }
-// from P and 1 - P
-__device__ __forceinline__ Quad shares(const Quad& P, const Quad& Q) {
-  Quad m;
-  #pragma unroll
-  for (int j = 0; j < 2; ++j)
-    m.v[j] = make_float2(P.v[j].x >= 0.5f ? -Q.v[j].x : P.v[j].x, P.v[j].y >= 0.5f ? -Q.v[j].y : P.v[j].y);
-  return m;
-}
 __device__ __forceinline__ Quad apply(const Run& r, const Quad& p) {
-  Quad q = fma(r.m, p, r.H), base;
-  #pragma unroll
-  for (int j = 0; j < 2; ++j)
-    base.v[j] = make_float2(keeps(r.m.v[j].x) ? p.v[j].x : 0.f, keeps(r.m.v[j].y) ? p.v[j].y : 0.f);
-  q = add(q, base);
+  Quad q = fma(r.k, p, fma(r.m, p, r.H));
   if (r.cut) q = r.H;
   return q;
 }
-// the share of two runs, one after the other
-__device__ __forceinline__ float both_shares(float a, float b) {
-  const bool ka = keeps(a), kb = keeps(b);
-  // (1 + a)(1 + b) - 1, a (1 + b), (1 + a) b or a b
-  const float m = fmaf(a, b, (kb ? a : 0.f) + (ka ? b : 0.f));
-  return ka && kb ? (m < -0.5f ? 1.f + m : -fabsf(m)) : m;
-}
-// first `a`, then `b`
+// first `a`, then `b`: (k + m) (k' + m') = k k' + the rest
 __device__ __forceinline__ Run then(const Run& a, const Run& b) {
+  return {fma(a.m, b.k, fma(a.k, b.m, mul(a.m, b.m))), mul(a.k, b.k), apply(b, a.H), a.cut || b.cut};
+}
+// a segment's factor, 1 minus it, and what its tokens add.  Both are sums of positive
+// terms, so each keeps its own precision.
+struct Segment {
+  Quad P, Q, H;
+  bool cut;
+};
+__device__ __forceinline__ Run run_of(const Segment& g) {
   Run r;
   #pragma unroll
-  for (int j = 0; j < 2; ++j)
-    r.m.v[j] = make_float2(both_shares(a.m.v[j].x, b.m.v[j].x), both_shares(a.m.v[j].y, b.m.v[j].y));
-  r.H = apply(b, a.H);
-  r.cut = a.cut || b.cut;
+  for (int j = 0; j < 2; ++j) {
+    const bool x = g.P.v[j].x >= 0.5f, y = g.P.v[j].y >= 0.5f;
+    r.m.v[j] = make_float2(x ? -g.Q.v[j].x : g.P.v[j].x, y ? -g.Q.v[j].y : g.P.v[j].y);
+    r.k.v[j] = make_float2(x ? 1.f : 0.f, y ? 1.f : 0.f);
+  }
+  r.H = g.H;
+  r.cut = g.cut;
   return r;
 }
 
 // what the runs of a block's warps, and of a cluster's blocks, are exchanged through
+struct RunSlot { float4 m[16], k[16], H[16]; };
 template <int W, int CL> struct RunSlots {
-  float4 m[2][W][16], H[2][W][16];
-  float4 cm[2][CL][16], cH[2][CL][16];
-  int cut[2][W], ccut[2][CL];
+  RunSlot warp[2][W], block[2][CL];
+  float4 carry[2][16];
+  int cut[2][W], block_cut[2][CL];
 };
 __device__ __forceinline__ float4 four(const Quad& q) {
   return make_float4(q.v[0].x, q.v[0].y, q.v[1].x, q.v[1].y);
 }
 __device__ __forceinline__ Quad quad(const float4& f) {
   return {{make_float2(f.x, f.y), make_float2(f.z, f.w)}};
+}
+__device__ __forceinline__ Run run_in(const RunSlot& s, int cut) {
+  const int l = threadIdx.x & 15;
+  return {quad(s.m[l]), quad(s.k[l]), quad(s.H[l]), cut != 0};
 }
 
 __device__ __forceinline__ void cluster_barrier() {
@@ -258,70 +255,83 @@ __device__ __forceinline__ void put_at(uint32_t to, int v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(v) : "memory");
 }
 
-// Joins the segments of a chunk in the order of `mine`: half warp 0 of warp 0 first, and
-// blocks of a cluster by rank.  carry: the state in front of the chunk, replaced by the one
-// behind it.  Returns the state in front of the thread's segment.  `round` counts up.
-// BACK: in the opposite order (last segment of the last warp first; ranks as before).
-template <int W, int CL, bool FLAGS, bool BACK>
-__device__ __forceinline__ Quad join_runs(RunSlots<W, CL>& sh, Run mine, Quad& carry, int round) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & 15, buf = round & 1;
-  const bool second = BACK ? lane < 16 : lane >= 16;
-  // the other half's run
-  Run other;
+__device__ __forceinline__ Quad from_other_half(const Quad& q) {
+  Quad r;
   #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    other.m.v[j].x = __shfl_xor_sync(~0u, mine.m.v[j].x, 16);
-    other.m.v[j].y = __shfl_xor_sync(~0u, mine.m.v[j].y, 16);
-    other.H.v[j].x = __shfl_xor_sync(~0u, mine.H.v[j].x, 16);
-    other.H.v[j].y = __shfl_xor_sync(~0u, mine.H.v[j].y, 16);
+    r.v[j].x = __shfl_xor_sync(~0u, q.v[j].x, 16);
+    r.v[j].y = __shfl_xor_sync(~0u, q.v[j].y, 16);
   }
-  other.cut = FLAGS ? (bool)__shfl_xor_sync(~0u, (int)mine.cut, 16) : false;
-  if (!FLAGS) mine.cut = false;
-  const Run whole = second ? then(other, mine) : then(mine, other);     // the same in both halves
-  Quad at = carry;
-  if constexpr (W == 1 && CL == 1) {
-    carry = apply(whole, carry);
-  } else {
-    if (second) {
-      sh.m[buf][warp][l] = four(whole.m);
-      sh.H[buf][warp][l] = four(whole.H);
-      if (FLAGS && l == 0) sh.cut[buf][warp] = whole.cut;
-    }
-    __syncthreads();
-    auto warp_run = [&](int w) {
-      return Run{quad(sh.m[buf][w][l]), quad(sh.H[buf][w][l]), FLAGS ? (bool)sh.cut[buf][w] : false};
-    };
-    Quad front = carry;
-    if constexpr (CL > 1) {
-      const int rank = cluster_rank();
-      if (threadIdx.x < 16 * CL) {      // 16 threads for each block of the cluster
-        const int to = threadIdx.x >> 4;
-        Run all = warp_run(BACK ? W - 1 : 0);
-        #pragma unroll
-        for (int i = 1; i < W; ++i) all = then(all, warp_run(BACK ? W - 1 - i : i));
-        put_at(at_rank(&sh.cm[buf][rank][l], to), four(all.m));
-        put_at(at_rank(&sh.cH[buf][rank][l], to), four(all.H));
-        if (FLAGS && l == 0) put_at(at_rank(&sh.ccut[buf][rank], to), (int)all.cut);
-      }
-      cluster_barrier();
+  return r;
+}
+
+// Joins the segments of chunk `round` in order: the first half of warp 0 first, blocks of
+// a cluster by rank.  BACK: the second half of the last warp first, blocks as before.
+// Returns the state in front of the thread's segment.  The state in front of the chunk is
+// read from sh.carry[round & 1] and the one behind it left in the other.  A warp applies
+// only the runs in front of its own; the last one goes on to the state behind the chunk.
+template <int W, int CL, bool FLAGS, bool BACK>
+__device__ __forceinline__ Quad join_segments(RunSlots<W, CL>& sh, const Segment& mine, int round) {
+  const int lane = threadIdx.x & 31, l = lane & 15, buf = round & 1;
+  const int warp = BACK ? W - 1 - (threadIdx.x >> 5) : threadIdx.x >> 5;      // in order
+  const bool second = BACK ? lane < 16 : lane >= 16;
+  Segment other = {from_other_half(mine.P), from_other_half(mine.Q), from_other_half(mine.H), false};
+  if (FLAGS) other.cut = __shfl_xor_sync(~0u, (int)mine.cut, 16) != 0;
+  // both halves' segments as one; right in the second half alone
+  Segment whole = {mul(other.P, mine.P), fma(other.P, mine.Q, other.Q), fma(mine.P, other.H, mine.H), false};
+  if (FLAGS) {
+    whole.cut = other.cut || mine.cut;
+    if (mine.cut) whole.H = mine.H;
+  }
+  const Run run = run_of(whole);
+  if (second) {
+    RunSlot& to = sh.warp[buf][warp];
+    to.m[l] = four(run.m);
+    to.k[l] = four(run.k);
+    to.H[l] = four(run.H);
+    if (FLAGS && l == 0) sh.cut[buf][warp] = run.cut;
+  }
+  if constexpr (W > 1 || CL > 1) __syncthreads();
+  else __syncwarp();
+  auto warp_run = [&](int w) { return run_in(sh.warp[buf][w], FLAGS ? sh.cut[buf][w] : 0); };
+  if constexpr (CL > 1) {
+    const int rank = cluster_rank();
+    if (threadIdx.x < 16 * CL) {      // 16 threads for each block of the cluster
+      const int to = threadIdx.x >> 4;
+      Run all = warp_run(0);
       #pragma unroll
-      for (int c = 0; c < CL; ++c) {
-        if (c == rank) front = carry;
-        carry = apply(Run{quad(sh.cm[buf][c][l]), quad(sh.cH[buf][c][l]), FLAGS ? (bool)sh.ccut[buf][c] : false},
-                      carry);
-      }
+      for (int i = 1; i < W; ++i) all = then(all, warp_run(i));
+      RunSlot& slot = sh.block[buf][rank];
+      put_at(at_rank(&slot.m[l], to), four(all.m));
+      put_at(at_rank(&slot.k[l], to), four(all.k));
+      put_at(at_rank(&slot.H[l], to), four(all.H));
+      if (FLAGS && l == 0) put_at(at_rank(&sh.block_cut[buf][rank], to), (int)all.cut);
     }
-    at = front;
-    #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const int w = BACK ? W - 1 - i : i;
-      if (w == warp) at = front;
-      if (CL == 1 || i + 1 < W) front = apply(warp_run(w), front);
-    }
-    if constexpr (CL == 1) carry = front;
+    cluster_barrier();
   }
-  if (second) at = apply(other, at);
-  return at;
+  Quad p = quad(sh.carry[buf][l]);
+  auto block_run = [&](int c) { return run_in(sh.block[buf][c], FLAGS ? sh.block_cut[buf][c] : 0); };
+  if constexpr (CL > 1) {
+    const int rank = cluster_rank();
+    for (int c = 0; c < rank; ++c) p = apply(block_run(c), p);
+    if (warp == 0) {
+      Quad q = p;
+      for (int c = rank; c < CL; ++c) q = apply(block_run(c), q);
+      if (second) sh.carry[buf ^ 1][l] = four(q);
+    }
+  }
+  for (int w = 0; w < warp; ++w) p = apply(warp_run(w), p);
+  if constexpr (CL == 1) {
+    if (warp == W - 1) {
+      const Quad q = apply(warp_run(warp), p);
+      if (second) sh.carry[buf ^ 1][l] = four(q);
+    }
+  }
+  if (second) {
+    Run first = run_of(other);
+    p = apply(first, p);
+  }
+  return p;
 }
 
 // --------------------------------------------------------------------- host

@@ -17,6 +17,21 @@ struct ScanBwd {
   float* dstate;
 };
 
+// t = 4 exp(-gate); a = 1 / (1 + t / 4), 1 - a = a t / 4, so that both have their own
+// precision.  The 4 makes t infinite before a is flushed to 0, and the minimum drops the
+// NaN of infinity times 0.
+__device__ __forceinline__ void shares_of(const Quad& g, Quad& keep, Quad& take) {
+  #pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float2 t = fma2(g.v[j], both(-1.4426950408889634f), both(2.f));
+    t = make_float2(exp2_fast(t.x), exp2_fast(t.y));
+    const float2 n = fma2(t, both(0.25f), both(1.f));
+    keep.v[j] = make_float2(reciprocal_fast(n.x), reciprocal_fast(n.y));
+    t = mul2(mul2(t, both(0.25f)), keep.v[j]);
+    take.v[j] = make_float2(fminf(t.x, 1.f), fminf(t.y, 1.f));
+  }
+}
+
 template <typename T, int W, int S, int CL, int D, bool VEC, bool FLAGS>
 __global__ void __launch_bounds__(32 * W, W >= 8 ? 2 : 16 / W)
 scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
@@ -27,31 +42,45 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
   const int rank = CL > 1 ? cluster_rank() : 0;      // rank 0 has the last chunk
   const int64_t unit = blockIdx.x / CL, b = unit / a.strips;
   const Channels<VEC> ch((int)(unit % a.strips), a.dim);
-  const int64_t row0 = b * a.length;
-  const T* dh = static_cast<const T*>(a.dh) + row0 * a.lddh + ch.first;
-  const T* gate = static_cast<const T*>(a.gate) + row0 * a.ldg + ch.first;
-  const T* x = static_cast<const T*>(a.x) + row0 * a.ldx + ch.first;
-  const T* h = static_cast<const T*>(a.h) + row0 * a.ldh + ch.first;
-  T* dg = static_cast<T*>(a.dgate) + row0 * a.dim + ch.first;
-  T* dx = static_cast<T*>(a.dx) + row0 * a.dim + ch.first;
+  const int64_t row0 = b * a.length, stride = (int64_t)kSpan * CL;
+  const int seg = threadIdx.x >> 4, length = (int)a.length;
+  const int chunks = (int)((a.length + kSpan - 1) / kSpan), rounds = (chunks + CL - 1) / CL;
+  // the segment's first token (in front of the sequence in the last round of some ranks)
+  // of the chunk to read next, and of the one to write
+  int64_t t_in = (int64_t)(chunks - 1 - rank) * kSpan + seg * S, t0 = t_in;
+  const T* dh = static_cast<const T*>(a.dh) + (row0 + t_in) * a.lddh + ch.first;
+  const T* gate = static_cast<const T*>(a.gate) + (row0 + t_in) * a.ldg + ch.first;
+  const T* x = static_cast<const T*>(a.x) + (row0 + t_in) * a.ldx + ch.first;
+  const T* h = static_cast<const T*>(a.h) + (row0 + t_in - 1) * a.ldh + ch.first;
+  const int64_t out = row0 * a.dim + ch.first;
   const bool mix = a.mix != 0.f;
-  Quad carry = a.dlast ? ch.state(a.dlast + b * a.dim + ch.first) : quad(0.f);
-  const int seg = threadIdx.x >> 4;
+  if (threadIdx.x < 16)
+    sh.carry[0][threadIdx.x] = four(a.dlast ? ch.state(a.dlast + b * a.dim + ch.first) : quad(0.f));
   Raw4<T>* const slots = reinterpret_cast<Raw4<T>*>(ring) + threadIdx.x;
   Flags ahead[D > 0 ? D : 1];
-  const int64_t chunks = (a.length + kSpan - 1) / kSpan, stride = (int64_t)kSpan * CL;
-  const int64_t first = (chunks - 1 - rank) * kSpan + seg * S;
-  auto start = [&](int64_t t0, int stage) {
+  auto ask_next = [&] { return ask<S>(a.starts, a.mask, row0, t_in, length); };
+  auto advance = [&] {
+    dh -= stride * a.lddh;
+    gate -= stride * a.ldg;
+    x -= stride * a.ldx;
+    h -= stride * a.ldh;
+    t_in -= stride;
+  };
+  // how many of a segment's tokens are inside, all from its first on (chunks start at 0)
+  auto inside = [&](int64_t t) {
+    return !ch.any() || t < 0 ? 0 : t + S <= length ? S : (int)(t < length ? length - t : 0);
+  };
+  auto start = [&](int stage) {
+    const int n = inside(t_in);
     #pragma unroll
     for (int i = 0; i < S; ++i) {
-      const int64_t t = t0 + i;
       Raw4<T>* const to = slots + (stage * 4 * S + i) * NT;
-      if (t >= 0 && t < a.length && ch.any()) {
-        ch.copy(to, dh + t * a.lddh);
-        ch.copy(to + S * NT, gate + t * a.ldg);
-        if (mix) ch.copy(to + 2 * S * NT, x + t * a.ldx);
+      if (i < n) {
+        ch.copy(to, dh + i * a.lddh);
+        ch.copy(to + S * NT, gate + i * a.ldg);
+        if (mix) ch.copy(to + 2 * S * NT, x + i * a.ldx);
         else zero(to[2 * S * NT]);
-        if (t > 0) ch.copy(to + 3 * S * NT, h + (t - 1) * a.ldh);
+        if (i > 0 || t_in > 0) ch.copy(to + 3 * S * NT, h + i * a.ldh);
         else zero(to[3 * S * NT]);
       } else {
         zero(to[0]);
@@ -64,36 +93,36 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
   };
   #pragma unroll
   for (int d = 0; d < D; ++d) {
-    start(first - d * stride, d);
-    if (FLAGS) ahead[d] = ask<S>(a.starts, a.mask, row0, first - d * stride, a.length);
+    start(d);
+    if (FLAGS) ahead[d] = ask_next();
+    advance();
   }
   if (CL > 1) cluster_barrier();      // every block has begun before one writes to another
-  int round = 0, stage = 0;
-  int64_t t0 = first;
-  for (int64_t done = 0; done < chunks; done += CL, t0 -= stride, ++round) {
-    if (FLAGS && D == 0) ahead[0] = ask<S>(a.starts, a.mask, row0, t0, a.length);
+  int stage = 0;
+  for (int round = 0; round < rounds; ++round) {
     Raw4<T> rd[S], rg[S], rx[S], rh[S];
     if constexpr (D > 0) {
       copies_wait<D - 1>();
     } else {
+      if (FLAGS) ahead[0] = ask_next();
+      const int n = inside(t_in);
       #pragma unroll
       for (int i = 0; i < S; ++i) {
-        const int64_t t = t0 + i;
         zero(rd[i]);
         infinite(rg[i]);
         zero(rx[i]);
         zero(rh[i]);
-        if (t >= 0 && t < a.length && ch.any()) {
-          ch.load(rd[i], dh + t * a.lddh);
-          ch.load(rg[i], gate + t * a.ldg);
-          if (mix) ch.load(rx[i], x + t * a.ldx);
-          if (t > 0) ch.load(rh[i], h + (t - 1) * a.ldh);
+        if (i < n) {
+          ch.load(rd[i], dh + i * a.lddh);
+          ch.load(rg[i], gate + i * a.ldg);
+          if (mix) ch.load(rx[i], x + i * a.ldx);
+          if (i > 0 || t_in > 0) ch.load(rh[i], h + i * a.ldh);
         }
       }
+      advance();
     }
     Quad keep[S], take[S], d[S], v[S];
-    Run run = {quad(1.f), quad(0.f), false};       // m: the factor, until the end
-    Quad lost = quad(0.f);                          // 1 minus it
+    Segment run = {quad(1.f), quad(0.f), quad(0.f), false};
     const Flags now = FLAGS ? bits(ahead[0]) : Flags{0, 0};
     #pragma unroll
     for (int i = S - 1; i >= 0; --i) {
@@ -111,57 +140,119 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
         hi = rh[i];
       }
       if (FLAGS && !(now.live >> i & 1)) infinite(gi);
-      const Quad g = widen(gi);
-      #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        // t = 4 exp(-gate); a = 1 / (1 + t / 4), 1 - a = a t / 4, so that both have their
-        // own precision.  The 4 makes t infinite before a is flushed to 0, and the minimum
-        // drops the NaN of infinity times 0.
-        float2 t = fma2(g.v[j], both(-1.4426950408889634f), both(2.f));
-        t = make_float2(exp2_fast(t.x), exp2_fast(t.y));
-        const float2 n = fma2(t, both(0.25f), both(1.f));
-        keep[i].v[j] = make_float2(reciprocal_fast(n.x), reciprocal_fast(n.y));
-        t = mul2(mul2(t, both(0.25f)), keep[i].v[j]);
-        take[i].v[j] = make_float2(fminf(t.x, 1.f), fminf(t.y, 1.f));
-      }
+      shares_of(widen(gi), keep[i], take[i]);
       d[i] = widen(di);
       v[i] = widen(hi);
-      if (t0 + i == 0 && a.state && ch.any()) v[i] = ch.state(a.state + b * a.dim + ch.first);
+      if (i == 0 && t0 == 0 && a.state && ch.any()) v[0] = ch.state(a.state + b * a.dim + ch.first);
       if (FLAGS && (now.starts >> i & 1)) v[i] = quad(0.f);
       v[i] = fma(widen(xi), quad(-a.mix), v[i]);
-      run.m = mul(run.m, keep[i]);
+      run.P = mul(run.P, keep[i]);
+      run.Q = fma(keep[i], run.Q, take[i]);
       run.H = mul(keep[i], add(run.H, d[i]));
-      lost = fma(keep[i], lost, take[i]);
       if (FLAGS && (now.starts >> i & 1)) {
-        run.m = run.H = quad(0.f);
+        run.P = run.H = quad(0.f);
         run.cut = true;
       }
     }
-    run.m = shares(run.m, lost);
     if constexpr (D > 0) {
-      start(t0 - D * stride, stage);
+      start(stage);
       stage = stage + 1 == D ? 0 : stage + 1;
       if (FLAGS) {
         #pragma unroll
         for (int k = 0; k + 1 < D; ++k) ahead[k] = ahead[k + 1];
-        ahead[D - 1] = ask<S>(a.starts, a.mask, row0, t0 - D * stride, a.length);
+        ahead[D - 1] = ask_next();
       }
+      advance();
     }
-    Quad c = join_runs<W, CL, FLAGS, true>(sh, run, carry, round);
+    Quad c = join_segments<W, CL, FLAGS, true>(sh, run, round);
+    const int n = inside(t0);
+    T* const dx = static_cast<T*>(a.dx) + out + t0 * a.dim;
+    T* const dg = static_cast<T*>(a.dgate) + out + t0 * a.dim;
     #pragma unroll
     for (int i = S - 1; i >= 0; --i) {
       const Quad l = add(d[i], c), u = mul(take[i], l);
       c = mul(keep[i], l);
       Quad gx = mix ? u : l, gg = mul(mul(u, keep[i]), v[i]);
       if (FLAGS && !(now.live >> i & 1)) gx = gg = quad(0.f);
-      if (t0 + i >= 0 && t0 + i < a.length && ch.any()) {
-        if (a.dx) ch.store(dx + (t0 + i) * a.dim, gx);
-        if (a.dgate) ch.store(dg + (t0 + i) * a.dim, gg);
+      if (i < n) {
+        if (a.dx) ch.store(dx + i * a.dim, gx);
+        if (a.dgate) ch.store(dg + i * a.dim, gg);
       }
       if (FLAGS && (now.starts >> i & 1)) c = quad(0.f);
     }
+    t0 -= stride;
   }
-  if (a.dstate && rank == 0 && seg == 0) ch.put_state(a.dstate + b * a.dim + ch.first, carry);
+  if (a.dstate && rank == 0) {
+    __syncthreads();
+    if (threadIdx.x < 16) ch.put_state(a.dstate + b * a.dim + ch.first, quad(sh.carry[rounds & 1][threadIdx.x]));
+  }
+}
+
+constexpr int kShortThreads = 128, kShortAhead = 2;
+// Short sequences, as in the forward pass
+template <typename T, bool VEC, bool FLAGS>
+__global__ void __launch_bounds__(kShortThreads)
+scan_short_bwd_kernel(const __grid_constant__ ScanBwd a, int64_t units) {
+  pdl_wait();
+  const int64_t unit = (int64_t)blockIdx.x * (kShortThreads / 16) + (threadIdx.x >> 4);
+  if (unit >= units) return;
+  const int64_t b = unit / a.strips, row0 = b * a.length;
+  const Channels<VEC> ch((int)(unit % a.strips), a.dim);
+  if (!ch.any()) return;
+  const T* dh = static_cast<const T*>(a.dh) + row0 * a.lddh + ch.first;
+  const T* gate = static_cast<const T*>(a.gate) + row0 * a.ldg + ch.first;
+  const T* x = static_cast<const T*>(a.x) + row0 * a.ldx + ch.first;
+  const T* h = static_cast<const T*>(a.h) + row0 * a.ldh + ch.first;
+  T* dx = static_cast<T*>(a.dx) + row0 * a.dim + ch.first;
+  T* dg = static_cast<T*>(a.dgate) + row0 * a.dim + ch.first;
+  const bool mix = a.mix != 0.f;
+  Quad c = a.dlast ? ch.state(a.dlast + b * a.dim + ch.first) : quad(0.f);
+  for (int t0 = (int)a.length - 1; t0 >= 0; t0 -= kShortAhead) {
+    Raw4<T> rd[kShortAhead], rg[kShortAhead], rx[kShortAhead], rh[kShortAhead];
+    bool live[kShortAhead], begins[kShortAhead];
+    #pragma unroll
+    for (int i = 0; i < kShortAhead; ++i) {
+      const int t = t0 - i;
+      if (t < 0) continue;
+      zero(rx[i]);
+      zero(rh[i]);
+      ch.load(rd[i], dh + t * a.lddh);
+      ch.load(rg[i], gate + t * a.ldg);
+      if (mix) ch.load(rx[i], x + t * a.ldx);
+      if (t > 0) ch.load(rh[i], h + (t - 1) * a.ldh);
+      if (FLAGS) {
+        live[i] = !a.mask || a.mask[row0 + t];
+        begins[i] = a.starts && a.starts[row0 + t];
+      }
+    }
+    #pragma unroll
+    for (int i = 0; i < kShortAhead; ++i) {
+      const int t = t0 - i;
+      if (t < 0) continue;
+      Quad keep, take, v = widen(rh[i]);
+      shares_of(widen(rg[i]), keep, take);
+      if (t == 0 && a.state) v = ch.state(a.state + b * a.dim + ch.first);
+      if (FLAGS && begins[i]) v = quad(0.f);
+      v = fma(widen(rx[i]), quad(-a.mix), v);
+      const Quad l = add(widen(rd[i]), c), u = mul(take, l);
+      Quad gx = mix ? u : l, gg = mul(mul(u, keep), v);
+      c = mul(keep, l);
+      if (FLAGS && begins[i]) c = quad(0.f);
+      if (FLAGS && !live[i]) {
+        gx = gg = quad(0.f);
+        c = l;
+      }
+      if (a.dx) ch.store(dx + t * a.dim, gx);
+      if (a.dgate) ch.store(dg + t * a.dim, gg);
+    }
+  }
+  if (a.dstate) ch.put_state(a.dstate + b * a.dim + ch.first, c);
+}
+
+template <typename T, bool VEC> cudaError_t scan_short_bwd(const ScanBwd& a, int64_t strips, cudaStream_t s) {
+  constexpr int per = kShortThreads / 16;
+  return launch_k(a.starts || a.mask ? scan_short_bwd_kernel<T, VEC, true> : scan_short_bwd_kernel<T, VEC, false>,
+                  dim3((unsigned)((strips + per - 1) / per)), dim3(kShortThreads), 0, s, true, a, strips);
 }
 
 template <typename T, int W, int S, int CL, int D, bool VEC>
@@ -179,11 +270,12 @@ cudaError_t scan_bwd_with(const ScanBwd& a, int64_t strips, cudaStream_t s) {
 
 template <typename T, bool VEC> cudaError_t scan_bwd_by_size(const ScanBwd& a, int64_t strips, cudaStream_t s) {
   constexpr int S = sizeof(T) == 2 ? 4 : 2, D = VEC ? 3 : 0;
+  if (a.length <= 4 || (a.length <= 32 && strips >= 2048)) return scan_short_bwd<T, VEC>(a, strips, s);
   if (a.length <= 2 * S) return scan_bwd_with<T, 1, S, 1, 0, VEC>(a, strips, s);
   if (a.length <= 8 * S) return scan_bwd_with<T, 4, S, 1, 0, VEC>(a, strips, s);
   if (strips >= 304 || a.length <= 16 * S) return scan_bwd_with<T, 8, S, 1, D, VEC>(a, strips, s);
-  if (strips >= 76 || a.length <= 64 * S) return scan_bwd_with<T, 8, S, 4, D, VEC>(a, strips, s);
-  return scan_bwd_with<T, 8, S, 8, D, VEC>(a, strips, s);
+  if (strips >= 76 || a.length <= 64 * S) return scan_bwd_with<T, 8, S, 4, VEC ? 2 : 0, VEC>(a, strips, s);
+  return scan_bwd_with<T, 8, S, 8, VEC ? 2 : 0, VEC>(a, strips, s);
 }
 
 }  // namespace
