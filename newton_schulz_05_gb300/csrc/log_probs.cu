@@ -1,5 +1,11 @@
 // Log probabilities of given tokens under a softmax over the vocabulary, and
 // their gradient.
+//
+// Both passes are bound by HBM: the logits are read once, with a running maximum and a
+// sum of exponentials to it a thread, and the gradient reads them once more and writes
+// theirs.  A row is cut into 16-byte pieces that are aligned in memory, so a row that does
+// not start at an aligned address has parts of pieces at its ends, taken element by
+// element.
 #include <cfloat>
 
 #include "sequence.cuh"
@@ -8,72 +14,235 @@ namespace muon {
 
 namespace {
 
-constexpr int kVocabThreads = 512;
+constexpr int kVocabThreads = 256;
+constexpr int kVocabPieces = 4;      // of a thread in flight
 constexpr float kLog2e = 1.4426950408889634f;
 
-// A running maximum (not under the lowest finite number, so that a difference to it is
-// not NaN for a -inf) and the sum of exp2((l - max) * c), joined with another.
-struct Mass { float top, sum; };
-__device__ __forceinline__ Mass join(Mass a, Mass b, float c) {
-  const float top = fmaxf(a.top, b.top);
-  return {top, a.sum * exp2f((a.top - top) * c) + b.sum * exp2f((b.top - top) * c)};
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
+// A row as pieces of E elements: piece i begins at column i * E - phase
+template <typename T> __device__ __forceinline__ int phase_of(const T* row) {
+  return (int)(reinterpret_cast<uintptr_t>(row) / sizeof(T) & (kEl<T> - 1));
+}
+
+// A running maximum (not under the lowest finite number, so that a difference to it is
+// not NaN for a -inf) and the sum of exp2((l - top) * c).  The difference is taken
+// first: it is exact next to the maximum, where the terms count, and does not overflow
+// to NaN where all logits are the type's lowest value.
+struct Mass { float top, sum; };
+__device__ __forceinline__ Mass join(const Mass& a, const Mass& b, float c) {
+  const float top = fmaxf(a.top, b.top);
+  return {top, a.sum * exp2_fast((a.top - top) * c) + b.sum * exp2_fast((b.top - top) * c)};
+}
+// the largest of a piece's elements (NaN counts as none)
+__device__ __forceinline__ float largest(const uint4& u, __nv_bfloat16) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&w[0]);
+  #pragma unroll
+  for (int j = 1; j < 4; ++j) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&w[j]));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float largest(const uint4& u, float) {
+  return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)),
+               fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+}
+template <typename T, int N> __device__ __forceinline__ void take(Mass& m, const uint4 (&u)[N], float c) {
+  constexpr int E = kEl<T>;
+  float top = m.top;
+  #pragma unroll
+  for (int k = 0; k < N; ++k) top = fmaxf(top, largest(u[k], T()));
+  float2 s = make_float2(m.sum * exp2_fast((m.top - top) * c), 0.f);
+  #pragma unroll
+  for (int k = 0; k < N; ++k) {
+    Piece<E> v;
+    widen(v, u[k]);
+    #pragma unroll
+    for (int j = 0; j < E / 2; ++j) {
+      const float2 d = mul2(add2(v.v[j], both(-top)), both(c));
+      s = add2(s, make_float2(exp2_fast(d.x), exp2_fast(d.y)));
+    }
+  }
+  m = {top, s.x + s.y};
+}
+// A piece's elements, those inside the columns [0, vocab), the others -inf.  col: of its first
 template <typename T>
-__global__ void __launch_bounds__(kVocabThreads)
-log_probs_kernel(int64_t vocab, const T* logits, int64_t ld, const int64_t* index, float scale,
-                 float* log_probs, float* lse) {
-  __shared__ Mass slots[kVocabThreads / 32];
+__device__ __forceinline__ uint4 piece_at(const T* row, int64_t col, int64_t vocab) {
+  constexpr int E = kEl<T>;
+  if (col >= 0 && col + E <= vocab) return *reinterpret_cast<const uint4*>(row + col);
+  Piece<E> v;
+  #pragma unroll
+  for (int j = 0; j < E; ++j)
+    elem(v, j) = col + j >= 0 && col + j < vocab ? to_f(row[col + j]) : -INFINITY;
+  return narrow(v);
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n"
+               "barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+
+// TPR threads a row, or CL blocks of TPR = kVocabThreads
+template <typename T, int TPR, int CL>
+__global__ void __launch_bounds__(kVocabThreads, 4)
+log_probs_kernel(int64_t tokens, int64_t vocab, const T* logits, int64_t ld, const int64_t* index,
+                 float scale, float* log_probs, float* lse) {
+  constexpr int E = kEl<T>, N = kVocabPieces, kWarps = kVocabThreads / 32;
+  __shared__ alignas(8) Mass slots[kWarps], blocks[CL];
   pdl_wait();
-  const int64_t t = blockIdx.x, y = index[t];
-  if (y < 0 || y >= vocab) {
-    if (threadIdx.x == 0) log_probs[t] = lse[t] = 0.f;
+  const int64_t row = TPR < kVocabThreads ? (int64_t)blockIdx.x * (kVocabThreads / TPR) + threadIdx.x / TPR
+                                          : blockIdx.x / CL;
+  const int rank = CL > 1 ? (int)(blockIdx.x % CL) : 0, thread = threadIdx.x % TPR;
+  const bool any = TPR == kVocabThreads || row < tokens;
+  const int64_t y = any ? index[row] : -1;
+  const T* l = logits + (any ? row * ld : 0);
+  const int phase = phase_of(l);
+  const float c = scale * kLog2e;
+  // The blocks of a cluster take turns of N pieces a thread.  The first is read before it is
+  // known whether the token counts.
+  constexpr int64_t kTurn = (int64_t)TPR * N * E;
+  int64_t col = rank * kTurn + thread * E - phase;
+  uint4 u[N];
+  auto fetch = [&] {
+    #pragma unroll
+    for (int k = 0; k < N; ++k) u[k] = piece_at(l, col + k * (TPR * E), vocab);
+    col += kTurn * CL;
+  };
+  if (any) fetch();
+  const bool live = y >= 0 && y < vocab;
+  if (TPR == kVocabThreads && !live) {        // in every block of the row
+    if (rank == 0 && thread == 0) log_probs[row] = lse[row] = 0.f;
     return;
   }
-  const T* row = logits + t * ld;
-  const float c = scale * kLog2e;
   Mass m = {-FLT_MAX, 0.f};
-  for (int64_t v = threadIdx.x; v < vocab; v += kVocabThreads) {
-    const float l = to_f(row[v]);
-    if (l > m.top) {
-      m.sum *= exp2f((m.top - l) * c);
-      m.top = l;
+  if (live) {
+    take<T>(m, u, c);
+    while (col < vocab) {
+      fetch();
+      take<T>(m, u, c);
     }
-    m.sum += exp2f((l - m.top) * c);
   }
   #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1)
     m = join(m, Mass{__shfl_xor_sync(~0u, m.top, o), __shfl_xor_sync(~0u, m.sum, o)}, c);
-  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = m;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < kVocabThreads / 32; ++i) m = join(m, slots[i], c);
+  if constexpr (TPR > 32) {
+    if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = m;
+    __syncthreads();
+    m = slots[0];
+    #pragma unroll
+    for (int i = 1; i < kWarps; ++i) m = join(m, slots[i], c);
+    if constexpr (CL > 1) {
+      cluster_barrier();      // rank 0 has begun
+      if (threadIdx.x == 0) {
+        uint32_t to;
+        const uint32_t from = (uint32_t)__cvta_generic_to_shared(&blocks[rank]);
+        asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to) : "r"(from));
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(m.top), "f"(m.sum) : "memory");
+      }
+      __syncwarp();
+      cluster_barrier();
+      if (rank > 0) return;
+      m = blocks[0];
+      #pragma unroll
+      for (int i = 1; i < CL; ++i) m = join(m, blocks[i], c);
+    }
+  }
+  if (any && thread == 0) {
     const float rest = logf(m.sum);
-    log_probs[t] = (to_f(row[y]) - m.top) * scale - rest;
-    lse[t] = fmaf(m.top, scale, rest);
+    log_probs[row] = live ? (to_f(l[y]) - m.top) * scale - rest : 0.f;
+    lse[row] = live ? fmaf(m.top, scale, rest) : 0.f;
   }
 }
 
-template <typename T>
+// TPR threads take a unit of kVocabPieces pieces each of one row
+template <typename T, int TPR>
 __global__ void __launch_bounds__(kVocabThreads)
-log_probs_bwd_kernel(int64_t vocab, const float* dlp, const T* logits, int64_t ld,
+log_probs_bwd_kernel(int64_t units, int units_a_row, int64_t vocab, const float* dlp, const T* logits, int64_t ld,
                      const int64_t* index, const float* lse, float scale, T* dlogits) {
+  constexpr int E = kEl<T>, N = kVocabPieces;
   pdl_wait();
-  const int64_t t = blockIdx.x, y = index[t];
-  const float d = y < 0 || y >= vocab ? 0.f : dlp[t] * scale;
-  const float s = lse[t];
-  for (int64_t v = threadIdx.x; v < vocab; v += kVocabThreads) {
-    float g = 0.f;
-    if (d != 0.f) g = d * ((v == y ? 1.f : 0.f) - expf(fmaf(to_f(logits[t * ld + v]), scale, -s)));
-    dlogits[t * vocab + v] = from_f<T>(g);
+  const int64_t unit = (int64_t)blockIdx.x * (kVocabThreads / TPR) + threadIdx.x / TPR;
+  if (TPR < kVocabThreads && unit >= units) return;
+  const int64_t row = unit / units_a_row;
+  const int64_t y = index[row];
+  const float d = y < 0 || y >= vocab ? 0.f : dlp[row] * scale;
+  const float less = -lse[row] * kLog2e, c = scale * kLog2e;
+  const T* l = logits + row * ld;
+  T* out = dlogits + row * vocab;
+  const int phase = phase_of(out);
+  const bool vec = phase == phase_of(l);
+  const int64_t p0 = unit % units_a_row * (TPR * N) + threadIdx.x % TPR;
+  uint4 u[N];
+  bool whole[N];
+  #pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int64_t p = p0 + k * TPR;
+    whole[k] = vec && p * E >= phase && (p + 1) * E <= vocab + phase;
+    u[k] = make_uint4(0, 0, 0, 0);
+    if (whole[k] && d != 0.f) u[k] = *reinterpret_cast<const uint4*>(l + (p * E - phase));
+  }
+  #pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int64_t col = (p0 + k * TPR) * E - phase;
+    if (col >= vocab) break;
+    Piece<E> v;
+    if (whole[k]) {
+      widen(v, u[k]);
+    } else {
+      #pragma unroll
+      for (int j = 0; j < E; ++j)
+        elem(v, j) = d != 0.f && col + j >= 0 && col + j < vocab ? to_f(l[col + j]) : 0.f;
+    }
+    #pragma unroll
+    for (int j = 0; j < E / 2; ++j) {
+      const float2 e = fma2(v.v[j], both(c), both(less));
+      v.v[j] = d != 0.f ? mul2(make_float2(exp2_fast(e.x), exp2_fast(e.y)), both(-d)) : both(0.f);
+    }
+    if (d != 0.f && y >= col && y < col + E) {
+      #pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (col + j == y) elem(v, j) += d;
+    }
+    if (whole[k]) {
+      *reinterpret_cast<uint4*>(out + col) = narrow(v);
+    } else {
+      #pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (col + j >= 0 && col + j < vocab) out[col + j] = from_f<T>(elem(v, j));
+    }
   }
 }
+
+// --------------------------------------------------------------------- host
 
 muon_status check_vocab(int64_t tokens, int64_t vocab, int dtype, int64_t ld, float scale) {
   if (tokens < 0 || ld < 0 || !(scale > 0.f) || std::isinf(scale)) return MUON_ERR_INVALID_ARG;
-  if (vocab < 1 || vocab > (int64_t)1 << 30 || tokens >= (int64_t)1 << 31)
+  if (vocab < 1 || vocab > (int64_t)1 << 30 || tokens >= (int64_t)1 << 31 || tokens > ((int64_t)1 << 40) / vocab)
     return MUON_ERR_UNSUPPORTED_SHAPE;
   return known(dtype) ? MUON_OK : MUON_ERR_DTYPE;
+}
+
+template <typename T, int TPR, int CL>
+cudaError_t log_probs_with(int64_t tokens, int64_t vocab, const void* logits, int64_t ld, const int64_t* index,
+                           float scale, float* log_probs, float* lse, cudaStream_t s) {
+  constexpr int rows = kVocabThreads / TPR;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((tokens + rows - 1) / rows * CL));
+  cfg.blockDim = dim3(kVocabThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CL;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CL > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, log_probs_kernel<T, TPR, CL>, tokens, vocab, static_cast<const T*>(logits), ld,
+                            index, scale, log_probs, lse);
 }
 
 }  // namespace
@@ -97,8 +266,14 @@ extern "C" muon_status muon_token_log_probs(int64_t tokens, int64_t vocab, int d
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = by_type(dtype, [&](auto t) {
     using T = decltype(t);
-    return launch_k(log_probs_kernel<T>, dim3((unsigned)tokens), dim3(kVocabThreads), 0, s, true, vocab,
-                    static_cast<const T*>(logits), ld, index, scale, log_probs, lse);
+    const int64_t turn = (int64_t)kVocabThreads * kVocabPieces * kEl<T>;      // elements of a block's turn
+    auto with = vocab * 32 <= turn ? log_probs_with<T, 8, 1>
+                : vocab * 4 <= turn ? log_probs_with<T, 32, 1>
+                : tokens > 304 || vocab <= turn ? log_probs_with<T, kVocabThreads, 1>
+                : tokens > 152 || vocab <= 2 * turn ? log_probs_with<T, kVocabThreads, 2>
+                : tokens > 76 || vocab <= 4 * turn ? log_probs_with<T, kVocabThreads, 4>
+                                                   : log_probs_with<T, kVocabThreads, 8>;
+    return with(tokens, vocab, logits, ld, index, scale, log_probs, lse, s);
   });
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
@@ -120,8 +295,16 @@ extern "C" muon_status muon_token_log_probs_backward(int64_t tokens, int64_t voc
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = by_type(dtype, [&](auto t) {
     using T = decltype(t);
-    return launch_k(log_probs_bwd_kernel<T>, dim3((unsigned)tokens), dim3(kVocabThreads), 0, s, true,
-                    vocab, dlog_probs, static_cast<const T*>(logits), ld, index, lse, scale,
+    constexpr int E = kEl<T>;
+    const int64_t lane = kVocabPieces * E;       // elements of a thread
+    const int tpr = vocab <= 8 * lane ? 8 : vocab <= 64 * lane ? 32 : kVocabThreads;
+    const int groups = kVocabThreads / tpr;
+    const int per_row = (int)((vocab + E - 1 + tpr * kVocabPieces * E - 1) / (tpr * kVocabPieces * E));
+    const int64_t units = tokens * per_row;
+    return launch_k(tpr == 8 ? log_probs_bwd_kernel<T, 8>
+                    : tpr == 32 ? log_probs_bwd_kernel<T, 32> : log_probs_bwd_kernel<T, kVocabThreads>,
+                    dim3((unsigned)((units + groups - 1) / groups)), dim3(kVocabThreads), 0, s, true, units,
+                    per_row, vocab, dlog_probs, static_cast<const T*>(logits), ld, index, lse, scale,
                     static_cast<T*>(dlogits));
   });
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
