@@ -136,6 +136,16 @@ def test_extreme_values(layers):
     assert bool(y[3, 0].isnan().all()) and not y[3, 1].any()
 
 
+def test_without_eps(layers):
+    # three heads of a warp's four, and a token that is none: no 0 / 0 from what is not there
+    q, k, wq, wk, how, n = inputs(layers, 9, 3, 1, 128, 128, F32, table=5)
+    how["positions"][4] = 7
+    o = layers.norm_rotate_heads_forward(q, k, wq, wk, eps=0.0, **how)
+    assert bool(o.q.isfinite().all()) and not o.q[4].any()
+    g = layers.norm_rotate_heads_backward(n(*q.shape), n(*k.shape), q, k, wq, wk, eps=0.0, **how)
+    assert all(bool(t.isfinite().all()) for t in g) and not g.dq[4].any()
+
+
 def test_no_tokens_and_no_heads(layers):
     how = dict(zip(("cos", "sin"), layers.rotation_table(4, 8)))
     w = torch.ones(8, device="cuda")
