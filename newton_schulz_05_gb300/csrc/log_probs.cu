@@ -18,12 +18,6 @@ constexpr int kVocabThreads = 256;
 constexpr int kVocabPieces = 4;      // of a thread in flight
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // A row as pieces of E elements: piece i begins at column i * E - phase
 template <typename T> __device__ __forceinline__ int phase_of(const T* row) {
   return (int)(reinterpret_cast<uintptr_t>(row) / sizeof(T) & (kEl<T> - 1));
@@ -80,11 +74,6 @@ __device__ __forceinline__ uint4 piece_at(const T* row, int64_t col, int64_t voc
   return narrow(v);
 }
 
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n"
-               "barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-}
-
 // TPR threads a row, or CL blocks of TPR = kVocabThreads
 template <typename T, int TPR, int CL>
 __global__ void __launch_bounds__(kVocabThreads, 4)
@@ -137,10 +126,8 @@ log_probs_kernel(int64_t tokens, int64_t vocab, const T* logits, int64_t ld, con
     if constexpr (CL > 1) {
       cluster_barrier();      // rank 0 has begun
       if (threadIdx.x == 0) {
-        uint32_t to;
-        const uint32_t from = (uint32_t)__cvta_generic_to_shared(&blocks[rank]);
-        asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to) : "r"(from));
-        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(m.top), "f"(m.sum) : "memory");
+        put_at(at_rank(&blocks[rank].top, 0), m.top);
+        put_at(at_rank(&blocks[rank].sum, 0), m.sum);
       }
       __syncwarp();
       cluster_barrier();
@@ -229,20 +216,8 @@ template <typename T, int TPR, int CL>
 cudaError_t log_probs_with(int64_t tokens, int64_t vocab, const void* logits, int64_t ld, const int64_t* index,
                            float scale, float* log_probs, float* lse, cudaStream_t s) {
   constexpr int rows = kVocabThreads / TPR;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((tokens + rows - 1) / rows * CL));
-  cfg.blockDim = dim3(kVocabThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = CL;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = CL > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, log_probs_kernel<T, TPR, CL>, tokens, vocab, static_cast<const T*>(logits), ld,
-                            index, scale, log_probs, lse);
+  return launch_cluster(log_probs_kernel<T, TPR, CL>, (tokens + rows - 1) / rows * CL, CL, kVocabThreads, 0, s, tokens,
+                        vocab, static_cast<const T*>(logits), ld, index, scale, log_probs, lse);
 }
 
 }  // namespace
@@ -299,7 +274,8 @@ extern "C" muon_status muon_token_log_probs_backward(int64_t tokens, int64_t voc
     const int64_t lane = kVocabPieces * E;       // elements of a thread
     const int tpr = vocab <= 8 * lane ? 8 : vocab <= 64 * lane ? 32 : kVocabThreads;
     const int groups = kVocabThreads / tpr;
-    const int per_row = (int)((vocab + E - 1 + tpr * kVocabPieces * E - 1) / (tpr * kVocabPieces * E));
+    const int64_t ahead = vocab % E || off(dlogits, 16) ? E - 1 : 0;      // of a row in its first piece
+    const int per_row = (int)((vocab + ahead + tpr * lane - 1) / (tpr * lane));
     const int64_t units = tokens * per_row;
     return launch_k(tpr == 8 ? log_probs_bwd_kernel<T, 8>
                     : tpr == 32 ? log_probs_bwd_kernel<T, 32> : log_probs_bwd_kernel<T, kVocabThreads>,

@@ -214,10 +214,10 @@ cudaError_t scan_with(const Scan& a, int64_t strips, cudaStream_t s) {
   constexpr auto plain = scan_kernel<T, W, S, CL, D, VEC, false>, flags = scan_kernel<T, W, S, CL, D, VEC, true>;
   if (a.starts || a.mask) {
     if (const cudaError_t e = smem ? allow_shared<flags>(smem) : cudaSuccess) return e;
-    return launch_strips<CL>(flags, strips, 32 * W, smem, s, a);
+    return launch_cluster(flags, strips * CL, CL, 32 * W, smem, s, a);
   }
   if (const cudaError_t e = smem ? allow_shared<plain>(smem) : cudaSuccess) return e;
-  return launch_strips<CL>(plain, strips, 32 * W, smem, s, a);
+  return launch_cluster(plain, strips * CL, CL, 32 * W, smem, s, a);
 }
 
 template <typename T, bool VEC> cudaError_t scan_by_size(const Scan& a, int64_t strips, cudaStream_t s) {

@@ -59,11 +59,6 @@ __device__ __forceinline__ Quad fma(const Quad& a, const Quad& b, const Quad& c)
   return {{fma2(a.v[0], b.v[0], c.v[0]), fma2(a.v[1], b.v[1], c.v[1])}};
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float reciprocal_fast(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -231,30 +226,6 @@ __device__ __forceinline__ Run run_in(const RunSlot& s, int cut) {
   return {quad(s.m[l]), quad(s.k[l]), quad(s.H[l]), cut != 0};
 }
 
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n"
-               "barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-}
-__device__ __forceinline__ int cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return (int)r;
-}
-// the address in block `rank` of the cluster of what is at p in this one
-__device__ __forceinline__ uint32_t at_rank(const void* p, int rank) {
-  uint32_t to;
-  const uint32_t from = (uint32_t)__cvta_generic_to_shared(p);
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(from), "r"(rank));
-  return to;
-}
-__device__ __forceinline__ void put_at(uint32_t to, const float4& f) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(f.x), "f"(f.y),
-               "f"(f.z), "f"(f.w) : "memory");
-}
-__device__ __forceinline__ void put_at(uint32_t to, int v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(v) : "memory");
-}
-
 __device__ __forceinline__ Quad from_other_half(const Quad& q) {
   Quad r;
   #pragma unroll
@@ -347,26 +318,6 @@ inline muon_status check_scan(int64_t batch, int64_t length, int64_t dim, int dt
 // whether rows of `p` are made of aligned pieces of four
 inline bool fours(const void* p, int64_t rows, int64_t ld, size_t es) {
   return !off(p, 4 * es) && (rows <= 1 || ld % 4 == 0);
-}
-
-// Launch with clusters of CL blocks along the length
-template <int CL, typename A>
-cudaError_t launch_strips(void (*kernel)(A), int64_t strips, int threads, size_t smem, cudaStream_t s,
-                          const A& a) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(strips * CL));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = CL;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = CL > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace
