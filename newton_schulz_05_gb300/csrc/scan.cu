@@ -1,6 +1,8 @@
 // Gated linear recurrence: the forward pass.
 #include "scan.cuh"
 
+#include <algorithm>
+
 namespace muon {
 
 namespace {
@@ -40,23 +42,27 @@ scan_kernel(const __grid_constant__ Scan a) {
   extern __shared__ uint4 ring[];
   __shared__ RunSlots<W, CL> sh;
   pdl_wait();
-  constexpr int kSpan = 2 * W * S, NT = 32 * W;      // tokens of a chunk
+  constexpr int kSpan = 2 * W * S;      // tokens of a chunk
   const int rank = CL > 1 ? cluster_rank() : 0;
   const int64_t unit = blockIdx.x / CL, b = unit / a.strips;
   const Channels<VEC> ch((int)(unit % a.strips), a.dim);
   const int64_t row0 = b * a.length;
   const int seg = threadIdx.x >> 4, length = (int)a.length;
   const int64_t stride = (int64_t)kSpan * CL;
-  // the chunk to read next and the one to write, at the lane's first channel
-  const T* gate = static_cast<const T*>(a.gate) + (row0 + rank * kSpan) * a.ldg + ch.first;
-  const T* x = static_cast<const T*>(a.x) + (row0 + rank * kSpan) * a.ldx + ch.first;
+  // the chunk to read next, at the strip's first channel or at the lane's, and the one to write
+  const int channel = D > 0 ? ch.strip : ch.first;
+  const T* gate = static_cast<const T*>(a.gate) + (row0 + rank * kSpan) * a.ldg + channel;
+  const T* x = static_cast<const T*>(a.x) + (row0 + rank * kSpan) * a.ldx + channel;
   T* h = static_cast<T*>(a.h) + (row0 + rank * kSpan + seg * S) * a.dim + ch.first;
   int left_in = length - rank * kSpan - seg * S, left = left_in;    // tokens from the segment's first on
   gate += seg * S * a.ldg;
   x += seg * S * a.ldx;
   if (threadIdx.x < 16)
     sh.carry[0][threadIdx.x] = four(a.state ? ch.state(a.state + b * a.dim + ch.first) : quad(0.f));
-  Raw4<T>* const slots = reinterpret_cast<Raw4<T>*>(ring) + threadIdx.x;
+  const Ring<T, VEC, 2, S, W> slots(ring, min(kStrip, (int)a.dim - ch.strip));
+  // elements of the segment's first row ahead of the strip, in the chunk to use next
+  uint32_t fg = VEC ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(gate + seg * S * a.ldg) / sizeof(T));
+  uint32_t fx = VEC ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(x + seg * S * a.ldx) / sizeof(T));
   Flags ahead[D > 0 ? D : 1];
   auto ask_next = [&] { return ask<S>(a.starts, a.mask, row0, length - left_in, length); };
   auto advance = [&] {
@@ -65,16 +71,22 @@ scan_kernel(const __grid_constant__ Scan a) {
     left_in -= (int)stride;
   };
   auto start = [&](int stage) {
-    const int n = ch.any() ? left_in : 0;
-    #pragma unroll
-    for (int i = 0; i < S; ++i) {
-      Raw4<T>* const to = slots + (stage * 2 * S + i) * NT;
-      if (i < n) {
-        ch.copy(to, gate + i * a.ldg);
-        ch.copy(to + S * NT, x + i * a.ldx);
-      } else {
-        infinite(to[0]);
-        zero(to[S * NT]);
+    slots.arrived();
+    if (left_in >= S) {
+      #pragma unroll
+      for (int i = 0; i < S; ++i) {
+        slots.copy(slots.row(stage, 0, i), gate + i * a.ldg);
+        slots.copy(slots.row(stage, 1, i), x + i * a.ldx);
+      }
+    } else {
+      for (int i = 0; i < S; ++i) {
+        if (i < left_in) {
+          slots.copy(slots.row(stage, 0, i), gate + i * a.ldg);
+          slots.copy(slots.row(stage, 1, i), x + i * a.ldx);
+        } else {
+          slots.fill(slots.row(stage, 0, i), true);
+          slots.fill(slots.row(stage, 1, i), false);
+        }
       }
     }
     copies_commit();
@@ -92,6 +104,7 @@ scan_kernel(const __grid_constant__ Scan a) {
     Raw4<T> rg[S], rx[S];
     if constexpr (D > 0) {
       copies_wait<D - 1>();
+      slots.arrived();
     } else {
       if (FLAGS) ahead[0] = ask_next();
       const int n = ch.any() ? left_in : 0;
@@ -113,8 +126,8 @@ scan_kernel(const __grid_constant__ Scan a) {
     for (int i = 0; i < S; ++i) {
       Raw4<T> gi, vi;
       if constexpr (D > 0) {
-        gi = slots[(stage * 2 * S + i) * NT];
-        vi = slots[(stage * 2 * S + S + i) * NT];
+        gi = slots.get(slots.row(stage, 0, i), (fg + i * (uint32_t)a.ldg) & 3);
+        vi = slots.get(slots.row(stage, 1, i), (fx + i * (uint32_t)a.ldx) & 3);
       } else {
         gi = rg[i];
         vi = rx[i];
@@ -134,6 +147,8 @@ scan_kernel(const __grid_constant__ Scan a) {
     }
     if constexpr (D > 0) {
       start(stage);
+      fg += (uint32_t)(stride * a.ldg);
+      fx += (uint32_t)(stride * a.ldx);
       stage = stage + 1 == D ? 0 : stage + 1;
       if (FLAGS) {
         #pragma unroll
@@ -144,10 +159,19 @@ scan_kernel(const __grid_constant__ Scan a) {
     }
     Quad front = join_segments<W, CL, FLAGS, false>(sh, run, round);
     const int n = ch.any() ? left : 0;
-    #pragma unroll
-    for (int i = 0; i < S; ++i) {
+    auto finish = [&](int i) {
       if (FLAGS && (now.starts >> i & 1)) front = quad(0.f);
-      if (i < n) ch.store(h + i * a.dim, fma(P[i], front, H[i]));
+      return fma(P[i], front, H[i]);
+    };
+    if (n >= S) {
+      #pragma unroll
+      for (int i = 0; i < S; ++i) ch.store(h + i * a.dim, finish(i));
+    } else {
+      #pragma unroll
+      for (int i = 0; i < S; ++i) {
+        const Quad q = finish(i);
+        if (i < n) ch.store(h + i * a.dim, q);
+      }
     }
     h += stride * a.dim;
     left -= (int)stride;
@@ -210,7 +234,7 @@ template <typename T, bool VEC> cudaError_t scan_short(const Scan& a, int64_t st
 
 template <typename T, int W, int S, int CL, int D, bool VEC>
 cudaError_t scan_with(const Scan& a, int64_t strips, cudaStream_t s) {
-  constexpr size_t smem = (size_t)D * 2 * S * 32 * W * sizeof(Raw4<T>);
+  constexpr size_t smem = D * Ring<T, VEC, 2, S, W>::kStage;
   constexpr auto plain = scan_kernel<T, W, S, CL, D, VEC, false>, flags = scan_kernel<T, W, S, CL, D, VEC, true>;
   if (a.starts || a.mask) {
     if (const cudaError_t e = smem ? allow_shared<flags>(smem) : cudaSuccess) return e;
@@ -220,14 +244,17 @@ cudaError_t scan_with(const Scan& a, int64_t strips, cudaStream_t s) {
   return launch_cluster(plain, strips * CL, CL, 32 * W, smem, s, a);
 }
 
-template <typename T, bool VEC> cudaError_t scan_by_size(const Scan& a, int64_t strips, cudaStream_t s) {
-  constexpr int S = sizeof(T) == 2 ? 8 : 4, D = VEC ? 3 : 0;
+// Blocks of 8 warps, two an SM, or of 4 where there are strips for more than two an SM;
+// clusters where there are few strips, although a round of joins through a cluster takes
+// about 1.3 us more: MEASURED
+template <typename T, bool VEC, bool RING> cudaError_t scan_by_size(const Scan& a, int64_t strips, cudaStream_t s) {
+  constexpr int S = sizeof(T) == 2 ? 8 : 4, D = RING ? 2 : 0;
   if (a.length <= 4 || (a.length <= 32 && strips >= 2048)) return scan_short<T, VEC>(a, strips, s);
   if (a.length <= 2 * S) return scan_with<T, 1, S, 1, 0, VEC>(a, strips, s);
-  if (a.length <= 8 * S) return scan_with<T, 4, S, 1, 0, VEC>(a, strips, s);
-  if (strips >= 304 || a.length <= 16 * S) return scan_with<T, 8, S, 1, D, VEC>(a, strips, s);
-  if (strips >= 76 || a.length <= 64 * S) return scan_with<T, 8, S, 4, VEC ? 2 : 0, VEC>(a, strips, s);
-  return scan_with<T, 8, S, 8, VEC ? 2 : 0, VEC>(a, strips, s);
+  if (a.length <= 8 * S || strips > 304) return scan_with<T, 4, S, 1, D, VEC>(a, strips, s);
+  if (strips >= 128 || a.length <= 16 * S) return scan_with<T, 8, S, 1, D, VEC>(a, strips, s);
+  if (strips >= 64 || a.length <= 64 * S) return scan_with<T, 8, S, 4, D, VEC>(a, strips, s);
+  return scan_with<T, 8, S, 8, D, VEC>(a, strips, s);
 }
 
 }  // namespace
@@ -252,11 +279,13 @@ extern "C" muon_status muon_gated_scan(int64_t batch, int64_t length, int64_t di
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int strips = (int)((dim + kStrip - 1) / kStrip);
   const Scan a = {length, dim, ldg, ldx, strips, mix ? 1.f : 0.f, gate, x, state, starts, token_mask, h, last};
-  const int64_t rows = batch * length;
-  const bool vec = dim % 4 == 0 && fours(gate, rows, ldg, es) && fours(x, rows, ldx, es) && !off(h, 4 * es);
+  const int64_t rows = batch * length, units = batch * strips;
+  const int how = std::max(lie(gate, rows, ldg, es), lie(x, rows, ldx, es));
+  const bool vec = how == kFours && dim % 4 == 0 && !off(h, 4 * es);
   const cudaError_t e = by_type(dtype, [&](auto t) {
     using T = decltype(t);
-    return vec ? scan_by_size<T, true>(a, batch * strips, s) : scan_by_size<T, false>(a, batch * strips, s);
+    return vec ? scan_by_size<T, true, true>(a, units, s)
+               : how != kAnyhow ? scan_by_size<T, false, true>(a, units, s) : scan_by_size<T, false, false>(a, units, s);
   });
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }

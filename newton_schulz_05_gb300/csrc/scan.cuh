@@ -92,11 +92,12 @@ __device__ __forceinline__ Flags bits(const Flags& f) {
 // Which channels a lane has: `has` of its four are inside the row.  VEC: four
 // neighbours, all inside or all outside.
 template <bool VEC> struct Channels {
-  int first;      // of the lane, in the row
+  int strip, first;      // first channel of the strip, and of the lane, in the row
   int left;       // channels from `first` on that are inside the row
-  __device__ __forceinline__ Channels(int strip, int64_t dim) {
+  __device__ __forceinline__ Channels(int index, int64_t dim) {
     const int l = threadIdx.x & 15;
-    first = strip * kStrip + (VEC ? 4 * l : l);
+    strip = index * kStrip;
+    first = strip + (VEC ? 4 * l : l);
     left = (int)dim - first;
   }
   __device__ __forceinline__ bool any() const { return left > 0; }
@@ -125,14 +126,6 @@ template <bool VEC> struct Channels {
       for (int j = 0; j < 4; ++j) w[j] = has(j) ? q[16 * j] : 0;
       r.u = make_uint4(w[0], w[1], w[2], w[3]);
     }
-  }
-  // asynchronous copy of a piece into the thread's slot of a ring
-  template <typename T> __device__ __forceinline__ static void copy(Raw4<T>* slot, const T* p) {
-    const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot);
-    if constexpr (sizeof(T) == 2)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(to), "l"(p) : "memory");
-    else
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(p) : "memory");
   }
   __device__ __forceinline__ void store(__nv_bfloat16* p, const Quad& q) const {
     const __nv_bfloat162 a = __float22bfloat162_rn(q.v[0]), b = __float22bfloat162_rn(q.v[1]);
@@ -169,6 +162,69 @@ template <bool VEC> struct Channels {
     for (int j = 0; j < 4; ++j)
       if (has(j)) p[at(j)] = w[j];
   }
+};
+
+// Rows of N operands on their way through shared memory: D chunks, S tokens a segment, 2 W
+// segments.  A row of a strip is copied by the half warp that reads it, in aligned pieces of
+// four channels; where rows are not made of those, its first piece may begin up to three
+// elements ahead (inside the tensor, whose first row is aligned) and there is one more.
+template <typename T, bool VEC, int N, int S, int W> struct Ring {
+  static constexpr int kRow = VEC ? 16 : 17;
+  static constexpr size_t kStage = sizeof(Raw4<T>) * N * S * 2 * W * kRow;
+  Raw4<T>* base;
+  int left;         // channels of the strip
+  __device__ __forceinline__ Ring(void* smem, int left)
+      : base(static_cast<Raw4<T>*>(smem) + (threadIdx.x >> 4) * kRow), left(left) {}
+  __device__ __forceinline__ Raw4<T>* row(int stage, int operand, int i) const {
+    return base + ((stage * N + operand) * S + i) * (2 * W * kRow);
+  }
+  // p: the strip's first channel in the row
+  __device__ __forceinline__ void copy(Raw4<T>* to, const T* p) const {
+    const int l = threadIdx.x & 15;
+    if constexpr (VEC) {
+      if (4 * l < left) piece(to + l, p + 4 * l, 4 * sizeof(T));
+    } else {
+      const int f = (int)(reinterpret_cast<uintptr_t>(p) / sizeof(T) & 3);
+      const int first = 4 * l - f, inside = left - first;
+      if (inside > 0) piece(to + l, p + first, (int)sizeof(T) * (inside < 4 ? inside : 4));
+      if (l == 0 && f > 0 && left > 64 - f) piece(to + 16, p + 64 - f, (int)sizeof(T) * (left - (64 - f)));
+    }
+  }
+  static __device__ __forceinline__ void piece(Raw4<T>* to, const T* p, int bytes) {
+    const uint32_t s = (uint32_t)__cvta_generic_to_shared(to);
+    if constexpr (VEC && sizeof(T) == 2)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(s), "l"(p) : "memory");
+    else if constexpr (VEC)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(s), "l"(p) : "memory");
+    else if constexpr (sizeof(T) == 2)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(s), "l"(p), "r"(bytes) : "memory");
+    else
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(p), "r"(bytes) : "memory");
+  }
+  // every element of a row
+  __device__ __forceinline__ void fill(Raw4<T>* to, bool gate) const {
+    const int l = threadIdx.x & 15;
+    Raw4<T> v;
+    if (gate) infinite(v);
+    else zero(v);
+    to[l] = v;
+    if (!VEC && l == 0) to[16] = v;
+  }
+  // the lane's channels; f: the row's elements ahead of the strip
+  __device__ __forceinline__ Raw4<T> get(const Raw4<T>* from, int f) const {
+    const int l = threadIdx.x & 15;
+    if constexpr (VEC) {
+      return from[l];
+    } else if constexpr (sizeof(T) == 2) {
+      const uint16_t* e = reinterpret_cast<const uint16_t*>(from) + f + l;
+      return {make_uint2(e[0] | (uint32_t)e[16] << 16, e[32] | (uint32_t)e[48] << 16)};
+    } else {
+      const uint32_t* e = reinterpret_cast<const uint32_t*>(from) + f + l;
+      return {make_uint4(e[0], e[16], e[32], e[48])};
+    }
+  }
+  // the half warp's lanes have copied for one another, and have read
+  __device__ __forceinline__ void arrived() const { if (!VEC) __syncwarp(); }
 };
 
 // A run of tokens as a map of the state p in front of it, H + (k + m) p: where its
@@ -315,9 +371,10 @@ inline muon_status check_scan(int64_t batch, int64_t length, int64_t dim, int dt
   return known(dtype) ? MUON_OK : MUON_ERR_DTYPE;
 }
 
-// whether rows of `p` are made of aligned pieces of four
-inline bool fours(const void* p, int64_t rows, int64_t ld, size_t es) {
-  return !off(p, 4 * es) && (rows <= 1 || ld % 4 == 0);
+// How rows lie: in aligned pieces of four channels; from an aligned first row on; or neither
+enum { kFours, kFromAligned, kAnyhow };
+inline int lie(const void* p, int64_t rows, int64_t ld, size_t es) {
+  return off(p, 4 * es) ? kAnyhow : rows <= 1 || ld % 4 == 0 ? kFours : kFromAligned;
 }
 
 }  // namespace

@@ -2,6 +2,8 @@
 // first, over what reaches the state behind each token, c -> a (dh + c).
 #include "scan.cuh"
 
+#include <algorithm>
+
 namespace muon {
 
 namespace {
@@ -38,7 +40,7 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
   extern __shared__ uint4 ring[];
   __shared__ RunSlots<W, CL> sh;
   pdl_wait();
-  constexpr int kSpan = 2 * W * S, NT = 32 * W;
+  constexpr int kSpan = 2 * W * S;
   const int rank = CL > 1 ? cluster_rank() : 0;      // rank 0 has the last chunk
   const int64_t unit = blockIdx.x / CL, b = unit / a.strips;
   const Channels<VEC> ch((int)(unit % a.strips), a.dim);
@@ -48,15 +50,19 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
   // the segment's first token (in front of the sequence in the last round of some ranks)
   // of the chunk to read next, and of the one to write
   int64_t t_in = (int64_t)(chunks - 1 - rank) * kSpan + seg * S, t0 = t_in;
-  const T* dh = static_cast<const T*>(a.dh) + (row0 + t_in) * a.lddh + ch.first;
-  const T* gate = static_cast<const T*>(a.gate) + (row0 + t_in) * a.ldg + ch.first;
-  const T* x = static_cast<const T*>(a.x) + (row0 + t_in) * a.ldx + ch.first;
-  const T* h = static_cast<const T*>(a.h) + (row0 + t_in - 1) * a.ldh + ch.first;
+  const int channel = D > 0 ? ch.strip : ch.first;
+  const T* dh = static_cast<const T*>(a.dh) + (row0 + t_in) * a.lddh + channel;
+  const T* gate = static_cast<const T*>(a.gate) + (row0 + t_in) * a.ldg + channel;
+  const T* x = static_cast<const T*>(a.x) + (row0 + t_in) * a.ldx + channel;
+  const T* h = static_cast<const T*>(a.h) + (row0 + t_in - 1) * a.ldh + channel;
   const int64_t out = row0 * a.dim + ch.first;
   const bool mix = a.mix != 0.f;
   if (threadIdx.x < 16)
     sh.carry[0][threadIdx.x] = four(a.dlast ? ch.state(a.dlast + b * a.dim + ch.first) : quad(0.f));
-  Raw4<T>* const slots = reinterpret_cast<Raw4<T>*>(ring) + threadIdx.x;
+  const Ring<T, VEC, 4, S, W> slots(ring, min(kStrip, (int)a.dim - ch.strip));
+  // elements of the segment's first row ahead of the strip, in the chunk to use next
+  auto ahead_of = [](const T* p) { return VEC ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(p) / sizeof(T)); };
+  uint32_t fd = ahead_of(dh), fg = ahead_of(gate), fx = ahead_of(x), fh = ahead_of(h);
   Flags ahead[D > 0 ? D : 1];
   auto ask_next = [&] { return ask<S>(a.starts, a.mask, row0, t_in, length); };
   auto advance = [&] {
@@ -68,25 +74,36 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
   };
   // how many of a segment's tokens are inside, all from its first on (chunks start at 0)
   auto inside = [&](int64_t t) {
-    return !ch.any() || t < 0 ? 0 : t + S <= length ? S : (int)(t < length ? length - t : 0);
+    return t < 0 ? 0 : t + S <= length ? S : (int)(t < length ? length - t : 0);
   };
   auto start = [&](int stage) {
     const int n = inside(t_in);
-    #pragma unroll
-    for (int i = 0; i < S; ++i) {
-      Raw4<T>* const to = slots + (stage * 4 * S + i) * NT;
-      if (i < n) {
-        ch.copy(to, dh + i * a.lddh);
-        ch.copy(to + S * NT, gate + i * a.ldg);
-        if (mix) ch.copy(to + 2 * S * NT, x + i * a.ldx);
-        else zero(to[2 * S * NT]);
-        if (i > 0 || t_in > 0) ch.copy(to + 3 * S * NT, h + i * a.ldh);
-        else zero(to[3 * S * NT]);
-      } else {
-        zero(to[0]);
-        infinite(to[S * NT]);
-        zero(to[2 * S * NT]);
-        zero(to[3 * S * NT]);
+    slots.arrived();
+    if (n == S && t_in > 0 && mix) {
+      #pragma unroll
+      for (int i = 0; i < S; ++i) {
+        slots.copy(slots.row(stage, 0, i), dh + i * a.lddh);
+        slots.copy(slots.row(stage, 1, i), gate + i * a.ldg);
+        slots.copy(slots.row(stage, 2, i), x + i * a.ldx);
+        slots.copy(slots.row(stage, 3, i), h + i * a.ldh);
+      }
+    } else {
+      for (int i = 0; i < S; ++i) {
+        Raw4<T>* const to[4] = {slots.row(stage, 0, i), slots.row(stage, 1, i), slots.row(stage, 2, i),
+                                slots.row(stage, 3, i)};
+        if (i < n) {
+          slots.copy(to[0], dh + i * a.lddh);
+          slots.copy(to[1], gate + i * a.ldg);
+          if (mix) slots.copy(to[2], x + i * a.ldx);
+          else slots.fill(to[2], false);
+          if (i > 0 || t_in > 0) slots.copy(to[3], h + i * a.ldh);
+          else slots.fill(to[3], false);
+        } else {
+          slots.fill(to[0], false);
+          slots.fill(to[1], true);
+          slots.fill(to[2], false);
+          slots.fill(to[3], false);
+        }
       }
     }
     copies_commit();
@@ -103,9 +120,10 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
     Raw4<T> rd[S], rg[S], rx[S], rh[S];
     if constexpr (D > 0) {
       copies_wait<D - 1>();
+      slots.arrived();
     } else {
       if (FLAGS) ahead[0] = ask_next();
-      const int n = inside(t_in);
+      const int n = ch.any() ? inside(t_in) : 0;
       #pragma unroll
       for (int i = 0; i < S; ++i) {
         zero(rd[i]);
@@ -128,11 +146,10 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
     for (int i = S - 1; i >= 0; --i) {
       Raw4<T> di, gi, xi, hi;
       if constexpr (D > 0) {
-        const Raw4<T>* const from = slots + (stage * 4 * S + i) * NT;
-        di = from[0];
-        gi = from[S * NT];
-        xi = from[2 * S * NT];
-        hi = from[3 * S * NT];
+        di = slots.get(slots.row(stage, 0, i), (fd + i * (uint32_t)a.lddh) & 3);
+        gi = slots.get(slots.row(stage, 1, i), (fg + i * (uint32_t)a.ldg) & 3);
+        xi = slots.get(slots.row(stage, 2, i), (fx + i * (uint32_t)a.ldx) & 3);
+        hi = slots.get(slots.row(stage, 3, i), (fh + i * (uint32_t)a.ldh) & 3);
       } else {
         di = rd[i];
         gi = rg[i];
@@ -156,6 +173,10 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
     }
     if constexpr (D > 0) {
       start(stage);
+      fd -= (uint32_t)(stride * a.lddh);
+      fg -= (uint32_t)(stride * a.ldg);
+      fx -= (uint32_t)(stride * a.ldx);
+      fh -= (uint32_t)(stride * a.ldh);
       stage = stage + 1 == D ? 0 : stage + 1;
       if (FLAGS) {
         #pragma unroll
@@ -165,19 +186,18 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
       advance();
     }
     Quad c = join_segments<W, CL, FLAGS, true>(sh, run, round);
-    const int n = inside(t0);
+    const int n = ch.any() ? inside(t0) : 0;
     T* const dx = static_cast<T*>(a.dx) + out + t0 * a.dim;
     T* const dg = static_cast<T*>(a.dgate) + out + t0 * a.dim;
+    const bool whole = n == S && a.dx && a.dgate;
     #pragma unroll
     for (int i = S - 1; i >= 0; --i) {
       const Quad l = add(d[i], c), u = mul(take[i], l);
       c = mul(keep[i], l);
       Quad gx = mix ? u : l, gg = mul(mul(u, keep[i]), v[i]);
       if (FLAGS && !(now.live >> i & 1)) gx = gg = quad(0.f);
-      if (i < n) {
-        if (a.dx) ch.store(dx + i * a.dim, gx);
-        if (a.dgate) ch.store(dg + i * a.dim, gg);
-      }
+      if (whole || (i < n && a.dx)) ch.store(dx + i * a.dim, gx);
+      if (whole || (i < n && a.dgate)) ch.store(dg + i * a.dim, gg);
       if (FLAGS && (now.starts >> i & 1)) c = quad(0.f);
     }
     t0 -= stride;
@@ -257,7 +277,7 @@ template <typename T, bool VEC> cudaError_t scan_short_bwd(const ScanBwd& a, int
 
 template <typename T, int W, int S, int CL, int D, bool VEC>
 cudaError_t scan_bwd_with(const ScanBwd& a, int64_t strips, cudaStream_t s) {
-  constexpr size_t smem = (size_t)D * 4 * S * 32 * W * sizeof(Raw4<T>);
+  constexpr size_t smem = D * Ring<T, VEC, 4, S, W>::kStage;
   constexpr auto plain = scan_bwd_kernel<T, W, S, CL, D, VEC, false>,
                  flags = scan_bwd_kernel<T, W, S, CL, D, VEC, true>;
   if (a.starts || a.mask) {
@@ -268,14 +288,14 @@ cudaError_t scan_bwd_with(const ScanBwd& a, int64_t strips, cudaStream_t s) {
   return launch_cluster(plain, strips * CL, CL, 32 * W, smem, s, a);
 }
 
-template <typename T, bool VEC> cudaError_t scan_bwd_by_size(const ScanBwd& a, int64_t strips, cudaStream_t s) {
-  constexpr int S = sizeof(T) == 2 ? 4 : 2, D = VEC ? 3 : 0;
+template <typename T, bool VEC, bool RING> cudaError_t scan_bwd_by_size(const ScanBwd& a, int64_t strips, cudaStream_t s) {
+  constexpr int S = sizeof(T) == 2 ? 4 : 2, D = RING ? 2 : 0;
   if (a.length <= 4 || (a.length <= 32 && strips >= 2048)) return scan_short_bwd<T, VEC>(a, strips, s);
   if (a.length <= 2 * S) return scan_bwd_with<T, 1, S, 1, 0, VEC>(a, strips, s);
-  if (a.length <= 8 * S) return scan_bwd_with<T, 4, S, 1, 0, VEC>(a, strips, s);
-  if (strips >= 304 || a.length <= 16 * S) return scan_bwd_with<T, 8, S, 1, D, VEC>(a, strips, s);
-  if (strips >= 76 || a.length <= 64 * S) return scan_bwd_with<T, 8, S, 4, VEC ? 2 : 0, VEC>(a, strips, s);
-  return scan_bwd_with<T, 8, S, 8, VEC ? 2 : 0, VEC>(a, strips, s);
+  if (a.length <= 8 * S || strips > 304) return scan_bwd_with<T, 4, S, 1, D, VEC>(a, strips, s);
+  if (strips >= 128 || a.length <= 16 * S) return scan_bwd_with<T, 8, S, 1, D, VEC>(a, strips, s);
+  if (strips >= 64 || a.length <= 64 * S) return scan_bwd_with<T, 8, S, 4, D, VEC>(a, strips, s);
+  return scan_bwd_with<T, 8, S, 8, D, VEC>(a, strips, s);
 }
 
 }  // namespace
@@ -304,14 +324,15 @@ extern "C" muon_status muon_gated_scan_backward(
   const int strips = (int)((dim + kStrip - 1) / kStrip);
   const ScanBwd a = {length, dim, lddh, ldg, ldx, ldh, strips, mix ? 1.f : 0.f, dh, gate, x, h, state, dlast, starts,
                      token_mask, dgate, dx, dstate};
-  const int64_t rows = batch * length;
-  const bool vec = dim % 4 == 0 && fours(dh, rows, lddh, es) && fours(gate, rows, ldg, es) &&
-                   (!mix || fours(x, rows, ldx, es)) && fours(h, rows, ldh, es) && !off(dgate, 4 * es) &&
-                   !off(dx, 4 * es);
+  const int64_t rows = batch * length, units = batch * strips;
+  const int how = std::max({lie(dh, rows, lddh, es), lie(gate, rows, ldg, es), lie(h, rows, ldh, es),
+                            mix ? lie(x, rows, ldx, es) : (int)kFours});
+  const bool vec = how == kFours && dim % 4 == 0 && !off(dgate, 4 * es) && !off(dx, 4 * es);
   const cudaError_t e = by_type(dtype, [&](auto t) {
     using T = decltype(t);
-    return vec ? scan_bwd_by_size<T, true>(a, batch * strips, s)
-               : scan_bwd_by_size<T, false>(a, batch * strips, s);
+    return vec ? scan_bwd_by_size<T, true, true>(a, units, s)
+               : how != kAnyhow ? scan_bwd_by_size<T, false, true>(a, units, s)
+                                : scan_bwd_by_size<T, false, false>(a, units, s);
   });
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
