@@ -145,19 +145,20 @@ scan_kernel(const __grid_constant__ Scan a) {
       H[i] = run.H = fma(st.keep, run.H, st.in);
       run.Q = fma(st.keep, run.Q, st.lose);
     }
-    if constexpr (D > 0) {
-      start(stage);
-      fg += (uint32_t)(stride * a.ldg);
-      fx += (uint32_t)(stride * a.ldx);
-      stage = stage + 1 == D ? 0 : stage + 1;
-      if (FLAGS) {
-        #pragma unroll
-        for (int d = 0; d + 1 < D; ++d) ahead[d] = ahead[d + 1];
-        ahead[D - 1] = ask_next();
+    Quad front = join_segments<W, CL, FLAGS, false>(sh, run, round, [&] {
+      if constexpr (D > 0) {
+        start(stage);
+        fg += (uint32_t)(stride * a.ldg);
+        fx += (uint32_t)(stride * a.ldx);
+        stage = stage + 1 == D ? 0 : stage + 1;
+        if (FLAGS) {
+          #pragma unroll
+          for (int d = 0; d + 1 < D; ++d) ahead[d] = ahead[d + 1];
+          ahead[D - 1] = ask_next();
+        }
+        advance();
       }
-      advance();
-    }
-    Quad front = join_segments<W, CL, FLAGS, false>(sh, run, round);
+    });
     const int n = ch.any() ? left : 0;
     auto finish = [&](int i) {
       if (FLAGS && (now.starts >> i & 1)) front = quad(0.f);

@@ -295,10 +295,11 @@ __device__ __forceinline__ Quad from_other_half(const Quad& q) {
 // Joins the segments of chunk `round` in order: the first half of warp 0 first, blocks of
 // a cluster by rank.  BACK: the second half of the last warp first, blocks as before.
 // Returns the state in front of the thread's segment.  The state in front of the chunk is
-// read from sh.carry[round & 1] and the one behind it left in the other.  A warp applies
-// only the runs in front of its own; the last one goes on to the state behind the chunk.
-template <int W, int CL, bool FLAGS, bool BACK>
-__device__ __forceinline__ Quad join_segments(RunSlots<W, CL>& sh, const Segment& mine, int round) {
+// read from sh.carry[round & 1] and the one behind it left in the other.  A warp goes
+// through the runs in front of its own only; the last one knows the block's run or the
+// state behind the chunk.  `meanwhile` is done while the blocks of a cluster wait.
+template <int W, int CL, bool FLAGS, bool BACK, typename F>
+__device__ __forceinline__ Quad join_segments(RunSlots<W, CL>& sh, const Segment& mine, int round, F meanwhile) {
   const int lane = threadIdx.x & 31, l = lane & 15, buf = round & 1;
   const int warp = BACK ? W - 1 - (threadIdx.x >> 5) : threadIdx.x >> 5;      // in order
   const bool second = BACK ? lane < 16 : lane >= 16;
@@ -310,54 +311,76 @@ __device__ __forceinline__ Quad join_segments(RunSlots<W, CL>& sh, const Segment
     whole.cut = other.cut || mine.cut;
     if (mine.cut) whole.H = mine.H;
   }
-  const Run run = run_of(whole);
   if (second) {
+    const Run run = run_of(whole);
     RunSlot& to = sh.warp[buf][warp];
     to.m[l] = four(run.m);
     to.k[l] = four(run.k);
     to.H[l] = four(run.H);
     if (FLAGS && l == 0) sh.cut[buf][warp] = run.cut;
   }
+  if (CL == 1) meanwhile();
   if constexpr (W > 1 || CL > 1) __syncthreads();
   else __syncwarp();
   auto warp_run = [&](int w) { return run_in(sh.warp[buf][w], FLAGS ? sh.cut[buf][w] : 0); };
+  Quad p;
   if constexpr (CL > 1) {
     const int rank = cluster_rank();
-    if (threadIdx.x < 16 * CL) {      // 16 threads for each block of the cluster
-      const int to = threadIdx.x >> 4;
-      Run all = warp_run(0);
-      #pragma unroll
-      for (int i = 1; i < W; ++i) all = then(all, warp_run(i));
-      RunSlot& slot = sh.block[buf][rank];
-      put_at(at_rank(&slot.m[l], to), four(all.m));
-      put_at(at_rank(&slot.k[l], to), four(all.k));
-      put_at(at_rank(&slot.H[l], to), four(all.H));
-      if (FLAGS && l == 0) put_at(at_rank(&sh.block_cut[buf][rank], to), (int)all.cut);
+    auto block_run = [&](int c) { return run_in(sh.block[buf][c], FLAGS ? sh.block_cut[buf][c] : 0); };
+    Run ahead = {quad(0.f), quad(1.f), quad(0.f), false}, next = warp_run(0);
+    #pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (w > warp || (w == warp && w < W - 1)) break;      // the last warp takes in its own, too
+      const Run now = next;
+      if (w + 1 < W) next = warp_run(w + 1);
+      if (w == W - 1) {
+        const Run all = then(ahead, now);
+        RunSlot& slot = sh.block[buf][rank];
+        for (int to = lane >> 4; to < CL; to += 2) {
+          put_at(at_rank(&slot.m[l], to), four(all.m));
+          put_at(at_rank(&slot.k[l], to), four(all.k));
+          put_at(at_rank(&slot.H[l], to), four(all.H));
+          if (FLAGS && l == 0) put_at(at_rank(&sh.block_cut[buf][rank], to), (int)all.cut);
+        }
+      } else {
+        ahead = then(ahead, now);
+      }
     }
-    cluster_barrier();
-  }
-  Quad p = quad(sh.carry[buf][l]);
-  auto block_run = [&](int c) { return run_in(sh.block[buf][c], FLAGS ? sh.block_cut[buf][c] : 0); };
-  if constexpr (CL > 1) {
-    const int rank = cluster_rank();
-    for (int c = 0; c < rank; ++c) p = apply(block_run(c), p);
-    if (warp == 0) {
-      Quad q = p;
-      for (int c = rank; c < CL; ++c) q = apply(block_run(c), q);
-      if (second) sh.carry[buf ^ 1][l] = four(q);
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+    meanwhile();
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    p = quad(sh.carry[buf][l]);
+    Run run = block_run(0);
+    Quad q = p;
+    #pragma unroll
+    for (int c = 0; c < CL; ++c) {
+      if (c == rank) p = q;
+      if (c >= rank && warp > 0) break;      // the first warp goes on to the state behind the chunk
+      const Run now = run;
+      if (c + 1 < CL) run = block_run(c + 1);
+      q = apply(now, q);
+    }
+    if (warp == 0 && second) sh.carry[buf ^ 1][l] = four(q);
+    p = apply(ahead, p);
+  } else {
+    p = quad(sh.carry[buf][l]);
+    Run run = warp_run(0);
+    #pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (w >= warp && w < W - 1) break;
+      const Run now = run;
+      if (w + 1 < W) run = warp_run(w + 1);
+      if (w == W - 1) {
+        const Quad q = apply(now, p);
+        if (second) sh.carry[buf ^ 1][l] = four(q);
+      } else {
+        p = apply(now, p);
+      }
     }
   }
-  for (int w = 0; w < warp; ++w) p = apply(warp_run(w), p);
-  if constexpr (CL == 1) {
-    if (warp == W - 1) {
-      const Quad q = apply(warp_run(warp), p);
-      if (second) sh.carry[buf ^ 1][l] = four(q);
-    }
-  }
-  if (second) {
-    Run first = run_of(other);
-    p = apply(first, p);
-  }
+  if (second) p = apply(run_of(other), p);
   return p;
 }
 

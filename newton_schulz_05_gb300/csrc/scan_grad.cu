@@ -171,21 +171,22 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
         run.cut = true;
       }
     }
-    if constexpr (D > 0) {
-      start(stage);
-      fd -= (uint32_t)(stride * a.lddh);
-      fg -= (uint32_t)(stride * a.ldg);
-      fx -= (uint32_t)(stride * a.ldx);
-      fh -= (uint32_t)(stride * a.ldh);
-      stage = stage + 1 == D ? 0 : stage + 1;
-      if (FLAGS) {
-        #pragma unroll
-        for (int k = 0; k + 1 < D; ++k) ahead[k] = ahead[k + 1];
-        ahead[D - 1] = ask_next();
+    Quad c = join_segments<W, CL, FLAGS, true>(sh, run, round, [&] {
+      if constexpr (D > 0) {
+        start(stage);
+        fd -= (uint32_t)(stride * a.lddh);
+        fg -= (uint32_t)(stride * a.ldg);
+        fx -= (uint32_t)(stride * a.ldx);
+        fh -= (uint32_t)(stride * a.ldh);
+        stage = stage + 1 == D ? 0 : stage + 1;
+        if (FLAGS) {
+          #pragma unroll
+          for (int k = 0; k + 1 < D; ++k) ahead[k] = ahead[k + 1];
+          ahead[D - 1] = ask_next();
+        }
+        advance();
       }
-      advance();
-    }
-    Quad c = join_segments<W, CL, FLAGS, true>(sh, run, round);
+    });
     const int n = ch.any() ? inside(t0) : 0;
     T* const dx = static_cast<T*>(a.dx) + out + t0 * a.dim;
     T* const dg = static_cast<T*>(a.dgate) + out + t0 * a.dim;
