@@ -157,28 +157,32 @@ template <typename T, int E> __device__ __forceinline__ typename RawPiece<T, E>:
     return narrow(p);
   }
 }
-template <int E> __device__ __forceinline__ void load_floats(Piece<E>& v, const float* p) {
-  #pragma unroll
-  for (int q = 0; q < E / 4; ++q) {
-    const float4 f = reinterpret_cast<const float4*>(p)[q];
-    v.v[2 * q] = make_float2(f.x, f.y);
-    v.v[2 * q + 1] = make_float2(f.z, f.w);
-  }
-}
-
 // A lane's two pieces of a head.  Those of the rotated part are turned into one another,
-// so no lane needs another's: m and m + rotary / 2 for one half against the other, or
-// neighbouring pieces, which hold their pairs whole.  Both ways they have the E pairs
-// from E * unit on.  G lanes a head, of which dim / 2E have work.
-template <int E> struct Unit {
+// so no lane needs another's: m and m + rotary / 2 for one half against the other, where
+// both pieces have the E pairs from E * unit on; neighbours have their pairs within a piece.
+// Neighbouring lanes have neighbouring pieces throughout.
+template <int E, bool NB> struct Unit {
   int a, b;              // first elements of the pieces
-  bool any, turned;
-  __device__ __forceinline__ Unit(int dim, int rotary, bool neighbours, int u) {
-    any = 2 * E * u < dim;
-    turned = 2 * E * u < rotary;
-    const bool halves = turned && !neighbours;
-    a = halves ? E * u : 2 * E * u;
-    b = halves ? E * u + rotary / 2 : 2 * E * u + E;
+  int pa, pb;            // first pairs of their halves of E angles
+  bool any, ta, tb;      // there is work; the pieces are turned
+  __device__ __forceinline__ Unit(int dim, int rotary, int u) {
+    const int units = dim / (2 * E), turned = rotary / (2 * E);
+    any = u < units;
+    if (NB) {
+      a = E * u;
+      b = E * (u + units);
+      ta = a < rotary;
+      tb = b < rotary;
+      pa = a / 2;
+      pb = b / 2;
+    } else {
+      ta = tb = u < turned;
+      const int first = ta ? 0 : turned;       // of the turned units, or of the others
+      a = E * (first + u);
+      b = a + E * (ta ? turned : units - turned);
+      pa = E * u;
+      pb = pa + E / 2;
+    }
   }
 };
 
@@ -191,6 +195,7 @@ __device__ __forceinline__ void turn(Piece<E>& a, Piece<E>& b, const Piece<E>& c
     };
     #pragma unroll
     for (int j = 0; j < E / 2; ++j) {
+      // pair j of the first piece, pair E / 2 + j of all
       one(a.v[j], j & 1 ? c.v[j / 2].y : c.v[j / 2].x, j & 1 ? s.v[j / 2].y : s.v[j / 2].x);
       const int k = j + E / 2;
       one(b.v[j], k & 1 ? c.v[k / 2].y : c.v[k / 2].x, k & 1 ? s.v[k / 2].y : s.v[k / 2].x);
@@ -198,251 +203,414 @@ __device__ __forceinline__ void turn(Piece<E>& a, Piece<E>& b, const Piece<E>& c
   } else {
     #pragma unroll
     for (int j = 0; j < E / 2; ++j) {
-      const float2 x = a.v[j], y = b.v[j], n = make_float2(-s.v[j].x, -s.v[j].y);
-      a.v[j] = fma2(y, n, mul2(x, c.v[j]));
+      const float2 x = a.v[j], y = b.v[j], t = mul2(x, c.v[j]);
+      a.v[j] = make_float2(fmaf(-s.v[j].x, y.x, t.x), fmaf(-s.v[j].y, y.y, t.y));
       b.v[j] = fma2(x, s.v[j], mul2(y, c.v[j]));
     }
   }
 }
-template <int G> __device__ __forceinline__ float group_sum(float v) {
-  #pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  return v;
-}
+// The lanes of a head: G neighbouring ones of which dim / 2E have work, or exactly dim / 2E
+// (G == 0) where more heads fit in a warp so, as three of 80 fp32 elements in place of two.
+template <int G> struct Lanes {
+  int length, heads, group, lane;      // lanes a head, heads a warp, the lane's head and place
+  __device__ __forceinline__ explicit Lanes(int units) {
+    const int l = threadIdx.x & 31;
+    length = G ? G : units;
+    heads = 32 / length;
+    group = l / length;
+    lane = l - group * length;
+  }
+  // over the lanes of a head, the same value in each
+  __device__ __forceinline__ float sum(float v) const {
+    if constexpr (G > 0) {
+      #pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+      return v;
+    } else {
+      #pragma unroll
+      for (int o = 8; o > 0; o >>= 1) {
+        const float u = __shfl_down_sync(~0u, v, o);
+        if (lane < o && lane + o < length) v += u;
+      }
+      return __shfl_sync(~0u, v, group * length);
+    }
+  }
+};
 
-// What a warp works through: `chunks` items a token, of `passes` passes over 32 / G heads.
-// The passes of a token: those of the queries, then those of the keys.
-struct HeadWork { int64_t items; int chunks, passes, q_passes, all_passes; };
+// The first blocks work on the queries, the others on the keys.  A side's heads are numbered
+// through, n = token * heads + head, and the side's warps take runs of them in turn: a run is
+// about a token, whose angles are loaded once, and what the warps read at a time lies together
+// (one long run a warp took 127 us where these take 108 for [32768, 32 + 8, 128] bf16).
+struct HeadWork { int blocks[2], run[2]; int wbf16; };      // run: passes
 
-// both sides' weights in fp32 (1 where there are none), for every thread of the block
-__device__ __forceinline__ void stage_weights(float* to, const Heads& a, int wbf16) {
-  for (int i = threadIdx.x; i < 2 * a.dim; i += kHeadThreads) {
-    const void* w = a.side[i >= a.dim].weight;
-    const int j = i >= a.dim ? i - a.dim : i;
-    to[i] = !w ? 1.f : wbf16 ? to_f(static_cast<const __nv_bfloat16*>(w)[j]) : static_cast<const float*>(w)[j];
+// One side's weights in fp32 (1 where there are none), as the lanes of a warp need them: four at a
+// time, those of all lanes next to one another
+template <int E> struct HeadWeights { float4 v[E / 2][32]; };
+template <int E, typename U>
+__device__ __forceinline__ void stage_weights(HeadWeights<E>& to, const HeadSide& side, const U& un, int wbf16) {
+  if (threadIdx.x < 32 && un.any) {
+    #pragma unroll
+    for (int q = 0; q < E / 2; ++q) {
+      const int at = q < E / 4 ? un.a + 4 * q : un.b + 4 * (q - E / 4);
+      float w[4];
+      #pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = !side.weight ? 1.f
+               : wbf16      ? to_f(static_cast<const __nv_bfloat16*>(side.weight)[at + j])
+                            : static_cast<const float*>(side.weight)[at + j];
+      to.v[q][threadIdx.x] = make_float4(w[0], w[1], w[2], w[3]);
+    }
   }
   __syncthreads();
+}
+// of the first piece or the second
+template <int E> __device__ __forceinline__ void load_weights(Piece<E>& v, const HeadWeights<E>& from, int piece) {
+  #pragma unroll
+  for (int q = 0; q < E / 4; ++q) {
+    const float4 f = from.v[piece * (E / 4) + q][threadIdx.x & 31];
+    v.v[2 * q] = make_float2(f.x, f.y);
+    v.v[2 * q + 1] = make_float2(f.z, f.w);
+  }
+}
+__device__ __forceinline__ float rsqrt_fast(float x) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A lane's N pieces of a pass (one head a group of lanes) and the position of its token, in a
+// ring of kHeadRing passes that it copies, waits for and reads alone
+constexpr int kHeadRing = 4;
+template <typename Raw, int N> struct HeadRing {
+  Raw* base;
+  int64_t* positions;
+  __device__ __forceinline__ explicit HeadRing(void* smem) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    base = static_cast<Raw*>(smem) + warp * (kHeadRing * N * 32) + lane;
+    positions = reinterpret_cast<int64_t*>(static_cast<Raw*>(smem) + kHeadWarps * (kHeadRing * N * 32)) +
+                warp * (kHeadRing * 32) + lane;
+  }
+  __device__ __forceinline__ Raw* slot(int stage, int n) const { return base + (stage * N + n) * 32; }
+  __device__ __forceinline__ int64_t* position(int stage) const { return positions + stage * 32; }
+  static constexpr size_t kBytes = (sizeof(Raw) * N + 8) * kHeadRing * kHeadThreads;
+  template <typename V> __device__ __forceinline__ static void copy(V* to, const void* p) {
+    const uint32_t s = (uint32_t)__cvta_generic_to_shared(to);
+    if constexpr (sizeof(V) == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(s), "l"(p) : "memory");
+    else asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(s), "l"(p) : "memory");
+  }
+};
+
+// Where a lane's group is in its walk through a side's heads
+struct HeadWalk {
+  int64_t n, all, token;
+  int head, heads;
+  int pass, run;          // of a run
+  int64_t jump;           // to the warp's next run
+  __device__ __forceinline__ void find() {
+    if (n >> 32) token = n / heads;
+    else token = (uint32_t)n / (uint32_t)heads;
+    head = (int)(n - token * heads);
+  }
+  __device__ __forceinline__ bool live() const { return n < all; }
+  // by `by` heads; whether the token may be another
+  __device__ __forceinline__ bool next(int by) {
+    n += by;
+    head += by;
+    if (++pass == run) {
+      pass = 0;
+      n += jump;
+    } else if (head < heads) {
+      return false;
+    }
+    find();
+    return true;
+  }
+};
+// of a lane with work, `group` of the warp's `by`; passes: of the warp's runs, all of them
+__device__ __forceinline__ HeadWalk walk_of(const Heads& a, const HeadWork& w, int key, int group, int by, bool has,
+                                            int& passes) {
+  const int64_t warps = (int64_t)w.blocks[key] * kHeadWarps, run = (int64_t)w.run[key] * by;
+  const int64_t warp = (int64_t)(blockIdx.x - (key ? w.blocks[0] : 0)) * kHeadWarps + (threadIdx.x >> 5);
+  HeadWalk k;
+  k.n = warp * run + group;
+  k.heads = a.side[key].heads;
+  k.all = has ? a.tokens * k.heads : 0;
+  k.pass = 0;
+  k.run = w.run[key];
+  k.jump = (warps - 1) * run;
+  k.find();
+  const int64_t runs = (a.tokens * k.heads + run - 1) / run;
+  passes = warp < runs ? (int)((runs - 1 - warp) / warps + 1) * k.run : 0;
+  return k;
+}
+
+// the angles of the lane's pairs at a position: 1 and 0 where there are none
+template <int E, bool NB>
+__device__ __forceinline__ void angles(Piece<E>& c, Piece<E>& s, const Heads& a, int64_t pos, const Unit<E, NB>& un) {
+  #pragma unroll
+  for (int j = 0; j < E / 2; ++j) {
+    c.v[j] = both(1.f);
+    s.v[j] = both(0.f);
+  }
+  if (pos < 0) return;
+  const float* const pc = a.cos + pos * (a.rotary / 2);
+  const float* const ps = a.sin + pos * (a.rotary / 2);
+  #pragma unroll
+  for (int j = 0; j < E / 4; ++j) {      // E / 2 angles a half
+    if (un.ta) {
+      c.v[j] = reinterpret_cast<const float2*>(pc + un.pa)[j];
+      s.v[j] = reinterpret_cast<const float2*>(ps + un.pa)[j];
+    }
+    if (un.tb) {
+      c.v[E / 4 + j] = reinterpret_cast<const float2*>(pc + un.pb)[j];
+      s.v[E / 4 + j] = reinterpret_cast<const float2*>(ps + un.pb)[j];
+    }
+  }
 }
 
 constexpr int kPieceDim = 512;        // widest head of these kernels
 
 template <typename T, int E, int G, bool NB>
 __global__ void __launch_bounds__(kHeadThreads, 3)
-heads_piece_kernel(const __grid_constant__ Heads a, const __grid_constant__ HeadWork w, int wbf16) {
+heads_piece_kernel(const __grid_constant__ Heads a, const __grid_constant__ HeadWork w) {
   using Raw = typename RawPiece<T, E>::type;
-  constexpr int B = 32 / G, U = 2;        // heads a pass, passes in flight
-  __shared__ alignas(16) float weights[2 * kPieceDim];
+  extern __shared__ uint4 ring[];
+  __shared__ HeadWeights<E> weights;
   pdl_wait();
-  stage_weights(weights, a, wbf16);
-  const int lane = threadIdx.x & 31, group = lane / G;
-  const Unit<E> un(a.dim, a.rotary, NB, lane % G);
+  const int key = (int)blockIdx.x >= w.blocks[0];
+  const HeadSide& side = a.side[key];
+  const Lanes<G> ln(a.dim / (2 * E));
+  const Unit<E, NB> un(a.dim, a.rotary, ln.lane);
+  stage_weights(weights, side, un, w.wbf16);
   const float inv = 1.f / (float)a.dim;
-  for (int64_t item = (int64_t)blockIdx.x * kHeadWarps + (threadIdx.x >> 5); item < w.items;
-       item += (int64_t)gridDim.x * kHeadWarps) {
-    const int64_t t = w.chunks == 1 ? item : item / w.chunks;
-    int pass = w.chunks == 1 ? 0 : (int)(item % w.chunks) * w.passes;
-    const int end = min(pass + w.passes, w.all_passes);
-    const int64_t pos = position_of(a, t);
-    Piece<E> c, s;
+  const HeadRing<Raw, 2> slots(ring);
+  int passes;
+  HeadWalk in = walk_of(a, w, key, ln.group, ln.heads, un.any && ln.group < ln.heads, passes), at = in;
+  const T* const x0 = static_cast<const T*>(side.x) + un.a;
+  const T* px = x0 + in.token * side.ld + in.head * side.step;
+  const int to_b = un.b - un.a;
+  const int64_t step = ln.heads * side.step;
+  bool other_in = true, other = true;      // another token than in the pass before
+  auto fetch = [&](int stage) {
+    if (in.live()) {
+      slots.copy(slots.slot(stage, 0), px);
+      slots.copy(slots.slot(stage, 1), px + to_b);
+      if (other_in && a.positions) slots.copy(slots.position(stage), a.positions + in.token);
+    }
+    copies_commit();
+    px += step;
+    other_in = in.next(ln.heads);
+    if (other_in) px = x0 + in.token * side.ld + in.head * side.step;
+  };
+  #pragma unroll
+  for (int d = 0; d < kHeadRing; ++d) fetch(d);
+  T* out = static_cast<T*>(side.out) + at.n * a.dim + un.a;
+  Piece<E> c, s;
+  int64_t pos = -1;
+  int stage = 0;
+  for (int i = 0; i < passes; ++i) {
+    copies_wait<kHeadRing - 1>();
+    Piece<E> x, y;
+    clear(x);
+    clear(y);
+    const bool live = at.live();
+    if (live) {
+      if (other) {
+        pos = !a.rotary ? 0 : a.positions ? *slots.position(stage) : at.token % a.period;
+        if (pos >= a.table && a.rotary) pos = -1;
+        angles(c, s, a, pos, un);
+      }
+      widen(x, *slots.slot(stage, 0));
+      widen(y, *slots.slot(stage, 1));
+    }
+    fetch(stage);
+    stage = stage + 1 == kHeadRing ? 0 : stage + 1;
+    float2 sq = both(0.f);
     #pragma unroll
-    for (int j = 0; j < E / 2; ++j) {
-      c.v[j] = both(1.f);
-      s.v[j] = both(0.f);
-    }
-    if (un.turned && pos >= 0) {
-      load_floats(c, a.cos + pos * (a.rotary / 2) + E * (lane % G));
-      load_floats(s, a.sin + pos * (a.rotary / 2) + E * (lane % G));
-    }
-    for (; pass < end; pass += U) {
-      Raw ra[U], rb[U];
-      int head[U];
-      bool key[U], has[U];
-      #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        key[k] = pass + k >= w.q_passes;
-        head[k] = (key[k] ? pass + k - w.q_passes : pass + k) * B + group;
-        has[k] = pass + k < end && un.any && head[k] < a.side[key[k]].heads;
-        ra[k] = rb[k] = Raw{};
-        if (has[k] && pos >= 0) {
-          const T* x = static_cast<const T*>(a.side[key[k]].x) + t * a.side[key[k]].ld + head[k] * a.side[key[k]].step;
-          ra[k] = *reinterpret_cast<const Raw*>(x + un.a);
-          rb[k] = *reinterpret_cast<const Raw*>(x + un.b);
-        }
-      }
-      #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        Piece<E> x, y, wx, wy;
-        widen(x, ra[k]);
-        widen(y, rb[k]);
-        float2 sq = both(0.f);
+    for (int j = 0; j < E / 2; ++j) sq = fma2(x.v[j], x.v[j], fma2(y.v[j], y.v[j], sq));
+    const float rstd = rsqrt_fast(fmaf(ln.sum(sq.x + sq.y), inv, a.eps));
+    if (live) {
+      Raw ra = Raw{}, rb = Raw{};
+      if (pos >= 0) {
+        Piece<E> wx;
+        load_weights(wx, weights, 0);
         #pragma unroll
-        for (int j = 0; j < E / 2; ++j) sq = fma2(x.v[j], x.v[j], fma2(y.v[j], y.v[j], sq));
-        const float rstd = 1.f / sqrtf(fmaf(group_sum<G>(sq.x + sq.y), inv, a.eps));
-        if (!has[k]) continue;
-        load_floats(wx, weights + key[k] * a.dim + un.a);
-        load_floats(wy, weights + key[k] * a.dim + un.b);
+        for (int j = 0; j < E / 2; ++j) x.v[j] = mul2(mul2(x.v[j], both(rstd)), wx.v[j]);
+        load_weights(wx, weights, 1);
         #pragma unroll
-        for (int j = 0; j < E / 2; ++j) {
-          x.v[j] = mul2(mul2(x.v[j], both(rstd)), wx.v[j]);
-          y.v[j] = mul2(mul2(y.v[j], both(rstd)), wy.v[j]);
-        }
-        if (un.turned) turn<E, NB>(x, y, c, s);
-        if (pos < 0) {
-          clear(x);
-          clear(y);
-        }
-        T* out = static_cast<T*>(a.side[key[k]].out) + (t * a.side[key[k]].heads + head[k]) * a.dim;
-        *reinterpret_cast<Raw*>(out + un.a) = pack<T>(x);
-        *reinterpret_cast<Raw*>(out + un.b) = pack<T>(y);
+        for (int j = 0; j < E / 2; ++j) y.v[j] = mul2(mul2(y.v[j], both(rstd)), wx.v[j]);
+        turn<E, NB>(x, y, c, s);
+        ra = pack<T>(x);
+        rb = pack<T>(y);
       }
+      *reinterpret_cast<Raw*>(out) = ra;
+      *reinterpret_cast<Raw*>(out + to_b) = rb;
     }
+    const int64_t before = at.n;
+    other = at.next(ln.heads);
+    out += (at.n - before) * a.dim;
   }
 }
 
-// The queries of all tokens first, then the keys: one set of weight sums in registers.
 template <typename T, int E, int G, bool NB>
 __global__ void __launch_bounds__(kHeadThreads, 2)
-heads_piece_bwd_kernel(const __grid_constant__ Heads a, const __grid_constant__ HeadWork wq,
-                       const __grid_constant__ HeadWork wk, int wbf16) {
+heads_piece_bwd_kernel(const __grid_constant__ Heads a, const __grid_constant__ HeadWork w) {
   using Raw = typename RawPiece<T, E>::type;
-  constexpr int B = 32 / G;
-  __shared__ alignas(16) float weights[2 * kPieceDim], sums[kHeadWarps * kPieceDim];
+  extern __shared__ uint4 ring[];
+  __shared__ HeadWeights<E> weights;
+  __shared__ alignas(16) float sums[kHeadWarps * kPieceDim];
   pdl_wait();
-  stage_weights(weights, a, wbf16);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = lane / G;
-  const Unit<E> un(a.dim, a.rotary, NB, lane % G);
+  const int key = (int)blockIdx.x >= w.blocks[0], warp = threadIdx.x >> 5;
+  const HeadSide& side = a.side[key];
+  const Lanes<G> ln(a.dim / (2 * E));
+  const Unit<E, NB> un(a.dim, a.rotary, ln.lane);
+  stage_weights(weights, side, un, w.wbf16);
   const float inv = 1.f / (float)a.dim;
-  for (int key = 0; key < 2; ++key) {
-    const HeadWork& w = key ? wk : wq;
-    const HeadSide& side = a.side[key];
-    Piece<E> sa, sb, wa, wb;
-    clear(sa);
-    clear(sb);
-    clear(wa);
-    clear(wb);
-    if (un.any) {
-      load_floats(wa, weights + key * a.dim + un.a);
-      load_floats(wb, weights + key * a.dim + un.b);
+  const HeadRing<Raw, 4> slots(ring);
+  int passes;
+  HeadWalk in = walk_of(a, w, key, ln.group, ln.heads, un.any && ln.group < ln.heads, passes), at = in;
+  const T* const x0 = static_cast<const T*>(side.x) + un.a;
+  const T* const d0 = static_cast<const T*>(side.dy) + un.a;
+  const T* px = x0 + in.token * side.ld + in.head * side.step;
+  const T* pd = d0 + in.token * side.lddy + in.head * side.stepdy;
+  const int to_b = un.b - un.a;
+  const int64_t step = ln.heads * side.step, step_d = ln.heads * side.stepdy;
+  bool other_in = true, other = true;
+  auto fetch = [&](int stage) {
+    if (in.live()) {
+      slots.copy(slots.slot(stage, 0), px);
+      slots.copy(slots.slot(stage, 1), px + to_b);
+      slots.copy(slots.slot(stage, 2), pd);
+      slots.copy(slots.slot(stage, 3), pd + to_b);
+      if (other_in && a.positions) slots.copy(slots.position(stage), a.positions + in.token);
     }
-    for (int64_t item = (int64_t)blockIdx.x * kHeadWarps + warp; item < w.items;
-         item += (int64_t)gridDim.x * kHeadWarps) {
-      const int64_t t = w.chunks == 1 ? item : item / w.chunks;
-      int pass = w.chunks == 1 ? 0 : (int)(item % w.chunks) * w.passes;
-      const int end = min(pass + w.passes, w.all_passes);
-      const int64_t pos = position_of(a, t);
-      Piece<E> c, s;
-      #pragma unroll
-      for (int j = 0; j < E / 2; ++j) {
-        c.v[j] = both(1.f);
-        s.v[j] = both(0.f);
-      }
-      if (un.turned && pos >= 0) {
-        load_floats(c, a.cos + pos * (a.rotary / 2) + E * (lane % G));
-        load_floats(s, a.sin + pos * (a.rotary / 2) + E * (lane % G));
-      }
-      Raw xa, xb, da, db;
-      auto fetch = [&](int p) {
-        const int head = p * B + group;
-        xa = xb = da = db = Raw{};
-        if (pos < 0 || p >= end || !un.any || head >= side.heads) return;
-        const T* x = static_cast<const T*>(side.x) + t * side.ld + head * side.step;
-        const T* d = static_cast<const T*>(side.dy) + t * side.lddy + head * side.stepdy;
-        xa = *reinterpret_cast<const Raw*>(x + un.a);
-        xb = *reinterpret_cast<const Raw*>(x + un.b);
-        da = *reinterpret_cast<const Raw*>(d + un.a);
-        db = *reinterpret_cast<const Raw*>(d + un.b);
-      };
-      fetch(pass);
-      for (; pass < end; ++pass) {
-        Piece<E> x, y, g, h;
-        widen(x, xa);
-        widen(y, xb);
-        widen(g, da);
-        widen(h, db);
-        fetch(pass + 1);
-        if (un.turned) {
-          Piece<E> n;
-          #pragma unroll
-          for (int j = 0; j < E / 2; ++j) n.v[j] = make_float2(-s.v[j].x, -s.v[j].y);
-          turn<E, NB>(g, h, c, n);
-        }
-        float2 sq = both(0.f), dot = both(0.f);
+    copies_commit();
+    px += step;
+    pd += step_d;
+    other_in = in.next(ln.heads);
+    if (other_in) {
+      px = x0 + in.token * side.ld + in.head * side.step;
+      pd = d0 + in.token * side.lddy + in.head * side.stepdy;
+    }
+  };
+  #pragma unroll
+  for (int d = 0; d < kHeadRing; ++d) fetch(d);
+  T* out = static_cast<T*>(side.out) + at.n * a.dim + un.a;
+  Piece<E> sa, sb, c, s;
+  clear(sa);
+  clear(sb);
+  int64_t pos = -1;
+  int stage = 0;
+  for (int i = 0; i < passes; ++i) {
+    copies_wait<kHeadRing - 1>();
+    Piece<E> x, y, g, h;
+    clear(x);
+    clear(y);
+    clear(g);
+    clear(h);
+    const bool live = at.live();
+    if (live) {
+      if (other) {
+        pos = !a.rotary ? 0 : a.positions ? *slots.position(stage) : at.token % a.period;
+        if (pos >= a.table && a.rotary) pos = -1;
+        angles(c, s, a, pos, un);
         #pragma unroll
-        for (int j = 0; j < E / 2; ++j) {
-          sq = fma2(x.v[j], x.v[j], fma2(y.v[j], y.v[j], sq));
-          dot = fma2(mul2(g.v[j], wa.v[j]), x.v[j], fma2(mul2(h.v[j], wb.v[j]), y.v[j], dot));
-        }
-        const int head = pass * B + group;
-        const bool live = pos >= 0 && head < side.heads;      // else 1 / 0 without eps
-        const float ms = fmaf(group_sum<G>(sq.x + sq.y), inv, a.eps);
-        const float rstd = live ? 1.f / sqrtf(ms) : 0.f;
-        // dx = rstd (g w - h mean(g w h)) with h = x rstd
-        const float mean = group_sum<G>(dot.x + dot.y) * rstd * inv;
-        #pragma unroll
-        for (int j = 0; j < E / 2; ++j) {
-          x.v[j] = mul2(x.v[j], both(rstd));
-          y.v[j] = mul2(y.v[j], both(rstd));
-          sa.v[j] = fma2(g.v[j], x.v[j], sa.v[j]);
-          sb.v[j] = fma2(h.v[j], y.v[j], sb.v[j]);
-          x.v[j] = mul2(fma2(x.v[j], both(-mean), mul2(g.v[j], wa.v[j])), both(rstd));
-          y.v[j] = mul2(fma2(y.v[j], both(-mean), mul2(h.v[j], wb.v[j])), both(rstd));
-        }
-        if (side.out && un.any && head < side.heads) {
-          T* out = static_cast<T*>(side.out) + (t * side.heads + head) * a.dim;
-          *reinterpret_cast<Raw*>(out + un.a) = pack<T>(x);
-          *reinterpret_cast<Raw*>(out + un.b) = pack<T>(y);
-        }
+        for (int j = 0; j < E / 2; ++j) s.v[j] = make_float2(-s.v[j].x, -s.v[j].y);      // turned back
+      }
+      if (pos >= 0) {
+        widen(x, *slots.slot(stage, 0));
+        widen(y, *slots.slot(stage, 1));
+        widen(g, *slots.slot(stage, 2));
+        widen(h, *slots.slot(stage, 3));
+        turn<E, NB>(g, h, c, s);
       }
     }
-    if (!a.part) continue;
-    // the warp's groups, then the block's warps in order
+    fetch(stage);
+    stage = stage + 1 == kHeadRing ? 0 : stage + 1;
+    float2 sq = both(0.f), dot = both(0.f);
     #pragma unroll
-    for (int o = G; o < 32; o <<= 1)
+    for (int j = 0; j < E / 2; ++j) sq = fma2(x.v[j], x.v[j], fma2(y.v[j], y.v[j], sq));
+    const float ms = fmaf(ln.sum(sq.x + sq.y), inv, a.eps);
+    const float rstd = live && pos >= 0 ? rsqrt_fast(ms) : 0.f;      // not 1 / 0 where there is no head
+    // h = x rstd; the sums of g h; then g w in g's place
+    #pragma unroll
+    for (int j = 0; j < E / 2; ++j) {
+      x.v[j] = mul2(x.v[j], both(rstd));
+      y.v[j] = mul2(y.v[j], both(rstd));
+      sa.v[j] = fma2(g.v[j], x.v[j], sa.v[j]);
+      sb.v[j] = fma2(h.v[j], y.v[j], sb.v[j]);
+    }
+    if (live) {
+      Piece<E> wa;
+      load_weights(wa, weights, 0);
+      #pragma unroll
+      for (int j = 0; j < E / 2; ++j) g.v[j] = mul2(g.v[j], wa.v[j]);
+      load_weights(wa, weights, 1);
+      #pragma unroll
+      for (int j = 0; j < E / 2; ++j) h.v[j] = mul2(h.v[j], wa.v[j]);
+    }
+    #pragma unroll
+    for (int j = 0; j < E / 2; ++j) dot = fma2(g.v[j], x.v[j], fma2(h.v[j], y.v[j], dot));
+    // dx = rstd (g w - h mean(g w h))
+    const float mean = ln.sum(dot.x + dot.y) * inv;
+    if (live && side.out) {
       #pragma unroll
       for (int j = 0; j < E / 2; ++j) {
-        sa.v[j].x += __shfl_xor_sync(~0u, sa.v[j].x, o);
-        sa.v[j].y += __shfl_xor_sync(~0u, sa.v[j].y, o);
-        sb.v[j].x += __shfl_xor_sync(~0u, sb.v[j].x, o);
-        sb.v[j].y += __shfl_xor_sync(~0u, sb.v[j].y, o);
+        x.v[j] = mul2(fma2(x.v[j], both(-mean), g.v[j]), both(rstd));
+        y.v[j] = mul2(fma2(y.v[j], both(-mean), h.v[j]), both(rstd));
       }
-    __syncthreads();
-    if (group == 0 && un.any) {
+      *reinterpret_cast<Raw*>(out) = pack<T>(x);
+      *reinterpret_cast<Raw*>(out + to_b) = pack<T>(y);
+    }
+    const int64_t before = at.n;
+    other = at.next(ln.heads);
+    out += (at.n - before) * a.dim;
+  }
+  if (!a.part) return;
+  // the warp's groups, then the block's warps in order
+  __syncwarp();
+  for (int group = 0; group < ln.heads; ++group) {
+    if (ln.group == group && un.any) {
       #pragma unroll
       for (int j = 0; j < E / 2; ++j) {
-        reinterpret_cast<float2*>(sums + warp * a.dim + un.a)[j] = sa.v[j];
-        reinterpret_cast<float2*>(sums + warp * a.dim + un.b)[j] = sb.v[j];
+        float2* const ta = reinterpret_cast<float2*>(sums + warp * a.dim + un.a) + j;
+        float2* const tb = reinterpret_cast<float2*>(sums + warp * a.dim + un.b) + j;
+        *ta = group ? add2(*ta, sa.v[j]) : sa.v[j];
+        *tb = group ? add2(*tb, sb.v[j]) : sb.v[j];
       }
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.dim; i += kHeadThreads) {
-      float v = 0.f;
-      #pragma unroll
-      for (int k = 0; k < kHeadWarps; ++k) v += sums[k * a.dim + i];
-      a.part[((int64_t)blockIdx.x * 2 + key) * a.dim + i] = v;
-    }
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.dim; i += kHeadThreads) {
+    float v = 0.f;
+    #pragma unroll
+    for (int k = 0; k < kHeadWarps; ++k) v += sums[k * a.dim + i];
+    a.part[(int64_t)blockIdx.x * a.dim + i] = v;
   }
 }
 
-// 32 columns a block, added up by eight warps
+// 32 columns of one side a block, added up by eight warps: rows of `part`
+// from first[side] on, or (both_rows) each row with both sides' columns
+struct HeadJoin { const float* part; int64_t ld; int first[2], parts[2]; bool both_rows; void* out[2]; };
 template <typename WT>
-__global__ void __launch_bounds__(kHeadThreads)
-heads_join_kernel(int dim, int parts, const float* part, WT* dq, WT* dk) {
+__global__ void __launch_bounds__(kHeadThreads) heads_join_kernel(int dim, const __grid_constant__ HeadJoin j) {
   __shared__ float sums[kHeadWarps][32];
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, key = blockIdx.y, i = blockIdx.x * 32 + lane;
+  const float* part = j.part + j.first[key] * j.ld + (j.both_rows ? key * dim : 0) + i;
   float v = 0.f;
-  if (i < 2 * dim) {
+  if (i < dim) {
     #pragma unroll 4
-    for (int p = warp; p < parts; p += kHeadWarps) v += part[(int64_t)p * 2 * dim + i];
+    for (int p = warp; p < j.parts[key]; p += kHeadWarps) v += part[p * j.ld];
   }
   sums[warp][lane] = v;
   __syncthreads();
-  if (warp > 0 || i >= 2 * dim) return;
+  if (warp > 0 || i >= dim) return;
   v = 0.f;
   #pragma unroll
   for (int k = 0; k < kHeadWarps; ++k) v += sums[k][lane];
-  WT* out = i < dim ? dq : dk;
-  if (out) out[i < dim ? i : i - dim] = from_f<WT>(v);
+  if (j.out[key]) static_cast<WT*>(j.out[key])[i] = from_f<WT>(v);
 }
 
 // --------------------------------------------------------------------- host
@@ -479,16 +647,19 @@ bool whole_units(const Heads& a, int e, size_t es) {
   return ok;
 }
 
-// f(pieces of E elements, lanes a head) as integral constants: 16-byte pieces where heads allow
-// them, else pieces of four; the least lanes that hold a head.  False where neither fits.
+// f(pieces of E elements, lanes a head, heads a warp), the first two as integral constants:
+// 16-byte pieces where heads allow them, else pieces of four; the least lanes that hold a head,
+// a power of two of them unless fewer let more heads in.  False where neither piece fits.
 template <typename T, typename F> bool by_units(const Heads& a, F f) {
   auto lanes = [&](auto e) {
     constexpr int E = decltype(e)::value;
-    const int l = a.dim / (2 * E);
-    if (l <= 4) f(e, std::integral_constant<int, 4>());
-    else if (l <= 8) f(e, std::integral_constant<int, 8>());
-    else if (l <= 16) f(e, std::integral_constant<int, 16>());
-    else f(e, std::integral_constant<int, 32>());
+    const int l = a.dim / (2 * E), g = l <= 2 ? 2 : l <= 4 ? 4 : l <= 8 ? 8 : l <= 16 ? 16 : 32;
+    if (32 / l > 32 / g && l > 2) f(e, std::integral_constant<int, 0>(), 32 / l);
+    else if (g == 2) f(e, std::integral_constant<int, 2>(), 16);
+    else if (g == 4) f(e, std::integral_constant<int, 4>(), 8);
+    else if (g == 8) f(e, std::integral_constant<int, 8>(), 4);
+    else if (g == 16) f(e, std::integral_constant<int, 16>(), 2);
+    else f(e, std::integral_constant<int, 32>(), 1);
   };
   if (whole_units(a, kEl<T>, sizeof(T))) {
     lanes(std::integral_constant<int, kEl<T>>());
@@ -501,14 +672,25 @@ template <typename T, typename F> bool by_units(const Heads& a, F f) {
   return false;
 }
 
-// A warp takes all passes of a token where there are tokens for all warps, else fewer.
-HeadWork work_of(int64_t tokens, int q_passes, int all_passes, int64_t warps) {
-  int64_t chunks = (warps + tokens - 1) / tokens;
-  if (chunks > all_passes) chunks = all_passes;
-  if (chunks < 1) chunks = 1;
-  const int passes = (int)((all_passes + chunks - 1) / chunks);
-  chunks = passes ? (all_passes + passes - 1) / passes : 0;
-  return {tokens * chunks, (int)chunks, passes, q_passes, all_passes};
+// Blocks for the two sides out of `most`, by their heads; B heads a pass of a warp.  A run is
+// a token's heads, or what a warp has at all.
+HeadWork work_of(const Heads& a, int B, int most, int wbf16) {
+  HeadWork w = {{0, 0}, {1, 1}, wbf16};
+  const int64_t q = a.tokens * a.side[0].heads, k = a.tokens * a.side[1].heads;
+  for (int i = 0; i < 2; ++i) {
+    const int64_t n = i ? k : q;
+    if (!n) continue;
+    const int64_t passes = (n + B - 1) / B;
+    int64_t blocks = i ? most - w.blocks[0] : (int64_t)((double)most * q / (q + k) + 0.5);
+    if (i == 0 && k && blocks > most - 1) blocks = most - 1;
+    if (blocks < 1) blocks = 1;
+    const int64_t of_warp = (passes + blocks * kHeadWarps - 1) / (blocks * kHeadWarps);
+    const int64_t of_token = (a.side[i].heads + B - 1) / B;
+    w.run[i] = (int)(of_token < of_warp ? of_token : of_warp);
+    const int64_t need = (passes + (int64_t)w.run[i] * kHeadWarps - 1) / ((int64_t)w.run[i] * kHeadWarps);
+    w.blocks[i] = (int)(need < blocks ? need : blocks);
+  }
+  return w;
 }
 
 template <typename F> cudaError_t by_both(int dtype, int wdtype, F f) {
@@ -547,14 +729,12 @@ extern "C" muon_status muon_norm_rotate_heads(
   const cudaError_t e = by_both(dtype, wdtype, [&](auto t, auto w) {
     using T = decltype(t);
     cudaError_t e = cudaSuccess;
-    if (by_units<T>(a, [&](auto pe, auto pg) {
-          constexpr int E = decltype(pe)::value, G = decltype(pg)::value, B = 32 / G, blocks = 152 * 3;
-          const int pq = (q_heads + B - 1) / B, all = pq + (k_heads + B - 1) / B;
-          const HeadWork hw = work_of(tokens, pq, all, blocks * kHeadWarps);
-          const int64_t need = (hw.items + kHeadWarps - 1) / kHeadWarps;
+    if (by_units<T>(a, [&](auto pe, auto pg, int B) {
+          constexpr int E = decltype(pe)::value, G = decltype(pg)::value;
+          constexpr size_t smem = HeadRing<typename RawPiece<T, E>::type, 2>::kBytes;
+          const HeadWork hw = work_of(a, B, 152 * 3, wdtype == MUON_BF16);
           e = launch_k(neighbours ? heads_piece_kernel<T, E, G, true> : heads_piece_kernel<T, E, G, false>,
-                       dim3((unsigned)(need < blocks ? need : blocks)), dim3(kHeadThreads), 0, s, true, a, hw,
-                       (int)(wdtype == MUON_BF16));
+                       dim3(hw.blocks[0] + hw.blocks[1]), dim3(kHeadThreads), smem, s, true, a, hw);
         }))
       return e;
     return launch_k(heads_kernel<decltype(t), decltype(w)>, dim3((unsigned)(want < 152 * 8 ? want : 152 * 8)),
@@ -615,26 +795,27 @@ extern "C" muon_status muon_norm_rotate_heads_backward(
     using T = decltype(t);
     using WT = decltype(w);
     cudaError_t e = cudaSuccess;
-    int used = parts;
-    if (!by_units<T>(a, [&](auto pe, auto pg) {
-          constexpr int E = decltype(pe)::value, G = decltype(pg)::value, B = 32 / G;
-          const int64_t warps = (int64_t)kHeadParts * kHeadWarps;
-          const int pq = (q_heads + B - 1) / B, pk = (k_heads + B - 1) / B;
-          const HeadWork wq = work_of(tokens, pq, pq, warps), wk = work_of(tokens, pk, pk, warps);
-          const int64_t items = wq.items > wk.items ? wq.items : wk.items;
-          const int64_t need = (items + kHeadWarps - 1) / kHeadWarps;
-          used = (int)(need < parts ? need : parts);
-          e = launch_k(neighbours ? heads_piece_bwd_kernel<T, E, G, true> : heads_piece_bwd_kernel<T, E, G, false>,
-                       dim3(used), dim3(kHeadThreads), 0, s, true, a, wq, wk, (int)(wdtype == MUON_BF16));
+    HeadJoin j = {a.part, dim, {0, 0}, {0, 0}, false, {q_dweight, k_dweight}};
+    if (!by_units<T>(a, [&](auto pe, auto pg, int B) {
+          constexpr int E = decltype(pe)::value, G = decltype(pg)::value;
+          constexpr size_t smem = HeadRing<typename RawPiece<T, E>::type, 4>::kBytes;
+          const HeadWork hw = work_of(a, B, 2 * parts < kHeadParts ? 2 * parts : kHeadParts, wdtype == MUON_BF16);
+          j.first[1] = j.parts[0] = hw.blocks[0];
+          j.parts[1] = hw.blocks[1];
+          e = neighbours ? allow_shared<heads_piece_bwd_kernel<T, E, G, true>>(smem)
+                         : allow_shared<heads_piece_bwd_kernel<T, E, G, false>>(smem);
+          if (e == cudaSuccess)
+            e = launch_k(neighbours ? heads_piece_bwd_kernel<T, E, G, true> : heads_piece_bwd_kernel<T, E, G, false>,
+                         dim3(hw.blocks[0] + hw.blocks[1]), dim3(kHeadThreads), smem, s, true, a, hw);
         })) {
-    const size_t smem = (size_t)kHeadWarps * 3 * dim * sizeof(float);
-    e = allow_shared<heads_bwd_kernel<T, WT>>(kHeadWarps * 3 * kHeadMaxDim * sizeof(float));
-    if (e == cudaSuccess)
-      e = launch_k(heads_bwd_kernel<T, WT>, dim3(parts), dim3(kHeadThreads), smem, s, true, a);
+      const size_t smem = (size_t)kHeadWarps * 3 * dim * sizeof(float);
+      j = {a.part, 2 * dim, {0, 0}, {parts, parts}, true, {q_dweight, k_dweight}};
+      e = allow_shared<heads_bwd_kernel<T, WT>>(kHeadWarps * 3 * kHeadMaxDim * sizeof(float));
+      if (e == cudaSuccess)
+        e = launch_k(heads_bwd_kernel<T, WT>, dim3(parts), dim3(kHeadThreads), smem, s, true, a);
     }
     if (e == cudaSuccess && sums)
-      e = launch_k(heads_join_kernel<WT>, dim3((2 * dim + 31) / 32), dim3(kHeadThreads), 0, s, true, dim, used, (const float*)a.part,
-                   static_cast<WT*>(q_dweight), static_cast<WT*>(k_dweight));
+      e = launch_k(heads_join_kernel<WT>, dim3((dim + 31) / 32, 2), dim3(kHeadThreads), 0, s, true, dim, j);
     return e;
   });
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;

@@ -65,12 +65,6 @@ __device__ __forceinline__ float reciprocal_fast(float x) {
   return y;
 }
 
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-// until at most N of the newest groups are in flight
-template <int N> __device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
-}
-
 // Flags of a segment's tokens: its first S lanes hold a byte each from when they are
 // asked for until they are needed.
 struct Flags { uint32_t starts, live; };
