@@ -1,6 +1,7 @@
 // Norms of query and key heads with the rotation of positions, and the gradient.
 #include "sequence.cuh"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace muon {
@@ -244,11 +245,11 @@ template <int G> struct Lanes {
 struct HeadWork { int blocks[2], run[2]; int wbf16; };      // run: passes
 
 // One side's weights in fp32 (1 where there are none), as the lanes of a warp need them: four at a
-// time, those of all lanes next to one another
+// time, those of all lanes next to one another; staged by one warp
 template <int E> struct HeadWeights { float4 v[E / 2][32]; };
 template <int E, typename U>
 __device__ __forceinline__ void stage_weights(HeadWeights<E>& to, const HeadSide& side, const U& un, int wbf16) {
-  if (threadIdx.x < 32 && un.any) {
+  if (un.any) {
     #pragma unroll
     for (int q = 0; q < E / 2; ++q) {
       const int at = q < E / 4 ? un.a + 4 * q : un.b + 4 * (q - E / 4);
@@ -258,10 +259,9 @@ __device__ __forceinline__ void stage_weights(HeadWeights<E>& to, const HeadSide
         w[j] = !side.weight ? 1.f
                : wbf16      ? to_f(static_cast<const __nv_bfloat16*>(side.weight)[at + j])
                             : static_cast<const float*>(side.weight)[at + j];
-      to.v[q][threadIdx.x] = make_float4(w[0], w[1], w[2], w[3]);
+      to.v[q][threadIdx.x & 31] = make_float4(w[0], w[1], w[2], w[3]);
     }
   }
-  __syncthreads();
 }
 // of the first piece or the second
 template <int E> __device__ __forceinline__ void load_weights(Piece<E>& v, const HeadWeights<E>& from, int piece) {
@@ -326,21 +326,22 @@ struct HeadWalk {
     return true;
   }
 };
-// of a lane with work, `group` of the warp's `by`; passes: of the warp's runs, all of them
-__device__ __forceinline__ HeadWalk walk_of(const Heads& a, const HeadWork& w, int key, int group, int by, bool has,
-                                            int& passes) {
-  const int64_t warps = (int64_t)w.blocks[key] * kHeadWarps, run = (int64_t)w.run[key] * by;
-  const int64_t warp = (int64_t)(blockIdx.x - (key ? w.blocks[0] : 0)) * kHeadWarps + (threadIdx.x >> 5);
+// of a lane with work, `group` of the warp's `by`, in block `block` of `blocks`; run: passes a run;
+// passes: of the warp's runs, all of them
+__device__ __forceinline__ HeadWalk walk_of(const Heads& a, const HeadWork& w, int heads, int block, int blocks, int run,
+                                            int group, int by, bool has, int& passes) {
+  const int64_t warps = (int64_t)blocks * kHeadWarps, in_run = (int64_t)run * by;
+  const int64_t warp = (int64_t)block * kHeadWarps + (threadIdx.x >> 5);
   HeadWalk k;
-  k.n = warp * run + group;
-  k.heads = a.side[key].heads;
-  k.all = has ? a.tokens * k.heads : 0;
+  k.n = warp * in_run + group;
+  k.heads = heads;
+  k.all = has ? a.tokens * heads : 0;
   k.pass = 0;
-  k.run = w.run[key];
-  k.jump = (warps - 1) * run;
+  k.run = run;
+  k.jump = (warps - 1) * in_run;
   k.find();
-  const int64_t runs = (a.tokens * k.heads + run - 1) / run;
-  passes = warp < runs ? (int)((runs - 1 - warp) / warps + 1) * k.run : 0;
+  const int64_t runs = (a.tokens * heads + in_run - 1) / in_run;
+  passes = warp < runs ? (int)((runs - 1 - warp) / warps + 1) * run : 0;
   return k;
 }
 
@@ -370,26 +371,42 @@ __device__ __forceinline__ void angles(Piece<E>& c, Piece<E>& s, const Heads& a,
 
 constexpr int kPieceDim = 512;        // widest head of these kernels
 
+// A token's queries and keys follow one another, so that a warp reads and writes about what lies
+// together.
 template <typename T, int E, int G, bool NB>
 __global__ void __launch_bounds__(kHeadThreads, 3)
 heads_piece_kernel(const __grid_constant__ Heads a, const __grid_constant__ HeadWork w) {
   using Raw = typename RawPiece<T, E>::type;
   extern __shared__ uint4 ring[];
-  __shared__ HeadWeights<E> weights;
+  __shared__ HeadWeights<E> weights[2];
   pdl_wait();
-  const int key = (int)blockIdx.x >= w.blocks[0];
-  const HeadSide& side = a.side[key];
   const Lanes<G> ln(a.dim / (2 * E));
   const Unit<E, NB> un(a.dim, a.rotary, ln.lane);
-  stage_weights(weights, side, un, w.wbf16);
+  if (threadIdx.x < 64) stage_weights(weights[threadIdx.x >> 5], a.side[threadIdx.x >> 5], un, w.wbf16);
+  __syncthreads();
   const float inv = 1.f / (float)a.dim;
   const HeadRing<Raw, 2> slots(ring);
   int passes;
-  HeadWalk in = walk_of(a, w, key, ln.group, ln.heads, un.any && ln.group < ln.heads, passes), at = in;
-  const T* const x0 = static_cast<const T*>(side.x) + un.a;
-  const T* px = x0 + in.token * side.ld + in.head * side.step;
+  const int queries = a.side[0].heads;
+  HeadWalk in = walk_of(a, w, queries + a.side[1].heads, blockIdx.x, gridDim.x, w.run[0], ln.group, ln.heads,
+                        un.any && ln.group < ln.heads, passes);
+  HeadWalk at = in;
+  const T* px;
+  T* out;
   const int to_b = un.b - un.a;
-  const int64_t step = ln.heads * side.step;
+  int64_t step;
+  bool key_in, key;
+  auto seek_in = [&] {
+    key_in = in.head >= queries;
+    const HeadSide& side = a.side[key_in];
+    px = static_cast<const T*>(side.x) + in.token * side.ld + (in.head - (key_in ? queries : 0)) * side.step + un.a;
+    step = ln.heads * side.step;
+  };
+  auto seek = [&] {
+    key = at.head >= queries;
+    const HeadSide& side = a.side[key];
+    out = static_cast<T*>(side.out) + (at.token * side.heads + at.head - (key ? queries : 0)) * a.dim + un.a;
+  };
   bool other_in = true, other = true;      // another token than in the pass before
   auto fetch = [&](int stage) {
     if (in.live()) {
@@ -397,14 +414,17 @@ heads_piece_kernel(const __grid_constant__ Heads a, const __grid_constant__ Head
       slots.copy(slots.slot(stage, 1), px + to_b);
       if (other_in && a.positions) slots.copy(slots.position(stage), a.positions + in.token);
     }
-    copies_commit();
-    px += step;
     other_in = in.next(ln.heads);
-    if (other_in) px = x0 + in.token * side.ld + in.head * side.step;
+    if (other_in || (!key_in && in.head >= queries)) seek_in();
+    else px += step;
   };
+  seek_in();
+  seek();
   #pragma unroll
-  for (int d = 0; d < kHeadRing; ++d) fetch(d);
-  T* out = static_cast<T*>(side.out) + at.n * a.dim + un.a;
+  for (int d = 0; d < kHeadRing; ++d) {
+    if (d < passes) fetch(d);
+    copies_commit();
+  }
   Piece<E> c, s;
   int64_t pos = -1;
   int stage = 0;
@@ -423,7 +443,8 @@ heads_piece_kernel(const __grid_constant__ Heads a, const __grid_constant__ Head
       widen(x, *slots.slot(stage, 0));
       widen(y, *slots.slot(stage, 1));
     }
-    fetch(stage);
+    if (i + kHeadRing < passes) fetch(stage);
+    copies_commit();
     stage = stage + 1 == kHeadRing ? 0 : stage + 1;
     float2 sq = both(0.f);
     #pragma unroll
@@ -433,10 +454,10 @@ heads_piece_kernel(const __grid_constant__ Heads a, const __grid_constant__ Head
       Raw ra = Raw{}, rb = Raw{};
       if (pos >= 0) {
         Piece<E> wx;
-        load_weights(wx, weights, 0);
+        load_weights(wx, weights[key], 0);
         #pragma unroll
         for (int j = 0; j < E / 2; ++j) x.v[j] = mul2(mul2(x.v[j], both(rstd)), wx.v[j]);
-        load_weights(wx, weights, 1);
+        load_weights(wx, weights[key], 1);
         #pragma unroll
         for (int j = 0; j < E / 2; ++j) y.v[j] = mul2(mul2(y.v[j], both(rstd)), wx.v[j]);
         turn<E, NB>(x, y, c, s);
@@ -446,9 +467,9 @@ heads_piece_kernel(const __grid_constant__ Heads a, const __grid_constant__ Head
       *reinterpret_cast<Raw*>(out) = ra;
       *reinterpret_cast<Raw*>(out + to_b) = rb;
     }
-    const int64_t before = at.n;
     other = at.next(ln.heads);
-    out += (at.n - before) * a.dim;
+    if (other || (!key && at.head >= queries)) seek();
+    else out += ln.heads * a.dim;
   }
 }
 
@@ -464,11 +485,14 @@ heads_piece_bwd_kernel(const __grid_constant__ Heads a, const __grid_constant__ 
   const HeadSide& side = a.side[key];
   const Lanes<G> ln(a.dim / (2 * E));
   const Unit<E, NB> un(a.dim, a.rotary, ln.lane);
-  stage_weights(weights, side, un, w.wbf16);
+  if (warp == 0) stage_weights(weights, side, un, w.wbf16);
+  __syncthreads();
   const float inv = 1.f / (float)a.dim;
   const HeadRing<Raw, 4> slots(ring);
   int passes;
-  HeadWalk in = walk_of(a, w, key, ln.group, ln.heads, un.any && ln.group < ln.heads, passes), at = in;
+  HeadWalk in = walk_of(a, w, side.heads, (int)blockIdx.x - (key ? w.blocks[0] : 0), w.blocks[key], w.run[key],
+                        ln.group, ln.heads, un.any && ln.group < ln.heads, passes);
+  HeadWalk at = in;
   const T* const x0 = static_cast<const T*>(side.x) + un.a;
   const T* const d0 = static_cast<const T*>(side.dy) + un.a;
   const T* px = x0 + in.token * side.ld + in.head * side.step;
@@ -484,7 +508,6 @@ heads_piece_bwd_kernel(const __grid_constant__ Heads a, const __grid_constant__ 
       slots.copy(slots.slot(stage, 3), pd + to_b);
       if (other_in && a.positions) slots.copy(slots.position(stage), a.positions + in.token);
     }
-    copies_commit();
     px += step;
     pd += step_d;
     other_in = in.next(ln.heads);
@@ -494,7 +517,10 @@ heads_piece_bwd_kernel(const __grid_constant__ Heads a, const __grid_constant__ 
     }
   };
   #pragma unroll
-  for (int d = 0; d < kHeadRing; ++d) fetch(d);
+  for (int d = 0; d < kHeadRing; ++d) {
+    if (d < passes) fetch(d);
+    copies_commit();
+  }
   T* out = static_cast<T*>(side.out) + at.n * a.dim + un.a;
   Piece<E> sa, sb, c, s;
   clear(sa);
@@ -525,7 +551,8 @@ heads_piece_bwd_kernel(const __grid_constant__ Heads a, const __grid_constant__ 
         turn<E, NB>(g, h, c, s);
       }
     }
-    fetch(stage);
+    if (i + kHeadRing < passes) fetch(stage);
+    copies_commit();
     stage = stage + 1 == kHeadRing ? 0 : stage + 1;
     float2 sq = both(0.f), dot = both(0.f);
     #pragma unroll
@@ -672,24 +699,22 @@ template <typename T, typename F> bool by_units(const Heads& a, F f) {
   return false;
 }
 
-// Blocks for the two sides out of `most`, by their heads; B heads a pass of a warp.  A run is
-// a token's heads, or what a warp has at all.
+// Blocks and a run for `n` heads, of which a token has `of_token`; B heads a pass of a warp.  A run
+// is a token's heads, or what a warp has at all.
+void share_out(int64_t n, int of_token, int B, int most, int& blocks, int& run) {
+  const int64_t passes = (n + B - 1) / B;
+  const int64_t of_warp = (passes + (int64_t)most * kHeadWarps - 1) / ((int64_t)most * kHeadWarps);
+  run = (int)std::min<int64_t>((of_token + B - 1) / B, of_warp);
+  blocks = (int)std::min<int64_t>((passes + (int64_t)run * kHeadWarps - 1) / ((int64_t)run * kHeadWarps), most);
+}
+// out of `most` blocks
 HeadWork work_of(const Heads& a, int B, int most, int wbf16) {
   HeadWork w = {{0, 0}, {1, 1}, wbf16};
-  const int64_t q = a.tokens * a.side[0].heads, k = a.tokens * a.side[1].heads;
-  for (int i = 0; i < 2; ++i) {
-    const int64_t n = i ? k : q;
-    if (!n) continue;
-    const int64_t passes = (n + B - 1) / B;
-    int64_t blocks = i ? most - w.blocks[0] : (int64_t)((double)most * q / (q + k) + 0.5);
-    if (i == 0 && k && blocks > most - 1) blocks = most - 1;
-    if (blocks < 1) blocks = 1;
-    const int64_t of_warp = (passes + blocks * kHeadWarps - 1) / (blocks * kHeadWarps);
-    const int64_t of_token = (a.side[i].heads + B - 1) / B;
-    w.run[i] = (int)(of_token < of_warp ? of_token : of_warp);
-    const int64_t need = (passes + (int64_t)w.run[i] * kHeadWarps - 1) / ((int64_t)w.run[i] * kHeadWarps);
-    w.blocks[i] = (int)(need < blocks ? need : blocks);
-  }
+  const int q = a.side[0].heads, k = a.side[1].heads;
+  int for_q = (int)((double)most * q / (q + k) + 0.5);
+  if (k && for_q > most - 1) for_q = most - 1;
+  if (q) share_out(a.tokens * q, q, B, for_q < 1 ? 1 : for_q, w.blocks[0], w.run[0]);
+  if (k) share_out(a.tokens * k, k, B, most - w.blocks[0], w.blocks[1], w.run[1]);
   return w;
 }
 
@@ -732,9 +757,10 @@ extern "C" muon_status muon_norm_rotate_heads(
     if (by_units<T>(a, [&](auto pe, auto pg, int B) {
           constexpr int E = decltype(pe)::value, G = decltype(pg)::value;
           constexpr size_t smem = HeadRing<typename RawPiece<T, E>::type, 2>::kBytes;
-          const HeadWork hw = work_of(a, B, 152 * 3, wdtype == MUON_BF16);
+          HeadWork hw = {{0, 0}, {1, 1}, wdtype == MUON_BF16};
+          share_out(tokens * (q_heads + k_heads), q_heads + k_heads, B, 152 * 3, hw.blocks[0], hw.run[0]);
           e = launch_k(neighbours ? heads_piece_kernel<T, E, G, true> : heads_piece_kernel<T, E, G, false>,
-                       dim3(hw.blocks[0] + hw.blocks[1]), dim3(kHeadThreads), smem, s, true, a, hw);
+                       dim3(hw.blocks[0]), dim3(kHeadThreads), smem, s, true, a, hw);
         }))
       return e;
     return launch_k(heads_kernel<decltype(t), decltype(w)>, dim3((unsigned)(want < 152 * 8 ? want : 152 * 8)),
