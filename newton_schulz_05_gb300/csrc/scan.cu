@@ -1,8 +1,6 @@
 // Gated linear recurrence: the forward pass.
 #include "scan.cuh"
 
-#include <algorithm>
-
 namespace muon {
 
 namespace {
@@ -248,8 +246,8 @@ cudaError_t scan_with(const Scan& a, int64_t strips, cudaStream_t s) {
 // Blocks of 8 warps, two an SM, or of 4 where there are strips for more than two an SM;
 // clusters where there are few strips, although a round of joins through a cluster takes
 // about 1.3 us more: MEASURED
-template <typename T, bool VEC, bool RING> cudaError_t scan_by_size(const Scan& a, int64_t strips, cudaStream_t s) {
-  constexpr int S = sizeof(T) == 2 ? 8 : 4, D = RING ? 2 : 0;
+template <typename T, bool VEC> cudaError_t scan_by_size(const Scan& a, int64_t strips, cudaStream_t s) {
+  constexpr int S = sizeof(T) == 2 ? 8 : 4, D = 2;
   if (a.length <= 4 || (a.length <= 32 && strips >= 2048)) return scan_short<T, VEC>(a, strips, s);
   if (a.length <= 2 * S) return scan_with<T, 1, S, 1, 0, VEC>(a, strips, s);
   if (a.length <= 8 * S || strips > 304) return scan_with<T, 4, S, 1, D, VEC>(a, strips, s);
@@ -281,12 +279,10 @@ extern "C" muon_status muon_gated_scan(int64_t batch, int64_t length, int64_t di
   const int strips = (int)((dim + kStrip - 1) / kStrip);
   const Scan a = {length, dim, ldg, ldx, strips, mix ? 1.f : 0.f, gate, x, state, starts, token_mask, h, last};
   const int64_t rows = batch * length, units = batch * strips;
-  const int how = std::max(lie(gate, rows, ldg, es), lie(x, rows, ldx, es));
-  const bool vec = how == kFours && dim % 4 == 0 && !off(h, 4 * es);
+  const bool vec = dim % 4 == 0 && fours(gate, rows, ldg, es) && fours(x, rows, ldx, es) && !off(h, 4 * es);
   const cudaError_t e = by_type(dtype, [&](auto t) {
     using T = decltype(t);
-    return vec ? scan_by_size<T, true, true>(a, units, s)
-               : how != kAnyhow ? scan_by_size<T, false, true>(a, units, s) : scan_by_size<T, false, false>(a, units, s);
+    return vec ? scan_by_size<T, true>(a, units, s) : scan_by_size<T, false>(a, units, s);
   });
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }

@@ -161,7 +161,8 @@ template <bool VEC> struct Channels {
 // Rows of N operands on their way through shared memory: D chunks, S tokens a segment, 2 W
 // segments.  A row of a strip is copied by the half warp that reads it, in aligned pieces of
 // four channels; where rows are not made of those, its first piece may begin up to three
-// elements ahead (inside the tensor, whose first row is aligned) and there is one more.
+// elements ahead of the row and there is one more.  Only pieces that hold an element of the
+// row are read: an aligned 8 or 16 bytes lie wholly in the allocation that one of them does.
 template <typename T, bool VEC, int N, int S, int W> struct Ring {
   static constexpr int kRow = VEC ? 16 : 17;
   static constexpr size_t kStage = sizeof(Raw4<T>) * N * S * 2 * W * kRow;
@@ -388,10 +389,9 @@ inline muon_status check_scan(int64_t batch, int64_t length, int64_t dim, int dt
   return known(dtype) ? MUON_OK : MUON_ERR_DTYPE;
 }
 
-// How rows lie: in aligned pieces of four channels; from an aligned first row on; or neither
-enum { kFours, kFromAligned, kAnyhow };
-inline int lie(const void* p, int64_t rows, int64_t ld, size_t es) {
-  return off(p, 4 * es) ? kAnyhow : rows <= 1 || ld % 4 == 0 ? kFours : kFromAligned;
+// whether rows of `p` are made of aligned pieces of four
+inline bool fours(const void* p, int64_t rows, int64_t ld, size_t es) {
+  return !off(p, 4 * es) && (rows <= 1 || ld % 4 == 0);
 }
 
 }  // namespace

@@ -2,8 +2,6 @@
 // first, over what reaches the state behind each token, c -> a (dh + c).
 #include "scan.cuh"
 
-#include <algorithm>
-
 namespace muon {
 
 namespace {
@@ -289,8 +287,8 @@ cudaError_t scan_bwd_with(const ScanBwd& a, int64_t strips, cudaStream_t s) {
   return launch_cluster(plain, strips * CL, CL, 32 * W, smem, s, a);
 }
 
-template <typename T, bool VEC, bool RING> cudaError_t scan_bwd_by_size(const ScanBwd& a, int64_t strips, cudaStream_t s) {
-  constexpr int S = sizeof(T) == 2 ? 4 : 2, D = RING ? 2 : 0;
+template <typename T, bool VEC> cudaError_t scan_bwd_by_size(const ScanBwd& a, int64_t strips, cudaStream_t s) {
+  constexpr int S = sizeof(T) == 2 ? 4 : 2, D = 2;
   if (a.length <= 4 || (a.length <= 32 && strips >= 2048)) return scan_short_bwd<T, VEC>(a, strips, s);
   if (a.length <= 2 * S) return scan_bwd_with<T, 1, S, 1, 0, VEC>(a, strips, s);
   if (a.length <= 8 * S || strips > 304) return scan_bwd_with<T, 4, S, 1, D, VEC>(a, strips, s);
@@ -326,14 +324,12 @@ extern "C" muon_status muon_gated_scan_backward(
   const ScanBwd a = {length, dim, lddh, ldg, ldx, ldh, strips, mix ? 1.f : 0.f, dh, gate, x, h, state, dlast, starts,
                      token_mask, dgate, dx, dstate};
   const int64_t rows = batch * length, units = batch * strips;
-  const int how = std::max({lie(dh, rows, lddh, es), lie(gate, rows, ldg, es), lie(h, rows, ldh, es),
-                            mix ? lie(x, rows, ldx, es) : (int)kFours});
-  const bool vec = how == kFours && dim % 4 == 0 && !off(dgate, 4 * es) && !off(dx, 4 * es);
+  const bool vec = dim % 4 == 0 && fours(dh, rows, lddh, es) && fours(gate, rows, ldg, es) &&
+                   (!mix || fours(x, rows, ldx, es)) && fours(h, rows, ldh, es) && !off(dgate, 4 * es) &&
+                   !off(dx, 4 * es);
   const cudaError_t e = by_type(dtype, [&](auto t) {
     using T = decltype(t);
-    return vec ? scan_bwd_by_size<T, true, true>(a, units, s)
-               : how != kAnyhow ? scan_bwd_by_size<T, false, true>(a, units, s)
-                                : scan_bwd_by_size<T, false, false>(a, units, s);
+    return vec ? scan_bwd_by_size<T, true>(a, units, s) : scan_bwd_by_size<T, false>(a, units, s);
   });
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }

@@ -96,6 +96,28 @@ def test_flags_and_strides(layers, b, t, d, layout, starts, masked, dtype):
     check(layers, v, n, False, dtype)
 
 
+# one case for each way the length is cut up: blocks of one, four and eight warps, clusters of
+# four and eight, few and many chunks
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("layout,extra", [("dense", 0), ("columns", 0), ("odd", 1), ("dense", 3)])
+@pytest.mark.parametrize("b,t,d", [(2, 9, 64), (3, 15, 128), (3, 50, 192), (310, 37, 64), (20, 70, 1024),
+                                   (9, 300, 960), (70, 200, 64), (3, 700, 64), (1, 2100, 128)])
+def test_flags_however_the_length_is_cut(layers, b, t, d, layout, extra, dtype):
+    v, n = inputs(b, t, d + extra, dtype, seed=13, starts=0.05, masked=True, layout=layout)
+    check(layers, v, n, (b + t) % 2 == 0, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_halves_of_one_projection(layers, dtype):
+    # gate and x side by side, an odd width each: rows and their first elements nowhere aligned
+    for b, t, d in ((2, 900, 177), (1, 40, 33), (150, 60, 65)):
+        gen = torch.Generator(device="cuda").manual_seed(d)
+        n = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+        both = n(b, t, 2 * d).to(dtype)
+        v = dict(gate=both[..., :d], x=both[..., d:], state=None, starts=None, token_mask=None)
+        check(layers, v, n, True, dtype)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_saturated_gates(layers, dtype):
     # gates of exactly 0 and 1, and far beyond where their exponentials over- or underflow
