@@ -21,6 +21,8 @@
 
 #include "sequence.cuh"
 
+#include <type_traits>
+
 namespace muon {
 
 namespace {
@@ -48,6 +50,30 @@ __device__ __forceinline__ Quad widen(const Raw4<float>& r) {
   return {{make_float2(__uint_as_float(r.u.x), __uint_as_float(r.u.y)),
            make_float2(__uint_as_float(r.u.z), __uint_as_float(r.u.w))}};
 }
+// what m (all ones or none) has of the bits
+__device__ __forceinline__ float masked(float v, uint32_t m) { return __uint_as_float(__float_as_uint(v) & m); }
+__device__ __forceinline__ Quad masked(const Quad& q, uint32_t m) {
+  return {{make_float2(masked(q.v[0].x, m), masked(q.v[0].y, m)),
+           make_float2(masked(q.v[1].x, m), masked(q.v[1].y, m))}};
+}
+__device__ __forceinline__ Raw4<__nv_bfloat16> masked(const Raw4<__nv_bfloat16>& r, uint32_t m) {
+  return {make_uint2(r.u.x & m, r.u.y & m)};
+}
+__device__ __forceinline__ Raw4<float> masked(const Raw4<float>& r, uint32_t m) {
+  return {make_uint4(r.u.x & m, r.u.y & m, r.u.z & m, r.u.w & m)};
+}
+// a gate, or the infinite one
+__device__ __forceinline__ Raw4<__nv_bfloat16> gate_or(const Raw4<__nv_bfloat16>& r, uint32_t m) {
+  const uint32_t n = 0x7f807f80u & ~m;
+  return {make_uint2((r.u.x & m) | n, (r.u.y & m) | n)};
+}
+__device__ __forceinline__ Raw4<float> gate_or(const Raw4<float>& r, uint32_t m) {
+  const uint32_t n = 0x7f800000u & ~m;
+  return {make_uint4((r.u.x & m) | n, (r.u.y & m) | n, (r.u.z & m) | n, (r.u.w & m) | n)};
+}
+// all ones where bit i is set
+__device__ __forceinline__ uint32_t ones(uint32_t bits, int i) { return (uint32_t)((int)(bits << (31 - i)) >> 31); }
+
 __device__ __forceinline__ Quad quad(float v) { return {{both(v), both(v)}}; }
 __device__ __forceinline__ Quad add(const Quad& a, const Quad& b) {
   return {{add2(a.v[0], b.v[0]), add2(a.v[1], b.v[1])}};
@@ -71,6 +97,7 @@ struct Flags { uint32_t starts, live; };
 template <int S>
 __device__ __forceinline__ Flags ask(const uint8_t* starts, const uint8_t* mask, int64_t row0, int64_t t0,
                                      int64_t length) {
+  static_assert(S <= 16, "a lane a token");
   const int l = threadIdx.x & 15;
   const int64_t t = t0 + l;
   const bool in = l < S && t >= 0 && t < length;
@@ -259,6 +286,11 @@ __device__ __forceinline__ Run run_of(const Segment& g) {
   return r;
 }
 
+// Blocks an SM: two of eight warps, or one where a thread has more tokens and needs the
+// registers of two
+template <typename T, int W, int OPERANDS, int S> constexpr int kScanBlocks =
+    W < 8 ? 16 / W : S * (int)sizeof(T) * OPERANDS > 32 ? 1 : 2;
+
 // what the runs of a block's warps, and of a cluster's blocks, are exchanged through
 struct RunSlot { float4 m[16], k[16], H[16]; };
 template <int W, int CL> struct RunSlots {
@@ -387,6 +419,35 @@ inline muon_status check_scan(int64_t batch, int64_t length, int64_t dim, int dt
       batch * dim >= (int64_t)1 << 33 || batch * ((dim + kStrip - 1) / kStrip) >= (int64_t)1 << 27)
     return MUON_ERR_UNSUPPORTED_SHAPE;
   return known(dtype) ? MUON_OK : MUON_ERR_DTYPE;
+}
+
+// How the length is cut up: f(warps a block, S's multiple, blocks a cluster, chunks in flight)
+// as integral constants.  A chunk of a block is 2 W S tokens.
+//   Few strips take blocks with twice the tokens a thread, one an SM, in clusters that fill
+// the SMs between them; a round of joins through a cluster takes 1 us more, so it is worth it
+// where it saves rounds only.  bf16, forward and gradient in us, with clusters of 8, 4, 2 and
+// without, then two blocks an SM in clusters of 8, 4 and without:
+//   [1, 65536, 64] 101, 181, 347 | 140: 210, 365, 698 | 328     8 from 1 strip on
+//   [1, 32768, 2048] 162, 103, 185 | 111: 328, 199, 372 | 236   4 from 20 strips on
+//   [2, 16384, 2048] 144, 106, 100 | 100: 283, 201, 197 | 210   2 from 39 strips on
+//   [1, 16000, 5120] -, -, 196, 140 | 158: 385, 285 | 340       none from 77 strips on
+//   [200, 4096, 64] -, -, 81, 74 | 79, 68: 154, 145 | 163, 136  two an SM from 153 strips on
+// In fp32 39 to 76 strips are the exception: clusters of four with two blocks an SM took 158
+// us for [2, 16384, 2048] where clusters of two took 178, and the gradient 318 and 354.
+// Smaller blocks with less to join from 305 strips on: [16, 1024, 4096] bf16 65 and 71 us,
+// gradient 133 and 136 ([16, 2048, 2048] fp32 154 and 137, 312 and 293, where the strips are
+// 1.7 times as many as the larger blocks' places), and for lengths of one chunk.
+template <int V> using Int = std::integral_constant<int, V>;
+template <typename T, int S, typename F> cudaError_t scan_layout(int64_t length, int64_t strips, F f) {
+  if (length <= 2 * S) return f(Int<1>(), Int<1>(), Int<1>(), Int<0>());
+  if (length <= 8 * S || strips > 304) return f(Int<4>(), Int<1>(), Int<1>(), Int<2>());
+  if (length <= 16 * S || strips > 152) return f(Int<8>(), Int<1>(), Int<1>(), Int<2>());
+  if (length <= 32 * S || strips > 76) return f(Int<8>(), Int<2>(), Int<1>(), Int<2>());
+  if constexpr (sizeof(T) == 4)
+    if (strips > 38) return f(Int<8>(), Int<1>(), Int<4>(), Int<2>());
+  if (length <= 64 * S || strips > 38) return f(Int<8>(), Int<2>(), Int<2>(), Int<2>());
+  if (length <= 128 * S || strips > 19) return f(Int<8>(), Int<2>(), Int<4>(), Int<2>());
+  return f(Int<8>(), Int<2>(), Int<8>(), Int<2>());
 }
 
 // whether rows of `p` are made of aligned pieces of four
