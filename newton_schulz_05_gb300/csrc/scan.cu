@@ -119,7 +119,7 @@ scan_kernel(const __grid_constant__ Scan a) {
     }
     Quad P[S], H[S];
     Segment run = {quad(1.f), quad(0.f), quad(0.f), false};
-    const Flags now = FLAGS ? bits(ahead[0]) : Flags{0, 0};
+    const Flags now = FLAGS ? bits<S>(ahead[0]) : Flags{0, 0, true};
     #pragma unroll
     for (int i = 0; i < S; ++i) {
       Raw4<T> gi, vi;
@@ -130,13 +130,13 @@ scan_kernel(const __grid_constant__ Scan a) {
         gi = rg[i];
         vi = rx[i];
       }
-      if (FLAGS) {
+      if (FLAGS && !now.quiet) {
         const uint32_t live = ones(now.live, i);
         gi = gate_or(gi, live);
         vi = masked(vi, live);
       }
       const Step st = step_of(widen(gi), widen(vi), a.mix);
-      if (FLAGS) {
+      if (FLAGS && !now.quiet) {
         const uint32_t on = ~ones(now.starts, i);
         run.P = masked(run.P, on);
         run.H = masked(run.H, on);
@@ -162,7 +162,7 @@ scan_kernel(const __grid_constant__ Scan a) {
     });
     const int n = ch.any() ? left : 0;
     auto finish = [&](int i) {
-      if (FLAGS) front = masked(front, ~ones(now.starts, i));
+      if (FLAGS && !now.quiet) front = masked(front, ~ones(now.starts, i));
       return fma(P[i], front, H[i]);
     };
     if (n >= S) {

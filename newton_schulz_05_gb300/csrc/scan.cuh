@@ -93,7 +93,7 @@ __device__ __forceinline__ float reciprocal_fast(float x) {
 
 // Flags of a segment's tokens: its first S lanes hold a byte each from when they are
 // asked for until they are needed.
-struct Flags { uint32_t starts, live; };
+struct Flags { uint32_t starts, live; bool quiet; };     // quiet: of the bits, none does anything in the warp
 template <int S>
 __device__ __forceinline__ Flags ask(const uint8_t* starts, const uint8_t* mask, int64_t row0, int64_t t0,
                                      int64_t length) {
@@ -101,13 +101,14 @@ __device__ __forceinline__ Flags ask(const uint8_t* starts, const uint8_t* mask,
   const int l = threadIdx.x & 15;
   const int64_t t = t0 + l;
   const bool in = l < S && t >= 0 && t < length;
-  return {in && starts ? starts[row0 + t] : 0u, in && mask ? mask[row0 + t] : (uint32_t)in};
+  return {in && starts ? starts[row0 + t] : 0u, in && mask ? mask[row0 + t] : (uint32_t)in, false};
 }
 // as bits by token: which are live, and which of those start over
-__device__ __forceinline__ Flags bits(const Flags& f) {
+template <int S> __device__ __forceinline__ Flags bits(const Flags& f) {
   const int half = threadIdx.x & 16;
-  const uint32_t live = __ballot_sync(~0u, f.live != 0) >> half & 0xffff;
-  return {__ballot_sync(~0u, f.starts != 0) >> half & live, live};
+  const uint32_t live = __ballot_sync(~0u, f.live != 0), starts = __ballot_sync(~0u, f.starts != 0) & live;
+  constexpr uint32_t whole = (S < 16 ? (1u << S) - 1 : 0xffffu) * 0x10001u;
+  return {starts >> half & 0xffff, live >> half & 0xffff, live == whole && starts == 0};
 }
 
 // Which channels a lane has: `has` of its four are inside the row.  VEC: four

@@ -139,7 +139,7 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
     }
     Quad keep[S], take[S], d[S], v[S];
     Segment run = {quad(1.f), quad(0.f), quad(0.f), false};
-    const Flags now = FLAGS ? bits(ahead[0]) : Flags{0, 0};
+    const Flags now = FLAGS ? bits<S>(ahead[0]) : Flags{0, 0, true};
     #pragma unroll
     for (int i = S - 1; i >= 0; --i) {
       Raw4<T> di, gi, xi, hi;
@@ -154,12 +154,12 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
         xi = rx[i];
         hi = rh[i];
       }
-      if (FLAGS) gi = gate_or(gi, ones(now.live, i));
+      if (FLAGS && !now.quiet) gi = gate_or(gi, ones(now.live, i));
       shares_of(widen(gi), keep[i], take[i]);
       d[i] = widen(di);
       v[i] = widen(hi);
       if (i == 0 && t0 == 0 && a.state && ch.any()) v[0] = ch.state(a.state + b * a.dim + ch.first);
-      if (FLAGS) {
+      if (FLAGS && !now.quiet) {
         v[i] = masked(v[i], ~ones(now.starts, i));
         xi = masked(xi, ones(now.live, i));
       }
@@ -167,7 +167,7 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
       run.P = mul(run.P, keep[i]);
       run.Q = fma(keep[i], run.Q, take[i]);
       run.H = mul(keep[i], add(run.H, d[i]));
-      if (FLAGS) {
+      if (FLAGS && !now.quiet) {
         const uint32_t on = ~ones(now.starts, i);
         run.P = masked(run.P, on);
         run.H = masked(run.H, on);
@@ -199,14 +199,14 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
       const Quad l = add(d[i], c), u = mul(take[i], l);
       c = mul(keep[i], l);
       Quad gx = mix ? u : l, gg = mul(mul(u, keep[i]), v[i]);
-      if (FLAGS) {
+      if (FLAGS && !now.quiet) {
         const uint32_t live = ones(now.live, i);
         gx = masked(gx, live);
         gg = masked(gg, live);
       }
       if (whole || (i < n && a.dx)) ch.store(dx + i * a.dim, gx);
       if (whole || (i < n && a.dgate)) ch.store(dg + i * a.dim, gg);
-      if (FLAGS) c = masked(c, ~ones(now.starts, i));
+      if (FLAGS && !now.quiet) c = masked(c, ~ones(now.starts, i));
     }
     t0 -= stride;
   }
