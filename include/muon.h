@@ -544,7 +544,7 @@ MUON_API muon_status muon_route_backward(int64_t tokens, int experts, int k, int
  * The state is held in fp32; h is that rounded.  Gate, x and states are finite;
  * what a sequence's state is after a value that is not, up to the next start,
  * is not defined (other sequences and channels are not affected).
- *   0 <= batch, length < 2^31, dim in [1, 2^20], batch * dim < 2^33
+ *   0 <= batch, length < 2^31, dim in [1, 2^20], batch * ceil(dim / 64) < 2^27
  *   gate, x      [batch * length, dim] of dtype, rows ldg and ldx apart
  *   state        [batch, dim] fp32: the state before the first token; null: 0
  *   starts       [batch, length] bytes, or null: no token starts over
@@ -676,7 +676,8 @@ MUON_API muon_status muon_token_log_probs_backward(int64_t tokens, int64_t vocab
  *   decided on the exact difference
  *   w = 1 / tokens (all that count), or with by_sequence != 0
  *   w = 1 / (sequences that have a token * tokens of the sequence)
- * Masked tokens have no effect, whatever they hold.  No token at all: all 0.
+ * Masked tokens have no effect, whatever they hold, nor has ref where kl_weight is 0,
+ * but on kl.  No token at all: all 0.
  *   0 <= batch, length < 2^31, batch * length < 2^40, 0 <= clip_low < 1,
  *   0 <= clip_high, both and kl_weight finite
  *   log_probs, old, ref  fp32 rows of `length`, ldl, ldo and ldr apart; ref may be

@@ -64,10 +64,11 @@ __device__ __forceinline__ Token token_of(const Policy& a, float lp, float old, 
   const float r = expf(d);
   if (GRAD) {
     k.slope = k.cut ? 0.f : -r * adv;
-    if (a.ref) k.slope = fmaf(-a.kl_weight, excess(ref - lp) + (ref - lp), k.slope);
+    if (a.ref && a.kl_weight != 0.f) k.slope = fmaf(-a.kl_weight, excess(ref - lp) + (ref - lp), k.slope);
   } else {
     k.kl = a.ref ? excess(ref - lp) : 0.f;
-    k.each = fmaf(k.cut ? (up ? -a.most : -a.least) : -r, adv, a.kl_weight * k.kl);
+    // without a weight not even an infinite k counts
+    k.each = fmaf(k.cut ? (up ? -a.most : -a.least) : -r, adv, a.kl_weight != 0.f ? a.kl_weight * k.kl : 0.f);
   }
   return k;
 }

@@ -62,7 +62,7 @@ scan_kernel(const __grid_constant__ Scan a) {
   uint32_t fg = VEC ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(gate + seg * S * a.ldg) / sizeof(T));
   uint32_t fx = VEC ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(x + seg * S * a.ldx) / sizeof(T));
   Flags ahead[D > 0 ? D : 1];
-  auto ask_next = [&] { return ask<S>(a.starts, a.mask, row0, length - left_in, length); };
+  auto ask_next = [&] { return ask<S>(a.starts, a.mask, row0, a.length - left_in, length); };
   auto advance = [&] {
     gate += stride * a.ldg;
     x += stride * a.ldx;

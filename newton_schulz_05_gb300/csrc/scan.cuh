@@ -417,7 +417,7 @@ __device__ __forceinline__ Quad join_segments(RunSlots<W, CL>& sh, const Segment
 inline muon_status check_scan(int64_t batch, int64_t length, int64_t dim, int dtype) {
   if (batch < 0 || length < 0) return MUON_ERR_INVALID_ARG;
   if (dim < 1 || dim > 1 << 20 || batch >= (int64_t)1 << 31 || length >= (int64_t)1 << 31 ||
-      batch * dim >= (int64_t)1 << 33 || batch * ((dim + kStrip - 1) / kStrip) >= (int64_t)1 << 27)
+      batch * ((dim + kStrip - 1) / kStrip) >= (int64_t)1 << 27)
     return MUON_ERR_UNSUPPORTED_SHAPE;
   return known(dtype) ? MUON_OK : MUON_ERR_DTYPE;
 }

@@ -405,7 +405,8 @@ class _GatedScan(torch.autograd.Function):
                                 state=state, dstate=None if dstate is None else dstate.contiguous(),
                                 starts=starts, token_mask=token_mask, mix=ctx.mix, need_gate=need[0],
                                 need_x=need[1], need_state=need[2])
-        return g.dgate, g.dx, g.dstate, None, None, None
+        ds = None if g.dstate is None else g.dstate.view(state.shape)      # batch in one dimension or several
+        return g.dgate, g.dx, ds, None, None, None
 
 
 def gated_scan(gate, x, *, state=None, starts=None, token_mask=None, mix: bool = True) -> ScanOut:

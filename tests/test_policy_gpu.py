@@ -127,6 +127,17 @@ def test_what_is_not_finite(layers):
     assert bool(g[1, 3].isnan()) and int(g.isnan().sum()) == 1
 
 
+def test_a_reference_without_weight_counts_for_nothing(layers):
+    v = inputs(3, 40, masked=False)
+    v["r"][1, 5] = float("-inf")
+    how = dict(kl=0.0)
+    a = layers.policy_loss_forward(v["lp"], v["old"], v["adv"], ref_log_probs=v["r"], **how)
+    b = layers.policy_loss_forward(v["lp"], v["old"], v["adv"], **how)
+    assert a.loss == b.loss and a.clipped == b.clipped and bool(a.kl.isinf())
+    g = layers.policy_loss_backward(v["lp"], v["old"], v["adv"], a.weights, ref_log_probs=v["r"], **how)
+    assert torch.equal(g, layers.policy_loss_backward(v["lp"], v["old"], v["adv"], b.weights, **how))
+
+
 def test_gradient_in_place_through_the_c_abi(layers):
     lib = muon().load()
     v = inputs(3, 700, masked=False)
@@ -155,7 +166,7 @@ def test_differentiable_and_shapes(layers):
     # rows that are not rows: transposed
     a = layers.policy_loss(lp.t(), v["old"].t(), v["adv"][:, None].expand(6, 40).t(), token_mask=v["mask"].t())
     b = layers.policy_loss(lp, v["old"], v["adv"], token_mask=v["mask"])
-    assert abs(float(a.loss) - float(b.loss)) < 1e-6
+    assert abs(float(a.loss.detach()) - float(b.loss.detach())) < 1e-6
     one = layers.policy_loss_forward(lp[0].detach(), v["old"][0], v["adv"][0], token_mask=v["mask"][0])
     assert one.weights.shape == ()
     f = layers.policy_loss_forward

@@ -203,6 +203,9 @@ def test_more_leading_dimensions_and_shapes_refused(layers):
     assert o.state.shape == s.shape and torch.equal(o.h.view(6, 5, 8), p.h) and torch.equal(o.state.view(6, 8), p.state)
     one = layers.gated_scan_forward(gate[0, 0], x[0, 0])
     assert one.h.shape == (5, 8) and one.state.shape == (8,)
+    flat = s.view(6, 8).clone().requires_grad_()        # the batch in one dimension
+    (g,) = torch.autograd.grad(layers.gated_scan(gate, x, state=flat).h.sum(), flat)
+    assert g.shape == (6, 8) and bool((g > 0).all())
     for bad in (dict(state=s.view(3, 2, 8)), dict(state=s.transpose(0, 1)), dict(state=s.view(-1)),
                 dict(starts=torch.zeros(5, 6, dtype=torch.bool, device="cuda")),
                 dict(token_mask=torch.zeros(2, 5, 3, dtype=torch.bool, device="cuda"))):
