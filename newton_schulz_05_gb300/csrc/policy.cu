@@ -131,6 +131,9 @@ __device__ __forceinline__ void add(Sum& s, float x) {
   s.hi = t;
 }
 
+// (what is left out of an infinite sum is NaN)
+__device__ __forceinline__ float value(const Sum& s) { return isfinite(s.hi) ? s.hi + s.lo : s.hi; }
+
 // What a thread, a warp and in the end all know of the sequences: tokens, sequences that have
 // one, and the sums of each, of k and of clipped tokens (by_sequence: of their means)
 struct alignas(16) Total {
@@ -210,10 +213,10 @@ __device__ __forceinline__ void join_units(const float4* __restrict__ part, int6
     t.filled += n > 0;
     const float w = by_sequence ? 1.f / (float)(n ? n : 1) : 1.f;
     #pragma unroll
-    for (int i = 0; i < 3; ++i) add(s[i], w * (v[i].hi + v[i].lo));
+    for (int i = 0; i < 3; ++i) add(s[i], w * value(v[i]));
   }
   #pragma unroll
-  for (int i = 0; i < 3; ++i) t.sum[i] = s[i].hi + s[i].lo;
+  for (int i = 0; i < 3; ++i) t.sum[i] = value(s[i]);
   add_all<CL>(t, all);
   const unsigned long long over = by_sequence ? t.filled : t.tokens;
   const float share = 1.f / (float)(over ? over : 1);

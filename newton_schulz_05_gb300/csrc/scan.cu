@@ -1,6 +1,8 @@
 // Gated linear recurrence: the forward pass.
 #include "scan.cuh"
 
+#include <algorithm>
+
 namespace muon {
 
 namespace {
@@ -34,7 +36,7 @@ __device__ __forceinline__ Step step_of(const Quad& g, const Quad& x, float mix)
 
 // W warps a block, S tokens a segment, CL blocks a cluster, D chunks in flight (0: a
 // chunk is read when it is needed)
-template <typename T, int W, int S, int CL, int D, bool VEC, bool FLAGS>
+template <typename T, int W, int S, int CL, int D, int HOW, bool FLAGS>
 __global__ void __launch_bounds__(32 * W, (kScanBlocks<T, W, 2, S>))
 scan_kernel(const __grid_constant__ Scan a) {
   extern __shared__ uint4 ring[];
@@ -43,12 +45,12 @@ scan_kernel(const __grid_constant__ Scan a) {
   constexpr int kSpan = 2 * W * S;      // tokens of a chunk
   const int rank = CL > 1 ? cluster_rank() : 0;
   const int64_t unit = blockIdx.x / CL, b = unit / a.strips;
-  const Channels<VEC> ch((int)(unit % a.strips), a.dim);
+  const Channels<T, HOW> ch((int)(unit % a.strips), a.dim);
   const int64_t row0 = b * a.length;
   const int seg = threadIdx.x >> 4, length = (int)a.length;
   const int64_t stride = (int64_t)kSpan * CL;
   // the chunk to read next, at the strip's first channel or at the lane's, and the one to write
-  const int channel = D > 0 ? ch.strip : ch.first;
+  const int channel = D > 0 && HOW != kPairs ? ch.strip : ch.first;
   const T* gate = static_cast<const T*>(a.gate) + (row0 + rank * kSpan) * a.ldg + channel;
   const T* x = static_cast<const T*>(a.x) + (row0 + rank * kSpan) * a.ldx + channel;
   T* h = static_cast<T*>(a.h) + (row0 + rank * kSpan + seg * S) * a.dim + ch.first;
@@ -57,10 +59,10 @@ scan_kernel(const __grid_constant__ Scan a) {
   x += seg * S * a.ldx;
   if (threadIdx.x < 16)
     sh.carry[0][threadIdx.x] = four(a.state ? ch.state(a.state + b * a.dim + ch.first) : quad(0.f));
-  const Ring<T, VEC, 2, S, W> slots(ring, min(kStrip, (int)a.dim - ch.strip));
+  const Ring<T, HOW, 2, S, W> slots(ring, ch, a.dim);
   // elements of the segment's first row ahead of the strip, in the chunk to use next
-  uint32_t fg = VEC ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(gate + seg * S * a.ldg) / sizeof(T));
-  uint32_t fx = VEC ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(x + seg * S * a.ldx) / sizeof(T));
+  uint32_t fg = HOW != kSingles ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(gate + seg * S * a.ldg) / sizeof(T));
+  uint32_t fx = HOW != kSingles ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(x + seg * S * a.ldx) / sizeof(T));
   Flags ahead[D > 0 ? D : 1];
   auto ask_next = [&] { return ask<S>(a.starts, a.mask, row0, a.length - left_in, length); };
   auto advance = [&] {
@@ -186,13 +188,13 @@ scan_kernel(const __grid_constant__ Scan a) {
 
 constexpr int kShortThreads = 128, kShortAhead = 4;
 // Short sequences: 16 lanes walk a strip's tokens, four of them in flight
-template <typename T, bool VEC, bool FLAGS>
+template <typename T, int HOW, bool FLAGS>
 __global__ void __launch_bounds__(kShortThreads) scan_short_kernel(const __grid_constant__ Scan a, int64_t units) {
   pdl_wait();
   const int64_t unit = (int64_t)blockIdx.x * (kShortThreads / 16) + (threadIdx.x >> 4);
   if (unit >= units) return;
   const int64_t b = unit / a.strips, row0 = b * a.length;
-  const Channels<VEC> ch((int)(unit % a.strips), a.dim);
+  const Channels<T, HOW> ch((int)(unit % a.strips), a.dim);
   if (!ch.any()) return;
   const int length = (int)a.length;
   const T* gate = static_cast<const T*>(a.gate) + row0 * a.ldg + ch.first;
@@ -228,16 +230,16 @@ __global__ void __launch_bounds__(kShortThreads) scan_short_kernel(const __grid_
   if (a.last) ch.put_state(a.last + b * a.dim + ch.first, p);
 }
 
-template <typename T, bool VEC> cudaError_t scan_short(const Scan& a, int64_t strips, cudaStream_t s) {
+template <typename T, int HOW> cudaError_t scan_short(const Scan& a, int64_t strips, cudaStream_t s) {
   constexpr int per = kShortThreads / 16;
-  return launch_k(a.starts || a.mask ? scan_short_kernel<T, VEC, true> : scan_short_kernel<T, VEC, false>,
+  return launch_k(a.starts || a.mask ? scan_short_kernel<T, HOW, true> : scan_short_kernel<T, HOW, false>,
                   dim3((unsigned)((strips + per - 1) / per)), dim3(kShortThreads), 0, s, true, a, strips);
 }
 
-template <typename T, int W, int S, int CL, int D, bool VEC>
+template <typename T, int W, int S, int CL, int D, int HOW>
 cudaError_t scan_with(const Scan& a, int64_t strips, cudaStream_t s) {
-  constexpr size_t smem = D * Ring<T, VEC, 2, S, W>::kStage;
-  constexpr auto plain = scan_kernel<T, W, S, CL, D, VEC, false>, flags = scan_kernel<T, W, S, CL, D, VEC, true>;
+  constexpr size_t smem = D * Ring<T, HOW, 2, S, W>::kStage;
+  constexpr auto plain = scan_kernel<T, W, S, CL, D, HOW, false>, flags = scan_kernel<T, W, S, CL, D, HOW, true>;
   if (a.starts || a.mask) {
     if (const cudaError_t e = smem ? allow_shared<flags>(smem) : cudaSuccess) return e;
     return launch_cluster(flags, strips * CL, CL, 32 * W, smem, s, a);
@@ -248,11 +250,11 @@ cudaError_t scan_with(const Scan& a, int64_t strips, cudaStream_t s) {
 
 // Up to four tokens, or 32 where there are strips enough for every SM's lanes, are walked one
 // after the other: one token of [256, 8192] bf16 5.5 us, 38.0 through the joins, 16 of [64, 4096] 5.7 and 9.2
-template <typename T, bool VEC> cudaError_t scan_by_size(const Scan& a, int64_t strips, cudaStream_t s) {
+template <typename T, int HOW> cudaError_t scan_by_size(const Scan& a, int64_t strips, cudaStream_t s) {
   constexpr int S = sizeof(T) == 2 ? 8 : 4;
-  if (a.length <= 4 || (a.length <= 32 && strips >= 2048)) return scan_short<T, VEC>(a, strips, s);
+  if (a.length <= 4 || (a.length <= 32 && strips >= 2048)) return scan_short<T, HOW>(a, strips, s);
   return scan_layout<T, S>(a.length, strips, [&](auto w, auto m, auto cl, auto d) {
-    return scan_with<T, decltype(w)::value, S * decltype(m)::value, decltype(cl)::value, decltype(d)::value, VEC>(
+    return scan_with<T, decltype(w)::value, S * decltype(m)::value, decltype(cl)::value, decltype(d)::value, HOW>(
         a, strips, s);
   });
 }
@@ -280,10 +282,11 @@ extern "C" muon_status muon_gated_scan(int64_t batch, int64_t length, int64_t di
   const int strips = (int)((dim + kStrip - 1) / kStrip);
   const Scan a = {length, dim, ldg, ldx, strips, mix ? 1.f : 0.f, gate, x, state, starts, token_mask, h, last};
   const int64_t rows = batch * length, units = batch * strips;
-  const bool vec = dim % 4 == 0 && fours(gate, rows, ldg, es) && fours(x, rows, ldx, es) && !off(h, 4 * es);
+  int how = std::max({lie(gate, rows, ldg, es), lie(x, rows, ldx, es), lie(h, rows, dim, es)});
+  if (rows <= 1) how = std::max(how, lie(nullptr, 2, dim, es));      // whole pieces in the row itself
   const cudaError_t e = by_type(dtype, [&](auto t) {
     using T = decltype(t);
-    return vec ? scan_by_size<T, true>(a, units, s) : scan_by_size<T, false>(a, units, s);
+    return by_how<T>(how, [&](auto h) { return scan_by_size<T, decltype(h)::value>(a, units, s); });
   });
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }

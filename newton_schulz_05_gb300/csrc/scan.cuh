@@ -15,8 +15,8 @@
 // underflows and a is 1.  A token that is masked or past the end is given the gate
 // +infinity and the input 0, which changes nothing.
 //
-// A block has a strip of 64 channels: 16 lanes of four channels (neighbouring ones
-// where rows allow pieces of four, else 16 apart), so a warp holds two segments.
+// A block has a strip of 64 channels: 16 lanes of four channels, so a warp holds two
+// segments.
 #pragma once
 
 #include "sequence.cuh"
@@ -111,49 +111,52 @@ template <int S> __device__ __forceinline__ Flags bits(const Flags& f) {
   return {starts >> half & 0xffff, live >> half & 0xffff, live == whole && starts == 0};
 }
 
-// Which channels a lane has: `has` of its four are inside the row.  VEC: four
-// neighbours, all inside or all outside.
-template <bool VEC> struct Channels {
+// How a lane's four channels lie in a row: neighbours, in aligned pieces of four; two aligned
+// pairs of bf16, 32 apart; or alone, 16 apart
+enum { kFours, kPairs, kSingles };
+
+template <typename T, int HOW> struct Channels {
   int strip, first;      // first channel of the strip, and of the lane, in the row
-  int left;       // channels from `first` on that are inside the row
+  int left;              // channels from `first` on that are inside the row
   __device__ __forceinline__ Channels(int index, int64_t dim) {
     const int l = threadIdx.x & 15;
     strip = index * kStrip;
-    first = strip + (VEC ? 4 * l : l);
+    first = strip + (HOW == kFours ? 4 * l : HOW == kPairs ? 2 * l : l);
     left = (int)dim - first;
   }
   __device__ __forceinline__ bool any() const { return left > 0; }
-  __device__ __forceinline__ int at(int j) const { return VEC ? j : 16 * j; }
+  // of channel j from the first
+  static __device__ __forceinline__ int at(int j) {
+    return HOW == kFours ? j : HOW == kPairs ? (j >> 1) * 32 + (j & 1) : 16 * j;
+  }
   __device__ __forceinline__ bool has(int j) const { return at(j) < left; }
 
   // p: the lane's first channel
-  __device__ __forceinline__ void load(Raw4<__nv_bfloat16>& r, const __nv_bfloat16* p) const {
-    if constexpr (VEC) {
-      r.u = *reinterpret_cast<const uint2*>(p);
-    } else {
+  __device__ __forceinline__ void load(Raw4<T>& r, const T* p) const {
+    if constexpr (HOW == kFours) {
+      r = *reinterpret_cast<const Raw4<T>*>(p);
+    } else if constexpr (HOW == kPairs) {
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
+      r.u = make_uint2(has(0) ? q[0] : 0, has(2) ? q[16] : 0);
+    } else if constexpr (sizeof(T) == 2) {
       const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
       uint32_t w[4];
       #pragma unroll
       for (int j = 0; j < 4; ++j) w[j] = has(j) ? q[16 * j] : 0;
       r.u = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-    }
-  }
-  __device__ __forceinline__ void load(Raw4<float>& r, const float* p) const {
-    if constexpr (VEC) {
-      r.u = *reinterpret_cast<const uint4*>(p);
     } else {
       const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
-      uint32_t w[4];
-      #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = has(j) ? q[16 * j] : 0;
-      r.u = make_uint4(w[0], w[1], w[2], w[3]);
+      r.u = make_uint4(has(0) ? q[0] : 0, has(1) ? q[16] : 0, has(2) ? q[32] : 0, has(3) ? q[48] : 0);
     }
   }
   __device__ __forceinline__ void store(__nv_bfloat16* p, const Quad& q) const {
     const __nv_bfloat162 a = __float22bfloat162_rn(q.v[0]), b = __float22bfloat162_rn(q.v[1]);
-    if constexpr (VEC) {
-      *reinterpret_cast<uint2*>(p) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    const uint2 u = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    if constexpr (HOW == kFours) {
+      *reinterpret_cast<uint2*>(p) = u;
+    } else if constexpr (HOW == kPairs) {
+      if (has(0)) *reinterpret_cast<uint32_t*>(p) = u.x;
+      if (has(2)) *reinterpret_cast<uint32_t*>(p + 32) = u.y;
     } else {
       if (has(0)) p[0] = a.x;
       if (has(1)) p[16] = a.y;
@@ -162,7 +165,7 @@ template <bool VEC> struct Channels {
     }
   }
   __device__ __forceinline__ void store(float* p, const Quad& q) const {
-    if constexpr (VEC) {
+    if constexpr (HOW == kFours) {
       *reinterpret_cast<float4*>(p) = make_float4(q.v[0].x, q.v[0].y, q.v[1].x, q.v[1].y);
     } else {
       if (has(0)) p[0] = q.v[0].x;
@@ -187,39 +190,49 @@ template <bool VEC> struct Channels {
 };
 
 // Rows of N operands on their way through shared memory: D chunks, S tokens a segment, 2 W
-// segments.  A row of a strip is copied by the half warp that reads it, in aligned pieces of
-// four channels; where rows are not made of those, its first piece may begin up to three
-// elements ahead of the row and there is one more.  Only pieces that hold an element of the
-// row are read: an aligned 8 or 16 bytes lie wholly in the allocation that one of them does.
-template <typename T, bool VEC, int N, int S, int W> struct Ring {
-  static constexpr int kRow = VEC ? 16 : 17;
+// segments.  A lane copies the piece or the pairs that it reads.  Singles are copied by the half
+// warp that reads the row, in aligned pieces of four, the first of which may begin up to three
+// elements ahead of the row, and one more: only pieces that hold an element of the row are read,
+// and an aligned 8 or 16 bytes lie wholly in the allocation that one of them does.  (Copies of
+// single fp32 elements took 179 us for [8, 4096, 1409] where these take 155.)
+template <typename T, int HOW, int N, int S, int W> struct Ring {
+  static constexpr int kRow = HOW == kSingles ? 17 : 16;
   static constexpr size_t kStage = sizeof(Raw4<T>) * N * S * 2 * W * kRow;
   Raw4<T>* base;
+  const Channels<T, HOW>& ch;
   int left;         // channels of the strip
-  __device__ __forceinline__ Ring(void* smem, int left)
-      : base(static_cast<Raw4<T>*>(smem) + (threadIdx.x >> 4) * kRow), left(left) {}
+  __device__ __forceinline__ Ring(void* smem, const Channels<T, HOW>& ch, int64_t dim)
+      : base(static_cast<Raw4<T>*>(smem) + (threadIdx.x >> 4) * kRow), ch(ch),
+        left(min(kStrip, (int)dim - ch.strip)) {}
   __device__ __forceinline__ Raw4<T>* row(int stage, int operand, int i) const {
     return base + ((stage * N + operand) * S + i) * (2 * W * kRow);
   }
-  // p: the strip's first channel in the row
+  // p: the strip's first channel in the row, for pairs the lane's
   __device__ __forceinline__ void copy(Raw4<T>* to, const T* p) const {
     const int l = threadIdx.x & 15;
-    if constexpr (VEC) {
-      if (4 * l < left) piece(to + l, p + 4 * l, 4 * sizeof(T));
+    if constexpr (HOW == kFours) {
+      if (4 * l < left) piece<4 * sizeof(T)>(to + l, p + 4 * l);
+    } else if constexpr (HOW == kPairs) {
+      if (ch.has(0)) piece<4>(to + l, p);
+      if (ch.has(2)) piece<4>(reinterpret_cast<uint32_t*>(to + l) + 1, p + 32);
     } else {
       const int f = (int)(reinterpret_cast<uintptr_t>(p) / sizeof(T) & 3);
       const int first = 4 * l - f, inside = left - first;
-      if (inside > 0) piece(to + l, p + first, (int)sizeof(T) * (inside < 4 ? inside : 4));
-      if (l == 0 && f > 0 && left > 64 - f) piece(to + 16, p + 64 - f, (int)sizeof(T) * (left - (64 - f)));
+      if (inside > 0) part(to + l, p + first, (int)sizeof(T) * (inside < 4 ? inside : 4));
+      if (l == 0 && f > 0 && left > 64 - f) part(to + 16, p + 64 - f, (int)sizeof(T) * (left - (64 - f)));
     }
   }
-  static __device__ __forceinline__ void piece(Raw4<T>* to, const T* p, int bytes) {
+  template <int BYTES> static __device__ __forceinline__ void piece(void* to, const T* p) {
     const uint32_t s = (uint32_t)__cvta_generic_to_shared(to);
-    if constexpr (VEC && sizeof(T) == 2)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(s), "l"(p) : "memory");
-    else if constexpr (VEC)
+    if constexpr (BYTES == 16)
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(s), "l"(p) : "memory");
-    else if constexpr (sizeof(T) == 2)
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(s), "l"(p), "n"(BYTES) : "memory");
+  }
+  // the first `bytes` of an aligned piece of four
+  static __device__ __forceinline__ void part(Raw4<T>* to, const T* p, int bytes) {
+    const uint32_t s = (uint32_t)__cvta_generic_to_shared(to);
+    if constexpr (sizeof(T) == 2)
       asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(s), "l"(p), "r"(bytes) : "memory");
     else
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(p), "r"(bytes) : "memory");
@@ -231,12 +244,12 @@ template <typename T, bool VEC, int N, int S, int W> struct Ring {
     if (gate) infinite(v);
     else zero(v);
     to[l] = v;
-    if (!VEC && l == 0) to[16] = v;
+    if (HOW == kSingles && l == 0) to[16] = v;
   }
   // the lane's channels; f: the row's elements ahead of the strip
   __device__ __forceinline__ Raw4<T> get(const Raw4<T>* from, int f) const {
     const int l = threadIdx.x & 15;
-    if constexpr (VEC) {
+    if constexpr (HOW != kSingles) {
       return from[l];
     } else if constexpr (sizeof(T) == 2) {
       const uint16_t* e = reinterpret_cast<const uint16_t*>(from) + f + l;
@@ -247,7 +260,7 @@ template <typename T, bool VEC, int N, int S, int W> struct Ring {
     }
   }
   // the half warp's lanes have copied for one another, and have read
-  __device__ __forceinline__ void arrived() const { if (!VEC) __syncwarp(); }
+  __device__ __forceinline__ void arrived() const { if (HOW == kSingles) __syncwarp(); }
 };
 
 // A run of tokens as a map of the state p in front of it, H + (k + m) p: where its
@@ -451,9 +464,17 @@ template <typename T, int S, typename F> cudaError_t scan_layout(int64_t length,
   return f(Int<8>(), Int<2>(), Int<8>(), Int<2>());
 }
 
-// whether rows of `p` are made of aligned pieces of four
-inline bool fours(const void* p, int64_t rows, int64_t ld, size_t es) {
-  return !off(p, 4 * es) && (rows <= 1 || ld % 4 == 0);
+// the widest access that all rows allow
+inline int lie(const void* p, int64_t rows, int64_t ld, size_t es) {
+  auto in = [&](int n) { return !off(p, n * es) && (rows <= 1 || ld % n == 0); };
+  return in(4) ? kFours : es == 2 && in(2) ? kPairs : kSingles;
+}
+// f(how), as an integral constant
+template <typename T, typename F> cudaError_t by_how(int how, F f) {
+  if (how == kFours) return f(Int<kFours>());
+  if constexpr (sizeof(T) == 2)
+    if (how == kPairs) return f(Int<kPairs>());
+  return f(Int<kSingles>());
 }
 
 }  // namespace

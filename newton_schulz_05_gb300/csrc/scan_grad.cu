@@ -2,6 +2,8 @@
 // first, over what reaches the state behind each token, c -> a (dh + c).
 #include "scan.cuh"
 
+#include <algorithm>
+
 namespace muon {
 
 namespace {
@@ -32,7 +34,7 @@ __device__ __forceinline__ void shares_of(const Quad& g, Quad& keep, Quad& take)
   }
 }
 
-template <typename T, int W, int S, int CL, int D, bool VEC, bool FLAGS>
+template <typename T, int W, int S, int CL, int D, int HOW, bool FLAGS>
 __global__ void __launch_bounds__(32 * W, (kScanBlocks<T, W, 4, S>))
 scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
   extern __shared__ uint4 ring[];
@@ -41,14 +43,14 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
   constexpr int kSpan = 2 * W * S;
   const int rank = CL > 1 ? cluster_rank() : 0;      // rank 0 has the last chunk
   const int64_t unit = blockIdx.x / CL, b = unit / a.strips;
-  const Channels<VEC> ch((int)(unit % a.strips), a.dim);
+  const Channels<T, HOW> ch((int)(unit % a.strips), a.dim);
   const int64_t row0 = b * a.length, stride = (int64_t)kSpan * CL;
   const int seg = threadIdx.x >> 4, length = (int)a.length;
   const int chunks = (int)((a.length + kSpan - 1) / kSpan), rounds = (chunks + CL - 1) / CL;
   // the segment's first token (in front of the sequence in the last round of some ranks)
   // of the chunk to read next, and of the one to write
   int64_t t_in = (int64_t)(chunks - 1 - rank) * kSpan + seg * S, t0 = t_in;
-  const int channel = D > 0 ? ch.strip : ch.first;
+  const int channel = D > 0 && HOW != kPairs ? ch.strip : ch.first;
   const T* dh = static_cast<const T*>(a.dh) + (row0 + t_in) * a.lddh + channel;
   const T* gate = static_cast<const T*>(a.gate) + (row0 + t_in) * a.ldg + channel;
   const T* x = static_cast<const T*>(a.x) + (row0 + t_in) * a.ldx + channel;
@@ -57,9 +59,9 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
   const bool mix = a.mix != 0.f;
   if (threadIdx.x < 16)
     sh.carry[0][threadIdx.x] = four(a.dlast ? ch.state(a.dlast + b * a.dim + ch.first) : quad(0.f));
-  const Ring<T, VEC, 4, S, W> slots(ring, min(kStrip, (int)a.dim - ch.strip));
+  const Ring<T, HOW, 4, S, W> slots(ring, ch, a.dim);
   // elements of the segment's first row ahead of the strip, in the chunk to use next
-  auto ahead_of = [](const T* p) { return VEC ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(p) / sizeof(T)); };
+  auto ahead_of = [](const T* p) { return HOW != kSingles ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(p) / sizeof(T)); };
   uint32_t fd = ahead_of(dh), fg = ahead_of(gate), fx = ahead_of(x), fh = ahead_of(h);
   Flags ahead[D > 0 ? D : 1];
   auto ask_next = [&] { return ask<S>(a.starts, a.mask, row0, t_in, length); };
@@ -218,14 +220,14 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
 
 constexpr int kShortThreads = 128, kShortAhead = 2;
 // Short sequences, as in the forward pass
-template <typename T, bool VEC, bool FLAGS>
+template <typename T, int HOW, bool FLAGS>
 __global__ void __launch_bounds__(kShortThreads)
 scan_short_bwd_kernel(const __grid_constant__ ScanBwd a, int64_t units) {
   pdl_wait();
   const int64_t unit = (int64_t)blockIdx.x * (kShortThreads / 16) + (threadIdx.x >> 4);
   if (unit >= units) return;
   const int64_t b = unit / a.strips, row0 = b * a.length;
-  const Channels<VEC> ch((int)(unit % a.strips), a.dim);
+  const Channels<T, HOW> ch((int)(unit % a.strips), a.dim);
   if (!ch.any()) return;
   const T* dh = static_cast<const T*>(a.dh) + row0 * a.lddh + ch.first;
   const T* gate = static_cast<const T*>(a.gate) + row0 * a.ldg + ch.first;
@@ -277,17 +279,17 @@ scan_short_bwd_kernel(const __grid_constant__ ScanBwd a, int64_t units) {
   if (a.dstate) ch.put_state(a.dstate + b * a.dim + ch.first, c);
 }
 
-template <typename T, bool VEC> cudaError_t scan_short_bwd(const ScanBwd& a, int64_t strips, cudaStream_t s) {
+template <typename T, int HOW> cudaError_t scan_short_bwd(const ScanBwd& a, int64_t strips, cudaStream_t s) {
   constexpr int per = kShortThreads / 16;
-  return launch_k(a.starts || a.mask ? scan_short_bwd_kernel<T, VEC, true> : scan_short_bwd_kernel<T, VEC, false>,
+  return launch_k(a.starts || a.mask ? scan_short_bwd_kernel<T, HOW, true> : scan_short_bwd_kernel<T, HOW, false>,
                   dim3((unsigned)((strips + per - 1) / per)), dim3(kShortThreads), 0, s, true, a, strips);
 }
 
-template <typename T, int W, int S, int CL, int D, bool VEC>
+template <typename T, int W, int S, int CL, int D, int HOW>
 cudaError_t scan_bwd_with(const ScanBwd& a, int64_t strips, cudaStream_t s) {
-  constexpr size_t smem = D * Ring<T, VEC, 4, S, W>::kStage;
-  constexpr auto plain = scan_bwd_kernel<T, W, S, CL, D, VEC, false>,
-                 flags = scan_bwd_kernel<T, W, S, CL, D, VEC, true>;
+  constexpr size_t smem = D * Ring<T, HOW, 4, S, W>::kStage;
+  constexpr auto plain = scan_bwd_kernel<T, W, S, CL, D, HOW, false>,
+                 flags = scan_bwd_kernel<T, W, S, CL, D, HOW, true>;
   if (a.starts || a.mask) {
     if (const cudaError_t e = smem ? allow_shared<flags>(smem) : cudaSuccess) return e;
     return launch_cluster(flags, strips * CL, CL, 32 * W, smem, s, a);
@@ -299,11 +301,11 @@ cudaError_t scan_bwd_with(const ScanBwd& a, int64_t strips, cudaStream_t s) {
 // Up to four tokens, or 32 where there are strips enough for every SM's lanes, are walked one
 // after the other: one token of [256, 8192] bf16 7.1 us, 37.0 through the
 // joins, 16 of [64, 4096] 10.7 and 25.4
-template <typename T, bool VEC> cudaError_t scan_bwd_by_size(const ScanBwd& a, int64_t strips, cudaStream_t s) {
+template <typename T, int HOW> cudaError_t scan_bwd_by_size(const ScanBwd& a, int64_t strips, cudaStream_t s) {
   constexpr int S = sizeof(T) == 2 ? 4 : 2;
-  if (a.length <= 4 || (a.length <= 32 && strips >= 2048)) return scan_short_bwd<T, VEC>(a, strips, s);
+  if (a.length <= 4 || (a.length <= 32 && strips >= 2048)) return scan_short_bwd<T, HOW>(a, strips, s);
   return scan_layout<T, S>(a.length, strips, [&](auto w, auto m, auto cl, auto d) {
-    return scan_bwd_with<T, decltype(w)::value, S * decltype(m)::value, decltype(cl)::value, decltype(d)::value, VEC>(
+    return scan_bwd_with<T, decltype(w)::value, S * decltype(m)::value, decltype(cl)::value, decltype(d)::value, HOW>(
         a, strips, s);
   });
 }
@@ -335,12 +337,12 @@ extern "C" muon_status muon_gated_scan_backward(
   const ScanBwd a = {length, dim, lddh, ldg, ldx, ldh, strips, mix ? 1.f : 0.f, dh, gate, x, h, state, dlast, starts,
                      token_mask, dgate, dx, dstate};
   const int64_t rows = batch * length, units = batch * strips;
-  const bool vec = dim % 4 == 0 && fours(dh, rows, lddh, es) && fours(gate, rows, ldg, es) &&
-                   (!mix || fours(x, rows, ldx, es)) && fours(h, rows, ldh, es) && !off(dgate, 4 * es) &&
-                   !off(dx, 4 * es);
+  int how = std::max({lie(dh, rows, lddh, es), lie(gate, rows, ldg, es), lie(h, rows, ldh, es),
+                            lie(dgate, rows, dim, es), lie(dx, rows, dim, es), mix ? lie(x, rows, ldx, es) : (int)kFours});
+  if (rows <= 1) how = std::max(how, lie(nullptr, 2, dim, es));      // whole pieces in the row itself
   const cudaError_t e = by_type(dtype, [&](auto t) {
     using T = decltype(t);
-    return vec ? scan_bwd_by_size<T, true>(a, units, s) : scan_bwd_by_size<T, false>(a, units, s);
+    return by_how<T>(how, [&](auto h) { return scan_bwd_by_size<T, decltype(h)::value>(a, units, s); });
   });
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }

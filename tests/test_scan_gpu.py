@@ -99,7 +99,7 @@ def test_flags_and_strides(layers, b, t, d, layout, starts, masked, dtype):
 # one case for each way the length is cut up: blocks of one, four and eight warps, clusters of
 # four and eight, few and many chunks
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("layout,extra", [("dense", 0), ("columns", 0), ("odd", 1), ("dense", 3)])
+@pytest.mark.parametrize("layout,extra", [("dense", 0), ("columns", 0), ("odd", 1), ("dense", 2), ("dense", 3)])
 @pytest.mark.parametrize("b,t,d", [(2, 9, 64), (3, 15, 128), (3, 50, 192), (310, 37, 64), (20, 70, 1024),
                                    (9, 300, 960), (70, 200, 64), (3, 700, 64), (1, 2100, 128)])
 def test_flags_however_the_length_is_cut(layers, b, t, d, layout, extra, dtype):
