@@ -8,7 +8,8 @@ namespace muon {
 namespace {
 
 struct Scan {
-  int64_t length, dim, ldg, ldx;
+  int64_t length, dim;
+  uint32_t ldg, ldx;          // 32 bits: one multiply-add makes an address
   int strips;
   float mix;          // 1: the input is multiplied by 1 - a; 0: it is not
   const void *gate, *x;
@@ -51,23 +52,23 @@ scan_kernel(const __grid_constant__ Scan a) {
   const int64_t stride = (int64_t)kSpan * CL;
   // the chunk to read next, at the strip's first channel or at the lane's, and the one to write
   const int channel = D > 0 && HOW != kPairs ? ch.strip : ch.first;
-  const T* gate = static_cast<const T*>(a.gate) + (row0 + rank * kSpan) * a.ldg + channel;
-  const T* x = static_cast<const T*>(a.x) + (row0 + rank * kSpan) * a.ldx + channel;
+  const T* gate = static_cast<const T*>(a.gate) + (row0 + rank * kSpan) * (int64_t)a.ldg + channel;
+  const T* x = static_cast<const T*>(a.x) + (row0 + rank * kSpan) * (int64_t)a.ldx + channel;
   T* h = static_cast<T*>(a.h) + (row0 + rank * kSpan + seg * S) * a.dim + ch.first;
   int left_in = length - rank * kSpan - seg * S, left = left_in;    // tokens from the segment's first on
-  gate += seg * S * a.ldg;
-  x += seg * S * a.ldx;
+  gate += seg * S * (int64_t)a.ldg;
+  x += seg * S * (int64_t)a.ldx;
   if (threadIdx.x < 16)
     sh.carry[0][threadIdx.x] = four(a.state ? ch.state(a.state + b * a.dim + ch.first) : quad(0.f));
   const Ring<T, HOW, 2, S, W> slots(ring, ch, a.dim);
   // elements of the segment's first row ahead of the strip, in the chunk to use next
-  uint32_t fg = HOW != kSingles ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(gate + seg * S * a.ldg) / sizeof(T));
-  uint32_t fx = HOW != kSingles ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(x + seg * S * a.ldx) / sizeof(T));
+  uint32_t fg = HOW != kSingles ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(gate) / sizeof(T));
+  uint32_t fx = HOW != kSingles ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(x) / sizeof(T));
   Flags ahead[D > 0 ? D : 1];
   auto ask_next = [&] { return ask<S>(a.starts, a.mask, row0, a.length - left_in, length); };
   auto advance = [&] {
-    gate += stride * a.ldg;
-    x += stride * a.ldx;
+    gate += (uint64_t)a.ldg * (kSpan * CL);
+    x += (uint64_t)a.ldx * (kSpan * CL);
     left_in -= (int)stride;
   };
   auto start = [&](int stage) {
@@ -75,14 +76,14 @@ scan_kernel(const __grid_constant__ Scan a) {
     if (left_in >= S) {
       #pragma unroll
       for (int i = 0; i < S; ++i) {
-        slots.copy(slots.row(stage, 0, i), gate + i * a.ldg);
-        slots.copy(slots.row(stage, 1, i), x + i * a.ldx);
+        slots.copy(slots.row(stage, 0, i), gate + (uint64_t)a.ldg * i);
+        slots.copy(slots.row(stage, 1, i), x + (uint64_t)a.ldx * i);
       }
     } else {
       for (int i = 0; i < S; ++i) {
         if (i < left_in) {
-          slots.copy(slots.row(stage, 0, i), gate + i * a.ldg);
-          slots.copy(slots.row(stage, 1, i), x + i * a.ldx);
+          slots.copy(slots.row(stage, 0, i), gate + (uint64_t)a.ldg * i);
+          slots.copy(slots.row(stage, 1, i), x + (uint64_t)a.ldx * i);
         } else {
           slots.fill(slots.row(stage, 0, i), true);
           slots.fill(slots.row(stage, 1, i), false);
@@ -113,8 +114,8 @@ scan_kernel(const __grid_constant__ Scan a) {
         infinite(rg[i]);
         zero(rx[i]);
         if (i < n) {
-          ch.load(rg[i], gate + i * a.ldg);
-          ch.load(rx[i], x + i * a.ldx);
+          ch.load(rg[i], gate + (uint64_t)a.ldg * i);
+          ch.load(rx[i], x + (uint64_t)a.ldx * i);
         }
       }
       advance();
@@ -122,37 +123,39 @@ scan_kernel(const __grid_constant__ Scan a) {
     Quad P[S], H[S];
     Segment run = {quad(1.f), quad(0.f), quad(0.f), false};
     const Flags now = FLAGS ? bits<S>(ahead[0]) : Flags{0, 0, true};
-    #pragma unroll
-    for (int i = 0; i < S; ++i) {
-      Raw4<T> gi, vi;
-      if constexpr (D > 0) {
-        gi = slots.get(slots.row(stage, 0, i), (fg + i * (uint32_t)a.ldg) & 3);
-        vi = slots.get(slots.row(stage, 1, i), (fx + i * (uint32_t)a.ldx) & 3);
-      } else {
-        gi = rg[i];
-        vi = rx[i];
+    // (a loop for chunks with a flag and one without, each a single run of instructions)
+    auto reduce = [&](auto flagged) {
+      #pragma unroll
+      for (int i = 0; i < S; ++i) {
+        Raw4<T> gi, vi;
+        if constexpr (D > 0) {
+          gi = slots.get(slots.row(stage, 0, i), (fg + i * a.ldg) & 3);
+          vi = slots.get(slots.row(stage, 1, i), (fx + i * a.ldx) & 3);
+        } else {
+          gi = rg[i];
+          vi = rx[i];
+        }
+        if constexpr (decltype(flagged)::value) {
+          const uint32_t live = ones(now.live, i), on = ~ones(now.starts, i);
+          gi = gate_or(gi, live);
+          vi = masked(vi, live);
+          run.P = masked(run.P, on);
+          run.H = masked(run.H, on);
+        }
+        const Step st = step_of(widen(gi), widen(vi), a.mix);
+        P[i] = run.P = mul(run.P, st.keep);
+        H[i] = run.H = fma(st.keep, run.H, st.in);
+        run.Q = fma(st.keep, run.Q, st.lose);
       }
-      if (FLAGS && !now.quiet) {
-        const uint32_t live = ones(now.live, i);
-        gi = gate_or(gi, live);
-        vi = masked(vi, live);
-      }
-      const Step st = step_of(widen(gi), widen(vi), a.mix);
-      if (FLAGS && !now.quiet) {
-        const uint32_t on = ~ones(now.starts, i);
-        run.P = masked(run.P, on);
-        run.H = masked(run.H, on);
-      }
-      P[i] = run.P = mul(run.P, st.keep);
-      H[i] = run.H = fma(st.keep, run.H, st.in);
-      run.Q = fma(st.keep, run.Q, st.lose);
-    }
+    };
+    if (FLAGS && !now.quiet) reduce(std::bool_constant<FLAGS>());
+    else reduce(std::false_type());
     run.cut = now.starts != 0;
     Quad front = join_segments<W, CL, FLAGS, false>(sh, run, round, [&] {
       if constexpr (D > 0) {
         start(stage);
-        fg += (uint32_t)(stride * a.ldg);
-        fx += (uint32_t)(stride * a.ldx);
+        fg += a.ldg * (kSpan * CL);
+        fx += a.ldx * (kSpan * CL);
         stage = stage + 1 == D ? 0 : stage + 1;
         if (FLAGS) {
           #pragma unroll
@@ -163,18 +166,15 @@ scan_kernel(const __grid_constant__ Scan a) {
       }
     });
     const int n = ch.any() ? left : 0;
-    auto finish = [&](int i) {
-      if (FLAGS && !now.quiet) front = masked(front, ~ones(now.starts, i));
-      return fma(P[i], front, H[i]);
-    };
-    if (n >= S) {
+    if (n >= S && (!FLAGS || now.quiet)) {
       #pragma unroll
-      for (int i = 0; i < S; ++i) ch.store(h + i * a.dim, finish(i));
+      for (int i = 0; i < S; ++i) ch.store(h + (uint64_t)(uint32_t)a.dim * i, fma(P[i], front, H[i]));
     } else {
       #pragma unroll
       for (int i = 0; i < S; ++i) {
-        const Quad q = finish(i);
-        if (i < n) ch.store(h + i * a.dim, q);
+        if (FLAGS) front = masked(front, ~ones(now.starts, i));
+        const Quad q = fma(P[i], front, H[i]);
+        if (i < n) ch.store(h + (uint64_t)(uint32_t)a.dim * i, q);
       }
     }
     h += stride * a.dim;
@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(kShortThreads) scan_short_kernel(const __grid_
   const Channels<T, HOW> ch((int)(unit % a.strips), a.dim);
   if (!ch.any()) return;
   const int length = (int)a.length;
-  const T* gate = static_cast<const T*>(a.gate) + row0 * a.ldg + ch.first;
-  const T* x = static_cast<const T*>(a.x) + row0 * a.ldx + ch.first;
+  const T* gate = static_cast<const T*>(a.gate) + row0 * (int64_t)a.ldg + ch.first;
+  const T* x = static_cast<const T*>(a.x) + row0 * (int64_t)a.ldx + ch.first;
   T* h = static_cast<T*>(a.h) + row0 * a.dim + ch.first;
   Quad p = a.state ? ch.state(a.state + b * a.dim + ch.first) : quad(0.f);
   for (int t0 = 0; t0 < length; t0 += kShortAhead) {
@@ -208,8 +208,8 @@ __global__ void __launch_bounds__(kShortThreads) scan_short_kernel(const __grid_
     for (int i = 0; i < kShortAhead; ++i) {
       const int t = t0 + i;
       if (t >= length) continue;
-      ch.load(rg[i], gate + t * a.ldg);
-      ch.load(rx[i], x + t * a.ldx);
+      ch.load(rg[i], gate + t * (int64_t)a.ldg);
+      ch.load(rx[i], x + t * (int64_t)a.ldx);
       if (FLAGS) {
         live[i] = !a.mask || a.mask[row0 + t];
         begins[i] = a.starts && a.starts[row0 + t];
@@ -273,6 +273,7 @@ extern "C" muon_status muon_gated_scan(int64_t batch, int64_t length, int64_t di
   const muon_status st = check_scan(batch, length, dim, dtype);
   if (st != MUON_OK) return st;
   if (ldg < 0 || ldx < 0 || (batch > 0 && length > 0 && (!gate || !x || !h))) return MUON_ERR_INVALID_ARG;
+  if ((ldg | ldx) >> 32) return MUON_ERR_UNSUPPORTED_SHAPE;
   const size_t es = size_of(dtype);
   if (any_off(es, gate, x, h) || any_off(4, state, last)) return MUON_ERR_ALIGNMENT;
   if (fault_switch() == kFaultLaunch) return MUON_ERR_CUDA;
@@ -280,7 +281,7 @@ extern "C" muon_status muon_gated_scan(int64_t batch, int64_t length, int64_t di
   NvtxRange range("muon_gated_scan");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int strips = (int)((dim + kStrip - 1) / kStrip);
-  const Scan a = {length, dim, ldg, ldx, strips, mix ? 1.f : 0.f, gate, x, state, starts, token_mask, h, last};
+  const Scan a = {length, dim, (uint32_t)ldg, (uint32_t)ldx, strips, mix ? 1.f : 0.f, gate, x, state, starts, token_mask, h, last};
   const int64_t rows = batch * length, units = batch * strips;
   int how = std::max({lie(gate, rows, ldg, es), lie(x, rows, ldx, es), lie(h, rows, dim, es)});
   if (rows <= 1) how = std::max(how, lie(nullptr, 2, dim, es));      // whole pieces in the row itself

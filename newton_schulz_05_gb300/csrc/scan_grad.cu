@@ -9,7 +9,8 @@ namespace muon {
 namespace {
 
 struct ScanBwd {
-  int64_t length, dim, lddh, ldg, ldx, ldh;
+  int64_t length, dim;
+  uint32_t lddh, ldg, ldx, ldh;
   int strips;
   float mix;          // 1 or 0: how much of x the state's difference has
   const void *dh, *gate, *x, *h;
@@ -44,17 +45,17 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
   const int rank = CL > 1 ? cluster_rank() : 0;      // rank 0 has the last chunk
   const int64_t unit = blockIdx.x / CL, b = unit / a.strips;
   const Channels<T, HOW> ch((int)(unit % a.strips), a.dim);
-  const int64_t row0 = b * a.length, stride = (int64_t)kSpan * CL;
+  const int64_t row0 = b * a.length;
   const int seg = threadIdx.x >> 4, length = (int)a.length;
   const int chunks = (int)((a.length + kSpan - 1) / kSpan), rounds = (chunks + CL - 1) / CL;
   // the segment's first token (in front of the sequence in the last round of some ranks)
   // of the chunk to read next, and of the one to write
-  int64_t t_in = (int64_t)(chunks - 1 - rank) * kSpan + seg * S, t0 = t_in;
+  int t_in = (int)((int64_t)(chunks - 1 - rank) * kSpan + seg * S), t0 = t_in;
   const int channel = D > 0 && HOW != kPairs ? ch.strip : ch.first;
-  const T* dh = static_cast<const T*>(a.dh) + (row0 + t_in) * a.lddh + channel;
-  const T* gate = static_cast<const T*>(a.gate) + (row0 + t_in) * a.ldg + channel;
-  const T* x = static_cast<const T*>(a.x) + (row0 + t_in) * a.ldx + channel;
-  const T* h = static_cast<const T*>(a.h) + (row0 + t_in - 1) * a.ldh + channel;
+  const T* dh = static_cast<const T*>(a.dh) + (row0 + t_in) * (int64_t)a.lddh + channel;
+  const T* gate = static_cast<const T*>(a.gate) + (row0 + t_in) * (int64_t)a.ldg + channel;
+  const T* x = static_cast<const T*>(a.x) + (row0 + t_in) * (int64_t)a.ldx + channel;
+  const T* h = static_cast<const T*>(a.h) + (row0 + t_in - 1) * (int64_t)a.ldh + channel;
   const int64_t out = row0 * a.dim + ch.first;
   const bool mix = a.mix != 0.f;
   if (threadIdx.x < 16)
@@ -66,37 +67,35 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
   Flags ahead[D > 0 ? D : 1];
   auto ask_next = [&] { return ask<S>(a.starts, a.mask, row0, t_in, length); };
   auto advance = [&] {
-    dh -= stride * a.lddh;
-    gate -= stride * a.ldg;
-    x -= stride * a.ldx;
-    h -= stride * a.ldh;
-    t_in -= stride;
+    dh -= (uint64_t)a.lddh * (kSpan * CL);
+    gate -= (uint64_t)a.ldg * (kSpan * CL);
+    x -= (uint64_t)a.ldx * (kSpan * CL);
+    h -= (uint64_t)a.ldh * (kSpan * CL);
+    t_in -= kSpan * CL;
   };
   // how many of a segment's tokens are inside, all from its first on (chunks start at 0)
-  auto inside = [&](int64_t t) {
-    return t < 0 ? 0 : t + S <= length ? S : (int)(t < length ? length - t : 0);
-  };
+  auto inside = [&](int t) { return t < 0 ? 0 : max(0, min(S, length - t)); };
   auto start = [&](int stage) {
     const int n = inside(t_in);
     slots.arrived();
     if (n == S && t_in > 0 && mix) {
       #pragma unroll
       for (int i = 0; i < S; ++i) {
-        slots.copy(slots.row(stage, 0, i), dh + i * a.lddh);
-        slots.copy(slots.row(stage, 1, i), gate + i * a.ldg);
-        slots.copy(slots.row(stage, 2, i), x + i * a.ldx);
-        slots.copy(slots.row(stage, 3, i), h + i * a.ldh);
+        slots.copy(slots.row(stage, 0, i), dh + (uint64_t)a.lddh * i);
+        slots.copy(slots.row(stage, 1, i), gate + (uint64_t)a.ldg * i);
+        slots.copy(slots.row(stage, 2, i), x + (uint64_t)a.ldx * i);
+        slots.copy(slots.row(stage, 3, i), h + (uint64_t)a.ldh * i);
       }
     } else {
       for (int i = 0; i < S; ++i) {
         Raw4<T>* const to[4] = {slots.row(stage, 0, i), slots.row(stage, 1, i), slots.row(stage, 2, i),
                                 slots.row(stage, 3, i)};
         if (i < n) {
-          slots.copy(to[0], dh + i * a.lddh);
-          slots.copy(to[1], gate + i * a.ldg);
-          if (mix) slots.copy(to[2], x + i * a.ldx);
+          slots.copy(to[0], dh + (uint64_t)a.lddh * i);
+          slots.copy(to[1], gate + (uint64_t)a.ldg * i);
+          if (mix) slots.copy(to[2], x + (uint64_t)a.ldx * i);
           else slots.fill(to[2], false);
-          if (i > 0 || t_in > 0) slots.copy(to[3], h + i * a.ldh);
+          if (i > 0 || t_in > 0) slots.copy(to[3], h + (uint64_t)a.ldh * i);
           else slots.fill(to[3], false);
         } else {
           slots.fill(to[0], false);
@@ -131,10 +130,10 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
         zero(rx[i]);
         zero(rh[i]);
         if (i < n) {
-          ch.load(rd[i], dh + i * a.lddh);
-          ch.load(rg[i], gate + i * a.ldg);
-          if (mix) ch.load(rx[i], x + i * a.ldx);
-          if (i > 0 || t_in > 0) ch.load(rh[i], h + i * a.ldh);
+          ch.load(rd[i], dh + (uint64_t)a.lddh * i);
+          ch.load(rg[i], gate + (uint64_t)a.ldg * i);
+          if (mix) ch.load(rx[i], x + (uint64_t)a.ldx * i);
+          if (i > 0 || t_in > 0) ch.load(rh[i], h + (uint64_t)a.ldh * i);
         }
       }
       advance();
@@ -142,47 +141,51 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
     Quad keep[S], take[S], d[S], v[S];
     Segment run = {quad(1.f), quad(0.f), quad(0.f), false};
     const Flags now = FLAGS ? bits<S>(ahead[0]) : Flags{0, 0, true};
-    #pragma unroll
-    for (int i = S - 1; i >= 0; --i) {
-      Raw4<T> di, gi, xi, hi;
-      if constexpr (D > 0) {
-        di = slots.get(slots.row(stage, 0, i), (fd + i * (uint32_t)a.lddh) & 3);
-        gi = slots.get(slots.row(stage, 1, i), (fg + i * (uint32_t)a.ldg) & 3);
-        xi = slots.get(slots.row(stage, 2, i), (fx + i * (uint32_t)a.ldx) & 3);
-        hi = slots.get(slots.row(stage, 3, i), (fh + i * (uint32_t)a.ldh) & 3);
-      } else {
-        di = rd[i];
-        gi = rg[i];
-        xi = rx[i];
-        hi = rh[i];
+    auto reduce = [&](auto flagged) {
+      #pragma unroll
+      for (int i = S - 1; i >= 0; --i) {
+        Raw4<T> di, gi, xi, hi;
+        if constexpr (D > 0) {
+          di = slots.get(slots.row(stage, 0, i), (fd + i * a.lddh) & 3);
+          gi = slots.get(slots.row(stage, 1, i), (fg + i * a.ldg) & 3);
+          xi = slots.get(slots.row(stage, 2, i), (fx + i * a.ldx) & 3);
+          hi = slots.get(slots.row(stage, 3, i), (fh + i * a.ldh) & 3);
+        } else {
+          di = rd[i];
+          gi = rg[i];
+          xi = rx[i];
+          hi = rh[i];
+        }
+        if constexpr (decltype(flagged)::value) {
+          gi = gate_or(gi, ones(now.live, i));
+          xi = masked(xi, ones(now.live, i));
+        }
+        shares_of(widen(gi), keep[i], take[i]);
+        d[i] = widen(di);
+        v[i] = widen(hi);
+        if (i == 0 && t0 == 0 && a.state && ch.any()) v[0] = ch.state(a.state + b * a.dim + ch.first);
+        if constexpr (decltype(flagged)::value) v[i] = masked(v[i], ~ones(now.starts, i));
+        v[i] = fma(widen(xi), quad(-a.mix), v[i]);
+        run.P = mul(run.P, keep[i]);
+        run.Q = fma(keep[i], run.Q, take[i]);
+        run.H = mul(keep[i], add(run.H, d[i]));
+        if constexpr (decltype(flagged)::value) {
+          const uint32_t on = ~ones(now.starts, i);
+          run.P = masked(run.P, on);
+          run.H = masked(run.H, on);
+        }
       }
-      if (FLAGS && !now.quiet) gi = gate_or(gi, ones(now.live, i));
-      shares_of(widen(gi), keep[i], take[i]);
-      d[i] = widen(di);
-      v[i] = widen(hi);
-      if (i == 0 && t0 == 0 && a.state && ch.any()) v[0] = ch.state(a.state + b * a.dim + ch.first);
-      if (FLAGS && !now.quiet) {
-        v[i] = masked(v[i], ~ones(now.starts, i));
-        xi = masked(xi, ones(now.live, i));
-      }
-      v[i] = fma(widen(xi), quad(-a.mix), v[i]);
-      run.P = mul(run.P, keep[i]);
-      run.Q = fma(keep[i], run.Q, take[i]);
-      run.H = mul(keep[i], add(run.H, d[i]));
-      if (FLAGS && !now.quiet) {
-        const uint32_t on = ~ones(now.starts, i);
-        run.P = masked(run.P, on);
-        run.H = masked(run.H, on);
-      }
-    }
+    };
+    if (FLAGS && !now.quiet) reduce(std::bool_constant<FLAGS>());
+    else reduce(std::false_type());
     run.cut = now.starts != 0;
     Quad c = join_segments<W, CL, FLAGS, true>(sh, run, round, [&] {
       if constexpr (D > 0) {
         start(stage);
-        fd -= (uint32_t)(stride * a.lddh);
-        fg -= (uint32_t)(stride * a.ldg);
-        fx -= (uint32_t)(stride * a.ldx);
-        fh -= (uint32_t)(stride * a.ldh);
+        fd -= a.lddh * (kSpan * CL);
+        fg -= a.ldg * (kSpan * CL);
+        fx -= a.ldx * (kSpan * CL);
+        fh -= a.ldh * (kSpan * CL);
         stage = stage + 1 == D ? 0 : stage + 1;
         if (FLAGS) {
           #pragma unroll
@@ -195,22 +198,36 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
     const int n = ch.any() ? inside(t0) : 0;
     T* const dx = static_cast<T*>(a.dx) + out + t0 * a.dim;
     T* const dg = static_cast<T*>(a.dgate) + out + t0 * a.dim;
-    const bool whole = n == S && a.dx && a.dgate;
-    #pragma unroll
-    for (int i = S - 1; i >= 0; --i) {
+    // what a token does with what reaches it, and what it passes on
+    auto finish = [&](int i, Quad& gx, Quad& gg) {
       const Quad l = add(d[i], c), u = mul(take[i], l);
       c = mul(keep[i], l);
-      Quad gx = mix ? u : l, gg = mul(mul(u, keep[i]), v[i]);
-      if (FLAGS && !now.quiet) {
-        const uint32_t live = ones(now.live, i);
-        gx = masked(gx, live);
-        gg = masked(gg, live);
+      gx = mix ? u : l;
+      gg = mul(mul(u, keep[i]), v[i]);
+    };
+    Quad gx, gg;
+    if (n == S && a.dx && a.dgate && (!FLAGS || now.quiet)) {
+      #pragma unroll
+      for (int i = S - 1; i >= 0; --i) {
+        finish(i, gx, gg);
+        ch.store(dx + (uint64_t)(uint32_t)a.dim * i, gx);
+        ch.store(dg + (uint64_t)(uint32_t)a.dim * i, gg);
       }
-      if (whole || (i < n && a.dx)) ch.store(dx + i * a.dim, gx);
-      if (whole || (i < n && a.dgate)) ch.store(dg + i * a.dim, gg);
-      if (FLAGS && !now.quiet) c = masked(c, ~ones(now.starts, i));
+    } else {
+      #pragma unroll
+      for (int i = S - 1; i >= 0; --i) {
+        finish(i, gx, gg);
+        if (FLAGS) {
+          const uint32_t live = ones(now.live, i);
+          gx = masked(gx, live);
+          gg = masked(gg, live);
+          c = masked(c, ~ones(now.starts, i));
+        }
+        if (i < n && a.dx) ch.store(dx + (uint64_t)(uint32_t)a.dim * i, gx);
+        if (i < n && a.dgate) ch.store(dg + (uint64_t)(uint32_t)a.dim * i, gg);
+      }
     }
-    t0 -= stride;
+    t0 -= kSpan * CL;
   }
   if (a.dstate && rank == 0) {
     __syncthreads();
@@ -229,10 +246,10 @@ scan_short_bwd_kernel(const __grid_constant__ ScanBwd a, int64_t units) {
   const int64_t b = unit / a.strips, row0 = b * a.length;
   const Channels<T, HOW> ch((int)(unit % a.strips), a.dim);
   if (!ch.any()) return;
-  const T* dh = static_cast<const T*>(a.dh) + row0 * a.lddh + ch.first;
-  const T* gate = static_cast<const T*>(a.gate) + row0 * a.ldg + ch.first;
-  const T* x = static_cast<const T*>(a.x) + row0 * a.ldx + ch.first;
-  const T* h = static_cast<const T*>(a.h) + row0 * a.ldh + ch.first;
+  const T* dh = static_cast<const T*>(a.dh) + row0 * (int64_t)a.lddh + ch.first;
+  const T* gate = static_cast<const T*>(a.gate) + row0 * (int64_t)a.ldg + ch.first;
+  const T* x = static_cast<const T*>(a.x) + row0 * (int64_t)a.ldx + ch.first;
+  const T* h = static_cast<const T*>(a.h) + row0 * (int64_t)a.ldh + ch.first;
   T* dx = static_cast<T*>(a.dx) + row0 * a.dim + ch.first;
   T* dg = static_cast<T*>(a.dgate) + row0 * a.dim + ch.first;
   const bool mix = a.mix != 0.f;
@@ -246,10 +263,10 @@ scan_short_bwd_kernel(const __grid_constant__ ScanBwd a, int64_t units) {
       if (t < 0) continue;
       zero(rx[i]);
       zero(rh[i]);
-      ch.load(rd[i], dh + t * a.lddh);
-      ch.load(rg[i], gate + t * a.ldg);
-      if (mix) ch.load(rx[i], x + t * a.ldx);
-      if (t > 0) ch.load(rh[i], h + (t - 1) * a.ldh);
+      ch.load(rd[i], dh + t * (int64_t)a.lddh);
+      ch.load(rg[i], gate + t * (int64_t)a.ldg);
+      if (mix) ch.load(rx[i], x + t * (int64_t)a.ldx);
+      if (t > 0) ch.load(rh[i], h + (t - 1) * (int64_t)a.ldh);
       if (FLAGS) {
         live[i] = !a.mask || a.mask[row0 + t];
         begins[i] = a.starts && a.starts[row0 + t];
@@ -326,6 +343,7 @@ extern "C" muon_status muon_gated_scan_backward(
   if (lddh < 0 || ldg < 0 || ldx < 0 || ldh < 0 ||
       (batch > 0 && length > 0 && (!dh || !gate || (mix && !x) || !h)))
     return MUON_ERR_INVALID_ARG;
+  if ((lddh | ldg | ldx | ldh) >> 32) return MUON_ERR_UNSUPPORTED_SHAPE;
   const size_t es = size_of(dtype);
   if (any_off(es, dh, gate, x, h, dgate, dx) || any_off(4, state, dlast, dstate))
     return MUON_ERR_ALIGNMENT;
@@ -334,7 +352,7 @@ extern "C" muon_status muon_gated_scan_backward(
   NvtxRange range("muon_gated_scan_backward");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int strips = (int)((dim + kStrip - 1) / kStrip);
-  const ScanBwd a = {length, dim, lddh, ldg, ldx, ldh, strips, mix ? 1.f : 0.f, dh, gate, x, h, state, dlast, starts,
+  const ScanBwd a = {length, dim, (uint32_t)lddh, (uint32_t)ldg, (uint32_t)ldx, (uint32_t)ldh, strips, mix ? 1.f : 0.f, dh, gate, x, h, state, dlast, starts,
                      token_mask, dgate, dx, dstate};
   const int64_t rows = batch * length, units = batch * strips;
   int how = std::max({lie(dh, rows, lddh, es), lie(gate, rows, ldg, es), lie(h, rows, ldh, es),

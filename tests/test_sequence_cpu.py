@@ -132,11 +132,13 @@ def test_scan_refusals(lib):
         for a in ("g", "x", "h"):
             assert call(lib, **{a: None}) == INVALID and call(lib, **{a: A + 1}) == ALIGN
         assert call(lib, ldg=-1) == INVALID and call(lib, ldx=-8) == INVALID
+        assert call(lib, ldg=1 << 32) == SHAPE and call(lib, ldx=1 << 32) == SHAPE
         assert call(lib, s=A + 2) == ALIGN
         assert call(lib, batch=0, g=None, x=None, h=None) == OK
     assert _scan(lib, last=A + 2) == ALIGN
     assert _scan_bwd(lib, dh=None) == INVALID and _scan_bwd(lib, dh=A + 1) == ALIGN
     assert _scan_bwd(lib, ldh=-1) == INVALID and _scan_bwd(lib, lddh=-1) == INVALID
+    assert _scan_bwd(lib, ldh=1 << 32) == SHAPE and _scan_bwd(lib, lddh=1 << 32) == SHAPE
     for a in ("dg", "dx"):
         assert _scan_bwd(lib, **{a: A + 1}) == ALIGN
     assert _scan_bwd(lib, dl=A + 2) == ALIGN and _scan_bwd(lib, ds=A + 2) == ALIGN
