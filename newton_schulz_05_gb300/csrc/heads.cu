@@ -279,19 +279,31 @@ __device__ __forceinline__ float rsqrt_fast(float x) {
 }
 
 // A lane's N pieces of a pass (one head a group of lanes) and the position of its token, in a
-// ring of kHeadRing passes that it copies, waits for and reads alone
+// ring of kHeadRing passes that it copies, waits for and reads alone.  Slots of lanes without
+// work hold zeros.
 constexpr int kHeadRing = 4;
 template <typename Raw, int N> struct HeadRing {
-  Raw* base;
-  int64_t* positions;
-  __device__ __forceinline__ explicit HeadRing(void* smem) {
+  Raw *at, *last;              // of the pass to use, and of the last one in the ring
+  int64_t* position;
+  __device__ __forceinline__ HeadRing(void* smem, bool has) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    base = static_cast<Raw*>(smem) + warp * (kHeadRing * N * 32) + lane;
-    positions = reinterpret_cast<int64_t*>(static_cast<Raw*>(smem) + kHeadWarps * (kHeadRing * N * 32)) +
-                warp * (kHeadRing * 32) + lane;
+    at = static_cast<Raw*>(smem) + warp * (kHeadRing * N * 32) + lane;
+    last = at + (kHeadRing - 1) * N * 32;
+    position = reinterpret_cast<int64_t*>(static_cast<Raw*>(smem) + kHeadWarps * (kHeadRing * N * 32)) +
+               warp * (kHeadRing * 32) + lane;
+    if (!has)
+      for (int i = 0; i < kHeadRing * N; ++i) at[i * 32] = Raw{};
   }
-  __device__ __forceinline__ Raw* slot(int stage, int n) const { return base + (stage * N + n) * 32; }
-  __device__ __forceinline__ int64_t* position(int stage) const { return positions + stage * 32; }
+  __device__ __forceinline__ Raw& piece(int n) const { return at[n * 32]; }
+  __device__ __forceinline__ void next() {
+    if (at == last) {
+      at -= (kHeadRing - 1) * N * 32;
+      position -= (kHeadRing - 1) * 32;
+    } else {
+      at += N * 32;
+      position += 32;
+    }
+  }
   static constexpr size_t kBytes = (sizeof(Raw) * N + 8) * kHeadRing * kHeadThreads;
   template <typename V> __device__ __forceinline__ static void copy(V* to, const void* p) {
     const uint32_t s = (uint32_t)__cvta_generic_to_shared(to);
@@ -300,25 +312,23 @@ template <typename Raw, int N> struct HeadRing {
   }
 };
 
-// Where a lane's group is in its walk through a side's heads
+// Where a lane's group is in its walk through heads, numbered in 32 bits
 struct HeadWalk {
-  int64_t n, all, token;
-  int head, heads;
-  int pass, run;          // of a run
-  int64_t jump;           // to the warp's next run
+  uint32_t n, all, stop;      // stop: the end of the run
+  int token, head, heads;
+  uint32_t run, jump;         // heads of a run, and from its end to that of the warp's next
   __device__ __forceinline__ void find() {
-    if (n >> 32) token = n / heads;
-    else token = (uint32_t)n / (uint32_t)heads;
-    head = (int)(n - token * heads);
+    token = (int)(n / (uint32_t)heads);
+    head = (int)(n - (uint32_t)token * (uint32_t)heads);
   }
   __device__ __forceinline__ bool live() const { return n < all; }
   // by `by` heads; whether the token may be another
   __device__ __forceinline__ bool next(int by) {
     n += by;
     head += by;
-    if (++pass == run) {
-      pass = 0;
+    if (n >= stop) {
       n += jump;
+      stop += jump + run;
     } else if (head < heads) {
       return false;
     }
@@ -328,22 +338,24 @@ struct HeadWalk {
 };
 // of a lane with work, `group` of the warp's `by`, in block `block` of `blocks`; run: passes a run;
 // passes: of the warp's runs, all of them
-__device__ __forceinline__ HeadWalk walk_of(const Heads& a, const HeadWork& w, int heads, int block, int blocks, int run,
-                                            int group, int by, bool has, int& passes) {
-  const int64_t warps = (int64_t)blocks * kHeadWarps, in_run = (int64_t)run * by;
-  const int64_t warp = (int64_t)block * kHeadWarps + (threadIdx.x >> 5);
+__device__ __forceinline__ HeadWalk walk_of(const Heads& a, int heads, int block, int blocks, int run, int group,
+                                            int by, bool has, int& passes) {
+  const uint32_t warps = (uint32_t)blocks * kHeadWarps, warp = (uint32_t)block * kHeadWarps + (threadIdx.x >> 5);
   HeadWalk k;
-  k.n = warp * in_run + group;
+  k.run = (uint32_t)(run * by);
   k.heads = heads;
-  k.all = has ? a.tokens * heads : 0;
-  k.pass = 0;
-  k.run = run;
-  k.jump = (warps - 1) * in_run;
+  const uint32_t all = (uint32_t)a.tokens * (uint32_t)heads, runs = (all + k.run - 1) / k.run;
+  k.n = warp * k.run + group;
+  k.stop = (warp + 1) * k.run;
+  k.all = has ? all : 0;
+  k.jump = (warps - 1) * k.run;
   k.find();
-  const int64_t runs = (a.tokens * heads + in_run - 1) / in_run;
   passes = warp < runs ? (int)((runs - 1 - warp) / warps + 1) * run : 0;
   return k;
 }
+// Heads that these walks can number: the last step of one goes by a run of every warp past the
+// end, at most 3648 runs of 131104 heads (under 2^29)
+constexpr int64_t kMostHeads = (int64_t)1 << 31;
 
 // the angles of the lane's pairs at a position: 1 and 0 where there are none
 template <int E, bool NB>
@@ -385,11 +397,11 @@ heads_piece_kernel(const __grid_constant__ Heads a, const __grid_constant__ Head
   if (threadIdx.x < 64) stage_weights(weights[threadIdx.x >> 5], a.side[threadIdx.x >> 5], un, w.wbf16);
   __syncthreads();
   const float inv = 1.f / (float)a.dim;
-  const HeadRing<Raw, 2> slots(ring);
+  const bool has = un.any && ln.group < ln.heads;
+  HeadRing<Raw, 2> slots(ring, has), fill = slots;
   int passes;
   const int queries = a.side[0].heads;
-  HeadWalk in = walk_of(a, w, queries + a.side[1].heads, blockIdx.x, gridDim.x, w.run[0], ln.group, ln.heads,
-                        un.any && ln.group < ln.heads, passes);
+  HeadWalk in = walk_of(a, queries + a.side[1].heads, blockIdx.x, gridDim.x, w.run[0], ln.group, ln.heads, has, passes);
   HeadWalk at = in;
   const T* px;
   T* out;
@@ -405,50 +417,48 @@ heads_piece_kernel(const __grid_constant__ Heads a, const __grid_constant__ Head
   auto seek = [&] {
     key = at.head >= queries;
     const HeadSide& side = a.side[key];
-    out = static_cast<T*>(side.out) + (at.token * side.heads + at.head - (key ? queries : 0)) * a.dim + un.a;
+    out = static_cast<T*>(side.out) + ((int64_t)at.token * side.heads + at.head - (key ? queries : 0)) * a.dim + un.a;
   };
   bool other_in = true, other = true;      // another token than in the pass before
-  auto fetch = [&](int stage) {
+  auto fetch = [&] {
     if (in.live()) {
-      slots.copy(slots.slot(stage, 0), px);
-      slots.copy(slots.slot(stage, 1), px + to_b);
-      if (other_in && a.positions) slots.copy(slots.position(stage), a.positions + in.token);
+      fill.copy(&fill.piece(0), px);
+      fill.copy(&fill.piece(1), px + to_b);
+      if (other_in && a.positions) fill.copy(fill.position, a.positions + in.token);
     }
     other_in = in.next(ln.heads);
     if (other_in || (!key_in && in.head >= queries)) seek_in();
     else px += step;
+    fill.next();
   };
   seek_in();
   seek();
   #pragma unroll
   for (int d = 0; d < kHeadRing; ++d) {
-    if (d < passes) fetch(d);
+    if (d < passes) fetch();
     copies_commit();
   }
   Piece<E> c, s;
   int64_t pos = -1;
-  int stage = 0;
   for (int i = 0; i < passes; ++i) {
     copies_wait<kHeadRing - 1>();
-    Piece<E> x, y;
-    clear(x);
-    clear(y);
     const bool live = at.live();
-    if (live) {
-      if (other) {
-        pos = !a.rotary ? 0 : a.positions ? *slots.position(stage) : at.token % a.period;
-        if (pos >= a.table && a.rotary) pos = -1;
-        angles(c, s, a, pos, un);
-      }
-      widen(x, *slots.slot(stage, 0));
-      widen(y, *slots.slot(stage, 1));
+    if (live && other) {
+      pos = !a.rotary ? 0 : a.positions ? *slots.position : at.token % a.period;
+      if (pos >= a.table && a.rotary) pos = -1;
+      angles(c, s, a, pos, un);
     }
-    if (i + kHeadRing < passes) fetch(stage);
+    Piece<E> x, y;      // of a group past the end: whatever was there, and goes nowhere
+    widen(x, slots.piece(0));
+    widen(y, slots.piece(1));
+    if (i + kHeadRing < passes) fetch();
     copies_commit();
-    stage = stage + 1 == kHeadRing ? 0 : stage + 1;
-    float2 sq = both(0.f);
+    slots.next();
+    float2 sq = mul2(x.v[0], x.v[0]);
     #pragma unroll
-    for (int j = 0; j < E / 2; ++j) sq = fma2(x.v[j], x.v[j], fma2(y.v[j], y.v[j], sq));
+    for (int j = 1; j < E / 2; ++j) sq = fma2(x.v[j], x.v[j], sq);
+    #pragma unroll
+    for (int j = 0; j < E / 2; ++j) sq = fma2(y.v[j], y.v[j], sq);
     const float rstd = rsqrt_fast(fmaf(ln.sum(sq.x + sq.y), inv, a.eps));
     if (live) {
       Raw ra = Raw{}, rb = Raw{};
@@ -488,10 +498,11 @@ heads_piece_bwd_kernel(const __grid_constant__ Heads a, const __grid_constant__ 
   if (warp == 0) stage_weights(weights, side, un, w.wbf16);
   __syncthreads();
   const float inv = 1.f / (float)a.dim;
-  const HeadRing<Raw, 4> slots(ring);
+  const bool has = un.any && ln.group < ln.heads;
+  HeadRing<Raw, 4> slots(ring, has), fill = slots;
   int passes;
-  HeadWalk in = walk_of(a, w, side.heads, (int)blockIdx.x - (key ? w.blocks[0] : 0), w.blocks[key], w.run[key],
-                        ln.group, ln.heads, un.any && ln.group < ln.heads, passes);
+  HeadWalk in = walk_of(a, side.heads, (int)blockIdx.x - (key ? w.blocks[0] : 0), w.blocks[key], w.run[key],
+                        ln.group, ln.heads, has, passes);
   HeadWalk at = in;
   const T* const x0 = static_cast<const T*>(side.x) + un.a;
   const T* const d0 = static_cast<const T*>(side.dy) + un.a;
@@ -500,13 +511,13 @@ heads_piece_bwd_kernel(const __grid_constant__ Heads a, const __grid_constant__ 
   const int to_b = un.b - un.a;
   const int64_t step = ln.heads * side.step, step_d = ln.heads * side.stepdy;
   bool other_in = true, other = true;
-  auto fetch = [&](int stage) {
+  auto fetch = [&] {
     if (in.live()) {
-      slots.copy(slots.slot(stage, 0), px);
-      slots.copy(slots.slot(stage, 1), px + to_b);
-      slots.copy(slots.slot(stage, 2), pd);
-      slots.copy(slots.slot(stage, 3), pd + to_b);
-      if (other_in && a.positions) slots.copy(slots.position(stage), a.positions + in.token);
+      fill.copy(&fill.piece(0), px);
+      fill.copy(&fill.piece(1), px + to_b);
+      fill.copy(&fill.piece(2), pd);
+      fill.copy(&fill.piece(3), pd + to_b);
+      if (other_in && a.positions) fill.copy(fill.position, a.positions + in.token);
     }
     px += step;
     pd += step_d;
@@ -515,59 +526,56 @@ heads_piece_bwd_kernel(const __grid_constant__ Heads a, const __grid_constant__ 
       px = x0 + in.token * side.ld + in.head * side.step;
       pd = d0 + in.token * side.lddy + in.head * side.stepdy;
     }
+    fill.next();
   };
   #pragma unroll
   for (int d = 0; d < kHeadRing; ++d) {
-    if (d < passes) fetch(d);
+    if (d < passes) fetch();
     copies_commit();
   }
-  T* out = static_cast<T*>(side.out) + at.n * a.dim + un.a;
+  T* const out0 = static_cast<T*>(side.out) + un.a;
   Piece<E> sa, sb, c, s;
   clear(sa);
   clear(sb);
+  clear(c);      // of lanes without work, whose zeros stay zeros
+  clear(s);
   int64_t pos = -1;
-  int stage = 0;
   for (int i = 0; i < passes; ++i) {
     copies_wait<kHeadRing - 1>();
-    Piece<E> x, y, g, h;
-    clear(x);
-    clear(y);
-    clear(g);
-    clear(h);
     const bool live = at.live();
-    if (live) {
-      if (other) {
-        pos = !a.rotary ? 0 : a.positions ? *slots.position(stage) : at.token % a.period;
-        if (pos >= a.table && a.rotary) pos = -1;
-        angles(c, s, a, pos, un);
-        #pragma unroll
-        for (int j = 0; j < E / 2; ++j) s.v[j] = make_float2(-s.v[j].x, -s.v[j].y);      // turned back
-      }
-      if (pos >= 0) {
-        widen(x, *slots.slot(stage, 0));
-        widen(y, *slots.slot(stage, 1));
-        widen(g, *slots.slot(stage, 2));
-        widen(h, *slots.slot(stage, 3));
-        turn<E, NB>(g, h, c, s);
-      }
+    if (live && other) {
+      pos = !a.rotary ? 0 : a.positions ? *slots.position : at.token % a.period;
+      if (pos >= a.table && a.rotary) pos = -1;
+      angles(c, s, a, pos, un);
+      #pragma unroll
+      for (int j = 0; j < E / 2; ++j) s.v[j] = make_float2(-s.v[j].x, -s.v[j].y);      // turned back
     }
-    if (i + kHeadRing < passes) fetch(stage);
+    const bool counts = live && pos >= 0;
+    Piece<E> x, y, g, h;
+    widen(x, slots.piece(0));
+    widen(y, slots.piece(1));
+    widen(g, slots.piece(2));
+    widen(h, slots.piece(3));
+    if (i + kHeadRing < passes) fetch();
     copies_commit();
-    stage = stage + 1 == kHeadRing ? 0 : stage + 1;
+    slots.next();
+    turn<E, NB>(g, h, c, s);
     float2 sq = both(0.f), dot = both(0.f);
     #pragma unroll
     for (int j = 0; j < E / 2; ++j) sq = fma2(x.v[j], x.v[j], fma2(y.v[j], y.v[j], sq));
-    const float ms = fmaf(ln.sum(sq.x + sq.y), inv, a.eps);
-    const float rstd = live && pos >= 0 ? rsqrt_fast(ms) : 0.f;      // not 1 / 0 where there is no head
+    const float rstd = rsqrt_fast(fmaf(ln.sum(sq.x + sq.y), inv, a.eps));
     // h = x rstd; the sums of g h; then g w in g's place
     #pragma unroll
     for (int j = 0; j < E / 2; ++j) {
       x.v[j] = mul2(x.v[j], both(rstd));
       y.v[j] = mul2(y.v[j], both(rstd));
-      sa.v[j] = fma2(g.v[j], x.v[j], sa.v[j]);
-      sb.v[j] = fma2(h.v[j], y.v[j], sb.v[j]);
     }
-    if (live) {
+    if (counts) {
+      #pragma unroll
+      for (int j = 0; j < E / 2; ++j) {
+        sa.v[j] = fma2(g.v[j], x.v[j], sa.v[j]);
+        sb.v[j] = fma2(h.v[j], y.v[j], sb.v[j]);
+      }
       Piece<E> wa;
       load_weights(wa, weights, 0);
       #pragma unroll
@@ -581,17 +589,21 @@ heads_piece_bwd_kernel(const __grid_constant__ Heads a, const __grid_constant__ 
     // dx = rstd (g w - h mean(g w h))
     const float mean = ln.sum(dot.x + dot.y) * inv;
     if (live && side.out) {
-      #pragma unroll
-      for (int j = 0; j < E / 2; ++j) {
-        x.v[j] = mul2(fma2(x.v[j], both(-mean), g.v[j]), both(rstd));
-        y.v[j] = mul2(fma2(y.v[j], both(-mean), h.v[j]), both(rstd));
+      Raw ra = Raw{}, rb = Raw{};
+      if (counts) {
+        #pragma unroll
+        for (int j = 0; j < E / 2; ++j) {
+          x.v[j] = mul2(fma2(x.v[j], both(-mean), g.v[j]), both(rstd));
+          y.v[j] = mul2(fma2(y.v[j], both(-mean), h.v[j]), both(rstd));
+        }
+        ra = pack<T>(x);
+        rb = pack<T>(y);
       }
-      *reinterpret_cast<Raw*>(out) = pack<T>(x);
-      *reinterpret_cast<Raw*>(out + to_b) = pack<T>(y);
+      T* const out = out0 + (int64_t)at.n * a.dim;
+      *reinterpret_cast<Raw*>(out) = ra;
+      *reinterpret_cast<Raw*>(out + to_b) = rb;
     }
-    const int64_t before = at.n;
     other = at.next(ln.heads);
-    out += (at.n - before) * a.dim;
   }
   if (!a.part) return;
   // the warp's groups, then the block's warps in order
@@ -664,7 +676,8 @@ muon_status check_heads(int64_t tokens, int q_heads, int k_heads, int dim, int r
 
 // Whether all heads are made of whole, aligned units of two pieces of `e` elements
 bool whole_units(const Heads& a, int e, size_t es) {
-  bool ok = a.dim % (2 * e) == 0 && a.rotary % (2 * e) == 0 && a.dim <= kPieceDim && a.dim <= 64 * e &&
+  const int64_t all = a.tokens * (a.side[0].heads + a.side[1].heads);
+  bool ok = all < kMostHeads && a.dim % (2 * e) == 0 && a.rotary % (2 * e) == 0 && a.dim <= kPieceDim && a.dim <= 64 * e &&
             !off(a.cos, 16) && !off(a.sin, 16);
   for (const HeadSide& s : a.side) {
     if (!s.heads) continue;
