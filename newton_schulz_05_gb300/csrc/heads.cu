@@ -720,6 +720,17 @@ void share_out(int64_t n, int of_token, int B, int most, int& blocks, int& run) 
   run = (int)std::min<int64_t>((of_token + B - 1) / B, of_warp);
   blocks = (int)std::min<int64_t>((passes + (int64_t)run * kHeadWarps - 1) / ((int64_t)run * kHeadWarps), most);
 }
+// Blocks of the forward pass: as many as are resident, three an SM, or up to eight times as many
+// where HBM limits it.  Resident blocks go in step, all reading and then all writing:
+// [32768, 32 + 8, 128] bf16 123 us, 104 with 3648 blocks, [8192, 16 + 16, 256] fp32 96 and 83.
+// Where it does not, the blocks' beginnings cost more than that: [16384, 12 + 12, 192] bf16 57
+// and 70.  A warp has about six passes at the least ([8192, 32 + 8, 64] fp32, with 1824 blocks
+// 28 and with 3648 33).
+int forward_blocks(const Heads& a, int B, size_t es) {
+  const int64_t heads = a.tokens * (a.side[0].heads + a.side[1].heads);
+  if (es == 2 && heads * a.dim < (int64_t)1 << 27) return 456;
+  return (int)std::max<int64_t>(456, std::min<int64_t>(3648, heads / B / (kHeadWarps * 45 / 8)));
+}
 // out of `most` blocks
 HeadWork work_of(const Heads& a, int B, int most, int wbf16) {
   HeadWork w = {{0, 0}, {1, 1}, wbf16};
@@ -771,7 +782,8 @@ extern "C" muon_status muon_norm_rotate_heads(
           constexpr int E = decltype(pe)::value, G = decltype(pg)::value;
           constexpr size_t smem = HeadRing<typename RawPiece<T, E>::type, 2>::kBytes;
           HeadWork hw = {{0, 0}, {1, 1}, wdtype == MUON_BF16};
-          share_out(tokens * (q_heads + k_heads), q_heads + k_heads, B, 152 * 3, hw.blocks[0], hw.run[0]);
+          share_out(tokens * (q_heads + k_heads), q_heads + k_heads, B, forward_blocks(a, B, sizeof(T)), hw.blocks[0],
+                    hw.run[0]);
           e = launch_k(neighbours ? heads_piece_kernel<T, E, G, true> : heads_piece_kernel<T, E, G, false>,
                        dim3(hw.blocks[0]), dim3(kHeadThreads), smem, s, true, a, hw);
         }))
