@@ -1,4 +1,19 @@
 // Norms of query and key heads with the rotation of positions, and the gradient.
+//
+// A head is read once and written once (the gradient reads two and writes one), so both are
+// bound by HBM where a head's arithmetic is short enough.  A head lies in the registers of a few
+// lanes of a warp, two pieces of 16 bytes each (8 where only those divide its parts), chosen so
+// that a pair's two elements are in one lane: its mean square is a few shuffles, its rotation
+// none.  A warp takes as many heads as fit, in passes that come through a ring of asynchronous
+// copies into shared memory; a token's angles are loaded once for its heads.  Weight gradients
+// add up in registers over all of a warp's heads, then over the block's warps, then over blocks,
+// always in the same order.  Heads of odd widths, at odd addresses, or more than 2^31 of them go
+// through kernels that move single elements, a warp a head (8 to 20% of the copy rate).
+//
+// Measured: [32768, 32 + 8, 128] bf16 104 us, 6.4 TB/s, its gradient 185 us, 5.5 TB/s; in fp32
+// [8192, 16 + 16, 256] 82 us, 6.6 TB/s, and 139 us, 5.9 TB/s; [8192, 16 + 4, 64] bf16 11.4 and
+// 21.7 us (57 and 44% of the copy rate: about 200 instructions a pass, prologue and join); one
+// token of 32 sequences 2.6 us.
 #include "sequence.cuh"
 
 #include <algorithm>
@@ -10,13 +25,15 @@ namespace {
 
 constexpr int kHeadThreads = 256, kHeadWarps = kHeadThreads / 32;
 constexpr int kHeadMaxDim = 1024;
-constexpr int kHeadParts = 304;       // blocks of the gradient, images of its weight sums
+// Blocks of the gradient and images of its weight sums, two an SM: with 152 and 608 the gradient of
+// [8191, 12 + 12, 80] fp32 takes 51 and 42 us, with these 37
+constexpr int kHeadParts = 304;
 
 // Queries or keys: heads `step` elements apart, tokens `ld`
 struct HeadSide {
   const void *x, *dy, *weight;
   int64_t ld, step, lddy, stepdy;
-  void *out, *dweight;
+  void* out;
   int heads;
 };
 struct Heads {
@@ -238,10 +255,12 @@ template <int G> struct Lanes {
   }
 };
 
-// The first blocks work on the queries, the others on the keys.  A side's heads are numbered
-// through, n = token * heads + head, and the side's warps take runs of them in turn: a run is
-// about a token, whose angles are loaded once, and what the warps read at a time lies together
-// (one long run a warp took 127 us where these take 108 for [32768, 32 + 8, 128] bf16).
+// A token's heads are numbered through, n = token * heads + head, and warps take runs of them in
+// turn: a run is about a token, and what the warps read at a time lies together.  In the forward
+// pass queries and keys are one row of heads (blocks[0] and run[0] are for both; in blocks of
+// their own they took 130 us where together they took 112, [32768, 32 + 8, 128] bf16); in the
+// gradient, with one set of weight sums a warp, the first blocks work on the queries, the others
+// on the keys.
 struct HeadWork { int blocks[2], run[2]; int wbf16; };      // run: passes
 
 // One side's weights in fp32 (1 where there are none), as the lanes of a warp need them: four at a
@@ -771,8 +790,8 @@ extern "C" muon_status muon_norm_rotate_heads(
   NvtxRange range("muon_norm_rotate_heads");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const Heads a = {tokens, table, period, dim, rotary, neighbours, eps, cos, sin, positions,
-                   {{q, nullptr, q_weight, ldq, q_step, 0, 0, q_out, nullptr, q_heads},
-                    {k, nullptr, k_weight, ldk, k_step, 0, 0, k_out, nullptr, k_heads}},
+                   {{q, nullptr, q_weight, ldq, q_step, 0, 0, q_out, q_heads},
+                    {k, nullptr, k_weight, ldk, k_step, 0, 0, k_out, k_heads}},
                    nullptr};
   const int64_t want = (tokens * (q_heads + k_heads) + kHeadWarps - 1) / kHeadWarps;
   const cudaError_t e = by_both(dtype, wdtype, [&](auto t, auto w) {
@@ -838,8 +857,8 @@ extern "C" muon_status muon_norm_rotate_heads_backward(
     return MUON_OK;
   }
   const Heads a = {tokens, table, period, dim, rotary, neighbours, eps, cos, sin, positions,
-                   {{q, dq, q_weight, ldq, q_step, lddq, dq_step, q_grad, q_dweight, q_heads},
-                    {k, dk, k_weight, ldk, k_step, lddk, dk_step, k_grad, k_dweight, k_heads}},
+                   {{q, dq, q_weight, ldq, q_step, lddq, dq_step, q_grad, q_heads},
+                    {k, dk, k_weight, ldk, k_step, lddk, dk_step, k_grad, k_heads}},
                    sums ? static_cast<float*>(workspace) : nullptr};
   const int parts = (int)head_parts(tokens, q_heads + k_heads);
   const cudaError_t e = by_both(dtype, wdtype, [&](auto t, auto w) {

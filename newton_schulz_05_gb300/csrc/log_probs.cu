@@ -5,7 +5,14 @@
 // sum of exponentials to it a thread, and the gradient reads them once more and writes
 // theirs.  A row is cut into 16-byte pieces that are aligned in memory, so a row that does
 // not start at an aligned address has parts of pieces at its ends, taken element by
-// element.
+// element.  A thread has four pieces in flight; the maximum of all of them is taken first,
+// in pairs of bf16, so that the sum is scaled once for 32 elements.
+//
+// Measured: [8192, 131072] bf16 294 us, 7.3 TB/s (reading alone is faster than a copy), the
+// gradient of three rows in four 550 us, 6.8 TB/s; [4096, 50021] 66 us and 114 us; [20000, 2048]
+// 15.5 and 29 us, 5.3 and 5.0 TB/s; one row of 262144 3.8 us in a cluster of eight blocks.
+// Few rows are uneven: 509 of 50021 fp32, a quarter of them ignored, take 15.8 us where their
+// bytes take 11.3, as the blocks of an SM end apart.
 #include <cfloat>
 
 #include "sequence.cuh"
@@ -242,6 +249,9 @@ extern "C" muon_status muon_token_log_probs(int64_t tokens, int64_t vocab, int d
   const cudaError_t e = by_type(dtype, [&](auto t) {
     using T = decltype(t);
     const int64_t turn = (int64_t)kVocabThreads * kVocabPieces * kEl<T>;      // elements of a block's turn
+    // 8 lanes a row, or a warp (65536 rows of 256 bf16: 8.1 us, 46 with a warp); from there on a
+    // block, or a cluster where blocks alone do not fill the SMs (300 rows of 50021: 9.4 us with
+    // two blocks a row, 19.3 with eight)
     auto with = vocab * 32 <= turn ? log_probs_with<T, 8, 1>
                 : vocab * 4 <= turn ? log_probs_with<T, 32, 1>
                 : tokens > 304 || vocab <= turn ? log_probs_with<T, kVocabThreads, 1>
@@ -272,6 +282,8 @@ extern "C" muon_status muon_token_log_probs_backward(int64_t tokens, int64_t voc
     using T = decltype(t);
     constexpr int E = kEl<T>;
     const int64_t lane = kVocabPieces * E;       // elements of a thread
+    // 8 lanes a unit, or a warp, where a block would be wider than the row (65536 rows of 256
+    // bf16: 16.7 us, 22.0 with a warp)
     const int tpr = vocab <= 8 * lane ? 8 : vocab <= 64 * lane ? 32 : kVocabThreads;
     const int groups = kVocabThreads / tpr;
     const int64_t ahead = vocab % E || off(dlogits, 16) ? E - 1 : 0;      // of a row in its first piece

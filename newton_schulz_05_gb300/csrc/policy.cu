@@ -1,5 +1,15 @@
 // Clipped policy loss with a KL term over the log probabilities of tokens, and
 // its gradient.
+//
+// Both passes read 12 or 16 bytes a token and a mask byte once, the gradient writes 4; what
+// they compute (two exponentials or a series of 11 terms) is near what the SMs have time for
+// meanwhile.  The forward pass leaves the sums of parts of sequences, which a cluster of blocks
+// joins into the means and the sequences' weights; few tokens are summed and joined by one
+// cluster in one launch.
+//
+// Measured: gradient of [2048, 8192] with mask and reference 57 us, 6.1 TB/s, the loss itself 52
+// us, of which the join takes about 5; [1024, 1000] 4.0 and 6.9 us; [64, 513] in one launch 6.7
+// us.
 #include "sequence.cuh"
 
 #include <cstddef>
@@ -432,6 +442,8 @@ extern "C" muon_status muon_policy_loss(int64_t batch, int64_t length, const flo
   float4* part = static_cast<float4*>(workspace);
   const PolicyOut out = {loss, kl, clipped, weights};
   cudaError_t e = cudaSuccess;
+  // One launch saves the host's time for the other, about 2 us of a call that the host bounds up
+  // to some 60 Ki tokens; beyond, eight blocks take longer ([256, 512] 11.2 us, 5 in two).
   const int64_t few = policy_chunks(length, 32);
   if (any && batch * few <= kFusedUnits) {
     e = launch_cluster(policy_kernel<32, true, kFusedThreads>, kFusedBlocks, kFusedBlocks, kFusedThreads, 0, s, a,

@@ -1,4 +1,10 @@
 // Gated linear recurrence: the forward pass.
+//
+// Bound by HBM where there are strips for all SMs, by the walk over chunks where there are few.
+// Measured: [16, 2048, 2048] bf16 72 us, 5.6 TB/s, [4, 8192, 2048] fp32 131 us, 6.2 TB/s;
+// [1, 65536, 2048] bf16 204 us, 4.0 TB/s (32 strips; 64 rounds of 3.2 us), [1, 65536, 64] 101 us
+// (one strip, 32 rounds); [3, 2047, 1409] fp32 with flags 32 us; one token of 48 x 2048 1.5 us.
+// Rows of an odd number of bf16 channels go at a third of the copy rate, in single elements.
 #include "scan.cuh"
 
 #include <algorithm>
