@@ -8,9 +8,10 @@
 // copies into shared memory; a token's angles are loaded once for its heads.  Weight gradients
 // add up in registers over all of a warp's heads, then over the block's warps, then over blocks,
 // always in the same order.  Heads of odd widths, at odd addresses, or more than 2^31 of them go
-// through kernels that move single elements, a warp a head (8 to 20% of the copy rate).
+// through kernels that move single elements, a warp a head (9 to 25% of the copy rate, the
+// gradient 5 to 13%).
 //
-// Measured: [32768, 32 + 8, 128] bf16 104 us, 6.4 TB/s, its gradient 185 us, 5.5 TB/s; in fp32
+// Measured: [32768, 32 + 8, 128] bf16 104 us, 6.4 TB/s, its gradient 193 us, 5.2 TB/s; in fp32
 // [8192, 16 + 16, 256] 82 us, 6.6 TB/s, and 139 us, 5.9 TB/s; [8192, 16 + 4, 64] bf16 11.4 and
 // 21.7 us (57 and 44% of the copy rate: about 200 instructions a pass, prologue and join); one
 // token of 32 sequences 2.6 us.

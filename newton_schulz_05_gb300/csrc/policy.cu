@@ -7,9 +7,9 @@
 // joins into the means and the sequences' weights; few tokens are summed and joined by one
 // cluster in one launch.
 //
-// Measured: gradient of [2048, 8192] with mask and reference 57 us, 6.1 TB/s, the loss itself 52
-// us, of which the join takes about 5; [1024, 1000] 4.0 and 6.9 us; [64, 513] in one launch 6.7
-// us.
+// Measured: gradient of [2048, 8192] with mask and reference 57 us, 6.1 TB/s, the loss itself 53
+// us, of which the join takes about 5; [1024, 1000] 5.0 and 8.0 us, with one advantage a sequence
+// 4.0 and 6.9; [64, 513] in one launch 6.7 us.
 #include "sequence.cuh"
 
 #include <cstddef>
@@ -443,7 +443,7 @@ extern "C" muon_status muon_policy_loss(int64_t batch, int64_t length, const flo
   const PolicyOut out = {loss, kl, clipped, weights};
   cudaError_t e = cudaSuccess;
   // One launch saves the host's time for the other, about 2 us of a call that the host bounds up
-  // to some 60 Ki tokens; beyond, eight blocks take longer ([256, 512] 11.2 us, 5 in two).
+  // to some 60 Ki tokens; beyond, eight blocks take longer ([256, 512] 11.2 us, 5.5 in two).
   const int64_t few = policy_chunks(length, 32);
   if (any && batch * few <= kFusedUnits) {
     e = launch_cluster(policy_kernel<32, true, kFusedThreads>, kFusedBlocks, kFusedBlocks, kFusedThreads, 0, s, a,

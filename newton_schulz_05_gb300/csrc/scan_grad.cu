@@ -3,7 +3,7 @@
 //
 // Measured: [8, 4096, 4096] bf16 with starts 292 us, 5.5 TB/s; [4, 8192, 2048] fp32 259 us, 6.2
 // TB/s; [142, 4255, 64] bf16 77 us, 6.0 TB/s; [2, 8192, 2048] bf16 93 us, 4.3 TB/s.  The larger
-// ones are bound by instructions: 45 an element in 16 bits, a third of them joins.
+// ones are bound by instructions: 43 an element in 16 bits, a third of them joins.
 #include "scan.cuh"
 
 #include <algorithm>
