@@ -67,7 +67,8 @@ scan_kernel(const __grid_constant__ Scan a) {
   if (threadIdx.x < 16)
     sh.carry[0][threadIdx.x] = four(a.state ? ch.state(a.state + b * a.dim + ch.first) : quad(0.f));
   const Ring<T, HOW, 2, S, W> slots(ring, ch, a.dim);
-  // elements of the segment's first row ahead of the strip, in the chunk to use next
+  // elements of the segment's first row ahead of the strip, the same in every chunk
+  static_assert(kSpan % 4 == 0 || D == 0);
   uint32_t fg = HOW != kSingles ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(gate) / sizeof(T));
   uint32_t fx = HOW != kSingles ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(x) / sizeof(T));
   Flags ahead[D > 0 ? D : 1];
@@ -135,8 +136,8 @@ scan_kernel(const __grid_constant__ Scan a) {
       for (int i = 0; i < S; ++i) {
         Raw4<T> gi, vi;
         if constexpr (D > 0) {
-          gi = slots.get(slots.row(stage, 0, i), (fg + i * a.ldg) & 3);
-          vi = slots.get(slots.row(stage, 1, i), (fx + i * a.ldx) & 3);
+          gi = slots.get(slots.row(stage, 0, i), (fg + (i & 3) * a.ldg) & 3);
+          vi = slots.get(slots.row(stage, 1, i), (fx + (i & 3) * a.ldx) & 3);
         } else {
           gi = rg[i];
           vi = rx[i];
@@ -160,8 +161,6 @@ scan_kernel(const __grid_constant__ Scan a) {
     Quad front = join_segments<W, CL, FLAGS, false>(sh, run, round, [&] {
       if constexpr (D > 0) {
         start(stage);
-        fg += a.ldg * (kSpan * CL);
-        fx += a.ldx * (kSpan * CL);
         stage = stage + 1 == D ? 0 : stage + 1;
         if (FLAGS) {
           #pragma unroll

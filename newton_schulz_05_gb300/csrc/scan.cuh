@@ -192,9 +192,11 @@ template <typename T, int HOW> struct Channels {
 // Rows of N operands on their way through shared memory: D chunks, S tokens a segment, 2 W
 // segments.  A lane copies the piece or the pairs that it reads.  Singles are copied by the half
 // warp that reads the row, in aligned pieces of four, the first of which may begin up to three
-// elements ahead of the row, and one more: only pieces that hold an element of the row are read,
-// and an aligned 8 or 16 bytes lie wholly in the allocation that one of them does.  (Copies of
-// single fp32 elements took 179 us for [8, 4096, 1409] where these take 155.)
+// elements ahead of the row and the last end up to three behind it, and one more: only pieces that
+// hold an element of the row are read, and an aligned 8 or 16 bytes lie wholly in the allocation
+// that one of them does.  (Copies of single fp32 elements took 179 us for [8, 4096, 1409] where
+// these take 155.)  How far a row is ahead of its first piece depends on the row's number modulo
+// four alone, and the chunks of a block are a multiple of four rows apart.
 template <typename T, int HOW, int N, int S, int W> struct Ring {
   static constexpr int kRow = HOW == kSingles ? 17 : 16;
   static constexpr size_t kStage = sizeof(Raw4<T>) * N * S * 2 * W * kRow;
@@ -216,10 +218,12 @@ template <typename T, int HOW, int N, int S, int W> struct Ring {
       if (ch.has(0)) piece<4>(to + l, p);
       if (ch.has(2)) piece<4>(reinterpret_cast<uint32_t*>(to + l) + 1, p + 32);
     } else {
-      const int f = (int)(reinterpret_cast<uintptr_t>(p) / sizeof(T) & 3);
-      const int first = 4 * l - f, inside = left - first;
-      if (inside > 0) part(to + l, p + first, (int)sizeof(T) * (inside < 4 ? inside : 4));
-      if (l == 0 && f > 0 && left > 64 - f) part(to + 16, p + 64 - f, (int)sizeof(T) * (left - (64 - f)));
+      const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+      const uint32_t f = (uint32_t)at & (4 * sizeof(T) - 1);
+      const int end = left * (int)sizeof(T) + (int)f;       // of the strip, in bytes from its first piece on
+      const T* first = reinterpret_cast<const T*>(at - f);
+      if (4 * l * (int)sizeof(T) < end) piece<4 * sizeof(T)>(to + l, first + 4 * l);
+      if (l == 15 && end > kStrip * (int)sizeof(T)) piece<4 * sizeof(T)>(to + 16, first + kStrip);
     }
   }
   template <int BYTES> static __device__ __forceinline__ void piece(void* to, const T* p) {
@@ -228,14 +232,6 @@ template <typename T, int HOW, int N, int S, int W> struct Ring {
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(s), "l"(p) : "memory");
     else
       asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(s), "l"(p), "n"(BYTES) : "memory");
-  }
-  // the first `bytes` of an aligned piece of four
-  static __device__ __forceinline__ void part(Raw4<T>* to, const T* p, int bytes) {
-    const uint32_t s = (uint32_t)__cvta_generic_to_shared(to);
-    if constexpr (sizeof(T) == 2)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(s), "l"(p), "r"(bytes) : "memory");
-    else
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(p), "r"(bytes) : "memory");
   }
   // every element of a row
   __device__ __forceinline__ void fill(Raw4<T>* to, bool gate) const {

@@ -65,9 +65,10 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
   if (threadIdx.x < 16)
     sh.carry[0][threadIdx.x] = four(a.dlast ? ch.state(a.dlast + b * a.dim + ch.first) : quad(0.f));
   const Ring<T, HOW, 4, S, W> slots(ring, ch, a.dim);
-  // elements of the segment's first row ahead of the strip, in the chunk to use next
+  // elements of the segment's first row ahead of the strip, the same in every chunk
+  static_assert(kSpan % 4 == 0 || D == 0);
   auto ahead_of = [](const T* p) { return HOW != kSingles ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(p) / sizeof(T)); };
-  uint32_t fd = ahead_of(dh), fg = ahead_of(gate), fx = ahead_of(x), fh = ahead_of(h);
+  const uint32_t fd = ahead_of(dh), fg = ahead_of(gate), fx = ahead_of(x), fh = ahead_of(h);
   Flags ahead[D > 0 ? D : 1];
   auto ask_next = [&] { return ask<S>(a.starts, a.mask, row0, t_in, length); };
   auto advance = [&] {
@@ -150,10 +151,10 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
       for (int i = S - 1; i >= 0; --i) {
         Raw4<T> di, gi, xi, hi;
         if constexpr (D > 0) {
-          di = slots.get(slots.row(stage, 0, i), (fd + i * a.lddh) & 3);
-          gi = slots.get(slots.row(stage, 1, i), (fg + i * a.ldg) & 3);
-          xi = slots.get(slots.row(stage, 2, i), (fx + i * a.ldx) & 3);
-          hi = slots.get(slots.row(stage, 3, i), (fh + i * a.ldh) & 3);
+          di = slots.get(slots.row(stage, 0, i), (fd + (i & 3) * a.lddh) & 3);
+          gi = slots.get(slots.row(stage, 1, i), (fg + (i & 3) * a.ldg) & 3);
+          xi = slots.get(slots.row(stage, 2, i), (fx + (i & 3) * a.ldx) & 3);
+          hi = slots.get(slots.row(stage, 3, i), (fh + (i & 3) * a.ldh) & 3);
         } else {
           di = rd[i];
           gi = rg[i];
@@ -186,10 +187,6 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
     Quad c = join_segments<W, CL, FLAGS, true>(sh, run, round, [&] {
       if constexpr (D > 0) {
         start(stage);
-        fd -= a.lddh * (kSpan * CL);
-        fg -= a.ldg * (kSpan * CL);
-        fx -= a.ldx * (kSpan * CL);
-        fh -= a.ldh * (kSpan * CL);
         stage = stage + 1 == D ? 0 : stage + 1;
         if (FLAGS) {
           #pragma unroll
