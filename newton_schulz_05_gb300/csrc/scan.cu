@@ -2,9 +2,10 @@
 //
 // Bound by HBM where there are strips for all SMs, by the walk over chunks where there are few.
 // Measured: [16, 2048, 2048] bf16 72 us, 5.6 TB/s, [4, 8192, 2048] fp32 131 us, 6.2 TB/s;
-// [1, 65536, 2048] bf16 204 us, 4.0 TB/s (32 strips; 64 rounds of 3.2 us), [1, 65536, 64] 101 us
+// [1, 65536, 2048] bf16 205 us, 4.0 TB/s (32 strips; 64 rounds of 3.2 us), [1, 65536, 64] 101 us
 // (one strip, 32 rounds); [3, 2047, 1409] fp32 with flags 32 us; one token of 48 x 2048 1.5 us.
-// Rows of an odd number of bf16 channels go at a third of the copy rate, in single elements.
+// Rows of an odd number of bf16 channels are stored in single elements and read in pieces from
+// any address: [4, 4096, 2047] 58 us, its gradient 115, where 2048 channels take 39 and 69.
 #include "scan.cuh"
 
 #include <algorithm>
@@ -56,6 +57,7 @@ scan_kernel(const __grid_constant__ Scan a) {
   const int64_t row0 = b * a.length;
   const int seg = threadIdx.x >> 4, length = (int)a.length;
   const int64_t stride = (int64_t)kSpan * CL;
+  const int rounds = (int)((a.length + stride - 1) / stride);
   // the chunk to read next, at the strip's first channel or at the lane's, and the one to write
   const int channel = D > 0 && HOW != kPairs ? ch.strip : ch.first;
   const T* gate = static_cast<const T*>(a.gate) + (row0 + rank * kSpan) * (int64_t)a.ldg + channel;
@@ -67,10 +69,8 @@ scan_kernel(const __grid_constant__ Scan a) {
   if (threadIdx.x < 16)
     sh.carry[0][threadIdx.x] = four(a.state ? ch.state(a.state + b * a.dim + ch.first) : quad(0.f));
   const Ring<T, HOW, 2, S, W> slots(ring, ch, a.dim);
-  // elements of the segment's first row ahead of the strip, the same in every chunk
-  static_assert(kSpan % 4 == 0 || D == 0);
-  uint32_t fg = HOW != kSingles ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(gate) / sizeof(T));
-  uint32_t fx = HOW != kSingles ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(x) / sizeof(T));
+  static_assert(kSpan % slots.kPiece == 0 || D == 0, "a row is as far ahead of its piece in every chunk");
+  const T *const gate0 = gate, *const x0 = x;
   Flags ahead[D > 0 ? D : 1];
   auto ask_next = [&] { return ask<S>(a.starts, a.mask, row0, a.length - left_in, length); };
   auto advance = [&] {
@@ -82,32 +82,27 @@ scan_kernel(const __grid_constant__ Scan a) {
     slots.arrived();
     if (left_in >= S) {
       #pragma unroll
-      for (int i = 0; i < S; ++i) {
-        slots.copy(slots.row(stage, 0, i), gate + (uint64_t)a.ldg * i);
-        slots.copy(slots.row(stage, 1, i), x + (uint64_t)a.ldx * i);
+      for (int i = 0; i < S; i += slots.kAtOnce) {
+        slots.copy(stage, 0, gate, a.ldg, i, 0, S);
+        slots.copy(stage, 1, x, a.ldx, i, 0, S);
       }
+      slots.copy_ends(stage, 0, gate, a.ldg, 0, S);
+      slots.copy_ends(stage, 1, x, a.ldx, 0, S);
     } else {
-      for (int i = 0; i < S; ++i) {
-        if (i < left_in) {
-          slots.copy(slots.row(stage, 0, i), gate + (uint64_t)a.ldg * i);
-          slots.copy(slots.row(stage, 1, i), x + (uint64_t)a.ldx * i);
-        } else {
-          slots.fill(slots.row(stage, 0, i), true);
-          slots.fill(slots.row(stage, 1, i), false);
-        }
-      }
+      slots.copy_some(stage, 0, gate, a.ldg, 0, left_in, true);
+      slots.copy_some(stage, 1, x, a.ldx, 0, left_in, false);
     }
     copies_commit();
   };
   #pragma unroll
   for (int d = 0; d < D; ++d) {
-    start(d);
+    if (d < rounds) start(d);
+    else copies_commit();
     if (FLAGS) ahead[d] = ask_next();
     advance();
   }
   if (CL > 1) cluster_barrier();      // every block has begun before one writes to another
   int stage = 0;
-  const int rounds = (int)((a.length + stride - 1) / stride);
   for (int round = 0; round < rounds; ++round) {
     Raw4<T> rg[S], rx[S];
     if constexpr (D > 0) {
@@ -136,8 +131,8 @@ scan_kernel(const __grid_constant__ Scan a) {
       for (int i = 0; i < S; ++i) {
         Raw4<T> gi, vi;
         if constexpr (D > 0) {
-          gi = slots.get(slots.row(stage, 0, i), (fg + (i & 3) * a.ldg) & 3);
-          vi = slots.get(slots.row(stage, 1, i), (fx + (i & 3) * a.ldx) & 3);
+          gi = slots.get(slots.row(stage, 0, i), slots.ahead(gate0, a.ldg, i));
+          vi = slots.get(slots.row(stage, 1, i), slots.ahead(x0, a.ldx, i));
         } else {
           gi = rg[i];
           vi = rx[i];
@@ -160,7 +155,8 @@ scan_kernel(const __grid_constant__ Scan a) {
     run.cut = now.starts != 0;
     Quad front = join_segments<W, CL, FLAGS, false>(sh, run, round, [&] {
       if constexpr (D > 0) {
-        start(stage);
+        if (round + D < rounds) start(stage);
+        else copies_commit();      // an empty group, for the count of those in flight
         stage = stage + 1 == D ? 0 : stage + 1;
         if (FLAGS) {
           #pragma unroll

@@ -191,15 +191,18 @@ template <typename T, int HOW> struct Channels {
 
 // Rows of N operands on their way through shared memory: D chunks, S tokens a segment, 2 W
 // segments.  A lane copies the piece or the pairs that it reads.  Singles are copied by the half
-// warp that reads the row, in aligned pieces of four, the first of which may begin up to three
-// elements ahead of the row and the last end up to three behind it, and one more: only pieces that
-// hold an element of the row are read, and an aligned 8 or 16 bytes lie wholly in the allocation
-// that one of them does.  (Copies of single fp32 elements took 179 us for [8, 4096, 1409] where
-// these take 155.)  How far a row is ahead of its first piece depends on the row's number modulo
-// four alone, and the chunks of a block are a multiple of four rows apart.
+// warp that reads their rows, in aligned pieces of 16 bytes, the first of which may begin ahead of
+// the row and the last end behind it: only pieces that hold an element of the row are read, and an
+// aligned 16 bytes lie wholly in the allocation that one of them does.  A lane's row then gets the
+// piece behind its last whole one.  (Copies of single fp32 elements took 179 us for [8, 4096, 1409]
+// where these take 153.)  How far a row is ahead of its first piece depends on its number
+// modulo kPiece alone, and the chunks of a block are a multiple of that apart.
 template <typename T, int HOW, int N, int S, int W> struct Ring {
-  static constexpr int kRow = HOW == kSingles ? 17 : 16;
+  static constexpr int kPiece = HOW == kSingles ? 16 / (int)sizeof(T) : 4;      // elements
+  static constexpr int kLanes = kStrip / kPiece, kAtOnce = HOW == kPairs ? 1 : 16 / kLanes;   // of a row; rows
+  static constexpr int kRow = 16 + (HOW == kSingles ? kPiece / 4 : 0);
   static constexpr size_t kStage = sizeof(Raw4<T>) * N * S * 2 * W * kRow;
+  static_assert(S <= 16, "a lane a row");
   Raw4<T>* base;
   const Channels<T, HOW>& ch;
   int left;         // channels of the strip
@@ -209,24 +212,57 @@ template <typename T, int HOW, int N, int S, int W> struct Ring {
   __device__ __forceinline__ Raw4<T>* row(int stage, int operand, int i) const {
     return base + ((stage * N + operand) * S + i) * (2 * W * kRow);
   }
-  // p: the strip's first channel in the row, for pairs the lane's
-  __device__ __forceinline__ void copy(Raw4<T>* to, const T* p) const {
-    const int l = threadIdx.x & 15;
+  // of a segment's rows from..n - 1, those of i to i + kAtOnce - 1; p: the strip's first channel in
+  // row 0, for pairs the lane's
+  __device__ __forceinline__ void copy(int stage, int operand, const T* p, uint32_t ld, int i, int from, int n) const {
+    const int l = threadIdx.x & 15, mine = l & (kLanes - 1);
+    if (kAtOnce > 1) i += l / kLanes;
+    if (i < from || i >= n) return;
+    p += (uint64_t)ld * i;
+    Raw4<T>* to = row(stage, operand, i);
     if constexpr (HOW == kFours) {
-      if (4 * l < left) piece<4 * sizeof(T)>(to + l, p + 4 * l);
+      if (4 * l < left) put<4 * sizeof(T)>(to + l, p + 4 * l);
     } else if constexpr (HOW == kPairs) {
-      if (ch.has(0)) piece<4>(to + l, p);
-      if (ch.has(2)) piece<4>(reinterpret_cast<uint32_t*>(to + l) + 1, p + 32);
+      if (ch.has(0)) put<4>(to + l, p);
+      if (ch.has(2)) put<4>(reinterpret_cast<uint32_t*>(to + l) + 1, p + 32);
     } else {
-      const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-      const uint32_t f = (uint32_t)at & (4 * sizeof(T) - 1);
-      const int end = left * (int)sizeof(T) + (int)f;       // of the strip, in bytes from its first piece on
-      const T* first = reinterpret_cast<const T*>(at - f);
-      if (4 * l * (int)sizeof(T) < end) piece<4 * sizeof(T)>(to + l, first + 4 * l);
-      if (l == 15 && end > kStrip * (int)sizeof(T)) piece<4 * sizeof(T)>(to + 16, first + kStrip);
+      const Pieces s(p);
+      if (kPiece * mine < left + s.ahead) put<16>(to + mine * (kPiece / 4), s.first + kPiece * mine);
     }
   }
-  template <int BYTES> static __device__ __forceinline__ void piece(void* to, const T* p) {
+  // the last pieces of rows from..n - 1, a lane a row
+  __device__ __forceinline__ void copy_ends(int stage, int operand, const T* p, uint32_t ld, int from, int n) const {
+    if constexpr (HOW == kSingles) {
+      const int i = threadIdx.x & 15;
+      if (i < from || i >= min(S, n)) return;
+      const Pieces s(p + (uint64_t)ld * i);
+      if (left + s.ahead > kStrip) put<16>(row(stage, operand, i) + 16, s.first + kStrip);
+    }
+  }
+  // rows from..n - 1, and the others as tokens that change nothing
+  __device__ __forceinline__ void copy_some(int stage, int operand, const T* p, uint32_t ld, int from, int n,
+                                            bool gate) const {
+    for (int i = 0; i < S; i += kAtOnce) copy(stage, operand, p, ld, i, from, n);
+    copy_ends(stage, operand, p, ld, from, n);
+    for (int i = 0; i < S; ++i)
+      if (i < from || i >= n) fill(row(stage, operand, i), gate);
+  }
+  // where the aligned pieces of a strip's row begin, and how many elements ahead of it
+  struct Pieces {
+    const T* first;
+    int ahead;
+    __device__ __forceinline__ Pieces(const T* p) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+      first = reinterpret_cast<const T*>(at & ~(uintptr_t)15);
+      ahead = (int)((uint32_t)at / sizeof(T) & (kPiece - 1));
+    }
+  };
+  // elements of row i ahead of the strip, of a segment whose row 0 is at p
+  static __device__ __forceinline__ uint32_t ahead(const T* p, uint32_t ld, int i) {
+    return HOW != kSingles ? 0 : ((uint32_t)(reinterpret_cast<uintptr_t>(p) / sizeof(T)) + (i & (kPiece - 1)) * ld) &
+                                     (kPiece - 1);
+  }
+  template <int BYTES> static __device__ __forceinline__ void put(void* to, const T* p) {
     const uint32_t s = (uint32_t)__cvta_generic_to_shared(to);
     if constexpr (BYTES == 16)
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(s), "l"(p) : "memory");
@@ -240,7 +276,7 @@ template <typename T, int HOW, int N, int S, int W> struct Ring {
     if (gate) infinite(v);
     else zero(v);
     to[l] = v;
-    if (HOW == kSingles && l == 0) to[16] = v;
+    if (HOW == kSingles && l < kRow - 16) to[16 + l] = v;
   }
   // the lane's channels; f: the row's elements ahead of the strip
   __device__ __forceinline__ Raw4<T> get(const Raw4<T>* from, int f) const {

@@ -65,10 +65,8 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
   if (threadIdx.x < 16)
     sh.carry[0][threadIdx.x] = four(a.dlast ? ch.state(a.dlast + b * a.dim + ch.first) : quad(0.f));
   const Ring<T, HOW, 4, S, W> slots(ring, ch, a.dim);
-  // elements of the segment's first row ahead of the strip, the same in every chunk
-  static_assert(kSpan % 4 == 0 || D == 0);
-  auto ahead_of = [](const T* p) { return HOW != kSingles ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(p) / sizeof(T)); };
-  const uint32_t fd = ahead_of(dh), fg = ahead_of(gate), fx = ahead_of(x), fh = ahead_of(h);
+  static_assert(kSpan % slots.kPiece == 0 || D == 0, "a row is as far ahead of its piece in every chunk");
+  const T *const dh0 = dh, *const gate0 = gate, *const x0 = x, *const h0 = h;
   Flags ahead[D > 0 ? D : 1];
   auto ask_next = [&] { return ask<S>(a.starts, a.mask, row0, t_in, length); };
   auto advance = [&] {
@@ -85,36 +83,28 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
     slots.arrived();
     if (n == S && t_in > 0 && mix) {
       #pragma unroll
-      for (int i = 0; i < S; ++i) {
-        slots.copy(slots.row(stage, 0, i), dh + (uint64_t)a.lddh * i);
-        slots.copy(slots.row(stage, 1, i), gate + (uint64_t)a.ldg * i);
-        slots.copy(slots.row(stage, 2, i), x + (uint64_t)a.ldx * i);
-        slots.copy(slots.row(stage, 3, i), h + (uint64_t)a.ldh * i);
+      for (int i = 0; i < S; i += slots.kAtOnce) {
+        slots.copy(stage, 0, dh, a.lddh, i, 0, S);
+        slots.copy(stage, 1, gate, a.ldg, i, 0, S);
+        slots.copy(stage, 2, x, a.ldx, i, 0, S);
+        slots.copy(stage, 3, h, a.ldh, i, 0, S);
       }
+      slots.copy_ends(stage, 0, dh, a.lddh, 0, S);
+      slots.copy_ends(stage, 1, gate, a.ldg, 0, S);
+      slots.copy_ends(stage, 2, x, a.ldx, 0, S);
+      slots.copy_ends(stage, 3, h, a.ldh, 0, S);
     } else {
-      for (int i = 0; i < S; ++i) {
-        Raw4<T>* const to[4] = {slots.row(stage, 0, i), slots.row(stage, 1, i), slots.row(stage, 2, i),
-                                slots.row(stage, 3, i)};
-        if (i < n) {
-          slots.copy(to[0], dh + (uint64_t)a.lddh * i);
-          slots.copy(to[1], gate + (uint64_t)a.ldg * i);
-          if (mix) slots.copy(to[2], x + (uint64_t)a.ldx * i);
-          else slots.fill(to[2], false);
-          if (i > 0 || t_in > 0) slots.copy(to[3], h + (uint64_t)a.ldh * i);
-          else slots.fill(to[3], false);
-        } else {
-          slots.fill(to[0], false);
-          slots.fill(to[1], true);
-          slots.fill(to[2], false);
-          slots.fill(to[3], false);
-        }
-      }
+      slots.copy_some(stage, 0, dh, a.lddh, 0, n, false);
+      slots.copy_some(stage, 1, gate, a.ldg, 0, n, true);
+      slots.copy_some(stage, 2, x, a.ldx, 0, mix ? n : 0, false);
+      slots.copy_some(stage, 3, h, a.ldh, t_in > 0 ? 0 : 1, n, false);
     }
     copies_commit();
   };
   #pragma unroll
   for (int d = 0; d < D; ++d) {
-    start(d);
+    if (d < rounds) start(d);
+    else copies_commit();
     if (FLAGS) ahead[d] = ask_next();
     advance();
   }
@@ -151,10 +141,10 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
       for (int i = S - 1; i >= 0; --i) {
         Raw4<T> di, gi, xi, hi;
         if constexpr (D > 0) {
-          di = slots.get(slots.row(stage, 0, i), (fd + (i & 3) * a.lddh) & 3);
-          gi = slots.get(slots.row(stage, 1, i), (fg + (i & 3) * a.ldg) & 3);
-          xi = slots.get(slots.row(stage, 2, i), (fx + (i & 3) * a.ldx) & 3);
-          hi = slots.get(slots.row(stage, 3, i), (fh + (i & 3) * a.ldh) & 3);
+          di = slots.get(slots.row(stage, 0, i), slots.ahead(dh0, a.lddh, i));
+          gi = slots.get(slots.row(stage, 1, i), slots.ahead(gate0, a.ldg, i));
+          xi = slots.get(slots.row(stage, 2, i), slots.ahead(x0, a.ldx, i));
+          hi = slots.get(slots.row(stage, 3, i), slots.ahead(h0, a.ldh, i));
         } else {
           di = rd[i];
           gi = rg[i];
@@ -186,7 +176,8 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
     run.cut = now.starts != 0;
     Quad c = join_segments<W, CL, FLAGS, true>(sh, run, round, [&] {
       if constexpr (D > 0) {
-        start(stage);
+        if (round + D < rounds) start(stage);
+        else copies_commit();      // an empty group, for the count of those in flight
         stage = stage + 1 == D ? 0 : stage + 1;
         if (FLAGS) {
           #pragma unroll
