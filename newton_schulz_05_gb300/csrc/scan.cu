@@ -5,7 +5,8 @@
 // [1, 65536, 2048] bf16 205 us, 4.0 TB/s (32 strips; 64 rounds of 3.2 us), [1, 65536, 64] 101 us
 // (one strip, 32 rounds); [3, 2047, 1409] fp32 with flags 32 us; one token of 48 x 2048 1.5 us.
 // Rows of an odd number of bf16 channels are stored in single elements and read in pieces from
-// any address: [4, 4096, 2047] 58 us, its gradient 115, where 2048 channels take 39 and 69.
+// any address: [4, 4096, 2047] 58 us, its gradient 115, where 2046 channels, in pairs, take 50 and
+// 95, and 2048 take 39 and 69.
 #include "scan.cuh"
 
 #include <algorithm>
@@ -59,7 +60,7 @@ scan_kernel(const __grid_constant__ Scan a) {
   const int64_t stride = (int64_t)kSpan * CL;
   const int rounds = (int)((a.length + stride - 1) / stride);
   // the chunk to read next, at the strip's first channel or at the lane's, and the one to write
-  const int channel = D > 0 && HOW != kPairs ? ch.strip : ch.first;
+  const int channel = D > 0 ? ch.strip : ch.first;
   const T* gate = static_cast<const T*>(a.gate) + (row0 + rank * kSpan) * (int64_t)a.ldg + channel;
   const T* x = static_cast<const T*>(a.x) + (row0 + rank * kSpan) * (int64_t)a.ldx + channel;
   T* h = static_cast<T*>(a.h) + (row0 + rank * kSpan + seg * S) * a.dim + ch.first;
@@ -68,7 +69,7 @@ scan_kernel(const __grid_constant__ Scan a) {
   x += seg * S * (int64_t)a.ldx;
   if (threadIdx.x < 16)
     sh.carry[0][threadIdx.x] = four(a.state ? ch.state(a.state + b * a.dim + ch.first) : quad(0.f));
-  const Ring<T, HOW, 2, S, W> slots(ring, ch, a.dim);
+  const Ring<T, HOW, 2, S, W> slots(ring, ch.strip, a.dim);
   static_assert(kSpan % slots.kPiece == 0 || D == 0, "a row is as far ahead of its piece in every chunk");
   const T *const gate0 = gate, *const x0 = x;
   Flags ahead[D > 0 ? D : 1];

@@ -190,7 +190,7 @@ template <typename T, int HOW> struct Channels {
 };
 
 // Rows of N operands on their way through shared memory: D chunks, S tokens a segment, 2 W
-// segments.  A lane copies the piece or the pairs that it reads.  Singles are copied by the half
+// segments.  A lane copies the piece of four that it reads.  Pairs and singles are copied by the half
 // warp that reads their rows, in aligned pieces of 16 bytes, the first of which may begin ahead of
 // the row and the last end behind it: only pieces that hold an element of the row are read, and an
 // aligned 16 bytes lie wholly in the allocation that one of them does.  A lane's row then gets the
@@ -198,22 +198,21 @@ template <typename T, int HOW> struct Channels {
 // where these take 153.)  How far a row is ahead of its first piece depends on its number
 // modulo kPiece alone, and the chunks of a block are a multiple of that apart.
 template <typename T, int HOW, int N, int S, int W> struct Ring {
-  static constexpr int kPiece = HOW == kSingles ? 16 / (int)sizeof(T) : 4;      // elements
-  static constexpr int kLanes = kStrip / kPiece, kAtOnce = HOW == kPairs ? 1 : 16 / kLanes;   // of a row; rows
-  static constexpr int kRow = 16 + (HOW == kSingles ? kPiece / 4 : 0);
+  static constexpr int kPiece = HOW != kFours ? 16 / (int)sizeof(T) : 4;      // elements
+  static constexpr int kLanes = kStrip / kPiece, kAtOnce = 16 / kLanes;   // of a row; rows
+  static constexpr int kRow = 16 + (HOW != kFours ? kPiece / 4 : 0);
   static constexpr size_t kStage = sizeof(Raw4<T>) * N * S * 2 * W * kRow;
   static_assert(S <= 16, "a lane a row");
   Raw4<T>* base;
-  const Channels<T, HOW>& ch;
   int left;         // channels of the strip
-  __device__ __forceinline__ Ring(void* smem, const Channels<T, HOW>& ch, int64_t dim)
-      : base(static_cast<Raw4<T>*>(smem) + (threadIdx.x >> 4) * kRow), ch(ch),
-        left(min(kStrip, (int)dim - ch.strip)) {}
+  __device__ __forceinline__ Ring(void* smem, int strip, int64_t dim)
+      : base(static_cast<Raw4<T>*>(smem) + (threadIdx.x >> 4) * kRow),
+        left(min(kStrip, (int)dim - strip)) {}
   __device__ __forceinline__ Raw4<T>* row(int stage, int operand, int i) const {
     return base + ((stage * N + operand) * S + i) * (2 * W * kRow);
   }
   // of a segment's rows from..n - 1, those of i to i + kAtOnce - 1; p: the strip's first channel in
-  // row 0, for pairs the lane's
+  // row 0
   __device__ __forceinline__ void copy(int stage, int operand, const T* p, uint32_t ld, int i, int from, int n) const {
     const int l = threadIdx.x & 15, mine = l & (kLanes - 1);
     if (kAtOnce > 1) i += l / kLanes;
@@ -222,9 +221,6 @@ template <typename T, int HOW, int N, int S, int W> struct Ring {
     Raw4<T>* to = row(stage, operand, i);
     if constexpr (HOW == kFours) {
       if (4 * l < left) put<4 * sizeof(T)>(to + l, p + 4 * l);
-    } else if constexpr (HOW == kPairs) {
-      if (ch.has(0)) put<4>(to + l, p);
-      if (ch.has(2)) put<4>(reinterpret_cast<uint32_t*>(to + l) + 1, p + 32);
     } else {
       const Pieces s(p);
       if (kPiece * mine < left + s.ahead) put<16>(to + mine * (kPiece / 4), s.first + kPiece * mine);
@@ -232,7 +228,7 @@ template <typename T, int HOW, int N, int S, int W> struct Ring {
   }
   // the last pieces of rows from..n - 1, a lane a row
   __device__ __forceinline__ void copy_ends(int stage, int operand, const T* p, uint32_t ld, int from, int n) const {
-    if constexpr (HOW == kSingles) {
+    if constexpr (HOW != kFours) {
       const int i = threadIdx.x & 15;
       if (i < from || i >= min(S, n)) return;
       const Pieces s(p + (uint64_t)ld * i);
@@ -259,7 +255,7 @@ template <typename T, int HOW, int N, int S, int W> struct Ring {
   };
   // elements of row i ahead of the strip, of a segment whose row 0 is at p
   static __device__ __forceinline__ uint32_t ahead(const T* p, uint32_t ld, int i) {
-    return HOW != kSingles ? 0 : ((uint32_t)(reinterpret_cast<uintptr_t>(p) / sizeof(T)) + (i & (kPiece - 1)) * ld) &
+    return HOW == kFours ? 0 : ((uint32_t)(reinterpret_cast<uintptr_t>(p) / sizeof(T)) + (i & (kPiece - 1)) * ld) &
                                      (kPiece - 1);
   }
   template <int BYTES> static __device__ __forceinline__ void put(void* to, const T* p) {
@@ -276,13 +272,16 @@ template <typename T, int HOW, int N, int S, int W> struct Ring {
     if (gate) infinite(v);
     else zero(v);
     to[l] = v;
-    if (HOW == kSingles && l < kRow - 16) to[16 + l] = v;
+    if (l < kRow - 16) to[16 + l] = v;
   }
   // the lane's channels; f: the row's elements ahead of the strip
   __device__ __forceinline__ Raw4<T> get(const Raw4<T>* from, int f) const {
     const int l = threadIdx.x & 15;
-    if constexpr (HOW != kSingles) {
+    if constexpr (HOW == kFours) {
       return from[l];
+    } else if constexpr (HOW == kPairs) {
+      const uint32_t* e = reinterpret_cast<const uint32_t*>(from) + f / 2 + l;
+      return {make_uint2(e[0], e[16])};
     } else if constexpr (sizeof(T) == 2) {
       const uint16_t* e = reinterpret_cast<const uint16_t*>(from) + f + l;
       return {make_uint2(e[0] | (uint32_t)e[16] << 16, e[32] | (uint32_t)e[48] << 16)};
@@ -292,7 +291,7 @@ template <typename T, int HOW, int N, int S, int W> struct Ring {
     }
   }
   // the half warp's lanes have copied for one another, and have read
-  __device__ __forceinline__ void arrived() const { if (HOW == kSingles) __syncwarp(); }
+  __device__ __forceinline__ void arrived() const { if (HOW != kFours) __syncwarp(); }
 };
 
 // A run of tokens as a map of the state p in front of it, H + (k + m) p: where its

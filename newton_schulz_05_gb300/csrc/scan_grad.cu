@@ -55,7 +55,7 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
   // the segment's first token (in front of the sequence in the last round of some ranks)
   // of the chunk to read next, and of the one to write
   int t_in = (int)((int64_t)(chunks - 1 - rank) * kSpan + seg * S), t0 = t_in;
-  const int channel = D > 0 && HOW != kPairs ? ch.strip : ch.first;
+  const int channel = D > 0 ? ch.strip : ch.first;
   const T* dh = static_cast<const T*>(a.dh) + (row0 + t_in) * (int64_t)a.lddh + channel;
   const T* gate = static_cast<const T*>(a.gate) + (row0 + t_in) * (int64_t)a.ldg + channel;
   const T* x = static_cast<const T*>(a.x) + (row0 + t_in) * (int64_t)a.ldx + channel;
@@ -64,7 +64,7 @@ scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
   const bool mix = a.mix != 0.f;
   if (threadIdx.x < 16)
     sh.carry[0][threadIdx.x] = four(a.dlast ? ch.state(a.dlast + b * a.dim + ch.first) : quad(0.f));
-  const Ring<T, HOW, 4, S, W> slots(ring, ch, a.dim);
+  const Ring<T, HOW, 4, S, W> slots(ring, ch.strip, a.dim);
   static_assert(kSpan % slots.kPiece == 0 || D == 0, "a row is as far ahead of its piece in every chunk");
   const T *const dh0 = dh, *const gate0 = gate, *const x0 = x, *const h0 = h;
   Flags ahead[D > 0 ? D : 1];
