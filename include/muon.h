@@ -546,7 +546,8 @@ MUON_API muon_status muon_route_backward(int64_t tokens, int experts, int k, int
  * is not defined (other sequences and channels are not affected).
  *   0 <= batch, length < 2^31, dim in [1, 2^20], batch * ceil(dim / 64) < 2^27
  *   gate, x      [batch * length, dim] of dtype, rows ldg and ldx apart (any stride
- *                below 2^32)
+ *                below 2^32); read in whole aligned 16 bytes, each of which holds
+ *                an element of a row, so up to 14 bytes beside a row are read, too
  *   state        [batch, dim] fp32: the state before the first token; null: 0
  *   starts       [batch, length] bytes, or null: no token starts over
  *   token_mask   [batch, length] bytes: 0 for masked tokens; null: none
