@@ -40,10 +40,9 @@ __device__ __forceinline__ float left_out(float lp, float old, float d) {
   return (lp - a) - (old - b);
 }
 
-// exp(e) - e - 1 without the cancellation at small e: its Taylor series where 12
-// terms are exact to fp32
-__device__ __forceinline__ float excess(float e) {
-  if (fabsf(e) > 1.f) return expf(e) - 1.f - e;
+// exp(e) - e - 1 for |e| <= 1, without the cancellation at small e: its Taylor series, of
+// which 12 terms are exact to fp32
+__device__ __forceinline__ float near_excess(float e) {
   float s = 1.f / 479001600.f;                 // 1 / 12!
   s = fmaf(s, e, 1.f / 39916800.f);
   s = fmaf(s, e, 1.f / 3628800.f);
@@ -57,6 +56,10 @@ __device__ __forceinline__ float excess(float e) {
   s = fmaf(s, e, 0.5f);
   return s * e * e;
 }
+// exp(e) - e - 1, and exp(e) - 1: not as the former plus e, which has no digits left for the
+// 1 where e is below -2^24 (references that forbid a token), and is NaN for -inf
+__device__ __forceinline__ float excess(float e) { return fabsf(e) > 1.f ? expf(e) - 1.f - e : near_excess(e); }
+__device__ __forceinline__ float change(float e) { return fabsf(e) > 1.f ? expf(e) - 1.f : near_excess(e) + e; }
 
 // The loss of one token and its slope in log_probs.  cut: the minimum is the clipped side.
 struct Token { float each, kl, slope; bool cut; };
@@ -74,7 +77,7 @@ __device__ __forceinline__ Token token_of(const Policy& a, float lp, float old, 
   const float r = expf(d);
   if (GRAD) {
     k.slope = k.cut ? 0.f : -r * adv;
-    if (a.ref && a.kl_weight != 0.f) k.slope = fmaf(-a.kl_weight, excess(ref - lp) + (ref - lp), k.slope);
+    if (a.ref && a.kl_weight != 0.f) k.slope = fmaf(-a.kl_weight, change(ref - lp), k.slope);
   } else {
     k.kl = a.ref ? excess(ref - lp) : 0.f;
     // without a weight not even an infinite k counts
