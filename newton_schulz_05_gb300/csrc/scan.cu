@@ -27,20 +27,27 @@ struct Scan {
   float* last;
 };
 
-// a = sigmoid(g), 1 - a, and the input's part of the step
-struct Step { Quad keep, lose, in; };
-__device__ __forceinline__ Step step_of(const Quad& g, const Quad& x, float mix) {
-  Step s;
+// the input's part of a step: (1 - a) x, or x
+__device__ __forceinline__ Quad input_of(const Quad& take, const Quad& x, float mix) {
+  return mul(fma(take, quad(mix), quad(1.f - mix)), x);
+}
+// One token of a walk, the state in front of it p.  With w the smaller of a and 1 - a, the new state is
+// what has the larger share, changed by w times what the other differs by (in two products,
+// so that far numbers do not overflow): a state that goes from call to call loses 1 - a and
+// not 1 minus the rounded a.
+__device__ __forceinline__ Quad walked(const Quad& g, const Quad& x, const Quad& p, bool mix) {
+  Quad q;
   #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    float2 t = mul2(g.v[j], both(-1.4426950408889634f));
-    t = add2(make_float2(exp2_fast(t.x), exp2_fast(t.y)), both(1.f));
-    s.keep.v[j] = make_float2(reciprocal_fast(t.x), reciprocal_fast(t.y));
-    // 1 - a of the rounded a: a constant input then comes out unchanged
-    s.lose.v[j] = fma2(s.keep.v[j], both(-1.f), both(1.f));
-    s.in.v[j] = mul2(fma2(s.keep.v[j], both(-mix), both(1.f)), x.v[j]);
+    const float2 v = g.v[j], in = x.v[j], from = p.v[j];
+    const float2 t = make_float2(exp2_fast(fabsf(v.x) * -1.4426950408889634f), exp2_fast(fabsf(v.y) * -1.4426950408889634f));
+    const float2 n = add2(t, both(1.f)), w = mul2(t, make_float2(reciprocal_fast(n.x), reciprocal_fast(n.y)));
+    // w of the input and -w of the state where the state has the larger share, else the other way
+    const float2 of_x = make_float2(copysignf(w.x, v.x), copysignf(w.y, v.y)), of_p = mul2(of_x, both(-1.f));
+    const float2 most = make_float2(!signbit(v.x) ? from.x : mix ? in.x : 0.f, !signbit(v.y) ? from.y : mix ? in.y : 0.f);
+    q.v[j] = add2(most, mix ? fma2(of_x, in, mul2(of_p, from)) : fma2(of_p, from, in));
   }
-  return s;
+  return q;
 }
 
 // W warps a block, S tokens a segment, CL blocks a cluster, D chunks in flight (0: a
@@ -145,10 +152,12 @@ scan_kernel(const __grid_constant__ Scan a) {
           run.P = masked(run.P, on);
           run.H = masked(run.H, on);
         }
-        const Step st = step_of(widen(gi), widen(vi), a.mix);
-        P[i] = run.P = mul(run.P, st.keep);
-        H[i] = run.H = fma(st.keep, run.H, st.in);
-        run.Q = fma(st.keep, run.Q, st.lose);
+        Quad keep, take;
+        shares_of(widen(gi), keep, take);
+        P[i] = run.P = mul(run.P, keep);
+        // a constant input comes out unchanged: what it adds is the same sum as what is lost
+        H[i] = run.H = fma(keep, run.H, input_of(take, widen(vi), a.mix));
+        run.Q = fma(keep, run.Q, take);
       }
     };
     if (FLAGS && !now.quiet) reduce(std::bool_constant<FLAGS>());
@@ -221,10 +230,9 @@ __global__ void __launch_bounds__(kShortThreads) scan_short_kernel(const __grid_
     for (int i = 0; i < kShortAhead; ++i) {
       const int t = t0 + i;
       if (t >= length) continue;
-      const Step st = step_of(widen(rg[i]), widen(rx[i]), a.mix);
       Quad q = p;
       if (FLAGS && begins[i]) q = quad(0.f);
-      q = fma(st.keep, q, st.in);
+      q = walked(widen(rg[i]), widen(rx[i]), q, a.mix != 0.f);
       if (!FLAGS || live[i]) p = q;
       ch.store(h + t * a.dim, p);
     }

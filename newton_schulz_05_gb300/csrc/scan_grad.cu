@@ -24,21 +24,6 @@ struct ScanBwd {
   float* dstate;
 };
 
-// t = 4 exp(-gate); a = 1 / (1 + t / 4), 1 - a = a t / 4, so that both have their own
-// precision.  The 4 makes t infinite before a is flushed to 0, and the minimum drops the
-// NaN of infinity times 0.
-__device__ __forceinline__ void shares_of(const Quad& g, Quad& keep, Quad& take) {
-  #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    float2 t = fma2(g.v[j], both(-1.4426950408889634f), both(2.f));
-    t = make_float2(exp2_fast(t.x), exp2_fast(t.y));
-    const float2 n = fma2(t, both(0.25f), both(1.f));
-    keep.v[j] = make_float2(reciprocal_fast(n.x), reciprocal_fast(n.y));
-    t = mul2(mul2(t, both(0.25f)), keep.v[j]);
-    take.v[j] = make_float2(fminf(t.x, 1.f), fminf(t.y, 1.f));
-  }
-}
-
 template <typename T, int W, int S, int CL, int D, int HOW, bool FLAGS>
 __global__ void __launch_bounds__(32 * W, (kScanBlocks<T, W, 4, S>))
 scan_bwd_kernel(const __grid_constant__ ScanBwd a) {
