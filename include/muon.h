@@ -652,7 +652,9 @@ MUON_API muon_status muon_token_log_probs(int64_t tokens, int64_t vocab, int dty
 
 /*
  * Gradient of muon_token_log_probs's log_probs:
- *   dlogits_v = scale * dlog_probs * ((v == index) - exp(scale * logits_v - lse))
+ *   dlogits_v = scale * dlog_probs * ((v == index) - exp(min(scale * logits_v - lse, 0)))
+ * (the minimum is the difference itself but for lse's rounding; it is 0 where scale *
+ * logits_v and lse overflow below, so rows of finite logits have finite gradients).
  * A token that is ignored, or whose dlog_probs is 0, gets zeros, whatever its
  * logits hold.
  *   dlog_probs   [tokens] fp32

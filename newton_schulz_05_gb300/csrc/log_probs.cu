@@ -151,7 +151,17 @@ log_probs_kernel(int64_t tokens, int64_t vocab, const T* logits, int64_t ld, con
   }
 }
 
-// TPR threads take a unit of kVocabPieces pieces each of one row
+// The smaller one; NaN where either is
+__device__ __forceinline__ float least(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// TPR threads take a unit of kVocabPieces pieces each of one row.  As in the forward pass the
+// difference is taken before the base is changed, so that it does not overflow where logits
+// and log sum are near the type's lowest value; a softmax is at most 1, whatever digits the log
+// sum of a row far from zero has lost.
 template <typename T, int TPR>
 __global__ void __launch_bounds__(kVocabThreads)
 log_probs_bwd_kernel(int64_t units, int units_a_row, int64_t vocab, const float* dlp, const T* logits, int64_t ld,
@@ -163,7 +173,7 @@ log_probs_bwd_kernel(int64_t units, int units_a_row, int64_t vocab, const float*
   const int64_t row = unit / units_a_row;
   const int64_t y = index[row];
   const float d = y < 0 || y >= vocab ? 0.f : dlp[row] * scale;
-  const float less = -lse[row] * kLog2e, c = scale * kLog2e;
+  const float less = -lse[row];
   const T* l = logits + row * ld;
   T* out = dlogits + row * vocab;
   const int phase = phase_of(out);
@@ -192,7 +202,8 @@ log_probs_bwd_kernel(int64_t units, int units_a_row, int64_t vocab, const float*
     }
     #pragma unroll
     for (int j = 0; j < E / 2; ++j) {
-      const float2 e = fma2(v.v[j], both(c), both(less));
+      float2 e = fma2(v.v[j], both(scale), both(less));
+      e = mul2(make_float2(least(e.x, 0.f), least(e.y, 0.f)), both(kLog2e));
       v.v[j] = d != 0.f ? mul2(make_float2(exp2_fast(e.x), exp2_fast(e.y)), both(-d)) : both(0.f);
     }
     if (d != 0.f && y >= col && y < col + E) {
