@@ -640,8 +640,8 @@ MUON_API muon_status muon_norm_rotate_heads_workspace_bytes(int64_t tokens, int 
  * A token whose index is outside of [0, vocab) is ignored: both are 0 whatever
  * its logits hold.  A logit of -inf has no share (scale > 0).  A row with a NaN, a
  * +inf or nothing above -inf has NaN in log_probs.
- *   0 <= tokens < 2^31, vocab in [1, 2^30], tokens * vocab <= 2^40, scale finite
- *   and > 0
+ *   0 <= tokens < 2^31, vocab in [1, 2^30], tokens * vocab <= 2^40, scale in
+ *   (0, 2^127]
  *   logits       [tokens, vocab] of dtype, rows ld apart
  *   index        [tokens]
  *   log_probs, lse [tokens] fp32

@@ -224,7 +224,8 @@ log_probs_bwd_kernel(int64_t units, int units_a_row, int64_t vocab, const float*
 // --------------------------------------------------------------------- host
 
 muon_status check_vocab(int64_t tokens, int64_t vocab, int dtype, int64_t ld, float scale) {
-  if (tokens < 0 || ld < 0 || !(scale > 0.f) || std::isinf(scale)) return MUON_ERR_INVALID_ARG;
+  // (beyond 2^127 the scale in base 2 is infinite, and every row NaN)
+  if (tokens < 0 || ld < 0 || !(scale > 0.f) || scale > 0x1p127f) return MUON_ERR_INVALID_ARG;
   if (vocab < 1 || vocab > (int64_t)1 << 30 || tokens >= (int64_t)1 << 31 || tokens > ((int64_t)1 << 40) / vocab)
     return MUON_ERR_UNSUPPORTED_SHAPE;
   return known(dtype) ? MUON_OK : MUON_ERR_DTYPE;
