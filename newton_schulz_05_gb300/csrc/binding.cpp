@@ -18,6 +18,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cstring>
 #include <string>
 
 #include "muon.h"
@@ -895,40 +896,46 @@ PyObject* is_heads(PyObject*, PyObject* o) {
   return PyBool_FromLong(heads_of(THPVariable_Unpack(o), &r) == nullptr);
 }
 
-// bind({name: address}): the library's entry points.  A name that is left out keeps what
-// it was bound to; each must be bound to something.
+// bind({name: address}): the library's entry points.  Those of the training operators are all
+// there, those over sequences all or, once they are bound, none; no other name is.  What
+// is refused binds nothing.
+struct Entry { const char* name; void* to; };
+#define ENTRY(f) Entry{"muon_" #f, &p_##f}
+const Entry training_entries[] = {ENTRY(layer_norm), ENTRY(layer_norm_backward), ENTRY(layer_norm_workspace_bytes),
+                                  ENTRY(dropout), ENTRY(route), ENTRY(route_workspace_bytes), ENTRY(route_backward)};
+const Entry sequence_entries[] = {
+    ENTRY(gated_scan), ENTRY(gated_scan_backward), ENTRY(norm_rotate_heads), ENTRY(norm_rotate_heads_backward),
+    ENTRY(norm_rotate_heads_workspace_bytes), ENTRY(token_log_probs), ENTRY(token_log_probs_backward),
+    ENTRY(policy_loss), ENTRY(policy_loss_backward), ENTRY(policy_loss_workspace_bytes)};
+#undef ENTRY
+
 PyObject* bind(PyObject*, PyObject* names) {
-  bool all = true;
-  auto get = [&](const char* name, auto& to) {
-    PyObject* v = PyDict_Check(names) ? PyDict_GetItemString(names, name) : nullptr;
-    if (void* p = v ? PyLong_AsVoidPtr(v) : nullptr) to = reinterpret_cast<std::decay_t<decltype(to)>>(p);
-    if (!to) all = false;
-  };
-#define BIND(f) get("muon_" #f, p_##f)
-  BIND(layer_norm);
-  BIND(layer_norm_backward);
-  BIND(layer_norm_workspace_bytes);
-  BIND(dropout);
-  BIND(route);
-  BIND(route_workspace_bytes);
-  BIND(route_backward);
-  BIND(gated_scan);
-  BIND(gated_scan_backward);
-  BIND(norm_rotate_heads);
-  BIND(norm_rotate_heads_backward);
-  BIND(norm_rotate_heads_workspace_bytes);
-  BIND(token_log_probs);
-  BIND(token_log_probs_backward);
-  BIND(policy_loss);
-  BIND(policy_loss_backward);
-  BIND(policy_loss_workspace_bytes);
-#undef BIND
-  if (PyErr_Occurred()) return nullptr;
-  if (!all) {
-    PyErr_SetString(PyExc_ValueError, "an entry point of libmuon is missing");
-    return nullptr;
-  }
-  Py_RETURN_NONE;
+  return guarded(0, 0, [&]() -> PyObject* {
+    if (!PyDict_Check(names)) type_error("entry points must be a dict of names and addresses");
+    auto given = [&](const Entry& e) { return PyDict_GetItemString(names, e.name); };
+    auto address = [&](const Entry& e) {
+      PyObject* v = given(e);
+      void* p = v ? PyLong_AsVoidPtr(v) : nullptr;
+      if (PyErr_Occurred()) throw Raise{nullptr, ""};
+      if (!p) value_error(std::string("the entry point ") + e.name + " of libmuon is missing");
+      return p;
+    };
+    bool sequences = !p_gated_scan;
+    Py_ssize_t known = 0;
+    for (const Entry& e : sequence_entries) sequences = sequences || given(e);
+    for (const Entry& e : training_entries) known += address(e) != nullptr;
+    if (sequences)
+      for (const Entry& e : sequence_entries) known += address(e) != nullptr;
+    if (PyDict_Size(names) != known) value_error("a name that is no entry point of libmuon");
+    auto put = [&](const Entry& e) {
+      void* const p = address(e);
+      std::memcpy(e.to, &p, sizeof(p));
+    };
+    for (const Entry& e : training_entries) put(e);
+    if (sequences)
+      for (const Entry& e : sequence_entries) put(e);
+    Py_RETURN_NONE;
+  });
 }
 
 #define FAST(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
