@@ -161,6 +161,10 @@ def _as_rows(t: torch.Tensor) -> torch.Tensor:
     return t if _b().is_rows(t) else t.contiguous()
 
 
+def _dense(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    return None if t is None else t.contiguous()
+
+
 def _on(stream, fn, args, kw):
     """fn on another stream: outputs are allocated there, and the inputs'
     memory is not reused before the stream has run the call."""
@@ -289,7 +293,7 @@ class _LayerNorm(torch.autograd.Function):
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5) -> torch.Tensor:
     """Differentiable layer norm over the last dimension."""
-    return _LayerNorm.apply(_as_rows(x), None, weight, bias, eps, 0.0, 0, 0)[0]
+    return _LayerNorm.apply(_as_rows(x), None, _dense(weight), _dense(bias), eps, 0.0, 0, 0)[0]
 
 
 def dropout_add_layer_norm(x, residual, weight=None, bias=None, *, p: float, seed: int,
@@ -298,7 +302,8 @@ def dropout_add_layer_norm(x, residual, weight=None, bias=None, *, p: float, see
     s: the end of one sublayer and the norm in front of the next."""
     if x.shape != residual.shape:
         raise ValueError("residual must have shape %s" % (tuple(x.shape),))
-    return _LayerNorm.apply(_as_rows(x), _as_rows(residual), weight, bias, eps, p, seed, offset)
+    return _LayerNorm.apply(_as_rows(x), _as_rows(residual), _dense(weight), _dense(bias), eps, p, seed,
+                            offset)
 
 
 class _Dropout(torch.autograd.Function):
@@ -412,7 +417,7 @@ class _GatedScan(torch.autograd.Function):
 def gated_scan(gate, x, *, state=None, starts=None, token_mask=None, mix: bool = True) -> ScanOut:
     """Differentiable gated linear recurrence: gradients flow to gate, x and
     state, from h and from the last state."""
-    dense = [None if t is None else t.contiguous() for t in (state, starts, token_mask)]
+    dense = [_dense(t) for t in (state, starts, token_mask)]
     return ScanOut(*_GatedScan.apply(_as_rows(gate), _as_rows(x), *dense, mix))
 
 
@@ -503,10 +508,9 @@ def norm_rotate_heads(q, k=None, q_weight=None, k_weight=None, *, cos=None, sin=
                       eps: float = 1e-6, neighbours: bool = False) -> HeadsOut:
     """Differentiable norms of query and key heads with the rotation of
     positions."""
-    if positions is not None:
-        positions = positions.contiguous()
-    return HeadsOut(*_NormRotateHeads.apply(_as_heads(q), None if k is None else _as_heads(k), q_weight,
-                                            k_weight, cos, sin, positions, eps, neighbours))
+    dense = [_dense(t) for t in (q_weight, k_weight, cos, sin, positions)]
+    return HeadsOut(*_NormRotateHeads.apply(_as_heads(q), None if k is None else _as_heads(k), *dense, eps,
+                                            neighbours))
 
 
 def token_log_probs_forward(logits, tokens, *, scale: float = 1.0, stream=None) -> LogProbsOut:
@@ -626,5 +630,5 @@ def policy_loss(log_probs, old_log_probs, advantages, *, ref_log_probs=None, tok
     rows = [_as_rows(t) for t in (log_probs, old_log_probs)]
     advantages = _as_rows(advantages) if advantages.shape == log_probs.shape else advantages.contiguous()
     ref = None if ref_log_probs is None else _as_rows(ref_log_probs)
-    mask = None if token_mask is None else token_mask.contiguous()
+    mask = _dense(token_mask)
     return PolicyOut(*_PolicyLoss.apply(*rows, advantages, ref, mask, clip_low, clip_high, kl, by_sequence))
