@@ -161,8 +161,9 @@ def _as_rows(t: torch.Tensor) -> torch.Tensor:
     return t if _b().is_rows(t) else t.contiguous()
 
 
-def _dense(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
-    return None if t is None else t.contiguous()
+def _dense(t):
+    """A dense tensor; what is none passes, for the binding to refuse (None: to take)."""
+    return t.contiguous() if isinstance(t, torch.Tensor) else t
 
 
 def _on(stream, fn, args, kw):

@@ -1,7 +1,8 @@
-"""What the binding takes for the library's entry points, without a GPU."""
+"""What the binding takes for the library's entry points and for tensors, without a GPU."""
 import ctypes
 
 import pytest
+import torch
 
 
 @pytest.fixture(scope="module")
@@ -31,3 +32,13 @@ def test_entry_points_that_are_missing_or_not_known_are_refused(lib):
         binding.bind(first)      # those over sequences keep what they are bound to
     finally:
         binding.bind(real)
+
+
+def test_what_is_no_tensor_is_refused_as_such():
+    from newton_schulz_05_gb300 import layers
+    x = torch.zeros(3, 2, 8)
+    for call in (lambda: layers.layer_norm(x, [1.0] * 8), lambda: layers.dropout_add_layer_norm(x, x, None, 0.5, p=0.1, seed=1),
+                 lambda: layers.norm_rotate_heads(x, x, [1.0] * 8), lambda: layers.norm_rotate_heads(x, cos=1, sin=1),
+                 lambda: layers.gated_scan(x, x, state=0.0), lambda: layers.policy_loss(x, x, x, token_mask=True)):
+        with pytest.raises(TypeError, match="must be a tensor"):
+            call()
