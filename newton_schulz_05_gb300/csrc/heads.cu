@@ -7,7 +7,7 @@
 // none.  A warp takes as many heads as fit, in passes that come through a ring of asynchronous
 // copies into shared memory; a token's angles are loaded once for its heads.  Weight gradients
 // add up in registers over all of a warp's heads, then over the block's warps, then over blocks,
-// always in the same order.  Heads of odd widths, at odd addresses, or more than 2^31 of them go
+// always in the same order.  Heads of odd widths, at odd addresses, or about 2^31 of them go
 // through kernels that move single elements, a warp a head (9 to 25% of the copy rate, the
 // gradient 5 to 13%).
 //
@@ -373,9 +373,12 @@ __device__ __forceinline__ HeadWalk walk_of(const Heads& a, int heads, int block
   passes = warp < runs ? (int)((runs - 1 - warp) / warps + 1) * run : 0;
   return k;
 }
-// Heads that these walks can number: the last step of one goes by a run of every warp past the
-// end, at most 3648 runs of 131104 heads (under 2^29)
-constexpr int64_t kMostHeads = (int64_t)1 << 31;
+// Heads that these walks can number without passing 2^32.  A walk's last step goes from the end of a
+// run, at most that many heads and a run (a token's, 131088) further, by a run of every warp.  A run is at
+// most what a warp has at all (share_out), so those are all heads again and a pass a warp.
+constexpr int64_t kMostHeads = ((int64_t)1 << 31) - (1 << 20);
+constexpr int kMostBlocks = 3648, kMostAPass = 16;
+static_assert(2 * kMostHeads + 131088 + (kMostBlocks * kHeadWarps + 1) * kMostAPass <= (int64_t)1 << 32, "32 bits");
 
 // the angles of the lane's pairs at a position: 1 and 0 where there are none
 template <int E, bool NB>
@@ -749,7 +752,7 @@ void share_out(int64_t n, int of_token, int B, int most, int& blocks, int& run) 
 int forward_blocks(const Heads& a, int B, size_t es) {
   const int64_t heads = a.tokens * (a.side[0].heads + a.side[1].heads);
   if (es == 2 && heads * a.dim < (int64_t)1 << 27) return 456;
-  return (int)std::max<int64_t>(456, std::min<int64_t>(3648, heads / B / (kHeadWarps * 45 / 8)));
+  return (int)std::max<int64_t>(456, std::min<int64_t>(kMostBlocks, heads / B / (kHeadWarps * 45 / 8)));
 }
 // out of `most` blocks
 HeadWork work_of(const Heads& a, int B, int most, int wbf16) {
