@@ -585,7 +585,8 @@ MUON_API muon_status muon_gated_scan_backward(
 /*
  * RMS norm of each query and key head, and the rotation of its first `rotary`
  * elements by the angles of the token's position:
- *   n = x / sqrt(mean(x^2) + eps) * weight   over the dim elements of a head
+ *   n = x / sqrt(mean(x^2) + eps) * weight   over the dim elements of a head,
+ *   in fp32: the squares' sum is below 2^128, and mean(x^2) + eps is at least 2^-126
  *   (y_i, y_j) = (n_i c - n_j s, n_j c + n_i s)   for pair m of rotary / 2, with
  *   c, s = cos[position, m], sin[position, m]; i, j = m, m + rotary / 2, or
  *   2 m, 2 m + 1 (neighbours != 0).  Elements from `rotary` on keep n.

@@ -26,8 +26,9 @@ namespace {
 
 constexpr int kHeadThreads = 256, kHeadWarps = kHeadThreads / 32;
 constexpr int kHeadMaxDim = 1024;
-// Blocks of the gradient and images of its weight sums, two an SM: with 152 and 608 the gradient of
-// [8191, 12 + 12, 80] fp32 takes 51 and 42 us, with these 37
+// Blocks of the gradient and images of its weight sums, two an SM: with 152, 456 and 608 the gradient of
+// [8191, 12 + 12, 80] fp32 takes 51, 47 and 44 us, with these 38; [32768, 32 + 8, 128] bf16 264, 210 and
+// 183, with these 184; [8192, 16 + 16, 256] fp32 133, 138 and 136, with these 139
 constexpr int kHeadParts = 304;
 
 // Queries or keys: heads `step` elements apart, tokens `ld`
@@ -743,12 +744,18 @@ void share_out(int64_t n, int of_token, int B, int most, int& blocks, int& run) 
   run = (int)std::min<int64_t>((of_token + B - 1) / B, of_warp);
   blocks = (int)std::min<int64_t>((passes + (int64_t)run * kHeadWarps - 1) / ((int64_t)run * kHeadWarps), most);
 }
-// Blocks of the forward pass: as many as are resident, three an SM, or up to eight times as many
-// where HBM limits it.  Resident blocks go in step, all reading and then all writing:
-// [32768, 32 + 8, 128] bf16 123 us, 104 with 3648 blocks, [8192, 16 + 16, 256] fp32 96 and 83.
-// Where it does not, the blocks' beginnings cost more than that: [16384, 12 + 12, 192] bf16 57
-// and 70.  A warp has about six passes at the least ([8192, 32 + 8, 64] fp32, with 1824 blocks
-// 28 and with 3648 33).
+// Blocks of the forward pass: as many as are resident, three an SM, or up to eight times as many.
+// Resident blocks go in step, all reading and then all writing, which wastes HBM; more blocks have
+// more beginnings, which cost instructions, and bf16 has twice as many of those a byte.  So fp32 takes
+// many, and bf16 from where the two cross.  In us, with 456 and with up to 3648 blocks (a warp has about
+// six passes at the least: [8192, 32 + 8, 64] fp32, with 1824 blocks 28 and with 3648 33):
+//   [tokens, 32 + 8, 128]  2048       4096       8192       16384      32768
+//   bf16                   9.7, 9.7   18.3, 17.7 31.1, 34.2 62.0, 61.5 123.7, 103.9
+//   fp32                   12.3, 14.4 31.6, 28.9 60.7, 52.7 110.8, 102 217, 200
+//   bf16 [16384, 12 + 12, 192] 57.2, 70.4, [65536, 16 + 4, 64] 65.7, 73.9, [8192, 16 + 16, 256] 51.2, 52.2
+//   fp32                       111.6, 95.1                     116, 102                         95.6, 82.5
+// (bf16 of 2^26 to 2^27 elements would take a few percent less with 912 to 1824 at 40 heads, and a few more
+// at 20 and 24.)
 int forward_blocks(const Heads& a, int B, size_t es) {
   const int64_t heads = a.tokens * (a.side[0].heads + a.side[1].heads);
   if (es == 2 && heads * a.dim < (int64_t)1 << 27) return 456;

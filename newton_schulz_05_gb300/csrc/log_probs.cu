@@ -9,8 +9,8 @@
 // in pairs of bf16, so that the sum is scaled once for 32 elements.
 //
 // Measured: [8192, 131072] bf16 294 us, 7.3 TB/s (reading alone is faster than a copy), the
-// gradient of three rows in four 550 us, 6.8 TB/s; [4096, 50021] 66 us and 114 us; [20000, 2048]
-// 15.5 and 29 us, 5.3 and 5.0 TB/s; one row of 262144 3.8 us in a cluster of eight blocks.
+// gradient of three rows in four 556 us, 6.8 TB/s; [4096, 50021] 66 us and 116 us; [20000, 2048]
+// 15.5 and 25 us, 5.3 and 5.7 TB/s; one row of 262144 3.8 us in a cluster of eight blocks.
 // Few rows are uneven: 509 of 50021 fp32, a quarter of them ignored, take 15.8 us where their
 // bytes take 11.3, as the blocks of an SM end apart.
 #include <cfloat>

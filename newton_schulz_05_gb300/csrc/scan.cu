@@ -1,12 +1,13 @@
 // Gated linear recurrence: the forward pass.
 //
 // Bound by HBM where there are strips for all SMs, by the walk over chunks where there are few.
-// Measured: [16, 2048, 2048] bf16 72 us, 5.6 TB/s, [4, 8192, 2048] fp32 131 us, 6.2 TB/s;
-// [1, 65536, 2048] bf16 205 us, 4.0 TB/s (32 strips; 64 rounds of 3.2 us), [1, 65536, 64] 101 us
-// (one strip, 32 rounds); [3, 2047, 1409] fp32 with flags 32 us; one token of 48 x 2048 1.5 us.
+// Measured: [16, 2048, 2048] bf16 73 us, 5.5 TB/s, [4, 8192, 2048] fp32 132 to 149 us by where its
+// buffers lie, 6.1 to 5.4 TB/s; [1, 65536, 2048] bf16 207 us, 3.9 TB/s (32 strips; 64 rounds of 3.2 us),
+// [1, 65536, 64] 103 us (one strip, 32 rounds); [3, 2047, 1409] fp32 with flags 32 us (69 strips; eight
+// rounds); one token of 48 x 2048 1.5 us.
 // Rows of an odd number of bf16 channels are stored in single elements and read in pieces from
-// any address: [4, 4096, 2047] 58 us, its gradient 115, where 2046 channels, in pairs, take 50 and
-// 95, and 2048 take 39 and 69.
+// any address: [4, 4096, 2047] 63 us, its gradient 115, where 2046 channels, in pairs, take 51 and
+// 95, and 2048 take 40 and 69.
 #include "scan.cuh"
 
 #include <algorithm>
@@ -259,7 +260,7 @@ cudaError_t scan_with(const Scan& a, int64_t strips, cudaStream_t s) {
 }
 
 // Up to four tokens, or 32 where there are strips enough for every SM's lanes, are walked one
-// after the other: one token of [256, 8192] bf16 5.5 us, 38.0 through the joins, 16 of [64, 4096] 5.7 and 9.2
+// after the other: one token of [256, 8192] bf16 5.7 us, 38.0 through the joins, 16 of [64, 4096] 6.3 and 9.2
 template <typename T, int HOW> cudaError_t scan_by_size(const Scan& a, int64_t strips, cudaStream_t s) {
   constexpr int S = sizeof(T) == 2 ? 8 : 4;
   if (a.length <= 4 || (a.length <= 32 && strips >= 2048)) return scan_short<T, HOW>(a, strips, s);

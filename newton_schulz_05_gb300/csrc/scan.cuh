@@ -329,8 +329,8 @@ __device__ __forceinline__ Quad apply(const Run& r, const Quad& p) {
 __device__ __forceinline__ Run then(const Run& a, const Run& b) {
   return {fma(a.m, b.k, fma(a.k, b.m, mul(a.m, b.m))), mul(a.k, b.k), apply(b, a.H), a.cut || b.cut};
 }
-// a segment's factor, 1 minus it, and what its tokens add.  Both are sums of positive
-// terms, so each keeps its own precision.
+// a segment's factor, 1 minus it, and what its tokens add.  1 minus the factor is a sum of
+// positive terms, each of which has its own digits (shares_of).
 struct Segment {
   Quad P, Q, H;
   bool cut;
