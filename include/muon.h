@@ -656,6 +656,7 @@ MUON_API muon_status muon_token_log_probs(int64_t tokens, int64_t vocab, int dty
  *   dlogits_v = scale * dlog_probs * ((v == index) - exp(min(scale * logits_v - lse, 0)))
  * (the minimum is the difference itself but for lse's rounding; it is 0 where scale *
  * logits_v and lse overflow below, so rows of finite logits have finite gradients).
+ * An exponential under 2^-126 counts as 0.
  * A token that is ignored, or whose dlog_probs is 0, gets zeros, whatever its
  * logits hold.
  *   dlog_probs   [tokens] fp32
